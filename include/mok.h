@@ -353,7 +353,11 @@ enum {
   MOK_PHASE_BWD_REPLAY = 13,   /* bounded-memory backward: GEMM1 recomputed, context copied back */
   MOK_PHASE_FWD_FUSED = 14,    /* single-launch forward: schedule, GEMMs, combine */
   MOK_PHASE_FWD_SORT = 15,     /* token-sorted copy of x and the ring's pair table (CTA-pair ring) */
-  MOK_NUM_PHASES = 16
+  MOK_PHASE_FEW = 16,          /* the layer for a few tokens */
+  MOK_PHASE_DISTILL = 17,      /* distillation loss, gradient or both */
+  MOK_PHASE_EMBED_FWD = 18,    /* embedding lookup */
+  MOK_PHASE_EMBED_BWD = 19,    /* embedding gradient */
+  MOK_NUM_PHASES = 20
 };
 mok_status mok_trace_enable(int32_t on);
 mok_status mok_trace_read(float* ms /* [MOK_NUM_PHASES] */, int32_t* count /* [MOK_NUM_PHASES] */);
@@ -550,6 +554,124 @@ mok_status mok_ep_combine_rows(const mok_shape* shape, const mok_config* cfg, co
  * routed nowhere: the returned per-row score gradients back in token order. */
 mok_status mok_ep_unsort_scores(const mok_shape* shape, const mok_config* cfg, const void* ws, size_t ws_bytes,
                                 const float* row_vals, float* out, void* stream);
+
+/*
+ * The layer for a few tokens: what mok_forward computes, for serving steps of
+ * 1 <= T <= MOK_FEW_MAX_TOKENS tokens, without a schedule, a padded copy of
+ * the rows or a forward context -- nothing is kept for a backward.  A pass
+ * reads the weights of the experts that the tokens chose and no others.
+ *
+ *   mok_few_forward  routing given: topk_idx (device int32 [T, k]) and scores
+ *                    (device f32 [T, k])
+ *   mok_few_layer    router included: topk_idx and scores are outputs, as
+ *                    mok_router_forward defines them (logits of bf16 x and Wr
+ *                    summed in f32; bias f32 [E] or NULL selects only; ties go
+ *                    to the lower expert); needs k <= E
+ *   x     (device) bf16 [T, H];  out (device) bf16 [T, H]
+ *   W1, W3, W2   as for mok_forward in the given precision
+ * h, u and y stay in f32; a = silu(h) * u is rounded to bf16 (MXFP8: x along
+ * H and a along I are quantised per 32, by the rule of mok_mxfp8_quantize);
+ * out is summed in f32 over j in increasing order and rounded once.  The
+ * order of the sums over H and I depends on the whole call's routing, so a
+ * token's last bits may depend on the tokens beside it; a call repeated with
+ * the same inputs gives the same bits.
+ *
+ * An id outside [0, E) records MOK_ERR_BAD_INDEX and adds nothing to its
+ * token; an expert may appear more than once in a token's list.
+ *
+ * ws: mok_few_workspace_size bytes (0: unsupported shape or precision) for
+ * this shape; a workspace of a shape with more tokens, all else equal, serves
+ * too.  The caller zeroes it once before its first use (cudaMemset); calls
+ * leave it ready for the next one.  After MOK_ERR_TIMEOUT it has to be zeroed
+ * again.  Errors stay in its first word until mok_check reads and clears it.
+ * Calls that share a workspace must not overlap.  Tensor pointers are 16-byte
+ * aligned (MOK_ERR_INVALID_ARG otherwise).
+ */
+#define MOK_FEW_MAX_TOKENS 128
+size_t mok_few_workspace_size(const mok_shape* shape, mok_precision prec);
+mok_status mok_few_forward(const mok_shape* shape, mok_precision prec, void* ws, size_t ws_bytes,
+                           const int32_t* topk_idx, const void* x, const float* scores, const void* W1,
+                           const void* W3, const void* W2, void* out, void* stream);
+mok_status mok_few_layer(const mok_shape* shape, mok_precision prec, void* ws, size_t ws_bytes, const void* x,
+                         const void* Wr, const float* bias, const void* W1, const void* W3, const void* W2,
+                         int32_t* topk_idx, float* scores, void* out, void* stream);
+
+/* Element type of the tensors that the calls below take in either. */
+typedef enum { MOK_TYPE_BF16 = 0, MOK_TYPE_F32 = 1 } mok_dtype;
+
+/*
+ * Distillation loss from a teacher's top logits.  Row t has student logits z
+ * (V of them) and a teacher's list of K (id_j, v_j); with temperature tau > 0
+ *
+ *   p    = softmax over the list of v / tau
+ *   lse  = log sum_v exp(z_v / tau),  log q_v = z_v / tau - lse
+ *   loss = sum_j p_j (log p_j - log q_(id_j))          = KL(p || q)
+ *   dz_v = (dloss / tau) (q_v - sum_{j: id_j = v} p_j)
+ *
+ *   z      (device) [T, V], bf16 or f32; rows ldz >= V elements apart, at any
+ *          element alignment
+ *   ids    (device) int32 [T, K]; -1 leaves an entry out (a list may hold
+ *          fewer than K, in any order and places; an id twice counts twice).
+ *          Any other id outside [0, V) records MOK_ERR_BAD_INDEX and is left out
+ *   vals   (device) f32 [T, K]; not read as numbers where the id is left out
+ *   dloss  (device) f32 [T]  weight of each row's loss in what is minimised
+ *   loss, lse   (device) f32 [T]
+ *   dz     (device) [T, V] of z's type, rows lddz apart; it may be z itself
+ *          (same pointer and stride)
+ * Entries with p_j = 0 add nothing, whatever q is there.  A row whose list is
+ * empty, or holds values of -inf alone, has loss 0 and gradient 0.  A student
+ * logit of -inf has q = 0; where p > 0 there, the loss is +inf.  The loss is
+ * not scaled by tau^2.  K = 1 is the cross entropy of a label.
+ *
+ *   mok_distill_forward   loss and lse
+ *   mok_distill_backward  dz from the forward's lse
+ *   mok_distill_step      both at once: loss, lse and dz
+ * All sums in f32 and in a fixed order.  1 <= K <= MOK_DISTILL_MAX_TOP; T = 0
+ * does nothing.  ws: mok_distill_workspace_size() bytes, zeroed once by the
+ * caller; its first word holds errors until mok_check.
+ */
+#define MOK_DISTILL_MAX_TOP 512
+size_t mok_distill_workspace_size(int32_t T, int32_t V, int32_t K);
+mok_status mok_distill_forward(int32_t T, int32_t V, int32_t K, mok_dtype type, const void* z, int64_t ldz,
+                               const int32_t* ids, const float* vals, float tau, float* loss, float* lse, void* ws,
+                               size_t ws_bytes, void* stream);
+mok_status mok_distill_backward(int32_t T, int32_t V, int32_t K, mok_dtype type, const void* z, int64_t ldz,
+                                const int32_t* ids, const float* vals, float tau, const float* lse,
+                                const float* dloss, void* dz, int64_t lddz, void* ws, size_t ws_bytes, void* stream);
+mok_status mok_distill_step(int32_t T, int32_t V, int32_t K, mok_dtype type, const void* z, int64_t ldz,
+                            const int32_t* ids, const float* vals, float tau, const float* dloss, float* loss,
+                            float* lse, void* dz, int64_t lddz, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Token embedding and its gradient.
+ *
+ *   forward   out_n = scale * table[ids_n]              ([N, H] of table's type)
+ *   backward  dtable_v = scale * sum of dx_n over the n with ids_n = v, in f32
+ *             and in ascending n, rounded once
+ *
+ *   table  (device) [V, H] bf16 or f32;  ids (device) int32 [N]
+ *   dx     (device) [N, H] bf16 or f32
+ *   dtable (device) [V, H] bf16 or f32.  accumulate = 0: every row is written,
+ *          zeros where no token has the id.  accumulate = 1: the sum is added
+ *          to the rows that tokens have, in f32 (one rounding for bf16); no
+ *          other row is touched.
+ *   pad_id  tokens with this id take no part in the gradient; the lookup
+ *          still reads its row, or gives zeros if it lies outside [0, V).
+ *          Use MOK_EMBED_NO_PAD for none.
+ * Any other id outside [0, V) records MOK_ERR_BAD_INDEX: zeros in the lookup,
+ * no part in the gradient.  Any H >= 1, V >= 1; N = 0 does nothing (backward
+ * with accumulate = 0 still writes the zeros).  No float atomics: the same
+ * inputs give the same bits.  ws: mok_embed_workspace_size bytes for this V,
+ * H and at least this N, its first 256 bytes zeroed once by the caller; its
+ * first word holds errors until mok_check.
+ */
+#define MOK_EMBED_NO_PAD INT32_MIN
+size_t mok_embed_workspace_size(int32_t V, int32_t H, int32_t N);
+mok_status mok_embed_forward(int32_t V, int32_t H, int32_t N, mok_dtype type, const void* table, const int32_t* ids,
+                             int32_t pad_id, float scale, void* out, void* ws, size_t ws_bytes, void* stream);
+mok_status mok_embed_backward(int32_t V, int32_t H, int32_t N, mok_dtype dx_type, const void* dx, const int32_t* ids,
+                              int32_t pad_id, float scale, mok_dtype grad_type, void* dtable, int32_t accumulate,
+                              void* ws, size_t ws_bytes, void* stream);
 
 /* Synchronise `stream`, then return (and clear) the status recorded in the
  * workspace's error word; MOK_OK if none. */

@@ -37,10 +37,14 @@ EXPORTS = ["mok_workspace_size", "mok_ctx_size", "mok_workspace_layout", "mok_bu
            "mok_device_sm_count", "mok_status_string", "mok_version", "mok_trace_enable", "mok_trace_read",
            "mok_launch_count", "mok_build_schedule_noalloc", "mok_gemm_mxfp8", "mok_router_workspace_size",
            "mok_router_forward", "mok_router_backward", "mok_schedule_workspace_size", "mok_ep_first_expert",
-           "mok_ep_plan", "mok_ep_pack_rows", "mok_ep_combine_rows", "mok_ep_unsort_scores"]
+           "mok_ep_plan", "mok_ep_pack_rows", "mok_ep_combine_rows", "mok_ep_unsort_scores",
+           "mok_few_workspace_size", "mok_few_forward", "mok_few_layer", "mok_distill_workspace_size",
+           "mok_distill_forward", "mok_distill_backward", "mok_distill_step", "mok_embed_workspace_size",
+           "mok_embed_forward", "mok_embed_backward"]
 
 PHASES = ["schedule", "fwd_gemm", "fwd_combine", "bwd_da", "bwd_ds", "bwd_dx", "bwd_dx_combine", "bwd_wg13",
-          "bwd_wg2", "quant", "bwd_sort", "router_fwd", "router_bwd", "bwd_replay", "fwd_fused", "fwd_sort"]
+          "bwd_wg2", "quant", "bwd_sort", "router_fwd", "router_bwd", "bwd_replay", "fwd_fused", "fwd_sort",
+          "few", "distill", "embed_fwd", "embed_bwd"]
 
 
 class MokError(RuntimeError):
@@ -83,7 +87,7 @@ def _load():
     P = ctypes.c_void_p
     S = ctypes.POINTER(MokShape)
     C = ctypes.POINTER(MokConfig)
-    i32, sz = ctypes.c_int32, ctypes.c_size_t
+    i32, sz, i64, f32 = ctypes.c_int32, ctypes.c_size_t, ctypes.c_int64, ctypes.c_float
     sig = {
         "mok_workspace_size": (sz, [S, C, i32]),
         "mok_ctx_size": (sz, [S, C, i32]),
@@ -113,6 +117,16 @@ def _load():
         "mok_ep_pack_rows": (i32, [S, C, P, sz, P, P, P, P, P]),
         "mok_ep_combine_rows": (i32, [S, C, P, sz, P, P, P, P]),
         "mok_ep_unsort_scores": (i32, [S, C, P, sz, P, P, P]),
+        "mok_few_workspace_size": (sz, [S, i32]),
+        "mok_few_forward": (i32, [S, i32, P, sz, P, P, P, P, P, P, P, P]),
+        "mok_few_layer": (i32, [S, i32, P, sz, P, P, P, P, P, P, P, P, P, P]),
+        "mok_distill_workspace_size": (sz, [i32, i32, i32]),
+        "mok_distill_forward": (i32, [i32, i32, i32, i32, P, i64, P, P, f32, P, P, P, sz, P]),
+        "mok_distill_backward": (i32, [i32, i32, i32, i32, P, i64, P, P, f32, P, P, P, i64, P, sz, P]),
+        "mok_distill_step": (i32, [i32, i32, i32, i32, P, i64, P, P, f32, P, P, P, P, i64, P, sz, P]),
+        "mok_embed_workspace_size": (sz, [i32, i32, i32]),
+        "mok_embed_forward": (i32, [i32, i32, i32, i32, P, P, i32, f32, P, P, sz, P]),
+        "mok_embed_backward": (i32, [i32, i32, i32, i32, P, P, i32, f32, i32, P, i32, P, sz, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -321,3 +335,79 @@ def mok_ep_combine_rows(shape, cfg, ws, rows, scores, out, stream=None):
 def mok_ep_unsort_scores(shape, cfg, ws, row_vals, out, stream=None):
     _ok(LIB.mok_ep_unsort_scores(ctypes.byref(shape), ctypes.byref(cfg), _ptr(ws), ws.numel() * ws.element_size(),
                                  _ptr(row_vals), _ptr(out), _stream(stream)), "mok_ep_unsort_scores")
+
+
+# ---------------------------------------------------------------- few tokens, distillation, embedding
+MOK_FEW_MAX_TOKENS = 128
+MOK_DISTILL_MAX_TOP = 512
+MOK_EMBED_NO_PAD = -2**31
+MOK_TYPE_BF16 = 0
+MOK_TYPE_F32 = 1
+
+
+def dtype_of(t):
+    """mok_dtype of a tensor (None: neither of the two)."""
+    return {torch.bfloat16: MOK_TYPE_BF16, torch.float32: MOK_TYPE_F32}.get(t.dtype)
+
+
+def _rows_apart(t):
+    """Elements between a matrix's rows (a single row's stride says nothing)."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def mok_few_workspace_size(shape, prec=MOK_BF16):
+    return LIB.mok_few_workspace_size(ctypes.byref(shape), prec)
+
+
+def mok_few_forward(shape, prec, ws, topk_idx, x, scores, W1, W3, W2, out, stream=None):
+    _ok(LIB.mok_few_forward(ctypes.byref(shape), prec, _ptr(ws), ws.numel() * ws.element_size(), _ptr(topk_idx),
+                            _ptr(x), _ptr(scores), _ptr(W1), _ptr(W3), _ptr(W2), _ptr(out), _stream(stream)),
+        "mok_few_forward")
+
+
+def mok_few_layer(shape, prec, ws, x, Wr, bias, W1, W3, W2, topk_idx, scores, out, stream=None):
+    _ok(LIB.mok_few_layer(ctypes.byref(shape), prec, _ptr(ws), ws.numel() * ws.element_size(), _ptr(x), _ptr(Wr),
+                          _ptr(bias), _ptr(W1), _ptr(W3), _ptr(W2), _ptr(topk_idx), _ptr(scores), _ptr(out),
+                          _stream(stream)), "mok_few_layer")
+
+
+def mok_distill_workspace_size(T, V, K):
+    return LIB.mok_distill_workspace_size(T, V, K)
+
+
+def mok_distill_forward(z, ids, vals, tau, loss, lse, ws, stream=None):
+    (T, V), K = z.shape, ids.shape[1]
+    _ok(LIB.mok_distill_forward(T, V, K, dtype_of(z), _ptr(z), _rows_apart(z), _ptr(ids), _ptr(vals), tau, _ptr(loss),
+                                _ptr(lse), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)),
+        "mok_distill_forward")
+
+
+def mok_distill_backward(z, ids, vals, tau, lse, dloss, dz, ws, stream=None):
+    (T, V), K = z.shape, ids.shape[1]
+    _ok(LIB.mok_distill_backward(T, V, K, dtype_of(z), _ptr(z), _rows_apart(z), _ptr(ids), _ptr(vals), tau, _ptr(lse),
+                                 _ptr(dloss), _ptr(dz), _rows_apart(dz), _ptr(ws), ws.numel() * ws.element_size(),
+                                 _stream(stream)), "mok_distill_backward")
+
+
+def mok_distill_step(z, ids, vals, tau, dloss, loss, lse, dz, ws, stream=None):
+    (T, V), K = z.shape, ids.shape[1]
+    _ok(LIB.mok_distill_step(T, V, K, dtype_of(z), _ptr(z), _rows_apart(z), _ptr(ids), _ptr(vals), tau, _ptr(dloss),
+                             _ptr(loss), _ptr(lse), _ptr(dz), _rows_apart(dz), _ptr(ws), ws.numel() * ws.element_size(),
+                             _stream(stream)), "mok_distill_step")
+
+
+def mok_embed_workspace_size(V, H, N):
+    return LIB.mok_embed_workspace_size(V, H, N)
+
+
+def mok_embed_forward(table, ids, pad_id, scale, out, ws, stream=None):
+    V, H = table.shape
+    _ok(LIB.mok_embed_forward(V, H, ids.numel(), dtype_of(table), _ptr(table), _ptr(ids), pad_id, scale, _ptr(out),
+                              _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)), "mok_embed_forward")
+
+
+def mok_embed_backward(dx, ids, pad_id, scale, dtable, accumulate, ws, stream=None):
+    V, H = dtable.shape
+    _ok(LIB.mok_embed_backward(V, H, ids.numel(), dtype_of(dx), _ptr(dx), _ptr(ids), pad_id, scale, dtype_of(dtable),
+                               _ptr(dtable), int(bool(accumulate)), _ptr(ws), ws.numel() * ws.element_size(),
+                               _stream(stream)), "mok_embed_backward")

@@ -12,6 +12,9 @@
 
 #include <nvtx3/nvToolsExt.h>
 
+#include "distill.cuh"
+#include "embed.cuh"
+#include "few.cuh"
 #include "gemm.cuh"
 
 namespace mok {
@@ -170,7 +173,7 @@ const char* const kPhaseNames[MOK_NUM_PHASES] = {
     "mok schedule",  "mok fwd gemm",   "mok fwd combine", "mok bwd dA'",      "mok bwd ds",
     "mok bwd dX",    "mok bwd dX combine", "mok bwd dW1|dW3", "mok bwd dW2",   "mok mxfp8 quant",
     "mok bwd sort",  "mok router fwd", "mok router bwd",  "mok bwd replay",   "mok fwd fused",
-    "mok fwd sort"};
+    "mok fwd sort",  "mok few tokens", "mok distill",     "mok embed",        "mok embed grad"};
 
 class Phase {
  public:
@@ -1511,6 +1514,252 @@ mok_status mok_router_backward(const mok_shape* shape, void* rws, size_t rws_byt
                         s.T, 2, st));
   }
   return MOK_OK;
+}
+
+// ---------------------------------------------------------------- few tokens
+namespace {
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+mok_status check_few(const mok_shape* s, mok_precision prec) {
+  MOK_TRY(check_shape(s));
+  MOK_TRY(check_prec(prec));
+  return s->T > MOK_FEW_MAX_TOKENS ? MOK_ERR_UNSUPPORTED : MOK_OK;
+}
+
+mok_status few_params(const mok_shape& s, mok_precision prec, void* ws, size_t ws_bytes, const void* x, const void* W1,
+                      const void* W3, const void* W2, void* out, FewParams* p) {
+  if (!ws || !x || !W1 || !W3 || !W2 || !out) return MOK_ERR_INVALID_ARG;
+  if (!aligned16(ws) || !aligned16(x) || !aligned16(out)) return MOK_ERR_INVALID_ARG;
+  memset(p, 0, sizeof(*p));
+  const FewLayout L = few_layout(s, prec);
+  if (ws_bytes < L.total) return MOK_ERR_WORKSPACE_TOO_SMALL;
+  if (prec == MOK_MXFP8) {
+    if (!mx_ok(W1) || !mx_ok(W3) || !mx_ok(W2)) return MOK_ERR_INVALID_ARG;
+    p->W1 = as_mx(W1)->q;
+    p->W3 = as_mx(W3)->q;
+    p->W2 = as_mx(W2)->q;
+    p->sf1 = as_mx(W1)->scale;
+    p->sf3 = as_mx(W3)->scale;
+    p->sf2 = as_mx(W2)->scale;
+    if (!aligned16(p->sf1) || !aligned16(p->sf3) || !aligned16(p->sf2)) return MOK_ERR_INVALID_ARG;
+  } else {
+    p->W1 = W1;
+    p->W3 = W3;
+    p->W2 = W2;
+  }
+  if (!aligned16(p->W1) || !aligned16(p->W3) || !aligned16(p->W2)) return MOK_ERR_INVALID_ARG;
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  p->T = s.T;
+  p->H = s.H;
+  p->I = s.I;
+  p->E = s.E;
+  p->k = s.k;
+  p->hdr = reinterpret_cast<int32_t*>(w + L.header);
+  p->x = static_cast<const __nv_bfloat16*>(x);
+  p->out = static_cast<__nv_bfloat16*>(out);
+  p->logits = reinterpret_cast<float*>(w + L.logits);
+  p->xq = w + L.xq;
+  p->xsf = w + L.xsf;
+  p->a = w + L.a;
+  p->asf = w + L.asf;
+  return MOK_OK;
+}
+
+mok_status few_run(const FewParams& p, mok_precision prec, void* stream) {
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  Phase ph(MOK_PHASE_FEW, st, 0);
+  int launches = 0;
+  const cudaError_t e = launch_few(p, prec == MOK_MXFP8, &launches, st);
+  g_launches += launches;
+  return e == cudaSuccess ? MOK_OK : MOK_ERR_CUDA;
+}
+
+}  // namespace
+
+size_t mok_few_workspace_size(const mok_shape* shape, mok_precision prec) {
+  return check_few(shape, prec) == MOK_OK ? few_layout(*shape, prec).total : 0;
+}
+
+mok_status mok_few_forward(const mok_shape* shape, mok_precision prec, void* ws, size_t ws_bytes,
+                           const int32_t* topk_idx, const void* x, const float* scores, const void* W1,
+                           const void* W3, const void* W2, void* out, void* stream) {
+  MOK_TRY(check_few(shape, prec));
+  if (!topk_idx || !scores) return MOK_ERR_INVALID_ARG;
+  FewParams p;
+  MOK_TRY(few_params(*shape, prec, ws, ws_bytes, x, W1, W3, W2, out, &p));
+  p.idx = topk_idx;
+  p.scores = scores;
+  return few_run(p, prec, stream);
+}
+
+mok_status mok_few_layer(const mok_shape* shape, mok_precision prec, void* ws, size_t ws_bytes, const void* x,
+                         const void* Wr, const float* bias, const void* W1, const void* W3, const void* W2,
+                         int32_t* topk_idx, float* scores, void* out, void* stream) {
+  MOK_TRY(check_few(shape, prec));
+  if (shape->k > shape->E || !Wr || !topk_idx || !scores) return MOK_ERR_INVALID_ARG;
+  FewParams p;
+  MOK_TRY(few_params(*shape, prec, ws, ws_bytes, x, W1, W3, W2, out, &p));
+  p.Wr = static_cast<const __nv_bfloat16*>(Wr);
+  p.bias = bias;
+  p.idx = p.idx_out = topk_idx;
+  p.scores = p.scores_out = scores;
+  return few_run(p, prec, stream);
+}
+
+// ---------------------------------------------------------------- distillation
+namespace {
+
+mok_status check_dtype(mok_dtype t) { return t == MOK_TYPE_BF16 || t == MOK_TYPE_F32 ? MOK_OK : MOK_ERR_INVALID_ARG; }
+
+bool aligned_to(const void* p, mok_dtype t) {
+  return (reinterpret_cast<uintptr_t>(p) & (t == MOK_TYPE_BF16 ? 1 : 3)) == 0;
+}
+
+mok_status check_distill_sizes(int32_t T, int32_t V, int32_t K) {
+  if (T < 0 || V < 1 || K < 1) return MOK_ERR_INVALID_ARG;
+  return K > MOK_DISTILL_MAX_TOP ? MOK_ERR_UNSUPPORTED : MOK_OK;
+}
+
+mok_status distill(DistillMode mode, int32_t T, int32_t V, int32_t K, mok_dtype type, const void* z, int64_t ldz,
+                   const int32_t* ids, const float* vals, float tau, const float* lse_in, const float* dloss,
+                   float* loss, float* lse, void* dz, int64_t lddz, void* ws, size_t ws_bytes, void* stream) {
+  MOK_TRY(check_distill_sizes(T, V, K));
+  MOK_TRY(check_dtype(type));
+  if (!(tau > 0.0f) || isinf(tau) || isinf(1.0f / tau)) return MOK_ERR_INVALID_ARG;
+  if (T == 0) return MOK_OK;
+  if (!z || !ids || !vals || !ws || ldz < V || !aligned_to(z, type)) return MOK_ERR_INVALID_ARG;
+  if (mode != DISTILL_BACKWARD && (!loss || !lse)) return MOK_ERR_INVALID_ARG;
+  if (mode == DISTILL_BACKWARD && !lse_in) return MOK_ERR_INVALID_ARG;
+  if (mode != DISTILL_FORWARD && (!dloss || !dz || lddz < V || !aligned_to(dz, type))) return MOK_ERR_INVALID_ARG;
+  if (ws_bytes < mok_distill_workspace_size(T, V, K)) return MOK_ERR_WORKSPACE_TOO_SMALL;
+  DistillParams p;
+  memset(&p, 0, sizeof(p));
+  p.T = T;
+  p.V = V;
+  p.K = K;
+  p.z = z;
+  p.ldz = ldz;
+  p.ids = ids;
+  p.vals = vals;
+  p.inv_tau = 1.0f / tau;
+  p.lse_in = lse_in;
+  p.dloss = dloss;
+  p.loss = loss;
+  p.lse = lse;
+  p.dz = dz;
+  p.lddz = lddz;
+  p.hdr = static_cast<int32_t*>(ws);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  Phase ph(MOK_PHASE_DISTILL, st, 0);
+  int launches = 0;
+  const cudaError_t e = launch_distill(mode, type, p, &launches, st);
+  g_launches += launches;
+  return e == cudaSuccess ? MOK_OK : MOK_ERR_CUDA;
+}
+
+}  // namespace
+
+size_t mok_distill_workspace_size(int32_t T, int32_t V, int32_t K) {
+  return check_distill_sizes(T, V, K) == MOK_OK ? kHeaderWords * 4 : 0;
+}
+
+mok_status mok_distill_forward(int32_t T, int32_t V, int32_t K, mok_dtype type, const void* z, int64_t ldz,
+                               const int32_t* ids, const float* vals, float tau, float* loss, float* lse, void* ws,
+                               size_t ws_bytes, void* stream) {
+  return distill(DISTILL_FORWARD, T, V, K, type, z, ldz, ids, vals, tau, nullptr, nullptr, loss, lse, nullptr, 0, ws,
+                 ws_bytes, stream);
+}
+
+mok_status mok_distill_backward(int32_t T, int32_t V, int32_t K, mok_dtype type, const void* z, int64_t ldz,
+                                const int32_t* ids, const float* vals, float tau, const float* lse,
+                                const float* dloss, void* dz, int64_t lddz, void* ws, size_t ws_bytes, void* stream) {
+  return distill(DISTILL_BACKWARD, T, V, K, type, z, ldz, ids, vals, tau, lse, dloss, nullptr, nullptr, dz, lddz, ws,
+                 ws_bytes, stream);
+}
+
+mok_status mok_distill_step(int32_t T, int32_t V, int32_t K, mok_dtype type, const void* z, int64_t ldz,
+                            const int32_t* ids, const float* vals, float tau, const float* dloss, float* loss,
+                            float* lse, void* dz, int64_t lddz, void* ws, size_t ws_bytes, void* stream) {
+  return distill(DISTILL_STEP, T, V, K, type, z, ldz, ids, vals, tau, nullptr, dloss, loss, lse, dz, lddz, ws,
+                 ws_bytes, stream);
+}
+
+// ---------------------------------------------------------------- embedding
+namespace {
+
+mok_status check_embed_sizes(int32_t V, int32_t H, int32_t N) {
+  if (V < 1 || H < 1 || N < 0) return MOK_ERR_INVALID_ARG;
+  // ids sort as keys 0 .. V; tokens and rows are int32
+  return V > (1 << 30) || N > (1 << 30) || H > (1 << 20) ? MOK_ERR_UNSUPPORTED : MOK_OK;
+}
+
+mok_status embed_params(int32_t V, int32_t H, int32_t N, const int32_t* ids, int32_t pad_id, float scale, void* ws,
+                        size_t ws_bytes, EmbedParams* p) {
+  if (!ws || !aligned16(ws) || (N > 0 && !ids)) return MOK_ERR_INVALID_ARG;
+  const EmbedLayout L = embed_layout(V, H, N);
+  if (ws_bytes < L.total) return MOK_ERR_WORKSPACE_TOO_SMALL;
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  memset(p, 0, sizeof(*p));
+  p->V = V;
+  p->H = H;
+  p->N = N;
+  p->ids = ids;
+  p->pad_id = pad_id;
+  p->scale = scale;
+  p->hdr = reinterpret_cast<int32_t*>(w + L.header);
+  for (int i = 0; i < 2; ++i) {
+    p->key[i] = reinterpret_cast<int32_t*>(w + L.key[i]);
+    p->pos[i] = reinterpret_cast<int32_t*>(w + L.pos[i]);
+  }
+  p->part = reinterpret_cast<float*>(w + L.part);
+  return MOK_OK;
+}
+
+}  // namespace
+
+size_t mok_embed_workspace_size(int32_t V, int32_t H, int32_t N) {
+  return check_embed_sizes(V, H, N) == MOK_OK ? embed_layout(V, H, N).total : 0;
+}
+
+mok_status mok_embed_forward(int32_t V, int32_t H, int32_t N, mok_dtype type, const void* table, const int32_t* ids,
+                             int32_t pad_id, float scale, void* out, void* ws, size_t ws_bytes, void* stream) {
+  MOK_TRY(check_embed_sizes(V, H, N));
+  MOK_TRY(check_dtype(type));
+  EmbedParams p;
+  MOK_TRY(embed_params(V, H, N, ids, pad_id, scale, ws, ws_bytes, &p));
+  if (N == 0) return MOK_OK;
+  if (!table || !out || !aligned_to(table, type) || !aligned_to(out, type)) return MOK_ERR_INVALID_ARG;
+  p.table = table;
+  p.out = out;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  Phase ph(MOK_PHASE_EMBED_FWD, st, 0);
+  int launches = 0;
+  const cudaError_t e = launch_embed_forward(type, p, &launches, st);
+  g_launches += launches;
+  return e == cudaSuccess ? MOK_OK : MOK_ERR_CUDA;
+}
+
+mok_status mok_embed_backward(int32_t V, int32_t H, int32_t N, mok_dtype dx_type, const void* dx, const int32_t* ids,
+                              int32_t pad_id, float scale, mok_dtype grad_type, void* dtable, int32_t accumulate,
+                              void* ws, size_t ws_bytes, void* stream) {
+  MOK_TRY(check_embed_sizes(V, H, N));
+  MOK_TRY(check_dtype(dx_type));
+  MOK_TRY(check_dtype(grad_type));
+  if (accumulate != 0 && accumulate != 1) return MOK_ERR_INVALID_ARG;
+  EmbedParams p;
+  MOK_TRY(embed_params(V, H, N, ids, pad_id, scale, ws, ws_bytes, &p));
+  if (!dtable || !aligned_to(dtable, grad_type)) return MOK_ERR_INVALID_ARG;
+  if (N > 0 && (!dx || !aligned_to(dx, dx_type))) return MOK_ERR_INVALID_ARG;
+  p.dx = dx;
+  p.dtable = dtable;
+  p.accumulate = accumulate;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  Phase ph(MOK_PHASE_EMBED_BWD, st, 0);
+  int launches = 0;
+  const cudaError_t e = launch_embed_backward(dx_type, grad_type, p, &launches, st);
+  g_launches += launches;
+  return e == cudaSuccess ? MOK_OK : MOK_ERR_CUDA;
 }
 
 mok_status mok_check(void* ws, void* stream) {

@@ -1,0 +1,81 @@
+"""Distillation loss from a teacher's top logits (mok_distill_*; no compute here)."""
+
+from __future__ import annotations
+
+import torch
+
+from . import _lib
+from ._check import on, require, tensor
+
+_TYPES = (torch.bfloat16, torch.float32)
+
+
+class DistillLoss:
+    """KL(p || softmax(z / temperature)) per row, p the softmax of the
+    teacher's listed logits / temperature over the list, for up to ``rows``
+    rows of ``vocab`` student logits (bf16 or f32, rows any distance apart)
+    and lists of up to ``top`` (id, value) pairs; an id of -1 leaves its entry
+    out.  Rows are weighted by ``dloss`` in the gradient.  Errors found on the
+    device (an id outside the vocabulary) are raised by ``check``."""
+
+    def __init__(self, rows, vocab, top, device="cuda"):
+        self.rows, self.vocab, self.top = rows, vocab, top
+        self.device = on(device)
+        n = _lib.mok_distill_workspace_size(rows, vocab, top)
+        if n == 0:
+            raise _lib.MokError(2, "unsupported sizes")
+        self.ws = torch.zeros(n, dtype=torch.uint8, device=self.device)
+
+    def _begin(self, z, ids, vals, temperature):
+        require(isinstance(z, torch.Tensor) and z.dim() == 2 and z.shape[0] <= self.rows,
+                f"z: at most {self.rows} rows of {self.vocab} are wanted")
+        require(isinstance(ids, torch.Tensor) and ids.dim() == 2 and 1 <= ids.shape[1] <= self.top,
+                f"ids: lists of 1 to {self.top} entries are wanted")
+        T, K = z.shape[0], ids.shape[1]
+        tensor(z, "z", (T, self.vocab), _TYPES, self.device, rows_apart=True)
+        tensor(ids, "ids", (T, K), (torch.int32,), self.device)
+        tensor(vals, "vals", (T, K), (torch.float32,), self.device)
+        tau = float(temperature)
+        require(0.0 < tau < float("inf"), f"temperature: {tau}, wanted a positive number")
+        return T, tau
+
+    def _row_values(self, T, **named):
+        for name, t in named.items():
+            tensor(t, name, (T,), (torch.float32,), self.device)
+
+    def _gradient(self, z, out):
+        if out is None:
+            return torch.empty(z.shape, dtype=z.dtype, device=self.device)
+        return tensor(out, "out", z.shape, (z.dtype,), self.device, rows_apart=True)
+
+    def forward(self, z, ids, vals, temperature=1.0, stream=None):
+        """(loss, lse), f32 [T] each."""
+        T, tau = self._begin(z, ids, vals, temperature)
+        loss = torch.empty(T, dtype=torch.float32, device=self.device)
+        lse = torch.empty(T, dtype=torch.float32, device=self.device)
+        _lib.mok_distill_forward(z, ids, vals, tau, loss, lse, self.ws, stream)
+        return loss, lse
+
+    def backward(self, z, ids, vals, lse, dloss, temperature=1.0, out=None, stream=None):
+        """dz of z's type, from the forward's ``lse``; ``out`` may be z itself."""
+        T, tau = self._begin(z, ids, vals, temperature)
+        self._row_values(T, lse=lse, dloss=dloss)
+        dz = self._gradient(z, out)
+        _lib.mok_distill_backward(z, ids, vals, tau, lse, dloss, dz, self.ws, stream)
+        return dz
+
+    def forward_backward(self, z, ids, vals, dloss, temperature=1.0, out=None, stream=None):
+        """(loss, dz) in one call; ``out`` may be z itself."""
+        T, tau = self._begin(z, ids, vals, temperature)
+        self._row_values(T, dloss=dloss)
+        dz = self._gradient(z, out)
+        loss = torch.empty(T, dtype=torch.float32, device=self.device)
+        lse = torch.empty(T, dtype=torch.float32, device=self.device)
+        _lib.mok_distill_step(z, ids, vals, tau, dloss, loss, lse, dz, self.ws, stream)
+        return loss, dz
+
+    def check(self, stream=None):
+        """Synchronise and raise if the device recorded an error."""
+        st = _lib.mok_check(self.ws, stream)
+        if st != 0:
+            raise _lib.MokError(st, "distillation: device status")
