@@ -557,7 +557,7 @@ mok_status mok_ep_unsort_scores(const mok_shape* shape, const mok_config* cfg, c
 
 /*
  * The layer for a few tokens: what mok_forward computes, for serving steps of
- * 1 <= T <= MOK_FEW_MAX_TOKENS tokens, without a schedule, a padded copy of
+ * 1 <= T <= MOK_FEW_MAX_TOKENS tokens and H <= MOK_FEW_MAX_HIDDEN, without a schedule, a padded copy of
  * the rows or a forward context -- nothing is kept for a backward.  A pass
  * reads the weights of the experts that the tokens chose and no others.
  *
@@ -569,9 +569,9 @@ mok_status mok_ep_unsort_scores(const mok_shape* shape, const mok_config* cfg, c
  *                    to the lower expert); needs k <= E
  *   x     (device) bf16 [T, H];  out (device) bf16 [T, H]
  *   W1, W3, W2   as for mok_forward in the given precision
- * h, u and y stay in f32; a = silu(h) * u is rounded to bf16 (MXFP8: x along
- * H and a along I are quantised per 32, by the rule of mok_mxfp8_quantize);
- * out is summed in f32 over j in increasing order and rounded once.  The
+ * h, u and y are f32 sums.  BF16: a = silu(h) * u enters the second GEMM as two
+ * bf16 (its rounding and what that left).  MXFP8: x along H and a along I are
+ * quantised per 32, by the rule of mok_mxfp8_quantize.  out is summed in f32 over j in increasing order and rounded once.  The
  * order of the sums over H and I depends on the whole call's routing, so a
  * token's last bits may depend on the tokens beside it; a call repeated with
  * the same inputs gives the same bits.
@@ -588,6 +588,7 @@ mok_status mok_ep_unsort_scores(const mok_shape* shape, const mok_config* cfg, c
  * aligned (MOK_ERR_INVALID_ARG otherwise).
  */
 #define MOK_FEW_MAX_TOKENS 128
+#define MOK_FEW_MAX_HIDDEN 32768
 size_t mok_few_workspace_size(const mok_shape* shape, mok_precision prec);
 mok_status mok_few_forward(const mok_shape* shape, mok_precision prec, void* ws, size_t ws_bytes,
                            const int32_t* topk_idx, const void* x, const float* scores, const void* W1,

@@ -1524,7 +1524,7 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 
 mok_status check_few(const mok_shape* s, mok_precision prec) {
   MOK_TRY(check_shape(s));
   MOK_TRY(check_prec(prec));
-  return s->T > MOK_FEW_MAX_TOKENS ? MOK_ERR_UNSUPPORTED : MOK_OK;
+  return s->T > MOK_FEW_MAX_TOKENS || s->H > MOK_FEW_MAX_HIDDEN ? MOK_ERR_UNSUPPORTED : MOK_OK;
 }
 
 mok_status few_params(const mok_shape& s, mok_precision prec, void* ws, size_t ws_bytes, const void* x, const void* W1,
@@ -1563,6 +1563,10 @@ mok_status few_params(const mok_shape& s, mok_precision prec, void* ws, size_t w
   p->xsf = w + L.xsf;
   p->a = w + L.a;
   p->asf = w + L.asf;
+  p->tile_count = reinterpret_cast<int32_t*>(w + L.tiles);
+  p->col_count = p->tile_count + L.tile_words;
+  p->part = reinterpret_cast<float*>(w + L.part);
+  p->y = reinterpret_cast<float*>(w + L.y);
   return MOK_OK;
 }
 

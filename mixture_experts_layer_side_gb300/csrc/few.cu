@@ -1,115 +1,842 @@
 // The layer for a few tokens (T <= MOK_FEW_MAX_TOKENS): routed SwiGLU experts
-// and combine, with or without the router, for serving steps.
+// and combine, with or without the router, in one launch.
 //
 //   h = x_t W1_e,  u = x_t W3_e,  a = silu(h) * u,  y = a W2_e,  e = idx[t, j]
 //   out_t = sum_j s[t, j] y_(t, j)
 //
-// One thread per output column walks the contraction: consecutive threads
-// read consecutive columns of a weight row.
-#include <cuda_fp8.h>
+// What bounds it is the read of the chosen experts' weights: a row or two of
+// tokens per expert is a few operations for each weight.  The design streams
+// weights without a pause:
+//
+//  * The weight is the MMA's A operand (128 output columns by K, straight
+//    from its row-major layout) and the tokens its B operand (N = 16 to 64 of
+//    them), so the tensor core takes weights from shared memory as TMA brings
+//    them and no thread touches one.
+//  * One CTA per SM.  A "unit" is up to unit_rows rows of one expert; a tile
+//    is 2 x 128 output columns of a unit (first GEMM: 128 of h and the same
+//    of u; second: 256 of y); a block is 64 (MXFP8: 128) of a tile's K.  All
+//    blocks of a GEMM, tiles in order, are cut into equal runs, one per CTA,
+//    whatever the number of experts: no SM waits for a last wave.  A tile
+//    that a cut splits leaves f32 sums in the workspace; the last of its CTAs
+//    to arrive adds them in the order of K.
+//  * The second GEMM needs all of a, but its weights do not: each CTA's ring
+//    of stages fills with W2 while the last tiles of a are finished.
+//  * Every CTA sorts the routing by expert for itself (at most 4,096 ids), so
+//    no launch or barrier stands between the routing and the first weight.
+//
+// The number of arrivals that a CTA waits for is counted in the workspace and
+// every CTA has to be resident: the launch is cooperative.  All waits are
+// bounded (MOK_ERR_TIMEOUT).  The counters are zero again when a call ends.
+#include <string.h>
 
 #include "few.cuh"
 #include "mx.cuh"
+#include "tc.cuh"
+#include "topk.cuh"
 
 namespace mok {
 
 namespace {
 
-__device__ __forceinline__ float e4m3_value(uint8_t q) {
-  __nv_fp8_e4m3 v;
-  v.__x = q;
-  return static_cast<float>(v);
+constexpr int kMaxFewStages = 8;
+constexpr int kATile = 128 * 128;      // one A operand: 128 output columns x 128 bytes of K
+constexpr int kSfBytes = 1024 + 1024 + 512;  // MXFP8, per stage: raw and tiled A scales (two tiles), B scales
+constexpr int kProducers = 64;         // threads that bring the tokens' operand
+constexpr int kEpilogue = 128;
+constexpr int kLogitTokens = 8;        // tokens side by side in the router's logits
+
+// header words
+constexpr int kWordPrepared = kHdrCounters;      // CTAs done with the logits' parts and x's quantisation
+constexpr int kWordRouted = kHdrCounters + 1;    // tokens routed
+constexpr int kWordHidden = kHdrCounters + 2;    // tiles of a finished
+constexpr int kWordLeft = kHdrCounters + 3;      // CTAs that ended
+
+struct Ctl {
+  uint64_t full_a[kMaxFewStages], full_b[kMaxFewStages], scales[kMaxFewStages], empty[kMaxFewStages];
+  uint64_t tfull[2], tempty[2], drained;
+  uint32_t tmem;
+  int abort, go;
+  int units;
+  int flag[2];
+};
+
+// The routing sorted by expert, in shared memory.
+struct Schedule {
+  int32_t* offset;  // [E + 1] sorted rows of each expert
+  uint16_t* perm;   // [T*k] sorted row -> flat index
+  uint16_t* unit_e; // [max_units] expert, first sorted row and rows of each unit
+  uint16_t* unit_r;
+  uint8_t* unit_n;
+};
+
+__host__ __device__ constexpr size_t schedule_bytes(int E, int R, int units) {
+  return (size_t)(E + 1) * 8 + (((size_t)R * 2 + 15) & ~15) + (size_t)units * 5 + 64;
 }
 
-// E8M0 scale: 2^(code - 127); 2^-127 is a subnormal float
-__device__ __forceinline__ float e8m0_value(uint8_t s) {
-  return s ? __int_as_float((int)s << 23) : __int_as_float(0x00400000);
-}
+// One GEMM cut into runs of blocks.
+struct Cut {
+  int tiles_per_unit, kb;  // column tiles, blocks along K
+  long blocks;
+  int ctas;                // that take part
+  __device__ long begin(int c) const { return blocks * c / ctas; }
+  // the CTA whose run holds block b
+  __device__ int owner(long b) const { return (int)(((b + 1) * ctas - 1) / blocks); }
+};
 
-// MXFP8: x [T, H] as the values its quantisation along H stands for.
-__global__ void few_quant_x_kernel(int nblocks, const __nv_bfloat16* __restrict__ x, uint8_t* __restrict__ q,
-                                   uint8_t* __restrict__ sf) {
-  const int b = blockIdx.x * blockDim.x + threadIdx.x;
-  if (b >= nblocks) return;
-  float v[32];
-  for (int i = 0; i < 32; ++i) v[i] = __bfloat162float(x[(long)b * 32 + i]);
-  uint32_t codes[8];
-  sf[b] = mx_quant32(v, codes);
-  for (int i = 0; i < 8; ++i) reinterpret_cast<uint32_t*>(q + (long)b * 32)[i] = codes[i];
-}
+// A run's share of one tile.
+struct Seg {
+  int unit, n;    // unit and column tile
+  int tile;       // index of its counter
+  int k0, k1;     // blocks
+};
 
-template <bool MX>
-__device__ __forceinline__ float row_value(const void* rows, const uint8_t* sf, long row, int K, int i) {
-  if (MX)
-    return e4m3_value(static_cast<const uint8_t*>(rows)[row * K + i]) * e8m0_value(sf[row * (K / 32) + i / 32]);
-  return __bfloat162float(static_cast<const __nv_bfloat16*>(rows)[row * K + i]);
-}
-
-template <bool MX>
-__device__ __forceinline__ float weight_value(const void* w, const uint8_t* sf, long e, int K, int N, int i, int n) {
-  if (MX)
-    return e4m3_value(static_cast<const uint8_t*>(w)[(e * K + i) * N + n]) *
-           e8m0_value(sf[(e * (K / 32) + i / 32) * N + n]);
-  return __bfloat162float(static_cast<const __nv_bfloat16*>(w)[(e * K + i) * N + n]);
-}
-
-// a of one routed row f and 128 intermediate columns
-template <bool MX>
-__global__ void __launch_bounds__(128) few_hidden_kernel(FewParams p) {
-  const int f = blockIdx.y, n = blockIdx.x * 128 + threadIdx.x;
-  const int e = p.idx[f];
-  if (e < 0 || e >= p.E) {
-    if (threadIdx.x == 0 && blockIdx.x == 0) atomicOr(p.hdr + kHdrError, MOK_ERRBIT_BAD_INDEX);
-    return;
-  }
-  const long t = f / p.k;
-  float h = 0.0f, u = 0.0f;
-  for (int i = 0; i < p.H; ++i) {
-    const float xv = row_value<MX>(MX ? (const void*)p.xq : p.x, p.xsf, t, p.H, i);
-    h = fmaf(xv, weight_value<MX>(p.W1, p.sf1, e, p.H, p.I, i, n), h);
-    u = fmaf(xv, weight_value<MX>(p.W3, p.sf3, e, p.H, p.I, i, n), u);
-  }
-  const float a = h / (1.0f + __expf(-h)) * u;
-  if (MX) {
-    // a warp's 32 columns are one block
-    const float amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(a))));
-    const int X = mx_block_exponent(amax);
-    static_cast<uint8_t*>(p.a)[(long)f * p.I + n] = (uint8_t)mx_cvt_e4m3x2(a * mx_exp2_int(-X), 0.0f);
-    if ((threadIdx.x & 31) == 0) p.asf[(long)f * (p.I / 32) + n / 32] = (uint8_t)(X + 127);
+// `by_column`: tiles ordered column tile first (so that columns of out are
+// finished one after another), else unit first.
+__device__ __forceinline__ Seg seg_at(const Cut& c, long b, long end, int units, bool by_column) {
+  Seg s;
+  s.tile = (int)(b / c.kb);
+  s.k0 = (int)(b - (long)s.tile * c.kb);
+  s.k1 = (int)(end - b < c.kb - s.k0 ? s.k0 + (end - b) : c.kb);
+  if (by_column) {
+    s.n = s.tile / units;
+    s.unit = s.tile - s.n * units;
   } else {
-    static_cast<__nv_bfloat16*>(p.a)[(long)f * p.I + n] = __float2bfloat16(a);
+    s.unit = s.tile / c.tiles_per_unit;
+    s.n = s.tile - s.unit * c.tiles_per_unit;
+  }
+  return s;
+}
+
+__device__ __forceinline__ bool vote_all(int bar, int threads, bool ok) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "barrier.red.and.pred q, %2, %3, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(ok ? 1u : 0u), "r"(bar), "r"(threads)
+      : "memory");
+  return r != 0;
+}
+
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+__device__ __forceinline__ void cp_async_arrive_noinc(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+__device__ __forceinline__ uint32_t* word(const FewParams& p, int i) { return reinterpret_cast<uint32_t*>(p.hdr + i); }
+
+// ---------------------------------------------------------------- router
+// This CTA's part of the logits: kLogitTokens tokens by h_rows rows of Wr.
+// A warp takes every other row, a lane 8 neighbouring experts; the warps'
+// sums are added in order.
+__device__ void router_logits(const FewParams& p, uint8_t* smem, int nthreads) {
+  const int groups = (p.T + kLogitTokens - 1) / kLogitTokens;
+  const int warps = nthreads / 32, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int part = blockIdx.x / groups, t0 = (blockIdx.x % groups) * kLogitTokens;
+  if (part >= p.h_parts) return;
+  const int nt = min(kLogitTokens, p.T - t0);
+  const int h0 = part * p.h_rows, rows = min(p.h_rows, p.H - h0);
+  float* xs = reinterpret_cast<float*>(smem);                 // [h_rows][kLogitTokens]
+  float* red = xs + (size_t)p.h_rows * kLogitTokens;          // [warps][kLogitTokens][256]
+  for (int i = threadIdx.x; i < rows * kLogitTokens; i += nthreads) {
+    const int t = i / rows, h = i - t * rows;
+    xs[h * kLogitTokens + t] = t < nt ? __bfloat162float(p.x[(long)(t0 + t) * p.H + h0 + h]) : 0.0f;
+  }
+  __syncthreads();
+  const bool vec = p.E % 8 == 0 && (reinterpret_cast<uintptr_t>(p.Wr) & 15) == 0;
+  for (int e0 = 0; e0 < p.E; e0 += 256) {
+    const int e = e0 + lane * 8;
+    float acc[kLogitTokens][8];
+#pragma unroll
+    for (int t = 0; t < kLogitTokens; ++t)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc[t][i] = 0.0f;
+#pragma unroll 4
+    for (int h = warp; h < rows; h += warps) {
+      const __nv_bfloat16* wr = p.Wr + (long)(h0 + h) * p.E + e;
+      float w[8];
+      if (vec) {
+        const uint4 v = e < p.E ? __ldg(reinterpret_cast<const uint4*>(wr)) : make_uint4(0, 0, 0, 0);
+        const uint32_t vv[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          w[2 * i] = __uint_as_float(vv[i] << 16);
+          w[2 * i + 1] = __uint_as_float(vv[i] & 0xffff0000u);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = e + i < p.E ? __bfloat162float(wr[i]) : 0.0f;
+      }
+      const float4* xv = reinterpret_cast<const float4*>(xs + h * kLogitTokens);
+      const float4 xa = xv[0], xb = xv[1];
+      const float xt[kLogitTokens] = {xa.x, xa.y, xa.z, xa.w, xb.x, xb.y, xb.z, xb.w};
+#pragma unroll
+      for (int t = 0; t < kLogitTokens; ++t)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[t][i] = fmaf(xt[t], w[i], acc[t][i]);
+    }
+#pragma unroll
+    for (int t = 0; t < kLogitTokens; ++t)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) red[(warp * kLogitTokens + t) * 256 + lane * 8 + i] = acc[t][i];
+    __syncthreads();
+    const int ne = min(256, p.E - e0);
+    for (int i = threadIdx.x; i < nt * 256; i += nthreads) {
+      const int t = i >> 8, c = i & 255;
+      if (c >= ne) continue;
+      float s = 0.0f;
+      for (int w = 0; w < warps; ++w) s += red[(w * kLogitTokens + t) * 256 + c];
+      p.logits[((long)part * p.T + t0 + t) * p.E + e0 + c] = s;
+    }
+    __syncthreads();
   }
 }
 
-// out of one token and 128 columns: y of its k experts, combined in f32 in
-// increasing j and rounded once
-template <bool MX>
-__global__ void __launch_bounds__(128) few_out_kernel(FewParams p) {
-  const int t = blockIdx.y, n = blockIdx.x * 128 + threadIdx.x;
-  float acc = 0.0f;
-  for (int j = 0; j < p.k; ++j) {
-    const long f = (long)t * p.k + j;
+// Selection and scores of one token from the parts of its logits.
+__device__ void router_select(const FewParams& p, int t, float* row, int nthreads) {
+  for (int e = threadIdx.x; e < p.E; e += nthreads) {
+    float s = 0.0f;
+#pragma unroll 8
+    for (int i = 0; i < p.h_parts; ++i) s += __ldcg(p.logits + ((long)i * p.T + t) * p.E + e);
+    row[e] = s;
+  }
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x;
+    int e;
+    float s;
+    if (p.E <= 256)
+      topk_softmax_warp<8>(row, p.bias, p.E, p.k, lane, e, s);
+    else
+      topk_softmax_warp<kMaxRouterExperts / 32>(row, p.bias, p.E, p.k, lane, e, s);
+    if (lane < p.k) {
+      p.idx_out[(long)t * p.k + lane] = e;
+      p.scores_out[(long)t * p.k + lane] = s;
+    }
+    __threadfence();
+    __syncwarp();
+    if (lane == 0) red_release_gpu_add(word(p, kWordRouted), 1u);
+  }
+  __syncthreads();
+}
+
+// MXFP8: x quantised along H, one thread per block of 32.
+__device__ void quantize_x(const FewParams& p, int nthreads) {
+  const int n = p.T * (p.H / 32);
+  for (int b = blockIdx.x * nthreads + threadIdx.x; b < n; b += gridDim.x * nthreads) {
+    const uint4* s = reinterpret_cast<const uint4*>(p.x + (long)b * 32);
+    float v[32];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint4 w = s[i];
+      const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        v[8 * i + 2 * j] = __uint_as_float(ww[j] << 16);
+        v[8 * i + 2 * j + 1] = __uint_as_float(ww[j] & 0xffff0000u);
+      }
+    }
+    uint32_t codes[8];
+    p.xsf[b] = mx_quant32(v, codes);
+    uint4* d = reinterpret_cast<uint4*>(p.xq + (long)b * 32);
+    d[0] = make_uint4(codes[0], codes[1], codes[2], codes[3]);
+    d[1] = make_uint4(codes[4], codes[5], codes[6], codes[7]);
+  }
+}
+
+// ---------------------------------------------------------------- schedule
+// Rows grouped by expert in ascending flat index, and cut into units.
+__device__ void build_units(const FewParams& p, const Schedule& s, int32_t* cursor, Ctl* ctl, int nthreads) {
+  const int R = p.T * p.k;
+  for (int e = threadIdx.x; e < p.E; e += nthreads) cursor[e] = 0;
+  __syncthreads();
+  bool bad = false;
+  for (int f = threadIdx.x; f < R; f += nthreads) {
     const int e = p.idx[f];
-    if (e < 0 || e >= p.E) continue;
-    float y = 0.0f;
-    for (int i = 0; i < p.I; ++i)
-      y = fmaf(row_value<MX>(p.a, p.asf, f, p.I, i), weight_value<MX>(p.W2, p.sf2, e, p.I, p.H, i, n), y);
-    acc = fmaf(p.scores[f], y, acc);
+    if (e >= 0 && e < p.E)
+      atomicAdd(&cursor[e], 1);
+    else
+      bad = true;
   }
-  p.out[(long)t * p.H + n] = __float2bfloat16(acc);
+  if (bad && blockIdx.x == 0) atomicOr(p.hdr + kHdrError, MOK_ERRBIT_BAD_INDEX);
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x;
+    int rows = 0, units = 0;
+    for (int e0 = 0; e0 < p.E; e0 += 32) {
+      const int e = e0 + lane;
+      const int c = e < p.E ? cursor[e] : 0;
+      const int u = (c + p.unit_rows - 1) / p.unit_rows;
+      int ic = c, iu = u;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int vc = __shfl_up_sync(0xffffffffu, ic, o), vu = __shfl_up_sync(0xffffffffu, iu, o);
+        if (lane >= o) {
+          ic += vc;
+          iu += vu;
+        }
+      }
+      const int off = rows + ic - c;
+      if (e < p.E) {
+        s.offset[e] = off;
+        cursor[e] = off;
+      }
+      for (int i = 0; i < u; ++i) {
+        const int at = units + iu - u + i;
+        s.unit_e[at] = (uint16_t)e;
+        s.unit_r[at] = (uint16_t)(off + i * p.unit_rows);
+        s.unit_n[at] = (uint8_t)min(p.unit_rows, c - i * p.unit_rows);
+      }
+      rows += __shfl_sync(0xffffffffu, ic, 31);
+      units += __shfl_sync(0xffffffffu, iu, 31);
+    }
+    __syncwarp();
+    for (int f0 = 0; f0 < R; f0 += 32) {
+      const int f = f0 + lane;
+      int e = f < R ? p.idx[f] : -1;
+      if (e < 0 || e >= p.E) e = -1;
+      const uint32_t same = __match_any_sync(0xffffffffu, e);
+      const int ahead = __popc(same & ((1u << lane) - 1u));
+      const int at = e >= 0 ? cursor[e] + ahead : 0;
+      __syncwarp();
+      if (e >= 0) {
+        s.perm[at] = (uint16_t)f;
+        if (ahead == 0) cursor[e] += __popc(same);
+      }
+      __syncwarp();
+    }
+    if (lane == 0) ctl->units = units;
+  }
+  __syncthreads();
 }
 
-// Router logits of one token: a warp per 32 experts, x row and Wr column-wise.
-__global__ void __launch_bounds__(256) few_logits_kernel(FewParams p) {
-  const int t = blockIdx.y, e = blockIdx.x * 256 + threadIdx.x;
-  if (e >= p.E) return;
-  float l = 0.0f;
-  for (int i = 0; i < p.H; ++i)
-    l = fmaf(__bfloat162float(p.x[(long)t * p.H + i]), __bfloat162float(p.Wr[(long)i * p.E + e]), l);
-  p.logits[(long)t * p.E + e] = l;
+// ---------------------------------------------------------------- epilogue
+__device__ __forceinline__ float silu_mul(float h, float u) { return h / (1.0f + __expf(-h)) * u; }
+
+// a of 16 rows in column `col` (a lane's): bf16 and what its rounding left
+// (so that y is that of an f32 a), or codes and a scale per 32 columns.
+template <bool MX>
+__device__ __forceinline__ void store_hidden(const FewParams& p, int row, int n, int col, int lane, const float* h,
+                                             const float* u) {
+  if constexpr (MX) {
+    uint8_t* q = static_cast<uint8_t*>(p.a);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      if (i >= n) break;
+      const float a = silu_mul(h[i], u[i]);
+      const float amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(a))));
+      const int X = mx_block_exponent(amax);
+      q[(long)(row + i) * p.I + col] = (uint8_t)mx_cvt_e4m3x2(a * mx_exp2_int(-X), 0.0f);
+      if (lane == 0) p.asf[(long)(row + i) * (p.I / 32) + col / 32] = (uint8_t)(X + 127);
+    }
+  } else {
+    __nv_bfloat16* hi = static_cast<__nv_bfloat16*>(p.a);
+    __nv_bfloat16* lo = hi + (long)p.T * p.k * p.I;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      if (i >= n) break;
+      const float a = silu_mul(h[i], u[i]);
+      const __nv_bfloat16 b = __float2bfloat16(a);
+      const float back = __bfloat162float(b);
+      hi[(long)(row + i) * p.I + col] = b;
+      lo[(long)(row + i) * p.I + col] = __float2bfloat16(isinf(back) ? 0.0f : a - back);
+    }
+  }
+}
+
+// out of one tile of 256 columns, all tokens: 2 columns a thread
+__device__ void combine_columns(const FewParams& p, int n, int tid) {
+  const int c = n * 256 + tid * 2;
+  if (c >= p.H) return;
+  for (int t = 0; t < p.T; ++t) {
+    float a0 = 0.0f, a1 = 0.0f;
+#pragma unroll 8
+    for (int j = 0; j < p.k; ++j) {
+      const long f = (long)t * p.k + j;
+      const int e = p.idx[f];
+      if (e < 0 || e >= p.E) continue;
+      const float s = p.scores[f];
+      const float2 y = __ldcg(reinterpret_cast<const float2*>(p.y + f * p.H + c));
+      a0 = fmaf(s, y.x, a0);
+      a1 = fmaf(s, y.y, a1);
+    }
+    *reinterpret_cast<uint32_t*>(p.out + (long)t * p.H + c) = pack_bf16x2(a0, a1);
+  }
+}
+
+template <bool MX>
+__global__ void __launch_bounds__(MX ? 320 : 256, 1) few_kernel(const __grid_constant__ FewMaps maps, FewParams p) {
+  constexpr int kThreads = MX ? 320 : 256;
+  constexpr int kEl = MX ? 128 : 64;  // K per block
+  extern __shared__ uint8_t raw_smem[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~uintptr_t(1023));
+  const int b_bytes = p.unit_rows * 128;
+  const int stage_bytes = 2 * kATile + (MX ? 1 : 2) * b_bytes;
+  uint8_t* sf_smem = smem + (size_t)p.stages * stage_bytes;
+  Ctl* ctl = reinterpret_cast<Ctl*>(sf_smem + (MX ? p.stages * kSfBytes : 0));
+  Schedule sched;
+  sched.offset = reinterpret_cast<int32_t*>(ctl + 1);
+  int32_t* cursor = sched.offset + p.E + 1;
+  sched.perm = reinterpret_cast<uint16_t*>(cursor + p.E + 1);
+  sched.unit_e = sched.perm + (((p.T * p.k) + 7) & ~7);
+  sched.unit_r = sched.unit_e + p.max_units;
+  sched.unit_n = reinterpret_cast<uint8_t*>(sched.unit_r + p.max_units);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  WaitCtx wc{&ctl->abort, p.hdr + kHdrAbort, p.hdr + kHdrError};
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < p.stages; ++i) {
+      mbar_init(&ctl->full_a[i], 1);
+      mbar_init(&ctl->full_b[i], kProducers);
+      mbar_init(&ctl->scales[i], 2);
+      mbar_init(&ctl->empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&ctl->tfull[i], 1);
+      mbar_init(&ctl->tempty[i], kEpilogue);
+    }
+    mbar_init(&ctl->drained, 1);
+    ctl->abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0) {
+    tmem_alloc(&ctl->tmem, 512);
+    tmem_relinquish();
+    if (lane < 3) tma_prefetch_desc(&maps.w[lane]);
+    if (MX && lane < 3) tma_prefetch_desc(&maps.sf[lane]);
+  }
+  __syncthreads();
+
+  // ---- routing and the quantised x
+  if (MX) quantize_x(p, kThreads);
+  if (p.Wr) router_logits(p, smem, kThreads);
+  bool ok = true;
+  if (MX || p.Wr) {
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) red_release_gpu_add(word(p, kWordPrepared), 1u);
+  }
+  if (p.Wr) {
+    if (blockIdx.x < p.T) {
+      if (threadIdx.x == 0) ctl->go = wait_flag_geq(word(p, kWordPrepared), gridDim.x, wc) ? 1 : 0;
+      __syncthreads();
+      if (ctl->go)
+        for (int t = blockIdx.x; t < p.T; t += gridDim.x)
+          router_select(p, t, reinterpret_cast<float*>(smem), kThreads);
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) ctl->go = wait_flag_geq(word(p, kWordRouted), p.T, wc) ? 1 : 0;
+    __syncthreads();
+    ok = ctl->go != 0;
+    // the stages' first loads (async proxy) come after these threads' use of the same shared memory
+    fence_proxy_async_shared();
+  }
+  if (ok) build_units(p, sched, cursor, ctl, kThreads);
+  __syncthreads();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctl->tmem;
+  const int units = ok ? ctl->units : 0;
+
+  Cut cut[2];
+  cut[0].tiles_per_unit = p.I / 128;
+  cut[0].kb = p.H / kEl;
+  cut[1].tiles_per_unit = (p.H + 255) / 256;
+  cut[1].kb = p.I / kEl;
+#pragma unroll
+  for (int g = 0; g < 2; ++g) {
+    cut[g].blocks = (long)units * cut[g].tiles_per_unit * cut[g].kb;
+    const long most = (cut[g].blocks + 1) / 2;
+    cut[g].ctas = (int)(most < (long)gridDim.x ? most : (long)gridDim.x);
+  }
+  const int hidden_tiles = units * cut[0].tiles_per_unit;
+  const int c = blockIdx.x;
+
+  if (units == 0) {
+    // nothing routed: zeros (or a call that gave up)
+    for (long i = (long)c * kThreads + threadIdx.x; i < (long)p.T * p.H; i += (long)gridDim.x * kThreads)
+      p.out[i] = __float2bfloat16(0.0f);
+  } else if (warp == 0) {
+    // ---------------------------------------------------------------- weights
+    if (lane == 0) {
+      uint32_t stage = 0, phase = 0;
+      long issued = 0;
+      bool fine = true;
+      for (int g = 0; g < 2 && fine; ++g) {
+        if (c >= cut[g].ctas) continue;
+        const long end = cut[g].begin(c + 1);
+        for (long b = cut[g].begin(c); b < end && fine;) {
+          const Seg s = seg_at(cut[g], b, end, units, g == 1);
+          const int e = sched.unit_e[s.unit];
+          const int col = g == 0 ? s.n * 128 : s.n * 256;
+          const bool second = g == 0 || col + 128 < p.H;
+          const CUtensorMap* m0 = &maps.w[g == 0 ? 0 : 2];
+          const CUtensorMap* m1 = &maps.w[g == 0 ? 1 : 2];
+          const int col1 = g == 0 ? col : col + 128;
+          const uint32_t bytes = (second ? 2 : 1) * (kATile + (MX ? 512 : 0));
+          for (int kb = s.k0; kb < s.k1; ++kb) {
+            if (!mbar_wait(&ctl->empty[stage], phase ^ 1, wc)) {
+              fine = false;
+              break;
+            }
+            uint8_t* a = smem + (size_t)stage * stage_bytes;
+            uint64_t* bar = &ctl->full_a[stage];
+            mbar_arrive_expect_tx(bar, bytes);
+            if constexpr (MX) {
+              uint8_t* sf = sf_smem + stage * kSfBytes;
+              tma_load_3d(a, m0, bar, col, kb * kEl, e);
+              tma_load_3d(sf, &maps.sf[g == 0 ? 0 : 2], bar, col, kb * 4, e);
+              if (second) {
+                tma_load_3d(a + kATile, m1, bar, col1, kb * kEl, e);
+                tma_load_3d(sf + 512, &maps.sf[g == 0 ? 1 : 2], bar, col1, kb * 4, e);
+              }
+            } else {
+              tma_load_3d(a, m0, bar, col, kb * kEl, e);
+              tma_load_3d(a + kATile / 2, m0, bar, col + 64, kb * kEl, e);
+              if (second) {
+                tma_load_3d(a + kATile, m1, bar, col1, kb * kEl, e);
+                tma_load_3d(a + kATile + kATile / 2, m1, bar, col1 + 64, kb * kEl, e);
+              }
+            }
+            ++issued;
+            if (++stage == (uint32_t)p.stages) { stage = 0; phase ^= 1; }
+          }
+          b += s.k1 - s.k0;
+        }
+      }
+      if (!fine) {
+        // no copy may still be in flight when the CTA leaves
+        for (long i = issued > p.stages ? issued - p.stages : 0; i < issued; ++i)
+          mbar_drain(&ctl->full_a[i % p.stages], (uint32_t)((i / p.stages) & 1), 1000000000ull);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ---------------------------------------------------------------- MMA
+    uint32_t stage = 0, phase = 0, count = 0;
+    bool fine = true;
+    for (int g = 0; g < 2 && fine; ++g) {
+      if (c >= cut[g].ctas) continue;
+      const long end = cut[g].begin(c + 1);
+      for (long b = cut[g].begin(c); b < end && fine;) {
+        const Seg s = seg_at(cut[g], b, end, units, g == 1);
+        const int n = (sched.unit_n[s.unit] + 15) & ~15;
+        const bool second = g == 0 || s.n * 256 + 128 < p.H;
+        const uint32_t buf = count & 1;
+        if (!mbar_wait(&ctl->tempty[buf], ((count >> 1) & 1) ^ 1, wc)) {
+          fine = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t d0 = tmem + buf * 2 * p.unit_rows, d1 = d0 + p.unit_rows;
+        for (int kb = s.k0; kb < s.k1; ++kb) {
+          if (!mbar_wait(&ctl->full_a[stage], phase, wc) || !mbar_wait(&ctl->full_b[stage], phase, wc) ||
+              (MX && !mbar_wait(&ctl->scales[stage], phase, wc))) {
+            fine = false;
+            break;
+          }
+          tc_fence_after();
+          if (lane == 0) {
+            // the tokens' operand was written with cp.async: order it before the tensor core's (async-proxy) reads
+            fence_proxy_async_shared();
+            const uint32_t a0 = smem_u32(smem + (size_t)stage * stage_bytes), a1 = a0 + kATile, b0 = a0 + 2 * kATile;
+            if constexpr (MX) {
+              const uint32_t sf = smem_u32(sf_smem + stage * kSfBytes);
+              const uint32_t t = tmem + 256 + stage * 16;  // scales: two A tiles, B
+              tmem_cp_32x128b_warpx4(t, sdesc_plain(sf + 1024, 16, 128));
+              if (second) tmem_cp_32x128b_warpx4(t + 4, sdesc_plain(sf + 1536, 16, 128));
+              tmem_cp_32x128b_warpx4(t + 8, sdesc_plain(sf + 2048, 16, 128));
+#pragma unroll
+              for (int k32 = 0; k32 < 4; ++k32) {
+                const uint32_t idesc = idesc_mxf8(128, n, 1, 0, k32, k32);
+                const uint64_t bd = sdesc_sw128(b0 + k32 * 32, 16, 1024);
+                const uint32_t acc = kb > s.k0 || k32 > 0;
+                mma_mxf8(d0, sdesc_sw128(a0 + k32 * 4096, 16384, 1024), bd, idesc, t, t + 8, acc);
+                if (second) mma_mxf8(d1, sdesc_sw128(a1 + k32 * 4096, 16384, 1024), bd, idesc, t + 4, t + 8, acc);
+              }
+            } else {
+              const uint32_t idesc = idesc_bf16(128, n, 1, 0);
+#pragma unroll
+              for (int k16 = 0; k16 < 4; ++k16) {
+                const uint64_t ad0 = sdesc_sw128(a0 + k16 * 2048, 8192, 1024);
+                const uint64_t ad1 = sdesc_sw128(a1 + k16 * 2048, 8192, 1024);
+                const uint64_t bd = sdesc_sw128(b0 + k16 * 32, 16, 1024);
+                const uint32_t acc = kb > s.k0 || k16 > 0;
+                mma_bf16(d0, ad0, bd, idesc, acc);
+                if (second) mma_bf16(d1, ad1, bd, idesc, acc);
+                if (g == 1) {
+                  const uint64_t bl = sdesc_sw128(b0 + b_bytes + k16 * 32, 16, 1024);
+                  mma_bf16(d0, ad0, bl, idesc, 1);
+                  if (second) mma_bf16(d1, ad1, bl, idesc, 1);
+                }
+              }
+            }
+            mma_commit(&ctl->empty[stage]);
+          }
+          __syncwarp();
+          if (++stage == (uint32_t)p.stages) { stage = 0; phase ^= 1; }
+        }
+        if (!fine) break;
+        if (lane == 0) mma_commit(&ctl->tfull[buf]);
+        __syncwarp();
+        ++count;
+        b += s.k1 - s.k0;
+      }
+    }
+    if (!fine) {
+      // no MMA may still run when the CTA leaves
+      if (lane == 0) {
+        mma_commit(&ctl->drained);
+        mbar_drain(&ctl->drained, 0, 1000000000ull);
+      }
+      __syncwarp();
+    }
+  } else if (warp < 4) {
+    // ---------------------------------------------------------------- tokens' operand
+    const int tid = threadIdx.x - 64;
+    const int ch = tid & 7;  // this thread's 16-byte piece of a row's 128 bytes
+    uint32_t stage = 0, phase = 0;
+    bool fine = true;
+    for (int g = 0; g < 2 && fine; ++g) {
+      if (c >= cut[g].ctas) continue;
+      // x is ready at once (MXFP8: once every CTA has quantised its share),
+      // a when every tile of it is finished
+      if (g == 1 || (MX && !p.Wr)) {
+        bool go = true;
+        if (tid == 0)
+          go = g == 0 ? wait_flag_geq(word(p, kWordPrepared), gridDim.x, wc)
+                      : wait_flag_geq(word(p, kWordHidden), hidden_tiles, wc);
+        if (!vote_all(2, kProducers, go)) break;
+      }
+      const int K = g == 0 ? p.H : p.I;
+      const uint8_t* src = g == 0 ? (MX ? p.xq : reinterpret_cast<const uint8_t*>(p.x)) : static_cast<uint8_t*>(p.a);
+      const uint8_t* sfs = g == 0 ? p.xsf : p.asf;
+      const long lo = (long)p.T * p.k * p.I * 2;  // a's second part
+      const long end = cut[g].begin(c + 1);
+      for (long b = cut[g].begin(c); b < end && fine;) {
+        const Seg s = seg_at(cut[g], b, end, units, g == 1);
+        const int n = sched.unit_n[s.unit], r0 = sched.unit_r[s.unit];
+        long at[8];  // byte offset of this thread's piece in rows tid / 8 + 8 i
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int r = (tid >> 3) + 8 * i;
+          at[i] = 0;
+          if (r < n) at[i] = (long)(g == 0 ? sched.perm[r0 + r] / p.k : r0 + r) * K * (MX ? 1 : 2) + ch * 16;
+        }
+        const long sf_at = MX && tid < n ? (long)(g == 0 ? sched.perm[r0 + tid] / p.k : r0 + tid) * (K / 32) : 0;
+        for (int kb = s.k0; kb < s.k1; ++kb) {
+          if (!mbar_wait(&ctl->empty[stage], phase ^ 1, wc)) {
+            fine = false;
+            break;
+          }
+          const uint32_t dst = smem_u32(smem + (size_t)stage * stage_bytes + 2 * kATile);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int r = (tid >> 3) + 8 * i;
+            if (r < n) {
+              const uint32_t d = dst + r * 128 + ((ch ^ (r & 7)) << 4);
+              cp_async_16(d, src + at[i] + (long)kb * 128);
+              if (!MX && g == 1) cp_async_16(d + b_bytes, src + lo + at[i] + (long)kb * 128);
+            }
+          }
+          if (MX && tid < n)
+            cp_async_4(smem_u32(sf_smem + stage * kSfBytes + 2048 + mx_sf_offset(tid, 0)), sfs + sf_at + kb * 4, 4);
+          cp_async_arrive_noinc(&ctl->full_b[stage]);
+          if (++stage == (uint32_t)p.stages) { stage = 0; phase ^= 1; }
+        }
+        b += s.k1 - s.k0;
+      }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+  } else if (warp < 8) {
+    // ---------------------------------------------------------------- epilogue
+    const int q = warp & 3;  // TMEM lanes this warp may read
+    const int tid = threadIdx.x - 128;
+    const int slot_floats = 2 * p.unit_rows * 128;
+    uint32_t count = 0;
+    bool fine = true;
+    for (int g = 0; g < 2 && fine; ++g) {
+      if (c >= cut[g].ctas) continue;
+      const long end = cut[g].begin(c + 1);
+      for (long b = cut[g].begin(c); b < end;) {
+        const Seg s = seg_at(cut[g], b, end, units, g == 1);
+        b += s.k1 - s.k0;
+        const int n = sched.unit_n[s.unit], r0 = sched.unit_r[s.unit];
+        const bool second = g == 0 || s.n * 256 + 128 < p.H;
+        const bool whole = s.k0 == 0 && s.k1 == cut[g].kb;
+        const int lane_col = q * 32 + lane;
+        auto finish = [&](int i0, const float* v0, const float* v1) {
+          const int rows = min(16, n - i0);
+          if (g == 0) {
+            store_hidden<MX>(p, r0 + i0, rows, s.n * 128 + lane_col, lane, v0, v1);
+          } else {
+            float* y = p.y + s.n * 256 + lane_col;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              if (i >= rows) break;
+              float* yr = y + (long)sched.perm[r0 + i0 + i] * p.H;
+              yr[0] = v0[i];
+              if (second) yr[128] = v1[i];
+            }
+          }
+        };
+        const uint32_t buf = count & 1;
+        fine = vote_all(1, kEpilogue, mbar_wait(&ctl->tfull[buf], (count >> 1) & 1, wc));
+        if (!fine) break;
+        tc_fence_after();
+        const uint32_t d = tmem + buf * 2 * p.unit_rows + ((uint32_t)(q * 32) << 16);
+        float* slot = p.part + (long)(2 * c + (s.k0 == 0 ? 1 : 0)) * slot_floats + lane_col;
+        for (int i0 = 0; i0 < n; i0 += 16) {
+          uint32_t w0[16], w1[16];
+          tmem_ld16_issue(d + i0, w0);
+          tmem_ld16_issue(d + p.unit_rows + i0, w1);
+          tmem_wait_ld();
+          tmem_regs_ready16(w0);
+          tmem_regs_ready16(w1);
+          float v0[16], v1[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            v0[i] = __uint_as_float(w0[i]);
+            v1[i] = __uint_as_float(w1[i]);
+          }
+          if (whole) {
+            finish(i0, v0, v1);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              if (i0 + i >= n) break;
+              __stcg(slot + (i0 + i) * 128, v0[i]);
+              if (second) __stcg(slot + (p.unit_rows + i0 + i) * 128, v1[i]);
+            }
+          }
+        }
+        tc_fence_before();
+        mbar_arrive(&ctl->tempty[buf]);
+        ++count;
+        if (!whole) {
+          const int first = cut[g].owner((long)s.tile * cut[g].kb);
+          const int last = cut[g].owner((long)s.tile * cut[g].kb + cut[g].kb - 1);
+          int32_t* arrivals = p.tile_count + (g == 0 ? 0 : p.max_units * cut[0].tiles_per_unit) + s.tile;
+          __threadfence();
+          named_bar_sync(1, kEpilogue);
+          if (tid == 0) {
+            const int old = atomicAdd(arrivals, 1);
+            ctl->flag[0] = old == last - first;
+            if (old == last - first) *arrivals = 0;
+            __threadfence();
+          }
+          __syncwarp();
+          named_bar_sync(1, kEpilogue);
+          if (!ctl->flag[0]) continue;
+          // the last to arrive: the parts in the order of K (the first CTA's
+          // part begins the tile; the others' are the head of their runs)
+          for (int i0 = 0; i0 < n; i0 += 16) {
+            float v0[16], v1[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v0[i] = v1[i] = 0.0f;
+            for (int o = first; o <= last; ++o) {
+              const float* from = p.part + (long)(2 * o + (o == first ? 1 : 0)) * slot_floats + lane_col;
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                if (i0 + i >= n) break;
+                v0[i] += __ldcg(from + (i0 + i) * 128);
+                if (second) v1[i] += __ldcg(from + (p.unit_rows + i0 + i) * 128);
+              }
+            }
+            finish(i0, v0, v1);
+          }
+        }
+        // a finished tile
+        __threadfence();
+        named_bar_sync(1, kEpilogue);
+        if (g == 0) {
+          if (tid == 0) red_release_gpu_add(word(p, kWordHidden), 1u);
+          continue;
+        }
+        if (tid == 0) {
+          const int old = atomicAdd(p.col_count + s.n, 1);
+          ctl->flag[1] = old == units - 1;
+          if (old == units - 1) p.col_count[s.n] = 0;
+          __threadfence();
+        }
+        __syncwarp();
+        named_bar_sync(1, kEpilogue);
+        if (ctl->flag[1]) combine_columns(p, s.n, tid);
+      }
+    }
+  } else {
+    // ---------------------------------------------------------------- MXFP8: weight scales
+    // from [4 K blocks][128 columns] as they lie in memory to the layout that
+    // the tensor core's scale copy takes; one warp per A tile
+    const int i = warp - 8;
+    uint32_t stage = 0, phase = 0;
+    bool fine = true;
+    for (int g = 0; g < 2 && fine; ++g) {
+      if (c >= cut[g].ctas) continue;
+      const long blocks = cut[g].begin(c + 1) - cut[g].begin(c);
+      for (long b = 0; b < blocks; ++b) {
+        fine = mbar_wait(&ctl->full_a[stage], phase, wc);
+        if (!fine) break;
+        const uint8_t* raw = sf_smem + stage * kSfBytes + i * 512;
+        uint8_t* tiled = sf_smem + stage * kSfBytes + 1024 + i * 512;
+        uint32_t w[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) w[r] = *reinterpret_cast<const uint32_t*>(raw + r * 128 + lane * 4);
+        const uint32_t l01 = __byte_perm(w[0], w[1], 0x5140), h01 = __byte_perm(w[0], w[1], 0x7362);
+        const uint32_t l23 = __byte_perm(w[2], w[3], 0x5140), h23 = __byte_perm(w[2], w[3], 0x7362);
+        const uint32_t o[4] = {__byte_perm(l01, l23, 0x5410), __byte_perm(l01, l23, 0x7632),
+                               __byte_perm(h01, h23, 0x5410), __byte_perm(h01, h23, 0x7632)};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          *reinterpret_cast<uint32_t*>(tiled + mx_sf_offset(lane * 4 + j, 0)) = o[j];
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->scales[stage]);
+        if (++stage == (uint32_t)p.stages) { stage = 0; phase ^= 1; }
+      }
+    }
+  }
+
+  tc_fence_before();
+  // (the non-aligned barrier form, defined for warps that arrive diverged)
+  asm volatile("barrier.sync 0;" ::: "memory");
+  tc_fence_after();
+  if (warp == 0) tmem_dealloc(tmem, 512);
+  if (threadIdx.x == 0) {
+    // the last CTA to end leaves the counters as it found them
+    __threadfence();
+    if (atomicAdd(p.hdr + kWordLeft, 1) == (int)gridDim.x - 1) {
+      p.hdr[kWordPrepared] = p.hdr[kWordRouted] = p.hdr[kWordHidden] = p.hdr[kWordLeft] = 0;
+    }
+  }
 }
 
 size_t align256(size_t b) { return (b + 255) & ~size_t(255); }
+
+// Units of any routing of T tokens: a part-filled one per expert at most,
+// beside full ones.
+int units_bound(int T, int E, int k, int unit_rows) {
+  const int R = T * k, experts = E < R ? E : R;
+  const int n = experts + R / unit_rows;
+  return n < R ? n : R;
+}
+
+void logit_parts(int T, int H, int ctas, int* parts, int* rows) {
+  const int groups = (T + kLogitTokens - 1) / kLogitTokens;
+  int n = ctas / groups;
+  if (n < 1) n = 1;
+  int r = (H + n - 1) / n;
+  r = (r + 7) & ~7;
+  *rows = r;
+  *parts = (H + r - 1) / r;
+}
 
 }  // namespace
 
@@ -122,38 +849,66 @@ FewLayout few_layout(const mok_shape& s, mok_precision prec) {
     return o;
   };
   const size_t R = (size_t)s.T * s.k;
+  const bool mx = prec == MOK_MXFP8;
+  const int ctas = device_sm_count() > 0 ? device_sm_count() : 1;
   L.header = take(kHeaderWords * 4);
-  L.logits = take((size_t)s.T * s.E * 4);
-  L.xq = prec == MOK_MXFP8 ? take((size_t)s.T * s.H) : 0;
-  L.xsf = prec == MOK_MXFP8 ? take((size_t)s.T * (s.H / 32)) : 0;
-  L.a = take(R * s.I * (prec == MOK_MXFP8 ? 1 : 2));
-  L.asf = prec == MOK_MXFP8 ? take(R * (s.I / 32)) : 0;
+  // room for the units of any call of this H, I, E and k
+  const size_t units = units_bound(MOK_FEW_MAX_TOKENS, s.E, s.k, 16);
+  L.tile_words = units * (s.I / 128 + (s.H + 255) / 256);
+  L.col_words = (s.H + 255) / 256;
+  L.tiles = take((L.tile_words + L.col_words) * 4);
+  int parts, rows;
+  logit_parts(s.T, s.H, ctas, &parts, &rows);
+  L.logits = take((size_t)parts * s.T * s.E * 4);
+  L.xq = mx ? take((size_t)s.T * s.H) : 0;
+  L.xsf = mx ? take((size_t)s.T * (s.H / 32)) : 0;
+  L.a = take(R * s.I * (mx ? 1 : 4));
+  L.asf = mx ? take(R * (s.I / 32)) : 0;
+  L.part = take((size_t)ctas * 2 * 2 * few_unit_rows(s.T) * 128 * 4);
+  L.y = take(R * s.H * 4);
   L.total = off;
   return L;
 }
 
-cudaError_t launch_few(const FewParams& p, bool mx, int* launches, cudaStream_t st) {
-  int n = 0;
-  if (p.Wr) {
-    few_logits_kernel<<<dim3((p.E + 255) / 256, p.T), 256, 0, st>>>(p);
-    cudaError_t e = launch_router_topk(p.T, p.E, p.E, p.k, p.logits, p.bias, p.idx_out, p.scores_out, st);
-    if (e != cudaSuccess) return e;
-    n += 2;
-  }
-  const dim3 g1(p.I / 128, p.T * p.k), g2(p.H / 128, p.T);
-  if (mx) {
-    const int nb = p.T * (p.H / 32);
-    few_quant_x_kernel<<<(nb + 127) / 128, 128, 0, st>>>(nb, p.x, p.xq, p.xsf);
-    few_hidden_kernel<true><<<g1, 128, 0, st>>>(p);
-    few_out_kernel<true><<<g2, 128, 0, st>>>(p);
-    n += 3;
-  } else {
-    few_hidden_kernel<false><<<g1, 128, 0, st>>>(p);
-    few_out_kernel<false><<<g2, 128, 0, st>>>(p);
-    n += 2;
-  }
-  *launches = n;
-  return cudaGetLastError();
+cudaError_t launch_few(FewParams p, bool mx, int* launches, cudaStream_t st) {
+  *launches = 0;
+  const int ctas = device_sm_count();
+  FewMaps maps;
+  const CUtensorMapDataType type = mx ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const int es = mx ? 1 : 2, kel = mx ? 128 : 64;
+  auto map = [&](CUtensorMap* m, CUtensorMap* ms, const void* w, const uint8_t* sf, int rows, int cols) {
+    const uint64_t dims[3] = {(uint64_t)cols, (uint64_t)rows, (uint64_t)p.E};
+    const uint64_t str[2] = {(uint64_t)cols * es, (uint64_t)cols * rows * es};
+    const uint32_t box[3] = {128u / es, (uint32_t)kel, 1};
+    if (!make_tmap(m, type, 3, w, dims, str, box, true)) return false;
+    if (!mx) return true;
+    const uint64_t sdims[3] = {(uint64_t)cols, (uint64_t)rows / 32, (uint64_t)p.E};
+    const uint64_t sstr[2] = {(uint64_t)cols, (uint64_t)cols * (rows / 32)};
+    const uint32_t sbox[3] = {128, 4, 1};
+    return make_tmap(ms, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, sf, sdims, sstr, sbox, false);
+  };
+  memset(&maps, 0, sizeof(maps));
+  if (!map(&maps.w[0], &maps.sf[0], p.W1, p.sf1, p.H, p.I) || !map(&maps.w[1], &maps.sf[1], p.W3, p.sf3, p.H, p.I) ||
+      !map(&maps.w[2], &maps.sf[2], p.W2, p.sf2, p.I, p.H))
+    return cudaErrorInvalidValue;
+  p.unit_rows = few_unit_rows(p.T);
+  p.max_units = units_bound(p.T, p.E, p.k, p.unit_rows);
+  logit_parts(p.T, p.H, ctas, &p.h_parts, &p.h_rows);
+  const size_t stage = 2 * kATile + (size_t)p.unit_rows * (mx ? 128 : 256) + (mx ? kSfBytes : 0);
+  const size_t rest = 1024 + sizeof(Ctl) + schedule_bytes(p.E, p.T * p.k, p.max_units);
+  constexpr size_t kMost = 227 * 1024;
+  int stages = (int)((kMost - rest) / stage);
+  if (stages > kMaxFewStages) stages = kMaxFewStages;
+  p.stages = stages;
+  const size_t smem = rest + stages * stage;
+  const void* kernel = mx ? (const void*)few_kernel<true> : (const void*)few_kernel<false>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMost);
+  if (e != cudaSuccess) return e;
+  void* args[] = {&maps, &p};
+  e = cudaLaunchCooperativeKernel(kernel, dim3(ctas), dim3(mx ? 320 : 256), args, smem, st);
+  if (e != cudaSuccess) return e;
+  *launches = 1;
+  return cudaSuccess;
 }
 
 }  // namespace mok

@@ -5,18 +5,37 @@
 
 namespace mok {
 
+// Tokens side by side in one tile (the N of its MMAs); an expert with more
+// rows takes several units.
+inline int few_unit_rows(int T) { return T <= 16 ? 16 : T <= 32 ? 32 : 64; }
+
+// The counters' place and number depend on H, I, E and k alone, so that a
+// workspace serves calls of fewer tokens: every counter is zero between calls.
 struct FewLayout {
   size_t header;   // int32 [kHeaderWords]: word 0 the error bits
-  size_t logits;   // f32 [T, E] router logits
+  size_t tiles;    // int32: tiles' arrivals (both GEMMs), then column tiles'
+  size_t tile_words, col_words;
+  size_t logits;   // f32 [parts, T, E] router logits, in parts along H
   size_t xq, xsf;  // MXFP8: codes [T, H] and scales [T, H/32] of x
-  size_t a, asf;   // bf16 [T*k, I]; MXFP8: codes, and scales [T*k, I/32]
+  size_t a, asf;   // bf16 [2][T*k, I] (a, and what its rounding left); MXFP8: codes, and scales [T*k, I/32]
+  size_t part;     // f32 [2 per CTA][2][unit rows][128] sums of tiles split along K
+  size_t y;        // f32 [T*k, H]
   size_t total;
 };
 FewLayout few_layout(const mok_shape& s, mok_precision prec);
 
+struct FewMaps {
+  CUtensorMap w[3];   // W1, W3, W2
+  CUtensorMap sf[3];  // MXFP8: their scales
+};
+
 struct FewParams {
   int T, H, I, E, k;
+  int unit_rows, stages;
   int32_t* hdr;
+  int32_t* tile_count;  // [units * I/128] first GEMM, then [units * column tiles] second
+  int32_t* col_count;   // [column tiles]
+  int max_units;        // capacity of the unit table
   const __nv_bfloat16* x;
   const int32_t* idx;
   const float* scores;
@@ -27,15 +46,18 @@ struct FewParams {
   uint8_t *xq, *xsf;
   void* a;
   uint8_t* asf;
+  float* part;
+  float* y;
   // router (Wr null: the routing is given)
   const __nv_bfloat16* Wr;
   const float* bias;
+  int h_parts, h_rows;  // logits: rows of Wr per part
   float* logits;
   int32_t* idx_out;
   float* scores_out;
 };
 
 // Enqueues one pass; *launches gets the number of kernels.
-cudaError_t launch_few(const FewParams& p, bool mx, int* launches, cudaStream_t st);
+cudaError_t launch_few(FewParams p, bool mx, int* launches, cudaStream_t st);
 
 }  // namespace mok

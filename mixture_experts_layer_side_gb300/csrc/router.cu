@@ -14,12 +14,11 @@
 // after "Three design decisions that matter": router weight gradients from
 // the SonicMoE-style score gradient in the SwiGLU backward).
 #include "mok_internal.cuh"
+#include "topk.cuh"
 
 namespace mok {
 
 namespace {
-
-constexpr int kMaxRouterExperts = 1024;  // keys held in registers: 32 per lane
 
 __global__ void __launch_bounds__(256) pad_weights_kernel(int H, int E, int Epad, const __nv_bfloat16* __restrict__ w,
                                                           __nv_bfloat16* __restrict__ wp) {
@@ -30,12 +29,7 @@ __global__ void __launch_bounds__(256) pad_weights_kernel(int H, int E, int Epad
   }
 }
 
-// (key, expert) pairs ordered by descending key, then ascending expert.
-__device__ __forceinline__ bool ranks_before(float ka, int ea, float kb, int eb) {
-  return ka > kb || (ka == kb && ea < eb);
-}
-
-// One warp per token; lane l holds the keys of experts l, l + 32, ...
+// One warp per token.
 __global__ void __launch_bounds__(256) topk_softmax_kernel(int T, int E, int Epad, int k,
                                                            const float* __restrict__ logits,
                                                            const float* __restrict__ bias, int32_t* __restrict__ idx,
@@ -43,56 +37,12 @@ __global__ void __launch_bounds__(256) topk_softmax_kernel(int T, int E, int Epa
   const int lane = threadIdx.x & 31;
   const int t = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
   if (t >= T) return;
-  const float* row = logits + (long)t * Epad;
-  float key[kMaxRouterExperts / 32];
-  const int per_lane = (E + 31) >> 5;
-#pragma unroll
-  for (int i = 0; i < kMaxRouterExperts / 32; ++i) {
-    const int e = lane + 32 * i;
-    const float v = (i < per_lane && e < E) ? row[e] + (bias ? bias[e] : 0.0f) : 0.0f;
-    key[i] = isnan(v) ? -INFINITY : v;  // a NaN key ranks last
-  }
-  uint32_t taken = 0;  // bit i: expert lane + 32 i already chosen
-  int my_e = -1;       // lane j < k ends with the j-th choice
-  float my_l = 0.0f;
-  for (int j = 0; j < k; ++j) {
-    float bk = 0.0f;
-    int be = INT_MAX;
-#pragma unroll
-    for (int i = 0; i < kMaxRouterExperts / 32; ++i) {
-      const int e = lane + 32 * i;
-      if (i < per_lane && e < E && !((taken >> i) & 1u) && (be == INT_MAX || ranks_before(key[i], e, bk, be))) {
-        bk = key[i];
-        be = e;
-      }
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const float ok = __shfl_xor_sync(0xffffffffu, bk, o);
-      const int oe = __shfl_xor_sync(0xffffffffu, be, o);
-      if (oe != INT_MAX && (be == INT_MAX || ranks_before(ok, oe, bk, be))) {
-        bk = ok;
-        be = oe;
-      }
-    }
-    if (be == INT_MAX) break;  // fewer than k experts (the host rules it out)
-    if ((be & 31) == lane) taken |= 1u << (be >> 5);
-    if (lane == j) {
-      my_e = be;
-      my_l = row[be];
-    }
-  }
-  // softmax over the k chosen, unbiased logits (lanes j < k)
-  float m = lane < k ? my_l : -INFINITY;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  const float ez = lane < k ? expf(my_l - m) : 0.0f;
-  float sum = ez;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  int e;
+  float s;
+  topk_softmax_warp<kMaxRouterExperts / 32>(logits + (long)t * Epad, bias, E, k, lane, e, s);
   if (lane < k) {
-    idx[(long)t * k + lane] = my_e;
-    scores[(long)t * k + lane] = ez / sum;
+    idx[(long)t * k + lane] = e;
+    scores[(long)t * k + lane] = s;
   }
 }
 
