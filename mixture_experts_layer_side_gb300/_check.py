@@ -20,19 +20,30 @@ def require(ok, what):
         raise MokArgError(what)
 
 
+def fits(t, shape, dtype, device):
+    """Whether ``t`` is a dense tensor as described: what a call asks of its
+    arguments each time, without the cost of saying what is wrong."""
+    return (type(t) is torch.Tensor and t.dtype is dtype and t.shape == shape and t.device == device and
+            t.is_contiguous())
+
+
+def rows_fit(t, shape, dtype, device):
+    """As ``fits``, for a matrix whose rows may be further apart than its columns."""
+    return (type(t) is torch.Tensor and t.dtype is dtype and t.shape == shape and t.device == device and
+            (t.is_contiguous() or ((t.stride(1) == 1 or shape[1] <= 1) and
+                                   (t.stride(0) >= shape[1] or shape[0] <= 1))))
+
+
 def tensor(t, name, shape, dtypes, device, rows_apart=False):
-    """``t`` is a tensor of this shape, one of these types, on this device and
-    dense in row-major order (``rows_apart``: a matrix whose rows may be
-    further apart than its columns)."""
+    """Raises unless ``t`` is a tensor of this shape, one of these types, on
+    this device and dense in row-major order (``rows_apart``: see ``rows_fit``)."""
     require(isinstance(t, torch.Tensor), f"{name}: a tensor is wanted")
     require(tuple(t.shape) == tuple(shape), f"{name}: shape {tuple(t.shape)}, wanted {tuple(shape)}")
     require(t.dtype in dtypes, f"{name}: {t.dtype}, wanted {' or '.join(str(d) for d in dtypes)}")
     require(t.device == device, f"{name}: on {t.device}, wanted {device}")
-    if rows_apart:
-        dense = t.shape[1] <= 1 or t.stride(1) == 1
-        dense = dense and (t.shape[0] <= 1 or t.stride(0) >= t.shape[1])
-    else:
-        dense = t.is_contiguous()
+    dense = t.is_contiguous()
+    if rows_apart and not dense:
+        dense = (t.stride(1) == 1 or t.shape[1] <= 1) and (t.stride(0) >= t.shape[1] or t.shape[0] <= 1)
     require(dense, f"{name}: strides {tuple(t.stride())} are not row-major")
     return t
 

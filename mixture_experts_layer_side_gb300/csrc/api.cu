@@ -1564,7 +1564,6 @@ mok_status few_params(const mok_shape& s, mok_precision prec, void* ws, size_t w
   p->a = w + L.a;
   p->asf = w + L.asf;
   p->tile_count = reinterpret_cast<int32_t*>(w + L.tiles);
-  p->col_count = p->tile_count + L.tile_words;
   p->part = reinterpret_cast<float*>(w + L.part);
   p->y = reinterpret_cast<float*>(w + L.y);
   return MOK_OK;

@@ -15,18 +15,22 @@
 //  * One CTA per SM.  A "unit" is up to unit_rows rows of one expert; a tile
 //    is 2 x 128 output columns of a unit (first GEMM: 128 of h and the same
 //    of u; second: 256 of y); a block is 64 (MXFP8: 128) of a tile's K.  All
-//    blocks of a GEMM, tiles in order, are cut into equal runs, one per CTA,
-//    whatever the number of experts: no SM waits for a last wave.  A tile
-//    that a cut splits leaves f32 sums in the workspace; the last of its CTAs
-//    to arrive adds them in the order of K.
-//  * The second GEMM needs all of a, but its weights do not: each CTA's ring
-//    of stages fills with W2 while the last tiles of a are finished.
+//    blocks of a GEMM, tiles in order, are cut into equal runs whatever the
+//    number of experts: no SM waits for a last wave.  A tile that a cut splits
+//    leaves f32 sums in the workspace; the last of its CTAs to arrive (first
+//    GEMM) or the combine (second) adds them in the order of K.
+//  * A run belongs to a group of CTAs that take neighbouring column tiles of
+//    the same K, so that the 128 or 256 bytes that one CTA reads of a weight
+//    row lie beside what its neighbours read at the same time.
+//  * The second GEMM needs all of a.  The units are split in two halves, A
+//    and B, and the order is a(A), a(B), y(A), y(B): while the last sums of
+//    one half are joined, the weights of the next part stream in.
 //  * Every CTA sorts the routing by expert for itself (at most 4,096 ids), so
 //    no launch or barrier stands between the routing and the first weight.
 //
-// The number of arrivals that a CTA waits for is counted in the workspace and
-// every CTA has to be resident: the launch is cooperative.  All waits are
-// bounded (MOK_ERR_TIMEOUT).  The counters are zero again when a call ends.
+// Arrivals are counted in the workspace and every CTA has to be resident: the
+// launch is cooperative.  All waits are bounded (MOK_ERR_TIMEOUT).  The
+// counters are zero again when a call ends.
 #include <string.h>
 
 #include "few.cuh"
@@ -48,8 +52,59 @@ constexpr int kLogitTokens = 8;        // tokens side by side in the router's lo
 // header words
 constexpr int kWordPrepared = kHdrCounters;      // CTAs done with the logits' parts and x's quantisation
 constexpr int kWordRouted = kHdrCounters + 1;    // tokens routed
-constexpr int kWordHidden = kHdrCounters + 2;    // tiles of a finished
-constexpr int kWordLeft = kHdrCounters + 3;      // CTAs that ended
+constexpr int kWordHidden = kHdrCounters + 2;    // [2] tiles of a finished, each half
+constexpr int kWordSummed = kHdrCounters + 4;    // CTAs whose sums of y are stored
+constexpr int kWordLeft = kHdrCounters + 5;      // CTAs that ended
+constexpr int kMinRun = 6;  // blocks: a shorter run would not fill the stages
+
+// The routing sorted by expert, in shared memory.
+struct Schedule {
+  uint16_t* offset;   // [E] first sorted row of each expert
+  uint16_t* unit0;    // [E] its first unit
+  uint16_t* perm;     // [T*k] sorted row -> flat index
+  uint16_t* unit_of;  // [T*k] flat index -> unit (kNoUnit: an id out of range)
+  uint16_t* unit_e;   // [max_units] expert, first sorted row and rows of each unit
+  uint16_t* unit_r;
+  uint8_t* row_of;    // [T*k] flat index -> row of its unit
+  uint8_t* unit_n;
+};
+constexpr int kNoUnit = 0xFFFF;
+
+__host__ __device__ constexpr size_t schedule_bytes(int E, int R, int units) {
+  return (size_t)E * 4 + (size_t)R * 5 + (size_t)units * 5 + 16;
+}
+
+// One GEMM of one half of the units, its blocks cut into runs.
+struct Cut {
+  int group;          // CTAs side by side on neighbouring column tiles
+  int supers;         // groups of column tiles in a unit
+  int kb;             // blocks along K
+  int unit0, units;
+  long blocks;        // of one CTA of a group
+  int runs;
+  __device__ bool takes(int c) const { return c < runs * group; }
+  __device__ long begin(int run) const { return blocks * run / runs; }
+  // the run that holds block b
+  __device__ int owner(long b) const {
+    if (blocks * runs < (1ll << 31)) return (int)(((unsigned)(b + 1) * (unsigned)runs - 1u) / (unsigned)blocks);
+    return (int)(((b + 1) * runs - 1) / blocks);
+  }
+};
+
+__device__ __forceinline__ Cut make_cut(int tiles, int kb, int unit0, int units, int ctas) {
+  Cut c;
+  c.group = tiles % 8 == 0 ? 8 : tiles % 4 == 0 ? 4 : tiles % 2 == 0 ? 2 : 1;
+  if (c.group > ctas) c.group = 1;
+  c.supers = tiles / c.group;
+  c.kb = kb;
+  c.unit0 = unit0;
+  c.units = units;
+  c.blocks = (long)units * c.supers * kb;
+  const long most = (c.blocks + kMinRun - 1) / kMinRun;
+  const int groups = ctas / c.group;
+  c.runs = (int)(most < groups ? most : groups);
+  return c;
+}
 
 struct Ctl {
   uint64_t full_a[kMaxFewStages], full_b[kMaxFewStages], scales[kMaxFewStages], empty[kMaxFewStages];
@@ -57,54 +112,34 @@ struct Ctl {
   uint32_t tmem;
   int abort, go;
   int units;
-  int flag[2];
-};
-
-// The routing sorted by expert, in shared memory.
-struct Schedule {
-  int32_t* offset;  // [E + 1] sorted rows of each expert
-  uint16_t* perm;   // [T*k] sorted row -> flat index
-  uint16_t* unit_e; // [max_units] expert, first sorted row and rows of each unit
-  uint16_t* unit_r;
-  uint8_t* unit_n;
-};
-
-__host__ __device__ constexpr size_t schedule_bytes(int E, int R, int units) {
-  return (size_t)(E + 1) * 8 + (((size_t)R * 2 + 15) & ~15) + (size_t)units * 5 + 64;
-}
-
-// One GEMM cut into runs of blocks.
-struct Cut {
-  int tiles_per_unit, kb;  // column tiles, blocks along K
-  long blocks;
-  int ctas;                // that take part
-  __device__ long begin(int c) const { return blocks * c / ctas; }
-  // the CTA whose run holds block b
-  __device__ int owner(long b) const { return (int)(((b + 1) * ctas - 1) / blocks); }
+  int last;
+  int warp_sum[16];
+  Cut cuts[4];  // in order: a of each half of the units, y of each half
 };
 
 // A run's share of one tile.
 struct Seg {
   int unit, n;    // unit and column tile
-  int tile;       // index of its counter
   int k0, k1;     // blocks
+  int super;      // index of the tile's group
 };
 
-// `by_column`: tiles ordered column tile first (so that columns of out are
-// finished one after another), else unit first.
-__device__ __forceinline__ Seg seg_at(const Cut& c, long b, long end, int units, bool by_column) {
+__device__ __forceinline__ Seg seg_at(const Cut& c, long b, long end, int rank) {
   Seg s;
-  s.tile = (int)(b / c.kb);
-  s.k0 = (int)(b - (long)s.tile * c.kb);
+  s.super = (int)(b / c.kb);
+  s.k0 = (int)(b - (long)s.super * c.kb);
   s.k1 = (int)(end - b < c.kb - s.k0 ? s.k0 + (end - b) : c.kb);
-  if (by_column) {
-    s.n = s.tile / units;
-    s.unit = s.tile - s.n * units;
-  } else {
-    s.unit = s.tile / c.tiles_per_unit;
-    s.n = s.tile - s.unit * c.tiles_per_unit;
-  }
+  const int u = s.super / c.supers;
+  s.unit = c.unit0 + u;
+  s.n = (s.super - u * c.supers) * c.group + rank;
   return s;
+}
+
+// The runs that a tile is split over.
+__device__ __forceinline__ void seg_runs(const Cut& c, int super, int& first, int& last) {
+  const long b = (long)super * c.kb;
+  first = c.owner(b);
+  last = c.owner(b + c.kb - 1);
 }
 
 __device__ __forceinline__ bool vote_all(int bar, int threads, bool ok) {
@@ -128,12 +163,19 @@ __device__ __forceinline__ void cp_async_arrive_noinc(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
+__device__ __forceinline__ int atom_add_acq_rel(int32_t* p, int v) {
+  int old;
+  asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], %2;" : "=r"(old) : "l"(p), "r"(v) : "memory");
+  return old;
+}
+
 __device__ __forceinline__ uint32_t* word(const FewParams& p, int i) { return reinterpret_cast<uint32_t*>(p.hdr + i); }
 
 // ---------------------------------------------------------------- router
-// This CTA's part of the logits: kLogitTokens tokens by h_rows rows of Wr.
-// A warp takes every other row, a lane 8 neighbouring experts; the warps'
-// sums are added in order.
+// This CTA's part of the logits: kLogitTokens tokens by h_rows rows of Wr.  A
+// lane takes 8 neighbouring experts, as many lanes as a row needs (32 at
+// most), the rest of the warp and the other warps other rows; the lanes' and
+// the warps' sums are added in a fixed order.
 __device__ void router_logits(const FewParams& p, uint8_t* smem, int nthreads) {
   const int groups = (p.T + kLogitTokens - 1) / kLogitTokens;
   const int warps = nthreads / 32, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -148,16 +190,19 @@ __device__ void router_logits(const FewParams& p, uint8_t* smem, int nthreads) {
     xs[h * kLogitTokens + t] = t < nt ? __bfloat162float(p.x[(long)(t0 + t) * p.H + h0 + h]) : 0.0f;
   }
   __syncthreads();
+  int across = 1;  // lanes along a row
+  while (across < 32 && across * 8 < p.E) across <<= 1;
+  const int down = 32 / across;
   const bool vec = p.E % 8 == 0 && (reinterpret_cast<uintptr_t>(p.Wr) & 15) == 0;
   for (int e0 = 0; e0 < p.E; e0 += 256) {
-    const int e = e0 + lane * 8;
+    const int e = e0 + (lane & (across - 1)) * 8;
     float acc[kLogitTokens][8];
 #pragma unroll
     for (int t = 0; t < kLogitTokens; ++t)
 #pragma unroll
       for (int i = 0; i < 8; ++i) acc[t][i] = 0.0f;
 #pragma unroll 4
-    for (int h = warp; h < rows; h += warps) {
+    for (int h = warp * down + lane / across; h < rows; h += warps * down) {
       const __nv_bfloat16* wr = p.Wr + (long)(h0 + h) * p.E + e;
       float w[8];
       if (vec) {
@@ -180,10 +225,18 @@ __device__ void router_logits(const FewParams& p, uint8_t* smem, int nthreads) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) acc[t][i] = fmaf(xt[t], w[i], acc[t][i]);
     }
+    for (int o = across; o < 32; o <<= 1)
 #pragma unroll
-    for (int t = 0; t < kLogitTokens; ++t)
+      for (int t = 0; t < kLogitTokens; ++t)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) red[(warp * kLogitTokens + t) * 256 + lane * 8 + i] = acc[t][i];
+        for (int i = 0; i < 8; ++i) acc[t][i] += __shfl_xor_sync(0xffffffffu, acc[t][i], o);
+    if (lane < across)
+#pragma unroll
+      for (int t = 0; t < kLogitTokens; ++t) {
+        float4* r = reinterpret_cast<float4*>(red + (warp * kLogitTokens + t) * 256 + lane * 8);
+        r[0] = make_float4(acc[t][0], acc[t][1], acc[t][2], acc[t][3]);
+        r[1] = make_float4(acc[t][4], acc[t][5], acc[t][6], acc[t][7]);
+      }
     __syncthreads();
     const int ne = min(256, p.E - e0);
     for (int i = threadIdx.x; i < nt * 256; i += nthreads) {
@@ -197,12 +250,27 @@ __device__ void router_logits(const FewParams& p, uint8_t* smem, int nthreads) {
   }
 }
 
-// Selection and scores of one token from the parts of its logits.
-__device__ void router_select(const FewParams& p, int t, float* row, int nthreads) {
+// Selection and scores of one token from the parts of its logits: groups of
+// threads take shares of the parts, so that the loads are in flight together.
+__device__ void router_select(const FewParams& p, int t, float* smem, int nthreads) {
+  float* row = smem;                  // [E]
+  float* red = smem + p.E;            // [shares][E]
+  const int shares = max(1, min(8, nthreads / p.E));
+  const int per = (p.h_parts + shares - 1) / shares;
+  const int width = nthreads / shares;
+  const int share = threadIdx.x / width;
+  if (share < shares)
+    for (int e = threadIdx.x - share * width; e < p.E; e += width) {
+      float s = 0.0f;
+      const int i1 = min(p.h_parts, (share + 1) * per);
+#pragma unroll 16
+      for (int i = share * per; i < i1; ++i) s += __ldcg(p.logits + ((long)i * p.T + t) * p.E + e);
+      red[share * p.E + e] = s;
+    }
+  __syncthreads();
   for (int e = threadIdx.x; e < p.E; e += nthreads) {
-    float s = 0.0f;
-#pragma unroll 8
-    for (int i = 0; i < p.h_parts; ++i) s += __ldcg(p.logits + ((long)i * p.T + t) * p.E + e);
+    float s = red[e];
+    for (int i = 1; i < shares; ++i) s += red[i * p.E + e];
     row[e] = s;
   }
   __syncthreads();
@@ -218,7 +286,6 @@ __device__ void router_select(const FewParams& p, int t, float* row, int nthread
       p.idx_out[(long)t * p.k + lane] = e;
       p.scores_out[(long)t * p.k + lane] = s;
     }
-    __threadfence();
     __syncwarp();
     if (lane == 0) red_release_gpu_add(word(p, kWordRouted), 1u);
   }
@@ -250,67 +317,88 @@ __device__ void quantize_x(const FewParams& p, int nthreads) {
 }
 
 // ---------------------------------------------------------------- schedule
-// Rows grouped by expert in ascending flat index, and cut into units.
-__device__ void build_units(const FewParams& p, const Schedule& s, int32_t* cursor, Ctl* ctl, int nthreads) {
-  const int R = p.T * p.k;
-  for (int e = threadIdx.x; e < p.E; e += nthreads) cursor[e] = 0;
-  __syncthreads();
+// Rows grouped by expert in ascending flat index, and cut into units: a
+// counting sort whose warps own contiguous ranges of the flat indices, so
+// that (warp, place) is their order.  `scratch`: the ids and a count per warp
+// and expert.
+__device__ void build_units(const FewParams& p, const Schedule& s, uint8_t* scratch, Ctl* ctl, int nthreads) {
+  const int R = p.T * p.k, W = nthreads / 32, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int shift = __ffs(p.unit_rows) - 1;
+  uint16_t* ids = reinterpret_cast<uint16_t*>(scratch);
+  uint32_t* hist = reinterpret_cast<uint32_t*>(scratch + (((size_t)R * 2 + 15) & ~15));  // [W][E]
+  for (int i = threadIdx.x; i < W * p.E; i += nthreads) hist[i] = 0;
   bool bad = false;
   for (int f = threadIdx.x; f < R; f += nthreads) {
     const int e = p.idx[f];
-    if (e >= 0 && e < p.E)
-      atomicAdd(&cursor[e], 1);
-    else
-      bad = true;
+    const bool in = e >= 0 && e < p.E;
+    bad |= !in;
+    ids[f] = (uint16_t)(in ? e : kNoUnit);
   }
   if (bad && blockIdx.x == 0) atomicOr(p.hdr + kHdrError, MOK_ERRBIT_BAD_INDEX);
   __syncthreads();
-  if (threadIdx.x < 32) {
-    const int lane = threadIdx.x;
-    int rows = 0, units = 0;
-    for (int e0 = 0; e0 < p.E; e0 += 32) {
-      const int e = e0 + lane;
-      const int c = e < p.E ? cursor[e] : 0;
-      const int u = (c + p.unit_rows - 1) / p.unit_rows;
-      int ic = c, iu = u;
+  const int per = ((R + 32 * W - 1) / (32 * W)) * 32;
+  const int f0 = warp * per, f1 = min(R, f0 + per);
+  uint32_t* mine = hist + warp * p.E;
+  for (int f = f0 + lane; f - lane < f1; f += 32) {
+    const int e = f < f1 ? ids[f] : kNoUnit;
+    const uint32_t same = __match_any_sync(0xffffffffu, e);
+    if (e != kNoUnit && (same & ((1u << lane) - 1u)) == 0) mine[e] += __popc(same);
+    __syncwarp();
+  }
+  __syncthreads();
+  // thread i: experts [i * each, (i + 1) * each); rows and units scanned in one word
+  const int each = (p.E + nthreads - 1) / nthreads;
+  const int e0 = threadIdx.x * each, e1 = min(p.E, e0 + each);
+  uint32_t sum = 0;
+  for (int e = e0; e < e1; ++e) {
+    uint32_t rows = 0;
+    for (int w = 0; w < W; ++w) {
+      const uint32_t v = hist[w * p.E + e];
+      hist[w * p.E + e] = rows;
+      rows += v;
+    }
+    s.offset[e] = (uint16_t)rows;  // the count, for now
+    sum += rows | (((rows + p.unit_rows - 1) >> shift) << 16);
+  }
+  uint32_t incl = sum;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int vc = __shfl_up_sync(0xffffffffu, ic, o), vu = __shfl_up_sync(0xffffffffu, iu, o);
-        if (lane >= o) {
-          ic += vc;
-          iu += vu;
-        }
-      }
-      const int off = rows + ic - c;
-      if (e < p.E) {
-        s.offset[e] = off;
-        cursor[e] = off;
-      }
-      for (int i = 0; i < u; ++i) {
-        const int at = units + iu - u + i;
-        s.unit_e[at] = (uint16_t)e;
-        s.unit_r[at] = (uint16_t)(off + i * p.unit_rows);
-        s.unit_n[at] = (uint8_t)min(p.unit_rows, c - i * p.unit_rows);
-      }
-      rows += __shfl_sync(0xffffffffu, ic, 31);
-      units += __shfl_sync(0xffffffffu, iu, 31);
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) ctl->warp_sum[warp] = (int)incl;
+  __syncthreads();
+  uint32_t at = incl - sum;
+  for (int w = 0; w < warp; ++w) at += (uint32_t)ctl->warp_sum[w];
+  for (int e = e0; e < e1; ++e) {
+    const int rows = s.offset[e], off = at & 0xFFFF, u0 = at >> 16;
+    const int units = (rows + p.unit_rows - 1) >> shift;
+    s.offset[e] = (uint16_t)off;
+    s.unit0[e] = (uint16_t)u0;
+    for (int i = 0; i < units; ++i) {
+      s.unit_e[u0 + i] = (uint16_t)e;
+      s.unit_r[u0 + i] = (uint16_t)(off + i * p.unit_rows);
+      s.unit_n[u0 + i] = (uint8_t)min(p.unit_rows, rows - i * p.unit_rows);
+    }
+    at += (uint32_t)rows | ((uint32_t)units << 16);
+  }
+  if (threadIdx.x == nthreads - 1) ctl->units = (int)(at >> 16);
+  __syncthreads();
+  for (int f = f0 + lane; f - lane < f1; f += 32) {
+    const int e = f < f1 ? ids[f] : kNoUnit;
+    const uint32_t same = __match_any_sync(0xffffffffu, e);
+    const int ahead = __popc(same & ((1u << lane) - 1u));
+    const int place = e != kNoUnit ? (int)mine[e] + ahead : 0;  // among the expert's rows
+    __syncwarp();
+    if (e != kNoUnit) {
+      if (ahead == 0) mine[e] += __popc(same);
+      s.perm[s.offset[e] + place] = (uint16_t)f;
+      s.unit_of[f] = (uint16_t)(s.unit0[e] + (place >> shift));
+      s.row_of[f] = (uint8_t)(place & (p.unit_rows - 1));
+    } else if (f < f1) {
+      s.unit_of[f] = (uint16_t)kNoUnit;
     }
     __syncwarp();
-    for (int f0 = 0; f0 < R; f0 += 32) {
-      const int f = f0 + lane;
-      int e = f < R ? p.idx[f] : -1;
-      if (e < 0 || e >= p.E) e = -1;
-      const uint32_t same = __match_any_sync(0xffffffffu, e);
-      const int ahead = __popc(same & ((1u << lane) - 1u));
-      const int at = e >= 0 ? cursor[e] + ahead : 0;
-      __syncwarp();
-      if (e >= 0) {
-        s.perm[at] = (uint16_t)f;
-        if (ahead == 0) cursor[e] += __popc(same);
-      }
-      __syncwarp();
-    }
-    if (lane == 0) ctl->units = units;
   }
   __syncthreads();
 }
@@ -349,23 +437,48 @@ __device__ __forceinline__ void store_hidden(const FewParams& p, int row, int n,
   }
 }
 
-// out of one tile of 256 columns, all tokens: 2 columns a thread
-__device__ void combine_columns(const FewParams& p, int n, int tid) {
-  const int c = n * 256 + tid * 2;
-  if (c >= p.H) return;
-  for (int t = 0; t < p.T; ++t) {
-    float a0 = 0.0f, a1 = 0.0f;
-#pragma unroll 8
+// The combine: 4 columns of a token a thread, y from its buffer or, where its
+// tile was split along K, as the sum of the parts.
+__device__ void combine(const FewParams& p, const Schedule& s, const Cut* cuts, int nthreads) {
+  const int vecs = p.H / 4;
+  const int slot_floats = 2 * p.unit_rows * 128;
+  for (long i = (long)blockIdx.x * nthreads + threadIdx.x; i < (long)p.T * vecs; i += (long)gridDim.x * nthreads) {
+    const int t = (int)(i / vecs), col = (int)(i - (long)t * vecs) * 4;
+    const int n = col >> 8, in_tile = (((col >> 7) & 1) * p.unit_rows) * 128 + (col & 127);
+    float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
     for (int j = 0; j < p.k; ++j) {
-      const long f = (long)t * p.k + j;
-      const int e = p.idx[f];
-      if (e < 0 || e >= p.E) continue;
-      const float s = p.scores[f];
-      const float2 y = __ldcg(reinterpret_cast<const float2*>(p.y + f * p.H + c));
-      a0 = fmaf(s, y.x, a0);
-      a1 = fmaf(s, y.y, a1);
+      const int f = t * p.k + j;
+      const int unit = s.unit_of[f];
+      if (unit == kNoUnit) continue;
+      const int half = unit >= cuts[1].unit0;
+      const Cut& c = cuts[half];
+      const int sup = (unit - c.unit0) * c.supers + n / c.group;
+      int first, last;
+      seg_runs(c, sup, first, last);
+      float4 y;
+      if (first == last) {
+        y = __ldcg(reinterpret_cast<const float4*>(p.y + (long)f * p.H + col));
+      } else {
+        const int rank = n % c.group, at = in_tile + s.row_of[f] * 128;
+        y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int o = first; o <= last; ++o) {
+          const long slot = (long)(o * c.group + rank) * 4 + half * 2 + (o == first ? 1 : 0);
+          const float4 v = __ldcg(reinterpret_cast<const float4*>(p.part + slot * slot_floats + at));
+          y.x += v.x;
+          y.y += v.y;
+          y.z += v.z;
+          y.w += v.w;
+        }
+      }
+      const float w = p.scores[f];
+      acc[0] = fmaf(w, y.x, acc[0]);
+      acc[1] = fmaf(w, y.y, acc[1]);
+      acc[2] = fmaf(w, y.z, acc[2]);
+      acc[3] = fmaf(w, y.w, acc[3]);
     }
-    *reinterpret_cast<uint32_t*>(p.out + (long)t * p.H + c) = pack_bf16x2(a0, a1);
+    *reinterpret_cast<uint2*>(p.out + (long)t * p.H + col) =
+        make_uint2(pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3]));
   }
 }
 
@@ -380,12 +493,15 @@ __global__ void __launch_bounds__(MX ? 320 : 256, 1) few_kernel(const __grid_con
   uint8_t* sf_smem = smem + (size_t)p.stages * stage_bytes;
   Ctl* ctl = reinterpret_cast<Ctl*>(sf_smem + (MX ? p.stages * kSfBytes : 0));
   Schedule sched;
-  sched.offset = reinterpret_cast<int32_t*>(ctl + 1);
-  int32_t* cursor = sched.offset + p.E + 1;
-  sched.perm = reinterpret_cast<uint16_t*>(cursor + p.E + 1);
-  sched.unit_e = sched.perm + (((p.T * p.k) + 7) & ~7);
+  const int R = p.T * p.k;
+  sched.offset = reinterpret_cast<uint16_t*>(ctl + 1);
+  sched.unit0 = sched.offset + p.E;
+  sched.perm = sched.unit0 + p.E;
+  sched.unit_of = sched.perm + R;
+  sched.unit_e = sched.unit_of + R;
   sched.unit_r = sched.unit_e + p.max_units;
-  sched.unit_n = reinterpret_cast<uint8_t*>(sched.unit_r + p.max_units);
+  sched.row_of = reinterpret_cast<uint8_t*>(sched.unit_r + p.max_units);
+  sched.unit_n = sched.row_of + R;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   WaitCtx wc{&ctl->abort, p.hdr + kHdrAbort, p.hdr + kHdrError};
@@ -418,7 +534,6 @@ __global__ void __launch_bounds__(MX ? 320 : 256, 1) few_kernel(const __grid_con
   if (p.Wr) router_logits(p, smem, kThreads);
   bool ok = true;
   if (MX || p.Wr) {
-    __threadfence();
     __syncthreads();
     if (threadIdx.x == 0) red_release_gpu_add(word(p, kWordPrepared), 1u);
   }
@@ -434,30 +549,22 @@ __global__ void __launch_bounds__(MX ? 320 : 256, 1) few_kernel(const __grid_con
     if (threadIdx.x == 0) ctl->go = wait_flag_geq(word(p, kWordRouted), p.T, wc) ? 1 : 0;
     __syncthreads();
     ok = ctl->go != 0;
-    // the stages' first loads (async proxy) come after these threads' use of the same shared memory
-    fence_proxy_async_shared();
   }
-  if (ok) build_units(p, sched, cursor, ctl, kThreads);
-  __syncthreads();
+  if (ok) build_units(p, sched, smem, ctl, kThreads);
+  // the stages' first loads (async proxy) come after these threads' use of the same shared memory
+  fence_proxy_async_shared();
+  const int c = blockIdx.x;
+  if (ok && threadIdx.x < 4) {
+    const int i = threadIdx.x, units = ctl->units, half = (units + 1) / 2;
+    const int u0 = i & 1 ? half : 0, nu = i & 1 ? units - half : half;
+    ctl->cuts[i] = i < 2 ? make_cut(p.I / 128, p.H / kEl, u0, nu, gridDim.x)
+                         : make_cut((p.H + 255) / 256, p.I / kEl, u0, nu, gridDim.x);
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ctl->tmem;
   const int units = ok ? ctl->units : 0;
-
-  Cut cut[2];
-  cut[0].tiles_per_unit = p.I / 128;
-  cut[0].kb = p.H / kEl;
-  cut[1].tiles_per_unit = (p.H + 255) / 256;
-  cut[1].kb = p.I / kEl;
-#pragma unroll
-  for (int g = 0; g < 2; ++g) {
-    cut[g].blocks = (long)units * cut[g].tiles_per_unit * cut[g].kb;
-    const long most = (cut[g].blocks + 1) / 2;
-    cut[g].ctas = (int)(most < (long)gridDim.x ? most : (long)gridDim.x);
-  }
-  const int hidden_tiles = units * cut[0].tiles_per_unit;
-  const int c = blockIdx.x;
 
   if (units == 0) {
     // nothing routed: zeros (or a call that gave up)
@@ -469,11 +576,13 @@ __global__ void __launch_bounds__(MX ? 320 : 256, 1) few_kernel(const __grid_con
       uint32_t stage = 0, phase = 0;
       long issued = 0;
       bool fine = true;
-      for (int g = 0; g < 2 && fine; ++g) {
-        if (c >= cut[g].ctas) continue;
-        const long end = cut[g].begin(c + 1);
-        for (long b = cut[g].begin(c); b < end && fine;) {
-          const Seg s = seg_at(cut[g], b, end, units, g == 1);
+      for (int ph = 0; ph < 4; ++ph) {
+        const Cut cut = ctl->cuts[ph];
+        const int g = ph >> 1;
+        if (!fine || !cut.takes(c)) continue;
+        const long end = cut.begin(c / cut.group + 1);
+        for (long b = cut.begin(c / cut.group); b < end && fine;) {
+          const Seg s = seg_at(cut, b, end, c % cut.group);
           const int e = sched.unit_e[s.unit];
           const int col = g == 0 ? s.n * 128 : s.n * 256;
           const bool second = g == 0 || col + 128 < p.H;
@@ -522,11 +631,13 @@ __global__ void __launch_bounds__(MX ? 320 : 256, 1) few_kernel(const __grid_con
     // ---------------------------------------------------------------- MMA
     uint32_t stage = 0, phase = 0, count = 0;
     bool fine = true;
-    for (int g = 0; g < 2 && fine; ++g) {
-      if (c >= cut[g].ctas) continue;
-      const long end = cut[g].begin(c + 1);
-      for (long b = cut[g].begin(c); b < end && fine;) {
-        const Seg s = seg_at(cut[g], b, end, units, g == 1);
+    for (int ph = 0; ph < 4; ++ph) {
+      const Cut cut = ctl->cuts[ph];
+      const int g = ph >> 1;
+      if (!fine || !cut.takes(c)) continue;
+      const long end = cut.begin(c / cut.group + 1);
+      for (long b = cut.begin(c / cut.group); b < end && fine;) {
+        const Seg s = seg_at(cut, b, end, c % cut.group);
         const int n = (sched.unit_n[s.unit] + 15) & ~15;
         const bool second = g == 0 || s.n * 256 + 128 < p.H;
         const uint32_t buf = count & 1;
@@ -604,24 +715,27 @@ __global__ void __launch_bounds__(MX ? 320 : 256, 1) few_kernel(const __grid_con
     const int ch = tid & 7;  // this thread's 16-byte piece of a row's 128 bytes
     uint32_t stage = 0, phase = 0;
     bool fine = true;
-    for (int g = 0; g < 2 && fine; ++g) {
-      if (c >= cut[g].ctas) continue;
+    for (int ph = 0; ph < 4; ++ph) {
+      const Cut cut = ctl->cuts[ph];
+      const int g = ph >> 1;
+      if (!fine || !cut.takes(c)) continue;
       // x is ready at once (MXFP8: once every CTA has quantised its share),
-      // a when every tile of it is finished
+      // a when every tile of this half of it is finished
       if (g == 1 || (MX && !p.Wr)) {
         bool go = true;
         if (tid == 0)
           go = g == 0 ? wait_flag_geq(word(p, kWordPrepared), gridDim.x, wc)
-                      : wait_flag_geq(word(p, kWordHidden), hidden_tiles, wc);
-        if (!vote_all(2, kProducers, go)) break;
+                      : wait_flag_geq(word(p, kWordHidden + (ph & 1)), cut.units * (p.I / 128), wc);
+        fine = vote_all(2, kProducers, go);
+        if (!fine) continue;
       }
       const int K = g == 0 ? p.H : p.I;
       const uint8_t* src = g == 0 ? (MX ? p.xq : reinterpret_cast<const uint8_t*>(p.x)) : static_cast<uint8_t*>(p.a);
       const uint8_t* sfs = g == 0 ? p.xsf : p.asf;
       const long lo = (long)p.T * p.k * p.I * 2;  // a's second part
-      const long end = cut[g].begin(c + 1);
-      for (long b = cut[g].begin(c); b < end && fine;) {
-        const Seg s = seg_at(cut[g], b, end, units, g == 1);
+      const long end = cut.begin(c / cut.group + 1);
+      for (long b = cut.begin(c / cut.group); b < end && fine;) {
+        const Seg s = seg_at(cut, b, end, c % cut.group);
         const int n = sched.unit_n[s.unit], r0 = sched.unit_r[s.unit];
         long at[8];  // byte offset of this thread's piece in rows tid / 8 + 8 i
 #pragma unroll
@@ -662,15 +776,18 @@ __global__ void __launch_bounds__(MX ? 320 : 256, 1) few_kernel(const __grid_con
     const int slot_floats = 2 * p.unit_rows * 128;
     uint32_t count = 0;
     bool fine = true;
-    for (int g = 0; g < 2 && fine; ++g) {
-      if (c >= cut[g].ctas) continue;
-      const long end = cut[g].begin(c + 1);
-      for (long b = cut[g].begin(c); b < end;) {
-        const Seg s = seg_at(cut[g], b, end, units, g == 1);
+    for (int ph = 0; ph < 4; ++ph) {
+      const Cut cut = ctl->cuts[ph];
+      const int g = ph >> 1, half = ph & 1;
+      if (!fine || !cut.takes(c)) continue;
+      const int run = c / cut.group, rank = c % cut.group;
+      const long end = cut.begin(run + 1);
+      for (long b = cut.begin(run); b < end;) {
+        const Seg s = seg_at(cut, b, end, rank);
         b += s.k1 - s.k0;
         const int n = sched.unit_n[s.unit], r0 = sched.unit_r[s.unit];
         const bool second = g == 0 || s.n * 256 + 128 < p.H;
-        const bool whole = s.k0 == 0 && s.k1 == cut[g].kb;
+        const bool whole = s.k0 == 0 && s.k1 == cut.kb;
         const int lane_col = q * 32 + lane;
         auto finish = [&](int i0, const float* v0, const float* v1) {
           const int rows = min(16, n - i0);
@@ -682,8 +799,8 @@ __global__ void __launch_bounds__(MX ? 320 : 256, 1) few_kernel(const __grid_con
             for (int i = 0; i < 16; ++i) {
               if (i >= rows) break;
               float* yr = y + (long)sched.perm[r0 + i0 + i] * p.H;
-              yr[0] = v0[i];
-              if (second) yr[128] = v1[i];
+              __stcg(yr, v0[i]);
+              if (second) __stcg(yr + 128, v1[i]);
             }
           }
         };
@@ -692,7 +809,8 @@ __global__ void __launch_bounds__(MX ? 320 : 256, 1) few_kernel(const __grid_con
         if (!fine) break;
         tc_fence_after();
         const uint32_t d = tmem + buf * 2 * p.unit_rows + ((uint32_t)(q * 32) << 16);
-        float* slot = p.part + (long)(2 * c + (s.k0 == 0 ? 1 : 0)) * slot_floats + lane_col;
+        // four slots a CTA: of each half, the tile that its run ends in (1) or begins in (0)
+        float* slot = p.part + (long)(4 * c + 2 * half + (s.k0 == 0 ? 1 : 0)) * slot_floats + lane_col;
         for (int i0 = 0; i0 < n; i0 += 16) {
           uint32_t w0[16], w1[16];
           tmem_ld16_issue(d + i0, w0);
@@ -720,56 +838,48 @@ __global__ void __launch_bounds__(MX ? 320 : 256, 1) few_kernel(const __grid_con
         tc_fence_before();
         mbar_arrive(&ctl->tempty[buf]);
         ++count;
+        if (g == 1) continue;
         if (!whole) {
-          const int first = cut[g].owner((long)s.tile * cut[g].kb);
-          const int last = cut[g].owner((long)s.tile * cut[g].kb + cut[g].kb - 1);
-          int32_t* arrivals = p.tile_count + (g == 0 ? 0 : p.max_units * cut[0].tiles_per_unit) + s.tile;
-          __threadfence();
+          int first, last;
+          seg_runs(cut, s.super, first, last);
           named_bar_sync(1, kEpilogue);
           if (tid == 0) {
-            const int old = atomicAdd(arrivals, 1);
-            ctl->flag[0] = old == last - first;
+            int32_t* arrivals = p.tile_count + s.unit * (p.I / 128) + s.n;
+            const int old = atom_add_acq_rel(arrivals, 1);
+            ctl->last = old == last - first;
             if (old == last - first) *arrivals = 0;
-            __threadfence();
           }
           __syncwarp();
           named_bar_sync(1, kEpilogue);
-          if (!ctl->flag[0]) continue;
-          // the last to arrive: the parts in the order of K (the first CTA's
-          // part begins the tile; the others' are the head of their runs)
+          if (!ctl->last) continue;
+          // the last to arrive: the parts in the order of K (the tile ends
+          // the first run, and begins the others)
           for (int i0 = 0; i0 < n; i0 += 16) {
             float v0[16], v1[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) v0[i] = v1[i] = 0.0f;
             for (int o = first; o <= last; ++o) {
-              const float* from = p.part + (long)(2 * o + (o == first ? 1 : 0)) * slot_floats + lane_col;
+              const float* from =
+                  p.part + (long)(4 * (o * cut.group + rank) + 2 * half + (o == first ? 1 : 0)) * slot_floats + lane_col;
 #pragma unroll
               for (int i = 0; i < 16; ++i) {
                 if (i0 + i >= n) break;
                 v0[i] += __ldcg(from + (i0 + i) * 128);
-                if (second) v1[i] += __ldcg(from + (p.unit_rows + i0 + i) * 128);
+                v1[i] += __ldcg(from + (p.unit_rows + i0 + i) * 128);
               }
             }
             finish(i0, v0, v1);
           }
         }
-        // a finished tile
-        __threadfence();
+        // a finished tile of a
         named_bar_sync(1, kEpilogue);
-        if (g == 0) {
-          if (tid == 0) red_release_gpu_add(word(p, kWordHidden), 1u);
-          continue;
-        }
-        if (tid == 0) {
-          const int old = atomicAdd(p.col_count + s.n, 1);
-          ctl->flag[1] = old == units - 1;
-          if (old == units - 1) p.col_count[s.n] = 0;
-          __threadfence();
-        }
+        if (tid == 0) red_release_gpu_add(word(p, kWordHidden + half), 1u);
         __syncwarp();
-        named_bar_sync(1, kEpilogue);
-        if (ctl->flag[1]) combine_columns(p, s.n, tid);
       }
+    }
+    if (fine && units > 0) {
+      named_bar_sync(1, kEpilogue);
+      if (tid == 0) red_release_gpu_add(word(p, kWordSummed), 1u);
     }
   } else {
     // ---------------------------------------------------------------- MXFP8: weight scales
@@ -778,9 +888,10 @@ __global__ void __launch_bounds__(MX ? 320 : 256, 1) few_kernel(const __grid_con
     const int i = warp - 8;
     uint32_t stage = 0, phase = 0;
     bool fine = true;
-    for (int g = 0; g < 2 && fine; ++g) {
-      if (c >= cut[g].ctas) continue;
-      const long blocks = cut[g].begin(c + 1) - cut[g].begin(c);
+    for (int ph = 0; ph < 4; ++ph) {
+      const Cut cut = ctl->cuts[ph];
+      if (!fine || !cut.takes(c)) continue;
+      const long blocks = cut.begin(c / cut.group + 1) - cut.begin(c / cut.group);
       for (long b = 0; b < blocks; ++b) {
         fine = mbar_wait(&ctl->full_a[stage], phase, wc);
         if (!fine) break;
@@ -809,11 +920,16 @@ __global__ void __launch_bounds__(MX ? 320 : 256, 1) few_kernel(const __grid_con
   asm volatile("barrier.sync 0;" ::: "memory");
   tc_fence_after();
   if (warp == 0) tmem_dealloc(tmem, 512);
+  if (units > 0 && (long)c * kThreads < (long)p.T * (p.H / 4)) {
+    if (threadIdx.x == 0) ctl->go = wait_flag_geq(word(p, kWordSummed), gridDim.x, wc) ? 1 : 0;
+    __syncthreads();
+    if (ctl->go) combine(p, sched, ctl->cuts + 2, kThreads);
+  }
   if (threadIdx.x == 0) {
     // the last CTA to end leaves the counters as it found them
     __threadfence();
     if (atomicAdd(p.hdr + kWordLeft, 1) == (int)gridDim.x - 1) {
-      p.hdr[kWordPrepared] = p.hdr[kWordRouted] = p.hdr[kWordHidden] = p.hdr[kWordLeft] = 0;
+      for (int i = kWordPrepared; i <= kWordLeft; ++i) p.hdr[i] = 0;
     }
   }
 }
@@ -828,9 +944,12 @@ int units_bound(int T, int E, int k, int unit_rows) {
   return n < R ? n : R;
 }
 
+// At most 64 parts of the logits: enough SMs to read Wr at once, and few
+// enough parts to add up quickly.
 void logit_parts(int T, int H, int ctas, int* parts, int* rows) {
   const int groups = (T + kLogitTokens - 1) / kLogitTokens;
   int n = ctas / groups;
+  if (n > 64) n = 64;
   if (n < 1) n = 1;
   int r = (H + n - 1) / n;
   r = (r + 7) & ~7;
@@ -854,9 +973,7 @@ FewLayout few_layout(const mok_shape& s, mok_precision prec) {
   L.header = take(kHeaderWords * 4);
   // room for the units of any call of this H, I, E and k
   const size_t units = units_bound(MOK_FEW_MAX_TOKENS, s.E, s.k, 16);
-  L.tile_words = units * (s.I / 128 + (s.H + 255) / 256);
-  L.col_words = (s.H + 255) / 256;
-  L.tiles = take((L.tile_words + L.col_words) * 4);
+  L.tiles = take(units * (s.I / 128) * 4);
   int parts, rows;
   logit_parts(s.T, s.H, ctas, &parts, &rows);
   L.logits = take((size_t)parts * s.T * s.E * 4);
@@ -864,7 +981,7 @@ FewLayout few_layout(const mok_shape& s, mok_precision prec) {
   L.xsf = mx ? take((size_t)s.T * (s.H / 32)) : 0;
   L.a = take(R * s.I * (mx ? 1 : 4));
   L.asf = mx ? take(R * (s.I / 32)) : 0;
-  L.part = take((size_t)ctas * 2 * 2 * few_unit_rows(s.T) * 128 * 4);
+  L.part = take((size_t)ctas * 4 * 2 * few_unit_rows(s.T) * 128 * 4);
   L.y = take(R * s.H * 4);
   L.total = off;
   return L;

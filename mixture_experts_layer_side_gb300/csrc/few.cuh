@@ -13,12 +13,11 @@ inline int few_unit_rows(int T) { return T <= 16 ? 16 : T <= 32 ? 32 : 64; }
 // workspace serves calls of fewer tokens: every counter is zero between calls.
 struct FewLayout {
   size_t header;   // int32 [kHeaderWords]: word 0 the error bits
-  size_t tiles;    // int32: tiles' arrivals (both GEMMs), then column tiles'
-  size_t tile_words, col_words;
+  size_t tiles;    // int32 [units, I/128]: arrivals at the tiles of a
   size_t logits;   // f32 [parts, T, E] router logits, in parts along H
   size_t xq, xsf;  // MXFP8: codes [T, H] and scales [T, H/32] of x
   size_t a, asf;   // bf16 [2][T*k, I] (a, and what its rounding left); MXFP8: codes, and scales [T*k, I/32]
-  size_t part;     // f32 [2 per CTA][2][unit rows][128] sums of tiles split along K
+  size_t part;     // f32 [4 per CTA][2][unit rows][128] sums of tiles split along K
   size_t y;        // f32 [T*k, H]
   size_t total;
 };
@@ -33,8 +32,7 @@ struct FewParams {
   int T, H, I, E, k;
   int unit_rows, stages;
   int32_t* hdr;
-  int32_t* tile_count;  // [units * I/128] first GEMM, then [units * column tiles] second
-  int32_t* col_count;   // [column tiles]
+  int32_t* tile_count;  // [units, I/128]
   int max_units;        // capacity of the unit table
   const __nv_bfloat16* x;
   const int32_t* idx;

@@ -5,7 +5,7 @@ from __future__ import annotations
 import torch
 
 from . import _lib
-from ._check import on, require, tensor
+from ._check import fits, on, require, tensor
 from .inputs import Shape
 from .layer import PRECISIONS
 
@@ -27,32 +27,41 @@ class MoKDecoder:
         if n == 0:
             raise _lib.MokError(2, "unsupported shape")
         self.ws = torch.zeros(n, dtype=torch.uint8, device=self.device)
+        self._w13, self._w2 = (shape.E, shape.H, shape.I), (shape.E, shape.I, shape.H)
 
     def _weights(self, W1, W3, W2):
-        s = self.shape
-        for name, W, rows, cols in (("W1", W1, s.H, s.I), ("W3", W3, s.H, s.I), ("W2", W2, s.I, s.H)):
-            if self.prec == _lib.MOK_BF16:
-                tensor(W, name, (s.E, rows, cols), (torch.bfloat16,), self.device)
-            else:
+        d, bf16 = self.device, torch.bfloat16
+        if self.prec == _lib.MOK_BF16:
+            if not (fits(W1, self._w13, bf16, d) and fits(W3, self._w13, bf16, d) and fits(W2, self._w2, bf16, d)):
+                for name, W, shape in (("W1", W1, self._w13), ("W3", W3, self._w13), ("W2", W2, self._w2)):
+                    tensor(W, name, shape, (bf16,), d)
+        elif not (type(W1) is type(W3) is type(W2) is _lib.MokMx):
+            for name, W in (("W1", W1), ("W3", W3), ("W2", W2)):
                 require(isinstance(W, _lib.MokMx), f"{name}: an MXFP8 descriptor is wanted")
 
     def _begin(self, x, out):
-        s = self.shape
-        require(isinstance(x, torch.Tensor) and x.dim() == 2 and x.shape[0] <= s.T,
-                f"x: at most {s.T} rows of {s.H} are wanted")
+        s, d = self.shape, self.device
+        if type(x) is not torch.Tensor or x.dim() != 2 or x.shape[0] > s.T:
+            require(isinstance(x, torch.Tensor) and x.dim() == 2 and x.shape[0] <= s.T,
+                    f"x: at most {s.T} rows of {s.H} are wanted")
         T = x.shape[0]
-        tensor(x, "x", (T, s.H), (torch.bfloat16,), self.device)
+        rows = (T, s.H)
+        if not fits(x, rows, torch.bfloat16, d):
+            tensor(x, "x", rows, (torch.bfloat16,), d)
         if out is None:
-            out = torch.empty((T, s.H), dtype=torch.bfloat16, device=self.device)
-        tensor(out, "out", (T, s.H), (torch.bfloat16,), self.device)
+            out = torch.empty(rows, dtype=torch.bfloat16, device=d)
+        elif not fits(out, rows, torch.bfloat16, d):
+            tensor(out, "out", rows, (torch.bfloat16,), d)
         return T, out, _lib.shape_of(T, s.H, s.I, s.E, s.k)
 
     def forward(self, x, topk_idx, scores, W1, W3, W2, out=None, stream=None):
         """out [T, H] for the routing given (int32 ids and f32 scores [T, k])."""
         T, out, cshape = self._begin(x, out)
         self._weights(W1, W3, W2)
-        tensor(topk_idx, "topk_idx", (T, self.shape.k), (torch.int32,), self.device)
-        tensor(scores, "scores", (T, self.shape.k), (torch.float32,), self.device)
+        rows, d = (T, self.shape.k), self.device
+        if not (fits(topk_idx, rows, torch.int32, d) and fits(scores, rows, torch.float32, d)):
+            tensor(topk_idx, "topk_idx", rows, (torch.int32,), d)
+            tensor(scores, "scores", rows, (torch.float32,), d)
         if T:
             _lib.mok_few_forward(cshape, self.prec, self.ws, topk_idx, x, scores, W1, W3, W2, out, stream)
         return out
@@ -60,14 +69,15 @@ class MoKDecoder:
     def layer(self, x, Wr, W1, W3, W2, bias=None, out=None, stream=None):
         """(out, topk_idx, scores), the router included: Wr bf16 [H, E], bias
         f32 [E] or None (selection only)."""
-        s = self.shape
+        s, d = self.shape, self.device
         T, out, cshape = self._begin(x, out)
         self._weights(W1, W3, W2)
-        tensor(Wr, "Wr", (s.H, s.E), (torch.bfloat16,), self.device)
-        if bias is not None:
-            tensor(bias, "bias", (s.E,), (torch.float32,), self.device)
-        idx = torch.empty((T, s.k), dtype=torch.int32, device=self.device)
-        scores = torch.empty((T, s.k), dtype=torch.float32, device=self.device)
+        if not fits(Wr, (s.H, s.E), torch.bfloat16, d):
+            tensor(Wr, "Wr", (s.H, s.E), (torch.bfloat16,), d)
+        if bias is not None and not fits(bias, (s.E,), torch.float32, d):
+            tensor(bias, "bias", (s.E,), (torch.float32,), d)
+        idx = torch.empty((T, s.k), dtype=torch.int32, device=d)
+        scores = torch.empty((T, s.k), dtype=torch.float32, device=d)
         if T:
             _lib.mok_few_layer(cshape, self.prec, self.ws, x, Wr, bias, W1, W3, W2, idx, scores, out, stream)
         return out, idx, scores

@@ -5,7 +5,7 @@ from __future__ import annotations
 import torch
 
 from . import _lib
-from ._check import on, require, tensor
+from ._check import fits, on, require, rows_fit, tensor
 
 _TYPES = (torch.bfloat16, torch.float32)
 
@@ -27,39 +27,48 @@ class DistillLoss:
         self.ws = torch.zeros(n, dtype=torch.uint8, device=self.device)
 
     def _begin(self, z, ids, vals, temperature):
-        require(isinstance(z, torch.Tensor) and z.dim() == 2 and z.shape[0] <= self.rows,
-                f"z: at most {self.rows} rows of {self.vocab} are wanted")
-        require(isinstance(ids, torch.Tensor) and ids.dim() == 2 and 1 <= ids.shape[1] <= self.top,
-                f"ids: lists of 1 to {self.top} entries are wanted")
+        d = self.device
+        if not (type(z) is type(ids) is torch.Tensor and z.dim() == ids.dim() == 2):
+            require(isinstance(z, torch.Tensor) and z.dim() == 2, "z: a matrix is wanted")
+            require(isinstance(ids, torch.Tensor) and ids.dim() == 2, "ids: a matrix is wanted")
         T, K = z.shape[0], ids.shape[1]
-        tensor(z, "z", (T, self.vocab), _TYPES, self.device, rows_apart=True)
-        tensor(ids, "ids", (T, K), (torch.int32,), self.device)
-        tensor(vals, "vals", (T, K), (torch.float32,), self.device)
+        if T > self.rows:
+            require(False, f"z: at most {self.rows} rows are wanted")
+        if not 1 <= K <= self.top:
+            require(False, f"ids: lists of 1 to {self.top} entries are wanted")
+        if not (rows_fit(z, (T, self.vocab), z.dtype, d) and z.dtype in _TYPES and fits(ids, (T, K), torch.int32, d) and
+                fits(vals, (T, K), torch.float32, d)):
+            tensor(z, "z", (T, self.vocab), _TYPES, d, rows_apart=True)
+            tensor(ids, "ids", (T, K), (torch.int32,), d)
+            tensor(vals, "vals", (T, K), (torch.float32,), d)
         tau = float(temperature)
-        require(0.0 < tau < float("inf"), f"temperature: {tau}, wanted a positive number")
+        if not 0.0 < tau < float("inf"):
+            require(False, f"temperature: {tau}, wanted a positive number")
         return T, tau
 
-    def _row_values(self, T, **named):
-        for name, t in named.items():
+    def _row_values(self, T, name, t):
+        if not fits(t, (T,), torch.float32, self.device):
             tensor(t, name, (T,), (torch.float32,), self.device)
 
     def _gradient(self, z, out):
         if out is None:
             return torch.empty(z.shape, dtype=z.dtype, device=self.device)
-        return tensor(out, "out", z.shape, (z.dtype,), self.device, rows_apart=True)
+        if not rows_fit(out, z.shape, z.dtype, self.device):
+            tensor(out, "out", z.shape, (z.dtype,), self.device, rows_apart=True)
+        return out
 
     def forward(self, z, ids, vals, temperature=1.0, stream=None):
         """(loss, lse), f32 [T] each."""
         T, tau = self._begin(z, ids, vals, temperature)
-        loss = torch.empty(T, dtype=torch.float32, device=self.device)
-        lse = torch.empty(T, dtype=torch.float32, device=self.device)
+        loss, lse = torch.empty((2, T), dtype=torch.float32, device=self.device).unbind(0)
         _lib.mok_distill_forward(z, ids, vals, tau, loss, lse, self.ws, stream)
         return loss, lse
 
     def backward(self, z, ids, vals, lse, dloss, temperature=1.0, out=None, stream=None):
         """dz of z's type, from the forward's ``lse``; ``out`` may be z itself."""
         T, tau = self._begin(z, ids, vals, temperature)
-        self._row_values(T, lse=lse, dloss=dloss)
+        self._row_values(T, "lse", lse)
+        self._row_values(T, "dloss", dloss)
         dz = self._gradient(z, out)
         _lib.mok_distill_backward(z, ids, vals, tau, lse, dloss, dz, self.ws, stream)
         return dz
@@ -67,10 +76,9 @@ class DistillLoss:
     def forward_backward(self, z, ids, vals, dloss, temperature=1.0, out=None, stream=None):
         """(loss, dz) in one call; ``out`` may be z itself."""
         T, tau = self._begin(z, ids, vals, temperature)
-        self._row_values(T, dloss=dloss)
+        self._row_values(T, "dloss", dloss)
         dz = self._gradient(z, out)
-        loss = torch.empty(T, dtype=torch.float32, device=self.device)
-        lse = torch.empty(T, dtype=torch.float32, device=self.device)
+        loss, lse = torch.empty((2, T), dtype=torch.float32, device=self.device).unbind(0)
         _lib.mok_distill_step(z, ids, vals, tau, dloss, loss, lse, dz, self.ws, stream)
         return loss, dz
 

@@ -5,7 +5,7 @@ from __future__ import annotations
 import torch
 
 from . import _lib
-from ._check import on, require, tensor
+from ._check import fits, on, require, tensor
 
 _TYPES = (torch.bfloat16, torch.float32)
 
@@ -20,6 +20,7 @@ class MoKEmbedding:
 
     def __init__(self, vocab, hidden, tokens, pad_id=None, device="cuda"):
         self.vocab, self.hidden, self.tokens = vocab, hidden, tokens
+        self._table = (vocab, hidden)
         self.pad_id = _lib.MOK_EMBED_NO_PAD if pad_id is None else int(pad_id)
         self.device = on(device)
         n = _lib.mok_embed_workspace_size(vocab, hidden, tokens)
@@ -28,17 +29,23 @@ class MoKEmbedding:
         self.ws = torch.zeros(n, dtype=torch.uint8, device=self.device)
 
     def _ids(self, ids):
-        require(isinstance(ids, torch.Tensor) and ids.numel() <= self.tokens, f"ids: at most {self.tokens} are wanted")
-        tensor(ids, "ids", ids.shape, (torch.int32,), self.device)
+        if not (type(ids) is torch.Tensor and ids.numel() <= self.tokens and
+                fits(ids, ids.shape, torch.int32, self.device)):
+            require(isinstance(ids, torch.Tensor) and ids.numel() <= self.tokens,
+                    f"ids: at most {self.tokens} are wanted")
+            tensor(ids, "ids", ids.shape, (torch.int32,), self.device)
+        return (*ids.shape, self.hidden)
 
     def forward(self, table, ids, scale=1.0, out=None, stream=None):
         """[*ids.shape, hidden] of the table's type."""
-        self._ids(ids)
-        tensor(table, "table", (self.vocab, self.hidden), _TYPES, self.device)
-        shape = (*ids.shape, self.hidden)
+        d = self.device
+        shape = self._ids(ids)
+        if not (getattr(table, "dtype", None) in _TYPES and fits(table, self._table, table.dtype, d)):
+            tensor(table, "table", self._table, _TYPES, d)
         if out is None:
-            out = torch.empty(shape, dtype=table.dtype, device=self.device)
-        tensor(out, "out", shape, (table.dtype,), self.device)
+            out = torch.empty(shape, dtype=table.dtype, device=d)
+        elif not fits(out, shape, table.dtype, d):
+            tensor(out, "out", shape, (table.dtype,), d)
         _lib.mok_embed_forward(table, ids, self.pad_id, float(scale), out, self.ws, stream)
         return out
 
@@ -46,12 +53,15 @@ class MoKEmbedding:
         """The table's gradient [vocab, hidden] in ``out`` (bf16 or f32; f32 by
         default): written whole, or with ``accumulate`` added to the rows that
         ``ids`` names."""
-        self._ids(ids)
-        tensor(dx, "dx", (*ids.shape, self.hidden), _TYPES, self.device)
-        require(out is not None or not accumulate, "out: wanted to accumulate into")
+        d = self.device
+        shape = self._ids(ids)
+        if not (getattr(dx, "dtype", None) in _TYPES and fits(dx, shape, dx.dtype, d)):
+            tensor(dx, "dx", shape, _TYPES, d)
         if out is None:
-            out = torch.empty((self.vocab, self.hidden), dtype=torch.float32, device=self.device)
-        tensor(out, "out", (self.vocab, self.hidden), _TYPES, self.device)
+            require(not accumulate, "out: wanted to accumulate into")
+            out = torch.empty(self._table, dtype=torch.float32, device=d)
+        elif not (getattr(out, "dtype", None) in _TYPES and fits(out, self._table, out.dtype, d)):
+            tensor(out, "out", self._table, _TYPES, d)
         _lib.mok_embed_backward(dx, ids, self.pad_id, float(scale), out, accumulate, self.ws, stream)
         return out
 
