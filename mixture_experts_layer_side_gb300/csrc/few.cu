@@ -55,6 +55,7 @@ constexpr int kWordRouted = kHdrCounters + 1;    // tokens routed
 constexpr int kWordHidden = kHdrCounters + 2;    // [2] tiles of a finished, each half
 constexpr int kWordSummed = kHdrCounters + 4;    // CTAs whose sums of y are stored
 constexpr int kWordLeft = kHdrCounters + 5;      // CTAs that ended
+constexpr int kHalvesFrom = 32;  // blocks a CTA of the first GEMM
 constexpr int kMinRun = 6;  // blocks: a shorter run would not fill the stages
 
 // The routing sorted by expert, in shared memory.
@@ -172,22 +173,23 @@ __device__ __forceinline__ int atom_add_acq_rel(int32_t* p, int v) {
 __device__ __forceinline__ uint32_t* word(const FewParams& p, int i) { return reinterpret_cast<uint32_t*>(p.hdr + i); }
 
 // ---------------------------------------------------------------- router
-// This CTA's part of the logits: kLogitTokens tokens by h_rows rows of Wr.  A
-// lane takes 8 neighbouring experts, as many lanes as a row needs (32 at
-// most), the rest of the warp and the other warps other rows; the lanes' and
-// the warps' sums are added in a fixed order.
-__device__ void router_logits(const FewParams& p, uint8_t* smem, int nthreads) {
-  const int groups = (p.T + kLogitTokens - 1) / kLogitTokens;
+// This CTA's part of the logits: TOK tokens by h_rows rows of Wr.  A lane
+// takes 8 neighbouring experts, as many lanes as a row needs (32 at most), the
+// rest of the warp and the other warps other rows; the lanes' and the warps'
+// sums are added in a fixed order.
+template <int TOK>
+__device__ __forceinline__ void router_logits(const FewParams& p, uint8_t* smem, int nthreads) {
+  const int groups = (p.T + TOK - 1) / TOK;
   const int warps = nthreads / 32, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int part = blockIdx.x / groups, t0 = (blockIdx.x % groups) * kLogitTokens;
+  const int part = blockIdx.x / groups, t0 = (blockIdx.x % groups) * TOK;
   if (part >= p.h_parts) return;
-  const int nt = min(kLogitTokens, p.T - t0);
+  const int nt = min(TOK, p.T - t0);
   const int h0 = part * p.h_rows, rows = min(p.h_rows, p.H - h0);
-  float* xs = reinterpret_cast<float*>(smem);                 // [h_rows][kLogitTokens]
-  float* red = xs + (size_t)p.h_rows * kLogitTokens;          // [warps][kLogitTokens][256]
-  for (int i = threadIdx.x; i < rows * kLogitTokens; i += nthreads) {
+  float* xs = reinterpret_cast<float*>(smem);                 // [h_rows][TOK]
+  float* red = xs + (size_t)p.h_rows * TOK;                   // [warps][TOK][256]
+  for (int i = threadIdx.x; i < rows * TOK; i += nthreads) {
     const int t = i / rows, h = i - t * rows;
-    xs[h * kLogitTokens + t] = t < nt ? __bfloat162float(p.x[(long)(t0 + t) * p.H + h0 + h]) : 0.0f;
+    xs[h * TOK + t] = t < nt ? __bfloat162float(p.x[(long)(t0 + t) * p.H + h0 + h]) : 0.0f;
   }
   __syncthreads();
   int across = 1;  // lanes along a row
@@ -196,44 +198,58 @@ __device__ void router_logits(const FewParams& p, uint8_t* smem, int nthreads) {
   const bool vec = p.E % 8 == 0 && (reinterpret_cast<uintptr_t>(p.Wr) & 15) == 0;
   for (int e0 = 0; e0 < p.E; e0 += 256) {
     const int e = e0 + (lane & (across - 1)) * 8;
-    float acc[kLogitTokens][8];
+    float acc[TOK][8];
 #pragma unroll
-    for (int t = 0; t < kLogitTokens; ++t)
+    for (int t = 0; t < TOK; ++t)
 #pragma unroll
       for (int i = 0; i < 8; ++i) acc[t][i] = 0.0f;
-#pragma unroll 4
-    for (int h = warp * down + lane / across; h < rows; h += warps * down) {
-      const __nv_bfloat16* wr = p.Wr + (long)(h0 + h) * p.E + e;
-      float w[8];
-      if (vec) {
-        const uint4 v = e < p.E ? __ldg(reinterpret_cast<const uint4*>(wr)) : make_uint4(0, 0, 0, 0);
-        const uint32_t vv[4] = {v.x, v.y, v.z, v.w};
+    // eight rows a warp in flight
+    constexpr int kAhead = 8;
+    for (int hb = warp * down + lane / across; hb - lane / across < rows; hb += warps * down * kAhead) {
+      uint4 v[kAhead];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          w[2 * i] = __uint_as_float(vv[i] << 16);
-          w[2 * i + 1] = __uint_as_float(vv[i] & 0xffff0000u);
+      for (int i = 0; i < kAhead; ++i) {
+        const int h = hb + i * warps * down;
+        const __nv_bfloat16* wr = p.Wr + (long)(h0 + h) * p.E + e;
+        v[i] = make_uint4(0, 0, 0, 0);
+        if (h < rows && e < p.E) {
+          if (vec) {
+            v[i] = __ldg(reinterpret_cast<const uint4*>(wr));
+          } else {
+            uint32_t w[4];
+            for (int m = 0; m < 4; ++m) {
+              const uint32_t lo = e + 2 * m < p.E ? __bfloat16_as_ushort(wr[2 * m]) : 0;
+              const uint32_t hi = e + 2 * m + 1 < p.E ? __bfloat16_as_ushort(wr[2 * m + 1]) : 0;
+              w[m] = lo | hi << 16;
+            }
+            v[i] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
         }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = e + i < p.E ? __bfloat162float(wr[i]) : 0.0f;
       }
-      const float4* xv = reinterpret_cast<const float4*>(xs + h * kLogitTokens);
-      const float4 xa = xv[0], xb = xv[1];
-      const float xt[kLogitTokens] = {xa.x, xa.y, xa.z, xa.w, xb.x, xb.y, xb.z, xb.w};
 #pragma unroll
-      for (int t = 0; t < kLogitTokens; ++t)
+      for (int i = 0; i < kAhead; ++i) {
+        const int h = min(hb + i * warps * down, rows - 1);
+        const uint32_t vv[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
-        for (int i = 0; i < 8; ++i) acc[t][i] = fmaf(xt[t], w[i], acc[t][i]);
+        for (int t = 0; t < TOK; ++t) {
+          const float x = xs[h * TOK + t];
+#pragma unroll
+          for (int m = 0; m < 4; ++m) {
+            acc[t][2 * m] = fmaf(x, __uint_as_float(vv[m] << 16), acc[t][2 * m]);
+            acc[t][2 * m + 1] = fmaf(x, __uint_as_float(vv[m] & 0xffff0000u), acc[t][2 * m + 1]);
+          }
+        }
+      }
     }
     for (int o = across; o < 32; o <<= 1)
 #pragma unroll
-      for (int t = 0; t < kLogitTokens; ++t)
+      for (int t = 0; t < TOK; ++t)
 #pragma unroll
         for (int i = 0; i < 8; ++i) acc[t][i] += __shfl_xor_sync(0xffffffffu, acc[t][i], o);
     if (lane < across)
 #pragma unroll
-      for (int t = 0; t < kLogitTokens; ++t) {
-        float4* r = reinterpret_cast<float4*>(red + (warp * kLogitTokens + t) * 256 + lane * 8);
+      for (int t = 0; t < TOK; ++t) {
+        float4* r = reinterpret_cast<float4*>(red + (warp * TOK + t) * 256 + lane * 8);
         r[0] = make_float4(acc[t][0], acc[t][1], acc[t][2], acc[t][3]);
         r[1] = make_float4(acc[t][4], acc[t][5], acc[t][6], acc[t][7]);
       }
@@ -243,7 +259,7 @@ __device__ void router_logits(const FewParams& p, uint8_t* smem, int nthreads) {
       const int t = i >> 8, c = i & 255;
       if (c >= ne) continue;
       float s = 0.0f;
-      for (int w = 0; w < warps; ++w) s += red[(w * kLogitTokens + t) * 256 + c];
+      for (int w = 0; w < warps; ++w) s += red[(w * TOK + t) * 256 + c];
       p.logits[((long)part * p.T + t0 + t) * p.E + e0 + c] = s;
     }
     __syncthreads();
@@ -254,19 +270,42 @@ __device__ void router_logits(const FewParams& p, uint8_t* smem, int nthreads) {
 // threads take shares of the parts, so that the loads are in flight together.
 __device__ void router_select(const FewParams& p, int t, float* smem, int nthreads) {
   float* row = smem;                  // [E]
-  float* red = smem + p.E;            // [shares][E]
-  const int shares = max(1, min(8, nthreads / p.E));
+  float* bias = row + p.E;            // [E]
+  float* red = bias + p.E;            // [shares][E]
+  const int w = p.E % 4 == 0 ? 4 : 1; // experts a load brings
+  const int cols = (p.E + w - 1) / w;
+  const int shares = max(1, min(16, nthreads / cols));
   const int per = (p.h_parts + shares - 1) / shares;
-  const int width = nthreads / shares;
-  const int share = threadIdx.x / width;
+  const int share = threadIdx.x / cols, c0 = threadIdx.x - share * cols;
   if (share < shares)
-    for (int e = threadIdx.x - share * width; e < p.E; e += width) {
-      float s = 0.0f;
-      const int i1 = min(p.h_parts, (share + 1) * per);
-#pragma unroll 16
-      for (int i = share * per; i < i1; ++i) s += __ldcg(p.logits + ((long)i * p.T + t) * p.E + e);
-      red[share * p.E + e] = s;
+    for (int c = c0; c < cols; c += shares > 1 ? cols : nthreads) {
+      const int i0 = share * per, i1 = min(p.h_parts, i0 + per);
+      const float* from = p.logits + (long)t * p.E + c * w;
+      const long step = (long)p.T * p.E;
+      float* to = red + share * p.E + c * w;
+      if (w == 4) {
+        float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+        for (int i = i0; i < i1; ++i) {
+          const float4 v = __ldcg(reinterpret_cast<const float4*>(from + i * step));
+          s.x += v.x;
+          s.y += v.y;
+          s.z += v.z;
+          s.w += v.w;
+        }
+        to[0] = s.x;
+        to[1] = s.y;
+        to[2] = s.z;
+        to[3] = s.w;
+      } else {
+        float s = 0.0f;
+#pragma unroll 8
+        for (int i = i0; i < i1; ++i) s += __ldcg(from + i * step);
+        to[0] = s;
+      }
     }
+  if (p.bias)
+    for (int e = threadIdx.x; e < p.E; e += nthreads) bias[e] = p.bias[e];
   __syncthreads();
   for (int e = threadIdx.x; e < p.E; e += nthreads) {
     float s = red[e];
@@ -278,10 +317,11 @@ __device__ void router_select(const FewParams& p, int t, float* smem, int nthrea
     const int lane = threadIdx.x;
     int e;
     float s;
+    const float* b = p.bias ? bias : nullptr;
     if (p.E <= 256)
-      topk_softmax_warp<8>(row, p.bias, p.E, p.k, lane, e, s);
+      topk_softmax_warp<8>(row, b, p.E, p.k, lane, e, s);
     else
-      topk_softmax_warp<kMaxRouterExperts / 32>(row, p.bias, p.E, p.k, lane, e, s);
+      topk_softmax_warp<kMaxRouterExperts / 32>(row, b, p.E, p.k, lane, e, s);
     if (lane < p.k) {
       p.idx_out[(long)t * p.k + lane] = e;
       p.scores_out[(long)t * p.k + lane] = s;
@@ -407,78 +447,212 @@ __device__ void build_units(const FewParams& p, const Schedule& s, uint8_t* scra
 __device__ __forceinline__ float silu_mul(float h, float u) { return h / (1.0f + __expf(-h)) * u; }
 
 // a of 16 rows in column `col` (a lane's): bf16 and what its rounding left
-// (so that y is that of an f32 a), or codes and a scale per 32 columns.
+// (so that y is that of an f32 a), or codes and a scale per 32 columns.  Four
+// rows at a time, so that their latencies overlap.
 template <bool MX>
 __device__ __forceinline__ void store_hidden(const FewParams& p, int row, int n, int col, int lane, const float* h,
                                              const float* u) {
-  if constexpr (MX) {
-    uint8_t* q = static_cast<uint8_t*>(p.a);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      if (i >= n) break;
-      const float a = silu_mul(h[i], u[i]);
-      const float amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(a))));
-      const int X = mx_block_exponent(amax);
-      q[(long)(row + i) * p.I + col] = (uint8_t)mx_cvt_e4m3x2(a * mx_exp2_int(-X), 0.0f);
-      if (lane == 0) p.asf[(long)(row + i) * (p.I / 32) + col / 32] = (uint8_t)(X + 127);
-    }
-  } else {
-    __nv_bfloat16* hi = static_cast<__nv_bfloat16*>(p.a);
-    __nv_bfloat16* lo = hi + (long)p.T * p.k * p.I;
+  for (int i0 = 0; i0 < 16; i0 += 4) {
+    if (i0 >= n) break;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      if (i >= n) break;
+    for (int i = i0; i < i0 + 4; ++i) {
       const float a = silu_mul(h[i], u[i]);
-      const __nv_bfloat16 b = __float2bfloat16(a);
-      const float back = __bfloat162float(b);
-      hi[(long)(row + i) * p.I + col] = b;
-      lo[(long)(row + i) * p.I + col] = __float2bfloat16(isinf(back) ? 0.0f : a - back);
+      if constexpr (MX) {
+        const float amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(a))));
+        const int X = mx_block_exponent(amax);
+        const uint8_t code = (uint8_t)mx_cvt_e4m3x2(a * mx_exp2_int(-X), 0.0f);
+        if (i < n) {
+          static_cast<uint8_t*>(p.a)[(long)(row + i) * p.I + col] = code;
+          if (lane == 0) p.asf[(long)(row + i) * (p.I / 32) + col / 32] = (uint8_t)(X + 127);
+        }
+      } else {
+        __nv_bfloat16* hi = static_cast<__nv_bfloat16*>(p.a);
+        __nv_bfloat16* lo = hi + (long)p.T * p.k * p.I;
+        const __nv_bfloat16 b = __float2bfloat16(a);
+        const float back = __bfloat162float(b);
+        if (i < n) {
+          hi[(long)(row + i) * p.I + col] = b;
+          lo[(long)(row + i) * p.I + col] = __float2bfloat16(isinf(back) ? 0.0f : a - back);
+        }
+      }
     }
   }
 }
 
-// The combine: 4 columns of a token a thread, y from its buffer or, where its
-// tile was split along K, as the sum of the parts.
-__device__ void combine(const FewParams& p, const Schedule& s, const Cut* cuts, int nthreads) {
-  const int vecs = p.H / 4;
+// The parts of a tile of a that is split along K, added in the order of K (the
+// tile ends the first run, and begins the others), and a of the sums.  A warp
+// takes every fourth row, a lane four columns; two rows and four parts are in
+// flight together.
+template <bool MX>
+__device__ void join_hidden(const FewParams& p, const Cut& cut, const Seg& s, int rank, int half, int first, int last,
+                            int r0, int n, int warp, int lane) {
   const int slot_floats = 2 * p.unit_rows * 128;
-  for (long i = (long)blockIdx.x * nthreads + threadIdx.x; i < (long)p.T * vecs; i += (long)gridDim.x * nthreads) {
-    const int t = (int)(i / vecs), col = (int)(i - (long)t * vecs) * 4;
-    const int n = col >> 8, in_tile = (((col >> 7) & 1) * p.unit_rows) * 128 + (col & 127);
-    float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 4
-    for (int j = 0; j < p.k; ++j) {
-      const int f = t * p.k + j;
-      const int unit = s.unit_of[f];
-      if (unit == kNoUnit) continue;
-      const int half = unit >= cuts[1].unit0;
-      const Cut& c = cuts[half];
-      const int sup = (unit - c.unit0) * c.supers + n / c.group;
-      int first, last;
-      seg_runs(c, sup, first, last);
-      float4 y;
-      if (first == last) {
-        y = __ldcg(reinterpret_cast<const float4*>(p.y + (long)f * p.H + col));
+  const int col = s.n * 128 + lane * 4;
+  const float* base = p.part + lane * 4;
+#pragma unroll 1
+  for (int row = warp; row < n; row += 8) {
+    float4 h[2], u[2];
+#pragma unroll
+    for (int m = 0; m < 2; ++m) h[m] = u[m] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 1
+    for (int o0 = first; o0 <= last; o0 += 4) {
+      float4 vh[2][4], vu[2][4];
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int o = 0; o < 4; ++o) {
+          vh[m][o] = vu[m][o] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          if (row + 4 * m < n && o0 + o <= last) {
+            const int slot = 4 * ((o0 + o) * cut.group + rank) + 2 * half + (o0 + o == first ? 1 : 0);
+            const float* from = base + (long)slot * slot_floats + (row + 4 * m) * 128;
+            vh[m][o] = __ldcg(reinterpret_cast<const float4*>(from));
+            vu[m][o] = __ldcg(reinterpret_cast<const float4*>(from + p.unit_rows * 128));
+          }
+        }
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int o = 0; o < 4; ++o) {
+          h[m].x += vh[m][o].x, h[m].y += vh[m][o].y, h[m].z += vh[m][o].z, h[m].w += vh[m][o].w;
+          u[m].x += vu[m][o].x, u[m].y += vu[m][o].y, u[m].z += vu[m][o].z, u[m].w += vu[m][o].w;
+        }
+    }
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      const long r = r0 + row + 4 * m;
+      const bool in = row + 4 * m < n;
+      const float a[4] = {silu_mul(h[m].x, u[m].x), silu_mul(h[m].y, u[m].y), silu_mul(h[m].z, u[m].z),
+                          silu_mul(h[m].w, u[m].w)};
+      if constexpr (MX) {
+        // eight lanes hold a block
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top = max(top, __float_as_uint(fabsf(a[i])));
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const int X = mx_block_exponent(__uint_as_float(top));
+        const float inv = mx_exp2_int(-X);
+        const uint32_t codes = mx_cvt_e4m3x2(a[0] * inv, a[1] * inv) | (uint32_t)mx_cvt_e4m3x2(a[2] * inv, a[3] * inv) << 16;
+        if (in) {
+          *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.a) + r * p.I + col) = codes;
+          if ((lane & 7) == 0) p.asf[r * (p.I / 32) + col / 32] = (uint8_t)(X + 127);
+        }
       } else {
-        const int rank = n % c.group, at = in_tile + s.row_of[f] * 128;
-        y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        for (int o = first; o <= last; ++o) {
-          const long slot = (long)(o * c.group + rank) * 4 + half * 2 + (o == first ? 1 : 0);
-          const float4 v = __ldcg(reinterpret_cast<const float4*>(p.part + slot * slot_floats + at));
-          y.x += v.x;
-          y.y += v.y;
-          y.z += v.z;
-          y.w += v.w;
+        __nv_bfloat16* hi = static_cast<__nv_bfloat16*>(p.a) + r * p.I + col;
+        __nv_bfloat16* lo = hi + (long)p.T * p.k * p.I;
+        float back[4], left[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          back[i] = bf16_round(a[i]);
+          left[i] = isinf(back[i]) ? 0.0f : a[i] - back[i];
+        }
+        if (in) {
+          *reinterpret_cast<uint2*>(hi) = make_uint2(pack_bf16x2(back[0], back[1]), pack_bf16x2(back[2], back[3]));
+          *reinterpret_cast<uint2*>(lo) = make_uint2(pack_bf16x2(left[0], left[1]), pack_bf16x2(left[2], left[3]));
         }
       }
-      const float w = p.scores[f];
-      acc[0] = fmaf(w, y.x, acc[0]);
-      acc[1] = fmaf(w, y.y, acc[1]);
-      acc[2] = fmaf(w, y.z, acc[2]);
-      acc[3] = fmaf(w, y.w, acc[3]);
     }
-    *reinterpret_cast<uint2*>(p.out + (long)t * p.H + col) =
-        make_uint2(pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3]));
+  }
+}
+
+// The combine: 4 columns of a token to LANES threads, each of which brings y
+// of every LANES-th expert -- from y's buffer or, where its tile was split
+// along K, as the sum of the parts -- and all of which add them up in the
+// order of j.  The loads of an item, and of ITEMS of them, are in flight
+// together.
+template <int LANES, int ITEMS>
+__device__ __forceinline__ void combine(const FewParams& p, const Schedule& s, const Cut* cuts, int nthreads) {
+  const int vecs = p.H / 4;
+  const int slot_floats = 2 * p.unit_rows * 128;
+  const int sub = threadIdx.x & (LANES - 1);
+  const int items = p.T * vecs, stride = gridDim.x * nthreads / LANES;
+  const int ahead = (threadIdx.x & 31) / LANES;  // items of the warp before this one: its lanes stay together
+  for (int i0 = (blockIdx.x * nthreads + threadIdx.x) / LANES; i0 - ahead < items; i0 += stride * ITEMS) {
+    float4 acc[ITEMS];
+#pragma unroll
+    for (int m = 0; m < ITEMS; ++m) acc[m] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int j0 = 0; j0 < p.k; j0 += LANES) {
+      const int j = j0 + sub;
+      const float4 *from[ITEMS], *next[ITEMS];
+      int more[ITEMS];  // parts past the first
+      float w[ITEMS];
+#pragma unroll
+      for (int m = 0; m < ITEMS; ++m) {
+        const int i = i0 + m * stride;
+        from[m] = nullptr;
+        more[m] = 0;
+        w[m] = 0.0f;
+        if (i >= items || j >= p.k) continue;
+        const int t = i / vecs, col = (i - t * vecs) * 4, f = t * p.k + j;
+        const int unit = s.unit_of[f];
+        if (unit == kNoUnit) continue;
+        w[m] = p.scores[f];
+        const int n = col >> 8, half = unit >= cuts[1].unit0;
+        const Cut& c = cuts[half];
+        const int in_unit = n / c.group, rank = n - in_unit * c.group;
+        int first, last;
+        seg_runs(c, (unit - c.unit0) * c.supers + in_unit, first, last);
+        if (first == last) {
+          from[m] = reinterpret_cast<const float4*>(p.y + (long)f * p.H + col);
+        } else {
+          const float* at = p.part + ((((col >> 7) & 1) * p.unit_rows) + s.row_of[f]) * 128 + (col & 127);
+          from[m] = reinterpret_cast<const float4*>(at + (long)((first * c.group + rank) * 4 + half * 2 + 1) * slot_floats);
+          next[m] = reinterpret_cast<const float4*>(at + (long)(((first + 1) * c.group + rank) * 4 + half * 2) * slot_floats);
+          more[m] = last - first;
+        }
+      }
+      float4 y[ITEMS], z[ITEMS];
+#pragma unroll
+      for (int m = 0; m < ITEMS; ++m) {
+        y[m] = from[m] ? __ldcg(from[m]) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        z[m] = more[m] ? __ldcg(next[m]) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      }
+#pragma unroll
+      for (int m = 0; m < ITEMS; ++m) {
+        const int group = cuts[0].group;
+        y[m].x += z[m].x;
+        y[m].y += z[m].y;
+        y[m].z += z[m].z;
+        y[m].w += z[m].w;
+#pragma unroll 1
+        for (int o = 1; o < more[m]; ++o) {
+          const float4 v = __ldcg(next[m] + (long)o * group * 4 * (slot_floats / 4));
+          y[m].x += v.x;
+          y[m].y += v.y;
+          y[m].z += v.z;
+          y[m].w += v.w;
+        }
+        const bool on = from[m] != nullptr;
+#pragma unroll
+        for (int l = 0; l < LANES; ++l) {
+          const float wl = LANES > 1 ? __shfl_sync(0xffffffffu, w[m], l, LANES) : w[m];
+          const bool ol = LANES > 1 ? __shfl_sync(0xffffffffu, (int)on, l, LANES) != 0 : on;
+          float4 v = y[m];
+          if (LANES > 1) {
+            v.x = __shfl_sync(0xffffffffu, y[m].x, l, LANES);
+            v.y = __shfl_sync(0xffffffffu, y[m].y, l, LANES);
+            v.z = __shfl_sync(0xffffffffu, y[m].z, l, LANES);
+            v.w = __shfl_sync(0xffffffffu, y[m].w, l, LANES);
+          }
+          if (ol) {
+            acc[m].x = fmaf(wl, v.x, acc[m].x);
+            acc[m].y = fmaf(wl, v.y, acc[m].y);
+            acc[m].z = fmaf(wl, v.z, acc[m].z);
+            acc[m].w = fmaf(wl, v.w, acc[m].w);
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int m = 0; m < ITEMS; ++m) {
+      const int i = i0 + m * stride;
+      if (sub == 0 && i < items) {
+        const int t = i / vecs, col = (i - t * vecs) * 4;
+        *reinterpret_cast<uint2*>(p.out + (long)t * p.H + col) =
+            make_uint2(pack_bf16x2(acc[m].x, acc[m].y), pack_bf16x2(acc[m].z, acc[m].w));
+      }
+    }
   }
 }
 
@@ -506,6 +680,15 @@ __global__ void __launch_bounds__(MX ? 320 : 256, 1) few_kernel(const __grid_con
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   WaitCtx wc{&ctl->abort, p.hdr + kHdrAbort, p.hdr + kHdrError};
 
+  // what the routing and the first tiles need soon, on its way from memory meanwhile
+  {
+    const char* a = reinterpret_cast<const char*>(p.x);
+    const long bytes = (long)p.T * p.H * 2, at = ((long)blockIdx.x * kThreads + threadIdx.x) * 128;
+    if (at < bytes) asm volatile("prefetch.global.L2 [%0];" ::"l"(a + at));
+    if (!p.Wr && threadIdx.x < R && warp == 0) asm volatile("prefetch.global.L2 [%0];" ::"l"(p.idx + threadIdx.x));
+    if (blockIdx.x == 0 && p.bias && threadIdx.x * 32 < p.E)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(p.bias + threadIdx.x * 32));
+  }
   if (threadIdx.x == 0) {
     for (int i = 0; i < p.stages; ++i) {
       mbar_init(&ctl->full_a[i], 1);
@@ -531,7 +714,12 @@ __global__ void __launch_bounds__(MX ? 320 : 256, 1) few_kernel(const __grid_con
 
   // ---- routing and the quantised x
   if (MX) quantize_x(p, kThreads);
-  if (p.Wr) router_logits(p, smem, kThreads);
+  if (p.Wr) {
+    if (p.logit_tokens == 1)
+      router_logits<1>(p, smem, kThreads);
+    else
+      router_logits<kLogitTokens>(p, smem, kThreads);
+  }
   bool ok = true;
   if (MX || p.Wr) {
     __syncthreads();
@@ -555,7 +743,12 @@ __global__ void __launch_bounds__(MX ? 320 : 256, 1) few_kernel(const __grid_con
   fence_proxy_async_shared();
   const int c = blockIdx.x;
   if (ok && threadIdx.x < 4) {
-    const int i = threadIdx.x, units = ctl->units, half = (units + 1) / 2;
+    // halves only where a half is long beside the joining it hides: at 10
+    // blocks a CTA the two extra joins cost more than they hid (1 token, H
+    // 2048, I 768: 49 us in halves)
+    const int i = threadIdx.x, units = ctl->units;
+    const long blocks = (long)units * (p.I / 128) * (p.H / kEl);
+    const int half = blocks >= (long)kHalvesFrom * gridDim.x ? (units + 1) / 2 : units;
     const int u0 = i & 1 ? half : 0, nu = i & 1 ? units - half : half;
     ctl->cuts[i] = i < 2 ? make_cut(p.I / 128, p.H / kEl, u0, nu, gridDim.x)
                          : make_cut((p.H + 255) / 256, p.I / kEl, u0, nu, gridDim.x);
@@ -797,10 +990,11 @@ __global__ void __launch_bounds__(MX ? 320 : 256, 1) few_kernel(const __grid_con
             float* y = p.y + s.n * 256 + lane_col;
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-              if (i >= rows) break;
-              float* yr = y + (long)sched.perm[r0 + i0 + i] * p.H;
-              __stcg(yr, v0[i]);
-              if (second) __stcg(yr + 128, v1[i]);
+              if (i < rows) {
+                float* yr = y + (long)sched.perm[r0 + i0 + i] * p.H;
+                __stcg(yr, v0[i]);
+                if (second) __stcg(yr + 128, v1[i]);
+              }
             }
           }
         };
@@ -829,9 +1023,10 @@ __global__ void __launch_bounds__(MX ? 320 : 256, 1) few_kernel(const __grid_con
           } else {
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-              if (i0 + i >= n) break;
-              __stcg(slot + (i0 + i) * 128, v0[i]);
-              if (second) __stcg(slot + (p.unit_rows + i0 + i) * 128, v1[i]);
+              if (i0 + i < n) {
+                __stcg(slot + (i0 + i) * 128, v0[i]);
+                if (second) __stcg(slot + (p.unit_rows + i0 + i) * 128, v1[i]);
+              }
             }
           }
         }
@@ -852,24 +1047,7 @@ __global__ void __launch_bounds__(MX ? 320 : 256, 1) few_kernel(const __grid_con
           __syncwarp();
           named_bar_sync(1, kEpilogue);
           if (!ctl->last) continue;
-          // the last to arrive: the parts in the order of K (the tile ends
-          // the first run, and begins the others)
-          for (int i0 = 0; i0 < n; i0 += 16) {
-            float v0[16], v1[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) v0[i] = v1[i] = 0.0f;
-            for (int o = first; o <= last; ++o) {
-              const float* from =
-                  p.part + (long)(4 * (o * cut.group + rank) + 2 * half + (o == first ? 1 : 0)) * slot_floats + lane_col;
-#pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                if (i0 + i >= n) break;
-                v0[i] += __ldcg(from + (i0 + i) * 128);
-                v1[i] += __ldcg(from + (p.unit_rows + i0 + i) * 128);
-              }
-            }
-            finish(i0, v0, v1);
-          }
+          join_hidden<MX>(p, cut, s, rank, half, first, last, r0, n, warp - 4, lane);
         }
         // a finished tile of a
         named_bar_sync(1, kEpilogue);
@@ -920,10 +1098,16 @@ __global__ void __launch_bounds__(MX ? 320 : 256, 1) few_kernel(const __grid_con
   asm volatile("barrier.sync 0;" ::: "memory");
   tc_fence_after();
   if (warp == 0) tmem_dealloc(tmem, 512);
-  if (units > 0 && (long)c * kThreads < (long)p.T * (p.H / 4)) {
+  const bool one = (long)p.T * (p.H / 4) * 8 <= (long)gridDim.x * kThreads;
+  if (units > 0 && (long)c * kThreads < (long)p.T * (p.H / 4) * 8) {
     if (threadIdx.x == 0) ctl->go = wait_flag_geq(word(p, kWordSummed), gridDim.x, wc) ? 1 : 0;
     __syncthreads();
-    if (ctl->go) combine(p, sched, ctl->cuts + 2, kThreads);
+    if (ctl->go) {
+      if (one)
+        combine<8, 1>(p, sched, ctl->cuts + 2, kThreads);
+      else
+        combine<8, 4>(p, sched, ctl->cuts + 2, kThreads);
+    }
   }
   if (threadIdx.x == 0) {
     // the last CTA to end leaves the counters as it found them
@@ -944,11 +1128,11 @@ int units_bound(int T, int E, int k, int unit_rows) {
   return n < R ? n : R;
 }
 
-// At most 64 parts of the logits: enough SMs to read Wr at once, and few
-// enough parts to add up quickly.
-void logit_parts(int T, int H, int ctas, int* parts, int* rows) {
-  const int groups = (T + kLogitTokens - 1) / kLogitTokens;
-  int n = ctas / groups;
+// Tokens side by side in a part of the logits, and the parts: at most 64,
+// enough SMs to read Wr at once and few enough parts to add up quickly.
+void logit_parts(int T, int H, int ctas, int* tokens, int* parts, int* rows) {
+  *tokens = T == 1 ? 1 : kLogitTokens;
+  int n = ctas / ((T + *tokens - 1) / *tokens);
   if (n > 64) n = 64;
   if (n < 1) n = 1;
   int r = (H + n - 1) / n;
@@ -974,8 +1158,8 @@ FewLayout few_layout(const mok_shape& s, mok_precision prec) {
   // room for the units of any call of this H, I, E and k
   const size_t units = units_bound(MOK_FEW_MAX_TOKENS, s.E, s.k, 16);
   L.tiles = take(units * (s.I / 128) * 4);
-  int parts, rows;
-  logit_parts(s.T, s.H, ctas, &parts, &rows);
+  int tokens, parts, rows;
+  logit_parts(s.T, s.H, ctas, &tokens, &parts, &rows);
   L.logits = take((size_t)parts * s.T * s.E * 4);
   L.xq = mx ? take((size_t)s.T * s.H) : 0;
   L.xsf = mx ? take((size_t)s.T * (s.H / 32)) : 0;
@@ -1010,7 +1194,7 @@ cudaError_t launch_few(FewParams p, bool mx, int* launches, cudaStream_t st) {
     return cudaErrorInvalidValue;
   p.unit_rows = few_unit_rows(p.T);
   p.max_units = units_bound(p.T, p.E, p.k, p.unit_rows);
-  logit_parts(p.T, p.H, ctas, &p.h_parts, &p.h_rows);
+  logit_parts(p.T, p.H, ctas, &p.logit_tokens, &p.h_parts, &p.h_rows);
   const size_t stage = 2 * kATile + (size_t)p.unit_rows * (mx ? 128 : 256) + (mx ? kSfBytes : 0);
   const size_t rest = 1024 + sizeof(Ctl) + schedule_bytes(p.E, p.T * p.k, p.max_units);
   constexpr size_t kMost = 227 * 1024;

@@ -49,7 +49,7 @@ struct FewParams {
   // router (Wr null: the routing is given)
   const __nv_bfloat16* Wr;
   const float* bias;
-  int h_parts, h_rows;  // logits: rows of Wr per part
+  int logit_tokens, h_parts, h_rows;  // logits: tokens side by side, parts along H, rows of Wr per part
   float* logits;
   int32_t* idx_out;
   float* scores_out;

@@ -10,9 +10,10 @@ namespace mok {
 
 constexpr int kMaxRouterExperts = 1024;  // keys held in registers: 32 per lane
 
-// (key, expert) pairs ordered by descending key, then ascending expert.
-__device__ __forceinline__ bool ranks_before(float ka, int ea, float kb, int eb) {
-  return ka > kb || (ka == kb && ea < eb);
+// Keys as integers in the same order; -0 and +0 are one key, 0 is below every key.
+__device__ __forceinline__ uint32_t order_key(float v) {
+  const uint32_t b = __float_as_uint(v + 0.0f);
+  return b ^ ((b >> 31) ? 0xffffffffu : 0x80000000u);
 }
 
 // The k largest row[e] + bias[e] (ties to the lower expert, descending key
@@ -22,42 +23,35 @@ __device__ __forceinline__ bool ranks_before(float ka, int ea, float kb, int eb)
 template <int PER>
 __device__ __forceinline__ void topk_softmax_warp(const float* row, const float* bias, int E, int k, int lane,
                                                   int& my_e, float& my_s) {
-  float key[PER];
-  const int per_lane = (E + 31) >> 5;
+  uint32_t key[PER];
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     const int e = lane + 32 * i;
-    const float v = (i < per_lane && e < E) ? row[e] + (bias ? bias[e] : 0.0f) : 0.0f;
-    key[i] = isnan(v) ? -INFINITY : v;
+    key[i] = 0;  // no expert, or one already chosen
+    if (e < E) {
+      const float v = row[e] + (bias ? bias[e] : 0.0f);
+      key[i] = order_key(isnan(v) ? -INFINITY : v);
+    }
   }
-  uint32_t taken = 0;  // bit i: expert lane + 32 i already chosen
   my_e = -1;
   float my_l = 0.0f;
   for (int j = 0; j < k; ++j) {
-    float bk = 0.0f;
-    int be = INT_MAX;
+    uint32_t best = 0;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int e = lane + 32 * i;
-      if (i < per_lane && e < E && !((taken >> i) & 1u) && (be == INT_MAX || ranks_before(key[i], e, bk, be))) {
-        bk = key[i];
-        be = e;
-      }
-    }
+    for (int i = 0; i < PER; ++i) best = max(best, key[i]);
+    best = __reduce_max_sync(0xffffffffu, best);
+    if (best == 0) break;  // fewer than k experts (the host rules it out)
+    int e = INT_MAX;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const float ok = __shfl_xor_sync(0xffffffffu, bk, o);
-      const int oe = __shfl_xor_sync(0xffffffffu, be, o);
-      if (oe != INT_MAX && (be == INT_MAX || ranks_before(ok, oe, bk, be))) {
-        bk = ok;
-        be = oe;
-      }
-    }
-    if (be == INT_MAX) break;  // fewer than k experts (the host rules it out)
-    if ((be & 31) == lane) taken |= 1u << (be >> 5);
+    for (int i = PER - 1; i >= 0; --i)
+      if (key[i] == best) e = lane + 32 * i;
+    e = (int)__reduce_min_sync(0xffffffffu, (unsigned)e);
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      if (lane + 32 * i == e) key[i] = 0;
     if (lane == j) {
-      my_e = be;
-      my_l = row[be];
+      my_e = e;
+      my_l = row[e];
     }
   }
   float m = lane < k ? my_l : -INFINITY;
