@@ -557,9 +557,9 @@ mok_status mok_ep_unsort_scores(const mok_shape* shape, const mok_config* cfg, c
 
 /*
  * The layer for a few tokens: what mok_forward computes, for serving steps of
- * 1 <= T <= MOK_FEW_MAX_TOKENS tokens and H <= MOK_FEW_MAX_HIDDEN, without a schedule, a padded copy of
- * the rows or a forward context -- nothing is kept for a backward.  A pass
- * reads the weights of the experts that the tokens chose and no others.
+ * 1 <= T <= MOK_FEW_MAX_TOKENS tokens (H and I <= MOK_FEW_MAX_HIDDEN), without
+ * a schedule, a padded copy of the rows or a forward context -- nothing is kept
+ * for a backward.  A pass reads the weights of the experts that the tokens chose and no others.
  *
  *   mok_few_forward  routing given: topk_idx (device int32 [T, k]) and scores
  *                    (device f32 [T, k])
@@ -571,9 +571,10 @@ mok_status mok_ep_unsort_scores(const mok_shape* shape, const mok_config* cfg, c
  *   W1, W3, W2   as for mok_forward in the given precision
  * h, u and y are f32 sums.  BF16: a = silu(h) * u enters the second GEMM as two
  * bf16 (its rounding and what that left).  MXFP8: x along H and a along I are
- * quantised per 32, by the rule of mok_mxfp8_quantize.  out is summed in f32 over j in increasing order and rounded once.  The
- * order of the sums over H and I depends on the whole call's routing, so a
- * token's last bits may depend on the tokens beside it; a call repeated with
+ * quantised per 32, by the rule of mok_mxfp8_quantize.  out is summed in f32
+ * over j in increasing order and rounded once.  The order of the sums over H
+ * and I depends on the whole call's routing, so a token's last bits may depend
+ * on the tokens beside it; a call repeated with
  * the same inputs gives the same bits.
  *
  * An id outside [0, E) records MOK_ERR_BAD_INDEX and adds nothing to its

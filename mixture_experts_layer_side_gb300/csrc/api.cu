@@ -1524,7 +1524,9 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 
 mok_status check_few(const mok_shape* s, mok_precision prec) {
   MOK_TRY(check_shape(s));
   MOK_TRY(check_prec(prec));
-  return s->T > MOK_FEW_MAX_TOKENS || s->H > MOK_FEW_MAX_HIDDEN ? MOK_ERR_UNSUPPORTED : MOK_OK;
+  return s->T > MOK_FEW_MAX_TOKENS || s->H > MOK_FEW_MAX_HIDDEN || s->I > MOK_FEW_MAX_HIDDEN
+             ? MOK_ERR_UNSUPPORTED
+             : MOK_OK;
 }
 
 mok_status few_params(const mok_shape& s, mok_precision prec, void* ws, size_t ws_bytes, const void* x, const void* W1,

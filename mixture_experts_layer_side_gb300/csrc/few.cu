@@ -55,6 +55,7 @@ constexpr int kWordRouted = kHdrCounters + 1;    // tokens routed
 constexpr int kWordHidden = kHdrCounters + 2;    // [2] tiles of a finished, each half
 constexpr int kWordSummed = kHdrCounters + 4;    // CTAs whose sums of y are stored
 constexpr int kWordLeft = kHdrCounters + 5;      // CTAs that ended
+constexpr int kTouchRows = 16;   // routed rows whose experts' pages are touched ahead
 constexpr int kHalvesFrom = 32;  // blocks a CTA of the first GEMM
 constexpr int kMinRun = 6;  // blocks: a shorter run would not fill the stages
 
@@ -63,6 +64,7 @@ struct Schedule {
   uint16_t* offset;   // [E] first sorted row of each expert
   uint16_t* unit0;    // [E] its first unit
   uint16_t* perm;     // [T*k] sorted row -> flat index
+  uint16_t* token;    // [T*k] sorted row -> token
   uint16_t* unit_of;  // [T*k] flat index -> unit (kNoUnit: an id out of range)
   uint16_t* unit_e;   // [max_units] expert, first sorted row and rows of each unit
   uint16_t* unit_r;
@@ -72,23 +74,27 @@ struct Schedule {
 constexpr int kNoUnit = 0xFFFF;
 
 __host__ __device__ constexpr size_t schedule_bytes(int E, int R, int units) {
-  return (size_t)E * 4 + (size_t)R * 5 + (size_t)units * 5 + 16;
+  return (size_t)E * 4 + (size_t)R * 7 + (size_t)units * 5 + 16;
 }
 
-// One GEMM of one half of the units, its blocks cut into runs.
+// One GEMM of one half of the units, its blocks cut into runs whose lengths
+// differ by one at most.
 struct Cut {
   int group;          // CTAs side by side on neighbouring column tiles
   int supers;         // groups of column tiles in a unit
   int kb;             // blocks along K
   int unit0, units;
-  long blocks;        // of one CTA of a group
-  int runs;
+  int blocks;         // of one CTA of a group
+  int runs, each, rest;  // blocks = runs * each + rest
   __device__ bool takes(int c) const { return c < runs * group; }
-  __device__ long begin(int run) const { return blocks * run / runs; }
+  __device__ int begin(int run) const { return each * run + rest * run / runs; }
   // the run that holds block b
-  __device__ int owner(long b) const {
-    if (blocks * runs < (1ll << 31)) return (int)(((unsigned)(b + 1) * (unsigned)runs - 1u) / (unsigned)blocks);
-    return (int)(((b + 1) * runs - 1) / blocks);
+  __device__ int owner(int b) const {
+    int o = (int)((float)b * (float)runs / (float)blocks);
+    o = min(o, runs - 1);
+    while (begin(o) > b) --o;
+    while (begin(o + 1) <= b) ++o;
+    return o;
   }
 };
 
@@ -100,11 +106,37 @@ __device__ __forceinline__ Cut make_cut(int tiles, int kb, int unit0, int units,
   c.kb = kb;
   c.unit0 = unit0;
   c.units = units;
-  c.blocks = (long)units * c.supers * kb;
-  const long most = (c.blocks + kMinRun - 1) / kMinRun;
-  const int groups = ctas / c.group;
-  c.runs = (int)(most < groups ? most : groups);
+  c.blocks = units * c.supers * kb;
+  c.runs = max(1, min((c.blocks + kMinRun - 1) / kMinRun, ctas / c.group));
+  if (units == 0) c.runs = 0;
+  c.each = units ? c.blocks / c.runs : 0;
+  c.rest = units ? c.blocks - c.each * c.runs : 0;
   return c;
+}
+
+// A run's share of one tile.
+struct Seg {
+  int unit, n;    // unit and column tile
+  int k0, k1;     // blocks
+  int super;      // index of the tile's group
+};
+
+__device__ __forceinline__ Seg seg_at(const Cut& c, int b, int end, int rank) {
+  Seg s;
+  s.super = b / c.kb;
+  s.k0 = b - s.super * c.kb;
+  s.k1 = min(c.kb, s.k0 + end - b);
+  const int u = s.super / c.supers;
+  s.unit = c.unit0 + u;
+  s.n = (s.super - u * c.supers) * c.group + rank;
+  return s;
+}
+
+// The runs that a tile is split over.
+__device__ __forceinline__ void seg_runs(const Cut& c, int super, int& first, int& last) {
+  const int b = super * c.kb;
+  first = c.owner(b);
+  last = c.owner(b + c.kb - 1);
 }
 
 struct Ctl {
@@ -117,31 +149,6 @@ struct Ctl {
   int warp_sum[16];
   Cut cuts[4];  // in order: a of each half of the units, y of each half
 };
-
-// A run's share of one tile.
-struct Seg {
-  int unit, n;    // unit and column tile
-  int k0, k1;     // blocks
-  int super;      // index of the tile's group
-};
-
-__device__ __forceinline__ Seg seg_at(const Cut& c, long b, long end, int rank) {
-  Seg s;
-  s.super = (int)(b / c.kb);
-  s.k0 = (int)(b - (long)s.super * c.kb);
-  s.k1 = (int)(end - b < c.kb - s.k0 ? s.k0 + (end - b) : c.kb);
-  const int u = s.super / c.supers;
-  s.unit = c.unit0 + u;
-  s.n = (s.super - u * c.supers) * c.group + rank;
-  return s;
-}
-
-// The runs that a tile is split over.
-__device__ __forceinline__ void seg_runs(const Cut& c, int super, int& first, int& last) {
-  const long b = (long)super * c.kb;
-  first = c.owner(b);
-  last = c.owner(b + c.kb - 1);
-}
 
 __device__ __forceinline__ bool vote_all(int bar, int threads, bool ok) {
   uint32_t r;
@@ -357,12 +364,26 @@ __device__ void quantize_x(const FewParams& p, int nthreads) {
 }
 
 // ---------------------------------------------------------------- schedule
+// One line of each of an expert's matrices, another place for each CTA: the
+// pages of the weights that are about to stream in are looked up while the
+// schedule is made.
+template <bool MX>
+__device__ __forceinline__ void touch_weights(const FewParams& p, int e) {
+  const long bytes = (long)p.H * p.I * (MX ? 1 : 2), at = e * bytes + bytes / gridDim.x * blockIdx.x;
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const uint8_t*>(p.W1) + at));
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const uint8_t*>(p.W3) + at));
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const uint8_t*>(p.W2) + at));
+}
+
 // Rows grouped by expert in ascending flat index, and cut into units: a
 // counting sort whose warps own contiguous ranges of the flat indices, so
 // that (warp, place) is their order.  `scratch`: the ids and a count per warp
 // and expert.
+template <bool MX>
 __device__ void build_units(const FewParams& p, const Schedule& s, uint8_t* scratch, Ctl* ctl, int nthreads) {
-  const int R = p.T * p.k, W = nthreads / 32, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int R = p.T * p.k, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int per = ((R + nthreads - 1) / nthreads) * 32;  // flat indices a warp
+  const int W = (R + per - 1) / per;                     // warps that have some
   const int shift = __ffs(p.unit_rows) - 1;
   uint16_t* ids = reinterpret_cast<uint16_t*>(scratch);
   uint32_t* hist = reinterpret_cast<uint32_t*>(scratch + (((size_t)R * 2 + 15) & ~15));  // [W][E]
@@ -372,11 +393,11 @@ __device__ void build_units(const FewParams& p, const Schedule& s, uint8_t* scra
     const int e = p.idx[f];
     const bool in = e >= 0 && e < p.E;
     bad |= !in;
+    if (in && f < kTouchRows) touch_weights<MX>(p, e);
     ids[f] = (uint16_t)(in ? e : kNoUnit);
   }
   if (bad && blockIdx.x == 0) atomicOr(p.hdr + kHdrError, MOK_ERRBIT_BAD_INDEX);
   __syncthreads();
-  const int per = ((R + 32 * W - 1) / (32 * W)) * 32;
   const int f0 = warp * per, f1 = min(R, f0 + per);
   uint32_t* mine = hist + warp * p.E;
   for (int f = f0 + lane; f - lane < f1; f += 32) {
@@ -433,6 +454,7 @@ __device__ void build_units(const FewParams& p, const Schedule& s, uint8_t* scra
     if (e != kNoUnit) {
       if (ahead == 0) mine[e] += __popc(same);
       s.perm[s.offset[e] + place] = (uint16_t)f;
+      s.token[s.offset[e] + place] = (uint16_t)(f / p.k);
       s.unit_of[f] = (uint16_t)(s.unit0[e] + (place >> shift));
       s.row_of[f] = (uint8_t)(place & (p.unit_rows - 1));
     } else if (f < f1) {
@@ -444,37 +466,49 @@ __device__ void build_units(const FewParams& p, const Schedule& s, uint8_t* scra
 }
 
 // ---------------------------------------------------------------- epilogue
+// Four columns of each of two accumulators, this lane's row.
+__device__ __forceinline__ void tmem_ld4x2(uint32_t a0, uint32_t a1, float (&v0)[4], float (&v1)[4]) {
+  uint32_t r[8];
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a0));
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(a1));
+  tmem_wait_ld();
+  asm volatile("" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v0[i] = __uint_as_float(r[i]);
+    v1[i] = __uint_as_float(r[4 + i]);
+  }
+}
+
 __device__ __forceinline__ float silu_mul(float h, float u) { return h / (1.0f + __expf(-h)) * u; }
 
-// a of 16 rows in column `col` (a lane's): bf16 and what its rounding left
-// (so that y is that of an f32 a), or codes and a scale per 32 columns.  Four
-// rows at a time, so that their latencies overlap.
+// a of 4 rows in column `col` (a lane's): bf16 and what its rounding left (so
+// that y is that of an f32 a), or codes and a scale per 32 columns.
 template <bool MX>
-__device__ __forceinline__ void store_hidden(const FewParams& p, int row, int n, int col, int lane, const float* h,
-                                             const float* u) {
+__device__ __forceinline__ void store_hidden(const FewParams& p, int row, int n, int col, int lane, const float (&h)[4],
+                                             const float (&u)[4]) {
 #pragma unroll
-  for (int i0 = 0; i0 < 16; i0 += 4) {
-    if (i0 >= n) break;
-#pragma unroll
-    for (int i = i0; i < i0 + 4; ++i) {
-      const float a = silu_mul(h[i], u[i]);
-      if constexpr (MX) {
-        const float amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(a))));
-        const int X = mx_block_exponent(amax);
-        const uint8_t code = (uint8_t)mx_cvt_e4m3x2(a * mx_exp2_int(-X), 0.0f);
-        if (i < n) {
-          static_cast<uint8_t*>(p.a)[(long)(row + i) * p.I + col] = code;
-          if (lane == 0) p.asf[(long)(row + i) * (p.I / 32) + col / 32] = (uint8_t)(X + 127);
-        }
-      } else {
-        __nv_bfloat16* hi = static_cast<__nv_bfloat16*>(p.a);
-        __nv_bfloat16* lo = hi + (long)p.T * p.k * p.I;
-        const __nv_bfloat16 b = __float2bfloat16(a);
-        const float back = __bfloat162float(b);
-        if (i < n) {
-          hi[(long)(row + i) * p.I + col] = b;
-          lo[(long)(row + i) * p.I + col] = __float2bfloat16(isinf(back) ? 0.0f : a - back);
-        }
+  for (int i = 0; i < 4; ++i) {
+    const float a = silu_mul(h[i], u[i]);
+    const long at = (long)(row + i) * p.I + col;
+    if constexpr (MX) {
+      const float amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(a))));
+      const int X = mx_block_exponent(amax);
+      const uint8_t code = (uint8_t)mx_cvt_e4m3x2(a * mx_exp2_int(-X), 0.0f);
+      if (i < n) {
+        static_cast<uint8_t*>(p.a)[at] = code;
+        if (lane == 0) p.asf[at / 32] = (uint8_t)(X + 127);
+      }
+    } else {
+      __nv_bfloat16* hi = static_cast<__nv_bfloat16*>(p.a) + at;
+      const float back = bf16_round(a);
+      if (i < n) {
+        hi[0] = __float2bfloat16(back);
+        hi[(long)p.T * p.k * p.I] = __float2bfloat16(isinf(back) ? 0.0f : a - back);
       }
     }
   }
@@ -482,8 +516,7 @@ __device__ __forceinline__ void store_hidden(const FewParams& p, int row, int n,
 
 // The parts of a tile of a that is split along K, added in the order of K (the
 // tile ends the first run, and begins the others), and a of the sums.  A warp
-// takes every fourth row, a lane four columns; two rows and four parts are in
-// flight together.
+// takes every fourth row, a lane four columns; four parts are in flight together.
 template <bool MX>
 __device__ void join_hidden(const FewParams& p, const Cut& cut, const Seg& s, int rank, int half, int first, int last,
                             int r0, int n, int warp, int lane) {
@@ -491,168 +524,159 @@ __device__ void join_hidden(const FewParams& p, const Cut& cut, const Seg& s, in
   const int col = s.n * 128 + lane * 4;
   const float* base = p.part + lane * 4;
 #pragma unroll 1
-  for (int row = warp; row < n; row += 8) {
-    float4 h[2], u[2];
-#pragma unroll
-    for (int m = 0; m < 2; ++m) h[m] = u[m] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  for (int row = warp; row < n; row += 4) {
+    float4 h = make_float4(0.0f, 0.0f, 0.0f, 0.0f), u = h;
 #pragma unroll 1
     for (int o0 = first; o0 <= last; o0 += 4) {
-      float4 vh[2][4], vu[2][4];
+      float4 vh[4], vu[4];
 #pragma unroll
-      for (int m = 0; m < 2; ++m)
-#pragma unroll
-        for (int o = 0; o < 4; ++o) {
-          vh[m][o] = vu[m][o] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          if (row + 4 * m < n && o0 + o <= last) {
-            const int slot = 4 * ((o0 + o) * cut.group + rank) + 2 * half + (o0 + o == first ? 1 : 0);
-            const float* from = base + (long)slot * slot_floats + (row + 4 * m) * 128;
-            vh[m][o] = __ldcg(reinterpret_cast<const float4*>(from));
-            vu[m][o] = __ldcg(reinterpret_cast<const float4*>(from + p.unit_rows * 128));
-          }
-        }
-#pragma unroll
-      for (int m = 0; m < 2; ++m)
-#pragma unroll
-        for (int o = 0; o < 4; ++o) {
-          h[m].x += vh[m][o].x, h[m].y += vh[m][o].y, h[m].z += vh[m][o].z, h[m].w += vh[m][o].w;
-          u[m].x += vu[m][o].x, u[m].y += vu[m][o].y, u[m].z += vu[m][o].z, u[m].w += vu[m][o].w;
-        }
-    }
-#pragma unroll
-    for (int m = 0; m < 2; ++m) {
-      const long r = r0 + row + 4 * m;
-      const bool in = row + 4 * m < n;
-      const float a[4] = {silu_mul(h[m].x, u[m].x), silu_mul(h[m].y, u[m].y), silu_mul(h[m].z, u[m].z),
-                          silu_mul(h[m].w, u[m].w)};
-      if constexpr (MX) {
-        // eight lanes hold a block
-        uint32_t top = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) top = max(top, __float_as_uint(fabsf(a[i])));
-#pragma unroll
-        for (int o = 1; o < 8; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-        const int X = mx_block_exponent(__uint_as_float(top));
-        const float inv = mx_exp2_int(-X);
-        const uint32_t codes = mx_cvt_e4m3x2(a[0] * inv, a[1] * inv) | (uint32_t)mx_cvt_e4m3x2(a[2] * inv, a[3] * inv) << 16;
-        if (in) {
-          *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.a) + r * p.I + col) = codes;
-          if ((lane & 7) == 0) p.asf[r * (p.I / 32) + col / 32] = (uint8_t)(X + 127);
-        }
-      } else {
-        __nv_bfloat16* hi = static_cast<__nv_bfloat16*>(p.a) + r * p.I + col;
-        __nv_bfloat16* lo = hi + (long)p.T * p.k * p.I;
-        float back[4], left[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          back[i] = bf16_round(a[i]);
-          left[i] = isinf(back[i]) ? 0.0f : a[i] - back[i];
-        }
-        if (in) {
-          *reinterpret_cast<uint2*>(hi) = make_uint2(pack_bf16x2(back[0], back[1]), pack_bf16x2(back[2], back[3]));
-          *reinterpret_cast<uint2*>(lo) = make_uint2(pack_bf16x2(left[0], left[1]), pack_bf16x2(left[2], left[3]));
+      for (int o = 0; o < 4; ++o) {
+        vh[o] = vu[o] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (o0 + o <= last) {
+          const int slot = 4 * ((o0 + o) * cut.group + rank) + 2 * half + (o0 + o == first ? 1 : 0);
+          const float* from = base + (long)slot * slot_floats + row * 128;
+          vh[o] = __ldcg(reinterpret_cast<const float4*>(from));
+          vu[o] = __ldcg(reinterpret_cast<const float4*>(from + p.unit_rows * 128));
         }
       }
+#pragma unroll
+      for (int o = 0; o < 4; ++o) {
+        h.x += vh[o].x, h.y += vh[o].y, h.z += vh[o].z, h.w += vh[o].w;
+        u.x += vu[o].x, u.y += vu[o].y, u.z += vu[o].z, u.w += vu[o].w;
+      }
+    }
+    const long at = (long)(r0 + row) * p.I + col;
+    const float a[4] = {silu_mul(h.x, u.x), silu_mul(h.y, u.y), silu_mul(h.z, u.z), silu_mul(h.w, u.w)};
+    if constexpr (MX) {
+      // eight lanes hold a block
+      uint32_t top = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) top = max(top, __float_as_uint(fabsf(a[i])));
+#pragma unroll
+      for (int o = 1; o < 8; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const int X = mx_block_exponent(__uint_as_float(top));
+      const float inv = mx_exp2_int(-X);
+      *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.a) + at) =
+          mx_cvt_e4m3x2(a[0] * inv, a[1] * inv) | (uint32_t)mx_cvt_e4m3x2(a[2] * inv, a[3] * inv) << 16;
+      if ((lane & 7) == 0) p.asf[at / 32] = (uint8_t)(X + 127);
+    } else {
+      __nv_bfloat16* hi = static_cast<__nv_bfloat16*>(p.a) + at;
+      float back[4], left[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        back[i] = bf16_round(a[i]);
+        left[i] = isinf(back[i]) ? 0.0f : a[i] - back[i];
+      }
+      *reinterpret_cast<uint2*>(hi) = make_uint2(pack_bf16x2(back[0], back[1]), pack_bf16x2(back[2], back[3]));
+      *reinterpret_cast<uint2*>(hi + (long)p.T * p.k * p.I) =
+          make_uint2(pack_bf16x2(left[0], left[1]), pack_bf16x2(left[2], left[3]));
     }
   }
 }
 
-// The combine: 4 columns of a token to LANES threads, each of which brings y
-// of every LANES-th expert -- from y's buffer or, where its tile was split
-// along K, as the sum of the parts -- and all of which add them up in the
-// order of j.  The loads of an item, and of ITEMS of them, are in flight
-// together.
-template <int LANES, int ITEMS>
-__device__ __forceinline__ void combine(const FewParams& p, const Schedule& s, const Cut* cuts, int nthreads) {
+// The runs of every tile of y, for the combine: first | last << 16,
+// [units][supers] of each half in turn.
+__device__ void list_runs(const Cut* cuts, uint32_t* table, int nthreads) {
+  const int n0 = cuts[0].units * cuts[0].supers, n = n0 + cuts[1].units * cuts[1].supers;
+  for (int i = threadIdx.x; i < n; i += nthreads) {
+    const Cut& c = cuts[i >= n0];
+    int first, last;
+    seg_runs(c, i - (i >= n0 ? n0 : 0), first, last);
+    table[i] = (uint32_t)first | (uint32_t)last << 16;
+  }
+}
+
+// The combine: 4 columns of a token to LANES threads.  Each brings y of
+// EACH experts at a time -- from y's buffer or, where its tile was split along
+// K, as the sum of the parts -- all their loads in flight together; the
+// lanes' values are added up in the order of j.
+template <int LANES, int EACH>
+__device__ __forceinline__ void combine(const FewParams& p, const Schedule& s, const Cut* cuts, const uint32_t* table,
+                                        int nthreads) {
+  static_assert(LANES == 1 || EACH == 1, "several lanes bring one expert each");
   const int vecs = p.H / 4;
   const int slot_floats = 2 * p.unit_rows * 128;
   const int sub = threadIdx.x & (LANES - 1);
   const int items = p.T * vecs, stride = gridDim.x * nthreads / LANES;
+  const int group = cuts[0].group, supers = cuts[0].supers;
   const int ahead = (threadIdx.x & 31) / LANES;  // items of the warp before this one: its lanes stay together
-  for (int i0 = (blockIdx.x * nthreads + threadIdx.x) / LANES; i0 - ahead < items; i0 += stride * ITEMS) {
-    float4 acc[ITEMS];
+#pragma unroll 1
+  for (int i = (blockIdx.x * nthreads + threadIdx.x) / LANES; i - ahead < items; i += stride) {
+    const bool in = i < items;
+    const int t = in ? i / vecs : 0, col = (in ? i - t * vecs : 0) * 4;
+    const int n = col >> 8, sup = n / group, rank = n - sup * group;
+    const float* part_at = p.part + ((col >> 7) & 1) * p.unit_rows * 128 + (col & 127);
+    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 1
+    for (int j0 = 0; j0 < p.k; j0 += LANES * EACH) {
+      const float4 *next[EACH];
+      int more[EACH];  // parts past the first
+      float w[EACH];
+      float4 y[EACH];
 #pragma unroll
-    for (int m = 0; m < ITEMS; ++m) acc[m] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (int j0 = 0; j0 < p.k; j0 += LANES) {
-      const int j = j0 + sub;
-      const float4 *from[ITEMS], *next[ITEMS];
-      int more[ITEMS];  // parts past the first
-      float w[ITEMS];
-#pragma unroll
-      for (int m = 0; m < ITEMS; ++m) {
-        const int i = i0 + m * stride;
-        from[m] = nullptr;
-        more[m] = 0;
+      for (int m = 0; m < EACH; ++m) {
+        const int j = j0 + sub + m, f = t * p.k + j;
+        more[m] = -1;
         w[m] = 0.0f;
-        if (i >= items || j >= p.k) continue;
-        const int t = i / vecs, col = (i - t * vecs) * 4, f = t * p.k + j;
-        const int unit = s.unit_of[f];
-        if (unit == kNoUnit) continue;
-        w[m] = p.scores[f];
-        const int n = col >> 8, half = unit >= cuts[1].unit0;
-        const Cut& c = cuts[half];
-        const int in_unit = n / c.group, rank = n - in_unit * c.group;
-        int first, last;
-        seg_runs(c, (unit - c.unit0) * c.supers + in_unit, first, last);
-        if (first == last) {
-          from[m] = reinterpret_cast<const float4*>(p.y + (long)f * p.H + col);
-        } else {
-          const float* at = p.part + ((((col >> 7) & 1) * p.unit_rows) + s.row_of[f]) * 128 + (col & 127);
-          from[m] = reinterpret_cast<const float4*>(at + (long)((first * c.group + rank) * 4 + half * 2 + 1) * slot_floats);
-          next[m] = reinterpret_cast<const float4*>(at + (long)(((first + 1) * c.group + rank) * 4 + half * 2) * slot_floats);
+        y[m] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        const int unit = in && j < p.k ? s.unit_of[f] : kNoUnit;
+        if (unit != kNoUnit) {
+          w[m] = p.scores[f];
+          const int half = unit >= cuts[1].unit0;
+          int first, last;
+          if (table) {
+            const uint32_t runs = table[unit * supers + sup];
+            first = runs & 0xFFFF;
+            last = runs >> 16;
+          } else {
+            seg_runs(cuts[half], (unit - cuts[half].unit0) * supers + sup, first, last);
+          }
           more[m] = last - first;
+          const float* from = p.y + (long)f * p.H + col;
+          if (more[m]) {
+            const float* at = part_at + s.row_of[f] * 128;
+            from = at + (long)((first * group + rank) * 4 + half * 2 + 1) * slot_floats;
+            next[m] = reinterpret_cast<const float4*>(at + (long)(((first + 1) * group + rank) * 4 + half * 2) * slot_floats);
+          }
+          y[m] = __ldcg(reinterpret_cast<const float4*>(from));
         }
       }
-      float4 y[ITEMS], z[ITEMS];
+      float4 z[EACH];
 #pragma unroll
-      for (int m = 0; m < ITEMS; ++m) {
-        y[m] = from[m] ? __ldcg(from[m]) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        z[m] = more[m] ? __ldcg(next[m]) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      }
+      for (int m = 0; m < EACH; ++m) z[m] = more[m] > 0 ? __ldcg(next[m]) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-      for (int m = 0; m < ITEMS; ++m) {
-        const int group = cuts[0].group;
-        y[m].x += z[m].x;
-        y[m].y += z[m].y;
-        y[m].z += z[m].z;
-        y[m].w += z[m].w;
+      for (int m = 0; m < EACH; ++m) {
+        y[m].x += z[m].x, y[m].y += z[m].y, y[m].z += z[m].z, y[m].w += z[m].w;
 #pragma unroll 1
         for (int o = 1; o < more[m]; ++o) {
-          const float4 v = __ldcg(next[m] + (long)o * group * 4 * (slot_floats / 4));
-          y[m].x += v.x;
-          y[m].y += v.y;
-          y[m].z += v.z;
-          y[m].w += v.w;
+          const float4 v = __ldcg(next[m] + o * group * slot_floats);  // 4 slots a CTA, 4 floats a vector
+          y[m].x += v.x, y[m].y += v.y, y[m].z += v.z, y[m].w += v.w;
         }
-        const bool on = from[m] != nullptr;
+      }
 #pragma unroll
-        for (int l = 0; l < LANES; ++l) {
-          const float wl = LANES > 1 ? __shfl_sync(0xffffffffu, w[m], l, LANES) : w[m];
-          const bool ol = LANES > 1 ? __shfl_sync(0xffffffffu, (int)on, l, LANES) != 0 : on;
-          float4 v = y[m];
-          if (LANES > 1) {
-            v.x = __shfl_sync(0xffffffffu, y[m].x, l, LANES);
-            v.y = __shfl_sync(0xffffffffu, y[m].y, l, LANES);
-            v.z = __shfl_sync(0xffffffffu, y[m].z, l, LANES);
-            v.w = __shfl_sync(0xffffffffu, y[m].w, l, LANES);
-          }
-          if (ol) {
-            acc[m].x = fmaf(wl, v.x, acc[m].x);
-            acc[m].y = fmaf(wl, v.y, acc[m].y);
-            acc[m].z = fmaf(wl, v.z, acc[m].z);
-            acc[m].w = fmaf(wl, v.w, acc[m].w);
-          }
+      for (int l = 0; l < LANES * EACH; ++l) {
+        float wl = w[EACH > 1 ? l : 0];
+        float4 v = y[EACH > 1 ? l : 0];
+        bool on = more[EACH > 1 ? l : 0] >= 0;
+        if (LANES > 1) {
+          wl = __shfl_sync(0xffffffffu, wl, l, LANES);
+          v.x = __shfl_sync(0xffffffffu, v.x, l, LANES);
+          v.y = __shfl_sync(0xffffffffu, v.y, l, LANES);
+          v.z = __shfl_sync(0xffffffffu, v.z, l, LANES);
+          v.w = __shfl_sync(0xffffffffu, v.w, l, LANES);
+          on = __shfl_sync(0xffffffffu, (int)on, l, LANES) != 0;
+        }
+        if (on) {
+          acc.x = fmaf(wl, v.x, acc.x);
+          acc.y = fmaf(wl, v.y, acc.y);
+          acc.z = fmaf(wl, v.z, acc.z);
+          acc.w = fmaf(wl, v.w, acc.w);
         }
       }
     }
-#pragma unroll
-    for (int m = 0; m < ITEMS; ++m) {
-      const int i = i0 + m * stride;
-      if (sub == 0 && i < items) {
-        const int t = i / vecs, col = (i - t * vecs) * 4;
-        *reinterpret_cast<uint2*>(p.out + (long)t * p.H + col) =
-            make_uint2(pack_bf16x2(acc[m].x, acc[m].y), pack_bf16x2(acc[m].z, acc[m].w));
-      }
-    }
+    if (sub == 0 && in)
+      *reinterpret_cast<uint2*>(p.out + (long)t * p.H + col) =
+          make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
   }
 }
 
@@ -671,7 +695,8 @@ __global__ void __launch_bounds__(MX ? 320 : 256, 1) few_kernel(const __grid_con
   sched.offset = reinterpret_cast<uint16_t*>(ctl + 1);
   sched.unit0 = sched.offset + p.E;
   sched.perm = sched.unit0 + p.E;
-  sched.unit_of = sched.perm + R;
+  sched.token = sched.perm + R;
+  sched.unit_of = sched.token + R;
   sched.unit_e = sched.unit_of + R;
   sched.unit_r = sched.unit_e + p.max_units;
   sched.row_of = reinterpret_cast<uint8_t*>(sched.unit_r + p.max_units);
@@ -685,7 +710,7 @@ __global__ void __launch_bounds__(MX ? 320 : 256, 1) few_kernel(const __grid_con
     const char* a = reinterpret_cast<const char*>(p.x);
     const long bytes = (long)p.T * p.H * 2, at = ((long)blockIdx.x * kThreads + threadIdx.x) * 128;
     if (at < bytes) asm volatile("prefetch.global.L2 [%0];" ::"l"(a + at));
-    if (!p.Wr && threadIdx.x < R && warp == 0) asm volatile("prefetch.global.L2 [%0];" ::"l"(p.idx + threadIdx.x));
+    if (!p.Wr && threadIdx.x * 32 < R) asm volatile("prefetch.global.L2 [%0];" ::"l"(p.idx + threadIdx.x * 32));
     if (blockIdx.x == 0 && p.bias && threadIdx.x * 32 < p.E)
       asm volatile("prefetch.global.L2 [%0];" ::"l"(p.bias + threadIdx.x * 32));
   }
@@ -738,7 +763,7 @@ __global__ void __launch_bounds__(MX ? 320 : 256, 1) few_kernel(const __grid_con
     __syncthreads();
     ok = ctl->go != 0;
   }
-  if (ok) build_units(p, sched, smem, ctl, kThreads);
+  if (ok) build_units<MX>(p, sched, smem, ctl, kThreads);
   // the stages' first loads (async proxy) come after these threads' use of the same shared memory
   fence_proxy_async_shared();
   const int c = blockIdx.x;
@@ -773,8 +798,8 @@ __global__ void __launch_bounds__(MX ? 320 : 256, 1) few_kernel(const __grid_con
         const Cut cut = ctl->cuts[ph];
         const int g = ph >> 1;
         if (!fine || !cut.takes(c)) continue;
-        const long end = cut.begin(c / cut.group + 1);
-        for (long b = cut.begin(c / cut.group); b < end && fine;) {
+        const int end = cut.begin(c / cut.group + 1);
+        for (int b = cut.begin(c / cut.group); b < end && fine;) {
           const Seg s = seg_at(cut, b, end, c % cut.group);
           const int e = sched.unit_e[s.unit];
           const int col = g == 0 ? s.n * 128 : s.n * 256;
@@ -828,8 +853,8 @@ __global__ void __launch_bounds__(MX ? 320 : 256, 1) few_kernel(const __grid_con
       const Cut cut = ctl->cuts[ph];
       const int g = ph >> 1;
       if (!fine || !cut.takes(c)) continue;
-      const long end = cut.begin(c / cut.group + 1);
-      for (long b = cut.begin(c / cut.group); b < end && fine;) {
+      const int end = cut.begin(c / cut.group + 1);
+      for (int b = cut.begin(c / cut.group); b < end && fine;) {
         const Seg s = seg_at(cut, b, end, c % cut.group);
         const int n = (sched.unit_n[s.unit] + 15) & ~15;
         const bool second = g == 0 || s.n * 256 + 128 < p.H;
@@ -850,36 +875,41 @@ __global__ void __launch_bounds__(MX ? 320 : 256, 1) few_kernel(const __grid_con
           if (lane == 0) {
             // the tokens' operand was written with cp.async: order it before the tensor core's (async-proxy) reads
             fence_proxy_async_shared();
-            const uint32_t a0 = smem_u32(smem + (size_t)stage * stage_bytes), a1 = a0 + kATile, b0 = a0 + 2 * kATile;
+            const uint32_t a0 = smem_u32(smem + (size_t)stage * stage_bytes), b0 = a0 + 2 * kATile;
+            // (small loops: a few tokens' pass runs each of these instructions a
+            // few times, and fetching them costs more than issuing them)
             if constexpr (MX) {
               const uint32_t sf = smem_u32(sf_smem + stage * kSfBytes);
               const uint32_t t = tmem + 256 + stage * 16;  // scales: two A tiles, B
+              uint64_t ad = sdesc_sw128(a0, 16384, 1024), bd = sdesc_sw128(b0, 16, 1024);
               tmem_cp_32x128b_warpx4(t, sdesc_plain(sf + 1024, 16, 128));
               if (second) tmem_cp_32x128b_warpx4(t + 4, sdesc_plain(sf + 1536, 16, 128));
               tmem_cp_32x128b_warpx4(t + 8, sdesc_plain(sf + 2048, 16, 128));
-#pragma unroll
+#pragma unroll 1
               for (int k32 = 0; k32 < 4; ++k32) {
                 const uint32_t idesc = idesc_mxf8(128, n, 1, 0, k32, k32);
-                const uint64_t bd = sdesc_sw128(b0 + k32 * 32, 16, 1024);
                 const uint32_t acc = kb > s.k0 || k32 > 0;
-                mma_mxf8(d0, sdesc_sw128(a0 + k32 * 4096, 16384, 1024), bd, idesc, t, t + 8, acc);
-                if (second) mma_mxf8(d1, sdesc_sw128(a1 + k32 * 4096, 16384, 1024), bd, idesc, t + 4, t + 8, acc);
+                mma_mxf8(d0, ad, bd, idesc, t, t + 8, acc);
+                if (second) mma_mxf8(d1, ad + kATile / 16, bd, idesc, t + 4, t + 8, acc);
+                ad += 4096 / 16;
+                bd += 32 / 16;
               }
             } else {
               const uint32_t idesc = idesc_bf16(128, n, 1, 0);
-#pragma unroll
-              for (int k16 = 0; k16 < 4; ++k16) {
-                const uint64_t ad0 = sdesc_sw128(a0 + k16 * 2048, 8192, 1024);
-                const uint64_t ad1 = sdesc_sw128(a1 + k16 * 2048, 8192, 1024);
-                const uint64_t bd = sdesc_sw128(b0 + k16 * 32, 16, 1024);
-                const uint32_t acc = kb > s.k0 || k16 > 0;
-                mma_bf16(d0, ad0, bd, idesc, acc);
-                if (second) mma_bf16(d1, ad1, bd, idesc, acc);
-                if (g == 1) {
-                  const uint64_t bl = sdesc_sw128(b0 + b_bytes + k16 * 32, 16, 1024);
-                  mma_bf16(d0, ad0, bl, idesc, 1);
-                  if (second) mma_bf16(d1, ad1, bl, idesc, 1);
+              uint64_t bd = sdesc_sw128(b0, 16, 1024);
+              // second GEMM: a's bf16, then what its rounding left
+#pragma unroll 1
+              for (int part = 0; part <= g; ++part) {
+                uint64_t ad = sdesc_sw128(a0, 8192, 1024);
+#pragma unroll 1
+                for (int k16 = 0; k16 < 4; ++k16) {
+                  const uint32_t acc = kb > s.k0 || (part | k16) > 0;
+                  mma_bf16(d0, ad, bd, idesc, acc);
+                  if (second) mma_bf16(d1, ad + kATile / 16, bd, idesc, acc);
+                  ad += 2048 / 16;
+                  bd += 32 / 16;
                 }
+                bd += (b_bytes - 128) / 16;
               }
             }
             mma_commit(&ctl->empty[stage]);
@@ -926,35 +956,29 @@ __global__ void __launch_bounds__(MX ? 320 : 256, 1) few_kernel(const __grid_con
       const uint8_t* src = g == 0 ? (MX ? p.xq : reinterpret_cast<const uint8_t*>(p.x)) : static_cast<uint8_t*>(p.a);
       const uint8_t* sfs = g == 0 ? p.xsf : p.asf;
       const long lo = (long)p.T * p.k * p.I * 2;  // a's second part
-      const long end = cut.begin(c / cut.group + 1);
-      for (long b = cut.begin(c / cut.group); b < end && fine;) {
+      const int end = cut.begin(c / cut.group + 1);
+      for (int b = cut.begin(c / cut.group); b < end && fine;) {
         const Seg s = seg_at(cut, b, end, c % cut.group);
         const int n = sched.unit_n[s.unit], r0 = sched.unit_r[s.unit];
-        long at[8];  // byte offset of this thread's piece in rows tid / 8 + 8 i
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int r = (tid >> 3) + 8 * i;
-          at[i] = 0;
-          if (r < n) at[i] = (long)(g == 0 ? sched.perm[r0 + r] / p.k : r0 + r) * K * (MX ? 1 : 2) + ch * 16;
-        }
-        const long sf_at = MX && tid < n ? (long)(g == 0 ? sched.perm[r0 + tid] / p.k : r0 + tid) * (K / 32) : 0;
+        const long row_bytes = (long)K * (MX ? 1 : 2);
+        const int sf_row = MX && tid < n ? (g == 0 ? sched.token[r0 + tid] : r0 + tid) : 0;
         for (int kb = s.k0; kb < s.k1; ++kb) {
           if (!mbar_wait(&ctl->empty[stage], phase ^ 1, wc)) {
             fine = false;
             break;
           }
           const uint32_t dst = smem_u32(smem + (size_t)stage * stage_bytes + 2 * kATile);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int r = (tid >> 3) + 8 * i;
-            if (r < n) {
-              const uint32_t d = dst + r * 128 + ((ch ^ (r & 7)) << 4);
-              cp_async_16(d, src + at[i] + (long)kb * 128);
-              if (!MX && g == 1) cp_async_16(d + b_bytes, src + lo + at[i] + (long)kb * 128);
-            }
+          const uint8_t* from = src + (long)kb * 128 + ch * 16;
+#pragma unroll 1
+          for (int r = tid >> 3; r < n; r += kProducers / 8) {
+            const uint8_t* piece = from + (g == 0 ? sched.token[r0 + r] : r0 + r) * row_bytes;
+            const uint32_t d = dst + r * 128 + ((ch ^ (r & 7)) << 4);
+            cp_async_16(d, piece);
+            if (!MX && g == 1) cp_async_16(d + b_bytes, piece + lo);
           }
           if (MX && tid < n)
-            cp_async_4(smem_u32(sf_smem + stage * kSfBytes + 2048 + mx_sf_offset(tid, 0)), sfs + sf_at + kb * 4, 4);
+            cp_async_4(smem_u32(sf_smem + stage * kSfBytes + 2048 + mx_sf_offset(tid, 0)),
+                       sfs + (long)sf_row * (K / 32) + kb * 4, 4);
           cp_async_arrive_noinc(&ctl->full_b[stage]);
           if (++stage == (uint32_t)p.stages) { stage = 0; phase ^= 1; }
         }
@@ -974,30 +998,14 @@ __global__ void __launch_bounds__(MX ? 320 : 256, 1) few_kernel(const __grid_con
       const int g = ph >> 1, half = ph & 1;
       if (!fine || !cut.takes(c)) continue;
       const int run = c / cut.group, rank = c % cut.group;
-      const long end = cut.begin(run + 1);
-      for (long b = cut.begin(run); b < end;) {
+      const int end = cut.begin(run + 1);
+      for (int b = cut.begin(run); b < end;) {
         const Seg s = seg_at(cut, b, end, rank);
         b += s.k1 - s.k0;
         const int n = sched.unit_n[s.unit], r0 = sched.unit_r[s.unit];
         const bool second = g == 0 || s.n * 256 + 128 < p.H;
         const bool whole = s.k0 == 0 && s.k1 == cut.kb;
         const int lane_col = q * 32 + lane;
-        auto finish = [&](int i0, const float* v0, const float* v1) {
-          const int rows = min(16, n - i0);
-          if (g == 0) {
-            store_hidden<MX>(p, r0 + i0, rows, s.n * 128 + lane_col, lane, v0, v1);
-          } else {
-            float* y = p.y + s.n * 256 + lane_col;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              if (i < rows) {
-                float* yr = y + (long)sched.perm[r0 + i0 + i] * p.H;
-                __stcg(yr, v0[i]);
-                if (second) __stcg(yr + 128, v1[i]);
-              }
-            }
-          }
-        };
         const uint32_t buf = count & 1;
         fine = vote_all(1, kEpilogue, mbar_wait(&ctl->tfull[buf], (count >> 1) & 1, wc));
         if (!fine) break;
@@ -1005,29 +1013,21 @@ __global__ void __launch_bounds__(MX ? 320 : 256, 1) few_kernel(const __grid_con
         const uint32_t d = tmem + buf * 2 * p.unit_rows + ((uint32_t)(q * 32) << 16);
         // four slots a CTA: of each half, the tile that its run ends in (1) or begins in (0)
         float* slot = p.part + (long)(4 * c + 2 * half + (s.k0 == 0 ? 1 : 0)) * slot_floats + lane_col;
-        for (int i0 = 0; i0 < n; i0 += 16) {
-          uint32_t w0[16], w1[16];
-          tmem_ld16_issue(d + i0, w0);
-          tmem_ld16_issue(d + p.unit_rows + i0, w1);
-          tmem_wait_ld();
-          tmem_regs_ready16(w0);
-          tmem_regs_ready16(w1);
-          float v0[16], v1[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            v0[i] = __uint_as_float(w0[i]);
-            v1[i] = __uint_as_float(w1[i]);
+#pragma unroll 1
+        for (int i0 = 0; i0 < n; i0 += 4) {
+          float v0[4], v1[4];
+          tmem_ld4x2(d + i0, d + p.unit_rows + i0, v0, v1);
+          if (g == 0 && whole) {
+            store_hidden<MX>(p, r0 + i0, n - i0, s.n * 128 + lane_col, lane, v0, v1);
+            continue;
           }
-          if (whole) {
-            finish(i0, v0, v1);
-          } else {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              if (i0 + i < n) {
-                __stcg(slot + (i0 + i) * 128, v0[i]);
-                if (second) __stcg(slot + (p.unit_rows + i0 + i) * 128, v1[i]);
-              }
-            }
+          for (int i = 0; i < 4; ++i) {
+            if (i0 + i >= n) break;
+            // y's row, or the row of this part's slot
+            float* to = whole ? p.y + (long)sched.perm[r0 + i0 + i] * p.H + s.n * 256 + lane_col : slot + (i0 + i) * 128;
+            __stcg(to, v0[i]);
+            if (second) __stcg(to + (whole ? 128 : p.unit_rows * 128), v1[i]);
           }
         }
         tc_fence_before();
@@ -1069,8 +1069,8 @@ __global__ void __launch_bounds__(MX ? 320 : 256, 1) few_kernel(const __grid_con
     for (int ph = 0; ph < 4; ++ph) {
       const Cut cut = ctl->cuts[ph];
       if (!fine || !cut.takes(c)) continue;
-      const long blocks = cut.begin(c / cut.group + 1) - cut.begin(c / cut.group);
-      for (long b = 0; b < blocks; ++b) {
+      const int blocks = cut.begin(c / cut.group + 1) - cut.begin(c / cut.group);
+      for (int b = 0; b < blocks; ++b) {
         fine = mbar_wait(&ctl->full_a[stage], phase, wc);
         if (!fine) break;
         const uint8_t* raw = sf_smem + stage * kSfBytes + i * 512;
@@ -1098,15 +1098,22 @@ __global__ void __launch_bounds__(MX ? 320 : 256, 1) few_kernel(const __grid_con
   asm volatile("barrier.sync 0;" ::: "memory");
   tc_fence_after();
   if (warp == 0) tmem_dealloc(tmem, 512);
+  // eight threads an item while there are threads for it
   const bool one = (long)p.T * (p.H / 4) * 8 <= (long)gridDim.x * kThreads;
-  if (units > 0 && (long)c * kThreads < (long)p.T * (p.H / 4) * 8) {
+  if (units > 0 && (long)c * kThreads < (long)p.T * (p.H / 4) * (one ? 8 : 1)) {
+    // the stages are free for the table (one that is too long for them is looked up as it goes)
+    uint32_t* table = reinterpret_cast<uint32_t*>(smem);
+    if ((size_t)units * ctl->cuts[2].supers * 4 <= (size_t)p.stages * stage_bytes)
+      list_runs(ctl->cuts + 2, table, kThreads);
+    else
+      table = nullptr;
     if (threadIdx.x == 0) ctl->go = wait_flag_geq(word(p, kWordSummed), gridDim.x, wc) ? 1 : 0;
     __syncthreads();
     if (ctl->go) {
       if (one)
-        combine<8, 1>(p, sched, ctl->cuts + 2, kThreads);
+        combine<8, 1>(p, sched, ctl->cuts + 2, table, kThreads);
       else
-        combine<8, 4>(p, sched, ctl->cuts + 2, kThreads);
+        combine<1, 4>(p, sched, ctl->cuts + 2, table, kThreads);
     }
   }
   if (threadIdx.x == 0) {
