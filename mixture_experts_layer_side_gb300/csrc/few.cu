@@ -702,6 +702,7 @@ __global__ void __launch_bounds__(MX ? 320 : 256, 1) few_kernel(const __grid_con
   sched.row_of = reinterpret_cast<uint8_t*>(sched.unit_r + p.max_units);
   sched.unit_n = sched.row_of + R;
 
+  const int d_cols = (MX ? 1 : 2) * p.unit_rows;  // TMEM columns of one accumulator: at most 4 x 64 (MXFP8), 4 x 128
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   WaitCtx wc{&ctl->abort, p.hdr + kHdrAbort, p.hdr + kHdrError};
 
@@ -864,7 +865,7 @@ __global__ void __launch_bounds__(MX ? 320 : 256, 1) few_kernel(const __grid_con
           break;
         }
         tc_fence_after();
-        const uint32_t d0 = tmem + buf * 2 * p.unit_rows, d1 = d0 + p.unit_rows;
+        const uint32_t d0 = tmem + buf * 2 * d_cols, d1 = d0 + d_cols;
         for (int kb = s.k0; kb < s.k1; ++kb) {
           if (!mbar_wait(&ctl->full_a[stage], phase, wc) || !mbar_wait(&ctl->full_b[stage], phase, wc) ||
               (MX && !mbar_wait(&ctl->scales[stage], phase, wc))) {
@@ -895,21 +896,18 @@ __global__ void __launch_bounds__(MX ? 320 : 256, 1) few_kernel(const __grid_con
                 bd += 32 / 16;
               }
             } else {
-              const uint32_t idesc = idesc_bf16(128, n, 1, 0);
-              uint64_t bd = sdesc_sw128(b0, 16, 1024);
-              // second GEMM: a's bf16, then what its rounding left
+              // second GEMM: a's bf16 and, as more columns, what its rounding
+              // left (a matrix instruction of so few columns takes as long as
+              // one of twice as many: it waits for its A operand)
+              const uint32_t idesc = idesc_bf16(128, g == 0 ? n : 2 * n, 1, 0);
+              uint64_t ad = sdesc_sw128(a0, 8192, 1024), bd = sdesc_sw128(b0, 16, 1024);
 #pragma unroll 1
-              for (int part = 0; part <= g; ++part) {
-                uint64_t ad = sdesc_sw128(a0, 8192, 1024);
-#pragma unroll 1
-                for (int k16 = 0; k16 < 4; ++k16) {
-                  const uint32_t acc = kb > s.k0 || (part | k16) > 0;
-                  mma_bf16(d0, ad, bd, idesc, acc);
-                  if (second) mma_bf16(d1, ad + kATile / 16, bd, idesc, acc);
-                  ad += 2048 / 16;
-                  bd += 32 / 16;
-                }
-                bd += (b_bytes - 128) / 16;
+              for (int k16 = 0; k16 < 4; ++k16) {
+                const uint32_t acc = kb > s.k0 || k16 > 0;
+                mma_bf16(d0, ad, bd, idesc, acc);
+                if (second) mma_bf16(d1, ad + kATile / 16, bd, idesc, acc);
+                ad += 2048 / 16;
+                bd += 32 / 16;
               }
             }
             mma_commit(&ctl->empty[stage]);
@@ -960,6 +958,7 @@ __global__ void __launch_bounds__(MX ? 320 : 256, 1) few_kernel(const __grid_con
       for (int b = cut.begin(c / cut.group); b < end && fine;) {
         const Seg s = seg_at(cut, b, end, c % cut.group);
         const int n = sched.unit_n[s.unit], r0 = sched.unit_r[s.unit];
+        const int n16 = (n + 15) & ~15;
         const long row_bytes = (long)K * (MX ? 1 : 2);
         const int sf_row = MX && tid < n ? (g == 0 ? sched.token[r0 + tid] : r0 + tid) : 0;
         for (int kb = s.k0; kb < s.k1; ++kb) {
@@ -974,7 +973,7 @@ __global__ void __launch_bounds__(MX ? 320 : 256, 1) few_kernel(const __grid_con
             const uint8_t* piece = from + (g == 0 ? sched.token[r0 + r] : r0 + r) * row_bytes;
             const uint32_t d = dst + r * 128 + ((ch ^ (r & 7)) << 4);
             cp_async_16(d, piece);
-            if (!MX && g == 1) cp_async_16(d + b_bytes, piece + lo);
+            if (!MX && g == 1) cp_async_16(d + n16 * 128, piece + lo);
           }
           if (MX && tid < n)
             cp_async_4(smem_u32(sf_smem + stage * kSfBytes + 2048 + mx_sf_offset(tid, 0)),
@@ -1005,18 +1004,28 @@ __global__ void __launch_bounds__(MX ? 320 : 256, 1) few_kernel(const __grid_con
         const int n = sched.unit_n[s.unit], r0 = sched.unit_r[s.unit];
         const bool second = g == 0 || s.n * 256 + 128 < p.H;
         const bool whole = s.k0 == 0 && s.k1 == cut.kb;
+        const int n16 = (n + 15) & ~15;
         const int lane_col = q * 32 + lane;
         const uint32_t buf = count & 1;
         fine = vote_all(1, kEpilogue, mbar_wait(&ctl->tfull[buf], (count >> 1) & 1, wc));
         if (!fine) break;
         tc_fence_after();
-        const uint32_t d = tmem + buf * 2 * p.unit_rows + ((uint32_t)(q * 32) << 16);
+        const uint32_t d = tmem + buf * 2 * d_cols + ((uint32_t)(q * 32) << 16);
         // four slots a CTA: of each half, the tile that its run ends in (1) or begins in (0)
         float* slot = p.part + (long)(4 * c + 2 * half + (s.k0 == 0 ? 1 : 0)) * slot_floats + lane_col;
 #pragma unroll 1
         for (int i0 = 0; i0 < n; i0 += 4) {
           float v0[4], v1[4];
-          tmem_ld4x2(d + i0, d + p.unit_rows + i0, v0, v1);
+          tmem_ld4x2(d + i0, d + d_cols + i0, v0, v1);
+          if (!MX && g == 1) {
+            float l0[4], l1[4];
+            tmem_ld4x2(d + n16 + i0, d + d_cols + n16 + i0, l0, l1);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              v0[i] += l0[i];
+              v1[i] += l1[i];
+            }
+          }
           if (g == 0 && whole) {
             store_hidden<MX>(p, r0 + i0, n - i0, s.n * 128 + lane_col, lane, v0, v1);
             continue;
