@@ -7,152 +7,434 @@
 //   dz_v = (dloss / tau) (q_v - sum_{j: id_j = v} p_j)
 //
 // An entry of p_j = 0 adds nothing; a row whose list is empty has loss 0 and
-// gradient 0.  One CTA per row: the row's maximum and sum in one pass over
-// the row, each thread keeping a running pair, joined in a fixed tree.
+// gradient 0.  Every operation is bound by the row's bytes: the forward reads
+// it once, the backward reads and writes it once, and the step, which needs
+// the row's sum before it can write, keeps the row on the chip in between:
+//
+//  * Rows are read in 16-byte vectors of the address grid (a row of any
+//    alignment has at most one part-filled vector at each end).
+//  * Each thread keeps a running maximum m and sum of exp2((z - m) c), c =
+//    log2(e) / tau; threads, warps and CTAs join theirs in a fixed tree.
+//  * A row is shared by a cluster of up to 8 CTAs, which exchange their
+//    (m, sum) through distributed shared memory: a few rows still fill the
+//    GPU, and in the step each thread holds its share of the row -- up to 8
+//    vectors -- in registers between the sum and the gradient.  Several CTAs
+//    an SM are in different phases, so loads and stores overlap.
+//  * The teacher's list (at most MOK_DISTILL_MAX_TOP entries) is a warp's
+//    work, hidden behind the row's loads.  Listed columns are stored after
+//    the rest of their vectors, by the thread that is the first with that id.
+//
+// Rows too long for the registers (more than 262,144 bf16 or 131,072 f32) take
+// the forward and then the backward.
+#include <cooperative_groups.h>
+
 #include "distill.cuh"
 
 namespace mok {
+
+namespace cg = cooperative_groups;
 
 namespace {
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
+constexpr int kMaxShare = 8;  // CTAs a row
+constexpr float kLog2e = 1.4426950408889634f;
+static_assert(MOK_DISTILL_MAX_TOP <= kThreads, "one thread an entry of the list");
 
-__device__ __forceinline__ float value(const __nv_bfloat16* z, long i) { return __bfloat162float(z[i]); }
-__device__ __forceinline__ float value(const float* z, long i) { return z[i]; }
-__device__ __forceinline__ void put(__nv_bfloat16* z, long i, float v) { z[i] = __float2bfloat16(v); }
-__device__ __forceinline__ void put(float* z, long i, float v) { z[i] = v; }
+__device__ __forceinline__ float fast_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 
-// (m, s) stands for s * exp(m); -inf, 0 for nothing
-__device__ __forceinline__ void join(float& m, float& s, float mo, float so) {
-  const float top = fmaxf(m, mo);
-  const float base = top == -INFINITY ? 0.0f : top;
-  s = s * expf(m - base) + so * expf(mo - base);
+// Vectors of a type: 16 bytes.
+template <typename Z>
+struct Vec;
+template <>
+struct Vec<__nv_bfloat16> {
+  static constexpr int kN = 8;
+  static __device__ __forceinline__ void unpack(const uint4& v, float (&f)[8]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = __uint_as_float(w[i] << 16);
+      f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+  static __device__ __forceinline__ uint4 pack(const float (&f)[8]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  static __device__ __forceinline__ float top(const uint4& v) {
+    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&v);
+    const __nv_bfloat162 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+    return fmaxf(__low2float(m), __high2float(m));
+  }
+  static __device__ __forceinline__ float value(__nv_bfloat16 z) { return __bfloat162float(z); }
+  static __device__ __forceinline__ __nv_bfloat16 from(float f) { return __float2bfloat16(f); }
+  static __device__ __forceinline__ uint4 lowest() { return make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u); }
+};
+template <>
+struct Vec<float> {
+  static constexpr int kN = 4;
+  static __device__ __forceinline__ void unpack(const uint4& v, float (&f)[4]) {
+    f[0] = __uint_as_float(v.x);
+    f[1] = __uint_as_float(v.y);
+    f[2] = __uint_as_float(v.z);
+    f[3] = __uint_as_float(v.w);
+  }
+  static __device__ __forceinline__ uint4 pack(const float (&f)[4]) {
+    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+  }
+  static __device__ __forceinline__ float top(const uint4& v) {
+    return fmaxf(fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)), fmaxf(__uint_as_float(v.z), __uint_as_float(v.w)));
+  }
+  static __device__ __forceinline__ float value(float z) { return z; }
+  static __device__ __forceinline__ float from(float f) { return f; }
+  static __device__ __forceinline__ uint4 lowest() { return make_uint4(0xFF800000u, 0xFF800000u, 0xFF800000u, 0xFF800000u); }
+};
+
+// A row on the grid of 16-byte vectors: vector i holds elements
+// [i * kN - head, i * kN - head + kN), those outside [0, V) not the row's.
+template <typename Z>
+struct RowGrid {
+  Z* z;
+  int V, head, vecs;
+  __device__ __forceinline__ RowGrid(const void* p, long at, int V_) : V(V_) {
+    z = static_cast<Z*>(const_cast<void*>(p)) + at;
+    head = (int)((reinterpret_cast<uintptr_t>(z) & 15) / sizeof(Z));
+    vecs = (V + head + Vec<Z>::kN - 1) / Vec<Z>::kN;
+  }
+  __device__ __forceinline__ int first(int i) const { return i * Vec<Z>::kN - head; }
+  __device__ __forceinline__ bool whole(int i) const { return first(i) >= 0 && first(i) + Vec<Z>::kN <= V; }
+  // -inf outside the row
+  __device__ __forceinline__ uint4 load(int i) const {
+    if (whole(i)) return __ldcs(reinterpret_cast<const uint4*>(z + first(i)));
+    uint4 v = Vec<Z>::lowest();
+    Z* e = reinterpret_cast<Z*>(&v);
+#pragma unroll
+    for (int k = 0; k < Vec<Z>::kN; ++k) {
+      const int c = first(i) + k;
+      if (c >= 0 && c < V) e[k] = z[c];
+    }
+    return v;
+  }
+};
+
+// (m, s) stands for s * 2^(m c); (-inf, 0) for nothing.  Differences are
+// taken before the product with c, so that rows of the type's lowest value
+// stay finite.
+__device__ __forceinline__ float finite_max(float m) { return m == -INFINITY ? 0.0f : m; }
+__device__ __forceinline__ void join(float& m, float& s, float mo, float so, float c) {
+  const float top = fmaxf(m, mo), base = finite_max(top);
+  s = s * fast_exp2((m - base) * c) + so * fast_exp2((mo - base) * c);
   m = top;
 }
 
-template <typename F>
-__device__ __forceinline__ float block_reduce(float v, float* red, F f) {
-  for (int o = 16; o > 0; o >>= 1) v = f(v, __shfl_xor_sync(0xffffffffu, v, o));
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = red[0];
-  for (int i = 1; i < kWarps; ++i) v = f(v, red[i]);
-  return v;
+// N vectors into a thread's running pair
+template <typename Z, int N>
+__device__ __forceinline__ void take(const uint4 (&v)[N], float& m, float& s, float c) {
+  float top = Vec<Z>::top(v[0]);
+#pragma unroll
+  for (int i = 1; i < N; ++i) top = fmaxf(top, Vec<Z>::top(v[i]));
+  if (top > m) {
+    s *= fast_exp2((m - top) * c);
+    m = top;
+  }
+  const float base = finite_max(m);
+  float sum[2] = {0.0f, 0.0f};
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    float f[Vec<Z>::kN];
+    Vec<Z>::unpack(v[i], f);
+#pragma unroll
+    for (int k = 0; k < Vec<Z>::kN; ++k) sum[k & 1] += fast_exp2((f[k] - base) * c);
+  }
+  s += sum[0] + sum[1];
 }
 
-struct Row {
+struct Shared {
   int32_t ids[MOK_DISTILL_MAX_TOP];
   float p[MOK_DISTILL_MAX_TOP];
-  float red[kWarps], red2[kWarps];
+  float m[kWarps], s[kWarps];
+  float share_m[kMaxShare], share_s[kMaxShare];
+  float loss[kWarps];
+  int any;
 };
 
-// The teacher's list in shared memory; returns the sum of p (1, or 0 for an
-// empty list).  Thread j holds entry j; log_p of its own entry.
-__device__ float load_list(const DistillParams& q, long t, Row& r, float& p, float& log_p) {
-  const int j = threadIdx.x;
+// The entry of thread j < K: its id (-1: left out) and, where asked, the student's logit there.
+template <typename Z>
+__device__ __forceinline__ int entry(const DistillParams& q, long t, const Z* z, bool wanted, float& logit) {
   int id = -1;
-  float v = -INFINITY;
-  if (j < q.K) {
-    id = q.ids[t * q.K + j];
+  logit = 0.0f;
+  if (threadIdx.x < q.K) {
+    id = q.ids[t * q.K + threadIdx.x];
     if (id >= q.V || id < -1) {
       atomicOr(q.hdr + kHdrError, MOK_ERRBIT_BAD_INDEX);
       id = -1;
     }
-    if (id >= 0) v = q.vals[t * q.K + j] * q.inv_tau;
+    if (id >= 0 && wanted) logit = Vec<Z>::value(z[id]);
   }
-  const float top = block_reduce(v, r.red, [](float a, float b) { return fmaxf(a, b); });
-  const float base = top == -INFINITY ? 0.0f : top;
-  const float e = id >= 0 ? expf(v - base) : 0.0f;
-  const float total = block_reduce(e, r.red, [](float a, float b) { return a + b; });
-  p = total > 0.0f || isnan(total) ? e / total : 0.0f;
-  log_p = p > 0.0f ? logf(p) : 0.0f;
-  if (j < q.K) {
-    r.ids[j] = id;
-    r.p[j] = p;
-  }
-  __syncthreads();
-  return total > 0.0f || isnan(total) ? 1.0f : 0.0f;
+  return id;
 }
 
-template <typename Z>
-__global__ void __launch_bounds__(kThreads) distill_forward_kernel(DistillParams q) {
-  __shared__ Row r;
-  const long t = blockIdx.x;
-  const Z* z = static_cast<const Z*>(q.z) + t * q.ldz;
-  float p, log_p;
-  load_list(q, t, r, p, log_p);
-  float m = -INFINITY, s = 0.0f;
-  for (int v = threadIdx.x; v < q.V; v += kThreads) join(m, s, value(z, v) * q.inv_tau, 1.0f);
+// The teacher's probabilities, by one warp.  NaN values make them NaN.
+__device__ __forceinline__ void teacher(const DistillParams& q, long t, Shared& sh, int lane) {
+  float top = -INFINITY;
+  bool nan = false;
+  for (int j = lane; j < q.K; j += 32) {
+    int id = q.ids[t * q.K + j];
+    if (id < 0 || id >= q.V) id = -1;
+    const float v = id >= 0 ? q.vals[t * q.K + j] * q.inv_tau : -INFINITY;
+    sh.ids[j] = id;
+    sh.p[j] = v;
+    nan |= isnan(v);
+    top = fmaxf(top, v);
+  }
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  nan = __any_sync(0xffffffffu, nan);
+  const float base = top == -INFINITY ? 0.0f : top;
+  float total = 0.0f;
+  for (int j = lane; j < q.K; j += 32) {
+    const float e = expf(sh.p[j] - base);  // exp(-inf) = 0 for what is left out
+    sh.p[j] = e;
+    total += e;
+  }
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  const bool any = total > 0.0f || nan || isnan(total);
+  for (int j = lane; j < q.K; j += 32) sh.p[j] = any ? sh.p[j] / total : 0.0f;
+  if (lane == 0) sh.any = any;
+}
+
+// The CTA's pair from its threads', the same in every thread.
+__device__ __forceinline__ void join_block(float& m, float& s, float c, Shared& sh) {
   for (int o = 16; o > 0; o >>= 1) {
     const float mo = __shfl_xor_sync(0xffffffffu, m, o), so = __shfl_xor_sync(0xffffffffu, s, o);
-    join(m, s, mo, so);
+    join(m, s, mo, so, c);
   }
-  __syncthreads();
   if ((threadIdx.x & 31) == 0) {
-    r.red[threadIdx.x >> 5] = m;
-    r.red2[threadIdx.x >> 5] = s;
+    sh.m[threadIdx.x >> 5] = m;
+    sh.s[threadIdx.x >> 5] = s;
   }
   __syncthreads();
-  m = r.red[0];
-  s = r.red2[0];
-  for (int i = 1; i < kWarps; ++i) join(m, s, r.red[i], r.red2[i]);
-  const float lse = m + logf(s);
+  // 16 pairs: every half-warp joins them all
+  static_assert(kWarps == 16, "half a warp holds the warps' pairs");
+  m = sh.m[threadIdx.x & 15];
+  s = sh.s[threadIdx.x & 15];
+  for (int o = 8; o > 0; o >>= 1) {
+    const float mo = __shfl_xor_sync(0xffffffffu, m, o), so = __shfl_xor_sync(0xffffffffu, s, o);
+    join(m, s, mo, so, c);
+  }
+}
+
+// The row's pair from its CTAs', the same in every thread.
+__device__ __forceinline__ void join_shares(float& m, float& s, float c, Shared& sh, int rank, int shares) {
+  if (shares == 1) return;
+  cg::cluster_group cluster = cg::this_cluster();
+  if (threadIdx.x < shares) {
+    *cluster.map_shared_rank(&sh.share_m[rank], threadIdx.x) = m;
+    *cluster.map_shared_rank(&sh.share_s[rank], threadIdx.x) = s;
+  }
+  cluster.sync();
+  m = sh.share_m[0];
+  s = sh.share_s[0];
+  for (int i = 1; i < shares; ++i) join(m, s, sh.share_m[i], sh.share_s[i], c);
+}
+
+// The row's loss and log-sum-exp from its pair (all threads of one CTA; after a
+// barrier that follows teacher()).
+__device__ __forceinline__ void store_loss(const DistillParams& q, long t, Shared& sh, int id, float logit, float m,
+                                           float s) {
+  const float base = finite_max(m), log_s = logf(s);
   float l = 0.0f;
-  if (p > 0.0f || isnan(p)) l = p * (log_p - (value(z, r.ids[threadIdx.x]) * q.inv_tau - lse));
-  l = block_reduce(l, r.red, [](float a, float b) { return a + b; });
+  if (id >= 0) {
+    const float p = sh.p[threadIdx.x];
+    if (p > 0.0f || isnan(p)) l = p * (logf(p) - ((logit - base) * q.inv_tau - log_s));
+  }
+  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  if ((threadIdx.x & 31) == 0) sh.loss[threadIdx.x >> 5] = l;
+  __syncthreads();
   if (threadIdx.x == 0) {
+    for (int w = 1; w < kWarps; ++w) l += sh.loss[w];
     q.loss[t] = l;
-    q.lse[t] = lse;
+    q.lse[t] = fmaf(base, q.inv_tau, log_s);
   }
 }
 
 template <typename Z>
-__global__ void __launch_bounds__(kThreads) distill_backward_kernel(DistillParams q) {
-  __shared__ Row r;
-  const long t = blockIdx.x;
-  const Z* z = static_cast<const Z*>(q.z) + t * q.ldz;
-  Z* dz = static_cast<Z*>(q.dz) + t * q.lddz;
-  float p, log_p;
-  const float any = load_list(q, t, r, p, log_p);
-  if (any == 0.0f) {
-    for (int v = threadIdx.x; v < q.V; v += kThreads) put(dz, v, 0.0f);
-    return;
+__global__ void __launch_bounds__(kThreads) distill_forward_kernel(DistillParams q, int shares) {
+  __shared__ Shared sh;
+  const long t = blockIdx.x / shares;
+  const int rank = blockIdx.x % shares;
+  const float c = q.inv_tau * kLog2e;
+  const RowGrid<Z> row(q.z, t * q.ldz, q.V);
+  float logit;
+  const int id = entry(q, t, row.z, rank == 0, logit);
+  if (rank == 0 && threadIdx.x >= kThreads - 32) teacher(q, t, sh, threadIdx.x & 31);
+  const int v1 = (int)((long)row.vecs * (rank + 1) / shares);
+  float m = -INFINITY, s = 0.0f;
+  constexpr int kAhead = 4;
+  for (int v = (int)((long)row.vecs * rank / shares) + threadIdx.x; v < v1; v += kAhead * kThreads) {
+    uint4 x[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) x[i] = v + i * kThreads < v1 ? row.load(v + i * kThreads) : Vec<Z>::lowest();
+    take<Z, kAhead>(x, m, s, c);
   }
-  const float lse = q.lse_in[t], g = q.dloss[t] * q.inv_tau;
-  // the listed columns: this thread's, if it is the first of its id
-  const int id = threadIdx.x < q.K ? r.ids[threadIdx.x] : -1;
+  join_block(m, s, c, sh);
+  join_shares(m, s, c, sh, rank, shares);
+  if (rank == 0) store_loss(q, t, sh, id, logit, m, s);
+}
+
+// The gradient of a share of a row, NV vectors a thread, and with STEP the
+// sum before it.  Without STEP the shares are CTAs of their own.
+template <typename Z, int NV, bool STEP>
+__global__ void __launch_bounds__(kThreads) distill_gradient_kernel(DistillParams q, int shares) {
+  __shared__ Shared sh;
+  constexpr int kN = Vec<Z>::kN;
+  const long t = blockIdx.x / shares;
+  const int rank = blockIdx.x % shares;
+  const float c = q.inv_tau * kLog2e;
+  const RowGrid<Z> row(q.z, t * q.ldz, q.V), grad(q.dz, t * q.lddz, q.V);
+  const int v0 = (int)((long)row.vecs * rank / shares), v1 = (int)((long)row.vecs * (rank + 1) / shares);
+  uint4 x[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int v = v0 + threadIdx.x + i * kThreads;
+    x[i] = v < v1 ? row.load(v) : Vec<Z>::lowest();
+  }
+  float logit;
+  const int id = entry(q, t, row.z, true, logit);
+  if (threadIdx.x >= kThreads - 32) teacher(q, t, sh, threadIdx.x & 31);
+  // q_v = 2^((z_v - base) c - log_s)
+  float base, log_s;
+  if constexpr (STEP) {
+    float m = -INFINITY, sum = 0.0f;
+    take<Z, NV>(x, m, sum, c);
+    join_block(m, sum, c, sh);
+    // (the logits that other CTAs list are read before the barrier in here, and overwritten after it)
+    join_shares(m, sum, c, sh, rank, shares);
+    base = finite_max(m);
+    log_s = log2f(sum);
+    if (rank == 0) store_loss(q, t, sh, id, logit, m, sum);
+  } else {
+    base = q.lse_in[t] / q.inv_tau;
+    log_s = 0.0f;
+    __syncthreads();
+  }
+  const float g = q.dloss[t] * q.inv_tau;
+  const bool any = sh.any;
+  // a listed column of this share: stored by the first thread that has it
+  bool mine = false;
   float at = 0.0f;
-  bool mine = id >= 0;
-  if (mine) {
-    float sum = 0.0f;
-    for (int j = 0; j < q.K; ++j)
-      if (r.ids[j] == id) {
-        sum += r.p[j];
-        mine = mine && j >= (int)threadIdx.x;
-      }
-    at = g * (expf(value(z, id) * q.inv_tau - lse) - sum);
+  if (id >= 0 && any) {
+    const int v = (id + row.head) / kN;
+    if (v >= v0 && v < v1) {
+      float sum = 0.0f;
+      mine = true;
+      for (int j = 0; j < q.K; ++j)
+        if (sh.ids[j] == id) {
+          sum += sh.p[j];
+          mine = mine && j >= (int)threadIdx.x;
+        }
+      at = g * (fast_exp2(fmaf(logit - base, c, -log_s)) - sum);
+    }
   }
-  __syncthreads();  // the listed logits are read before a gradient in their place overwrites them
-  for (int v = threadIdx.x; v < q.V; v += kThreads) put(dz, v, g * expf(value(z, v) * q.inv_tau - lse));
+  const bool same = row.head == grad.head;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int v = v0 + threadIdx.x + i * kThreads;
+    if (v >= v1) break;
+    float f[kN];
+    Vec<Z>::unpack(x[i], f);
+#pragma unroll
+    for (int k = 0; k < kN; ++k) f[k] = any ? g * fast_exp2(fmaf(f[k] - base, c, -log_s)) : 0.0f;
+    if (same && row.whole(v)) {
+      __stcs(reinterpret_cast<uint4*>(grad.z + row.first(v)), Vec<Z>::pack(f));
+    } else {
+#pragma unroll
+      for (int k = 0; k < kN; ++k) {
+        const int col = row.first(v) + k;
+        if (col >= 0 && col < q.V) grad.z[col] = Vec<Z>::from(f[k]);
+      }
+    }
+  }
   __syncthreads();
-  if (mine) put(dz, id, at);
+  if (mine) grad.z[id] = Vec<Z>::from(at);
+}
+
+int sm_count() {
+  const int n = device_sm_count();
+  return n > 0 ? n : 1;
+}
+
+template <typename... Args>
+cudaError_t launch_shares(void (*kernel)(Args...), long rows, int shares, bool cluster, cudaStream_t st, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(rows * shares));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = shares;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = cluster && shares > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// Vectors of the longest row on its grid, a thread of one CTA.
+template <typename Z>
+int vectors_per_thread(const DistillParams& p) {
+  const int kN = Vec<Z>::kN;
+  const bool aligned = (reinterpret_cast<uintptr_t>(p.z) & 15) == 0 && (p.T == 1 || p.ldz % kN == 0);
+  const long vecs = ((long)p.V + (aligned ? 0 : kN - 1) + kN - 1) / kN;
+  return (int)((vecs + kThreads - 1) / kThreads);
+}
+
+template <typename Z>
+cudaError_t launch_forward(const DistillParams& p, int* launches, cudaStream_t st) {
+  // a CTA a row, or more while SMs are left and each keeps two vectors a thread
+  int shares = 1;
+  const int need = vectors_per_thread<Z>(p);
+  while (shares < kMaxShare && (long)p.T * shares < 2l * sm_count() && need >= 4 * shares) shares *= 2;
+  *launches += 1;
+  return launch_shares(distill_forward_kernel<Z>, p.T, shares, true, st, p, shares);
+}
+
+template <typename Z, bool STEP>
+cudaError_t launch_gradient(const DistillParams& p, int shares, int nv, int* launches, cudaStream_t st) {
+  *launches += 1;
+  if (nv <= 1) return launch_shares(distill_gradient_kernel<Z, 1, STEP>, p.T, shares, STEP, st, p, shares);
+  if (nv <= 2) return launch_shares(distill_gradient_kernel<Z, 2, STEP>, p.T, shares, STEP, st, p, shares);
+  if (nv <= 4) return launch_shares(distill_gradient_kernel<Z, 4, STEP>, p.T, shares, STEP, st, p, shares);
+  return launch_shares(distill_gradient_kernel<Z, 8, STEP>, p.T, shares, STEP, st, p, shares);
 }
 
 template <typename Z>
 cudaError_t launch(DistillMode mode, DistillParams p, int* launches, cudaStream_t st) {
   *launches = 0;
-  if (mode != DISTILL_BACKWARD) {
-    distill_forward_kernel<Z><<<p.T, kThreads, 0, st>>>(p);
-    *launches += 1;
+  if (mode == DISTILL_FORWARD) return launch_forward<Z>(p, launches, st);
+  const int need = vectors_per_thread<Z>(p);
+  if (mode == DISTILL_STEP) {
+    int shares = 1;
+    while (shares < kMaxShare && need > 4 * shares) shares *= 2;
+    while (shares < kMaxShare && (long)p.T * shares < 2l * sm_count() && need >= 2 * shares) shares *= 2;
+    const int nv = (need + shares - 1) / shares;
+    // (a share may hold one vector more than an even split of the longest row)
+    if (nv <= 8) return launch_gradient<Z, true>(p, shares, nv, launches, st);
+    const cudaError_t e = launch_forward<Z>(p, launches, st);
+    if (e != cudaSuccess) return e;
+    p.lse_in = p.lse;
   }
-  if (mode != DISTILL_FORWARD) {
-    if (mode == DISTILL_STEP) p.lse_in = p.lse;
-    distill_backward_kernel<Z><<<p.T, kThreads, 0, st>>>(p);
-    *launches += 1;
-  }
-  return cudaGetLastError();
+  const int shares = (need + 3) / 4;
+  if ((long)p.T * shares > 0x7fffffffl) return cudaErrorInvalidValue;
+  return launch_gradient<Z, false>(p, shares, need < 4 ? need : 4, launches, st);
 }
 
 }  // namespace

@@ -257,3 +257,25 @@ def test_distill_no_rows():
     loss, lse = d.forward(z, ids, vals)
     assert loss.shape == lse.shape == (0,)
     assert d.forward_backward(z, ids, vals, loss)[1].shape == (0, 100)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_distill_rows_of_the_lowest_value(dtype):
+    """Every logit at the type's lowest value: the student is uniform."""
+    require_gpu()
+    from mixture_experts_layer_side_gb300.distill import DistillLoss
+    T, V, K = 3, 9000, 2
+    z = torch.full((T, V), torch.finfo(TYPES[dtype]).min, dtype=TYPES[dtype])
+    z[1, 100:] = -np.inf
+    z[2, 3] = 0.0
+    ids = torch.tensor([[0, 5], [7, 9], [3, -1]]).int()
+    d = DistillLoss(T, V, K)
+    loss, dz = d.forward_backward(z.cuda(), ids.cuda(), torch.zeros(T, K).cuda(), torch.ones(T).cuda())
+    want = [np.log(V) + np.log(0.5), np.log(100) + np.log(0.5), 0.0]
+    np.testing.assert_allclose(loss.cpu().numpy(), want, rtol=1e-5, atol=1e-6)
+    q = torch.zeros((T, V), dtype=torch.float64)
+    q[0], q[1, :100], q[2, 3] = 1 / V, 1 / 100, 1
+    q[0, ids[0].long()] -= 0.5
+    q[1, ids[1].long()] -= 0.5
+    q[2, 3] -= 1
+    assert (dz.double().cpu() - q).abs().max() <= (2.0 ** -8 if dtype == "bf16" else 1e-5) * 0.5
