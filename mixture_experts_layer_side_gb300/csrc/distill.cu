@@ -17,18 +17,21 @@
 //    log2(e) / tau; threads, warps and CTAs join theirs in a fixed tree.
 //  * A row is shared by a cluster of up to 8 CTAs, which exchange their
 //    (m, sum) through distributed shared memory: a few rows still fill the
-//    GPU, and in the step each thread holds its share of the row -- up to 8
-//    vectors -- in registers between the sum and the gradient.  Several CTAs
-//    an SM are in different phases, so loads and stores overlap.
+//    GPU.  In the step a CTA brings its share, 32 KB where eight are enough,
+//    to shared memory with bulk copies, where it stays between the sum and the
+//    gradient; seven such CTAs an SM are in different phases, so that loads
+//    and stores overlap.  (Shares held in registers let two CTAs an SM run:
+//    876 us for 4,096 rows of 131,072 bf16.)
 //  * The teacher's list (at most MOK_DISTILL_MAX_TOP entries) is a warp's
 //    work, hidden behind the row's loads.  Listed columns are stored after
 //    the rest of their vectors, by the thread that is the first with that id.
 //
-// Rows too long for the registers (more than 262,144 bf16 or 131,072 f32) take
-// the forward and then the backward.
+// Rows too long for eight CTAs' shared memory (more than about 800,000 bf16)
+// take the forward and then the backward.
 #include <cooperative_groups.h>
 
 #include "distill.cuh"
+#include "tc.cuh"
 
 namespace mok {
 
@@ -36,11 +39,8 @@ namespace cg = cooperative_groups;
 
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
 constexpr int kMaxShare = 8;  // CTAs a row
 constexpr float kLog2e = 1.4426950408889634f;
-static_assert(MOK_DISTILL_MAX_TOP <= kThreads, "one thread an entry of the list");
 
 __device__ __forceinline__ float fast_exp2(float x) {
   float y;
@@ -159,38 +159,31 @@ __device__ __forceinline__ void take(const uint4 (&v)[N], float& m, float& s, fl
   s += sum[0] + sum[1];
 }
 
+template <int WARPS>
 struct Shared {
   int32_t ids[MOK_DISTILL_MAX_TOP];
   float p[MOK_DISTILL_MAX_TOP];
-  float m[kWarps], s[kWarps];
+  float m[WARPS], s[WARPS];
   float share_m[kMaxShare], share_s[kMaxShare];
-  float loss[kWarps];
+  float loss[WARPS];
   int any;
 };
 
-// The entry of thread j < K: its id (-1: left out) and, where asked, the student's logit there.
-template <typename Z>
-__device__ __forceinline__ int entry(const DistillParams& q, long t, const Z* z, bool wanted, float& logit) {
-  int id = -1;
-  logit = 0.0f;
-  if (threadIdx.x < q.K) {
-    id = q.ids[t * q.K + threadIdx.x];
-    if (id >= q.V || id < -1) {
-      atomicOr(q.hdr + kHdrError, MOK_ERRBIT_BAD_INDEX);
-      id = -1;
-    }
-    if (id >= 0 && wanted) logit = Vec<Z>::value(z[id]);
-  }
-  return id;
+// An entry's id, or -1 where it is left out.
+__device__ __forceinline__ int entry_id(const DistillParams& q, long t, int j, bool tell) {
+  const int id = q.ids[t * q.K + j];
+  if (id >= -1 && id < q.V) return id;
+  if (tell) atomicOr(q.hdr + kHdrError, MOK_ERRBIT_BAD_INDEX);
+  return -1;
 }
 
 // The teacher's probabilities, by one warp.  NaN values make them NaN.
-__device__ __forceinline__ void teacher(const DistillParams& q, long t, Shared& sh, int lane) {
+template <int W>
+__device__ __forceinline__ void teacher(const DistillParams& q, long t, Shared<W>& sh, int lane) {
   float top = -INFINITY;
   bool nan = false;
   for (int j = lane; j < q.K; j += 32) {
-    int id = q.ids[t * q.K + j];
-    if (id < 0 || id >= q.V) id = -1;
+    const int id = entry_id(q, t, j, true);
     const float v = id >= 0 ? q.vals[t * q.K + j] * q.inv_tau : -INFINITY;
     sh.ids[j] = id;
     sh.p[j] = v;
@@ -213,7 +206,8 @@ __device__ __forceinline__ void teacher(const DistillParams& q, long t, Shared& 
 }
 
 // The CTA's pair from its threads', the same in every thread.
-__device__ __forceinline__ void join_block(float& m, float& s, float c, Shared& sh) {
+template <int W>
+__device__ __forceinline__ void join_block(float& m, float& s, float c, Shared<W>& sh) {
   for (int o = 16; o > 0; o >>= 1) {
     const float mo = __shfl_xor_sync(0xffffffffu, m, o), so = __shfl_xor_sync(0xffffffffu, s, o);
     join(m, s, mo, so, c);
@@ -223,18 +217,19 @@ __device__ __forceinline__ void join_block(float& m, float& s, float c, Shared& 
     sh.s[threadIdx.x >> 5] = s;
   }
   __syncthreads();
-  // 16 pairs: every half-warp joins them all
-  static_assert(kWarps == 16, "half a warp holds the warps' pairs");
-  m = sh.m[threadIdx.x & 15];
-  s = sh.s[threadIdx.x & 15];
-  for (int o = 8; o > 0; o >>= 1) {
+  // W lanes of every warp join the warps' pairs
+  static_assert(W <= 32 && (W & (W - 1)) == 0, "a group of lanes holds the warps' pairs");
+  m = sh.m[threadIdx.x & (W - 1)];
+  s = sh.s[threadIdx.x & (W - 1)];
+  for (int o = W / 2; o > 0; o >>= 1) {
     const float mo = __shfl_xor_sync(0xffffffffu, m, o), so = __shfl_xor_sync(0xffffffffu, s, o);
     join(m, s, mo, so, c);
   }
 }
 
 // The row's pair from its CTAs', the same in every thread.
-__device__ __forceinline__ void join_shares(float& m, float& s, float c, Shared& sh, int rank, int shares) {
+template <int W>
+__device__ __forceinline__ void join_shares(float& m, float& s, float c, Shared<W>& sh, int rank, int shares) {
   if (shares == 1) return;
   cg::cluster_group cluster = cg::this_cluster();
   if (threadIdx.x < shares) {
@@ -249,34 +244,48 @@ __device__ __forceinline__ void join_shares(float& m, float& s, float c, Shared&
 
 // The row's loss and log-sum-exp from its pair (all threads of one CTA; after a
 // barrier that follows teacher()).
-__device__ __forceinline__ void store_loss(const DistillParams& q, long t, Shared& sh, int id, float logit, float m,
+template <typename Z, int W>
+__device__ __forceinline__ void store_loss(const DistillParams& q, long t, Shared<W>& sh, const Z* logits, float m,
                                            float s) {
   const float base = finite_max(m), log_s = logf(s);
   float l = 0.0f;
-  if (id >= 0) {
-    const float p = sh.p[threadIdx.x];
-    if (p > 0.0f || isnan(p)) l = p * (logf(p) - ((logit - base) * q.inv_tau - log_s));
+  for (int j = threadIdx.x; j < q.K; j += W * 32) {
+    const float p = sh.p[j];
+    if (p > 0.0f || isnan(p)) l += p * (logf(p) - ((Vec<Z>::value(logits[j]) - base) * q.inv_tau - log_s));
   }
   for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
   if ((threadIdx.x & 31) == 0) sh.loss[threadIdx.x >> 5] = l;
   __syncthreads();
   if (threadIdx.x == 0) {
-    for (int w = 1; w < kWarps; ++w) l += sh.loss[w];
+    for (int w = 1; w < W; ++w) l += sh.loss[w];
     q.loss[t] = l;
-    q.lse[t] = fmaf(base, q.inv_tau, log_s);
+    if (q.lse) q.lse[t] = fmaf(base, q.inv_tau, log_s);
   }
 }
 
+// The student's logits at the listed columns, while the row still holds them.
+template <typename Z>
+__device__ __forceinline__ void read_listed(const DistillParams& q, long t, const Z* z, Z* logits, int threads) {
+  for (int j = threadIdx.x; j < q.K; j += threads) {
+    const int id = entry_id(q, t, j, false);
+    if (id >= 0) logits[j] = z[id];
+  }
+}
+
+constexpr int kThreads = 512;
+
 template <typename Z>
 __global__ void __launch_bounds__(kThreads) distill_forward_kernel(DistillParams q, int shares) {
-  __shared__ Shared sh;
+  __shared__ Shared<kThreads / 32> sh;
+  __shared__ Z logits[MOK_DISTILL_MAX_TOP];
   const long t = blockIdx.x / shares;
   const int rank = blockIdx.x % shares;
   const float c = q.inv_tau * kLog2e;
   const RowGrid<Z> row(q.z, t * q.ldz, q.V);
-  float logit;
-  const int id = entry(q, t, row.z, rank == 0, logit);
-  if (rank == 0 && threadIdx.x >= kThreads - 32) teacher(q, t, sh, threadIdx.x & 31);
+  if (rank == 0) {
+    read_listed(q, t, row.z, logits, kThreads);
+    if (threadIdx.x >= kThreads - 32) teacher(q, t, sh, threadIdx.x & 31);
+  }
   const int v1 = (int)((long)row.vecs * (rank + 1) / shares);
   float m = -INFINITY, s = 0.0f;
   constexpr int kAhead = 4;
@@ -288,68 +297,80 @@ __global__ void __launch_bounds__(kThreads) distill_forward_kernel(DistillParams
   }
   join_block(m, s, c, sh);
   join_shares(m, s, c, sh, rank, shares);
-  if (rank == 0) store_loss(q, t, sh, id, logit, m, s);
+  if (rank == 0) store_loss(q, t, sh, logits, m, s);
 }
 
-// The gradient of a share of a row, NV vectors a thread, and with STEP the
-// sum before it.  Without STEP the shares are CTAs of their own.
-template <typename Z, int NV, bool STEP>
-__global__ void __launch_bounds__(kThreads) distill_gradient_kernel(DistillParams q, int shares) {
-  __shared__ Shared sh;
+// The gradient of a share of a row, and with STEP the sum before it.  Without
+// STEP the shares are CTAs of their own.  Shared memory: the share's vectors.
+constexpr int kGradThreads = 256;
+constexpr int kPieces = 4;  // copies of a share, so that the sum begins with the first
+
+template <typename Z, bool STEP>
+__global__ void __launch_bounds__(kGradThreads, 7) distill_gradient_kernel(DistillParams q, int shares) {
+  extern __shared__ __align__(128) uint8_t share_smem[];
+  __shared__ Shared<kGradThreads / 32> sh;
+  __shared__ Z logits[MOK_DISTILL_MAX_TOP];
+  __shared__ uint64_t full[kPieces];
   constexpr int kN = Vec<Z>::kN;
+  uint4* x = reinterpret_cast<uint4*>(share_smem);
   const long t = blockIdx.x / shares;
   const int rank = blockIdx.x % shares;
   const float c = q.inv_tau * kLog2e;
   const RowGrid<Z> row(q.z, t * q.ldz, q.V), grad(q.dz, t * q.lddz, q.V);
-  const int v0 = (int)((long)row.vecs * rank / shares), v1 = (int)((long)row.vecs * (rank + 1) / shares);
-  uint4 x[NV];
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int v = v0 + threadIdx.x + i * kThreads;
-    x[i] = v < v1 ? row.load(v) : Vec<Z>::lowest();
+  const int v0 = (int)((long)row.vecs * rank / shares), n = (int)((long)row.vecs * (rank + 1) / shares) - v0;
+  // bulk copies take whole vectors; a part-filled one at the row's ends goes by hand
+  const int lead = n > 0 && !row.whole(v0) ? 1 : 0, tail = n > lead && !row.whole(v0 + n - 1) ? 1 : 0;
+  const int whole = n - lead - tail, piece = (whole + kPieces - 1) / kPieces;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kPieces; ++i) mbar_init(&full[i], 1);
+    fence_mbar_init();
+    for (int i = 0; i < kPieces; ++i) {
+      const int at = i * piece, len = max(0, min(piece, whole - at));
+      mbar_arrive_expect_tx(&full[i], len * 16);
+      if (len) bulk_load(x + lead + at, row.z + row.first(v0 + lead + at), len * 16, &full[i]);
+    }
   }
-  float logit;
-  const int id = entry(q, t, row.z, true, logit);
-  if (threadIdx.x >= kThreads - 32) teacher(q, t, sh, threadIdx.x & 31);
+  if (lead && threadIdx.x == 32) x[0] = row.load(v0);
+  if (tail && threadIdx.x == 64) x[n - 1] = row.load(v0 + n - 1);
+  read_listed(q, t, row.z, logits, kGradThreads);
+  if (threadIdx.x >= kGradThreads - 32) teacher(q, t, sh, threadIdx.x & 31);
+  __syncthreads();
+  // the copies always arrive (the limit is there for what no one foresaw: the sum would be of other values)
+  auto arrived = [&](int i) { return mbar_drain(&full[i], 0, kWaitLimitNs); };
+  bool fine = true;
+
   // q_v = 2^((z_v - base) c - log_s)
   float base, log_s;
   if constexpr (STEP) {
     float m = -INFINITY, sum = 0.0f;
-    take<Z, NV>(x, m, sum, c);
+    for (int i = 0; i < kPieces; ++i) {
+      fine &= arrived(i);
+      // piece i, with the vectors that went by hand beside the first and the last
+      const int b = i == 0 ? 0 : lead + i * piece, e = i == kPieces - 1 ? n : min(n, lead + (i + 1) * piece);
+      constexpr int kAhead = 2;
+      for (int v = b + threadIdx.x; v < e; v += kAhead * kGradThreads) {
+        uint4 y[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) y[k] = v + k * kGradThreads < e ? x[v + k * kGradThreads] : Vec<Z>::lowest();
+        take<Z, kAhead>(y, m, sum, c);
+      }
+    }
     join_block(m, sum, c, sh);
     // (the logits that other CTAs list are read before the barrier in here, and overwritten after it)
     join_shares(m, sum, c, sh, rank, shares);
     base = finite_max(m);
     log_s = log2f(sum);
-    if (rank == 0) store_loss(q, t, sh, id, logit, m, sum);
+    if (rank == 0) store_loss(q, t, sh, logits, m, sum);
   } else {
+    for (int i = 0; i < kPieces; ++i) fine &= arrived(i);
     base = q.lse_in[t] / q.inv_tau;
     log_s = 0.0f;
-    __syncthreads();
   }
+  if (!fine && threadIdx.x == 0) atomicOr(q.hdr + kHdrError, MOK_ERRBIT_TIMEOUT);
   const float g = q.dloss[t] * q.inv_tau;
-  const bool any = sh.any;
-  // a listed column of this share: stored by the first thread that has it
-  bool mine = false;
-  float at = 0.0f;
-  if (id >= 0 && any) {
-    const int v = (id + row.head) / kN;
-    if (v >= v0 && v < v1) {
-      float sum = 0.0f;
-      mine = true;
-      for (int j = 0; j < q.K; ++j)
-        if (sh.ids[j] == id) {
-          sum += sh.p[j];
-          mine = mine && j >= (int)threadIdx.x;
-        }
-      at = g * (fast_exp2(fmaf(logit - base, c, -log_s)) - sum);
-    }
-  }
-  const bool same = row.head == grad.head;
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int v = v0 + threadIdx.x + i * kThreads;
-    if (v >= v1) break;
+  const bool any = sh.any, same = row.head == grad.head;
+  for (int i = threadIdx.x; i < n; i += kGradThreads) {
+    const int v = v0 + i;
     float f[kN];
     Vec<Z>::unpack(x[i], f);
 #pragma unroll
@@ -364,8 +385,22 @@ __global__ void __launch_bounds__(kThreads) distill_gradient_kernel(DistillParam
       }
     }
   }
+  if (!any) return;
+  // the listed columns of this share, each stored by the first entry that has it
   __syncthreads();
-  if (mine) grad.z[id] = Vec<Z>::from(at);
+  for (int j = threadIdx.x; j < q.K; j += kGradThreads) {
+    const int id = sh.ids[j];
+    const int v = (id + row.head) / kN;
+    if (id < 0 || v < v0 || v >= v0 + n) continue;
+    float sum = 0.0f;
+    bool mine = true;
+    for (int i = 0; i < q.K; ++i)
+      if (sh.ids[i] == id) {
+        sum += sh.p[i];
+        mine = mine && i >= j;
+      }
+    if (mine) grad.z[id] = Vec<Z>::from(g * (fast_exp2(fmaf(Vec<Z>::value(logits[j]) - base, c, -log_s)) - sum));
+  }
 }
 
 int sm_count() {
@@ -374,10 +409,13 @@ int sm_count() {
 }
 
 template <typename... Args>
-cudaError_t launch_shares(void (*kernel)(Args...), long rows, int shares, bool cluster, cudaStream_t st, Args... args) {
+cudaError_t launch_shares(void (*kernel)(Args...), long rows, int shares, bool cluster, int threads, size_t smem,
+                          cudaStream_t st, Args... args) {
+  if (rows * shares > 0x7fffffffl) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(rows * shares));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeClusterDimension;
@@ -388,53 +426,55 @@ cudaError_t launch_shares(void (*kernel)(Args...), long rows, int shares, bool c
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-// Vectors of the longest row on its grid, a thread of one CTA.
+// Vectors of the longest row on its grid.
 template <typename Z>
-int vectors_per_thread(const DistillParams& p) {
+long row_vectors(const DistillParams& p) {
   const int kN = Vec<Z>::kN;
   const bool aligned = (reinterpret_cast<uintptr_t>(p.z) & 15) == 0 && (p.T == 1 || p.ldz % kN == 0);
-  const long vecs = ((long)p.V + (aligned ? 0 : kN - 1) + kN - 1) / kN;
-  return (int)((vecs + kThreads - 1) / kThreads);
+  return ((long)p.V + (aligned ? 0 : kN - 1) + kN - 1) / kN;
 }
 
 template <typename Z>
 cudaError_t launch_forward(const DistillParams& p, int* launches, cudaStream_t st) {
   // a CTA a row, or more while SMs are left and each keeps two vectors a thread
   int shares = 1;
-  const int need = vectors_per_thread<Z>(p);
-  while (shares < kMaxShare && (long)p.T * shares < 2l * sm_count() && need >= 4 * shares) shares *= 2;
+  const long vecs = row_vectors<Z>(p);
+  while (shares < kMaxShare && (long)p.T * shares < 2l * sm_count() && vecs >= 4l * kThreads * shares) shares *= 2;
   *launches += 1;
-  return launch_shares(distill_forward_kernel<Z>, p.T, shares, true, st, p, shares);
+  return launch_shares(distill_forward_kernel<Z>, p.T, shares, true, kThreads, 0, st, p, shares);
 }
 
+constexpr long kShareVecs = 2048;   // 32 KB: seven CTAs an SM
+constexpr long kMostVecs = 13312;   // 208 KB: what a CTA can hold at most
+
 template <typename Z, bool STEP>
-cudaError_t launch_gradient(const DistillParams& p, int shares, int nv, int* launches, cudaStream_t st) {
+cudaError_t launch_gradient(const DistillParams& p, int shares, int* launches, cudaStream_t st) {
+  const long vecs = row_vectors<Z>(p);
+  const size_t smem = (size_t)((vecs + shares - 1) / shares) * 16;
+  auto kernel = distill_gradient_kernel<Z, STEP>;
+  if (smem > 32 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostVecs * 16);
+    if (e != cudaSuccess) return e;
+  }
   *launches += 1;
-  if (nv <= 1) return launch_shares(distill_gradient_kernel<Z, 1, STEP>, p.T, shares, STEP, st, p, shares);
-  if (nv <= 2) return launch_shares(distill_gradient_kernel<Z, 2, STEP>, p.T, shares, STEP, st, p, shares);
-  if (nv <= 4) return launch_shares(distill_gradient_kernel<Z, 4, STEP>, p.T, shares, STEP, st, p, shares);
-  return launch_shares(distill_gradient_kernel<Z, 8, STEP>, p.T, shares, STEP, st, p, shares);
+  return launch_shares(kernel, p.T, shares, STEP, kGradThreads, smem, st, p, shares);
 }
 
 template <typename Z>
 cudaError_t launch(DistillMode mode, DistillParams p, int* launches, cudaStream_t st) {
   *launches = 0;
   if (mode == DISTILL_FORWARD) return launch_forward<Z>(p, launches, st);
-  const int need = vectors_per_thread<Z>(p);
+  const long vecs = row_vectors<Z>(p);
   if (mode == DISTILL_STEP) {
     int shares = 1;
-    while (shares < kMaxShare && need > 4 * shares) shares *= 2;
-    while (shares < kMaxShare && (long)p.T * shares < 2l * sm_count() && need >= 2 * shares) shares *= 2;
-    const int nv = (need + shares - 1) / shares;
-    // (a share may hold one vector more than an even split of the longest row)
-    if (nv <= 8) return launch_gradient<Z, true>(p, shares, nv, launches, st);
+    while (shares < kMaxShare && vecs > kShareVecs * shares) shares *= 2;
+    while (shares < kMaxShare && (long)p.T * shares < 2l * sm_count() && vecs >= 2l * kGradThreads * shares) shares *= 2;
+    if (vecs <= kMostVecs * shares) return launch_gradient<Z, true>(p, shares, launches, st);
     const cudaError_t e = launch_forward<Z>(p, launches, st);
     if (e != cudaSuccess) return e;
     p.lse_in = p.lse;
   }
-  const int shares = (need + 3) / 4;
-  if ((long)p.T * shares > 0x7fffffffl) return cudaErrorInvalidValue;
-  return launch_gradient<Z, false>(p, shares, need < 4 ? need : 4, launches, st);
+  return launch_gradient<Z, false>(p, (int)((vecs + kShareVecs - 1) / kShareVecs), launches, st);
 }
 
 }  // namespace
