@@ -1647,6 +1647,7 @@ mok_status distill(DistillMode mode, int32_t T, int32_t V, int32_t K, mok_dtype 
   p.ldz = ldz;
   p.ids = ids;
   p.vals = vals;
+  p.tau = tau;
   p.inv_tau = 1.0f / tau;
   p.lse_in = lse_in;
   p.dloss = dloss;

@@ -7,24 +7,28 @@
 //   dz_v = (dloss / tau) (q_v - sum_{j: id_j = v} p_j)
 //
 // An entry of p_j = 0 adds nothing; a row whose list is empty has loss 0 and
-// gradient 0.  Every operation is bound by the row's bytes: the forward reads
-// it once, the backward reads and writes it once, and the step, which needs
-// the row's sum before it can write, keeps the row on the chip in between:
+// gradient 0.  Every operation is bound by the row's bytes -- the forward
+// reads it once, the backward reads and writes it once, and the step, which
+// needs the row's sum before it can write, keeps the row on the chip in
+// between -- with the instructions of an element close behind:
 //
+//  * A sum is kept as (m, s), s * 2^(m c), m the largest logit so far and c =
+//    log2(e) / tau; a term is 2^((z - m) c) -- the difference first, so that
+//    the largest term is 1 exactly and rows of the type's lowest value stay
+//    finite.  Differences, products and sums go two at a time (f32x2).
+//    Threads, warps and CTAs join their pairs in a fixed tree.
 //  * Rows are read in 16-byte vectors of the address grid (a row of any
 //    alignment has at most one part-filled vector at each end).
-//  * Each thread keeps a running maximum m and sum of exp2((z - m) c), c =
-//    log2(e) / tau; threads, warps and CTAs join theirs in a fixed tree.
-//  * A row is shared by a cluster of up to 8 CTAs, which exchange their
-//    (m, sum) through distributed shared memory: a few rows still fill the
-//    GPU.  In the step a CTA brings its share, 32 KB where eight are enough,
-//    to shared memory with bulk copies, where it stays between the sum and the
-//    gradient; seven such CTAs an SM are in different phases, so that loads
-//    and stores overlap.  (Shares held in registers let two CTAs an SM run:
-//    876 us for 4,096 rows of 131,072 bf16.)
+//  * A row is shared by a cluster of up to 8 CTAs, which exchange their pairs
+//    through distributed shared memory: a few rows still fill the GPU.  In
+//    the step a CTA brings its share, 32 KB where eight are enough, to shared
+//    memory with bulk copies, where it stays between the sum and the gradient;
+//    six such CTAs an SM are in different phases, so that loads and stores
+//    overlap.  (Shares held in registers let two CTAs an SM run: 876 us for
+//    4,096 rows of 131,072 bf16.)
 //  * The teacher's list (at most MOK_DISTILL_MAX_TOP entries) is a warp's
-//    work, hidden behind the row's loads.  Listed columns are stored after
-//    the rest of their vectors, by the thread that is the first with that id.
+//    work, hidden behind the row's copies.  Listed columns are stored after
+//    the rest, by the first entry that has them.
 //
 // Rows too long for eight CTAs' shared memory (more than about 800,000 bf16)
 // take the forward and then the backward.
@@ -48,26 +52,57 @@ __device__ __forceinline__ float fast_exp2(float x) {
   return y;
 }
 
-// Vectors of a type: 16 bytes.
+// ---------------------------------------------------------------- pairs of floats
+struct F2 {
+  uint64_t v;
+};
+__device__ __forceinline__ F2 pair(float lo, float hi) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void split(F2 p, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(p.v));
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 exp2_2(F2 a) {
+  float lo, hi;
+  split(a, lo, hi);
+  return pair(fast_exp2(lo), fast_exp2(hi));
+}
+
+// ---------------------------------------------------------------- vectors of 16 bytes
 template <typename Z>
 struct Vec;
 template <>
 struct Vec<__nv_bfloat16> {
   static constexpr int kN = 8;
-  static __device__ __forceinline__ void unpack(const uint4& v, float (&f)[8]) {
+  static __device__ __forceinline__ void unpack(const uint4& v, F2 (&f)[4]) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      f[2 * i] = __uint_as_float(w[i] << 16);
-      f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
+    for (int i = 0; i < 4; ++i) f[i] = pair(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
   }
-  static __device__ __forceinline__ uint4 pack(const float (&f)[8]) {
+  static __device__ __forceinline__ uint4 pack(const F2 (&f)[4]) {
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-      w[i] = *reinterpret_cast<const uint32_t*>(&h);
+      float lo, hi;
+      split(f[i], lo, hi);
+      w[i] = pack_bf16x2(lo, hi);
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
   }
@@ -78,26 +113,31 @@ struct Vec<__nv_bfloat16> {
   }
   static __device__ __forceinline__ float value(__nv_bfloat16 z) { return __bfloat162float(z); }
   static __device__ __forceinline__ __nv_bfloat16 from(float f) { return __float2bfloat16(f); }
-  static __device__ __forceinline__ uint4 lowest() { return make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u); }
+  static __device__ __forceinline__ uint4 lowest() {
+    return make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u);
+  }
 };
 template <>
 struct Vec<float> {
   static constexpr int kN = 4;
-  static __device__ __forceinline__ void unpack(const uint4& v, float (&f)[4]) {
-    f[0] = __uint_as_float(v.x);
-    f[1] = __uint_as_float(v.y);
-    f[2] = __uint_as_float(v.z);
-    f[3] = __uint_as_float(v.w);
+  static __device__ __forceinline__ void unpack(const uint4& v, F2 (&f)[2]) {
+    f[0] = pair(__uint_as_float(v.x), __uint_as_float(v.y));
+    f[1] = pair(__uint_as_float(v.z), __uint_as_float(v.w));
   }
-  static __device__ __forceinline__ uint4 pack(const float (&f)[4]) {
-    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+  static __device__ __forceinline__ uint4 pack(const F2 (&f)[2]) {
+    float a, b, c, d;
+    split(f[0], a, b);
+    split(f[1], c, d);
+    return make_uint4(__float_as_uint(a), __float_as_uint(b), __float_as_uint(c), __float_as_uint(d));
   }
   static __device__ __forceinline__ float top(const uint4& v) {
     return fmaxf(fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)), fmaxf(__uint_as_float(v.z), __uint_as_float(v.w)));
   }
   static __device__ __forceinline__ float value(float z) { return z; }
   static __device__ __forceinline__ float from(float f) { return f; }
-  static __device__ __forceinline__ uint4 lowest() { return make_uint4(0xFF800000u, 0xFF800000u, 0xFF800000u, 0xFF800000u); }
+  static __device__ __forceinline__ uint4 lowest() {
+    return make_uint4(0xFF800000u, 0xFF800000u, 0xFF800000u, 0xFF800000u);
+  }
 };
 
 // A row on the grid of 16-byte vectors: vector i holds elements
@@ -113,80 +153,116 @@ struct RowGrid {
   }
   __device__ __forceinline__ int first(int i) const { return i * Vec<Z>::kN - head; }
   __device__ __forceinline__ bool whole(int i) const { return first(i) >= 0 && first(i) + Vec<Z>::kN <= V; }
-  // -inf outside the row
-  __device__ __forceinline__ uint4 load(int i) const {
-    if (whole(i)) return __ldcs(reinterpret_cast<const uint4*>(z + first(i)));
+  // a part-filled vector: -inf outside the row
+  __device__ __noinline__ uint4 load_part(int i) const {
     uint4 v = Vec<Z>::lowest();
     Z* e = reinterpret_cast<Z*>(&v);
-#pragma unroll
+#pragma unroll 1
     for (int k = 0; k < Vec<Z>::kN; ++k) {
       const int c = first(i) + k;
       if (c >= 0 && c < V) e[k] = z[c];
     }
     return v;
   }
+  __device__ __noinline__ void store_part(int i, uint4 v) const {
+    const Z* e = reinterpret_cast<const Z*>(&v);
+#pragma unroll 1
+    for (int k = 0; k < Vec<Z>::kN; ++k) {
+      const int c = first(i) + k;
+      if (c >= 0 && c < V) z[c] = e[k];
+    }
+  }
 };
 
-// (m, s) stands for s * 2^(m c); (-inf, 0) for nothing.  Differences are
-// taken before the product with c, so that rows of the type's lowest value
-// stay finite.
-__device__ __forceinline__ float finite_max(float m) { return m == -INFINITY ? 0.0f : m; }
-__device__ __forceinline__ void join(float& m, float& s, float mo, float so, float c) {
-  const float top = fmaxf(m, mo), base = finite_max(top);
-  s = s * fast_exp2((m - base) * c) + so * fast_exp2((mo - base) * c);
-  m = top;
-}
+// ---------------------------------------------------------------- sums
+struct Sum {
+  float m, s;  // s * 2^(m c); (-inf, 0) for nothing
+};
 
-// N vectors into a thread's running pair
+// 2^((from - to) c) for from <= to; 0 for a sum of nothing
+__device__ __forceinline__ float rescale(float from, float to, float c) {
+  return from == -INFINITY ? 0.0f : fast_exp2((from - to) * c);
+}
+__device__ __forceinline__ float finite_max(float m) { return m == -INFINITY ? 0.0f : m; }
+
+// N vectors into a thread's sum
 template <typename Z, int N>
-__device__ __forceinline__ void take(const uint4 (&v)[N], float& m, float& s, float c) {
+__device__ __forceinline__ void take(const uint4 (&v)[N], Sum& sum, float c) {
   float top = Vec<Z>::top(v[0]);
 #pragma unroll
   for (int i = 1; i < N; ++i) top = fmaxf(top, Vec<Z>::top(v[i]));
-  if (top > m) {
-    s *= fast_exp2((m - top) * c);
-    m = top;
+  if (top > sum.m) {
+    sum.s *= rescale(sum.m, top, c);
+    sum.m = top;
   }
-  const float base = finite_max(m);
-  float sum[2] = {0.0f, 0.0f};
+  const float base = -finite_max(sum.m);
+  const F2 b2 = pair(base, base), c2 = pair(c, c);
+  F2 acc[2] = {pair(0.0f, 0.0f), pair(0.0f, 0.0f)};
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    float f[Vec<Z>::kN];
+    F2 f[Vec<Z>::kN / 2];
     Vec<Z>::unpack(v[i], f);
 #pragma unroll
-    for (int k = 0; k < Vec<Z>::kN; ++k) sum[k & 1] += fast_exp2((f[k] - base) * c);
+    for (int k = 0; k < Vec<Z>::kN / 2; ++k) acc[k & 1] = add2(acc[k & 1], exp2_2(mul2(add2(f[k], b2), c2)));
   }
-  s += sum[0] + sum[1];
+  float a, b;
+  split(add2(acc[0], acc[1]), a, b);
+  sum.s += a + b;
 }
 
+template <int WIDTH>
+__device__ __forceinline__ void join_lanes(Sum& a, float c) {
+  float top = a.m;
+#pragma unroll
+  for (int o = WIDTH / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  a.s *= a.m == top ? 1.0f : rescale(a.m, top, c);  // (a NaN sum stays one: 0 * NaN)
+  a.m = top;
+#pragma unroll
+  for (int o = WIDTH / 2; o > 0; o >>= 1) a.s += __shfl_xor_sync(0xffffffffu, a.s, o);
+}
+
+// ---------------------------------------------------------------- what a CTA shares
 template <int WARPS>
 struct Shared {
-  int32_t ids[MOK_DISTILL_MAX_TOP];
-  float p[MOK_DISTILL_MAX_TOP];
-  float m[WARPS], s[WARPS];
-  float share_m[kMaxShare], share_s[kMaxShare];
+  Sum warp[WARPS];
+  Sum share[kMaxShare];
   float loss[WARPS];
   int any;
 };
 
-// An entry's id, or -1 where it is left out.
-__device__ __forceinline__ int entry_id(const DistillParams& q, long t, int j, bool tell) {
-  const int id = q.ids[t * q.K + j];
-  if (id >= -1 && id < q.V) return id;
-  if (tell) atomicOr(q.hdr + kHdrError, MOK_ERRBIT_BAD_INDEX);
-  return -1;
+// The list, in dynamic shared memory.
+struct List {
+  int32_t* ids;   // [K]
+  float* p;       // [K]
+  float* logits;  // [K] the student's, at the ids
+};
+__host__ __device__ constexpr size_t list_bytes(int K) { return (size_t)K * 12; }
+__device__ __forceinline__ List list_at(uint8_t* smem, int K) {
+  List l;
+  l.ids = reinterpret_cast<int32_t*>(smem);
+  l.p = reinterpret_cast<float*>(l.ids + K);
+  l.logits = l.p + K;
+  return l;
 }
 
-// The teacher's probabilities, by one warp.  NaN values make them NaN.
-template <int W>
-__device__ __forceinline__ void teacher(const DistillParams& q, long t, Shared<W>& sh, int lane) {
+// One warp: the list, the student's logits at it (while the row still holds
+// them) and the teacher's probabilities.  NaN values make them NaN.
+template <typename Z>
+__device__ __forceinline__ int read_list(const DistillParams& q, long t, const Z* z, const List& l, int lane) {
   float top = -INFINITY;
   bool nan = false;
+#pragma unroll 1
   for (int j = lane; j < q.K; j += 32) {
-    const int id = entry_id(q, t, j, true);
-    const float v = id >= 0 ? q.vals[t * q.K + j] * q.inv_tau : -INFINITY;
-    sh.ids[j] = id;
-    sh.p[j] = v;
+    int id = q.ids[t * q.K + j];
+    float v = q.vals[t * q.K + j] * q.inv_tau;
+    if (id < -1 || id >= q.V) {
+      atomicOr(q.hdr + kHdrError, MOK_ERRBIT_BAD_INDEX);
+      id = -1;
+    }
+    if (id < 0) v = -INFINITY;
+    l.ids[j] = id;
+    l.p[j] = v;
+    l.logits[j] = id >= 0 ? Vec<Z>::value(z[id]) : 0.0f;
     nan |= isnan(v);
     top = fmaxf(top, v);
   }
@@ -194,64 +270,48 @@ __device__ __forceinline__ void teacher(const DistillParams& q, long t, Shared<W
   nan = __any_sync(0xffffffffu, nan);
   const float base = top == -INFINITY ? 0.0f : top;
   float total = 0.0f;
+#pragma unroll 1
   for (int j = lane; j < q.K; j += 32) {
-    const float e = expf(sh.p[j] - base);  // exp(-inf) = 0 for what is left out
-    sh.p[j] = e;
+    const float e = expf(l.p[j] - base);  // exp(-inf) = 0 for what is left out
+    l.p[j] = e;
     total += e;
   }
   for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
   const bool any = total > 0.0f || nan || isnan(total);
-  for (int j = lane; j < q.K; j += 32) sh.p[j] = any ? sh.p[j] / total : 0.0f;
-  if (lane == 0) sh.any = any;
+#pragma unroll 1
+  for (int j = lane; j < q.K; j += 32) l.p[j] = any ? l.p[j] / total : 0.0f;
+  return any;
 }
 
-// The CTA's pair from its threads', the same in every thread.
+// The row's sum from the threads' of its CTAs, the same in every thread.
 template <int W>
-__device__ __forceinline__ void join_block(float& m, float& s, float c, Shared<W>& sh) {
-  for (int o = 16; o > 0; o >>= 1) {
-    const float mo = __shfl_xor_sync(0xffffffffu, m, o), so = __shfl_xor_sync(0xffffffffu, s, o);
-    join(m, s, mo, so, c);
-  }
-  if ((threadIdx.x & 31) == 0) {
-    sh.m[threadIdx.x >> 5] = m;
-    sh.s[threadIdx.x >> 5] = s;
-  }
+__device__ __forceinline__ void join_row(Sum& a, float c, Shared<W>& sh, int rank, int shares) {
+  join_lanes<32>(a, c);
+  if ((threadIdx.x & 31) == 0) sh.warp[threadIdx.x >> 5] = a;
   __syncthreads();
-  // W lanes of every warp join the warps' pairs
-  static_assert(W <= 32 && (W & (W - 1)) == 0, "a group of lanes holds the warps' pairs");
-  m = sh.m[threadIdx.x & (W - 1)];
-  s = sh.s[threadIdx.x & (W - 1)];
-  for (int o = W / 2; o > 0; o >>= 1) {
-    const float mo = __shfl_xor_sync(0xffffffffu, m, o), so = __shfl_xor_sync(0xffffffffu, s, o);
-    join(m, s, mo, so, c);
-  }
-}
-
-// The row's pair from its CTAs', the same in every thread.
-template <int W>
-__device__ __forceinline__ void join_shares(float& m, float& s, float c, Shared<W>& sh, int rank, int shares) {
+  static_assert(W <= 32 && (W & (W - 1)) == 0, "a group of lanes holds the warps' sums");
+  a = sh.warp[threadIdx.x & (W - 1)];
+  join_lanes<W>(a, c);
   if (shares == 1) return;
   cg::cluster_group cluster = cg::this_cluster();
-  if (threadIdx.x < shares) {
-    *cluster.map_shared_rank(&sh.share_m[rank], threadIdx.x) = m;
-    *cluster.map_shared_rank(&sh.share_s[rank], threadIdx.x) = s;
-  }
+  if (threadIdx.x < shares) *cluster.map_shared_rank(&sh.share[rank], threadIdx.x) = a;
   cluster.sync();
-  m = sh.share_m[0];
-  s = sh.share_s[0];
-  for (int i = 1; i < shares; ++i) join(m, s, sh.share_m[i], sh.share_s[i], c);
+  const int i = threadIdx.x & (kMaxShare - 1);
+  a.m = -INFINITY;
+  a.s = 0.0f;
+  if (i < shares) a = sh.share[i];
+  join_lanes<kMaxShare>(a, c);
 }
 
-// The row's loss and log-sum-exp from its pair (all threads of one CTA; after a
-// barrier that follows teacher()).
-template <typename Z, int W>
-__device__ __forceinline__ void store_loss(const DistillParams& q, long t, Shared<W>& sh, const Z* logits, float m,
-                                           float s) {
-  const float base = finite_max(m), log_s = logf(s);
+// The row's loss and log-sum-exp from its sum (all threads of one CTA, after a
+// barrier that follows read_list()).
+template <int W>
+__device__ __forceinline__ void store_loss(const DistillParams& q, long t, Shared<W>& sh, const List& list, Sum a) {
+  const float base = finite_max(a.m), log_s = logf(a.s);
   float l = 0.0f;
   for (int j = threadIdx.x; j < q.K; j += W * 32) {
-    const float p = sh.p[j];
-    if (p > 0.0f || isnan(p)) l += p * (logf(p) - ((Vec<Z>::value(logits[j]) - base) * q.inv_tau - log_s));
+    const float p = list.p[j];
+    if (p > 0.0f || isnan(p)) l += p * (logf(p) - ((list.logits[j] - base) * q.inv_tau - log_s));
   }
   for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
   if ((threadIdx.x & 31) == 0) sh.loss[threadIdx.x >> 5] = l;
@@ -259,147 +319,175 @@ __device__ __forceinline__ void store_loss(const DistillParams& q, long t, Share
   if (threadIdx.x == 0) {
     for (int w = 1; w < W; ++w) l += sh.loss[w];
     q.loss[t] = l;
-    if (q.lse) q.lse[t] = fmaf(base, q.inv_tau, log_s);
+    q.lse[t] = fmaf(base, q.inv_tau, log_s);
   }
 }
 
-// The student's logits at the listed columns, while the row still holds them.
-template <typename Z>
-__device__ __forceinline__ void read_listed(const DistillParams& q, long t, const Z* z, Z* logits, int threads) {
-  for (int j = threadIdx.x; j < q.K; j += threads) {
-    const int id = entry_id(q, t, j, false);
-    if (id >= 0) logits[j] = z[id];
-  }
-}
-
-constexpr int kThreads = 512;
+constexpr int kForwardThreads = 512;
 
 template <typename Z>
-__global__ void __launch_bounds__(kThreads) distill_forward_kernel(DistillParams q, int shares) {
-  __shared__ Shared<kThreads / 32> sh;
-  __shared__ Z logits[MOK_DISTILL_MAX_TOP];
+__global__ void __launch_bounds__(kForwardThreads) distill_forward_kernel(DistillParams q, int shares) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ Shared<kForwardThreads / 32> sh;
   const long t = blockIdx.x / shares;
   const int rank = blockIdx.x % shares;
   const float c = q.inv_tau * kLog2e;
   const RowGrid<Z> row(q.z, t * q.ldz, q.V);
-  if (rank == 0) {
-    read_listed(q, t, row.z, logits, kThreads);
-    if (threadIdx.x >= kThreads - 32) teacher(q, t, sh, threadIdx.x & 31);
+  const List list = list_at(smem, q.K);
+  if (rank == 0 && threadIdx.x >= kForwardThreads - 32) read_list(q, t, row.z, list, threadIdx.x & 31);
+  const int v0 = (int)((long)row.vecs * rank / shares), v1 = (int)((long)row.vecs * (rank + 1) / shares);
+  Sum a{-INFINITY, 0.0f};
+  // the part-filled vectors at the row's ends apart
+  const int b = v1 > v0 && !row.whole(v0) ? v0 + 1 : v0, e = v1 > b && !row.whole(v1 - 1) ? v1 - 1 : v1;
+  if ((b > v0 && threadIdx.x == 0) || (e < v1 && threadIdx.x == 32)) {
+    const uint4 x[1] = {row.load_part(threadIdx.x == 0 ? v0 : e)};
+    take<Z, 1>(x, a, c);
   }
-  const int v1 = (int)((long)row.vecs * (rank + 1) / shares);
-  float m = -INFINITY, s = 0.0f;
   constexpr int kAhead = 4;
-  for (int v = (int)((long)row.vecs * rank / shares) + threadIdx.x; v < v1; v += kAhead * kThreads) {
+  for (int v = b + threadIdx.x; v < e; v += kAhead * kForwardThreads) {
     uint4 x[kAhead];
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) x[i] = v + i * kThreads < v1 ? row.load(v + i * kThreads) : Vec<Z>::lowest();
-    take<Z, kAhead>(x, m, s, c);
+    for (int i = 0; i < kAhead; ++i)
+      x[i] = v + i * kForwardThreads < e
+                 ? __ldcs(reinterpret_cast<const uint4*>(row.z + row.first(v + i * kForwardThreads)))
+                 : Vec<Z>::lowest();
+    take<Z, kAhead>(x, a, c);
   }
-  join_block(m, s, c, sh);
-  join_shares(m, s, c, sh, rank, shares);
-  if (rank == 0) store_loss(q, t, sh, logits, m, s);
+  join_row(a, c, sh, rank, shares);
+  if (rank == 0) store_loss(q, t, sh, list, a);
 }
 
 // The gradient of a share of a row, and with STEP the sum before it.  Without
-// STEP the shares are CTAs of their own.  Shared memory: the share's vectors.
-constexpr int kGradThreads = 256;
+// STEP the shares are CTAs of their own.  Shared memory: the share's vectors,
+// then the list.
+constexpr int kGradThreads = 128;
 constexpr int kPieces = 4;  // copies of a share, so that the sum begins with the first
 
 template <typename Z, bool STEP>
-__global__ void __launch_bounds__(kGradThreads, 7) distill_gradient_kernel(DistillParams q, int shares) {
-  extern __shared__ __align__(128) uint8_t share_smem[];
+__global__ void __launch_bounds__(kGradThreads) distill_gradient_kernel(DistillParams q, int shares, int most) {
+  extern __shared__ __align__(128) uint8_t smem[];
   __shared__ Shared<kGradThreads / 32> sh;
-  __shared__ Z logits[MOK_DISTILL_MAX_TOP];
   __shared__ uint64_t full[kPieces];
   constexpr int kN = Vec<Z>::kN;
-  uint4* x = reinterpret_cast<uint4*>(share_smem);
+  uint4* x = reinterpret_cast<uint4*>(smem);
+  const List list = list_at(smem + (size_t)most * 16, q.K);
   const long t = blockIdx.x / shares;
   const int rank = blockIdx.x % shares;
   const float c = q.inv_tau * kLog2e;
   const RowGrid<Z> row(q.z, t * q.ldz, q.V), grad(q.dz, t * q.lddz, q.V);
   const int v0 = (int)((long)row.vecs * rank / shares), n = (int)((long)row.vecs * (rank + 1) / shares) - v0;
-  // bulk copies take whole vectors; a part-filled one at the row's ends goes by hand
-  const int lead = n > 0 && !row.whole(v0) ? 1 : 0, tail = n > lead && !row.whole(v0 + n - 1) ? 1 : 0;
-  const int whole = n - lead - tail, piece = (whole + kPieces - 1) / kPieces;
+  // bulk copies take whole vectors [b, e); a part-filled one at the row's ends goes by hand
+  const int b = n > 0 && !row.whole(v0) ? 1 : 0, e = n > b && !row.whole(v0 + n - 1) ? n - 1 : n;
+  const int piece = (e - b + kPieces - 1) / kPieces;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kPieces; ++i) mbar_init(&full[i], 1);
     fence_mbar_init();
     for (int i = 0; i < kPieces; ++i) {
-      const int at = i * piece, len = max(0, min(piece, whole - at));
+      const int at = b + i * piece, len = max(0, min(piece, e - at));
       mbar_arrive_expect_tx(&full[i], len * 16);
-      if (len) bulk_load(x + lead + at, row.z + row.first(v0 + lead + at), len * 16, &full[i]);
+      if (len) bulk_load(x + at, row.z + row.first(v0 + at), len * 16, &full[i]);
     }
   }
-  if (lead && threadIdx.x == 32) x[0] = row.load(v0);
-  if (tail && threadIdx.x == 64) x[n - 1] = row.load(v0 + n - 1);
-  read_listed(q, t, row.z, logits, kGradThreads);
-  if (threadIdx.x >= kGradThreads - 32) teacher(q, t, sh, threadIdx.x & 31);
+  if (threadIdx.x == 32 && b > 0) x[0] = row.load_part(v0);
+  if (threadIdx.x == 64 && e < n) x[n - 1] = row.load_part(v0 + n - 1);
+  if (threadIdx.x >= kGradThreads - 32) {
+    const int any = read_list(q, t, row.z, list, threadIdx.x & 31);
+    if (threadIdx.x == kGradThreads - 1) sh.any = any;
+  }
   __syncthreads();
-  // the copies always arrive (the limit is there for what no one foresaw: the sum would be of other values)
-  auto arrived = [&](int i) { return mbar_drain(&full[i], 0, kWaitLimitNs); };
   bool fine = true;
+  // the copies always arrive; a wait that gave up all the same is told to the caller
+  auto wait_piece = [&](int i) {
+    if (!mbar_try_wait(&full[i], 0)) fine &= mbar_drain(&full[i], 0, kWaitLimitNs);
+  };
 
-  // q_v = 2^((z_v - base) c - log_s)
-  float base, log_s;
+  // q_v = 2^((z_v - base) c) q_base
+  Sum a{-INFINITY, 0.0f};
+  float base, q_base;
+  const float g = q.dloss[t] * q.inv_tau;
+  const bool any = sh.any;
   if constexpr (STEP) {
-    float m = -INFINITY, sum = 0.0f;
+    if (threadIdx.x == 0 && b > 0) {
+      const uint4 y[1] = {x[0]};
+      take<Z, 1>(y, a, c);
+    }
+    if (threadIdx.x == 32 && e < n) {
+      const uint4 y[1] = {x[n - 1]};
+      take<Z, 1>(y, a, c);
+    }
+#pragma unroll 1
     for (int i = 0; i < kPieces; ++i) {
-      fine &= arrived(i);
-      // piece i, with the vectors that went by hand beside the first and the last
-      const int b = i == 0 ? 0 : lead + i * piece, e = i == kPieces - 1 ? n : min(n, lead + (i + 1) * piece);
-      constexpr int kAhead = 2;
-      for (int v = b + threadIdx.x; v < e; v += kAhead * kGradThreads) {
+      wait_piece(i);
+      const int p1 = min(e, b + (i + 1) * piece);
+      constexpr int kAhead = 4;
+#pragma unroll 1
+      for (int v = b + i * piece + threadIdx.x; v < p1; v += kAhead * kGradThreads) {
         uint4 y[kAhead];
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) y[k] = v + k * kGradThreads < e ? x[v + k * kGradThreads] : Vec<Z>::lowest();
-        take<Z, kAhead>(y, m, sum, c);
+        for (int k = 0; k < kAhead; ++k) y[k] = v + k * kGradThreads < p1 ? x[v + k * kGradThreads] : Vec<Z>::lowest();
+        take<Z, kAhead>(y, a, c);
       }
     }
-    join_block(m, sum, c, sh);
     // (the logits that other CTAs list are read before the barrier in here, and overwritten after it)
-    join_shares(m, sum, c, sh, rank, shares);
-    base = finite_max(m);
-    log_s = log2f(sum);
-    if (rank == 0) store_loss(q, t, sh, logits, m, sum);
+    join_row(a, c, sh, rank, shares);
+    if (rank == 0) store_loss(q, t, sh, list, a);
+    base = finite_max(a.m);
+    q_base = 1.0f / a.s;
   } else {
-    for (int i = 0; i < kPieces; ++i) fine &= arrived(i);
-    base = q.lse_in[t] / q.inv_tau;
-    log_s = 0.0f;
+    for (int i = 0; i < kPieces; ++i) wait_piece(i);
+    // z / tau - lse = (z - lse tau) / tau: base is that logit, q_base what its rounding left
+    const double z0 = (double)q.lse_in[t] * (double)q.tau;
+    base = (float)z0;
+    const float left = isinf(base) ? 0.0f : (float)((double)base - z0);
+    q_base = left == 0.0f ? 1.0f : fast_exp2(left * c);
   }
   if (!fine && threadIdx.x == 0) atomicOr(q.hdr + kHdrError, MOK_ERRBIT_TIMEOUT);
-  const float g = q.dloss[t] * q.inv_tau;
-  const bool any = sh.any, same = row.head == grad.head;
-  for (int i = threadIdx.x; i < n; i += kGradThreads) {
-    const int v = v0 + i;
-    float f[kN];
-    Vec<Z>::unpack(x[i], f);
+
+  const bool same = row.head == grad.head;
+  const float scale = g * q_base;
+  const F2 b2 = pair(-base, -base), c2 = pair(c, c), s2 = pair(scale, scale);
+  auto gradient = [&](const uint4& v) {
+    F2 f[kN / 2];
+    Vec<Z>::unpack(v, f);
 #pragma unroll
-    for (int k = 0; k < kN; ++k) f[k] = any ? g * fast_exp2(fmaf(f[k] - base, c, -log_s)) : 0.0f;
-    if (same && row.whole(v)) {
-      __stcs(reinterpret_cast<uint4*>(grad.z + row.first(v)), Vec<Z>::pack(f));
-    } else {
-#pragma unroll
+    for (int k = 0; k < kN / 2; ++k) f[k] = mul2(s2, exp2_2(mul2(add2(f[k], b2), c2)));
+    return Vec<Z>::pack(f);
+  };
+  if (any && same) {
+    uint4* out = reinterpret_cast<uint4*>(grad.z + row.first(v0 + b));
+#pragma unroll 4
+    for (int i = threadIdx.x; i < e - b; i += kGradThreads) __stcs(out + i, gradient(x[b + i]));
+    if (threadIdx.x == 0 && b > 0) grad.store_part(v0, gradient(x[0]));
+    if (threadIdx.x == 32 && e < n) grad.store_part(v0 + n - 1, gradient(x[n - 1]));
+  } else {
+    // a row without a list, or a gradient of another alignment
+#pragma unroll 1
+    for (int i = threadIdx.x; i < n; i += kGradThreads) {
+      const uint4 v = any ? gradient(x[i]) : make_uint4(0, 0, 0, 0);
+      const Z* w = reinterpret_cast<const Z*>(&v);
       for (int k = 0; k < kN; ++k) {
-        const int col = row.first(v) + k;
-        if (col >= 0 && col < q.V) grad.z[col] = Vec<Z>::from(f[k]);
+        const int col = row.first(v0 + i) + k;
+        if (col >= 0 && col < q.V) grad.z[col] = w[k];
       }
     }
   }
   if (!any) return;
   // the listed columns of this share, each stored by the first entry that has it
   __syncthreads();
+#pragma unroll 1
   for (int j = threadIdx.x; j < q.K; j += kGradThreads) {
-    const int id = sh.ids[j];
+    const int id = list.ids[j];
     const int v = (id + row.head) / kN;
     if (id < 0 || v < v0 || v >= v0 + n) continue;
     float sum = 0.0f;
     bool mine = true;
     for (int i = 0; i < q.K; ++i)
-      if (sh.ids[i] == id) {
-        sum += sh.p[i];
+      if (list.ids[i] == id) {
+        sum += list.p[i];
         mine = mine && i >= j;
       }
-    if (mine) grad.z[id] = Vec<Z>::from(g * (fast_exp2(fmaf(Vec<Z>::value(logits[j]) - base, c, -log_s)) - sum));
+    const float e_j = fast_exp2((list.logits[j] - base) * c);
+    if (mine) grad.z[id] = Vec<Z>::from(g * ((STEP ? e_j / a.s : e_j * q_base) - sum));
   }
 }
 
@@ -412,6 +500,11 @@ template <typename... Args>
 cudaError_t launch_shares(void (*kernel)(Args...), long rows, int shares, bool cluster, int threads, size_t smem,
                           cudaStream_t st, Args... args) {
   if (rows * shares > 0x7fffffffl) return cudaErrorInvalidValue;
+  if (smem > 32 * 1024) {
+    const cudaError_t e =
+        cudaFuncSetAttribute((const void*)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(rows * shares));
   cfg.blockDim = dim3(threads);
@@ -439,25 +532,21 @@ cudaError_t launch_forward(const DistillParams& p, int* launches, cudaStream_t s
   // a CTA a row, or more while SMs are left and each keeps two vectors a thread
   int shares = 1;
   const long vecs = row_vectors<Z>(p);
-  while (shares < kMaxShare && (long)p.T * shares < 2l * sm_count() && vecs >= 4l * kThreads * shares) shares *= 2;
+  while (shares < kMaxShare && (long)p.T * shares < 2l * sm_count() && vecs >= 4l * kForwardThreads * shares)
+    shares *= 2;
   *launches += 1;
-  return launch_shares(distill_forward_kernel<Z>, p.T, shares, true, kThreads, 0, st, p, shares);
+  return launch_shares(distill_forward_kernel<Z>, p.T, shares, true, kForwardThreads, list_bytes(p.K), st, p, shares);
 }
 
-constexpr long kShareVecs = 2048;   // 32 KB: seven CTAs an SM
+constexpr long kShareVecs = 2048;   // 32 KB: six CTAs an SM
 constexpr long kMostVecs = 13312;   // 208 KB: what a CTA can hold at most
 
 template <typename Z, bool STEP>
 cudaError_t launch_gradient(const DistillParams& p, int shares, int* launches, cudaStream_t st) {
-  const long vecs = row_vectors<Z>(p);
-  const size_t smem = (size_t)((vecs + shares - 1) / shares) * 16;
-  auto kernel = distill_gradient_kernel<Z, STEP>;
-  if (smem > 32 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostVecs * 16);
-    if (e != cudaSuccess) return e;
-  }
+  const int most = (int)((row_vectors<Z>(p) + shares - 1) / shares);
   *launches += 1;
-  return launch_shares(kernel, p.T, shares, STEP, kGradThreads, smem, st, p, shares);
+  return launch_shares(distill_gradient_kernel<Z, STEP>, p.T, shares, STEP, kGradThreads,
+                       (size_t)most * 16 + list_bytes(p.K), st, p, shares, most);
 }
 
 template <typename Z>
@@ -468,7 +557,7 @@ cudaError_t launch(DistillMode mode, DistillParams p, int* launches, cudaStream_
   if (mode == DISTILL_STEP) {
     int shares = 1;
     while (shares < kMaxShare && vecs > kShareVecs * shares) shares *= 2;
-    while (shares < kMaxShare && (long)p.T * shares < 2l * sm_count() && vecs >= 2l * kGradThreads * shares) shares *= 2;
+    while (shares < kMaxShare && (long)p.T * shares < 2l * sm_count() && vecs >= 4l * kGradThreads * shares) shares *= 2;
     if (vecs <= kMostVecs * shares) return launch_gradient<Z, true>(p, shares, launches, st);
     const cudaError_t e = launch_forward<Z>(p, launches, st);
     if (e != cudaSuccess) return e;

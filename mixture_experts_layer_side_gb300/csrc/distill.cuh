@@ -11,7 +11,7 @@ struct DistillParams {
   long ldz;
   const int32_t* ids;
   const float* vals;
-  float inv_tau;
+  float tau, inv_tau;
   const float* lse_in;  // backward alone
   const float* dloss;
   float* loss;
