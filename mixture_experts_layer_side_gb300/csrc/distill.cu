@@ -164,15 +164,16 @@ struct RowGrid {
     }
     return v;
   }
-  __device__ __noinline__ void store_part(int i, uint4 v) const {
-    const Z* e = reinterpret_cast<const Z*>(&v);
-#pragma unroll 1
-    for (int k = 0; k < Vec<Z>::kN; ++k) {
-      const int c = first(i) + k;
-      if (c >= 0 && c < V) z[c] = e[k];
-    }
-  }
 };
+
+// The elements of a vector, col the first's, that lie in [0, V).
+template <typename Z>
+__device__ __noinline__ void row_store(Z* z, int V, int col, uint4 v) {
+  const Z* e = reinterpret_cast<const Z*>(&v);
+#pragma unroll 1
+  for (int k = 0; k < Vec<Z>::kN; ++k)
+    if (col + k >= 0 && col + k < V) z[col + k] = e[k];
+}
 
 // ---------------------------------------------------------------- sums
 struct Sum {
@@ -226,7 +227,6 @@ template <int WARPS>
 struct Shared {
   Sum warp[WARPS];
   Sum share[kMaxShare];
-  float loss[WARPS];
   int any;
 };
 
@@ -283,11 +283,12 @@ __device__ __forceinline__ int read_list(const DistillParams& q, long t, const Z
   return any;
 }
 
-// The row's sum from the threads' of its CTAs, the same in every thread.
+// The row's sum from those of the threads of its CTAs, the same in every
+// thread.  The first W warps hold sums; others only take part in the barriers.
 template <int W>
 __device__ __forceinline__ void join_row(Sum& a, float c, Shared<W>& sh, int rank, int shares) {
   join_lanes<32>(a, c);
-  if ((threadIdx.x & 31) == 0) sh.warp[threadIdx.x >> 5] = a;
+  if ((threadIdx.x & 31) == 0 && threadIdx.x < W * 32) sh.warp[threadIdx.x >> 5] = a;
   __syncthreads();
   static_assert(W <= 32 && (W & (W - 1)) == 0, "a group of lanes holds the warps' sums");
   a = sh.warp[threadIdx.x & (W - 1)];
@@ -303,147 +304,143 @@ __device__ __forceinline__ void join_row(Sum& a, float c, Shared<W>& sh, int ran
   join_lanes<kMaxShare>(a, c);
 }
 
-// The row's loss and log-sum-exp from its sum (all threads of one CTA, after a
-// barrier that follows read_list()).
-template <int W>
-__device__ __forceinline__ void store_loss(const DistillParams& q, long t, Shared<W>& sh, const List& list, Sum a) {
+// The row's loss and log-sum-exp from its sum, by the warp that read the list.
+__device__ __forceinline__ void store_loss(const DistillParams& q, long t, const List& list, Sum a, int lane) {
   const float base = finite_max(a.m), log_s = logf(a.s);
   float l = 0.0f;
-  for (int j = threadIdx.x; j < q.K; j += W * 32) {
+#pragma unroll 1
+  for (int j = lane; j < q.K; j += 32) {
     const float p = list.p[j];
     if (p > 0.0f || isnan(p)) l += p * (logf(p) - ((list.logits[j] - base) * q.inv_tau - log_s));
   }
   for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-  if ((threadIdx.x & 31) == 0) sh.loss[threadIdx.x >> 5] = l;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int w = 1; w < W; ++w) l += sh.loss[w];
+  if (lane == 0) {
     q.loss[t] = l;
     q.lse[t] = fmaf(base, q.inv_tau, log_s);
   }
 }
 
-constexpr int kForwardThreads = 512;
+// Both kernels: workers, and a last warp for the list.
+constexpr int kForwardWorkers = 512;
+constexpr int kGradWorkers = 128;
 
 template <typename Z>
-__global__ void __launch_bounds__(kForwardThreads) distill_forward_kernel(DistillParams q, int shares) {
+__global__ void __launch_bounds__(kForwardWorkers + 32) distill_forward_kernel(DistillParams q, int shares, int most) {
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ Shared<kForwardThreads / 32> sh;
+  __shared__ Shared<kForwardWorkers / 32> sh;
   const long t = blockIdx.x / shares;
   const int rank = blockIdx.x % shares;
   const float c = q.inv_tau * kLog2e;
   const RowGrid<Z> row(q.z, t * q.ldz, q.V);
   const List list = list_at(smem, q.K);
-  if (rank == 0 && threadIdx.x >= kForwardThreads - 32) read_list(q, t, row.z, list, threadIdx.x & 31);
-  const int v0 = (int)((long)row.vecs * rank / shares), v1 = (int)((long)row.vecs * (rank + 1) / shares);
   Sum a{-INFINITY, 0.0f};
-  // the part-filled vectors at the row's ends apart
-  const int b = v1 > v0 && !row.whole(v0) ? v0 + 1 : v0, e = v1 > b && !row.whole(v1 - 1) ? v1 - 1 : v1;
-  if ((b > v0 && threadIdx.x == 0) || (e < v1 && threadIdx.x == 32)) {
-    const uint4 x[1] = {row.load_part(threadIdx.x == 0 ? v0 : e)};
-    take<Z, 1>(x, a, c);
-  }
-  constexpr int kAhead = 4;
-  for (int v = b + threadIdx.x; v < e; v += kAhead * kForwardThreads) {
-    uint4 x[kAhead];
+  if (threadIdx.x >= kForwardWorkers) {
+    if (rank == 0) read_list(q, t, row.z, list, threadIdx.x & 31);
+  } else {
+    const int v0 = min(rank * most, row.vecs), v1 = min(v0 + most, row.vecs);
+    // the part-filled vectors at the row's ends apart
+    const int b = v1 > v0 && !row.whole(v0) ? v0 + 1 : v0, e = v1 > b && !row.whole(v1 - 1) ? v1 - 1 : v1;
+    if ((b > v0 && threadIdx.x == 0) || (e < v1 && threadIdx.x == 32)) {
+      const uint4 x[1] = {row.load_part(threadIdx.x == 0 ? v0 : e)};
+      take<Z, 1>(x, a, c);
+    }
+    constexpr int kAhead = 4;
+    const uint4* from = reinterpret_cast<const uint4*>(row.z + row.first(0));
+    for (int v = b + threadIdx.x; v < e; v += kAhead * kForwardWorkers) {
+      uint4 x[kAhead];
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i)
-      x[i] = v + i * kForwardThreads < e
-                 ? __ldcs(reinterpret_cast<const uint4*>(row.z + row.first(v + i * kForwardThreads)))
-                 : Vec<Z>::lowest();
-    take<Z, kAhead>(x, a, c);
+      for (int i = 0; i < kAhead; ++i)
+        x[i] = v + i * kForwardWorkers < e ? __ldcs(from + v + i * kForwardWorkers) : Vec<Z>::lowest();
+      take<Z, kAhead>(x, a, c);
+    }
   }
   join_row(a, c, sh, rank, shares);
-  if (rank == 0) store_loss(q, t, sh, list, a);
+  if (rank == 0 && threadIdx.x >= kForwardWorkers) store_loss(q, t, list, a, threadIdx.x & 31);
 }
 
 // The gradient of a share of a row, and with STEP the sum before it.  Without
 // STEP the shares are CTAs of their own.  Shared memory: the share's vectors,
 // then the list.
-constexpr int kGradThreads = 128;
 constexpr int kPieces = 4;  // copies of a share, so that the sum begins with the first
 
 template <typename Z, bool STEP>
-__global__ void __launch_bounds__(kGradThreads) distill_gradient_kernel(DistillParams q, int shares, int most) {
+__global__ void __launch_bounds__(kGradWorkers + 32) distill_gradient_kernel(DistillParams q, int shares, int most) {
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ Shared<kGradThreads / 32> sh;
+  __shared__ Shared<kGradWorkers / 32> sh;
   __shared__ uint64_t full[kPieces];
   constexpr int kN = Vec<Z>::kN;
   uint4* x = reinterpret_cast<uint4*>(smem);
   const List list = list_at(smem + (size_t)most * 16, q.K);
   const long t = blockIdx.x / shares;
-  const int rank = blockIdx.x % shares;
+  const int rank = blockIdx.x % shares, lane = threadIdx.x & 31;
+  const bool worker = threadIdx.x < kGradWorkers;
   const float c = q.inv_tau * kLog2e;
   const RowGrid<Z> row(q.z, t * q.ldz, q.V), grad(q.dz, t * q.lddz, q.V);
-  const int v0 = (int)((long)row.vecs * rank / shares), n = (int)((long)row.vecs * (rank + 1) / shares) - v0;
+  const int v0 = min(rank * most, row.vecs), n = min(most, row.vecs - v0);
   // bulk copies take whole vectors [b, e); a part-filled one at the row's ends goes by hand
   const int b = n > 0 && !row.whole(v0) ? 1 : 0, e = n > b && !row.whole(v0 + n - 1) ? n - 1 : n;
   const int piece = (e - b + kPieces - 1) / kPieces;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kPieces; ++i) mbar_init(&full[i], 1);
     fence_mbar_init();
+#pragma unroll 1
     for (int i = 0; i < kPieces; ++i) {
       const int at = b + i * piece, len = max(0, min(piece, e - at));
       mbar_arrive_expect_tx(&full[i], len * 16);
       if (len) bulk_load(x + at, row.z + row.first(v0 + at), len * 16, &full[i]);
     }
   }
-  if (threadIdx.x == 32 && b > 0) x[0] = row.load_part(v0);
-  if (threadIdx.x == 64 && e < n) x[n - 1] = row.load_part(v0 + n - 1);
-  if (threadIdx.x >= kGradThreads - 32) {
-    const int any = read_list(q, t, row.z, list, threadIdx.x & 31);
-    if (threadIdx.x == kGradThreads - 1) sh.any = any;
-  }
   __syncthreads();
-  bool fine = true;
-  // the copies always arrive; a wait that gave up all the same is told to the caller
-  auto wait_piece = [&](int i) {
-    if (!mbar_try_wait(&full[i], 0)) fine &= mbar_drain(&full[i], 0, kWaitLimitNs);
-  };
 
-  // q_v = 2^((z_v - base) c) q_base
   Sum a{-INFINITY, 0.0f};
-  float base, q_base;
-  const float g = q.dloss[t] * q.inv_tau;
-  const bool any = sh.any;
-  if constexpr (STEP) {
-    if (threadIdx.x == 0 && b > 0) {
-      const uint4 y[1] = {x[0]};
-      take<Z, 1>(y, a, c);
-    }
-    if (threadIdx.x == 32 && e < n) {
-      const uint4 y[1] = {x[n - 1]};
+  bool fine = true;
+  const bool first_part = threadIdx.x == 32 && b > 0, last_part = threadIdx.x == 64 && e < n;
+  if (!worker) {
+    const int any = read_list(q, t, row.z, list, lane);
+    if (lane == 0) sh.any = any;
+  } else {
+    // a part-filled vector stays with the thread that brings it
+    if (first_part) x[0] = row.load_part(v0);
+    if (last_part) x[n - 1] = row.load_part(v0 + n - 1);
+    if (STEP && (first_part || last_part)) {
+      const uint4 y[1] = {first_part ? x[0] : x[n - 1]};
       take<Z, 1>(y, a, c);
     }
 #pragma unroll 1
     for (int i = 0; i < kPieces; ++i) {
-      wait_piece(i);
+      // the copies always arrive; a wait that gave up all the same is told to the caller
+      if (!mbar_try_wait(&full[i], 0)) fine &= mbar_drain(&full[i], 0, kWaitLimitNs);
+      if (!STEP) continue;
       const int p1 = min(e, b + (i + 1) * piece);
       constexpr int kAhead = 4;
 #pragma unroll 1
-      for (int v = b + i * piece + threadIdx.x; v < p1; v += kAhead * kGradThreads) {
+      for (int v = b + i * piece + threadIdx.x; v < p1; v += kAhead * kGradWorkers) {
         uint4 y[kAhead];
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) y[k] = v + k * kGradThreads < p1 ? x[v + k * kGradThreads] : Vec<Z>::lowest();
+        for (int k = 0; k < kAhead; ++k) y[k] = v + k * kGradWorkers < p1 ? x[v + k * kGradWorkers] : Vec<Z>::lowest();
         take<Z, kAhead>(y, a, c);
       }
     }
+  }
+  if (!fine && lane == 0) atomicOr(q.hdr + kHdrError, MOK_ERRBIT_TIMEOUT);
+
+  // q_v = 2^((z_v - base) c) q_base
+  float base, q_base;
+  if constexpr (STEP) {
     // (the logits that other CTAs list are read before the barrier in here, and overwritten after it)
     join_row(a, c, sh, rank, shares);
-    if (rank == 0) store_loss(q, t, sh, list, a);
     base = finite_max(a.m);
     q_base = 1.0f / a.s;
   } else {
-    for (int i = 0; i < kPieces; ++i) wait_piece(i);
+    __syncthreads();
     // z / tau - lse = (z - lse tau) / tau: base is that logit, q_base what its rounding left
     const double z0 = (double)q.lse_in[t] * (double)q.tau;
     base = (float)z0;
     const float left = isinf(base) ? 0.0f : (float)((double)base - z0);
     q_base = left == 0.0f ? 1.0f : fast_exp2(left * c);
   }
-  if (!fine && threadIdx.x == 0) atomicOr(q.hdr + kHdrError, MOK_ERRBIT_TIMEOUT);
-
-  const bool same = row.head == grad.head;
+  const float g = q.dloss[t] * q.inv_tau;
+  const bool any = sh.any, same = row.head == grad.head;
   const float scale = g * q_base;
   const F2 b2 = pair(-base, -base), c2 = pair(c, c), s2 = pair(scale, scale);
   auto gradient = [&](const uint4& v) {
@@ -453,42 +450,50 @@ __global__ void __launch_bounds__(kGradThreads) distill_gradient_kernel(DistillP
     for (int k = 0; k < kN / 2; ++k) f[k] = mul2(s2, exp2_2(mul2(add2(f[k], b2), c2)));
     return Vec<Z>::pack(f);
   };
-  if (any && same) {
-    uint4* out = reinterpret_cast<uint4*>(grad.z + row.first(v0 + b));
-#pragma unroll 4
-    for (int i = threadIdx.x; i < e - b; i += kGradThreads) __stcs(out + i, gradient(x[b + i]));
-    if (threadIdx.x == 0 && b > 0) grad.store_part(v0, gradient(x[0]));
-    if (threadIdx.x == 32 && e < n) grad.store_part(v0 + n - 1, gradient(x[n - 1]));
-  } else {
-    // a row without a list, or a gradient of another alignment
+  uint32_t mine = 0;  // list warp: its entries that are the first of a column of this share
+  if (!worker) {
+    if (STEP && rank == 0) store_loss(q, t, list, a, lane);
+    if (any) {
 #pragma unroll 1
-    for (int i = threadIdx.x; i < n; i += kGradThreads) {
-      const uint4 v = any ? gradient(x[i]) : make_uint4(0, 0, 0, 0);
-      const Z* w = reinterpret_cast<const Z*>(&v);
-      for (int k = 0; k < kN; ++k) {
-        const int col = row.first(v0 + i) + k;
-        if (col >= 0 && col < q.V) grad.z[col] = w[k];
+      for (int j = lane; j < q.K; j += 32) {
+        const int id = list.ids[j], v = (id + row.head) / kN;
+        if (id < 0 || v < v0 || v >= v0 + n) continue;
+        float sum = 0.0f;
+        bool first = true;
+#pragma unroll 4
+        for (int i = 0; i < q.K; ++i)
+          if (list.ids[i] == id) {
+            sum += list.p[i];
+            first = first && i >= j;
+          }
+        const float e_j = fast_exp2((list.logits[j] - base) * c);
+        list.logits[j] = g * ((STEP ? e_j / a.s : e_j * q_base) - sum);
+        mine |= (uint32_t)first << (j >> 5);
       }
     }
+  } else if (any && same) {
+    uint4* out = reinterpret_cast<uint4*>(grad.z + row.first(v0 + b));
+#pragma unroll 4
+    for (int i = threadIdx.x; i < e - b; i += kGradWorkers) __stcs(out + i, gradient(x[b + i]));
+    if (first_part) row_store(grad.z, q.V, row.first(v0), gradient(x[0]));
+    if (last_part) row_store(grad.z, q.V, row.first(v0 + n - 1), gradient(x[n - 1]));
+  } else {
+    // a row without a list, or a gradient of another alignment
+    if (first_part || last_part) {
+      const int i = first_part ? 0 : n - 1;
+      row_store(grad.z, q.V, row.first(v0 + i), any ? gradient(x[i]) : make_uint4(0, 0, 0, 0));
+    }
+#pragma unroll 1
+    for (int i = b + threadIdx.x; i < e; i += kGradWorkers)
+      row_store(grad.z, q.V, row.first(v0 + i), any ? gradient(x[i]) : make_uint4(0, 0, 0, 0));
   }
   if (!any) return;
-  // the listed columns of this share, each stored by the first entry that has it
+  // the listed columns of this share, over what the rest of their vectors stored there
   __syncthreads();
+  if (!worker)
 #pragma unroll 1
-  for (int j = threadIdx.x; j < q.K; j += kGradThreads) {
-    const int id = list.ids[j];
-    const int v = (id + row.head) / kN;
-    if (id < 0 || v < v0 || v >= v0 + n) continue;
-    float sum = 0.0f;
-    bool mine = true;
-    for (int i = 0; i < q.K; ++i)
-      if (list.ids[i] == id) {
-        sum += list.p[i];
-        mine = mine && i >= j;
-      }
-    const float e_j = fast_exp2((list.logits[j] - base) * c);
-    if (mine) grad.z[id] = Vec<Z>::from(g * ((STEP ? e_j / a.s : e_j * q_base) - sum));
-  }
+    for (int j = lane; j < q.K; j += 32)
+      if ((mine >> (j >> 5)) & 1u) grad.z[list.ids[j]] = Vec<Z>::from(list.logits[j]);
 }
 
 int sm_count() {
@@ -532,10 +537,11 @@ cudaError_t launch_forward(const DistillParams& p, int* launches, cudaStream_t s
   // a CTA a row, or more while SMs are left and each keeps two vectors a thread
   int shares = 1;
   const long vecs = row_vectors<Z>(p);
-  while (shares < kMaxShare && (long)p.T * shares < 2l * sm_count() && vecs >= 4l * kForwardThreads * shares)
+  while (shares < kMaxShare && (long)p.T * shares < 2l * sm_count() && vecs >= 4l * kForwardWorkers * shares)
     shares *= 2;
   *launches += 1;
-  return launch_shares(distill_forward_kernel<Z>, p.T, shares, true, kForwardThreads, list_bytes(p.K), st, p, shares);
+  return launch_shares(distill_forward_kernel<Z>, p.T, shares, true, kForwardWorkers + 32, list_bytes(p.K), st, p,
+                       shares, (int)((vecs + shares - 1) / shares));
 }
 
 constexpr long kShareVecs = 2048;   // 32 KB: six CTAs an SM
@@ -545,7 +551,7 @@ template <typename Z, bool STEP>
 cudaError_t launch_gradient(const DistillParams& p, int shares, int* launches, cudaStream_t st) {
   const int most = (int)((row_vectors<Z>(p) + shares - 1) / shares);
   *launches += 1;
-  return launch_shares(distill_gradient_kernel<Z, STEP>, p.T, shares, STEP, kGradThreads,
+  return launch_shares(distill_gradient_kernel<Z, STEP>, p.T, shares, STEP, kGradWorkers + 32,
                        (size_t)most * 16 + list_bytes(p.K), st, p, shares, most);
 }
 
@@ -557,7 +563,7 @@ cudaError_t launch(DistillMode mode, DistillParams p, int* launches, cudaStream_
   if (mode == DISTILL_STEP) {
     int shares = 1;
     while (shares < kMaxShare && vecs > kShareVecs * shares) shares *= 2;
-    while (shares < kMaxShare && (long)p.T * shares < 2l * sm_count() && vecs >= 4l * kGradThreads * shares) shares *= 2;
+    while (shares < kMaxShare && (long)p.T * shares < 2l * sm_count() && vecs >= 4l * kGradWorkers * shares) shares *= 2;
     if (vecs <= kMostVecs * shares) return launch_gradient<Z, true>(p, shares, launches, st);
     const cudaError_t e = launch_forward<Z>(p, launches, st);
     if (e != cudaSuccess) return e;
