@@ -617,7 +617,7 @@ typedef enum { MOK_TYPE_BF16 = 0, MOK_TYPE_F32 = 1 } mok_dtype;
  *          Any other id outside [0, V) records MOK_ERR_BAD_INDEX and is left out
  *   vals   (device) f32 [T, K]; not read as numbers where the id is left out
  *   dloss  (device) f32 [T]  weight of each row's loss in what is minimised
- *   loss, lse   (device) f32 [T]
+ *   loss, lse   (device) f32 [T]; the step's lse may be NULL
  *   dz     (device) [T, V] of z's type, rows lddz apart; it may be z itself
  *          (same pointer and stride)
  * Entries with p_j = 0 add nothing, whatever q is there.  A row whose list is
@@ -629,8 +629,9 @@ typedef enum { MOK_TYPE_BF16 = 0, MOK_TYPE_F32 = 1 } mok_dtype;
  *   mok_distill_backward  dz from the forward's lse
  *   mok_distill_step      both at once: loss, lse and dz
  * All sums in f32 and in a fixed order.  1 <= K <= MOK_DISTILL_MAX_TOP; T = 0
- * does nothing.  ws: mok_distill_workspace_size() bytes, zeroed once by the
- * caller; its first word holds errors until mok_check.
+ * does nothing.  ws: mok_distill_workspace_size bytes (for at
+ * least this T), its first 256 zeroed once by the caller; its first word holds
+ * errors until mok_check.  Calls that share a workspace must not overlap.
  */
 #define MOK_DISTILL_MAX_TOP 512
 size_t mok_distill_workspace_size(int32_t T, int32_t V, int32_t K);

@@ -402,7 +402,7 @@ def mok_distill_backward(z, ids, vals, tau, lse, dloss, dz, ws, stream=None):
 def mok_distill_step(z, ids, vals, tau, dloss, loss, lse, dz, ws, stream=None):
     (T, V), K = z.shape, ids.shape[1]
     _ok(LIB.mok_distill_step(T, V, K, dtype_of(z), z.data_ptr(), _rows_apart(z), ids.data_ptr(), vals.data_ptr(), tau,
-                             dloss.data_ptr(), loss.data_ptr(), lse.data_ptr(), dz.data_ptr(), _rows_apart(dz),
+                             dloss.data_ptr(), loss.data_ptr(), _ptr(lse), dz.data_ptr(), _rows_apart(dz),
                              ws.data_ptr(), ws.nbytes, _stream(stream)), "mok_distill_step")
 
 

@@ -56,6 +56,17 @@ int device_sm_count() {
   return n;
 }
 
+cudaError_t allow_smem(const void* kernel, size_t bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
+
 bool make_tmap(CUtensorMap* m, CUtensorMapDataType dt, int rank, const void* ptr, const uint64_t* dims,
                const uint64_t* strides_bytes, const uint32_t* box, bool swizzle128) {
   EncodeTiledFn fn = encode_fn();
@@ -1633,8 +1644,8 @@ mok_status distill(DistillMode mode, int32_t T, int32_t V, int32_t K, mok_dtype 
   MOK_TRY(check_dtype(type));
   if (!(tau > 0.0f) || isinf(tau) || isinf(1.0f / tau)) return MOK_ERR_INVALID_ARG;
   if (T == 0) return MOK_OK;
-  if (!z || !ids || !vals || !ws || ldz < V || !aligned_to(z, type)) return MOK_ERR_INVALID_ARG;
-  if (mode != DISTILL_BACKWARD && (!loss || !lse)) return MOK_ERR_INVALID_ARG;
+  if (!z || !ids || !vals || !ws || !aligned16(ws) || ldz < V || !aligned_to(z, type)) return MOK_ERR_INVALID_ARG;
+  if (mode != DISTILL_BACKWARD && (!loss || (!lse && mode == DISTILL_FORWARD))) return MOK_ERR_INVALID_ARG;
   if (mode == DISTILL_BACKWARD && !lse_in) return MOK_ERR_INVALID_ARG;
   if (mode != DISTILL_FORWARD && (!dloss || !dz || lddz < V || !aligned_to(dz, type))) return MOK_ERR_INVALID_ARG;
   if (ws_bytes < mok_distill_workspace_size(T, V, K)) return MOK_ERR_WORKSPACE_TOO_SMALL;
@@ -1656,6 +1667,7 @@ mok_status distill(DistillMode mode, int32_t T, int32_t V, int32_t K, mok_dtype 
   p.dz = dz;
   p.lddz = lddz;
   p.hdr = static_cast<int32_t*>(ws);
+  p.lse_scratch = reinterpret_cast<float*>(p.hdr + kHeaderWords);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   Phase ph(MOK_PHASE_DISTILL, st, 0);
   int launches = 0;
@@ -1667,7 +1679,7 @@ mok_status distill(DistillMode mode, int32_t T, int32_t V, int32_t K, mok_dtype 
 }  // namespace
 
 size_t mok_distill_workspace_size(int32_t T, int32_t V, int32_t K) {
-  return check_distill_sizes(T, V, K) == MOK_OK ? kHeaderWords * 4 : 0;
+  return check_distill_sizes(T, V, K) == MOK_OK ? align256(kHeaderWords * 4 + (size_t)T * 4) : 0;
 }
 
 mok_status mok_distill_forward(int32_t T, int32_t V, int32_t K, mok_dtype type, const void* z, int64_t ldz,

@@ -316,7 +316,7 @@ __device__ __forceinline__ void store_loss(const DistillParams& q, long t, const
   for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
   if (lane == 0) {
     q.loss[t] = l;
-    q.lse[t] = fmaf(base, q.inv_tau, log_s);
+    if (q.lse) q.lse[t] = fmaf(base, q.inv_tau, log_s);
   }
 }
 
@@ -505,11 +505,6 @@ template <typename... Args>
 cudaError_t launch_shares(void (*kernel)(Args...), long rows, int shares, bool cluster, int threads, size_t smem,
                           cudaStream_t st, Args... args) {
   if (rows * shares > 0x7fffffffl) return cudaErrorInvalidValue;
-  if (smem > 32 * 1024) {
-    const cudaError_t e =
-        cudaFuncSetAttribute((const void*)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(rows * shares));
   cfg.blockDim = dim3(threads);
@@ -550,6 +545,10 @@ constexpr long kMostVecs = 13312;   // 208 KB: what a CTA can hold at most
 template <typename Z, bool STEP>
 cudaError_t launch_gradient(const DistillParams& p, int shares, int* launches, cudaStream_t st) {
   const int most = (int)((row_vectors<Z>(p) + shares - 1) / shares);
+  static std::atomic<uint64_t> allowed{0};
+  const cudaError_t e = allow_smem((const void*)distill_gradient_kernel<Z, STEP>,
+                                   kMostVecs * 16 + list_bytes(MOK_DISTILL_MAX_TOP), allowed);
+  if (e != cudaSuccess) return e;
   *launches += 1;
   return launch_shares(distill_gradient_kernel<Z, STEP>, p.T, shares, STEP, kGradWorkers + 32,
                        (size_t)most * 16 + list_bytes(p.K), st, p, shares, most);
@@ -565,6 +564,7 @@ cudaError_t launch(DistillMode mode, DistillParams p, int* launches, cudaStream_
     while (shares < kMaxShare && vecs > kShareVecs * shares) shares *= 2;
     while (shares < kMaxShare && (long)p.T * shares < 2l * sm_count() && vecs >= 4l * kGradWorkers * shares) shares *= 2;
     if (vecs <= kMostVecs * shares) return launch_gradient<Z, true>(p, shares, launches, st);
+    if (!p.lse) p.lse = p.lse_scratch;
     const cudaError_t e = launch_forward<Z>(p, launches, st);
     if (e != cudaSuccess) return e;
     p.lse_in = p.lse;

@@ -15,7 +15,8 @@ struct DistillParams {
   const float* lse_in;  // backward alone
   const float* dloss;
   float* loss;
-  float* lse;
+  float* lse;          // may be null in the step
+  float* lse_scratch;  // [T]
   void* dz;        // [T, lddz]
   long lddz;
   int32_t* hdr;

@@ -485,7 +485,8 @@ cudaError_t launch_backward(const EmbedParams& p, int* launches, cudaStream_t st
   const int passes = (key_bits + 9) / 10, bits = (key_bits + passes - 1) / passes;
   constexpr size_t kMost = ((size_t)(kSortWarps + 2) * kMaxDigits + kSortWarps) * 4;
   static_assert(kMarkRows / 8 + kZeroBytes <= kMost, "what marks and zeros rows fits the sort's shared memory");
-  cudaError_t e = cudaFuncSetAttribute(embed_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMost);
+  static std::atomic<uint64_t> allowed{0};
+  cudaError_t e = allow_smem((const void*)embed_sort_kernel, kMost, allowed);
   if (e != cudaSuccess) return e;
   // the zeros of the rows that no token has: by the clusters beside the sort's
   const int sms = device_sm_count(), zero = p.accumulate ? 0 : sms > 2 * kSortCtas ? sms / kSortCtas - 1 : 1;

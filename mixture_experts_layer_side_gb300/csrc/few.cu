@@ -1219,7 +1219,8 @@ cudaError_t launch_few(FewParams p, bool mx, int* launches, cudaStream_t st) {
   p.stages = stages;
   const size_t smem = rest + stages * stage;
   const void* kernel = mx ? (const void*)few_kernel<true> : (const void*)few_kernel<false>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMost);
+  static std::atomic<uint64_t> allowed[2];
+  cudaError_t e = allow_smem(kernel, kMost, allowed[mx]);
   if (e != cudaSuccess) return e;
   void* args[] = {&maps, &p};
   e = cudaLaunchCooperativeKernel(kernel, dim3(ctas), dim3(mx ? 320 : 256), args, smem, st);

@@ -7,6 +7,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/mok.h"
 
 // Device error bits of the workspace error word (header word 0).
@@ -79,6 +81,9 @@ struct WsLayout {
 WsLayout ws_layout(const mok_shape& s, const mok_config& c, mok_precision prec, int num_sms);
 int effective_minibatch_rows(const mok_shape& s, const mok_config& c, int num_sms);
 int device_sm_count();
+// Lets a kernel use up to `bytes` of dynamic shared memory; asks the runtime
+// once per device (`done`: a bit per device, the kernel's own).
+cudaError_t allow_smem(const void* kernel, size_t bytes, std::atomic<uint64_t>& done);
 
 // Host: tensor maps (driver entry point resolved once).
 bool make_tmap(CUtensorMap* m, CUtensorMapDataType dt, int rank, const void* ptr, const uint64_t* dims,

@@ -52,7 +52,7 @@ class DistillLoss:
 
     def _gradient(self, z, out):
         if out is None:
-            return torch.empty(z.shape, dtype=z.dtype, device=self.device)
+            return torch.empty(z.shape, dtype=z.dtype, device=z.device)
         if not rows_fit(out, z.shape, z.dtype, self.device):
             tensor(out, "out", z.shape, (z.dtype,), self.device, rows_apart=True)
         return out
@@ -60,7 +60,8 @@ class DistillLoss:
     def forward(self, z, ids, vals, temperature=1.0, stream=None):
         """(loss, lse), f32 [T] each."""
         T, tau = self._begin(z, ids, vals, temperature)
-        loss, lse = torch.empty((2, T), dtype=torch.float32, device=self.device).unbind(0)
+        loss = torch.empty(T, dtype=torch.float32, device=self.device)
+        lse = torch.empty(T, dtype=torch.float32, device=self.device)
         _lib.mok_distill_forward(z, ids, vals, tau, loss, lse, self.ws, stream)
         return loss, lse
 
@@ -78,8 +79,8 @@ class DistillLoss:
         T, tau = self._begin(z, ids, vals, temperature)
         self._row_values(T, "dloss", dloss)
         dz = self._gradient(z, out)
-        loss, lse = torch.empty((2, T), dtype=torch.float32, device=self.device).unbind(0)
-        _lib.mok_distill_step(z, ids, vals, tau, dloss, loss, lse, dz, self.ws, stream)
+        loss = torch.empty(T, dtype=torch.float32, device=self.device)
+        _lib.mok_distill_step(z, ids, vals, tau, dloss, loss, None, dz, self.ws, stream)
         return loss, dz
 
     def check(self, stream=None):
