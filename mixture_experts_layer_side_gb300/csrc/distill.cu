@@ -283,6 +283,13 @@ __device__ __forceinline__ int read_list(const DistillParams& q, long t, const Z
   return any;
 }
 
+// The cluster's CTAs tell one another that they run (begin), before any writes
+// into another's shared memory (wait): a CTA that has not begun has none.
+__device__ __forceinline__ void cluster_begin(int shares) {
+  if (shares > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_begun() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
+
 // The row's sum from those of the threads of its CTAs, the same in every
 // thread.  The first W warps hold sums; others only take part in the barriers.
 template <int W>
@@ -295,6 +302,7 @@ __device__ __forceinline__ void join_row(Sum& a, float c, Shared<W>& sh, int ran
   join_lanes<W>(a, c);
   if (shares == 1) return;
   cg::cluster_group cluster = cg::this_cluster();
+  cluster_begun();
   if (threadIdx.x < shares) *cluster.map_shared_rank(&sh.share[rank], threadIdx.x) = a;
   cluster.sync();
   const int i = threadIdx.x & (kMaxShare - 1);
@@ -321,13 +329,14 @@ __device__ __forceinline__ void store_loss(const DistillParams& q, long t, const
 }
 
 // Both kernels: workers, and a last warp for the list.
-constexpr int kForwardWorkers = 512;
+constexpr int kForwardWorkers = 256;
 constexpr int kGradWorkers = 128;
 
 template <typename Z>
 __global__ void __launch_bounds__(kForwardWorkers + 32) distill_forward_kernel(DistillParams q, int shares, int most) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ Shared<kForwardWorkers / 32> sh;
+  cluster_begin(shares);
   const long t = blockIdx.x / shares;
   const int rank = blockIdx.x % shares;
   const float c = q.inv_tau * kLog2e;
@@ -361,13 +370,14 @@ __global__ void __launch_bounds__(kForwardWorkers + 32) distill_forward_kernel(D
 // The gradient of a share of a row, and with STEP the sum before it.  Without
 // STEP the shares are CTAs of their own.  Shared memory: the share's vectors,
 // then the list.
-constexpr int kPieces = 4;  // copies of a share, so that the sum begins with the first
+constexpr int kPieces = 2;  // copies of a share, so that the sum begins with the first
 
 template <typename Z, bool STEP>
 __global__ void __launch_bounds__(kGradWorkers + 32) distill_gradient_kernel(DistillParams q, int shares, int most) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ Shared<kGradWorkers / 32> sh;
   __shared__ uint64_t full[kPieces];
+  if (STEP) cluster_begin(shares);
   constexpr int kN = Vec<Z>::kN;
   uint4* x = reinterpret_cast<uint4*>(smem);
   const List list = list_at(smem + (size_t)most * 16, q.K);
