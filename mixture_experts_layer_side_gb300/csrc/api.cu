@@ -1668,6 +1668,11 @@ mok_status distill(DistillMode mode, int32_t T, int32_t V, int32_t K, mok_dtype 
   p.lddz = lddz;
   p.hdr = static_cast<int32_t*>(ws);
   p.lse_scratch = reinterpret_cast<float*>(p.hdr + kHeaderWords);
+  if (mode != DISTILL_FORWARD) {
+    const uintptr_t es = type == MOK_TYPE_BF16 ? 2 : 4, z0 = reinterpret_cast<uintptr_t>(z),
+                    d0 = reinterpret_cast<uintptr_t>(dz);
+    p.overlap = d0 < z0 + es * ((T - 1) * (uintptr_t)ldz + V) && z0 < d0 + es * ((T - 1) * (uintptr_t)lddz + V);
+  }
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   Phase ph(MOK_PHASE_DISTILL, st, 0);
   int launches = 0;

@@ -245,12 +245,11 @@ __device__ __forceinline__ List list_at(uint8_t* smem, int K) {
   return l;
 }
 
-// One warp: the list, the student's logits at it (while the row still holds
-// them) and the teacher's probabilities.  NaN values make them NaN.
-template <typename Z>
-__device__ __forceinline__ int read_list(const DistillParams& q, long t, const Z* z, const List& l, int lane) {
-  float top = -INFINITY;
-  bool nan = false;
+// By one warp, in three steps of which the others wait for the first alone:
+// the ids and values (tau already divided out; -inf for what is left out) --
+// returns whether there is anything to learn from: an entry above -inf.
+__device__ __forceinline__ bool read_list(const DistillParams& q, long t, const List& l, int lane) {
+  bool any = false;
 #pragma unroll 1
   for (int j = lane; j < q.K; j += 32) {
     int id = q.ids[t * q.K + j];
@@ -262,12 +261,24 @@ __device__ __forceinline__ int read_list(const DistillParams& q, long t, const Z
     if (id < 0) v = -INFINITY;
     l.ids[j] = id;
     l.p[j] = v;
-    l.logits[j] = id >= 0 ? Vec<Z>::value(z[id]) : 0.0f;
-    nan |= isnan(v);
-    top = fmaxf(top, v);
+    any |= v != -INFINITY;  // a NaN value counts: it makes the row NaN
   }
+  return __any_sync(0xffffffffu, any);
+}
+
+// The student's logits at the ids, while the row still holds them.
+template <typename Z>
+__device__ __forceinline__ void read_logits(const DistillParams& q, const Z* z, const List& l, int lane) {
+#pragma unroll 4
+  for (int j = lane; j < q.K; j += 32) l.logits[j] = l.ids[j] >= 0 ? Vec<Z>::value(z[l.ids[j]]) : 0.0f;
+}
+
+// The teacher's probabilities in place of its values, for a list that has any.
+__device__ __forceinline__ void softmax_list(const DistillParams& q, const List& l, int lane) {
+  float top = -INFINITY;
+#pragma unroll 1
+  for (int j = lane; j < q.K; j += 32) top = fmaxf(top, l.p[j]);
   for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  nan = __any_sync(0xffffffffu, nan);
   const float base = top == -INFINITY ? 0.0f : top;
   float total = 0.0f;
 #pragma unroll 1
@@ -277,10 +288,9 @@ __device__ __forceinline__ int read_list(const DistillParams& q, long t, const Z
     total += e;
   }
   for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-  const bool any = total > 0.0f || nan || isnan(total);
 #pragma unroll 1
-  for (int j = lane; j < q.K; j += 32) l.p[j] = any ? l.p[j] / total : 0.0f;
-  return any;
+  for (int j = lane; j < q.K; j += 32) l.p[j] /= total;
+  __syncwarp();
 }
 
 // The cluster's CTAs tell one another that they run (begin), before any writes
@@ -313,11 +323,11 @@ __device__ __forceinline__ void join_row(Sum& a, float c, Shared<W>& sh, int ran
 }
 
 // The row's loss and log-sum-exp from its sum, by the warp that read the list.
-__device__ __forceinline__ void store_loss(const DistillParams& q, long t, const List& list, Sum a, int lane) {
+__device__ __forceinline__ void store_loss(const DistillParams& q, long t, const List& list, bool any, Sum a, int lane) {
   const float base = finite_max(a.m), log_s = logf(a.s);
   float l = 0.0f;
 #pragma unroll 1
-  for (int j = lane; j < q.K; j += 32) {
+  for (int j = lane; any && j < q.K; j += 32) {
     const float p = list.p[j];
     if (p > 0.0f || isnan(p)) l += p * (logf(p) - ((list.logits[j] - base) * q.inv_tau - log_s));
   }
@@ -344,7 +354,15 @@ __global__ void __launch_bounds__(kForwardWorkers + 32) distill_forward_kernel(D
   const List list = list_at(smem, q.K);
   Sum a{-INFINITY, 0.0f};
   if (threadIdx.x >= kForwardWorkers) {
-    if (rank == 0) read_list(q, t, row.z, list, threadIdx.x & 31);
+    if (rank == 0) {
+      const int lane = threadIdx.x & 31;
+      const bool any = read_list(q, t, list, lane);
+      if (any) {
+        read_logits(q, row.z, list, lane);
+        softmax_list(q, list, lane);
+      }
+      if (lane == 0) sh.any = any;
+    }
   } else {
     const int v0 = min(rank * most, row.vecs), v1 = min(v0 + most, row.vecs);
     // the part-filled vectors at the row's ends apart
@@ -364,7 +382,7 @@ __global__ void __launch_bounds__(kForwardWorkers + 32) distill_forward_kernel(D
     }
   }
   join_row(a, c, sh, rank, shares);
-  if (rank == 0 && threadIdx.x >= kForwardWorkers) store_loss(q, t, list, a, threadIdx.x & 31);
+  if (rank == 0 && threadIdx.x >= kForwardWorkers) store_loss(q, t, list, sh.any, a, threadIdx.x & 31);
 }
 
 // The gradient of a share of a row, and with STEP the sum before it.  Without
@@ -384,6 +402,8 @@ __global__ void __launch_bounds__(kGradWorkers + 32) distill_gradient_kernel(Dis
   const long t = blockIdx.x / shares;
   const int rank = blockIdx.x % shares, lane = threadIdx.x & 31;
   const bool worker = threadIdx.x < kGradWorkers;
+  // the gradient takes the logits' place, or may: then a logit is read before any is overwritten
+  const bool in_place = q.overlap;
   const float c = q.inv_tau * kLog2e;
   const RowGrid<Z> row(q.z, t * q.ldz, q.V), grad(q.dz, t * q.lddz, q.V);
   const int v0 = min(rank * most, row.vecs), n = min(most, row.vecs - v0);
@@ -406,8 +426,9 @@ __global__ void __launch_bounds__(kGradWorkers + 32) distill_gradient_kernel(Dis
   bool fine = true;
   const bool first_part = threadIdx.x == 32 && b > 0, last_part = threadIdx.x == 64 && e < n;
   if (!worker) {
-    const int any = read_list(q, t, row.z, list, lane);
+    const bool any = read_list(q, t, list, lane);
     if (lane == 0) sh.any = any;
+    if (in_place && any) read_logits(q, row.z, list, lane);
   } else {
     // a part-filled vector stays with the thread that brings it
     if (first_part) x[0] = row.load_part(v0);
@@ -437,7 +458,7 @@ __global__ void __launch_bounds__(kGradWorkers + 32) distill_gradient_kernel(Dis
   // q_v = 2^((z_v - base) c) q_base
   float base, q_base;
   if constexpr (STEP) {
-    // (the logits that other CTAs list are read before the barrier in here, and overwritten after it)
+    // (in place, the logits that other CTAs list are read before the barrier in here, and overwritten after it)
     join_row(a, c, sh, rank, shares);
     base = finite_max(a.m);
     q_base = 1.0f / a.s;
@@ -462,7 +483,11 @@ __global__ void __launch_bounds__(kGradWorkers + 32) distill_gradient_kernel(Dis
   };
   uint32_t mine = 0;  // list warp: its entries that are the first of a column of this share
   if (!worker) {
-    if (STEP && rank == 0) store_loss(q, t, list, a, lane);
+    if (any) {
+      if (!in_place) read_logits(q, row.z, list, lane);
+      softmax_list(q, list, lane);
+    }
+    if (STEP && rank == 0) store_loss(q, t, list, any, a, lane);
     if (any) {
 #pragma unroll 1
       for (int j = lane; j < q.K; j += 32) {
@@ -470,12 +495,12 @@ __global__ void __launch_bounds__(kGradWorkers + 32) distill_gradient_kernel(Dis
         if (id < 0 || v < v0 || v >= v0 + n) continue;
         float sum = 0.0f;
         bool first = true;
-#pragma unroll 4
-        for (int i = 0; i < q.K; ++i)
-          if (list.ids[i] == id) {
-            sum += list.p[i];
-            first = first && i >= j;
-          }
+#pragma unroll 8
+        for (int i = 0; i < q.K; ++i) {
+          const bool same_id = list.ids[i] == id;
+          sum += same_id ? list.p[i] : 0.0f;
+          first = first && !(same_id && i < j);
+        }
         const float e_j = fast_exp2((list.logits[j] - base) * c);
         list.logits[j] = g * ((STEP ? e_j / a.s : e_j * q_base) - sum);
         mine |= (uint32_t)first << (j >> 5);
