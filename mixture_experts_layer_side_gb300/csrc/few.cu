@@ -81,7 +81,7 @@ __host__ __device__ constexpr size_t schedule_bytes(int E, int R, int units) {
 // differ by one at most.
 struct Cut {
   int group;          // CTAs side by side on neighbouring column tiles
-  int supers;         // groups of column tiles in a unit
+  int supers, tiles;  // groups of column tiles, and column tiles, of a unit
   int kb;             // blocks along K
   int unit0, units;
   int blocks;         // of one CTA of a group
@@ -103,6 +103,7 @@ __device__ __forceinline__ Cut make_cut(int tiles, int kb, int unit0, int units,
   c.group = tiles % 8 == 0 ? 8 : tiles % 4 == 0 ? 4 : tiles % 2 == 0 ? 2 : 1;
   if (c.group > ctas) c.group = 1;
   c.supers = tiles / c.group;
+  c.tiles = c.supers * c.group;
   c.kb = kb;
   c.unit0 = unit0;
   c.units = units;
@@ -121,15 +122,41 @@ struct Seg {
   int super;      // index of the tile's group
 };
 
-__device__ __forceinline__ Seg seg_at(const Cut& c, int b, int end, int rank) {
-  Seg s;
+// A CTA's run of a cut: its first share, and the blocks from there on.  (Made
+// once per CTA; the roles step through it without a division.)
+struct Run {
+  Seg seg;
+  int left;
+};
+
+__device__ __forceinline__ Run run_of(const Cut& c, int cta) {
+  Run r;
+  r.left = 0;
+  if (!c.takes(cta)) return r;
+  const int run = cta / c.group, b = c.begin(run);
+  r.left = c.begin(run + 1) - b;
+  Seg& s = r.seg;
   s.super = b / c.kb;
   s.k0 = b - s.super * c.kb;
-  s.k1 = min(c.kb, s.k0 + end - b);
+  s.k1 = min(c.kb, s.k0 + r.left);
   const int u = s.super / c.supers;
   s.unit = c.unit0 + u;
-  s.n = (s.super - u * c.supers) * c.group + rank;
-  return s;
+  s.n = (s.super - u * c.supers) * c.group + cta - run * c.group;
+  return r;
+}
+
+// The next share.
+__device__ __forceinline__ void step(Run& r, const Cut& c) {
+  Seg& s = r.seg;
+  r.left -= s.k1 - s.k0;
+  ++s.super;
+  s.n += c.group;
+  if (s.n >= c.tiles) {
+    s.n -= c.tiles;
+    ++s.unit;
+  }
+  s.k0 = 0;
+  s.k1 = min(c.kb, r.left);
 }
 
 // The runs that a tile is split over.
@@ -148,6 +175,7 @@ struct Ctl {
   int last;
   int warp_sum[16];
   Cut cuts[4];  // in order: a of each half of the units, y of each half
+  Run runs[4];  // this CTA's
 };
 
 __device__ __forceinline__ bool vote_all(int bar, int threads, bool ok) {
@@ -373,6 +401,46 @@ __device__ __forceinline__ void touch_weights(const FewParams& p, int e) {
   asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const uint8_t*>(p.W1) + at));
   asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const uint8_t*>(p.W3) + at));
   asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const uint8_t*>(p.W2) + at));
+}
+
+// The same for at most 32 rows, by one warp: lane f's row goes after those of
+// lower experts and of lower f.  False where an expert has more rows than a
+// unit takes.
+template <bool MX>
+__device__ __forceinline__ bool build_few(const FewParams& p, const Schedule& s, Ctl* ctl, int id, int lane) {
+  const int R = p.T * p.k;
+  if (p.Wr) id = lane < R ? __ldcg(p.idx + lane) : -1;
+  const bool in = lane < R && id >= 0 && id < p.E;
+  if (in && lane < kTouchRows) touch_weights<MX>(p, id);
+  const uint32_t valid = __ballot_sync(0xffffffffu, in);
+  const uint32_t same = __match_any_sync(0xffffffffu, in ? id : -1);
+  const int rows = __popc(same), ahead = __popc(same & ((1u << lane) - 1u));
+  if (__any_sync(0xffffffffu, in && rows > p.unit_rows)) return false;
+  const bool first = in && ahead == 0;
+  const uint32_t firsts = __ballot_sync(0xffffffffu, first);
+  int before = 0, unit = 0;
+#pragma unroll 4
+  for (int j = 0; j < 32; ++j) {
+    const int e = __shfl_sync(0xffffffffu, id, j);
+    const bool lower = e < id;
+    before += lower && ((valid >> j) & 1u);
+    unit += lower && ((firsts >> j) & 1u);
+  }
+  if (in) {
+    s.perm[before + ahead] = (uint16_t)lane;
+    s.token[before + ahead] = (uint16_t)(lane / p.k);
+    s.row_of[lane] = (uint8_t)ahead;
+  }
+  if (lane < R) s.unit_of[lane] = (uint16_t)(in ? unit : kNoUnit);
+  if (first) {
+    s.unit_e[unit] = (uint16_t)id;
+    s.unit_r[unit] = (uint16_t)before;
+    s.unit_n[unit] = (uint8_t)rows;
+  }
+  if (lane == 0) ctl->units = __popc(firsts);
+  if (blockIdx.x == 0 && lane < R && !in) atomicOr(p.hdr + kHdrError, MOK_ERRBIT_BAD_INDEX);
+  __syncwarp();
+  return true;
 }
 
 // Rows grouped by expert in ascending flat index, and cut into units: a
@@ -707,11 +775,12 @@ __global__ void __launch_bounds__(MX ? 320 : 256, 1) few_kernel(const __grid_con
   WaitCtx wc{&ctl->abort, p.hdr + kHdrAbort, p.hdr + kHdrError};
 
   // what the routing and the first tiles need soon, on its way from memory meanwhile
+  const int early_id = !p.Wr && warp == 0 && lane < R ? __ldg(p.idx + lane) : -1;
   {
     const char* a = reinterpret_cast<const char*>(p.x);
     const long bytes = (long)p.T * p.H * 2, at = ((long)blockIdx.x * kThreads + threadIdx.x) * 128;
     if (at < bytes) asm volatile("prefetch.global.L2 [%0];" ::"l"(a + at));
-    if (!p.Wr && threadIdx.x * 32 < R) asm volatile("prefetch.global.L2 [%0];" ::"l"(p.idx + threadIdx.x * 32));
+    if (!p.Wr && R > 32 && threadIdx.x * 32 < R) asm volatile("prefetch.global.L2 [%0];" ::"l"(p.idx + threadIdx.x * 32));
     if (blockIdx.x == 0 && p.bias && threadIdx.x * 32 < p.E)
       asm volatile("prefetch.global.L2 [%0];" ::"l"(p.bias + threadIdx.x * 32));
   }
@@ -764,20 +833,25 @@ __global__ void __launch_bounds__(MX ? 320 : 256, 1) few_kernel(const __grid_con
     __syncthreads();
     ok = ctl->go != 0;
   }
-  if (ok) build_units<MX>(p, sched, smem, ctl, kThreads);
+  const int c = blockIdx.x;
+  bool made = false;  // (uniform in warp 0, which alone knows)
+  if (ok && R <= 32 && warp == 0) made = build_few<MX>(p, sched, ctl, early_id, lane);
+  if (ok && R <= 32) made = __syncthreads_or(made);
+  if (ok && !made) build_units<MX>(p, sched, smem, ctl, kThreads);
   // the stages' first loads (async proxy) come after these threads' use of the same shared memory
   fence_proxy_async_shared();
-  const int c = blockIdx.x;
   if (ok && threadIdx.x < 4) {
     // halves only where a half is long beside the joining it hides: at 10
     // blocks a CTA the two extra joins cost more than they hid (1 token, H
     // 2048, I 768: 49 us in halves)
     const int i = threadIdx.x, units = ctl->units;
-    const long blocks = (long)units * (p.I / 128) * (p.H / kEl);
-    const int half = blocks >= (long)kHalvesFrom * gridDim.x ? (units + 1) / 2 : units;
+    const int blocks = units * (p.I / 128) * (p.H / kEl);
+    const int half = blocks >= kHalvesFrom * (int)gridDim.x ? (units + 1) / 2 : units;
     const int u0 = i & 1 ? half : 0, nu = i & 1 ? units - half : half;
-    ctl->cuts[i] = i < 2 ? make_cut(p.I / 128, p.H / kEl, u0, nu, gridDim.x)
-                         : make_cut((p.H + 255) / 256, p.I / kEl, u0, nu, gridDim.x);
+    const Cut cut = i < 2 ? make_cut(p.I / 128, p.H / kEl, u0, nu, gridDim.x)
+                          : make_cut((p.H + 255) / 256, p.I / kEl, u0, nu, gridDim.x);
+    ctl->cuts[i] = cut;
+    ctl->runs[i] = run_of(cut, c);
   }
   tc_fence_before();
   __syncthreads();
@@ -796,12 +870,10 @@ __global__ void __launch_bounds__(MX ? 320 : 256, 1) few_kernel(const __grid_con
       long issued = 0;
       bool fine = true;
       for (int ph = 0; ph < 4; ++ph) {
-        const Cut cut = ctl->cuts[ph];
+        const Cut& cut = ctl->cuts[ph];
         const int g = ph >> 1;
-        if (!fine || !cut.takes(c)) continue;
-        const int end = cut.begin(c / cut.group + 1);
-        for (int b = cut.begin(c / cut.group); b < end && fine;) {
-          const Seg s = seg_at(cut, b, end, c % cut.group);
+        for (Run r = ctl->runs[ph]; r.left > 0 && fine; step(r, cut)) {
+          const Seg s = r.seg;
           const int e = sched.unit_e[s.unit];
           const int col = g == 0 ? s.n * 128 : s.n * 256;
           const bool second = g == 0 || col + 128 < p.H;
@@ -836,7 +908,6 @@ __global__ void __launch_bounds__(MX ? 320 : 256, 1) few_kernel(const __grid_con
             ++issued;
             if (++stage == (uint32_t)p.stages) { stage = 0; phase ^= 1; }
           }
-          b += s.k1 - s.k0;
         }
       }
       if (!fine) {
@@ -851,12 +922,10 @@ __global__ void __launch_bounds__(MX ? 320 : 256, 1) few_kernel(const __grid_con
     uint32_t stage = 0, phase = 0, count = 0;
     bool fine = true;
     for (int ph = 0; ph < 4; ++ph) {
-      const Cut cut = ctl->cuts[ph];
+      const Cut& cut = ctl->cuts[ph];
       const int g = ph >> 1;
-      if (!fine || !cut.takes(c)) continue;
-      const int end = cut.begin(c / cut.group + 1);
-      for (int b = cut.begin(c / cut.group); b < end && fine;) {
-        const Seg s = seg_at(cut, b, end, c % cut.group);
+      for (Run r = ctl->runs[ph]; r.left > 0 && fine; step(r, cut)) {
+        const Seg s = r.seg;
         const int n = (sched.unit_n[s.unit] + 15) & ~15;
         const bool second = g == 0 || s.n * 256 + 128 < p.H;
         const uint32_t buf = count & 1;
@@ -877,8 +946,6 @@ __global__ void __launch_bounds__(MX ? 320 : 256, 1) few_kernel(const __grid_con
             // the tokens' operand was written with cp.async: order it before the tensor core's (async-proxy) reads
             fence_proxy_async_shared();
             const uint32_t a0 = smem_u32(smem + (size_t)stage * stage_bytes), b0 = a0 + 2 * kATile;
-            // (small loops: a few tokens' pass runs each of these instructions a
-            // few times, and fetching them costs more than issuing them)
             if constexpr (MX) {
               const uint32_t sf = smem_u32(sf_smem + stage * kSfBytes);
               const uint32_t t = tmem + 256 + stage * 16;  // scales: two A tiles, B
@@ -901,7 +968,7 @@ __global__ void __launch_bounds__(MX ? 320 : 256, 1) few_kernel(const __grid_con
               // one of twice as many: it waits for its A operand)
               const uint32_t idesc = idesc_bf16(128, g == 0 ? n : 2 * n, 1, 0);
               uint64_t ad = sdesc_sw128(a0, 8192, 1024), bd = sdesc_sw128(b0, 16, 1024);
-#pragma unroll 1
+#pragma unroll
               for (int k16 = 0; k16 < 4; ++k16) {
                 const uint32_t acc = kb > s.k0 || k16 > 0;
                 mma_bf16(d0, ad, bd, idesc, acc);
@@ -919,7 +986,6 @@ __global__ void __launch_bounds__(MX ? 320 : 256, 1) few_kernel(const __grid_con
         if (lane == 0) mma_commit(&ctl->tfull[buf]);
         __syncwarp();
         ++count;
-        b += s.k1 - s.k0;
       }
     }
     if (!fine) {
@@ -937,9 +1003,9 @@ __global__ void __launch_bounds__(MX ? 320 : 256, 1) few_kernel(const __grid_con
     uint32_t stage = 0, phase = 0;
     bool fine = true;
     for (int ph = 0; ph < 4; ++ph) {
-      const Cut cut = ctl->cuts[ph];
+      const Cut& cut = ctl->cuts[ph];
       const int g = ph >> 1;
-      if (!fine || !cut.takes(c)) continue;
+      if (!fine || ctl->runs[ph].left == 0) continue;
       // x is ready at once (MXFP8: once every CTA has quantised its share),
       // a when every tile of this half of it is finished
       if (g == 1 || (MX && !p.Wr)) {
@@ -954,9 +1020,8 @@ __global__ void __launch_bounds__(MX ? 320 : 256, 1) few_kernel(const __grid_con
       const uint8_t* src = g == 0 ? (MX ? p.xq : reinterpret_cast<const uint8_t*>(p.x)) : static_cast<uint8_t*>(p.a);
       const uint8_t* sfs = g == 0 ? p.xsf : p.asf;
       const long lo = (long)p.T * p.k * p.I * 2;  // a's second part
-      const int end = cut.begin(c / cut.group + 1);
-      for (int b = cut.begin(c / cut.group); b < end && fine;) {
-        const Seg s = seg_at(cut, b, end, c % cut.group);
+      for (Run run = ctl->runs[ph]; run.left > 0 && fine; step(run, cut)) {
+        const Seg s = run.seg;
         const int n = sched.unit_n[s.unit], r0 = sched.unit_r[s.unit];
         const int n16 = (n + 15) & ~15;
         const long row_bytes = (long)K * (MX ? 1 : 2);
@@ -981,7 +1046,6 @@ __global__ void __launch_bounds__(MX ? 320 : 256, 1) few_kernel(const __grid_con
           cp_async_arrive_noinc(&ctl->full_b[stage]);
           if (++stage == (uint32_t)p.stages) { stage = 0; phase ^= 1; }
         }
-        b += s.k1 - s.k0;
       }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
@@ -993,14 +1057,10 @@ __global__ void __launch_bounds__(MX ? 320 : 256, 1) few_kernel(const __grid_con
     uint32_t count = 0;
     bool fine = true;
     for (int ph = 0; ph < 4; ++ph) {
-      const Cut cut = ctl->cuts[ph];
+      const Cut& cut = ctl->cuts[ph];
       const int g = ph >> 1, half = ph & 1;
-      if (!fine || !cut.takes(c)) continue;
-      const int run = c / cut.group, rank = c % cut.group;
-      const int end = cut.begin(run + 1);
-      for (int b = cut.begin(run); b < end;) {
-        const Seg s = seg_at(cut, b, end, rank);
-        b += s.k1 - s.k0;
+      for (Run r = ctl->runs[ph]; r.left > 0 && fine; step(r, cut)) {
+        const Seg s = r.seg;
         const int n = sched.unit_n[s.unit], r0 = sched.unit_r[s.unit];
         const bool second = g == 0 || s.n * 256 + 128 < p.H;
         const bool whole = s.k0 == 0 && s.k1 == cut.kb;
@@ -1056,7 +1116,7 @@ __global__ void __launch_bounds__(MX ? 320 : 256, 1) few_kernel(const __grid_con
           __syncwarp();
           named_bar_sync(1, kEpilogue);
           if (!ctl->last) continue;
-          join_hidden<MX>(p, cut, s, rank, half, first, last, r0, n, warp - 4, lane);
+          join_hidden<MX>(p, cut, s, c % cut.group, half, first, last, r0, n, warp - 4, lane);
         }
         // a finished tile of a
         named_bar_sync(1, kEpilogue);
@@ -1076,10 +1136,8 @@ __global__ void __launch_bounds__(MX ? 320 : 256, 1) few_kernel(const __grid_con
     uint32_t stage = 0, phase = 0;
     bool fine = true;
     for (int ph = 0; ph < 4; ++ph) {
-      const Cut cut = ctl->cuts[ph];
-      if (!fine || !cut.takes(c)) continue;
-      const int blocks = cut.begin(c / cut.group + 1) - cut.begin(c / cut.group);
-      for (int b = 0; b < blocks; ++b) {
+      const int blocks = ctl->runs[ph].left;
+      for (int b = 0; b < blocks && fine; ++b) {
         fine = mbar_wait(&ctl->full_a[stage], phase, wc);
         if (!fine) break;
         const uint8_t* raw = sf_smem + stage * kSfBytes + i * 512;
