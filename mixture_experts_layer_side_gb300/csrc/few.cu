@@ -77,17 +77,20 @@ __host__ __device__ constexpr size_t schedule_bytes(int E, int R, int units) {
   return (size_t)E * 4 + (size_t)R * 7 + (size_t)units * 5 + 16;
 }
 
+// (a call, so that its instructions are fetched once)
+__device__ __noinline__ int quotient(int a, int b) { return (int)((unsigned)a / (unsigned)b); }
+
 // One GEMM of one half of the units, its blocks cut into runs whose lengths
 // differ by one at most.
 struct Cut {
-  int group;          // CTAs side by side on neighbouring column tiles
+  int group, group_shift;  // CTAs side by side on neighbouring column tiles
   int supers, tiles;  // groups of column tiles, and column tiles, of a unit
   int kb;             // blocks along K
   int unit0, units;
   int blocks;         // of one CTA of a group
   int runs, each, rest;  // blocks = runs * each + rest
   __device__ bool takes(int c) const { return c < runs * group; }
-  __device__ int begin(int run) const { return each * run + rest * run / runs; }
+  __device__ int begin(int run) const { return each * run + quotient(rest * run, runs); }
   // the run that holds block b
   __device__ int owner(int b) const {
     int o = (int)((float)b * (float)runs / (float)blocks);
@@ -98,20 +101,23 @@ struct Cut {
   }
 };
 
-__device__ __forceinline__ Cut make_cut(int tiles, int kb, int unit0, int units, int ctas) {
+__device__ __forceinline__ Cut make_cut(const FewShape& f, int unit0, int units, int ctas) {
   Cut c;
-  c.group = tiles % 8 == 0 ? 8 : tiles % 4 == 0 ? 4 : tiles % 2 == 0 ? 2 : 1;
-  if (c.group > ctas) c.group = 1;
-  c.supers = tiles / c.group;
-  c.tiles = c.supers * c.group;
-  c.kb = kb;
+  c.group = 1 << f.group_shift;
+  c.group_shift = f.group_shift;
+  c.supers = f.supers;
+  c.tiles = f.supers << f.group_shift;
+  c.kb = f.kb;
   c.unit0 = unit0;
   c.units = units;
-  c.blocks = units * c.supers * kb;
-  c.runs = max(1, min((c.blocks + kMinRun - 1) / kMinRun, ctas / c.group));
-  if (units == 0) c.runs = 0;
-  c.each = units ? c.blocks / c.runs : 0;
-  c.rest = units ? c.blocks - c.each * c.runs : 0;
+  c.blocks = units * c.supers * c.kb;
+  c.runs = 0;
+  c.each = c.rest = 0;
+  if (units) {
+    c.runs = max(1, min(quotient(c.blocks + kMinRun - 1, kMinRun), ctas >> f.group_shift));
+    c.each = quotient(c.blocks, c.runs);
+    c.rest = c.blocks - c.each * c.runs;
+  }
   return c;
 }
 
@@ -133,15 +139,15 @@ __device__ __forceinline__ Run run_of(const Cut& c, int cta) {
   Run r;
   r.left = 0;
   if (!c.takes(cta)) return r;
-  const int run = cta / c.group, b = c.begin(run);
+  const int run = cta >> c.group_shift, b = c.begin(run);
   r.left = c.begin(run + 1) - b;
   Seg& s = r.seg;
-  s.super = b / c.kb;
+  s.super = quotient(b, c.kb);
   s.k0 = b - s.super * c.kb;
   s.k1 = min(c.kb, s.k0 + r.left);
-  const int u = s.super / c.supers;
+  const int u = quotient(s.super, c.supers);
   s.unit = c.unit0 + u;
-  s.n = (s.super - u * c.supers) * c.group + cta - run * c.group;
+  s.n = ((s.super - u * c.supers) << c.group_shift) + cta - (run << c.group_shift);
   return r;
 }
 
@@ -445,33 +451,48 @@ __device__ __forceinline__ bool build_few(const FewParams& p, const Schedule& s,
 
 // Rows grouped by expert in ascending flat index, and cut into units: a
 // counting sort whose warps own contiguous ranges of the flat indices, so
-// that (warp, place) is their order.  `scratch`: the ids and a count per warp
+// that (warp, place) is their order.  `scratch`: of each flat index its expert
+// and its place among the warp's rows of that expert, and a count per warp
 // and expert.
 template <bool MX>
 __device__ void build_units(const FewParams& p, const Schedule& s, uint8_t* scratch, Ctl* ctl, int nthreads) {
   const int R = p.T * p.k, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int per = ((R + nthreads - 1) / nthreads) * 32;  // flat indices a warp
-  const int W = (R + per - 1) / per;                     // warps that have some
+  const int per_shift = max(5, 32 - __clz((R - 1) / (nthreads / 32)));  // flat indices a warp, a power of two
+  const int per = 1 << per_shift, W = (R + per - 1) >> per_shift;       // warps that have some
   const int shift = __ffs(p.unit_rows) - 1;
   uint16_t* ids = reinterpret_cast<uint16_t*>(scratch);
-  uint32_t* hist = reinterpret_cast<uint32_t*>(scratch + (((size_t)R * 2 + 15) & ~15));  // [W][E]
-  for (int i = threadIdx.x; i < W * p.E; i += nthreads) hist[i] = 0;
+  uint16_t* place = ids + R;
+  uint32_t* hist = reinterpret_cast<uint32_t*>(scratch + (((size_t)R * 4 + 15) & ~15));  // [W][E]
   bool bad = false;
-  for (int f = threadIdx.x; f < R; f += nthreads) {
-    const int e = p.idx[f];
-    const bool in = e >= 0 && e < p.E;
-    bad |= !in;
-    if (in && f < kTouchRows) touch_weights<MX>(p, e);
-    ids[f] = (uint16_t)(in ? e : kNoUnit);
+  for (int f0 = threadIdx.x; f0 < R; f0 += 4 * nthreads) {
+    int e[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) e[i] = f0 + i * nthreads < R ? __ldcg(p.idx + f0 + i * nthreads) : 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int f = f0 + i * nthreads;
+      if (f >= R) break;
+      const bool in = e[i] >= 0 && e[i] < p.E;
+      bad |= !in;
+      ids[f] = (uint16_t)(in ? e[i] : kNoUnit);
+      if (in && f < kTouchRows) touch_weights<MX>(p, e[i]);
+    }
   }
+  for (int i = threadIdx.x; i < W * p.E; i += nthreads) hist[i] = 0;
   if (bad && blockIdx.x == 0) atomicOr(p.hdr + kHdrError, MOK_ERRBIT_BAD_INDEX);
   __syncthreads();
-  const int f0 = warp * per, f1 = min(R, f0 + per);
+  const int f0 = warp << per_shift, f1 = min(R, f0 + per);
   uint32_t* mine = hist + warp * p.E;
   for (int f = f0 + lane; f - lane < f1; f += 32) {
     const int e = f < f1 ? ids[f] : kNoUnit;
     const uint32_t same = __match_any_sync(0xffffffffu, e);
-    if (e != kNoUnit && (same & ((1u << lane) - 1u)) == 0) mine[e] += __popc(same);
+    const int ahead = __popc(same & ((1u << lane) - 1u));
+    const uint32_t so_far = e != kNoUnit ? mine[e] : 0;
+    __syncwarp();
+    if (e != kNoUnit) {
+      place[f] = (uint16_t)(so_far + ahead);
+      if (ahead == 0) mine[e] = so_far + __popc(same);
+    }
     __syncwarp();
   }
   __syncthreads();
@@ -481,6 +502,7 @@ __device__ void build_units(const FewParams& p, const Schedule& s, uint8_t* scra
   uint32_t sum = 0;
   for (int e = e0; e < e1; ++e) {
     uint32_t rows = 0;
+#pragma unroll 4
     for (int w = 0; w < W; ++w) {
       const uint32_t v = hist[w * p.E + e];
       hist[w * p.E + e] = rows;
@@ -513,22 +535,17 @@ __device__ void build_units(const FewParams& p, const Schedule& s, uint8_t* scra
   }
   if (threadIdx.x == nthreads - 1) ctl->units = (int)(at >> 16);
   __syncthreads();
-  for (int f = f0 + lane; f - lane < f1; f += 32) {
-    const int e = f < f1 ? ids[f] : kNoUnit;
-    const uint32_t same = __match_any_sync(0xffffffffu, e);
-    const int ahead = __popc(same & ((1u << lane) - 1u));
-    const int place = e != kNoUnit ? (int)mine[e] + ahead : 0;  // among the expert's rows
-    __syncwarp();
-    if (e != kNoUnit) {
-      if (ahead == 0) mine[e] += __popc(same);
-      s.perm[s.offset[e] + place] = (uint16_t)f;
-      s.token[s.offset[e] + place] = (uint16_t)(f / p.k);
-      s.unit_of[f] = (uint16_t)(s.unit0[e] + (place >> shift));
-      s.row_of[f] = (uint8_t)(place & (p.unit_rows - 1));
-    } else if (f < f1) {
-      s.unit_of[f] = (uint16_t)kNoUnit;
-    }
-    __syncwarp();
+#pragma unroll 2
+  for (int f = threadIdx.x; f < R; f += nthreads) {
+    const int e = ids[f];
+    s.unit_of[f] = (uint16_t)kNoUnit;
+    if (e == kNoUnit) continue;
+    const int n = (int)hist[(f >> per_shift) * p.E + e] + place[f];  // among the expert's rows
+    const int to = s.offset[e] + n;
+    s.perm[to] = (uint16_t)f;
+    s.token[to] = (uint16_t)(f / p.k);
+    s.unit_of[f] = (uint16_t)(s.unit0[e] + (n >> shift));
+    s.row_of[f] = (uint8_t)(n & (p.unit_rows - 1));
   }
   __syncthreads();
 }
@@ -582,63 +599,85 @@ __device__ __forceinline__ void store_hidden(const FewParams& p, int row, int n,
   }
 }
 
-// The parts of a tile of a that is split along K, added in the order of K (the
-// tile ends the first run, and begins the others), and a of the sums.  A warp
-// takes every fourth row, a lane four columns; four parts are in flight together.
+// a of four columns of a row, from the sums of its h and u.
 template <bool MX>
-__device__ void join_hidden(const FewParams& p, const Cut& cut, const Seg& s, int rank, int half, int first, int last,
-                            int r0, int n, int warp, int lane) {
-  const int slot_floats = 2 * p.unit_rows * 128;
-  const int col = s.n * 128 + lane * 4;
-  const float* base = p.part + lane * 4;
-#pragma unroll 1
-  for (int row = warp; row < n; row += 4) {
-    float4 h = make_float4(0.0f, 0.0f, 0.0f, 0.0f), u = h;
-#pragma unroll 1
-    for (int o0 = first; o0 <= last; o0 += 4) {
-      float4 vh[4], vu[4];
+__device__ __forceinline__ void store_hidden4(const FewParams& p, int row, int col, int lane, bool in, float4 h,
+                                              float4 u) {
+  const long at = (long)row * p.I + col;
+  const float a[4] = {silu_mul(h.x, u.x), silu_mul(h.y, u.y), silu_mul(h.z, u.z), silu_mul(h.w, u.w)};
+  if constexpr (MX) {
+    // eight lanes hold a block
+    uint32_t top = 0;
 #pragma unroll
-      for (int o = 0; o < 4; ++o) {
-        vh[o] = vu[o] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (o0 + o <= last) {
-          const int slot = 4 * ((o0 + o) * cut.group + rank) + 2 * half + (o0 + o == first ? 1 : 0);
-          const float* from = base + (long)slot * slot_floats + row * 128;
-          vh[o] = __ldcg(reinterpret_cast<const float4*>(from));
-          vu[o] = __ldcg(reinterpret_cast<const float4*>(from + p.unit_rows * 128));
-        }
-      }
+    for (int i = 0; i < 4; ++i) top = max(top, __float_as_uint(fabsf(a[i])));
 #pragma unroll
-      for (int o = 0; o < 4; ++o) {
-        h.x += vh[o].x, h.y += vh[o].y, h.z += vh[o].z, h.w += vh[o].w;
-        u.x += vu[o].x, u.y += vu[o].y, u.z += vu[o].z, u.w += vu[o].w;
-      }
-    }
-    const long at = (long)(r0 + row) * p.I + col;
-    const float a[4] = {silu_mul(h.x, u.x), silu_mul(h.y, u.y), silu_mul(h.z, u.z), silu_mul(h.w, u.w)};
-    if constexpr (MX) {
-      // eight lanes hold a block
-      uint32_t top = 0;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) top = max(top, __float_as_uint(fabsf(a[i])));
-#pragma unroll
-      for (int o = 1; o < 8; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-      const int X = mx_block_exponent(__uint_as_float(top));
-      const float inv = mx_exp2_int(-X);
-      *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.a) + at) =
-          mx_cvt_e4m3x2(a[0] * inv, a[1] * inv) | (uint32_t)mx_cvt_e4m3x2(a[2] * inv, a[3] * inv) << 16;
+    for (int o = 1; o < 8; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const int X = mx_block_exponent(__uint_as_float(top));
+    const float inv = mx_exp2_int(-X);
+    const uint32_t codes =
+        mx_cvt_e4m3x2(a[0] * inv, a[1] * inv) | (uint32_t)mx_cvt_e4m3x2(a[2] * inv, a[3] * inv) << 16;
+    if (in) {
+      *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.a) + at) = codes;
       if ((lane & 7) == 0) p.asf[at / 32] = (uint8_t)(X + 127);
-    } else {
-      __nv_bfloat16* hi = static_cast<__nv_bfloat16*>(p.a) + at;
-      float back[4], left[4];
+    }
+  } else {
+    __nv_bfloat16* hi = static_cast<__nv_bfloat16*>(p.a) + at;
+    float back[4], left[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        back[i] = bf16_round(a[i]);
-        left[i] = isinf(back[i]) ? 0.0f : a[i] - back[i];
-      }
+    for (int i = 0; i < 4; ++i) {
+      back[i] = bf16_round(a[i]);
+      left[i] = isinf(back[i]) ? 0.0f : a[i] - back[i];
+    }
+    if (in) {
       *reinterpret_cast<uint2*>(hi) = make_uint2(pack_bf16x2(back[0], back[1]), pack_bf16x2(back[2], back[3]));
       *reinterpret_cast<uint2*>(hi + (long)p.T * p.k * p.I) =
           make_uint2(pack_bf16x2(left[0], left[1]), pack_bf16x2(left[2], left[3]));
     }
+  }
+}
+
+// The parts of a tile of a that is split along K, added in the order of K (the
+// tile ends the first run, and begins the others), and a of the sums.  A warp
+// takes every fourth row, ROWS of them at a time, a lane four columns; the
+// loads of PARTS parts of each are in flight together.
+template <bool MX, int ROWS, int PARTS>
+__device__ __forceinline__ void join_hidden(const FewParams& p, const Cut& cut, const Seg& s, int rank, int half,
+                                            int first, int last, int r0, int n, int warp, int lane) {
+  const int slot_floats = 2 * p.unit_rows * 128;
+  const int col = s.n * 128 + lane * 4;
+  const float* base = p.part + lane * 4;
+#pragma unroll 1
+  for (int row = warp; row < n; row += 4 * ROWS) {
+    float4 h[ROWS], u[ROWS];
+#pragma unroll
+    for (int m = 0; m < ROWS; ++m) h[m] = u[m] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 1
+    for (int o0 = first; o0 <= last; o0 += PARTS) {
+      float4 vh[ROWS][PARTS], vu[ROWS][PARTS];
+#pragma unroll
+      for (int o = 0; o < PARTS; ++o) {
+        const int slot = 4 * ((o0 + o) * cut.group + rank) + 2 * half + (o0 + o == first ? 1 : 0);
+        const float* from = base + (long)slot * slot_floats + row * 128;
+#pragma unroll
+        for (int m = 0; m < ROWS; ++m) {
+          vh[m][o] = vu[m][o] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          if (o0 + o <= last && row + 4 * m < n) {
+            vh[m][o] = __ldcg(reinterpret_cast<const float4*>(from + m * 512));
+            vu[m][o] = __ldcg(reinterpret_cast<const float4*>(from + m * 512 + p.unit_rows * 128));
+          }
+        }
+      }
+#pragma unroll
+      for (int m = 0; m < ROWS; ++m)
+#pragma unroll
+        for (int o = 0; o < PARTS; ++o) {
+          h[m].x += vh[m][o].x, h[m].y += vh[m][o].y, h[m].z += vh[m][o].z, h[m].w += vh[m][o].w;
+          u[m].x += vu[m][o].x, u[m].y += vu[m][o].y, u[m].z += vu[m][o].z, u[m].w += vu[m][o].w;
+        }
+    }
+#pragma unroll
+    for (int m = 0; m < ROWS; ++m)
+      store_hidden4<MX>(p, r0 + row + 4 * m, col, lane, row + 4 * m < n, h[m], u[m]);
   }
 }
 
@@ -677,19 +716,15 @@ __device__ __forceinline__ void combine(const FewParams& p, const Schedule& s, c
     float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 1
     for (int j0 = 0; j0 < p.k; j0 += LANES * EACH) {
-      const float4 *next[EACH];
-      int more[EACH];  // parts past the first
-      float w[EACH];
-      float4 y[EACH];
+      const float4 *from[EACH], *next[EACH];
+      int more[EACH];  // parts past the first; -1: nothing there
 #pragma unroll
       for (int m = 0; m < EACH; ++m) {
         const int j = j0 + sub + m, f = t * p.k + j;
-        more[m] = -1;
-        w[m] = 0.0f;
-        y[m] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         const int unit = in && j < p.k ? s.unit_of[f] : kNoUnit;
+        more[m] = -1;
+        from[m] = next[m] = reinterpret_cast<const float4*>(p.y);
         if (unit != kNoUnit) {
-          w[m] = p.scores[f];
           const int half = unit >= cuts[1].unit0;
           int first, last;
           if (table) {
@@ -700,18 +735,21 @@ __device__ __forceinline__ void combine(const FewParams& p, const Schedule& s, c
             seg_runs(cuts[half], (unit - cuts[half].unit0) * supers + sup, first, last);
           }
           more[m] = last - first;
-          const float* from = p.y + (long)f * p.H + col;
-          if (more[m]) {
-            const float* at = part_at + s.row_of[f] * 128;
-            from = at + (long)((first * group + rank) * 4 + half * 2 + 1) * slot_floats;
-            next[m] = reinterpret_cast<const float4*>(at + (long)(((first + 1) * group + rank) * 4 + half * 2) * slot_floats);
-          }
-          y[m] = __ldcg(reinterpret_cast<const float4*>(from));
+          const float* at = part_at + s.row_of[f] * 128;
+          from[m] = reinterpret_cast<const float4*>(
+              more[m] ? at + (long)((first * group + rank) * 4 + half * 2 + 1) * slot_floats : p.y + (long)f * p.H + col);
+          next[m] = reinterpret_cast<const float4*>(at + (long)(((first + 1) * group + rank) * 4 + half * 2) * slot_floats);
         }
       }
-      float4 z[EACH];
+      float w[EACH];
+      float4 y[EACH], z[EACH];
 #pragma unroll
-      for (int m = 0; m < EACH; ++m) z[m] = more[m] > 0 ? __ldcg(next[m]) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      for (int m = 0; m < EACH; ++m) {
+        const float4 none = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        w[m] = more[m] >= 0 ? p.scores[t * p.k + j0 + sub + m] : 0.0f;
+        y[m] = more[m] >= 0 ? __ldcg(from[m]) : none;
+        z[m] = more[m] > 0 ? __ldcg(next[m]) : none;
+      }
 #pragma unroll
       for (int m = 0; m < EACH; ++m) {
         y[m].x += z[m].x, y[m].y += z[m].y, y[m].z += z[m].z, y[m].w += z[m].w;
@@ -848,8 +886,7 @@ __global__ void __launch_bounds__(MX ? 320 : 256, 1) few_kernel(const __grid_con
     const int blocks = units * (p.I / 128) * (p.H / kEl);
     const int half = blocks >= kHalvesFrom * (int)gridDim.x ? (units + 1) / 2 : units;
     const int u0 = i & 1 ? half : 0, nu = i & 1 ? units - half : half;
-    const Cut cut = i < 2 ? make_cut(p.I / 128, p.H / kEl, u0, nu, gridDim.x)
-                          : make_cut((p.H + 255) / 256, p.I / kEl, u0, nu, gridDim.x);
+    const Cut cut = make_cut(p.gemm[i >> 1], u0, nu, gridDim.x);
     ctl->cuts[i] = cut;
     ctl->runs[i] = run_of(cut, c);
   }
@@ -1116,7 +1153,10 @@ __global__ void __launch_bounds__(MX ? 320 : 256, 1) few_kernel(const __grid_con
           __syncwarp();
           named_bar_sync(1, kEpilogue);
           if (!ctl->last) continue;
-          join_hidden<MX>(p, cut, s, c % cut.group, half, first, last, r0, n, warp - 4, lane);
+          if (n <= 4)
+            join_hidden<MX, 1, 4>(p, cut, s, c & (cut.group - 1), half, first, last, r0, n, warp - 4, lane);
+          else
+            join_hidden<MX, 4, MX ? 2 : 3>(p, cut, s, c & (cut.group - 1), half, first, last, r0, n, warp - 4, lane);
         }
         // a finished tile of a
         named_bar_sync(1, kEpilogue);
@@ -1202,6 +1242,18 @@ int units_bound(int T, int E, int k, int unit_rows) {
   return n < R ? n : R;
 }
 
+// Neighbouring column tiles are taken by up to 8 CTAs side by side, so that
+// they read up to 2 KB of each weight row together.  1 token, H 7168, I 2048,
+// MXFP8: 70 us, each tile apart 76; 16 tokens in bf16: 758 and 778.
+FewShape gemm_shape(int tiles, int kb, int ctas) {
+  FewShape f;
+  f.group_shift = 3;
+  while (f.group_shift > 0 && (tiles % (1 << f.group_shift) || (1 << f.group_shift) > ctas)) --f.group_shift;
+  f.supers = tiles >> f.group_shift;
+  f.kb = kb;
+  return f;
+}
+
 // Tokens side by side in a part of the logits, and the parts: at most 64,
 // enough SMs to read Wr at once and few enough parts to add up quickly.
 void logit_parts(int T, int H, int ctas, int* tokens, int* parts, int* rows) {
@@ -1268,6 +1320,8 @@ cudaError_t launch_few(FewParams p, bool mx, int* launches, cudaStream_t st) {
     return cudaErrorInvalidValue;
   p.unit_rows = few_unit_rows(p.T);
   p.max_units = units_bound(p.T, p.E, p.k, p.unit_rows);
+  p.gemm[0] = gemm_shape(p.I / 128, p.H / kel, ctas);
+  p.gemm[1] = gemm_shape((p.H + 255) / 256, p.I / kel, ctas);
   logit_parts(p.T, p.H, ctas, &p.logit_tokens, &p.h_parts, &p.h_rows);
   const size_t stage = 2 * kATile + (size_t)p.unit_rows * (mx ? 128 : 256) + (mx ? kSfBytes : 0);
   const size_t rest = 1024 + sizeof(Ctl) + schedule_bytes(p.E, p.T * p.k, p.max_units);

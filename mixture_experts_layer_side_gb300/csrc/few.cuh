@@ -28,7 +28,13 @@ struct FewMaps {
   CUtensorMap sf[3];  // MXFP8: their scales
 };
 
+// What a GEMM's cut (few.cu) has of the call's sizes.
+struct FewShape {
+  int group_shift, supers, kb;
+};
+
 struct FewParams {
+  FewShape gemm[2];
   int T, H, I, E, k;
   int unit_rows, stages;
   int32_t* hdr;
