@@ -46,7 +46,8 @@ constexpr int kMaxFewStages = 8;
 constexpr int kATile = 128 * 128;      // one A operand: 128 output columns x 128 bytes of K
 constexpr int kSfBytes = 1024 + 1024 + 512;  // MXFP8, per stage: raw and tiled A scales (two tiles), B scales
 constexpr int kProducers = 64;         // threads that bring the tokens' operand
-constexpr int kEpilogue = 128;
+constexpr int kEpilogue = 256;         // two warps for each quarter of the accumulator's rows
+constexpr int kLogitWarps = 8;
 constexpr int kLogitTokens = 8;        // tokens side by side in the router's logits
 
 // header words
@@ -221,7 +222,7 @@ __device__ __forceinline__ uint32_t* word(const FewParams& p, int i) { return re
 template <int TOK>
 __device__ __forceinline__ void router_logits(const FewParams& p, uint8_t* smem, int nthreads) {
   const int groups = (p.T + TOK - 1) / TOK;
-  const int warps = nthreads / 32, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warps = kLogitWarps, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int part = blockIdx.x / groups, t0 = (blockIdx.x % groups) * TOK;
   if (part >= p.h_parts) return;
   const int nt = min(TOK, p.T - t0);
@@ -246,7 +247,7 @@ __device__ __forceinline__ void router_logits(const FewParams& p, uint8_t* smem,
       for (int i = 0; i < 8; ++i) acc[t][i] = 0.0f;
     // eight rows a warp in flight
     constexpr int kAhead = 8;
-    for (int hb = warp * down + lane / across; hb - lane / across < rows; hb += warps * down * kAhead) {
+    for (int hb = warp * down + lane / across; warp < warps && hb - lane / across < rows; hb += warps * down * kAhead) {
       uint4 v[kAhead];
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
@@ -287,7 +288,7 @@ __device__ __forceinline__ void router_logits(const FewParams& p, uint8_t* smem,
       for (int t = 0; t < TOK; ++t)
 #pragma unroll
         for (int i = 0; i < 8; ++i) acc[t][i] += __shfl_xor_sync(0xffffffffu, acc[t][i], o);
-    if (lane < across)
+    if (lane < across && warp < warps)
 #pragma unroll
       for (int t = 0; t < TOK; ++t) {
         float4* r = reinterpret_cast<float4*>(red + (warp * TOK + t) * 256 + lane * 8);
@@ -638,7 +639,7 @@ __device__ __forceinline__ void store_hidden4(const FewParams& p, int row, int c
 
 // The parts of a tile of a that is split along K, added in the order of K (the
 // tile ends the first run, and begins the others), and a of the sums.  A warp
-// takes every fourth row, ROWS of them at a time, a lane four columns; the
+// takes every eighth row, ROWS of them at a time, a lane four columns; the
 // loads of PARTS parts of each are in flight together.
 template <bool MX, int ROWS, int PARTS>
 __device__ __forceinline__ void join_hidden(const FewParams& p, const Cut& cut, const Seg& s, int rank, int half,
@@ -647,7 +648,7 @@ __device__ __forceinline__ void join_hidden(const FewParams& p, const Cut& cut, 
   const int col = s.n * 128 + lane * 4;
   const float* base = p.part + lane * 4;
 #pragma unroll 1
-  for (int row = warp; row < n; row += 4 * ROWS) {
+  for (int row = warp; row < n; row += 8 * ROWS) {
     float4 h[ROWS], u[ROWS];
 #pragma unroll
     for (int m = 0; m < ROWS; ++m) h[m] = u[m] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -661,9 +662,9 @@ __device__ __forceinline__ void join_hidden(const FewParams& p, const Cut& cut, 
 #pragma unroll
         for (int m = 0; m < ROWS; ++m) {
           vh[m][o] = vu[m][o] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          if (o0 + o <= last && row + 4 * m < n) {
-            vh[m][o] = __ldcg(reinterpret_cast<const float4*>(from + m * 512));
-            vu[m][o] = __ldcg(reinterpret_cast<const float4*>(from + m * 512 + p.unit_rows * 128));
+          if (o0 + o <= last && row + 8 * m < n) {
+            vh[m][o] = __ldcg(reinterpret_cast<const float4*>(from + m * 1024));
+            vu[m][o] = __ldcg(reinterpret_cast<const float4*>(from + m * 1024 + p.unit_rows * 128));
           }
         }
       }
@@ -677,7 +678,7 @@ __device__ __forceinline__ void join_hidden(const FewParams& p, const Cut& cut, 
     }
 #pragma unroll
     for (int m = 0; m < ROWS; ++m)
-      store_hidden4<MX>(p, r0 + row + 4 * m, col, lane, row + 4 * m < n, h[m], u[m]);
+      store_hidden4<MX>(p, r0 + row + 8 * m, col, lane, row + 8 * m < n, h[m], u[m]);
   }
 }
 
@@ -787,8 +788,8 @@ __device__ __forceinline__ void combine(const FewParams& p, const Schedule& s, c
 }
 
 template <bool MX>
-__global__ void __launch_bounds__(MX ? 320 : 256, 1) few_kernel(const __grid_constant__ FewMaps maps, FewParams p) {
-  constexpr int kThreads = MX ? 320 : 256;
+__global__ void __launch_bounds__(MX ? 448 : 384, 1) few_kernel(const __grid_constant__ FewMaps maps, FewParams p) {
+  constexpr int kThreads = MX ? 448 : 384;  // warps: weights, MMA, 2 tokens, 8 epilogue, MXFP8: 2 scales
   constexpr int kEl = MX ? 128 : 64;  // K per block
   extern __shared__ uint8_t raw_smem[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~uintptr_t(1023));
@@ -1086,7 +1087,7 @@ __global__ void __launch_bounds__(MX ? 320 : 256, 1) few_kernel(const __grid_con
       }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
-  } else if (warp < 8) {
+  } else if (warp < 12) {
     // ---------------------------------------------------------------- epilogue
     const int q = warp & 3;  // TMEM lanes this warp may read
     const int tid = threadIdx.x - 128;
@@ -1111,7 +1112,7 @@ __global__ void __launch_bounds__(MX ? 320 : 256, 1) few_kernel(const __grid_con
         // four slots a CTA: of each half, the tile that its run ends in (1) or begins in (0)
         float* slot = p.part + (long)(4 * c + 2 * half + (s.k0 == 0 ? 1 : 0)) * slot_floats + lane_col;
 #pragma unroll 1
-        for (int i0 = 0; i0 < n; i0 += 4) {
+        for (int i0 = ((warp - 4) >> 2) * 4; i0 < n; i0 += 8) {
           float v0[4], v1[4];
           tmem_ld4x2(d + i0, d + d_cols + i0, v0, v1);
           if (!MX && g == 1) {
@@ -1153,10 +1154,10 @@ __global__ void __launch_bounds__(MX ? 320 : 256, 1) few_kernel(const __grid_con
           __syncwarp();
           named_bar_sync(1, kEpilogue);
           if (!ctl->last) continue;
-          if (n <= 4)
+          if (n <= 8)
             join_hidden<MX, 1, 4>(p, cut, s, c & (cut.group - 1), half, first, last, r0, n, warp - 4, lane);
           else
-            join_hidden<MX, 4, MX ? 2 : 3>(p, cut, s, c & (cut.group - 1), half, first, last, r0, n, warp - 4, lane);
+            join_hidden<MX, 2, 3>(p, cut, s, c & (cut.group - 1), half, first, last, r0, n, warp - 4, lane);
         }
         // a finished tile of a
         named_bar_sync(1, kEpilogue);
@@ -1172,7 +1173,7 @@ __global__ void __launch_bounds__(MX ? 320 : 256, 1) few_kernel(const __grid_con
     // ---------------------------------------------------------------- MXFP8: weight scales
     // from [4 K blocks][128 columns] as they lie in memory to the layout that
     // the tensor core's scale copy takes; one warp per A tile
-    const int i = warp - 8;
+    const int i = warp - 12;
     uint32_t stage = 0, phase = 0;
     bool fine = true;
     for (int ph = 0; ph < 4; ++ph) {
@@ -1335,7 +1336,7 @@ cudaError_t launch_few(FewParams p, bool mx, int* launches, cudaStream_t st) {
   cudaError_t e = allow_smem(kernel, kMost, allowed[mx]);
   if (e != cudaSuccess) return e;
   void* args[] = {&maps, &p};
-  e = cudaLaunchCooperativeKernel(kernel, dim3(ctas), dim3(mx ? 320 : 256), args, smem, st);
+  e = cudaLaunchCooperativeKernel(kernel, dim3(ctas), dim3(mx ? 448 : 384), args, smem, st);
   if (e != cudaSuccess) return e;
   *launches = 1;
   return cudaSuccess;
