@@ -229,9 +229,17 @@ __device__ __forceinline__ void router_logits(const FewParams& p, uint8_t* smem,
   const int h0 = part * p.h_rows, rows = min(p.h_rows, p.H - h0);
   float* xs = reinterpret_cast<float*>(smem);                 // [h_rows][TOK]
   float* red = xs + (size_t)p.h_rows * TOK;                   // [warps][TOK][256]
-  for (int i = threadIdx.x; i < rows * TOK; i += nthreads) {
-    const int t = i / rows, h = i - t * rows;
-    xs[h * TOK + t] = t < nt ? __bfloat162float(p.x[(long)(t0 + t) * p.H + h0 + h]) : 0.0f;
+  // (h0 and rows are multiples of 8)
+  for (int i = threadIdx.x; i < rows / 8 * TOK; i += nthreads) {
+    const int t = i % TOK, h = i / TOK * 8;
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (t < nt) v = __ldg(reinterpret_cast<const uint4*>(p.x + (long)(t0 + t) * p.H + h0 + h));
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      xs[(h + 2 * m) * TOK + t] = __uint_as_float(w[m] << 16);
+      xs[(h + 2 * m + 1) * TOK + t] = __uint_as_float(w[m] & 0xffff0000u);
+    }
   }
   __syncthreads();
   int across = 1;  // lanes along a row
@@ -310,10 +318,11 @@ __device__ __forceinline__ void router_logits(const FewParams& p, uint8_t* smem,
 
 // Selection and scores of one token from the parts of its logits: groups of
 // threads take shares of the parts, so that the loads are in flight together.
+// (smem: first the bias, which the caller brings while the parts are awaited.)
 __device__ void router_select(const FewParams& p, int t, float* smem, int nthreads) {
-  float* row = smem;                  // [E]
-  float* bias = row + p.E;            // [E]
-  float* red = bias + p.E;            // [shares][E]
+  float* bias = smem;                 // [E]
+  float* row = bias + p.E;            // [E]
+  float* red = row + p.E;             // [shares][E]
   const int w = p.E % 4 == 0 ? 4 : 1; // experts a load brings
   const int cols = (p.E + w - 1) / w;
   const int shares = max(1, min(16, nthreads / cols));
@@ -346,11 +355,10 @@ __device__ void router_select(const FewParams& p, int t, float* smem, int nthrea
         to[0] = s;
       }
     }
-  if (p.bias)
-    for (int e = threadIdx.x; e < p.E; e += nthreads) bias[e] = p.bias[e];
   __syncthreads();
   for (int e = threadIdx.x; e < p.E; e += nthreads) {
     float s = red[e];
+#pragma unroll 4
     for (int i = 1; i < shares; ++i) s += red[i * p.E + e];
     row[e] = s;
   }
@@ -861,6 +869,8 @@ __global__ void __launch_bounds__(MX ? 448 : 384, 1) few_kernel(const __grid_con
   }
   if (p.Wr) {
     if (blockIdx.x < p.T) {
+      if (p.bias)
+        for (int e = threadIdx.x; e < p.E; e += kThreads) reinterpret_cast<float*>(smem)[e] = p.bias[e];
       if (threadIdx.x == 0) ctl->go = wait_flag_geq(word(p, kWordPrepared), gridDim.x, wc) ? 1 : 0;
       __syncthreads();
       if (ctl->go)
@@ -1221,7 +1231,7 @@ __global__ void __launch_bounds__(MX ? 448 : 384, 1) few_kernel(const __grid_con
       if (one)
         combine<8, 1>(p, sched, ctl->cuts + 2, table, kThreads);
       else
-        combine<1, 4>(p, sched, ctl->cuts + 2, table, kThreads);
+        combine<1, 8>(p, sched, ctl->cuts + 2, table, kThreads);
     }
   }
   if (threadIdx.x == 0) {
