@@ -12,7 +12,11 @@
 // token) pairs, then sums over runs of equal ids.  No float is added to by
 // two threads: the order of each sum is fixed by the input.
 //
-//  * The sort is one cluster of kSortCtas CTAs: the pairs of a few thousand to
+//  * Up to kRankTokens tokens are placed by counting the pairs before each of
+//    them, 16 threads a token: no pass waits for another.  (With the sums of
+//    1,024 bf16 columns: 2,048 tokens 15 us, by the radix sort 23; 8,192
+//    tokens 36 and 31.)
+//  * More are sorted by one cluster of kSortCtas CTAs: the pairs of a few thousand to
 //    a few million tokens are small beside dx, and a cluster's barriers and
 //    distributed shared memory join its histograms without a launch or a
 //    device-wide barrier per pass.  When the gradient is written whole, the
@@ -24,6 +28,7 @@
 //  * Accumulating into f32 rows is one vector reduction at L2 per row and
 //    slab, which nothing waits for.
 #include <cooperative_groups.h>
+#include <limits.h>
 
 #include "embed.cuh"
 #include "tc.cuh"
@@ -124,8 +129,7 @@ __device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t 
   asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(src)), "r"(bytes)
                : "memory");
 }
-__device__ void zero_rows(const EmbedParams& p, uint32_t* taken, int grad_bytes) {
-  const int ctas = gridDim.x - kSortCtas, c = blockIdx.x - kSortCtas;
+__device__ void zero_rows(const EmbedParams& p, uint32_t* taken, int grad_bytes, int c, int ctas) {
   const int lo = (int)((long)p.V * c / ctas), hi = (int)((long)p.V * (c + 1) / ctas);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const long row_bytes = (long)p.H * grad_bytes;
@@ -171,6 +175,49 @@ __device__ void zero_rows(const EmbedParams& p, uint32_t* taken, int grad_bytes)
   bulk_wait<0>();
 }
 
+// The key of token i in the sort: its id, or V (which goes last) for one that
+// takes no part -- padding, or an id outside [0, V).
+__device__ __forceinline__ int key_of(const EmbedParams& p, long i, bool tell) {
+  const int id = p.ids[i];
+  if (id == p.pad_id) return p.V;
+  if (id >= 0 && id < p.V) return id;
+  if (tell) atomicOr(p.hdr + kHdrError, MOK_ERRBIT_BAD_INDEX);
+  return p.V;
+}
+
+// Few tokens: a token's place is the number of pairs before it, a pair being
+// one word, key over token (of `bits` bits).  A CTA places kRankShare tokens,
+// kRankLanes threads each a share of the pairs; CTAs past `ranks` write zeros.
+constexpr int kRankTokens = 4096;
+constexpr int kRankLanes = 16, kRankShare = kSortThreads / kRankLanes;
+__global__ void __launch_bounds__(kSortThreads) embed_rank_kernel(EmbedParams p, int bits, int ranks, int grad_bytes) {
+  extern __shared__ __align__(16) uint32_t pairs[];
+  griddep_launch_dependents();
+  if (blockIdx.x >= ranks) {
+    zero_rows(p, pairs, grad_bytes, blockIdx.x - ranks, gridDim.x - ranks);
+    return;
+  }
+  // to whole vectors, with pairs that come before none
+  const int padded = (p.N + 3) & ~3;
+  for (int i = threadIdx.x; i < padded; i += kSortThreads)
+    pairs[i] = i < p.N ? (uint32_t)key_of(p, i, blockIdx.x == 0) << bits | i : 0xffffffffu;
+  __syncthreads();
+  const int i = blockIdx.x * kRankShare + threadIdx.x / kRankLanes, lane = threadIdx.x % kRankLanes;
+  const uint32_t pair = i < p.N ? pairs[i] : 0;
+  int before = 0;
+#pragma unroll 4
+  for (int j = lane * 4; j < padded; j += kRankLanes * 4) {
+    const uint4 k = *reinterpret_cast<const uint4*>(pairs + j);
+    before += (k.x < pair) + (k.y < pair) + (k.z < pair) + (k.w < pair);
+  }
+#pragma unroll
+  for (int o = kRankLanes / 2; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
+  if (i < p.N && lane == 0) {
+    p.key[0][before] = (int32_t)(pair >> bits);
+    p.pos[0][before] = i;
+  }
+}
+
 // Stable least-significant-digit radix sort of the tokens by id; a token
 // that takes no part (padding, or an id outside [0, V)) gets key V and goes
 // last.  `bits` per pass, `passes` passes; the sorted pairs end in key/pos
@@ -181,7 +228,7 @@ __global__ void __launch_bounds__(kSortThreads) __cluster_dims__(kSortCtas, 1, 1
   extern __shared__ int sm[];
   griddep_launch_dependents();
   if (blockIdx.x >= kSortCtas) {
-    zero_rows(p, reinterpret_cast<uint32_t*>(sm), grad_bytes);
+    zero_rows(p, reinterpret_cast<uint32_t*>(sm), grad_bytes, blockIdx.x - kSortCtas, gridDim.x - kSortCtas);
     return;
   }
   int* hist = sm;                                // [kSortWarps][digits]
@@ -204,16 +251,7 @@ __global__ void __launch_bounds__(kSortThreads) __cluster_dims__(kSortCtas, 1, 1
     const int32_t* pin = p.pos[pass & 1];
     int32_t* kout = p.key[(pass + 1) & 1];
     int32_t* pout = p.pos[(pass + 1) & 1];
-    auto key_at = [&](long i) {
-      if (pass > 0) return kin[i];
-      const int id = p.ids[i];
-      if (id == p.pad_id) return p.V;
-      if (id < 0 || id >= p.V) {
-        atomicOr(p.hdr + kHdrError, MOK_ERRBIT_BAD_INDEX);
-        return p.V;
-      }
-      return id;
-    };
+    auto key_at = [&](long i) { return pass > 0 ? kin[i] : key_of(p, i, true); };
     for (int d = threadIdx.x; d < kSortWarps * digits; d += kSortThreads) hist[d] = 0;
     __syncthreads();
     int* mine = hist + warp * digits;
@@ -479,23 +517,39 @@ template <typename D, typename G>
 cudaError_t launch_backward(const EmbedParams& p, int* launches, cudaStream_t st) {
   *launches = 0;
   if (p.N == 0) return p.accumulate ? cudaSuccess : cudaMemsetAsync(p.dtable, 0, (size_t)p.V * p.H * sizeof(G), st);
-  // keys are 0 .. V
-  int key_bits = 3;  // (8 digits at least: kQuarter lanes each fill a warp)
-  while (key_bits < 31 && (1 << key_bits) <= p.V) ++key_bits;
-  const int passes = (key_bits + 9) / 10, bits = (key_bits + passes - 1) / passes;
-  constexpr size_t kMost = ((size_t)(kSortWarps + 2) * kMaxDigits + kSortWarps) * 4;
-  static_assert(kMarkRows / 8 + kZeroBytes <= kMost, "what marks and zeros rows fits the sort's shared memory");
-  static std::atomic<uint64_t> allowed{0};
-  cudaError_t e = allow_smem((const void*)embed_sort_kernel, kMost, allowed);
-  if (e != cudaSuccess) return e;
-  // the zeros of the rows that no token has: by the clusters beside the sort's
-  const int sms = device_sm_count(), zero = p.accumulate ? 0 : sms > 2 * kSortCtas ? sms / kSortCtas - 1 : 1;
-  embed_sort_kernel<<<kSortCtas * (1 + zero), kSortThreads, kMost, st>>>(p, bits, passes, (int)sizeof(G));
-  e = cudaGetLastError();
+  const int sms = device_sm_count();
+  int sorted = 0;  // where the pairs end
+  int token_bits = 0;
+  while ((1 << token_bits) < p.N) ++token_bits;
+  if (p.N <= kRankTokens && p.V < (1ll << (32 - token_bits))) {
+    // (both kinds of CTA fit an SM together)
+    const int ranks = (p.N + kRankShare - 1) / kRankShare, zero = p.accumulate ? 0 : sms > 0 ? sms : 1;
+    constexpr size_t kBytes = kMarkRows / 8 + kZeroBytes;
+    static_assert(kRankTokens * 4 <= kBytes, "the keys fit");
+    static std::atomic<uint64_t> allowed{0};
+    const cudaError_t e = allow_smem((const void*)embed_rank_kernel, kBytes, allowed);
+    if (e != cudaSuccess) return e;
+    embed_rank_kernel<<<ranks + zero, kSortThreads, kBytes, st>>>(p, token_bits, ranks, (int)sizeof(G));
+  } else {
+    // keys are 0 .. V
+    int key_bits = 3;  // (8 digits at least: kQuarter lanes each fill a warp)
+    while (key_bits < 31 && (1 << key_bits) <= p.V) ++key_bits;
+    const int passes = (key_bits + 9) / 10, bits = (key_bits + passes - 1) / passes;
+    constexpr size_t kMost = ((size_t)(kSortWarps + 2) * kMaxDigits + kSortWarps) * 4;
+    static_assert(kMarkRows / 8 + kZeroBytes <= kMost, "what marks and zeros rows fits the sort's shared memory");
+    static std::atomic<uint64_t> allowed{0};
+    const cudaError_t e = allow_smem((const void*)embed_sort_kernel, kMost, allowed);
+    if (e != cudaSuccess) return e;
+    // the zeros of the rows that no token has: by the clusters beside the sort's
+    const int zero = p.accumulate ? 0 : sms > 2 * kSortCtas ? sms / kSortCtas - 1 : 1;
+    embed_sort_kernel<<<kSortCtas * (1 + zero), kSortThreads, kMost, st>>>(p, bits, passes, (int)sizeof(G));
+    sorted = passes & 1;
+  }
+  cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   // a thread's vector of dx may be half of one of the gradient, or two
   const bool vec = rows_of_vectors(p.dx, p.H, sizeof(D)) && rows_of_vectors(p.dtable, p.H, sizeof(G));
-  e = vec ? launch_sums<D, G, true>(p, passes & 1, st) : launch_sums<D, G, false>(p, passes & 1, st);
+  e = vec ? launch_sums<D, G, true>(p, sorted, st) : launch_sums<D, G, false>(p, sorted, st);
   *launches = 3;
   return e;
 }

@@ -100,7 +100,8 @@ CASES = [(1, 1, 1, "uniform"), (1, 1000, 256, "uniform"), (7, 3, 5, "uniform"), 
          (33, 9, 130, "one"), (64, 9, 512, "one"), (1000, 100, 264, "skew"), (3000, 50, 1003, "uniform"),
          (5000, 1, 64, "one"), (4096, 5000, 328, "skew"), (9000, 70000, 40, "skew"), (20000, 2000, 96, "one"),
          (2049, 1023, 33, "uniform"), (2049, 1024, 33, "uniform"), (70001, 300, 16, "skew"),
-         (300, 1100000, 8, "uniform")]
+         (300, 1100000, 8, "uniform"), (8192, 524287, 8, "skew"), (8193, 300, 24, "skew"), (4096, 1048575, 4, "uniform"),
+         (4096, 1048576, 4, "uniform"), (2000, 2097152, 2, "uniform")]
 
 
 @pytest.mark.parametrize("dx_type,grad", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "f32"), ("f32", "bf16")])
