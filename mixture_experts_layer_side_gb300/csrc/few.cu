@@ -1295,9 +1295,14 @@ FewLayout few_layout(const mok_shape& s, mok_precision prec) {
   // room for the units of any call of this H, I, E and k
   const size_t units = units_bound(MOK_FEW_MAX_TOKENS, s.E, s.k, 16);
   L.tiles = take(units * (s.I / 128) * 4);
-  int tokens, parts, rows;
-  logit_parts(s.T, s.H, ctas, &tokens, &parts, &rows);
-  L.logits = take((size_t)parts * s.T * s.E * 4);
+  // (the parts' number falls as tokens are added: room for every call of up to T tokens)
+  size_t logits = 0;
+  for (int t = 1; t <= s.T; ++t) {
+    int tokens, parts, rows;
+    logit_parts(t, s.H, ctas, &tokens, &parts, &rows);
+    if ((size_t)parts * t > logits) logits = (size_t)parts * t;
+  }
+  L.logits = take(logits * s.E * 4);
   L.xq = mx ? take((size_t)s.T * s.H) : 0;
   L.xsf = mx ? take((size_t)s.T * (s.H / 32)) : 0;
   L.a = take(R * s.I * (mx ? 1 : 4));

@@ -14,7 +14,7 @@ inline int few_unit_rows(int T) { return T <= 16 ? 16 : T <= 32 ? 32 : 64; }
 struct FewLayout {
   size_t header;   // int32 [kHeaderWords]: word 0 the error bits
   size_t tiles;    // int32 [units, I/128]: arrivals at the tiles of a
-  size_t logits;   // f32 [parts, T, E] router logits, in parts along H
+  size_t logits;   // f32 [parts, T, E] router logits, in parts along H (room for any smaller T's)
   size_t xq, xsf;  // MXFP8: codes [T, H] and scales [T, H/32] of x
   size_t a, asf;   // bf16 [2][T*k, I] (a, and what its rounding left); MXFP8: codes, and scales [T*k, I/32]
   size_t part;     // f32 [4 per CTA][2][unit rows][128] sums of tiles split along K

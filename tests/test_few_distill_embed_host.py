@@ -31,9 +31,15 @@ def test_few_host_checks(lib):
     assert lib.mok_few_workspace_size(good, lib.MOK_MXFP8) > 0
     assert lib.mok_few_workspace_size(shape(128, 256, 128, 8, 2)) > 0
     for bad in (shape(129, 256, 128, 8, 2), shape(0, 256, 128, 8, 2), shape(8, 200, 128, 8, 2),
-                shape(8, 256, 100, 8, 2), shape(8, 256, 128, 1025, 2), shape(8, 256, 128, 8, 33)):
+                shape(8, 256, 100, 8, 2), shape(8, 256, 128, 1025, 2), shape(8, 256, 128, 8, 33), shape(8, 32896, 128, 8, 2),
+                shape(8, 256, 32896, 8, 2)):
         assert lib.mok_few_workspace_size(bad) == 0
     assert L.mok_few_workspace_size(ctypes.byref(good), 7) == 0
+    # a workspace for more tokens serves fewer
+    for prec in (lib.MOK_BF16, lib.MOK_MXFP8):
+        for sizes in ((128, 128, 1024, 1), (256, 128, 8, 2), (7168, 2048, 256, 8)):
+            need = [lib.mok_few_workspace_size(shape(t, *sizes), prec) for t in range(1, 129)]
+            assert need == sorted(need) and need[0] > 0
     assert L.mok_few_workspace_size(None, 0) == 0
 
     def forward(s=good, prec=0, ws=A, n=BIG, idx=A, x=A, sc=A, W1=A, W3=A, W2=A, out=A):
