@@ -24,8 +24,9 @@
 //    the step a CTA brings its share, 32 KB where eight are enough, to shared
 //    memory with bulk copies, where it stays between the sum and the gradient;
 //    six such CTAs an SM are in different phases, so that loads and stores
-//    overlap.  (Shares held in registers let two CTAs an SM run: 876 us for
-//    4,096 rows of 131,072 bf16.)
+//    overlap: 395 us for 4,096 rows of 131,072 bf16, loss and gradient, 81% of
+//    the rate of a copy.  (Twice the threads a CTA: 412; a CTA a row of its own
+//    that streams it twice, the second time from L2: 471.)
 //  * The teacher's list (at most MOK_DISTILL_MAX_TOP entries) is a warp's
 //    work, hidden behind the row's copies.  Listed columns are stored after
 //    the rest, by the first entry that has them.
@@ -173,6 +174,20 @@ __device__ __noinline__ void row_store(Z* z, int V, int col, uint4 v) {
 #pragma unroll 1
   for (int k = 0; k < Vec<Z>::kN; ++k)
     if (col + k >= 0 && col + k < V) z[col + k] = e[k];
+}
+
+// Zeros in a share of a gradient row, on the row's own grid.
+template <typename Z>
+__device__ __forceinline__ void zero_share(const RowGrid<Z>& grad, int rank, int shares, int threads) {
+  const int most = (grad.vecs + shares - 1) / shares, v1 = min(grad.vecs, (rank + 1) * most);
+  const uint4 none = make_uint4(0, 0, 0, 0);
+#pragma unroll 4
+  for (int v = rank * most + threadIdx.x; v < v1; v += threads) {
+    if (grad.whole(v))
+      __stcs(reinterpret_cast<uint4*>(grad.z + grad.first(v)), none);
+    else
+      row_store(grad.z, grad.V, grad.first(v), none);
+  }
 }
 
 // ---------------------------------------------------------------- sums
@@ -338,7 +353,49 @@ __device__ __forceinline__ void store_loss(const DistillParams& q, long t, const
   }
 }
 
-// Both kernels: workers, and a last warp for the list.
+// The gradients of the listed columns in vectors [v0, v1) in place of their
+// logits; returns a bit for each of the lane's entries that is the first of
+// its column.  e_j q_base - sum of p: where there is one token its e_j is the
+// sum, and the division says 1 exactly.
+template <typename Z, bool STEP>
+__device__ __forceinline__ uint32_t list_gradients(const DistillParams& q, const List& list, int head, int v0, int v1,
+                                                   float base, float q_base, float sum, float g, float c, int lane) {
+  uint32_t mine = 0;
+#pragma unroll 1
+  for (int j = lane; j < q.K; j += 32) {
+    const int id = list.ids[j], v = (id + head) / Vec<Z>::kN;
+    if (id < 0 || v < v0 || v >= v1) continue;
+    float p = 0.0f;
+    bool first = true;
+#pragma unroll 8
+    for (int i = 0; i < q.K; ++i) {
+      const bool same_id = list.ids[i] == id;
+      p += same_id ? list.p[i] : 0.0f;
+      first = first && !(same_id && i < j);
+    }
+    const float e_j = fast_exp2((list.logits[j] - base) * c);
+    list.logits[j] = g * ((STEP ? e_j / sum : e_j * q_base) - p);
+    mine |= (uint32_t)first << (j >> 5);
+  }
+  return mine;
+}
+
+// A vector's gradient.
+template <typename Z>
+struct Gradient {
+  F2 b2, c2, s2;
+  __device__ __forceinline__ Gradient(float base, float c, float scale)
+      : b2(pair(-base, -base)), c2(pair(c, c)), s2(pair(scale, scale)) {}
+  __device__ __forceinline__ uint4 operator()(const uint4& v) const {
+    F2 f[Vec<Z>::kN / 2];
+    Vec<Z>::unpack(v, f);
+#pragma unroll
+    for (int k = 0; k < Vec<Z>::kN / 2; ++k) f[k] = mul2(s2, exp2_2(mul2(add2(f[k], b2), c2)));
+    return Vec<Z>::pack(f);
+  }
+};
+
+// All kernels: workers, and a last warp for the list.
 constexpr int kForwardWorkers = 256;
 constexpr int kGradWorkers = 128;
 
@@ -473,14 +530,7 @@ __global__ void __launch_bounds__(kGradWorkers + 32) distill_gradient_kernel(Dis
   const float g = q.dloss[t] * q.inv_tau;
   const bool any = sh.any, same = row.head == grad.head;
   const float scale = g * q_base;
-  const F2 b2 = pair(-base, -base), c2 = pair(c, c), s2 = pair(scale, scale);
-  auto gradient = [&](const uint4& v) {
-    F2 f[kN / 2];
-    Vec<Z>::unpack(v, f);
-#pragma unroll
-    for (int k = 0; k < kN / 2; ++k) f[k] = mul2(s2, exp2_2(mul2(add2(f[k], b2), c2)));
-    return Vec<Z>::pack(f);
-  };
+  const Gradient<Z> gradient(base, c, scale);
   uint32_t mine = 0;  // list warp: its entries that are the first of a column of this share
   if (!worker) {
     if (any) {
@@ -488,39 +538,23 @@ __global__ void __launch_bounds__(kGradWorkers + 32) distill_gradient_kernel(Dis
       softmax_list(q, list, lane);
     }
     if (STEP && rank == 0) store_loss(q, t, list, any, a, lane);
-    if (any) {
-#pragma unroll 1
-      for (int j = lane; j < q.K; j += 32) {
-        const int id = list.ids[j], v = (id + row.head) / kN;
-        if (id < 0 || v < v0 || v >= v0 + n) continue;
-        float sum = 0.0f;
-        bool first = true;
-#pragma unroll 8
-        for (int i = 0; i < q.K; ++i) {
-          const bool same_id = list.ids[i] == id;
-          sum += same_id ? list.p[i] : 0.0f;
-          first = first && !(same_id && i < j);
-        }
-        const float e_j = fast_exp2((list.logits[j] - base) * c);
-        list.logits[j] = g * ((STEP ? e_j / a.s : e_j * q_base) - sum);
-        mine |= (uint32_t)first << (j >> 5);
-      }
-    }
+    if (any) mine = list_gradients<Z, STEP>(q, list, row.head, v0, v0 + n, base, q_base, a.s, g, c, lane);
   } else if (any && same) {
     uint4* out = reinterpret_cast<uint4*>(grad.z + row.first(v0 + b));
 #pragma unroll 4
     for (int i = threadIdx.x; i < e - b; i += kGradWorkers) __stcs(out + i, gradient(x[b + i]));
     if (first_part) row_store(grad.z, q.V, row.first(v0), gradient(x[0]));
     if (last_part) row_store(grad.z, q.V, row.first(v0 + n - 1), gradient(x[n - 1]));
-  } else {
-    // a row without a list, or a gradient of another alignment
+  } else if (any) {
+    // a gradient of another alignment
     if (first_part || last_part) {
       const int i = first_part ? 0 : n - 1;
-      row_store(grad.z, q.V, row.first(v0 + i), any ? gradient(x[i]) : make_uint4(0, 0, 0, 0));
+      row_store(grad.z, q.V, row.first(v0 + i), gradient(x[i]));
     }
 #pragma unroll 1
-    for (int i = b + threadIdx.x; i < e; i += kGradWorkers)
-      row_store(grad.z, q.V, row.first(v0 + i), any ? gradient(x[i]) : make_uint4(0, 0, 0, 0));
+    for (int i = b + threadIdx.x; i < e; i += kGradWorkers) row_store(grad.z, q.V, row.first(v0 + i), gradient(x[i]));
+  } else {
+    zero_share(grad, rank, shares, kGradWorkers);  // a row without a list
   }
   if (!any) return;
   // the listed columns of this share, over what the rest of their vectors stored there

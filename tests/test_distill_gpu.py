@@ -113,7 +113,8 @@ def run_all(T, V, K, dtype, tau, seed, **kw):
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("T,V,K", [(1, 1, 1), (3, 2, 2), (5, 7, 3), (2, 31, 31), (9, 257, 5), (4, 1000, 512),
-                                   (17, 4099, 33), (6, 32000, 64), (3, 50001, 20), (2, 131072, 100), (130, 515, 8)])
+                                   (17, 4099, 33), (6, 32000, 64), (3, 50001, 20), (2, 131072, 100), (130, 515, 8), (400, 16385, 12),
+                                   (650, 40007, 9)])
 def test_distill_matches_formula(T, V, K, dtype):
     require_gpu()
     run_all(T, V, K, dtype, 1.0 if T % 2 else 2.5, T + V)
