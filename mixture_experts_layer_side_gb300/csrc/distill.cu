@@ -353,6 +353,23 @@ __device__ __forceinline__ void store_loss(const DistillParams& q, long t, const
   }
 }
 
+// The kN elements from element `by` on of two neighbouring vectors.
+template <typename Z>
+__device__ __forceinline__ uint4 shifted(const uint4& a, const uint4& b, int by) {
+  uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  const int words = sizeof(Z) == 2 ? by >> 1 : by;
+  if (words & 2)
+#pragma unroll
+    for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+  if (words & 1)
+#pragma unroll
+    for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+  if (sizeof(Z) == 2 && (by & 1))
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 // The gradients of the listed columns in vectors [v0, v1) in place of their
 // logits; returns a bit for each of the lane's entries that is the first of
 // its column.  e_j q_base - sum of p: where there is one token its e_j is the
@@ -546,13 +563,23 @@ __global__ void __launch_bounds__(kGradWorkers + 32) distill_gradient_kernel(Dis
     if (first_part) row_store(grad.z, q.V, row.first(v0), gradient(x[0]));
     if (last_part) row_store(grad.z, q.V, row.first(v0 + n - 1), gradient(x[n - 1]));
   } else if (any) {
-    // a gradient of another alignment
-    if (first_part || last_part) {
-      const int i = first_part ? 0 : n - 1;
-      row_store(grad.z, q.V, row.first(v0 + i), gradient(x[i]));
+    // a gradient of another alignment: the vectors of its grid that lie in
+    // this share's columns, each out of two of the logits', and its few
+    // elements before and after them
+    const int c0 = max(0, row.first(v0)), c1 = min(q.V, row.first(v0 + n));
+    const int g0 = (c0 + grad.head + kN - 1) / kN, g1 = max(g0, (c1 + grad.head) / kN);
+    const int shift = (grad.first(g0) - row.first(v0)) & (kN - 1);
+#pragma unroll 2
+    for (int v = g0 + threadIdx.x; v < g1; v += kGradWorkers) {
+      const int i = (grad.first(v) - row.first(v0)) / kN;
+      __stcs(reinterpret_cast<uint4*>(grad.z + grad.first(v)), gradient(shifted<Z>(x[i], x[i + 1], shift)));
     }
-#pragma unroll 1
-    for (int i = b + threadIdx.x; i < e; i += kGradWorkers) row_store(grad.z, q.V, row.first(v0 + i), gradient(x[i]));
+    const int before = min(grad.first(g0), c1) - c0, after = max(c0 + before, grad.first(g1));
+    for (int k = threadIdx.x; k < before + max(0, c1 - after); k += kGradWorkers) {
+      const int col = k < before ? c0 + k : after + k - before;
+      const float z = Vec<Z>::value(reinterpret_cast<const Z*>(x)[col - row.first(v0)]);
+      grad.z[col] = Vec<Z>::from(scale * fast_exp2((z - base) * c));
+    }
   } else {
     zero_share(grad, rank, shares, kGradWorkers);  // a row without a list
   }
