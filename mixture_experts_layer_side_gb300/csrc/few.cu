@@ -804,7 +804,7 @@ __global__ void __launch_bounds__(MX ? 448 : 384, 1) few_kernel(const __grid_con
   const int b_bytes = p.unit_rows * 128;
   const int stage_bytes = 2 * kATile + (MX ? 1 : 2) * b_bytes;
   uint8_t* sf_smem = smem + (size_t)p.stages * stage_bytes;
-  Ctl* ctl = reinterpret_cast<Ctl*>(sf_smem + (MX ? p.stages * kSfBytes : 0));
+  Ctl* ctl = reinterpret_cast<Ctl*>(smem + p.area);
   Schedule sched;
   const int R = p.T * p.k;
   sched.offset = reinterpret_cast<uint16_t*>(ctl + 1);
@@ -1345,7 +1345,16 @@ cudaError_t launch_few(FewParams p, bool mx, int* launches, cudaStream_t st) {
   int stages = (int)((kMost - rest) / stage);
   if (stages > kMaxFewStages) stages = kMaxFewStages;
   p.stages = stages;
-  const size_t smem = rest + stages * stage;
+  // (128 tokens of 32,768: the logits' inputs and sums are longer than four stages)
+  size_t area = stages * stage;
+  if (p.Wr) {
+    const size_t tokens = (size_t)p.logit_tokens * 4;
+    const size_t logits = p.h_rows * tokens + kLogitWarps * 256 * tokens;
+    if (logits > area) area = logits;
+  }
+  p.area = (int)area;
+  const size_t smem = rest + area;
+  if (smem > kMost) return cudaErrorInvalidValue;
   const void* kernel = mx ? (const void*)few_kernel<true> : (const void*)few_kernel<false>;
   static std::atomic<uint64_t> allowed[2];
   cudaError_t e = allow_smem(kernel, kMost, allowed[mx]);

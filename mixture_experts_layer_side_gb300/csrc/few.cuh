@@ -37,6 +37,7 @@ struct FewParams {
   FewShape gemm[2];
   int T, H, I, E, k;
   int unit_rows, stages;
+  int area;             // bytes of shared memory ahead of the control block: the stages, before them the router's sums
   int32_t* hdr;
   int32_t* tile_count;  // [units, I/128]
   int max_units;        // capacity of the unit table

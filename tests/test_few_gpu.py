@@ -192,6 +192,29 @@ def test_few_layer_with_router(shape, biased, prec):
     assert_close(out, oracle_out(inp, prec, idx=idx_ref, s=s_ref), prec, "layer")
 
 
+def test_few_router_of_the_longest_rows():
+    """128 tokens of the longest rows: what the logits' sums take of shared
+    memory is longer than the stages beside them."""
+    require_gpu()
+    T, H, I, E, k = 128, 32768, 128, 16, 16
+    inp = make(T, H, I, E, k, "uniform", 9)
+    x, Wr, _ = router_inputs(T, H, E, 3, False)
+    inp["x"] = x
+    dec = decoder(T, H, I, E, k, "mxfp8")
+    W, _keep = weights(inp, "mxfp8")
+    out, idx, s = dec.layer(x.cuda(), Wr.cuda(), *W)
+    dec.check()
+    logits = np64(x) @ np64(Wr)
+    assert (logits.astype(np.float32) == logits).all()
+    idx_ref, _ = router.topk_softmax(logits, None, k)
+    np.testing.assert_array_equal(idx.cpu().numpy(), idx_ref)
+    ch = np.take_along_axis(logits, idx_ref, axis=1)
+    ez = np.exp(ch - ch.max(axis=1, keepdims=True))
+    s_ref = ez / ez.sum(axis=1, keepdims=True)
+    np.testing.assert_allclose(s.cpu().numpy(), s_ref, rtol=2e-6, atol=1e-7)
+    assert_close(out, oracle_out(inp, "mxfp8", idx=idx_ref, s=s_ref), "mxfp8", "longest rows")
+
+
 def test_few_router_ties_and_nan():
     """Equal logits go to the lower expert; a NaN logit ranks last."""
     require_gpu()
