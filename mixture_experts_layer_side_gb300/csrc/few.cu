@@ -42,7 +42,14 @@ namespace mok {
 
 namespace {
 
-constexpr int kMaxFewStages = 8;
+// Stages of 32 KB of weights in flight on an SM.  bf16: four; a fifth only
+// delays the loads that others wait for (4 tokens, H 7168, I 2048: 233 us;
+// three 239, five 237, six 247).  MXFP8 needs six (8 tokens: 395 us; four 402,
+// three 420), but four where a CTA has few blocks of the first GEMM (128
+// tokens, H 2048, I 768, E 64: 83.5 us; three 84.3, five 85.4, as many as fit 85.5).
+constexpr int kStages = 4;
+constexpr int kMaxFewStages = 6;
+constexpr int kLongRun = 64;
 constexpr int kATile = 128 * 128;      // one A operand: 128 output columns x 128 bytes of K
 constexpr int kSfBytes = 1024 + 1024 + 512;  // MXFP8, per stage: raw and tiled A scales (two tiles), B scales
 constexpr int kProducers = 64;         // threads that bring the tokens' operand
@@ -56,9 +63,13 @@ constexpr int kWordRouted = kHdrCounters + 1;    // tokens routed
 constexpr int kWordHidden = kHdrCounters + 2;    // [2] tiles of a finished, each half
 constexpr int kWordSummed = kHdrCounters + 4;    // CTAs whose sums of y are stored
 constexpr int kWordLeft = kHdrCounters + 5;      // CTAs that ended
-constexpr int kTouchRows = 16;   // routed rows whose experts' pages are touched ahead
-constexpr int kHalvesFrom = 32;  // blocks a CTA of the first GEMM
-constexpr int kMinRun = 6;  // blocks: a shorter run would not fill the stages
+// Two halves only where a half is long beside the joining it hides, in blocks a
+// CTA of the first GEMM: 128 tokens, H 2048, I 768, E 64, bf16 (77 blocks) 114
+// us, in one 123; 1 token (10 blocks) 37 us in halves, in one 30.
+constexpr int kHalvesFrom = 32;
+// Blocks: a shorter run would not fill the stages (1 token, H 2048, I 768: 29.9
+// us; runs of 3 or more 30.3, of 12 or more 31.8).
+constexpr int kMinRun = 6;
 
 // The routing sorted by expert, in shared memory.
 struct Schedule {
@@ -407,26 +418,13 @@ __device__ void quantize_x(const FewParams& p, int nthreads) {
 }
 
 // ---------------------------------------------------------------- schedule
-// One line of each of an expert's matrices, another place for each CTA: the
-// pages of the weights that are about to stream in are looked up while the
-// schedule is made.
-template <bool MX>
-__device__ __forceinline__ void touch_weights(const FewParams& p, int e) {
-  const long bytes = (long)p.H * p.I * (MX ? 1 : 2), at = e * bytes + bytes / gridDim.x * blockIdx.x;
-  asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const uint8_t*>(p.W1) + at));
-  asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const uint8_t*>(p.W3) + at));
-  asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const uint8_t*>(p.W2) + at));
-}
-
-// The same for at most 32 rows, by one warp: lane f's row goes after those of
-// lower experts and of lower f.  False where an expert has more rows than a
-// unit takes.
-template <bool MX>
+// At most 32 rows, by one warp: lane f's row goes after those of lower experts
+// and of lower f.  False where an expert has more rows than a unit takes.  (1
+// token, H 2048, I 768: 28 us, with the sort below 31.)
 __device__ __forceinline__ bool build_few(const FewParams& p, const Schedule& s, Ctl* ctl, int id, int lane) {
   const int R = p.T * p.k;
   if (p.Wr) id = lane < R ? __ldcg(p.idx + lane) : -1;
   const bool in = lane < R && id >= 0 && id < p.E;
-  if (in && lane < kTouchRows) touch_weights<MX>(p, id);
   const uint32_t valid = __ballot_sync(0xffffffffu, in);
   const uint32_t same = __match_any_sync(0xffffffffu, in ? id : -1);
   const int rows = __popc(same), ahead = __popc(same & ((1u << lane) - 1u));
@@ -463,7 +461,6 @@ __device__ __forceinline__ bool build_few(const FewParams& p, const Schedule& s,
 // that (warp, place) is their order.  `scratch`: of each flat index its expert
 // and its place among the warp's rows of that expert, and a count per warp
 // and expert.
-template <bool MX>
 __device__ void build_units(const FewParams& p, const Schedule& s, uint8_t* scratch, Ctl* ctl, int nthreads) {
   const int R = p.T * p.k, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int per_shift = max(5, 32 - __clz((R - 1) / (nthreads / 32)));  // flat indices a warp, a power of two
@@ -484,7 +481,6 @@ __device__ void build_units(const FewParams& p, const Schedule& s, uint8_t* scra
       const bool in = e[i] >= 0 && e[i] < p.E;
       bad |= !in;
       ids[f] = (uint16_t)(in ? e[i] : kNoUnit);
-      if (in && f < kTouchRows) touch_weights<MX>(p, e[i]);
     }
   }
   for (int i = threadIdx.x; i < W * p.E; i += nthreads) hist[i] = 0;
@@ -884,15 +880,12 @@ __global__ void __launch_bounds__(MX ? 448 : 384, 1) few_kernel(const __grid_con
   }
   const int c = blockIdx.x;
   bool made = false;  // (uniform in warp 0, which alone knows)
-  if (ok && R <= 32 && warp == 0) made = build_few<MX>(p, sched, ctl, early_id, lane);
+  if (ok && R <= 32 && warp == 0) made = build_few(p, sched, ctl, early_id, lane);
   if (ok && R <= 32) made = __syncthreads_or(made);
-  if (ok && !made) build_units<MX>(p, sched, smem, ctl, kThreads);
+  if (ok && !made) build_units(p, sched, smem, ctl, kThreads);
   // the stages' first loads (async proxy) come after these threads' use of the same shared memory
   fence_proxy_async_shared();
   if (ok && threadIdx.x < 4) {
-    // halves only where a half is long beside the joining it hides: at 10
-    // blocks a CTA the two extra joins cost more than they hid (1 token, H
-    // 2048, I 768: 49 us in halves)
     const int i = threadIdx.x, units = ctl->units;
     const int blocks = units * (p.I / 128) * (p.H / kEl);
     const int half = blocks >= kHalvesFrom * (int)gridDim.x ? (units + 1) / 2 : units;
@@ -1254,8 +1247,9 @@ int units_bound(int T, int E, int k, int unit_rows) {
 }
 
 // Neighbouring column tiles are taken by up to 8 CTAs side by side, so that
-// they read up to 2 KB of each weight row together.  1 token, H 7168, I 2048,
-// MXFP8: 70 us, each tile apart 76; 16 tokens in bf16: 758 and 778.
+// they read up to 2 KB of each weight row together.  H 7168, I 2048: 8 tokens,
+// MXFP8, 394 us, each tile apart 570, four together 399; 24 tokens, bf16, 430,
+// 444 and 432.
 FewShape gemm_shape(int tiles, int kb, int ctas) {
   FewShape f;
   f.group_shift = 3;
@@ -1342,8 +1336,11 @@ cudaError_t launch_few(FewParams p, bool mx, int* launches, cudaStream_t st) {
   const size_t stage = 2 * kATile + (size_t)p.unit_rows * (mx ? 128 : 256) + (mx ? kSfBytes : 0);
   const size_t rest = 1024 + sizeof(Ctl) + schedule_bytes(p.E, p.T * p.k, p.max_units);
   constexpr size_t kMost = 227 * 1024;
+  // (an expert or more of every routed row)
+  const long blocks = (long)p.max_units * (p.I / 128) * (p.H / kel);
+  const int most = mx && blocks >= (long)kLongRun * ctas ? kMaxFewStages : kStages;
   int stages = (int)((kMost - rest) / stage);
-  if (stages > kMaxFewStages) stages = kMaxFewStages;
+  if (stages > most) stages = most;
   p.stages = stages;
   // (128 tokens of 32,768: the logits' inputs and sums are longer than four stages)
   size_t area = stages * stage;
