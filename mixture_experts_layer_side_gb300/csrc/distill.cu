@@ -21,9 +21,9 @@
 //    alignment has at most one part-filled vector at each end).
 //  * A row is shared by a cluster of up to 8 CTAs, which exchange their pairs
 //    through distributed shared memory: a few rows still fill the GPU.  In
-//    the step a CTA brings its share, 32 KB where eight are enough, to shared
+//    the step a CTA brings its share, 32 or 64 KB where eight are enough, to shared
 //    memory with bulk copies, where it stays between the sum and the gradient;
-//    six such CTAs an SM are in different phases, so that loads and stores
+//    six CTAs of 32 KB an SM are in different phases, so that loads and stores
 //    overlap: 395 us for 4,096 rows of 131,072 bf16, loss and gradient, 81% of
 //    the rate of a copy.  (Twice the threads a CTA: 412; a CTA a row of its own
 //    that streams it twice, the second time from L2: 471.)
@@ -413,6 +413,8 @@ struct Gradient {
 };
 
 // All kernels: workers, and a last warp for the list.
+// Forward: 1,000 rows of 50,001 bf16 20 us, 75% of the rate of a copy; of 128
+// workers 22, of 512 26.  4,096 rows of 131,072: 150 us, all of it.
 constexpr int kForwardWorkers = 256;
 constexpr int kGradWorkers = 128;
 
@@ -636,6 +638,11 @@ cudaError_t launch_forward(const DistillParams& p, int* launches, cudaStream_t s
 }
 
 constexpr long kShareVecs = 2048;   // 32 KB: six CTAs an SM
+// 64 KB, where it makes a row one CTA, or in f32, and rows fill the GPU.  4,096
+// rows of 32,000 bf16: 88 us, in two shares 97; f32 175, in four 185.  Else more
+// CTAs overlap better: 2,048 rows of 65,536 bf16 in two 102, in four 101; 256
+// rows of 32,000 in one 17.5, in shares of 32 KB 14.9.
+constexpr long kLongShareVecs = 4096;
 constexpr long kMostVecs = 13312;   // 208 KB: what a CTA can hold at most
 
 template <typename Z, bool STEP>
@@ -656,8 +663,10 @@ cudaError_t launch(DistillMode mode, DistillParams p, int* launches, cudaStream_
   if (mode == DISTILL_FORWARD) return launch_forward<Z>(p, launches, st);
   const long vecs = row_vectors<Z>(p);
   if (mode == DISTILL_STEP) {
+    const bool is_long = p.T >= 2l * sm_count() && (vecs <= kLongShareVecs || sizeof(Z) == 4);
+    const long share = is_long ? kLongShareVecs : kShareVecs;
     int shares = 1;
-    while (shares < kMaxShare && vecs > kShareVecs * shares) shares *= 2;
+    while (shares < kMaxShare && vecs > share * shares) shares *= 2;
     while (shares < kMaxShare && (long)p.T * shares < 2l * sm_count() && vecs >= 4l * kGradWorkers * shares) shares *= 2;
     if (vecs <= kMostVecs * shares) return launch_gradient<Z, true>(p, shares, launches, st);
     if (!p.lse) p.lse = p.lse_scratch;

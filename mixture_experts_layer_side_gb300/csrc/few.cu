@@ -28,6 +28,14 @@
 //  * Every CTA sorts the routing by expert for itself (at most 4,096 ids), so
 //    no launch or barrier stands between the routing and the first weight.
 //
+// Measured, of the rate of a copy (6.69 TB/s), on the weights of the experts
+// chosen: H 7168, I 2048, top-8: bf16 24 tokens 426 us (all of it), 4 tokens
+// 234 us (97%), 1 token with the router 120 us (88%); MXFP8 8 tokens 393 us (all
+// of it), 128 tokens 446 us (81%, the joins of experts with many rows).  H
+// 2048, I 768, top-8 of 64: bf16 1 token 29 us (39%: the start, the join
+// between the GEMMs and the combine stand beside 11 us of weights), 128 tokens
+// 114 us (61%).
+//
 // Arrivals are counted in the workspace and every CTA has to be resident: the
 // launch is cooperative.  All waits are bounded (MOK_ERR_TIMEOUT).  The
 // counters are zero again when a call ends.
