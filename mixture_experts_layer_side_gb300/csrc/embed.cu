@@ -27,13 +27,14 @@
 //    tokens' loads in flight.  A run of equal ids that crosses chunks leaves
 //    its parts to a last launch, so that a token that is everywhere is summed
 //    by as many blocks as its rows fill.
-//  * Accumulating into f32 rows is one vector reduction at L2 per row and
-//    slab, which nothing waits for.
+//  * Accumulating, the rows whose runs end among the eight tokens are loaded
+//    with them, so that nothing waits for a row alone.  (16,384 uniform ids in
+//    131,072 f32 rows: 196 us; by reductions at L2 233.)
 //
 // 8,192 tokens of 2,048 bf16 columns into a table of 65,536 rows, written
 // whole: 83 us, where 268 MB of stores alone take 67 (a fill's rate, 4 TB/s).
-// 16,384 tokens of 7,168 added to f32 rows: 129 us, 66% of the rate of a copy;
-// the sums take 90, the rest are the sort and the last launch.
+// 16,384 tokens of 7,168 (Zipf ids) added to f32 rows: 119 us, 71% of the rate
+// of a copy; beside the sums, the sort takes 17 and the last launch under 10.
 #include <cooperative_groups.h>
 #include <limits.h>
 
@@ -343,36 +344,50 @@ __global__ void __launch_bounds__(kSortThreads) __cluster_dims__(kSortCtas, 1, 1
   }
 }
 
-// kN values of a row of the gradient: written, or added to what is there.
+// N values of a row of the gradient as they were; what is added to them, or 0.
 template <typename G, int N>
-__device__ __forceinline__ void finish(const EmbedParams& p, G* g, const float (&acc)[N]) {
-  float f[N];
-#pragma unroll
-  for (int i = 0; i < N; ++i) f[i] = p.scale * acc[i];
+__device__ __forceinline__ void load_row(const G* g, float (&f)[N]) {
   if constexpr (N == 1) {
-    put(g, p.accumulate ? f[0] + to_f(*g) : f[0]);
+    f[0] = to_f(*g);
   } else if constexpr (sizeof(G) == 4) {
 #pragma unroll
     for (int i = 0; i < N; i += 4) {
-      if (p.accumulate)  // the only addition to these places in this call
-        asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(g + i), "f"(f[i]), "f"(f[i + 1]),
-                     "f"(f[i + 2]), "f"(f[i + 3])
-                     : "memory");
-      else
-        __stcs(reinterpret_cast<float4*>(g + i), make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]));
+      const float4 v = __ldcs(reinterpret_cast<const float4*>(g + i));
+      f[i] = v.x;
+      f[i + 1] = v.y;
+      f[i + 2] = v.z;
+      f[i + 3] = v.w;
     }
   } else {
     // bf16: N is 8, or 4 where dx is f32
-    uint32_t* w = reinterpret_cast<uint32_t*>(g);
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(g);
 #pragma unroll
     for (int i = 0; i < N; i += 2) {
-      if (p.accumulate) {
-        const uint32_t was = w[i / 2];
-        f[i] += __uint_as_float(was << 16);
-        f[i + 1] += __uint_as_float(was & 0xffff0000u);
-      }
-      w[i / 2] = pack_bf16x2(f[i], f[i + 1]);
+      f[i] = __uint_as_float(w[i / 2] << 16);
+      f[i + 1] = __uint_as_float(w[i / 2] & 0xffff0000u);
     }
+  }
+}
+
+// N values of a row of the gradient: scale * acc + was, rounded once.
+template <typename G, int N, bool ADD>
+__device__ __forceinline__ void finish(const EmbedParams& p, G* g, const float (&acc)[N], const float (&was)[N]) {
+  float f[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    f[i] = p.scale * acc[i];
+    if constexpr (ADD) f[i] += was[i];
+  }
+  if constexpr (N == 1) {
+    put(g, f[0]);
+  } else if constexpr (sizeof(G) == 4) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4)
+      __stcs(reinterpret_cast<float4*>(g + i), make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]));
+  } else {
+    uint32_t* w = reinterpret_cast<uint32_t*>(g);
+#pragma unroll
+    for (int i = 0; i < N; i += 2) w[i / 2] = pack_bf16x2(f[i], f[i + 1]);
   }
 }
 
@@ -382,7 +397,7 @@ __device__ __forceinline__ void finish(const EmbedParams& p, G* g, const float (
 // earlier) or part[2c + 1] (the one that began here and goes on).  VEC: a
 // thread has the columns of one 16-byte vector of dx, else one column.
 constexpr int kSumThreads = 128;
-template <typename D, typename G, bool VEC>
+template <typename D, typename G, bool VEC, bool ADD>
 __global__ void __launch_bounds__(kSumThreads) embed_sum_kernel(EmbedParams p, const int32_t* __restrict__ key,
                                                                 const int32_t* __restrict__ pos) {
   constexpr int kN = VEC ? Vec<D>::kN : 1;
@@ -403,13 +418,18 @@ __global__ void __launch_bounds__(kSumThreads) embed_sum_kernel(EmbedParams p, c
   for (int k = 0; k < kN; ++k) acc[k] = 0.0f;
   // (tokens that take no part have key V and come last)
   bool began_before = keys[1] < p.V && keys[0] == keys[1];
-  constexpr int kAhead = 8;
+  constexpr int kAhead = 8;  // (16,384 tokens of 7,168 accumulated: 119 us, of four 122, of two 128)
 #pragma unroll 1
   for (int i0 = 0; i0 < kChunk; i0 += kAhead) {
     if (keys[1 + i0] >= p.V) break;
     uint4 v[kAhead];
+    float was[kAhead][kN];  // ADD: the rows whose runs end here, before
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
+      if constexpr (ADD) {
+        const int k = keys[1 + i0 + i];
+        if (k < p.V && keys[2 + i0 + i] != k) load_row(static_cast<const G*>(p.dtable) + (long)k * p.H + col, was[i]);
+      }
       v[i] = make_uint4(0, 0, 0, 0);
       if (keys[1 + i0 + i] < p.V) {
         const D* from = static_cast<const D*>(p.dx) + (long)at[i0 + i] * p.H + col;
@@ -437,7 +457,7 @@ __global__ void __launch_bounds__(kSumThreads) embed_sum_kernel(EmbedParams p, c
 #pragma unroll
         for (int c = 0; c < kN; ++c) to[c] = acc[c];
       } else {
-        finish<G, kN>(p, static_cast<G*>(p.dtable) + (long)k * p.H + col, acc);
+        finish<G, kN, ADD>(p, static_cast<G*>(p.dtable) + (long)k * p.H + col, acc, was[i]);
       }
 #pragma unroll
       for (int c = 0; c < kN; ++c) acc[c] = 0.0f;
@@ -448,7 +468,7 @@ __global__ void __launch_bounds__(kSumThreads) embed_sum_kernel(EmbedParams p, c
 
 // Joins the runs that cross chunks: the block of the chunk where such a run
 // began adds its parts in order.
-template <typename G, bool VEC>
+template <typename G, bool VEC, bool ADD>
 __global__ void __launch_bounds__(kSumThreads) embed_join_kernel(EmbedParams p, const int32_t* __restrict__ key) {
   constexpr int kN = VEC ? 4 : 1;
   griddep_wait();
@@ -467,7 +487,9 @@ __global__ void __launch_bounds__(kSumThreads) embed_join_kernel(EmbedParams p, 
   }
   const int col = (blockIdx.y * kSumThreads + threadIdx.x) * kN;
   if (col < p.H) {
-    float acc[kN];
+    float acc[kN], was[kN];
+    G* to = static_cast<G*>(p.dtable) + (long)k * p.H + col;
+    if constexpr (ADD) load_row(to, was);
     const float* from = p.part + (2l * blockIdx.x + 1) * p.H + col;
 #pragma unroll
     for (int c = 0; c < kN; ++c) acc[c] = from[c];
@@ -484,7 +506,7 @@ __global__ void __launch_bounds__(kSumThreads) embed_join_kernel(EmbedParams p, 
         acc[0] += from[2l * i * p.H];
       }
     }
-    finish<G, kN>(p, static_cast<G*>(p.dtable) + (long)k * p.H + col, acc);
+    finish<G, kN, ADD>(p, to, acc, was);
   }
 }
 
@@ -503,17 +525,17 @@ cudaError_t launch_after(void (*kernel)(Args...), dim3 grid, int threads, cudaSt
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-template <typename D, typename G, bool VEC>
+template <typename D, typename G, bool VEC, bool ADD>
 cudaError_t launch_sums(const EmbedParams& p, int sorted, cudaStream_t st) {
   const unsigned chunks = (unsigned)((p.N + kChunk - 1) / kChunk);
   const int slab = kSumThreads * (VEC ? Vec<D>::kN : 1);
   const int32_t* key = p.key[sorted];
   const int32_t* pos = p.pos[sorted];
   cudaError_t e =
-      launch_after(embed_sum_kernel<D, G, VEC>, dim3(chunks, (p.H + slab - 1) / slab), kSumThreads, st, p, key, pos);
+      launch_after(embed_sum_kernel<D, G, VEC, ADD>, dim3(chunks, (p.H + slab - 1) / slab), kSumThreads, st, p, key, pos);
   if (e != cudaSuccess) return e;
   const int joined = kSumThreads * (VEC ? 4 : 1);
-  return launch_after(embed_join_kernel<G, VEC>, dim3(chunks, (p.H + joined - 1) / joined), kSumThreads, st, p, key);
+  return launch_after(embed_join_kernel<G, VEC, ADD>, dim3(chunks, (p.H + joined - 1) / joined), kSumThreads, st, p, key);
 }
 
 bool rows_of_vectors(const void* p, int H, int bytes) {
@@ -556,7 +578,10 @@ cudaError_t launch_backward(const EmbedParams& p, int* launches, cudaStream_t st
   if (e != cudaSuccess) return e;
   // a thread's vector of dx may be half of one of the gradient, or two
   const bool vec = rows_of_vectors(p.dx, p.H, sizeof(D)) && rows_of_vectors(p.dtable, p.H, sizeof(G));
-  e = vec ? launch_sums<D, G, true>(p, sorted, st) : launch_sums<D, G, false>(p, sorted, st);
+  if (p.accumulate)
+    e = vec ? launch_sums<D, G, true, true>(p, sorted, st) : launch_sums<D, G, false, true>(p, sorted, st);
+  else
+    e = vec ? launch_sums<D, G, true, false>(p, sorted, st) : launch_sums<D, G, false, false>(p, sorted, st);
   *launches = 3;
   return e;
 }
