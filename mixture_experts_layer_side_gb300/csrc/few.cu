@@ -197,6 +197,7 @@ struct Ctl {
   uint64_t tfull[2], tempty[2], drained;
   uint32_t tmem;
   int abort, go;
+  int failed;  // a wait of this CTA gave up
   int units;
   int last;
   int warp_sum[16];
@@ -823,10 +824,13 @@ __global__ void __launch_bounds__(MX ? 448 : 384, 1) few_kernel(const __grid_con
 
   const int d_cols = (MX ? 1 : 2) * p.unit_rows;  // TMEM columns of one accumulator: at most 4 x 64 (MXFP8), 4 x 128
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int c = blockIdx.x;
   WaitCtx wc{&ctl->abort, p.hdr + kHdrAbort, p.hdr + kHdrError};
 
   // what the routing and the first tiles need soon, on its way from memory meanwhile
   const int early_id = !p.Wr && warp == 0 && lane < R ? __ldg(p.idx + lane) : -1;
+  // a call that timed out left the abort word set: this one's results cannot be trusted either
+  const int stale = c == 0 && threadIdx.x == 0 ? __ldcg(p.hdr + kHdrAbort) : 0;
   {
     const char* a = reinterpret_cast<const char*>(p.x);
     const long bytes = (long)p.T * p.H * 2, at = ((long)blockIdx.x * kThreads + threadIdx.x) * 128;
@@ -848,6 +852,7 @@ __global__ void __launch_bounds__(MX ? 448 : 384, 1) few_kernel(const __grid_con
     }
     mbar_init(&ctl->drained, 1);
     ctl->abort = 0;
+    ctl->failed = 0;
     fence_mbar_init();
   }
   if (warp == 0) {
@@ -886,7 +891,6 @@ __global__ void __launch_bounds__(MX ? 448 : 384, 1) few_kernel(const __grid_con
     __syncthreads();
     ok = ctl->go != 0;
   }
-  const int c = blockIdx.x;
   bool made = false;  // (uniform in warp 0, which alone knows)
   if (ok && R <= 32 && warp == 0) made = build_few(p, sched, ctl, early_id, lane);
   if (ok && R <= 32) made = __syncthreads_or(made);
@@ -908,6 +912,12 @@ __global__ void __launch_bounds__(MX ? 448 : 384, 1) few_kernel(const __grid_con
   const uint32_t tmem = ctl->tmem;
   const int units = ok ? ctl->units : 0;
 
+  // From here a wait that gives up ends its role.  What the threads of a role
+  // do next is decided by all of them together: between the answers of two
+  // threads to the same wait the abort word may change, and a barrier or a
+  // warp-wide instruction that some have left never completes.
+  int issued = 0;  // thread 0: blocks of weights asked for
+  if (!ok && threadIdx.x == 0) ctl->failed = 1;
   if (units == 0) {
     // nothing routed: zeros (or a call that gave up)
     for (long i = (long)c * kThreads + threadIdx.x; i < (long)p.T * p.H; i += (long)gridDim.x * kThreads)
@@ -916,7 +926,6 @@ __global__ void __launch_bounds__(MX ? 448 : 384, 1) few_kernel(const __grid_con
     // ---------------------------------------------------------------- weights
     if (lane == 0) {
       uint32_t stage = 0, phase = 0;
-      long issued = 0;
       bool fine = true;
       for (int ph = 0; ph < 4; ++ph) {
         const Cut& cut = ctl->cuts[ph];
@@ -959,11 +968,7 @@ __global__ void __launch_bounds__(MX ? 448 : 384, 1) few_kernel(const __grid_con
           }
         }
       }
-      if (!fine) {
-        // no copy may still be in flight when the CTA leaves
-        for (long i = issued > p.stages ? issued - p.stages : 0; i < issued; ++i)
-          mbar_drain(&ctl->full_a[i % p.stages], (uint32_t)((i / p.stages) & 1), 1000000000ull);
-      }
+      if (!fine) ctl->failed = 1;
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -978,18 +983,15 @@ __global__ void __launch_bounds__(MX ? 448 : 384, 1) few_kernel(const __grid_con
         const int n = (sched.unit_n[s.unit] + 15) & ~15;
         const bool second = g == 0 || s.n * 256 + 128 < p.H;
         const uint32_t buf = count & 1;
-        if (!mbar_wait(&ctl->tempty[buf], ((count >> 1) & 1) ^ 1, wc)) {
-          fine = false;
-          break;
-        }
+        fine = __all_sync(0xffffffffu, mbar_wait(&ctl->tempty[buf], ((count >> 1) & 1) ^ 1, wc));
+        if (!fine) break;
         tc_fence_after();
         const uint32_t d0 = tmem + buf * 2 * d_cols, d1 = d0 + d_cols;
         for (int kb = s.k0; kb < s.k1; ++kb) {
-          if (!mbar_wait(&ctl->full_a[stage], phase, wc) || !mbar_wait(&ctl->full_b[stage], phase, wc) ||
-              (MX && !mbar_wait(&ctl->scales[stage], phase, wc))) {
-            fine = false;
-            break;
-          }
+          fine = __all_sync(0xffffffffu, mbar_wait(&ctl->full_a[stage], phase, wc) &&
+                                             mbar_wait(&ctl->full_b[stage], phase, wc) &&
+                                             (!MX || mbar_wait(&ctl->scales[stage], phase, wc)));
+          if (!fine) break;
           tc_fence_after();
           if (lane == 0) {
             // the tokens' operand was written with cp.async: order it before the tensor core's (async-proxy) reads
@@ -1040,6 +1042,7 @@ __global__ void __launch_bounds__(MX ? 448 : 384, 1) few_kernel(const __grid_con
     if (!fine) {
       // no MMA may still run when the CTA leaves
       if (lane == 0) {
+        ctl->failed = 1;
         mma_commit(&ctl->drained);
         mbar_drain(&ctl->drained, 0, 1000000000ull);
       }
@@ -1054,16 +1057,16 @@ __global__ void __launch_bounds__(MX ? 448 : 384, 1) few_kernel(const __grid_con
     for (int ph = 0; ph < 4; ++ph) {
       const Cut& cut = ctl->cuts[ph];
       const int g = ph >> 1;
-      if (!fine || ctl->runs[ph].left == 0) continue;
+      if (ctl->runs[ph].left == 0) continue;
       // x is ready at once (MXFP8: once every CTA has quantised its share),
       // a when every tile of this half of it is finished
       if (g == 1 || (MX && !p.Wr)) {
-        bool go = true;
-        if (tid == 0)
+        // (a thread whose waits gave up votes too)
+        bool go = fine;
+        if (tid == 0 && fine)
           go = g == 0 ? wait_flag_geq(word(p, kWordPrepared), gridDim.x, wc)
                       : wait_flag_geq(word(p, kWordHidden + (ph & 1)), cut.units * (p.I / 128), wc);
         fine = vote_all(2, kProducers, go);
-        if (!fine) continue;
       }
       const int K = g == 0 ? p.H : p.I;
       const uint8_t* src = g == 0 ? (MX ? p.xq : reinterpret_cast<const uint8_t*>(p.x)) : static_cast<uint8_t*>(p.a);
@@ -1097,6 +1100,7 @@ __global__ void __launch_bounds__(MX ? 448 : 384, 1) few_kernel(const __grid_con
         }
       }
     }
+    if (!fine) ctl->failed = 1;
     asm volatile("cp.async.wait_all;" ::: "memory");
   } else if (warp < 12) {
     // ---------------------------------------------------------------- epilogue
@@ -1180,6 +1184,7 @@ __global__ void __launch_bounds__(MX ? 448 : 384, 1) few_kernel(const __grid_con
       named_bar_sync(1, kEpilogue);
       if (tid == 0) red_release_gpu_add(word(p, kWordSummed), 1u);
     }
+    if (!fine && tid == 0) ctl->failed = 1;
   } else {
     // ---------------------------------------------------------------- MXFP8: weight scales
     // from [4 K blocks][128 columns] as they lie in memory to the layout that
@@ -1190,7 +1195,7 @@ __global__ void __launch_bounds__(MX ? 448 : 384, 1) few_kernel(const __grid_con
     for (int ph = 0; ph < 4; ++ph) {
       const int blocks = ctl->runs[ph].left;
       for (int b = 0; b < blocks && fine; ++b) {
-        fine = mbar_wait(&ctl->full_a[stage], phase, wc);
+        fine = __all_sync(0xffffffffu, mbar_wait(&ctl->full_a[stage], phase, wc));
         if (!fine) break;
         const uint8_t* raw = sf_smem + stage * kSfBytes + i * 512;
         uint8_t* tiled = sf_smem + stage * kSfBytes + 1024 + i * 512;
@@ -1210,6 +1215,7 @@ __global__ void __launch_bounds__(MX ? 448 : 384, 1) few_kernel(const __grid_con
         if (++stage == (uint32_t)p.stages) { stage = 0; phase ^= 1; }
       }
     }
+    if (!fine && lane == 0) ctl->failed = 1;
   }
 
   tc_fence_before();
@@ -1217,6 +1223,11 @@ __global__ void __launch_bounds__(MX ? 448 : 384, 1) few_kernel(const __grid_con
   asm volatile("barrier.sync 0;" ::: "memory");
   tc_fence_after();
   if (warp == 0) tmem_dealloc(tmem, 512);
+  if (threadIdx.x == 0 && ctl->failed) {
+    // no copy may still be in flight when the CTA leaves, whichever role gave up
+    for (int i = issued > p.stages ? issued - p.stages : 0; i < issued; ++i)
+      mbar_drain(&ctl->full_a[i % p.stages], (uint32_t)((i / p.stages) & 1), 1000000000ull);
+  }
   // eight threads an item while there are threads for it
   const bool one = (long)p.T * (p.H / 4) * 8 <= (long)gridDim.x * kThreads;
   if (units > 0 && (long)c * kThreads < (long)p.T * (p.H / 4) * (one ? 8 : 1)) {
@@ -1226,7 +1237,10 @@ __global__ void __launch_bounds__(MX ? 448 : 384, 1) few_kernel(const __grid_con
       list_runs(ctl->cuts + 2, table, kThreads);
     else
       table = nullptr;
-    if (threadIdx.x == 0) ctl->go = wait_flag_geq(word(p, kWordSummed), gridDim.x, wc) ? 1 : 0;
+    if (threadIdx.x == 0) {
+      ctl->go = wait_flag_geq(word(p, kWordSummed), gridDim.x, wc) ? 1 : 0;
+      if (!ctl->go) ctl->failed = 1;
+    }
     __syncthreads();
     if (ctl->go) {
       if (one)
@@ -1236,6 +1250,8 @@ __global__ void __launch_bounds__(MX ? 448 : 384, 1) few_kernel(const __grid_con
     }
   }
   if (threadIdx.x == 0) {
+    // (a wait that only saw another's abort has not recorded it)
+    if (stale | ctl->failed) atomicOr(p.hdr + kHdrError, MOK_ERRBIT_TIMEOUT);
     // the last CTA to end leaves the counters as it found them
     __threadfence();
     if (atomicAdd(p.hdr + kWordLeft, 1) == (int)gridDim.x - 1) {
