@@ -396,10 +396,13 @@ __device__ __forceinline__ void finish(const EmbedParams& p, G* g, const float (
 // chunk's start or end leaves its part in part[2c] (the run that began
 // earlier) or part[2c + 1] (the one that began here and goes on).  VEC: a
 // thread has the columns of one 16-byte vector of dx, else one column.
+// (Started while the sort still writes the pairs: key and pos are no
+// __restrict__ pointers here and in the join, which would allow reads ahead of
+// griddep_wait and past coherence.)
 constexpr int kSumThreads = 128;
 template <typename D, typename G, bool VEC, bool ADD>
-__global__ void __launch_bounds__(kSumThreads) embed_sum_kernel(EmbedParams p, const int32_t* __restrict__ key,
-                                                                const int32_t* __restrict__ pos) {
+__global__ void __launch_bounds__(kSumThreads) embed_sum_kernel(EmbedParams p, const int32_t* key,
+                                                                const int32_t* pos) {
   constexpr int kN = VEC ? Vec<D>::kN : 1;
   __shared__ int keys[kChunk + 2], at[kChunk];  // keys[1 + i]; the neighbours' at the ends
   griddep_launch_dependents();
@@ -469,7 +472,7 @@ __global__ void __launch_bounds__(kSumThreads) embed_sum_kernel(EmbedParams p, c
 // Joins the runs that cross chunks: the block of the chunk where such a run
 // began adds its parts in order.
 template <typename G, bool VEC, bool ADD>
-__global__ void __launch_bounds__(kSumThreads) embed_join_kernel(EmbedParams p, const int32_t* __restrict__ key) {
+__global__ void __launch_bounds__(kSumThreads) embed_join_kernel(EmbedParams p, const int32_t* key) {
   constexpr int kN = VEC ? 4 : 1;
   griddep_wait();
   const long c0 = (long)blockIdx.x * kChunk, end = c0 + kChunk;
