@@ -17,7 +17,9 @@ class MoKDecoder:
     Weights as for ``MoKLayer.forward``: bf16 tensors, or in MXFP8 mode the
     forward descriptors of ``quantize_weights``.  Calls on one object must not
     overlap (they share the workspace).  Errors found on the device (an expert
-    id outside [0, E)) are raised by ``check``."""
+    id outside [0, E)) are raised by ``check``.  After a timeout the results
+    of all calls since the last ``check`` are void; ``check`` raises it and
+    makes the workspace ready again."""
 
     def __init__(self, shape: Shape, precision="bf16", device="cuda"):
         self.shape = shape
@@ -85,5 +87,10 @@ class MoKDecoder:
     def check(self, stream=None):
         """Synchronise and raise if the device recorded an error."""
         st = _lib.mok_check(self.ws, stream)
+        if st == _lib.MOK_ERR_TIMEOUT:
+            # a call that gave up leaves the abort word and counts of arrivals behind
+            self.ws.zero_()
+            if self.device.type == "cuda":
+                torch.cuda.current_stream(self.device).synchronize()
         if st != 0:
             raise _lib.MokError(st, "few tokens: device status")
