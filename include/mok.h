@@ -619,7 +619,8 @@ typedef enum { MOK_TYPE_BF16 = 0, MOK_TYPE_F32 = 1 } mok_dtype;
  *   dloss  (device) f32 [T]  weight of each row's loss in what is minimised
  *   loss, lse   (device) f32 [T]; the step's lse may be NULL
  *   dz     (device) [T, V] of z's type, rows lddz apart; it may be z itself
- *          (same pointer and stride)
+ *          (same pointer and stride), else no row of it may share a byte with
+ *          a row of z (MOK_ERR_INVALID_ARG)
  * Entries with p_j = 0 add nothing, whatever q is there.  A row whose list is
  * empty, or holds values of -inf alone, has loss 0 and gradient 0.  A student
  * logit of -inf has q = 0; where p > 0 there, the loss is +inf.  The loss is

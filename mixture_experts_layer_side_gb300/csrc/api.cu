@@ -1637,6 +1637,26 @@ mok_status check_distill_sizes(int32_t T, int32_t V, int32_t K) {
   return K > MOK_DISTILL_MAX_TOP ? MOK_ERR_UNSUPPORTED : MOK_OK;
 }
 
+// Whether any of T rows of `w` bytes, `za` bytes apart from z on, has a byte in
+// common with any of those `db` apart from d on.  (za, db >= w)
+bool rows_meet(uintptr_t z, uintptr_t za, uintptr_t d, uintptr_t db, uintptr_t w, int32_t T) {
+  if (d >= z + za * (T - 1) + w || z >= d + db * (T - 1) + w) return false;
+  if (za == db) {
+    // the distance from a row of z on to the next row of d, which are all alike
+    const uintptr_t off = d >= z ? (d - z) % za : (za - (z - d) % za) % za;
+    return off < w || off + w > za;
+  }
+  for (int32_t i = 0, j = 0; i < T && j < T;) {
+    const uintptr_t a = z + za * i, b = d + db * j;
+    if (a < b + w && b < a + w) return true;
+    if (a < b)
+      ++i;
+    else
+      ++j;
+  }
+  return false;
+}
+
 mok_status distill(DistillMode mode, int32_t T, int32_t V, int32_t K, mok_dtype type, const void* z, int64_t ldz,
                    const int32_t* ids, const float* vals, float tau, const float* lse_in, const float* dloss,
                    float* loss, float* lse, void* dz, int64_t lddz, void* ws, size_t ws_bytes, void* stream) {
@@ -1648,6 +1668,12 @@ mok_status distill(DistillMode mode, int32_t T, int32_t V, int32_t K, mok_dtype 
   if (mode != DISTILL_BACKWARD && (!loss || (!lse && mode == DISTILL_FORWARD))) return MOK_ERR_INVALID_ARG;
   if (mode == DISTILL_BACKWARD && !lse_in) return MOK_ERR_INVALID_ARG;
   if (mode != DISTILL_FORWARD && (!dloss || !dz || lddz < V || !aligned_to(dz, type))) return MOK_ERR_INVALID_ARG;
+  const uintptr_t es = type == MOK_TYPE_BF16 ? 2 : 4, z0 = reinterpret_cast<uintptr_t>(z),
+                  d0 = reinterpret_cast<uintptr_t>(dz);
+  const bool in_place = mode != DISTILL_FORWARD && d0 == z0 && (T == 1 || ldz == lddz);
+  // a row of the gradient over another row's logits, or shifted over its own, would be written while those are read
+  if (mode != DISTILL_FORWARD && !in_place && rows_meet(z0, es * ldz, d0, es * lddz, es * V, T))
+    return MOK_ERR_INVALID_ARG;
   if (ws_bytes < mok_distill_workspace_size(T, V, K)) return MOK_ERR_WORKSPACE_TOO_SMALL;
   DistillParams p;
   memset(&p, 0, sizeof(p));
@@ -1668,11 +1694,7 @@ mok_status distill(DistillMode mode, int32_t T, int32_t V, int32_t K, mok_dtype 
   p.lddz = lddz;
   p.hdr = static_cast<int32_t*>(ws);
   p.lse_scratch = reinterpret_cast<float*>(p.hdr + kHeaderWords);
-  if (mode != DISTILL_FORWARD) {
-    const uintptr_t es = type == MOK_TYPE_BF16 ? 2 : 4, z0 = reinterpret_cast<uintptr_t>(z),
-                    d0 = reinterpret_cast<uintptr_t>(dz);
-    p.overlap = d0 < z0 + es * ((T - 1) * (uintptr_t)ldz + V) && z0 < d0 + es * ((T - 1) * (uintptr_t)lddz + V);
-  }
+  p.in_place = in_place;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   Phase ph(MOK_PHASE_DISTILL, st, 0);
   int launches = 0;

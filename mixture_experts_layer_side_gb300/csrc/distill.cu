@@ -478,8 +478,8 @@ __global__ void __launch_bounds__(kGradWorkers + 32) distill_gradient_kernel(Dis
   const long t = blockIdx.x / shares;
   const int rank = blockIdx.x % shares, lane = threadIdx.x & 31;
   const bool worker = threadIdx.x < kGradWorkers;
-  // the gradient takes the logits' place, or may: then a logit is read before any is overwritten
-  const bool in_place = q.overlap;
+  // the gradient takes the logits' place: then a logit is read before any is overwritten
+  const bool in_place = q.in_place;
   const float c = q.inv_tau * kLog2e;
   const RowGrid<Z> row(q.z, t * q.ldz, q.V), grad(q.dz, t * q.lddz, q.V);
   const int v0 = min(rank * most, row.vecs), n = min(most, row.vecs - v0);

@@ -19,7 +19,7 @@ struct DistillParams {
   float* lse_scratch;  // [T]
   void* dz;        // [T, lddz]
   long lddz;
-  int overlap;     // the gradient's rows may lie where the logits are
+  int in_place;    // the gradient's rows lie where the logits are
   int32_t* hdr;
 };
 

@@ -66,7 +66,8 @@ class DistillLoss:
         return loss, lse
 
     def backward(self, z, ids, vals, lse, dloss, temperature=1.0, out=None, stream=None):
-        """dz of z's type, from the forward's ``lse``; ``out`` may be z itself."""
+        """dz of z's type, from the forward's ``lse``; ``out`` may be z itself,
+        but not overlap it in part."""
         T, tau = self._begin(z, ids, vals, temperature)
         self._row_values(T, "lse", lse)
         self._row_values(T, "dloss", dloss)
@@ -75,7 +76,7 @@ class DistillLoss:
         return dz
 
     def forward_backward(self, z, ids, vals, dloss, temperature=1.0, out=None, stream=None):
-        """(loss, dz) in one call; ``out`` may be z itself."""
+        """(loss, dz) in one call; ``out`` as in ``backward``."""
         T, tau = self._begin(z, ids, vals, temperature)
         self._row_values(T, "dloss", dloss)
         dz = self._gradient(z, out)

@@ -37,3 +37,49 @@ def test_decoder_is_ready_again_after_a_timeout(lib, monkeypatch, status, zeroed
         dec.check()
     assert err.value.status == status
     assert bool((dec.ws == 0).all()) == zeroed
+
+
+def distill_calls(lib):
+    """The step and the backward on 4 rows of 100 bf16 logits at `z`, rows `ldz` apart, in a workspace that is too
+    small for them, so that what passes the other checks is still not enqueued."""
+    L = lib.LIB
+
+    def step(z, ldz, dz, lddz, T=4, V=100):
+        return L.mok_distill_step(T, V, 8, 0, z, ldz, A, A, 1.0, A, A, A, dz, lddz, A, 8, None)
+
+    def backward(z, ldz, dz, lddz, T=4, V=100):
+        return L.mok_distill_backward(T, V, 8, 0, z, ldz, A, A, 1.0, A, A, dz, lddz, A, 8, None)
+
+    return step, backward
+
+
+def test_distill_refuses_a_gradient_that_overlaps_the_logits_in_part(lib):
+    SMALL = 3
+    Z = 1 << 20
+    for call in distill_calls(lib):
+        # in place, apart, and rows that lie between one another
+        assert call(Z, 100, Z, 100) == SMALL
+        assert call(Z, 100, Z, 200, T=1) == SMALL
+        assert call(Z, 100, Z + 800, 100) == call(Z + 800, 100, Z, 100) == SMALL
+        assert call(Z, 200, Z + 200, 200) == call(Z + 200, 200, Z, 200) == SMALL
+        assert call(Z, 300, Z + 200, 300) == call(Z, 300, Z + 400, 300) == SMALL
+        assert call(Z, 300, Z + 200 - 1200, 300) == SMALL
+        # (z in columns 0-99 of rows of 400, the gradient's at 100 and 300 of each)
+        assert call(Z, 400, Z + 200, 200) == SMALL
+        # a row over itself with another stride, shifted, or over another row
+        assert call(Z, 100, Z, 200) == call(Z, 200, Z, 100) == INVALID
+        assert call(Z, 100, Z + 2, 100) == call(Z, 100, Z - 2, 100) == INVALID
+        assert call(Z, 100, Z + 200, 100) == call(Z, 100, Z - 200, 100) == INVALID
+        assert call(Z, 300, Z + 198, 300) == call(Z, 300, Z + 402, 300) == INVALID
+        assert call(Z, 300, Z + 198 - 600, 300) == INVALID
+        assert call(Z, 400, Z + 200, 201) == INVALID
+        assert call(Z, 100, Z + 2, 300, T=1) == INVALID
+    # every pair of small strides and offsets against the bytes themselves
+    step, _ = distill_calls(lib)
+    for lz in (3, 4, 7):
+        for ld in (3, 5, 7):
+            rows = [set(range(2 * lz * i, 2 * lz * i + 6)) for i in range(3)]
+            for off in range(-60, 60, 2):
+                grad = [set(range(off + 2 * ld * i, off + 2 * ld * i + 6)) for i in range(3)]
+                meet = any(a & b for a in rows for b in grad) and not (off == 0 and lz == ld)
+                assert step(Z, lz, Z + off, ld, T=3, V=3) == (INVALID if meet else SMALL), (lz, ld, off)
