@@ -629,8 +629,8 @@ typedef enum { MOK_TYPE_BF16 = 0, MOK_TYPE_F32 = 1 } mok_dtype;
  *   mok_distill_forward   loss and lse
  *   mok_distill_backward  dz from the forward's lse
  *   mok_distill_step      both at once: loss, lse and dz
- * All sums in f32 and in a fixed order.  1 <= K <= MOK_DISTILL_MAX_TOP; T = 0
- * does nothing.  ws: mok_distill_workspace_size bytes (for at
+ * All sums in f32 and in a fixed order.  1 <= K <= MOK_DISTILL_MAX_TOP, V <= 2^30;
+ * T = 0 does nothing.  ws: mok_distill_workspace_size bytes (for at
  * least this T), its first 256 zeroed once by the caller; its first word holds
  * errors until mok_check.  Calls that share a workspace must not overlap.
  */

@@ -1634,7 +1634,8 @@ bool aligned_to(const void* p, mok_dtype t) {
 
 mok_status check_distill_sizes(int32_t T, int32_t V, int32_t K) {
   if (T < 0 || V < 1 || K < 1) return MOK_ERR_INVALID_ARG;
-  return K > MOK_DISTILL_MAX_TOP ? MOK_ERR_UNSUPPORTED : MOK_OK;
+  // a row's columns and vectors are counted in 32 bits
+  return V > (1 << 30) || K > MOK_DISTILL_MAX_TOP ? MOK_ERR_UNSUPPORTED : MOK_OK;
 }
 
 // Whether any of T rows of `w` bytes, `za` bytes apart from z on, has a byte in

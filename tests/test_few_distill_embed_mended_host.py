@@ -83,3 +83,12 @@ def test_distill_refuses_a_gradient_that_overlaps_the_logits_in_part(lib):
                 grad = [set(range(off + 2 * ld * i, off + 2 * ld * i + 6)) for i in range(3)]
                 meet = any(a & b for a in rows for b in grad) and not (off == 0 and lz == ld)
                 assert step(Z, lz, Z + off, ld, T=3, V=3) == (INVALID if meet else SMALL), (lz, ld, off)
+
+
+def test_distill_refuses_rows_past_32_bit_columns(lib):
+    assert lib.mok_distill_workspace_size(1, 1 << 30, 8) > 0
+    for V in ((1 << 30) + 1, 2 ** 31 - 9, 2 ** 31 - 1):
+        assert lib.mok_distill_workspace_size(1, V, 8) == 0
+        for call in distill_calls(lib):
+            assert call(1 << 20, V, 1 << 40, V, T=1, V=V) == UNSUPPORTED
+        assert lib.LIB.mok_distill_forward(1, V, 8, 0, A, V, A, A, 1.0, A, A, A, BIG, None) == UNSUPPORTED
