@@ -22,6 +22,8 @@ class MoKEmbedding:
         self.vocab, self.hidden, self.tokens = vocab, hidden, tokens
         self._table = (vocab, hidden)
         self.pad_id = _lib.MOK_EMBED_NO_PAD if pad_id is None else int(pad_id)
+        # (a wider number would name another id in the call; the lowest says that there is none)
+        require(pad_id is None or -2**31 < self.pad_id < 2**31, f"pad_id: {pad_id}, wanted an int32 above the lowest")
         self.device = on(device)
         n = _lib.mok_embed_workspace_size(vocab, hidden, tokens)
         if n == 0:

@@ -92,3 +92,12 @@ def test_distill_refuses_rows_past_32_bit_columns(lib):
         for call in distill_calls(lib):
             assert call(1 << 20, V, 1 << 40, V, T=1, V=V) == UNSUPPORTED
         assert lib.LIB.mok_distill_forward(1, V, 8, 0, A, V, A, A, 1.0, A, A, A, BIG, None) == UNSUPPORTED
+
+
+def test_embedding_refuses_a_pad_id_that_is_no_int32(lib):
+    from mixture_experts_layer_side_gb300.embedding import MoKEmbedding
+    for pad in (None, 0, -1, 9, 10, 2 ** 31 - 1, -2 ** 31 + 1):
+        assert MoKEmbedding(10, 8, 4, pad_id=pad, device="cpu").pad_id == (lib.MOK_EMBED_NO_PAD if pad is None else pad)
+    for pad in (2 ** 32 + 5, 2 ** 31, -2 ** 31, -2 ** 32 + 3):
+        with pytest.raises(ValueError):
+            MoKEmbedding(10, 8, 4, pad_id=pad, device="cpu")
