@@ -91,6 +91,11 @@ __device__ __forceinline__ uint4 pack(const float (&f)[4]) {
   return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
 }
 
+// Whether an id is the padding's.  (What says that there is none is no id either.)
+__device__ __forceinline__ bool is_pad(const EmbedParams& p, int id) {
+  return id == p.pad_id && id != MOK_EMBED_NO_PAD;
+}
+
 // VEC: rows of whole aligned vectors; else one element a lane.  A warp brings
 // kLookup pieces of 32 vectors (elements) of one row.
 constexpr int kLookup = 4;  // (of 2: 58 us where 4 and 8 take 55)
@@ -103,7 +108,7 @@ __global__ void __launch_bounds__(256) embed_lookup_kernel(EmbedParams p, int pi
   if (n >= p.N) return;
   const int id = p.ids[n], cols = p.H / kN;
   const bool ok = id >= 0 && id < p.V;
-  if (!ok && id != p.pad_id && c0 == 0) atomicOr(p.hdr + kHdrError, MOK_ERRBIT_BAD_INDEX);
+  if (!ok && !is_pad(p, id) && c0 == 0) atomicOr(p.hdr + kHdrError, MOK_ERRBIT_BAD_INDEX);
   const T* src = static_cast<const T*>(p.table) + (long)(ok ? id : 0) * p.H;
   T* dst = static_cast<T*>(p.out) + (long)n * p.H;
   if constexpr (VEC) {
@@ -187,7 +192,7 @@ __device__ void zero_rows(const EmbedParams& p, uint32_t* taken, int grad_bytes,
 // takes no part -- padding, or an id outside [0, V).
 __device__ __forceinline__ int key_of(const EmbedParams& p, long i, bool tell) {
   const int id = p.ids[i];
-  if (id == p.pad_id) return p.V;
+  if (is_pad(p, id)) return p.V;
   if (id >= 0 && id < p.V) return id;
   if (tell) atomicOr(p.hdr + kHdrError, MOK_ERRBIT_BAD_INDEX);
   return p.V;
