@@ -298,11 +298,11 @@ __device__ __forceinline__ void router_logits(const FewParams& p, uint8_t* smem,
       }
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
-        const int h = min(hb + i * warps * down, rows - 1);
+        const int h = hb + i * warps * down;
         const uint32_t vv[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
         for (int t = 0; t < TOK; ++t) {
-          const float x = xs[h * TOK + t];
+          const float x = h < rows ? xs[h * TOK + t] : 0.0f;  // (past the part both are 0: an infinite x times 0 is NaN)
 #pragma unroll
           for (int m = 0; m < 4; ++m) {
             acc[t][2 * m] = fmaf(x, __uint_as_float(vv[m] << 16), acc[t][2 * m]);

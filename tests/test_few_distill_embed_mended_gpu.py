@@ -10,6 +10,44 @@ from _helpers import np64, require_gpu
 pytestmark = pytest.mark.gpu
 
 
+# ---------------------------------------------------------------- few tokens
+def small_layer(shape, prec="bf16", seed=3):
+    from mixture_experts_layer_side_gb300.decode import MoKDecoder
+    from mixture_experts_layer_side_gb300.inputs import Shape, make_inputs
+    return MoKDecoder(Shape(*shape), precision=prec), make_inputs(Shape(*shape), "uniform", seed=seed)
+
+
+@pytest.mark.parametrize("shape", [(1, 7168, 128, 256, 8), (5, 7168, 128, 256, 8), (3, 1152, 128, 130, 8)])
+def test_few_router_with_an_infinite_input(shape):
+    """An infinite x makes the token's logits +-inf, wherever in its row it stands: the experts of +inf come first,
+    those of -inf last, each in ascending order.  As MoKRouter has it; other tokens are as without it."""
+    require_gpu()
+    from mixture_experts_layer_side_gb300.inputs import Shape
+    from mixture_experts_layer_side_gb300.layer import MoKRouter
+    T, H, I, E, k = shape
+    dec, inp = small_layer(shape)
+    g = torch.Generator().manual_seed(5)
+    Wr = (torch.randint(1, 128, (H, E), generator=g) * (torch.randint(0, 2, (H, E), generator=g) * 2 - 1) / 2048).bfloat16()
+    x = ((torch.randn((T, H), generator=g) * 32).round().clamp(-127, 127) / 32).bfloat16()
+    W = [inp[n].cuda() for n in ("W1", "W3", "W2")]
+    clean = dec.layer(x.cuda(), Wr.cuda(), *W)[1].cpu()
+    router = MoKRouter(Shape(*shape))
+    # the rows at the ends of a part of the logits' sums, and others
+    for at in [0, 1, H - 1] + [r for p in (H // 64 + 7 & ~7, (H // 64 + 7 & ~7) * 3) for r in (p - 1, p)]:
+        xi = x.clone()
+        xi[T - 1, at] = float("inf")
+        Wr_at = Wr.clone()
+        Wr_at[at] = -1
+        Wr_at[at, 3::E // 4] = 1
+        _, idx, _ = dec.layer(xi.cuda(), Wr_at.cuda(), *W)
+        dec.check()
+        up = list(range(3, E, E // 4))
+        want = (up + [e for e in range(E) if e not in up])[:k]
+        assert idx[T - 1].tolist() == want, at
+        assert torch.equal(idx, router.forward(xi.cuda(), Wr_at.cuda())[0])
+    assert torch.equal(dec.layer(x.cuda(), Wr.cuda(), *W)[1].cpu(), clean)
+
+
 # ---------------------------------------------------------------- embedding
 @pytest.mark.parametrize("N", [40, 5000])
 def test_embedding_the_lowest_id_is_an_error_where_there_is_no_padding(N):
