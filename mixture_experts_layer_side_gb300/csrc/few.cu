@@ -1131,12 +1131,13 @@ __global__ void __launch_bounds__(MX ? 448 : 384, 1) few_kernel(const __grid_con
           float v0[4], v1[4];
           tmem_ld4x2(d + i0, d + d_cols + i0, v0, v1);
           if (!MX && g == 1) {
+            // (an infinite weight times a remainder of 0 or of the other sign: the first part says what y is)
             float l0[4], l1[4];
             tmem_ld4x2(d + n16 + i0, d + d_cols + n16 + i0, l0, l1);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              v0[i] += l0[i];
-              v1[i] += l1[i];
+              v0[i] += isfinite(v0[i]) ? l0[i] : 0.0f;
+              v1[i] += isfinite(v1[i]) ? l1[i] : 0.0f;
             }
           }
           if (g == 0 && whole) {

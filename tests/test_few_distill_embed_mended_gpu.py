@@ -48,6 +48,30 @@ def test_few_router_with_an_infinite_input(shape):
     assert torch.equal(dec.layer(x.cuda(), Wr.cuda(), *W)[1].cpu(), clean)
 
 
+@pytest.mark.parametrize("shape", [(1, 128, 128, 4, 2), (6, 512, 1024, 4, 1), (33, 384, 640, 9, 3), (128, 1024, 384, 3, 2)])
+def test_few_infinite_weights(shape):
+    """An infinite W2 makes y what its one product says, +-inf, whatever a's second part is."""
+    require_gpu()
+    from oracle import moe
+    T, H, I, E, k = shape
+    dec, inp = small_layer(shape)
+    W2 = inp["W2"].clone()
+    for i, n in [(0, 5), (I // 2, 64), (I - 1, H - 1), (17, H // 2)]:
+        W2[1, i, n] = float("inf")
+        W2[1, i, (n + 9) % H] = -float("inf")
+    out = dec.forward(*[inp[n].cuda() for n in ("x", "idx", "s", "W1", "W3")], W2.cuda())
+    dec.check()
+    a = {n: np64(v) for n, v in inp.items()}
+    with np.errstate(invalid="ignore"):
+        ref = moe.forward(a["x"], inp["idx"].numpy(), a["s"], a["W1"], a["W3"], np64(W2))[0]
+    got = np64(out)
+    assert np.isinf(ref).any()
+    np.testing.assert_array_equal(np.isnan(got), np.isnan(ref))  # (two of either sign in one sum)
+    np.testing.assert_array_equal(np.where(np.isinf(ref), ref, 0), np.where(np.isinf(got), got, 0))
+    fin = np.isfinite(ref)
+    assert np.abs(got[fin] - ref[fin]).max() <= 2e-2 * np.abs(ref[fin]).max()
+
+
 # ---------------------------------------------------------------- embedding
 @pytest.mark.parametrize("N", [40, 5000])
 def test_embedding_the_lowest_id_is_an_error_where_there_is_no_padding(N):
