@@ -261,14 +261,14 @@ __device__ __forceinline__ List list_at(uint8_t* smem, int K) {
 }
 
 // By one warp, in three steps of which the others wait for the first alone:
-// the ids and values (tau already divided out; -inf for what is left out) --
+// the ids and values (-inf for what is left out) --
 // returns whether there is anything to learn from: an entry above -inf.
 __device__ __forceinline__ bool read_list(const DistillParams& q, long t, const List& l, int lane) {
   bool any = false;
 #pragma unroll 1
   for (int j = lane; j < q.K; j += 32) {
     int id = q.ids[t * q.K + j];
-    float v = q.vals[t * q.K + j] * q.inv_tau;
+    float v = q.vals[t * q.K + j];
     if (id < -1 || id >= q.V) {
       atomicOr(q.hdr + kHdrError, MOK_ERRBIT_BAD_INDEX);
       id = -1;
@@ -289,6 +289,7 @@ __device__ __forceinline__ void read_logits(const DistillParams& q, const Z* z, 
 }
 
 // The teacher's probabilities in place of its values, for a list that has any.
+// (The difference first: a value over tau may be past f32 where the difference is 0.)
 __device__ __forceinline__ void softmax_list(const DistillParams& q, const List& l, int lane) {
   float top = -INFINITY;
 #pragma unroll 1
@@ -298,7 +299,7 @@ __device__ __forceinline__ void softmax_list(const DistillParams& q, const List&
   float total = 0.0f;
 #pragma unroll 1
   for (int j = lane; j < q.K; j += 32) {
-    const float e = expf(l.p[j] - base);  // exp(-inf) = 0 for what is left out
+    const float e = expf((l.p[j] - base) * q.inv_tau);  // exp(-inf) = 0 for what is left out
     l.p[j] = e;
     total += e;
   }

@@ -72,6 +72,33 @@ def test_few_infinite_weights(shape):
     assert np.abs(got[fin] - ref[fin]).max() <= 2e-2 * np.abs(ref[fin]).max()
 
 
+# ---------------------------------------------------------------- distillation
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("tau", [0.25, 1.0, 4.0])
+def test_distill_teacher_values_of_the_types_ends(tau, dtype):
+    """Values at f32's lowest and highest: differences first, whatever the temperature."""
+    require_gpu()
+    from mixture_experts_layer_side_gb300.distill import DistillLoss
+    from test_distill_gpu import check, make
+    T, V, K = 5, 900, 6
+    lo, hi = torch.finfo(torch.float32).min, torch.finfo(torch.float32).max
+    _, z, ids, vals, dloss = make(T, V, K, dtype, 4, masked=0.0)
+    vals[0] = lo                                  # all masked alike: uniform
+    vals[1] = torch.tensor([lo, lo, lo, 1.0, 2.0, -3.0])
+    vals[2] = torch.tensor([hi, 0.0, 1.0, lo, 5.0, 6.0])
+    vals[3] = hi
+    vals[4] = torch.tensor([lo, -np.inf, lo, -np.inf, 0.0, 0.0])
+    ids[4, 4:] = -1
+    d = DistillLoss(T, V, K)
+    a = [t.cuda() for t in (z, ids, vals, dloss)]
+    loss, lse = d.forward(*a[:3], temperature=tau)
+    dz = d.backward(*a[:3], lse, a[3], temperature=tau)
+    loss2, dz2 = d.forward_backward(*a, temperature=tau)
+    d.check()
+    check(z, ids, vals, dloss, tau, loss, lse, dz, dtype)
+    check(z, ids, vals, dloss, tau, loss2, None, dz2, dtype)
+
+
 # ---------------------------------------------------------------- embedding
 @pytest.mark.parametrize("N", [40, 5000])
 def test_embedding_the_lowest_id_is_an_error_where_there_is_no_padding(N):
