@@ -99,6 +99,21 @@ def test_distill_teacher_values_of_the_types_ends(tau, dtype):
     check(z, ids, vals, dloss, tau, loss2, None, dz2, dtype)
 
 
+@pytest.mark.parametrize("V,dtype", [(900011, "bf16"), (600011, "f32")])
+def test_distill_rows_past_eight_blocks(V, dtype):
+    """A row too long for eight blocks' shared memory: the step is two launches."""
+    require_gpu()
+    from mixture_experts_layer_side_gb300 import _lib
+    from mixture_experts_layer_side_gb300.distill import DistillLoss
+    from test_distill_gpu import make, run_all
+    run_all(2, V, 16, dtype, 1.0, 1)
+    _, z, ids, vals, dloss = make(2, V, 16, dtype, 1)
+    d = DistillLoss(2, V, 16)
+    before = _lib.mok_launch_count()
+    d.forward_backward(z.cuda(), ids.cuda(), vals.cuda(), dloss.cuda())
+    assert _lib.mok_launch_count() - before == 2
+
+
 # ---------------------------------------------------------------- embedding
 @pytest.mark.parametrize("N", [40, 5000])
 def test_embedding_the_lowest_id_is_an_error_where_there_is_no_padding(N):
