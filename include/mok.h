@@ -627,7 +627,8 @@ typedef enum { MOK_TYPE_BF16 = 0, MOK_TYPE_F32 = 1 } mok_dtype;
  * not scaled by tau^2.  K = 1 is the cross entropy of a label.
  *
  *   mok_distill_forward   loss and lse
- *   mok_distill_backward  dz from the forward's lse
+ *   mok_distill_backward  dz from the forward's lse (which has to be in f32's
+ *                         range: with tau < 1 a row of the lowest value's is not)
  *   mok_distill_step      both at once: loss, lse and dz
  * All sums in f32 and in a fixed order.  1 <= K <= MOK_DISTILL_MAX_TOP, V <= 2^30;
  * T = 0 does nothing.  ws: mok_distill_workspace_size bytes (for at

@@ -1694,7 +1694,7 @@ mok_status distill(DistillMode mode, int32_t T, int32_t V, int32_t K, mok_dtype 
   p.dz = dz;
   p.lddz = lddz;
   p.hdr = static_cast<int32_t*>(ws);
-  p.lse_scratch = reinterpret_cast<float*>(p.hdr + kHeaderWords);
+  p.sums = reinterpret_cast<float2*>(p.hdr + kHeaderWords);
   p.in_place = in_place;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   Phase ph(MOK_PHASE_DISTILL, st, 0);
@@ -1707,7 +1707,7 @@ mok_status distill(DistillMode mode, int32_t T, int32_t V, int32_t K, mok_dtype 
 }  // namespace
 
 size_t mok_distill_workspace_size(int32_t T, int32_t V, int32_t K) {
-  return check_distill_sizes(T, V, K) == MOK_OK ? align256(kHeaderWords * 4 + (size_t)T * 4) : 0;
+  return check_distill_sizes(T, V, K) == MOK_OK ? align256(kHeaderWords * 4 + (size_t)T * sizeof(float2)) : 0;
 }
 
 mok_status mok_distill_forward(int32_t T, int32_t V, int32_t K, mok_dtype type, const void* z, int64_t ldz,

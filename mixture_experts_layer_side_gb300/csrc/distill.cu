@@ -351,6 +351,7 @@ __device__ __forceinline__ void store_loss(const DistillParams& q, long t, const
   if (lane == 0) {
     q.loss[t] = l;
     if (q.lse) q.lse[t] = fmaf(base, q.inv_tau, log_s);
+    if (q.sums) q.sums[t] = make_float2(base, a.s);
   }
 }
 
@@ -541,11 +542,17 @@ __global__ void __launch_bounds__(kGradWorkers + 32) distill_gradient_kernel(Dis
     q_base = 1.0f / a.s;
   } else {
     __syncthreads();
-    // z / tau - lse = (z - lse tau) / tau: base is that logit, q_base what its rounding left
-    const double z0 = (double)q.lse_in[t] * (double)q.tau;
-    base = (float)z0;
-    const float left = isinf(base) ? 0.0f : (float)((double)base - z0);
-    q_base = left == 0.0f ? 1.0f : fast_exp2(left * c);
+    if (q.sums) {
+      const float2 s = q.sums[t];
+      base = s.x;
+      q_base = 1.0f / s.y;
+    } else {
+      // z / tau - lse = (z - lse tau) / tau: base is that logit, q_base what its rounding left
+      const double z0 = (double)q.lse_in[t] * (double)q.tau;
+      base = (float)z0;
+      const float left = isinf(base) ? 0.0f : (float)((double)base - z0);
+      q_base = left == 0.0f ? 1.0f : fast_exp2(left * c);
+    }
   }
   const float g = q.dloss[t] * q.inv_tau;
   const bool any = sh.any, same = row.head == grad.head;
@@ -661,6 +668,8 @@ cudaError_t launch_gradient(const DistillParams& p, int shares, int* launches, c
 template <typename Z>
 cudaError_t launch(DistillMode mode, DistillParams p, int* launches, cudaStream_t st) {
   *launches = 0;
+  float2* const sums = p.sums;
+  p.sums = nullptr;
   if (mode == DISTILL_FORWARD) return launch_forward<Z>(p, launches, st);
   const long vecs = row_vectors<Z>(p);
   if (mode == DISTILL_STEP) {
@@ -670,10 +679,10 @@ cudaError_t launch(DistillMode mode, DistillParams p, int* launches, cudaStream_
     while (shares < kMaxShare && vecs > share * shares) shares *= 2;
     while (shares < kMaxShare && (long)p.T * shares < 2l * sm_count() && vecs >= 4l * kGradWorkers * shares) shares *= 2;
     if (vecs <= kMostVecs * shares) return launch_gradient<Z, true>(p, shares, launches, st);
-    if (!p.lse) p.lse = p.lse_scratch;
+    // (with the sums themselves in between: lse may be past f32 where the step's gradient is not)
+    p.sums = sums;
     const cudaError_t e = launch_forward<Z>(p, launches, st);
     if (e != cudaSuccess) return e;
-    p.lse_in = p.lse;
   }
   return launch_gradient<Z, false>(p, (int)((vecs + kShareVecs - 1) / kShareVecs), launches, st);
 }

@@ -15,8 +15,8 @@ struct DistillParams {
   const float* lse_in;  // backward alone
   const float* dloss;
   float* loss;
-  float* lse;          // may be null in the step
-  float* lse_scratch;  // [T]
+  float* lse;        // may be null in the step
+  float2* sums;      // [T] largest logit and sum of the row, for a step in two launches; else null
   void* dz;        // [T, lddz]
   long lddz;
   int in_place;    // the gradient's rows lie where the logits are

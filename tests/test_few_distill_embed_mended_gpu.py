@@ -114,6 +114,26 @@ def test_distill_rows_past_eight_blocks(V, dtype):
     assert _lib.mok_launch_count() - before == 2
 
 
+@pytest.mark.parametrize("V", [9000, 900011])
+def test_distill_step_on_rows_of_the_lowest_value_at_a_low_temperature(V):
+    """The lowest value over the temperature is past f32; the differences are zero all the same."""
+    require_gpu()
+    from mixture_experts_layer_side_gb300.distill import DistillLoss
+    z = torch.full((2, V), torch.finfo(torch.bfloat16).min, dtype=torch.bfloat16)
+    z[1, 100:] = -np.inf
+    ids = torch.tensor([[0, 5], [7, 9]]).int()
+    d = DistillLoss(2, V, 2)
+    loss, dz = d.forward_backward(z.cuda(), ids.cuda(), torch.zeros(2, 2).cuda(), torch.ones(2).cuda(), temperature=0.5)
+    d.check()
+    np.testing.assert_allclose(loss.cpu().numpy(), [np.log(V) + np.log(0.5), np.log(100) + np.log(0.5)], rtol=1e-5)
+    q = torch.zeros((2, V), dtype=torch.float64)
+    q[0], q[1, :100] = 1 / V, 1 / 100
+    q[0, ids[0].long()] -= 0.5
+    q[1, ids[1].long()] -= 0.5
+    err = (dz.double().cpu() - 2 * q).abs()
+    assert (err <= 2.0 ** -8 * (2 * q).abs() + 1e-5 * 2 * q.abs().amax(1, keepdim=True)).all()
+
+
 # ---------------------------------------------------------------- embedding
 @pytest.mark.parametrize("N", [40, 5000])
 def test_embedding_the_lowest_id_is_an_error_where_there_is_no_padding(N):
