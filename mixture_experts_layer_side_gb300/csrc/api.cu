@@ -1663,7 +1663,8 @@ mok_status distill(DistillMode mode, int32_t T, int32_t V, int32_t K, mok_dtype 
                    float* loss, float* lse, void* dz, int64_t lddz, void* ws, size_t ws_bytes, void* stream) {
   MOK_TRY(check_distill_sizes(T, V, K));
   MOK_TRY(check_dtype(type));
-  if (!(tau > 0.0f) || isinf(tau) || isinf(1.0f / tau)) return MOK_ERR_INVALID_ARG;
+  // (the kernels multiply by log2(e) / tau)
+  if (!(tau > 0.0f) || isinf(tau) || isinf(1.4426950408889634f / tau)) return MOK_ERR_INVALID_ARG;
   if (T == 0) return MOK_OK;
   if (!z || !ids || !vals || !ws || !aligned16(ws) || ldz < V || !aligned_to(z, type)) return MOK_ERR_INVALID_ARG;
   if (mode != DISTILL_BACKWARD && (!loss || (!lse && mode == DISTILL_FORWARD))) return MOK_ERR_INVALID_ARG;

@@ -94,6 +94,15 @@ def test_distill_refuses_rows_past_32_bit_columns(lib):
         assert lib.LIB.mok_distill_forward(1, V, 8, 0, A, V, A, A, 1.0, A, A, A, BIG, None) == UNSUPPORTED
 
 
+def test_distill_refuses_a_temperature_whose_factor_is_infinite(lib):
+    def forward(tau):
+        return lib.LIB.mok_distill_forward(4, 100, 8, 0, A, 100, A, A, tau, A, A, A, 8, None)
+
+    assert forward(4.3e-39) == forward(1e-30) == 3  # (the workspace is too small)
+    for tau in (4.2e-39, 3.5e-39, 2.9e-39, 1e-45):
+        assert forward(tau) == INVALID
+
+
 def test_embedding_refuses_a_pad_id_that_is_no_int32(lib):
     from mixture_experts_layer_side_gb300.embedding import MoKEmbedding
     for pad in (None, 0, -1, 9, 10, 2 ** 31 - 1, -2 ** 31 + 1):
