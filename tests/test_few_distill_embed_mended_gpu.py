@@ -17,6 +17,44 @@ def small_layer(shape, prec="bf16", seed=3):
     return MoKDecoder(Shape(*shape), precision=prec), make_inputs(Shape(*shape), "uniform", seed=seed)
 
 
+# a unit whose tiles are whole, tiles cut along K, experts of more rows than a step of the epilogue, 64 rows side by side
+A_SHAPES = [(1, 128, 128, 4, 1), (7, 512, 1024, 4, 2), (33, 384, 640, 9, 3), (128, 1024, 384, 3, 2)]
+
+
+@pytest.mark.parametrize("shape", A_SHAPES)
+def test_few_second_part_of_the_hidden_values(shape):
+    """h = h_t and u = h_t (even columns) or h_t (1 + 2^-12) (odd ones), W2 = +w and -w in turn: a's first bf16
+    parts are equal but for boundaries between two bf16, so that y is what the second parts say.
+
+    Tolerance.  a as two bf16 is off by 2^-9 of its second part, which is at most 2^-9 of a: 2^-18 |a|.  Its f32
+    arithmetic (an exponential, a division, two products) and the sums over K (the tensor core's too, a few units of
+    2^-23 of the largest term for each 16 of K) stay under 2^-19 |a| beside it.  y sums I of them; out is rounded
+    once, 2^-8 of itself at most.  Without the second parts y would be off by half of I |a| 2^-12, 16 times the bound."""
+    require_gpu()
+    T, H, I, E, k = shape
+    dec, inp = small_layer(shape)
+    x = torch.zeros((T, H), dtype=torch.bfloat16)
+    x[:, 0] = 1 + torch.arange(T) / 32         # exact in bf16
+    x[:, H - 1] = x[:, 0] / 64
+    W1, W3 = torch.zeros((E, H, I)), torch.zeros((E, H, I))
+    W1[:, 0], W3[:, 0] = 1, 1
+    W3[:, H - 1, 1::2] = 1 / 64                # x_0 / 64 / 64 = x_0 2^-12
+    w = 1 + (torch.arange(H) % 4) / 4
+    W2 = torch.empty((E, I, H))
+    W2[:, 0::2], W2[:, 1::2] = w, -w
+    s = torch.zeros((T, k))
+    s[:, 0] = 1
+    idx = (torch.arange(T)[:, None] + torch.arange(k)) % E
+    out = dec.forward(x.cuda(), idx.int().cuda(), s.cuda(), *[m.bfloat16().cuda() for m in (W1, W3, W2)])
+    dec.check()
+    h = np64(x[:, 0])
+    a = h / (1 + np.exp(-h)) * h
+    ref = -(I / 2) * 2.0 ** -12 * a[:, None] * np64(w)
+    bound = I * (2.0 ** -18 + 2.0 ** -19) * a[:, None] * np64(w) + 2.0 ** -8 * np.abs(ref)
+    err = np.abs(np64(out) - ref)
+    assert (err <= bound).all(), float((err / bound).max())
+
+
 @pytest.mark.parametrize("shape", [(1, 7168, 128, 256, 8), (5, 7168, 128, 256, 8), (3, 1152, 128, 130, 8)])
 def test_few_router_with_an_infinite_input(shape):
     """An infinite x makes the token's logits +-inf, wherever in its row it stands: the experts of +inf come first,
