@@ -67,6 +67,8 @@ class MokConfig(ctypes.Structure):
 
 class MokMx(ctypes.Structure):
     _fields_ = [("q", ctypes.c_void_p), ("scale", ctypes.c_void_p)]
+    tensors = None  # (codes, scales) of a descriptor made by mx(), which keeps them alive
+    made_of = None  # their shapes and device (None: not both dense and of one byte an element)
 
 
 class MokLayout(ctypes.Structure):
@@ -180,7 +182,12 @@ def config(minibatch_rows=0, ring_slots=0, capacity_mult=0.0, comm_sms=0, debug_
 
 def mx(q, scale):
     """MXFP8 tensor descriptor (codes, scales) for mok_forward / mok_backward."""
-    return MokMx(q.data_ptr(), scale.data_ptr())
+    m = MokMx(q.data_ptr(), scale.data_ptr())
+    m.tensors = (q, scale)
+    if q.is_contiguous() and scale.is_contiguous() and q.element_size() == scale.element_size() == 1 and \
+            q.device == scale.device:
+        m.made_of = (tuple(q.shape), tuple(scale.shape), q.device)
+    return m
 
 
 def mok_version():

@@ -2,6 +2,8 @@
 
 from __future__ import annotations
 
+import math
+
 import torch
 
 from . import _lib
@@ -15,7 +17,8 @@ class MoKDecoder:
     (at most 128); a call takes any number from 0 to that.
 
     Weights as for ``MoKLayer.forward``: bf16 tensors, or in MXFP8 mode the
-    forward descriptors of ``quantize_weights``.  Calls on one object must not
+    forward descriptors of ``quantize_weights`` (or of ``_lib.mx``; one that was
+    filled with bare addresses names no tensors to check).  Calls on one object must not
     overlap (they share the workspace).  Errors found on the device (an expert
     id outside [0, E)) are raised by ``check``.  After a timeout the results
     of all calls since the last ``check`` are void; ``check`` raises it and
@@ -30,6 +33,7 @@ class MoKDecoder:
             raise _lib.MokError(2, "unsupported shape")
         self.ws = torch.zeros(n, dtype=torch.uint8, device=self.device)
         self._w13, self._w2 = (shape.E, shape.H, shape.I), (shape.E, shape.I, shape.H)
+        self._mx13, self._mx2 = (((E, r, c), (E, r // 32, c), self.device) for E, r, c in (self._w13, self._w2))
 
     def _weights(self, W1, W3, W2):
         d, bf16 = self.device, torch.bfloat16
@@ -37,9 +41,17 @@ class MoKDecoder:
             if not (fits(W1, self._w13, bf16, d) and fits(W3, self._w13, bf16, d) and fits(W2, self._w2, bf16, d)):
                 for name, W, shape in (("W1", W1, self._w13), ("W3", W3, self._w13), ("W2", W2, self._w2)):
                     tensor(W, name, shape, (bf16,), d)
-        elif not (type(W1) is type(W3) is type(W2) is _lib.MokMx):
-            for name, W in (("W1", W1), ("W3", W3), ("W2", W2)):
+        elif not (type(W1) is type(W3) is type(W2) is _lib.MokMx and
+                  W1.made_of == W3.made_of == self._mx13 and W2.made_of == self._mx2):
+            for name, W, (codes, scales, _) in (("W1", W1, self._mx13), ("W3", W3, self._mx13), ("W2", W2, self._mx2)):
                 require(isinstance(W, _lib.MokMx), f"{name}: an MXFP8 descriptor is wanted")
+                if W.tensors is None:
+                    continue
+                for part, t, shape in (("codes", W.tensors[0], codes), ("scales", W.tensors[1], scales)):
+                    require(t.element_size() == 1, f"{name}: {part} of {t.dtype}, wanted bytes")
+                    # (as one long row, or as a matrix, they are the same bytes)
+                    same = t.dim() != 3 and t.is_contiguous() and t.numel() == math.prod(shape)
+                    tensor(t.view(shape) if same else t, f"{name}: {part}", shape, (t.dtype,), d)
 
     def _begin(self, x, out):
         s, d = self.shape, self.device

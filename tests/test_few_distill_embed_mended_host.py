@@ -39,6 +39,40 @@ def test_decoder_is_ready_again_after_a_timeout(lib, monkeypatch, status, zeroed
     assert bool((dec.ws == 0).all()) == zeroed
 
 
+def test_decoder_refuses_mxfp8_descriptors_of_other_tensors(lib, monkeypatch):
+    """Codes and scales of another shape, orientation or type, which would be read out of range or as other
+    values.  (The call itself is taken away: what passes the checks is not enqueued.)"""
+    called = []
+    monkeypatch.setattr(lib, "mok_few_forward", lambda *a: called.append(a))
+    monkeypatch.setattr(lib, "mok_few_layer", lambda *a: called.append(a))
+    T, H, I, E, k = 4, 256, 128, 4, 2
+    dec = small_decoder("mxfp8")
+
+    def mx(*shape, scales=None, dtype=torch.uint8):
+        scales = scales or (shape[0], shape[1] // 32, shape[2])
+        return lib.mx(torch.zeros(shape, dtype=dtype), torch.zeros(scales, dtype=torch.uint8))
+
+    x, idx, s = torch.zeros((T, H)).bfloat16(), torch.zeros((T, k), dtype=torch.int32), torch.zeros((T, k))
+    Wr = torch.zeros((H, E)).bfloat16()
+    w13, w2 = mx(E, H, I), mx(E, I, H)
+    raw = lib.MokMx(256, 256)
+    flat = lib.mx(torch.zeros(E * H * I, dtype=torch.uint8), torch.zeros((E * H // 32, I), dtype=torch.uint8))
+    for W in ((w13, w13, w2), (mx(E, H, I, dtype=torch.float8_e4m3fn), w13, w2), (raw, raw, raw), (flat, w13, w2)):
+        called.clear()
+        dec.forward(x, idx, s, *W)
+        dec.layer(x, Wr, *W)
+        assert len(called) == 2
+    called.clear()
+    for W in ((w2, w13, w2), (w13, w2, w2), (w13, w13, w13), (mx(E - 1, H, I), w13, w2), (w13, mx(E, H, I // 2), w2),
+              (w13, w13, mx(E, I, H, scales=(E, I, H // 32))), (mx(E, H, I, scales=(E, H // 32 - 1, I)), w13, w2),
+              (mx(E, H, I, dtype=torch.int16), w13, w2), (lib.mx(torch.zeros(9, dtype=torch.uint8), w13.tensors[1]), w13, w2),
+              (lib.mx(w13.tensors[0][..., ::2], w13.tensors[1]), w13, w2), (torch.zeros((E, H, I)).bfloat16(), w13, w2)):
+        for call in (lambda: dec.forward(x, idx, s, *W), lambda: dec.layer(x, Wr, *W)):
+            with pytest.raises(ValueError):
+                call()
+    assert not called
+
+
 def distill_calls(lib):
     """The step and the backward on 4 rows of 100 bf16 logits at `z`, rows `ldz` apart, in a workspace that is too
     small for them, so that what passes the other checks is still not enqueued."""
