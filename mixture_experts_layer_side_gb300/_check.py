@@ -3,9 +3,14 @@ from serving and training code directly (the C ABI sees only pointers)."""
 
 from __future__ import annotations
 
+import contextlib
+
 import torch
 
 from . import _lib
+
+# (without the look whether CUDA is initialised: a call's tensors are there)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 class MokArgError(_lib.MokError, ValueError):
@@ -52,3 +57,25 @@ def on(device):
     """``device`` with its index, as tensors name it."""
     d = torch.device(device)
     return torch.device(d.type, torch.cuda.current_device()) if d.type == "cuda" and d.index is None else d
+
+
+def workspace(size, device, what):
+    """size() bytes of zeros on ``device``.  (The size goes by the device's
+    SMs: it is asked for with that device current.)"""
+    with torch.cuda.device(device) if device.type == "cuda" else contextlib.nullcontext():
+        n = size()
+        if n == 0:
+            raise _lib.MokError(2, what)
+        return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def away(device, stream):
+    """Whether a call on ``device`` and ``stream`` (None: the current one) is
+    to be made by ``run_on``: it is not on the current device."""
+    return device.type == "cuda" and _current_device() != device.index
+
+
+def run_on(owner, stream, call, *args):
+    """call(*args) with the owner's device current."""
+    with torch.cuda.device(owner.device):
+        return call(*args, stream=stream)

@@ -7,7 +7,7 @@ import math
 import torch
 
 from . import _lib
-from ._check import fits, on, require, tensor
+from ._check import away, fits, on, require, run_on, tensor, workspace
 from .inputs import Shape
 from .layer import PRECISIONS
 
@@ -28,10 +28,8 @@ class MoKDecoder:
         self.shape = shape
         self.prec = PRECISIONS[precision]
         self.device = on(device)
-        n = _lib.mok_few_workspace_size(_lib.shape_of(shape.T, shape.H, shape.I, shape.E, shape.k), self.prec)
-        if n == 0:
-            raise _lib.MokError(2, "unsupported shape")
-        self.ws = torch.zeros(n, dtype=torch.uint8, device=self.device)
+        cshape = _lib.shape_of(shape.T, shape.H, shape.I, shape.E, shape.k)
+        self.ws = workspace(lambda: _lib.mok_few_workspace_size(cshape, self.prec), self.device, "unsupported shape")
         self._w13, self._w2 = (shape.E, shape.H, shape.I), (shape.E, shape.I, shape.H)
         self._mx13, self._mx2 = (((E, r, c), (E, r // 32, c), self.device) for E, r, c in (self._w13, self._w2))
 
@@ -70,6 +68,8 @@ class MoKDecoder:
 
     def forward(self, x, topk_idx, scores, W1, W3, W2, out=None, stream=None):
         """out [T, H] for the routing given (int32 ids and f32 scores [T, k])."""
+        if away(self.device, stream):
+            return run_on(self, stream, self.forward, x, topk_idx, scores, W1, W3, W2, out)
         T, out, cshape = self._begin(x, out)
         self._weights(W1, W3, W2)
         rows, d = (T, self.shape.k), self.device
@@ -83,6 +83,8 @@ class MoKDecoder:
     def layer(self, x, Wr, W1, W3, W2, bias=None, out=None, stream=None):
         """(out, topk_idx, scores), the router included: Wr bf16 [H, E], bias
         f32 [E] or None (selection only)."""
+        if away(self.device, stream):
+            return run_on(self, stream, self.layer, x, Wr, W1, W3, W2, bias, out)
         s, d = self.shape, self.device
         T, out, cshape = self._begin(x, out)
         self._weights(W1, W3, W2)
@@ -98,6 +100,8 @@ class MoKDecoder:
 
     def check(self, stream=None):
         """Synchronise and raise if the device recorded an error."""
+        if away(self.device, stream):
+            return run_on(self, stream, self.check)
         st = _lib.mok_check(self.ws, stream)
         if st == _lib.MOK_ERR_TIMEOUT:
             # a call that gave up leaves the abort word and counts of arrivals behind

@@ -5,7 +5,7 @@ from __future__ import annotations
 import torch
 
 from . import _lib
-from ._check import fits, on, require, rows_fit, tensor
+from ._check import away, fits, on, require, rows_fit, run_on, tensor, workspace
 
 _TYPES = (torch.bfloat16, torch.float32)
 
@@ -21,10 +21,7 @@ class DistillLoss:
     def __init__(self, rows, vocab, top, device="cuda"):
         self.rows, self.vocab, self.top = rows, vocab, top
         self.device = on(device)
-        n = _lib.mok_distill_workspace_size(rows, vocab, top)
-        if n == 0:
-            raise _lib.MokError(2, "unsupported sizes")
-        self.ws = torch.zeros(n, dtype=torch.uint8, device=self.device)
+        self.ws = workspace(lambda: _lib.mok_distill_workspace_size(rows, vocab, top), self.device, "unsupported sizes")
 
     def _begin(self, z, ids, vals, temperature):
         d = self.device
@@ -59,6 +56,8 @@ class DistillLoss:
 
     def forward(self, z, ids, vals, temperature=1.0, stream=None):
         """(loss, lse), f32 [T] each."""
+        if away(self.device, stream):
+            return run_on(self, stream, self.forward, z, ids, vals, temperature)
         T, tau = self._begin(z, ids, vals, temperature)
         loss = torch.empty(T, dtype=torch.float32, device=self.device)
         lse = torch.empty(T, dtype=torch.float32, device=self.device)
@@ -68,6 +67,8 @@ class DistillLoss:
     def backward(self, z, ids, vals, lse, dloss, temperature=1.0, out=None, stream=None):
         """dz of z's type, from the forward's ``lse``; ``out`` may be z itself,
         but not overlap it in part."""
+        if away(self.device, stream):
+            return run_on(self, stream, self.backward, z, ids, vals, lse, dloss, temperature, out)
         T, tau = self._begin(z, ids, vals, temperature)
         self._row_values(T, "lse", lse)
         self._row_values(T, "dloss", dloss)
@@ -77,6 +78,8 @@ class DistillLoss:
 
     def forward_backward(self, z, ids, vals, dloss, temperature=1.0, out=None, stream=None):
         """(loss, dz) in one call; ``out`` as in ``backward``."""
+        if away(self.device, stream):
+            return run_on(self, stream, self.forward_backward, z, ids, vals, dloss, temperature, out)
         T, tau = self._begin(z, ids, vals, temperature)
         self._row_values(T, "dloss", dloss)
         dz = self._gradient(z, out)
@@ -86,6 +89,8 @@ class DistillLoss:
 
     def check(self, stream=None):
         """Synchronise and raise if the device recorded an error."""
+        if away(self.device, stream):
+            return run_on(self, stream, self.check)
         st = _lib.mok_check(self.ws, stream)
         if st != 0:
             raise _lib.MokError(st, "distillation: device status")

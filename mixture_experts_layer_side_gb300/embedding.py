@@ -5,7 +5,7 @@ from __future__ import annotations
 import torch
 
 from . import _lib
-from ._check import fits, on, require, tensor
+from ._check import away, fits, on, require, run_on, tensor, workspace
 
 _TYPES = (torch.bfloat16, torch.float32)
 
@@ -25,10 +25,8 @@ class MoKEmbedding:
         # (a wider number would name another id in the call; the lowest says that there is none)
         require(pad_id is None or -2**31 < self.pad_id < 2**31, f"pad_id: {pad_id}, wanted an int32 above the lowest")
         self.device = on(device)
-        n = _lib.mok_embed_workspace_size(vocab, hidden, tokens)
-        if n == 0:
-            raise _lib.MokError(2, "unsupported sizes")
-        self.ws = torch.zeros(n, dtype=torch.uint8, device=self.device)
+        self.ws = workspace(lambda: _lib.mok_embed_workspace_size(vocab, hidden, tokens), self.device,
+                            "unsupported sizes")
 
     def _ids(self, ids):
         if not (type(ids) is torch.Tensor and ids.numel() <= self.tokens and
@@ -40,6 +38,8 @@ class MoKEmbedding:
 
     def forward(self, table, ids, scale=1.0, out=None, stream=None):
         """[*ids.shape, hidden] of the table's type."""
+        if away(self.device, stream):
+            return run_on(self, stream, self.forward, table, ids, scale, out)
         d = self.device
         shape = self._ids(ids)
         if not (getattr(table, "dtype", None) in _TYPES and fits(table, self._table, table.dtype, d)):
@@ -55,6 +55,8 @@ class MoKEmbedding:
         """The table's gradient [vocab, hidden] in ``out`` (bf16 or f32; f32 by
         default): written whole, or with ``accumulate`` added to the rows that
         ``ids`` names."""
+        if away(self.device, stream):
+            return run_on(self, stream, self.backward, dx, ids, scale, out, accumulate)
         d = self.device
         shape = self._ids(ids)
         if not (getattr(dx, "dtype", None) in _TYPES and fits(dx, shape, dx.dtype, d)):
@@ -69,6 +71,8 @@ class MoKEmbedding:
 
     def check(self, stream=None):
         """Synchronise and raise if the device recorded an error."""
+        if away(self.device, stream):
+            return run_on(self, stream, self.check)
         st = _lib.mok_check(self.ws, stream)
         if st != 0:
             raise _lib.MokError(st, "embedding: device status")

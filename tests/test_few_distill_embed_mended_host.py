@@ -144,3 +144,53 @@ def test_embedding_refuses_a_pad_id_that_is_no_int32(lib):
     for pad in (2 ** 32 + 5, 2 ** 31, -2 ** 31, -2 ** 32 + 3):
         with pytest.raises(ValueError):
             MoKEmbedding(10, 8, 4, pad_id=pad, device="cpu")
+
+
+def test_calls_are_made_on_the_device_of_their_tensors(lib, monkeypatch):
+    """With another device current than the object's: the workspace's size is asked for, and every call made, with
+    the object's own.  (Devices of a fake; "meta" tensors, and checks that take them for the device's.)"""
+    from mixture_experts_layer_side_gb300 import _check, decode, distill, embedding
+    from mixture_experts_layer_side_gb300.inputs import Shape
+    now, real_zeros, real_empty = [0], torch.zeros, torch.empty
+
+    class Device:
+        def __init__(self, device):
+            self.index = torch.device(device).index
+
+        def __enter__(self):
+            self.was, now[0] = now[0], self.index
+
+        def __exit__(self, *a):
+            now[0] = self.was
+
+    monkeypatch.setattr(_check, "_current_device", lambda: now[0])
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+    monkeypatch.setattr(torch, "zeros", lambda *a, device=None, **kw: real_zeros(*a, device="meta", **kw))
+    monkeypatch.setattr(torch, "empty", lambda *a, device=None, **kw: real_empty(*a, device="meta", **kw))
+    for m in (_check, decode, distill, embedding):
+        for n in ("fits", "rows_fit"):
+            if hasattr(m, n):
+                monkeypatch.setattr(m, n, lambda *a: True)
+    seen, asked = [], []
+    for n in ("mok_few_forward", "mok_few_layer", "mok_distill_forward", "mok_distill_backward", "mok_distill_step",
+              "mok_embed_forward", "mok_embed_backward"):
+        monkeypatch.setattr(lib, n, lambda *a, n=n: seen.append((n, now[0])))
+    monkeypatch.setattr(lib, "mok_check", lambda *a: seen.append(("mok_check", now[0])) or 0)
+    for n in ("mok_few_workspace_size", "mok_distill_workspace_size", "mok_embed_workspace_size"):
+        monkeypatch.setattr(lib, n, lambda *a: asked.append(now[0]) or 256)
+    t = real_empty((4, 2), device="meta")
+    dec = decode.MoKDecoder(Shape(4, 256, 128, 4, 2), device="cuda:1")
+    loss = distill.DistillLoss(4, 2, 2, device="cuda:1")
+    emb = embedding.MoKEmbedding(10, 8, 8, device="cuda:1")
+    assert asked == [1, 1, 1] and now == [0]
+    dec.forward(t, t, t, t, t, t)
+    dec.layer(t, t, t, t, t)
+    loss.forward(t, t, t)
+    loss.backward(t, t, t, t, t)
+    loss.forward_backward(t, t, t, t)
+    emb.forward(t, t)
+    emb.backward(t, t)
+    for part in (dec, loss, emb):
+        part.check()
+    assert len(seen) == 10 and all(dev == 1 for _, dev in seen) and now == [0], seen
