@@ -60,22 +60,50 @@ def on(device):
 
 
 def workspace(size, device, what):
-    """size() bytes of zeros on ``device``.  (The size goes by the device's
-    SMs: it is asked for with that device current.)"""
+    """size() bytes of zeros on ``device``, there for every stream.  (The size
+    goes by the device's SMs: it is asked for with that device current.)"""
     with torch.cuda.device(device) if device.type == "cuda" else contextlib.nullcontext():
         n = size()
         if n == 0:
             raise _lib.MokError(2, what)
-        return torch.zeros(n, dtype=torch.uint8, device=device)
+        ws = torch.zeros(n, dtype=torch.uint8, device=device)
+        if device.type == "cuda" and not torch.cuda.is_current_stream_capturing():
+            torch.cuda.current_stream().synchronize()
+    return ws
+
+
+def _handle(stream):
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
 def away(device, stream):
     """Whether a call on ``device`` and ``stream`` (None: the current one) is
-    to be made by ``run_on``: it is not on the current device."""
-    return device.type == "cuda" and _current_device() != device.index
+    to be made by ``run_on``: it is not on the current device and stream."""
+    if device.type != "cuda":
+        return False
+    return (_current_device() != device.index or
+            stream is not None and _handle(stream) != torch.cuda.current_stream().cuda_stream)
 
 
 def run_on(owner, stream, call, *args):
-    """call(*args) with the owner's device current."""
-    with torch.cuda.device(owner.device):
-        return call(*args, stream=stream)
+    """call(*args) with the owner's device and ``stream`` current, as under
+    torch.cuda.stream: what the call allocates is the stream's own, so that it
+    takes no memory that another stream still reads, and what it returns may
+    be used and dropped on the caller's stream."""
+    d = owner.device
+    if stream is None:
+        with torch.cuda.device(d):
+            return call(*args)
+    if not isinstance(stream, torch.cuda.Stream):
+        h = int(stream)
+        stream = torch.cuda.default_stream(d) if h == 0 else torch.cuda.ExternalStream(h, device=d)
+    require(stream.device == d, f"stream: on {stream.device}, wanted {d}")
+    caller = torch.cuda.current_stream(d)
+    if type(stream) is torch.cuda.Stream:  # (a foreign stream may be gone when the workspace is freed)
+        owner.ws.record_stream(stream)
+    with torch.cuda.stream(stream):
+        got = call(*args)
+    for t in got if isinstance(got, tuple) else (got,):
+        if t is not None:
+            t.record_stream(caller)
+    return got

@@ -189,3 +189,93 @@ def test_embedding_the_lowest_id_is_an_error_where_there_is_no_padding(N):
             e.check()
         assert err.value.status == 5
         e.check()
+
+
+# ---------------------------------------------------------------- streams
+def stream_calls():
+    """(name, call(stream) -> tensors, bytes of the largest of them) of every class's methods, of sizes that the
+    allocator serves with a block of their own."""
+    from mixture_experts_layer_side_gb300.distill import DistillLoss
+    from mixture_experts_layer_side_gb300.embedding import MoKEmbedding
+    from test_distill_gpu import make
+    dec, inp = small_layer((128, 16384, 128, 4, 2))
+    i = {n: v.cuda() for n, v in inp.items()}
+    Wr = torch.randn((16384, 4), device="cuda").bfloat16()
+    W = [i[n] for n in ("W1", "W3", "W2")]
+    yield "few forward", lambda s: dec.forward(i["x"], i["idx"], i["s"], *W, stream=s), 128 * 16384 * 2, dec
+    yield "few layer", lambda s: dec.layer(i["x"], Wr, *W, stream=s), 128 * 16384 * 2, dec
+    T, V = 512, 8192
+    a = [t.cuda() for t in make(T, V, 8, "f32", 1)[1:]]
+    d = DistillLoss(T, V, 8)
+    lse = d.forward(*a[:3])[1]
+    yield "distill backward", lambda s: d.backward(*a[:3], lse, a[3], stream=s), T * V * 4, d
+    yield "distill step", lambda s: d.forward_backward(*a, stream=s), T * V * 4, d
+    e = MoKEmbedding(4096, 1024, 4096)
+    table, ids = torch.randn(4096, 1024, device="cuda"), torch.randint(0, 4096, (4096,), device="cuda").int()
+    yield "embed forward", lambda s: e.forward(table, ids, stream=s), 4096 * 1024 * 4, e
+    yield "embed backward", lambda s: e.backward(table, ids, stream=s), 4096 * 1024 * 4, e
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_outputs_on_another_stream_take_no_memory_in_use(raw):
+    """A tensor that the current stream still has to read is dropped, and a call is made on another stream at once:
+    its outputs may not take that memory.  And outputs that are dropped while the current stream still reads them
+    are not taken by the next call on the other."""
+    require_gpu()
+    side = torch.cuda.Stream()
+    arg = side.cuda_stream if raw else side
+    for name, call, size, owner in stream_calls():
+        want = call(None)
+        want = want if isinstance(want, tuple) else (want,)
+        torch.cuda.synchronize()
+        torch.cuda.empty_cache()
+        kept = torch.full((size // 4,), 7, dtype=torch.int32, device="cuda")
+        torch.cuda.synchronize()
+        torch.cuda._sleep(100_000_000)  # 50 ms
+        copy = kept.clone()
+        del kept
+        got = call(arg)
+        got = got if isinstance(got, tuple) else (got,)
+        torch.cuda.synchronize()
+        assert (copy == 7).all(), name
+        assert all(torch.equal(a, b) for a, b in zip(want, got)), name
+        del copy, got
+        # outputs read on the current stream, late, and dropped before
+        got = call(arg)
+        got = got if isinstance(got, tuple) else (got,)
+        torch.cuda.current_stream().wait_stream(side)
+        torch.cuda._sleep(100_000_000)
+        copies = [t.clone() for t in got]
+        del got
+        with torch.cuda.stream(side):
+            over = [torch.zeros_like(t) for t in want]
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(want, copies)), name
+        owner.check(stream=arg)
+        del over, copies, want
+
+
+def test_a_workspace_is_ready_for_every_stream():
+    """The zeros of a new workspace are there for a first call on another stream."""
+    require_gpu()
+    from mixture_experts_layer_side_gb300.embedding import MoKEmbedding
+    side = torch.cuda.Stream()
+    table, ids = torch.randn(64, 64, device="cuda"), torch.arange(64, device="cuda").int()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100_000_000)
+    e = MoKEmbedding(64, 64, 64)
+    assert torch.cuda.current_stream().query()  # nothing of it is still to come
+    out = e.forward(table, ids, stream=side)
+    e.check(stream=side)
+    assert torch.equal(out, table)
+
+
+def test_a_stream_of_another_device_is_refused():
+    require_gpu()
+    from mixture_experts_layer_side_gb300 import _check
+
+    class Other:
+        device = torch.device("cuda", 7)
+
+    with pytest.raises(ValueError):
+        _check.run_on(Other, torch.cuda.Stream(), lambda: None)
