@@ -299,10 +299,11 @@ __device__ __forceinline__ void router_logits(const FewParams& p, uint8_t* smem,
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
         const int h = hb + i * warps * down;
+        if (h >= rows) break;  // (an infinite x times 0 is NaN)
         const uint32_t vv[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
         for (int t = 0; t < TOK; ++t) {
-          const float x = h < rows ? xs[h * TOK + t] : 0.0f;  // (past the part both are 0: an infinite x times 0 is NaN)
+          const float x = xs[h * TOK + t];
 #pragma unroll
           for (int m = 0; m < 4; ++m) {
             acc[t][2 * m] = fmaf(x, __uint_as_float(vv[m] << 16), acc[t][2 * m]);
@@ -975,27 +976,26 @@ __global__ void __launch_bounds__(MX ? 448 : 384, 1) few_kernel(const __grid_con
     __syncwarp();
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA
-    uint32_t stage = 0, phase = 0, count = 0;
-    bool fine = true;
-    for (int ph = 0; ph < 4; ++ph) {
-      const Cut& cut = ctl->cuts[ph];
-      const int g = ph >> 1;
-      for (Run r = ctl->runs[ph]; r.left > 0 && fine; step(r, cut)) {
-        const Seg s = r.seg;
-        const int n = (sched.unit_n[s.unit] + 15) & ~15;
-        const bool second = g == 0 || s.n * 256 + 128 < p.H;
-        const uint32_t buf = count & 1;
-        fine = __all_sync(0xffffffffu, mbar_wait(&ctl->tempty[buf], ((count >> 1) & 1) ^ 1, wc));
-        if (!fine) break;
-        tc_fence_after();
-        const uint32_t d0 = tmem + buf * 2 * d_cols, d1 = d0 + d_cols;
-        for (int kb = s.k0; kb < s.k1; ++kb) {
-          fine = __all_sync(0xffffffffu, mbar_wait(&ctl->full_a[stage], phase, wc) &&
-                                             mbar_wait(&ctl->full_b[stage], phase, wc) &&
-                                             (!MX || mbar_wait(&ctl->scales[stage], phase, wc)));
+    if (lane == 0) {
+      uint32_t stage = 0, phase = 0, count = 0;
+      bool fine = true;
+      for (int ph = 0; ph < 4; ++ph) {
+        const Cut& cut = ctl->cuts[ph];
+        const int g = ph >> 1;
+        for (Run r = ctl->runs[ph]; r.left > 0 && fine; step(r, cut)) {
+          const Seg s = r.seg;
+          const int n = (sched.unit_n[s.unit] + 15) & ~15;
+          const bool second = g == 0 || s.n * 256 + 128 < p.H;
+          const uint32_t buf = count & 1;
+          fine = mbar_wait(&ctl->tempty[buf], ((count >> 1) & 1) ^ 1, wc);
           if (!fine) break;
           tc_fence_after();
-          if (lane == 0) {
+          const uint32_t d0 = tmem + buf * 2 * d_cols, d1 = d0 + d_cols;
+          for (int kb = s.k0; kb < s.k1; ++kb) {
+            fine = mbar_wait(&ctl->full_a[stage], phase, wc) && mbar_wait(&ctl->full_b[stage], phase, wc) &&
+                   (!MX || mbar_wait(&ctl->scales[stage], phase, wc));
+            if (!fine) break;
+            tc_fence_after();
             // the tokens' operand was written with cp.async: order it before the tensor core's (async-proxy) reads
             fence_proxy_async_shared();
             const uint32_t a0 = smem_u32(smem + (size_t)stage * stage_bytes), b0 = a0 + 2 * kATile;
@@ -1031,25 +1031,21 @@ __global__ void __launch_bounds__(MX ? 448 : 384, 1) few_kernel(const __grid_con
               }
             }
             mma_commit(&ctl->empty[stage]);
+            if (++stage == (uint32_t)p.stages) { stage = 0; phase ^= 1; }
           }
-          __syncwarp();
-          if (++stage == (uint32_t)p.stages) { stage = 0; phase ^= 1; }
+          if (!fine) break;
+          mma_commit(&ctl->tfull[buf]);
+          ++count;
         }
-        if (!fine) break;
-        if (lane == 0) mma_commit(&ctl->tfull[buf]);
-        __syncwarp();
-        ++count;
       }
-    }
-    if (!fine) {
-      // no MMA may still run when the CTA leaves
-      if (lane == 0) {
+      if (!fine) {
+        // no MMA may still run when the CTA leaves
         ctl->failed = 1;
         mma_commit(&ctl->drained);
         mbar_drain(&ctl->drained, 0, 1000000000ull);
       }
-      __syncwarp();
     }
+    __syncwarp();
   } else if (warp < 4) {
     // ---------------------------------------------------------------- tokens' operand
     const int tid = threadIdx.x - 64;
