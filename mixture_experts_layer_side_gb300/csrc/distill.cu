@@ -65,11 +65,6 @@ __device__ __forceinline__ F2 pair(float lo, float hi) {
 __device__ __forceinline__ void split(F2 p, float& lo, float& hi) {
   asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(p.v));
 }
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-  F2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-  return r;
-}
 __device__ __forceinline__ F2 add2(F2 a, F2 b) {
   F2 r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
@@ -422,7 +417,7 @@ constexpr int kGradWorkers = 128;
 
 template <typename Z>
 __global__ void __launch_bounds__(kForwardWorkers + 32) distill_forward_kernel(DistillParams q, int shares, int most) {
-  extern __shared__ __align__(16) uint8_t smem[];
+  extern __shared__ __align__(128) uint8_t smem[];
   __shared__ Shared<kForwardWorkers / 32> sh;
   cluster_begin(shares);
   const long t = blockIdx.x / shares;
