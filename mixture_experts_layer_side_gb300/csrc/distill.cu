@@ -24,7 +24,7 @@
 //    the step a CTA brings its share, 32 or 64 KB where eight are enough, to shared
 //    memory with bulk copies, where it stays between the sum and the gradient;
 //    six CTAs of 32 KB an SM are in different phases, so that loads and stores
-//    overlap: 395 us for 4,096 rows of 131,072 bf16, loss and gradient, 81% of
+//    overlap: 393 us for 4,096 rows of 131,072 bf16, loss and gradient, 82% of
 //    the rate of a copy.  (Twice the threads a CTA: 412; a CTA a row of its own
 //    that streams it twice, the second time from L2: 471.)
 //  * The teacher's list (at most MOK_DISTILL_MAX_TOP entries) is a warp's
@@ -410,8 +410,9 @@ struct Gradient {
 };
 
 // All kernels: workers, and a last warp for the list.
-// Forward: 1,000 rows of 50,001 bf16 20 us, 75% of the rate of a copy; of 128
-// workers 22, of 512 26.  4,096 rows of 131,072: 150 us, all of it.
+// Forward: 1,000 rows of 50,001 bf16 20 to 23 us (boxes differ), 65 to 75% of
+// the rate of a copy; of 128 workers 22, of 512 26 where 256 take 20.  4,096
+// rows of 131,072: 150 us, all of it; the gradient of them alone 339, 95%.
 constexpr int kForwardWorkers = 256;
 constexpr int kGradWorkers = 128;
 
@@ -642,7 +643,8 @@ cudaError_t launch_forward(const DistillParams& p, int* launches, cudaStream_t s
 
 constexpr long kShareVecs = 2048;   // 32 KB: six CTAs an SM
 // 64 KB, where it makes a row one CTA, or in f32, and rows fill the GPU.  4,096
-// rows of 32,000 bf16: 88 us, in two shares 97; f32 175, in four 185.  Else more
+// rows of 32,000 bf16 with lists of 8: 88 us, in two shares 94 (of 64: 99 and
+// 103); f32 with lists of 64 196, in four 202 (of 8: 171 and 170).  Else more
 // CTAs overlap better: 2,048 rows of 65,536 bf16 in two 102, in four 101; 256
 // rows of 32,000 in one 17.5, in shares of 32 KB 14.9.
 constexpr long kLongShareVecs = 4096;

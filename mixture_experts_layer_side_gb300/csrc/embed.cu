@@ -16,7 +16,8 @@
 //  * Up to kRankTokens tokens are placed by counting the pairs before each of
 //    them, 16 threads a token: no pass waits for another.  (With the sums of
 //    1,024 bf16 columns: 2,048 tokens 15 us, by the radix sort 23; 8,192
-//    tokens 36 and 31.)
+//    tokens 36 and 31.  Of 8 threads a token: 2,048 tokens 17.5 us, 4,096 23.1,
+//    where 16 take 15.2 and 20.4, and 32 14.2 and 17.1.)
 //  * More are sorted by one cluster of kSortCtas CTAs: the pairs of a few
 //    thousand to a few million tokens are small beside dx, and a cluster's
 //    barriers and distributed shared memory join its histograms without a
@@ -32,7 +33,10 @@
 //    131,072 f32 rows: 196 us; by reductions at L2 233.)
 //
 // 8,192 tokens of 2,048 bf16 columns into a table of 65,536 rows, written
-// whole: 83 us, where 268 MB of stores alone take 67 (a fill's rate, 4 TB/s).
+// whole: 83 us.  The zeros are the most of it: the launch that writes them
+// beside the sort takes 67 (3.7 TB/s; beside the counting of one token 49, where
+// a memset of the table takes 38), and the sums and the last launch, 13 and 8 by
+// themselves, wait for all of it.
 // 16,384 tokens of 7,168 (Zipf ids) added to f32 rows: 119 us, 71% of the rate
 // of a copy; beside the sums, the sort takes 17 and the last launch under 10.
 #include <cooperative_groups.h>
