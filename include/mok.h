@@ -584,7 +584,7 @@ mok_status mok_ep_unsort_scores(const mok_shape* shape, const mok_config* cfg, c
  * this shape; a workspace of a shape with more tokens, all else equal, serves
  * too.  The caller zeroes it once before its first use (cudaMemset); calls
  * leave it ready for the next one.  After MOK_ERR_TIMEOUT it has to be zeroed
- * again.  Errors stay in its first word until mok_check reads and clears it.
+ * again; calls before that record MOK_ERR_TIMEOUT too.  Errors stay in its first word until mok_check reads and clears it.
  * Calls that share a workspace must not overlap.  Tensor pointers are 16-byte
  * aligned (MOK_ERR_INVALID_ARG otherwise).
  */
