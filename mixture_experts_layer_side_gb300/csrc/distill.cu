@@ -410,7 +410,7 @@ struct Gradient {
 };
 
 // All kernels: workers, and a last warp for the list.
-// Forward: 1,000 rows of 50,001 bf16 20 to 23 us (boxes differ), 65 to 75% of
+// Forward: 1,000 rows of 50,001 bf16 20 to 23 us (GPUs differ), 65 to 75% of
 // the rate of a copy; of 128 workers 22, of 512 26 where 256 take 20.  4,096
 // rows of 131,072: 150 us, all of it; the gradient of them alone 339, 95%.
 constexpr int kForwardWorkers = 256;

@@ -279,3 +279,90 @@ def test_a_stream_of_another_device_is_refused():
 
     with pytest.raises(ValueError):
         _check.run_on(Other, torch.cuda.Stream(), lambda: None)
+
+
+# ---------------------------------------------------------------- the longest rows and offsets
+@pytest.mark.parametrize("V,launches", [(851968, 1), (851976, 2)])
+def test_distill_rows_that_just_fit_eight_blocks(V, launches):
+    """The last length of eight blocks' shared memory, with the longest list beside it, and the next."""
+    require_gpu()
+    from mixture_experts_layer_side_gb300 import _lib
+    from mixture_experts_layer_side_gb300.distill import DistillLoss
+    from test_distill_gpu import check, make
+    _, z, ids, vals, dloss = make(2, V, 512, "bf16", 5)
+    d = DistillLoss(2, V, 512)
+    before = _lib.mok_launch_count()
+    loss, dz = d.forward_backward(z.cuda(), ids.cuda(), vals.cuda(), dloss.cuda())
+    assert _lib.mok_launch_count() - before == launches
+    d.check()
+    check(z, ids, vals, dloss, 1.0, loss, None, dz, "bf16")
+
+
+def test_distill_offsets_past_32_bits():
+    """Rows 2^26 elements apart: the last lies 2.6e9 elements from the first."""
+    require_gpu()
+    from mixture_experts_layer_side_gb300.distill import DistillLoss
+    from test_distill_gpu import check, make
+    T, V, K, ld = 40, 5003, 7, 1 << 26
+    _, z, ids, vals, dloss = make(T, V, K, "bf16", 6)
+    a = [t.cuda() for t in (ids, vals, dloss)]
+    far = torch.empty((T - 1) * ld + V, dtype=torch.bfloat16, device="cuda").as_strided((T, V), (ld, 1))
+    far.copy_(z)
+    d = DistillLoss(T, V, K)
+    loss, lse = d.forward(far, *a[:2])
+    dz = d.backward(far, *a[:2], lse, a[2])
+    check(z, ids, vals, dloss, 1.0, loss, lse, dz, "bf16")
+    loss2, dz2 = d.forward_backward(far, *a, out=far)
+    d.check()
+    check(z, ids, vals, dloss, 1.0, loss2, None, dz2, "bf16")
+
+
+def test_distill_the_longest_row():
+    """2^30 logits of 0 but for a few: sums of terms that are 1 are exact, so that the tolerances are the types'."""
+    require_gpu()
+    from mixture_experts_layer_side_gb300.distill import DistillLoss
+    V = 1 << 30
+    z = torch.zeros((1, V), dtype=torch.bfloat16, device="cuda")
+    z[0, V - 1], z[0, 1 << 29] = 16.0, -float("inf")
+    ids = torch.tensor([[V - 1, 3]], dtype=torch.int32, device="cuda")
+    d = DistillLoss(1, V, 2)
+    one = torch.ones(1, device="cuda")
+    total = V - 2 + np.exp(16.0)
+    loss, dz = d.forward_backward(z, ids, torch.zeros((1, 2), device="cuda"), one)
+    want = np.log(0.5) - (0.5 * 16.0 - np.log(total))
+    assert abs(float(loss) - want) <= 1e-5 * (1 + abs(want))
+    fwd, lse = d.forward(z, ids, torch.zeros((1, 2), device="cuda"))
+    assert abs(float(lse) - np.log(total)) <= 1e-5 * np.log(total) and abs(float(fwd) - want) <= 1e-5 * (1 + abs(want))
+    d.check()
+    g = dz[0]
+    assert float(g[1 << 29]) == 0.0
+    for at, q in ((V - 1, np.exp(16.0) / total - 0.5), (3, 1 / total - 0.5)):
+        assert abs(float(g[at]) - q) <= 2.0 ** -8 * abs(q)
+    rest = torch.ones(V, dtype=torch.bool, device="cuda")
+    rest[[V - 1, 3, 1 << 29]] = False
+    lo, hi = g.masked_fill(~rest, float(g[0])).aminmax()
+    assert abs(float(lo) * total - 1) <= 2.0 ** -8 + 1e-5 and abs(float(hi) * total - 1) <= 2.0 ** -8 + 1e-5
+
+
+@pytest.mark.parametrize("V,H,N", [(300000, 8192, 100), (300000, 8192, 5000), (1 << 30, 2, 100), (1 << 30, 2, 5000)])
+def test_embedding_offsets_past_32_bits(V, H, N):
+    """Rows past 2^31 elements, and the most rows that a table may have: ids near the end, two tokens each."""
+    require_gpu()
+    from mixture_experts_layer_side_gb300.embedding import MoKEmbedding
+    e = MoKEmbedding(V, H, N, pad_id=V - 1)
+    g = torch.Generator(device="cuda").manual_seed(N)
+    ids = V - 2 - torch.randperm(N, generator=g, device="cuda") // 2
+    ids[0] = V - 1
+    dx = torch.randn((N, H), generator=g, device="cuda").bfloat16()
+    want = torch.zeros((N, H), device="cuda", dtype=torch.float64)      # of the last N rows
+    use = ids != V - 1
+    want.index_add_(0, (ids - (V - N))[use], dx[use].double())
+    out = torch.full((V, H), 3.0, dtype=torch.bfloat16, device="cuda")
+    e.backward(dx, ids.int(), out=out)
+    assert torch.equal(out[V - N:], want.float().bfloat16())            # (two bf16 terms: exact in f32 but for their span)
+    assert not out[:V - N].any()
+    e.backward(dx, ids.int(), out=out, accumulate=True)
+    assert (out[V - N:].double() - 2 * want).abs().max() <= 2.0 ** -7 * want.abs().max()
+    got = e.forward(out, ids.int())
+    e.check()
+    assert torch.equal(got, out[ids])
