@@ -357,7 +357,12 @@ enum {
   MOK_PHASE_DISTILL = 17,      /* distillation loss, gradient or both */
   MOK_PHASE_EMBED_FWD = 18,    /* embedding lookup */
   MOK_PHASE_EMBED_BWD = 19,    /* embedding gradient */
-  MOK_NUM_PHASES = 20
+  MOK_PHASE_RESIDUAL_FWD = 20, /* residual join: norms, gate, dropout */
+  MOK_PHASE_RESIDUAL_BWD = 21, /* its gradients */
+  MOK_PHASE_DROPOUT = 22,      /* dropout by itself */
+  MOK_PHASE_FFN_FWD = 23,      /* dense feed-forward block */
+  MOK_PHASE_FFN_BWD = 24,      /* its gradients */
+  MOK_NUM_PHASES = 25
 };
 mok_status mok_trace_enable(int32_t on);
 mok_status mok_trace_read(float* ms /* [MOK_NUM_PHASES] */, int32_t* count /* [MOK_NUM_PHASES] */);
@@ -677,6 +682,89 @@ mok_status mok_embed_forward(int32_t V, int32_t H, int32_t N, mok_dtype type, co
 mok_status mok_embed_backward(int32_t V, int32_t H, int32_t N, mok_dtype dx_type, const void* dx, const int32_t* ids,
                               int32_t pad_id, float scale, mok_dtype grad_type, void* dtable, int32_t accumulate,
                               void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Dropout from a counter-based generator, whose mask is never stored.
+ *
+ *   out_i = x_i / (1 - p)  where element i is kept, else 0 (whatever x_i is)
+ *
+ * i counts a [rows, cols] matrix's elements in row-major order, without the
+ * gaps between rows.  Element i is kept unless its 16 bits are below p * 2^16,
+ * p being rounded to a multiple of 2^-16: Philox-4x32-10 (Salmon, Moraes, Dror,
+ * Shaw, "Parallel random numbers: as easy as 1, 2, 3", SC 2011) with the seed
+ * as its key (low word first) and the counter words (low, high of i / 8, low,
+ * high of the call's number) gives eight elements' bits, low halves first.
+ * The gradient of x is the same call on the gradient of out.
+ *
+ *   call      number of the call: another for each mask
+ *   call_dev  (device) int64 or NULL: added to `call` when the kernel runs, so
+ *             that a captured graph's replays get masks of their own
+ * 0 <= p <= 1 (1: all dropped).  x and out may be the same (pointer and
+ * stride), else no row of one may share a byte with a row of the other
+ * (MOK_ERR_INVALID_ARG).  rows * cols < 2^60; either may be 0.
+ */
+typedef struct {
+  float p;
+  uint64_t seed;
+  uint64_t call;
+  const int64_t* call_dev;
+} mok_drop;
+mok_status mok_dropout(int64_t rows, int64_t cols, mok_dtype type, const void* x, int64_t ldx, const mok_drop* drop,
+                       void* out, int64_t ldo, void* stream);
+
+/*
+ * The join of a block with its residual stream: the norm after the block, its
+ * gate, scale and dropout, the addition, and the norm before the next block.
+ *
+ *   z  = y / sqrt(mean y^2 + eps) * w_out      (z = y where w_out is NULL)
+ *   x' = x + scale * gate * dropout(z)         (no gate: 1)
+ *   n  = x' / sqrt(mean x'^2 + eps) * w_next   (no n where w_next is NULL)
+ *
+ * x and x' are the stream, y and n the branch; both bf16 or f32, the branch no
+ * wider than the stream.  Weights and gate have the branch's type.  The means
+ * go over the H elements of a row, the squares are summed in f32 (values past
+ * about 1e18 overflow).  Everything is computed in f32 and each output rounded
+ * once: n comes from x' before its rounding.
+ *
+ *   w_out, w_next  (device) [H] or NULL;  gate  (device) [gate_rows, H], row r
+ *   of it for T / gate_rows consecutive rows of the batch (gate_rows divides T;
+ *   1: a gate per channel, T: per element), or NULL with gate_rows 0
+ *   dropout        p = 0: none; else as mok_dropout of the [T, H] matrix z
+ *
+ *   forward   (device) x [T, H], y [T, H] -> xo = x' [T, H], n [T, H], rows ldx,
+ *             ldy, ldxo, ldn elements apart, at any element alignment.
+ *             y NULL: n of x alone (no w_out, gate or dropout; xo has to be NULL)
+ *   backward  from the gradients dxo of x' and dn of n (either may be NULL: 0),
+ *             x' as the forward stored it and y:
+ *             dx, dy [T, H] in the types of x and y (a NULL one is not written);
+ *             dw_out, dw_next f32 [H], dgate [gate_rows, H] in the branch's type
+ *             x' is read where dn is given, y where w_out or gate is.
+ *             With w_next, dn and dw_next are both there or both NULL; dy, and
+ *             with it dw_out and dgate where their weights are, goes with y.
+ * xo may be x, n may be y, dx may be dxo and dy may be dn or y (same pointer,
+ * type and stride); otherwise outputs share no byte with inputs or each other
+ * (MOK_ERR_INVALID_ARG, for the matrices).  1 <= H <= MOK_RESIDUAL_MAX_HIDDEN,
+ * T <= 2^30; T = 0 gives zero gradients of the weights.  Sums in a fixed order:
+ * the same call gives the same bits.
+ * ws: mok_residual_workspace_size bytes for at least this T, for the backward
+ * pass alone; calls that share it must not overlap.
+ */
+#define MOK_RESIDUAL_MAX_HIDDEN 16384
+typedef struct {
+  int32_t T, H;
+  mok_dtype stream_type, branch_type;
+  int32_t gate_rows;
+  float eps, scale;
+  const void *w_out, *gate, *w_next;
+  mok_drop drop;
+} mok_residual;
+size_t mok_residual_workspace_size(int32_t T, int32_t H);
+mok_status mok_residual_forward(const mok_residual* r, const void* x, int64_t ldx, const void* y, int64_t ldy, void* xo,
+                                int64_t ldxo, void* n, int64_t ldn, void* stream);
+mok_status mok_residual_backward(const mok_residual* r, const void* x, int64_t ldx, const void* y, int64_t ldy,
+                                 const void* dxo, int64_t lddxo, const void* dn, int64_t lddn, void* dx, int64_t lddx,
+                                 void* dy, int64_t lddy, float* dw_out, void* dgate, float* dw_next, void* ws,
+                                 size_t ws_bytes, void* stream);
 
 /* Synchronise `stream`, then return (and clear) the status recorded in the
  * workspace's error word; MOK_OK if none. */

@@ -100,10 +100,12 @@ def run_on(owner, stream, call, *args):
     require(stream.device == d, f"stream: on {stream.device}, wanted {d}")
     caller = torch.cuda.current_stream(d)
     if type(stream) is torch.cuda.Stream:  # (a foreign stream may be gone when the workspace is freed)
-        owner.ws.record_stream(stream)
+        for ws in (owner.ws, getattr(owner, "ctx", None)):
+            if ws is not None:
+                ws.record_stream(stream)
     with torch.cuda.stream(stream):
         got = call(*args)
-    for t in got if isinstance(got, tuple) else (got,):
+    for t in got if isinstance(got, tuple) else got.values() if isinstance(got, dict) else (got,):
         if t is not None:
             t.record_stream(caller)
     return got

@@ -41,11 +41,12 @@ EXPORTS = ["mok_workspace_size", "mok_ctx_size", "mok_workspace_layout", "mok_bu
            "mok_ep_plan", "mok_ep_pack_rows", "mok_ep_combine_rows", "mok_ep_unsort_scores",
            "mok_few_workspace_size", "mok_few_forward", "mok_few_layer", "mok_distill_workspace_size",
            "mok_distill_forward", "mok_distill_backward", "mok_distill_step", "mok_embed_workspace_size",
-           "mok_embed_forward", "mok_embed_backward"]
+           "mok_embed_forward", "mok_embed_backward", "mok_dropout", "mok_residual_workspace_size",
+           "mok_residual_forward", "mok_residual_backward"]
 
 PHASES = ["schedule", "fwd_gemm", "fwd_combine", "bwd_da", "bwd_ds", "bwd_dx", "bwd_dx_combine", "bwd_wg13",
           "bwd_wg2", "quant", "bwd_sort", "router_fwd", "router_bwd", "bwd_replay", "fwd_fused", "fwd_sort",
-          "few", "distill", "embed_fwd", "embed_bwd"]
+          "few", "distill", "embed_fwd", "embed_bwd", "residual_fwd", "residual_bwd", "dropout", "ffn_fwd", "ffn_bwd"]
 
 
 class MokError(RuntimeError):
@@ -69,6 +70,18 @@ class MokMx(ctypes.Structure):
     _fields_ = [("q", ctypes.c_void_p), ("scale", ctypes.c_void_p)]
     tensors = None  # (codes, scales) of a descriptor made by mx(), which keeps them alive
     made_of = None  # their shapes and device (None: not both dense and of one byte an element)
+
+
+class MokDrop(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_float), ("seed", ctypes.c_uint64), ("call", ctypes.c_uint64),
+                ("call_dev", ctypes.c_void_p)]
+
+
+class MokResidual(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("H", ctypes.c_int32), ("stream_type", ctypes.c_int32),
+                ("branch_type", ctypes.c_int32), ("gate_rows", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("scale", ctypes.c_float), ("w_out", ctypes.c_void_p), ("gate", ctypes.c_void_p),
+                ("w_next", ctypes.c_void_p), ("drop", MokDrop)]
 
 
 class MokLayout(ctypes.Structure):
@@ -130,6 +143,11 @@ def _load():
         "mok_embed_workspace_size": (sz, [i32, i32, i32]),
         "mok_embed_forward": (i32, [i32, i32, i32, i32, P, P, i32, f32, P, P, sz, P]),
         "mok_embed_backward": (i32, [i32, i32, i32, i32, P, P, i32, f32, i32, P, i32, P, sz, P]),
+        "mok_dropout": (i32, [i64, i64, i32, P, i64, ctypes.POINTER(MokDrop), P, i64, P]),
+        "mok_residual_workspace_size": (sz, [i32, i32]),
+        "mok_residual_forward": (i32, [ctypes.POINTER(MokResidual), P, i64, P, i64, P, i64, P, i64, P]),
+        "mok_residual_backward": (i32, [ctypes.POINTER(MokResidual), P, i64, P, i64, P, i64, P, i64, P, i64, P, i64, P,
+                                        P, P, P, sz, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -429,3 +447,45 @@ def mok_embed_backward(dx, ids, pad_id, scale, dtable, accumulate, ws, stream=No
     _ok(LIB.mok_embed_backward(V, H, ids.numel(), dtype_of(dx), dx.data_ptr(), ids.data_ptr(), pad_id, scale,
                                dtype_of(dtable), dtable.data_ptr(), 1 if accumulate else 0, ws.data_ptr(), ws.nbytes,
                                _stream(stream)), "mok_embed_backward")
+
+
+# ---------------------------------------------------------------- dropout, residual join
+MOK_RESIDUAL_MAX_HIDDEN = 16384
+
+
+def mok_drop(p, seed, call=0, call_dev=None):
+    return MokDrop(p, seed, call, _ptr(call_dev))
+
+
+def mok_dropout(x, drop, out, stream=None):
+    """x and out: matrices whose rows may be apart."""
+    rows, cols = x.shape
+    _ok(LIB.mok_dropout(rows, cols, dtype_of(x), x.data_ptr(), _rows_apart(x), drop, out.data_ptr(), _rows_apart(out),
+                        _stream(stream)), "mok_dropout")
+
+
+def mok_residual(T, H, stream_type, branch_type, eps, scale, w_out, gate, gate_rows, w_next, drop):
+    r = MokResidual(T, H, stream_type, branch_type, gate_rows, eps, scale, _ptr(w_out), _ptr(gate), _ptr(w_next))
+    if drop is not None:
+        r.drop = drop
+    return r
+
+
+def mok_residual_workspace_size(T, H):
+    return LIB.mok_residual_workspace_size(T, H)
+
+
+def _rows(t):
+    """Pointer and distance of the rows of a matrix, or of none."""
+    return (None, 0) if t is None else (t.data_ptr(), _rows_apart(t))
+
+
+def mok_residual_forward(r, x, y, xo, n, stream=None):
+    _ok(LIB.mok_residual_forward(r, *_rows(x), *_rows(y), *_rows(xo), *_rows(n), _stream(stream)),
+        "mok_residual_forward")
+
+
+def mok_residual_backward(r, x, y, dxo, dn, dx, dy, dw_out, dgate, dw_next, ws, stream=None):
+    _ok(LIB.mok_residual_backward(r, *_rows(x), *_rows(y), *_rows(dxo), *_rows(dn), *_rows(dx), *_rows(dy),
+                                  _ptr(dw_out), _ptr(dgate), _ptr(dw_next), ws.data_ptr(), ws.nbytes, _stream(stream)),
+        "mok_residual_backward")

@@ -16,6 +16,7 @@
 #include "embed.cuh"
 #include "few.cuh"
 #include "gemm.cuh"
+#include "residual.cuh"
 
 namespace mok {
 
@@ -184,7 +185,8 @@ const char* const kPhaseNames[MOK_NUM_PHASES] = {
     "mok schedule",  "mok fwd gemm",   "mok fwd combine", "mok bwd dA'",      "mok bwd ds",
     "mok bwd dX",    "mok bwd dX combine", "mok bwd dW1|dW3", "mok bwd dW2",   "mok mxfp8 quant",
     "mok bwd sort",  "mok router fwd", "mok router bwd",  "mok bwd replay",   "mok fwd fused",
-    "mok fwd sort",  "mok few tokens", "mok distill",     "mok embed",        "mok embed grad"};
+    "mok fwd sort",  "mok few tokens", "mok distill",     "mok embed",        "mok embed grad",
+    "mok residual",  "mok residual grad", "mok dropout",   "mok ffn",          "mok ffn grad"};
 
 class Phase {
  public:
@@ -1805,6 +1807,206 @@ mok_status mok_embed_backward(int32_t V, int32_t H, int32_t N, mok_dtype dx_type
   Phase ph(MOK_PHASE_EMBED_BWD, st, 0);
   int launches = 0;
   const cudaError_t e = launch_embed_backward(dx_type, grad_type, p, &launches, st);
+  g_launches += launches;
+  return e == cudaSuccess ? MOK_OK : MOK_ERR_CUDA;
+}
+
+// ---------------------------------------------------------------- dropout, residual join
+namespace {
+
+// A matrix of T rows of `w` bytes, `ld` bytes apart (null: none).
+struct Rows {
+  uintptr_t at, w, ld;
+};
+Rows rows_of(const void* p, int64_t ld, int64_t cols, mok_dtype type) {
+  const uintptr_t es = type == MOK_TYPE_BF16 ? 2 : 4;
+  return {reinterpret_cast<uintptr_t>(p), es * (uintptr_t)cols, es * (uintptr_t)ld};
+}
+// The same rows (then an element is read before it is written), or none in common.
+bool same_or_apart(const Rows& a, const Rows& b, int64_t T) {
+  if (!a.at || !b.at || T == 0 || a.w == 0) return true;
+  if (a.at == b.at && a.w == b.w && (T == 1 || a.ld == b.ld)) return true;
+  if (b.at >= a.at + a.ld * (T - 1) + a.w || a.at >= b.at + b.ld * (T - 1) + b.w) return true;
+  if (a.ld == b.ld) {
+    // the distance from a row of a on to the next row of b, which are all alike
+    const uintptr_t off = b.at >= a.at ? (b.at - a.at) % a.ld : (a.ld - (a.at - b.at) % a.ld) % a.ld;
+    return off >= a.w && off + b.w <= a.ld;
+  }
+  for (int64_t i = 0, j = 0; i < T && j < T;) {
+    const uintptr_t p = a.at + a.ld * i, q = b.at + b.ld * j;
+    if (p < q + b.w && q < p + a.w) return false;
+    if (p < q)
+      ++i;
+    else
+      ++j;
+  }
+  return true;
+}
+bool apart(const Rows& a, const Rows& b, int64_t T) {
+  return !(a.at && a.at == b.at && T > 0 && a.w > 0) && same_or_apart(a, b, T);
+}
+
+mok_status check_matrix(const void* p, int64_t ld, int64_t cols, mok_dtype type) {
+  return p && aligned_to(p, type) && ld >= cols && ld < (int64_t(1) << 40) ? MOK_OK : MOK_ERR_INVALID_ARG;
+}
+
+mok_status drop_params(const mok_drop& d, DropParams* p) {
+  if (!(d.p >= 0.0f && d.p <= 1.0f) || (reinterpret_cast<uintptr_t>(d.call_dev) & 7)) return MOK_ERR_INVALID_ARG;
+  p->key0 = (uint32_t)d.seed;
+  p->key1 = (uint32_t)(d.seed >> 32);
+  p->call = d.call;
+  p->call_dev = d.call_dev;
+  p->below = (uint32_t)lrint((double)d.p * 65536.0);
+  p->scale = p->below < 65536u ? (float)(65536.0 / (65536.0 - p->below)) : 0.0f;
+  return MOK_OK;
+}
+
+mok_status residual_params(const mok_residual* r, ResidualParams* p) {
+  if (!r || r->T < 0 || r->H < 1) return MOK_ERR_INVALID_ARG;
+  MOK_TRY(check_dtype(r->stream_type));
+  MOK_TRY(check_dtype(r->branch_type));
+  if (r->stream_type == MOK_TYPE_BF16 && r->branch_type != MOK_TYPE_BF16) return MOK_ERR_UNSUPPORTED;
+  if (r->H > MOK_RESIDUAL_MAX_HIDDEN || r->T > (1 << 30)) return MOK_ERR_UNSUPPORTED;
+  if (!(r->eps > 0.0f) || isinf(r->eps) || !isfinite(r->scale)) return MOK_ERR_INVALID_ARG;
+  if (r->gate ? r->gate_rows < 1 || r->T % r->gate_rows || r->gate_rows > std::max(r->T, 1) : r->gate_rows != 0)
+    return MOK_ERR_INVALID_ARG;
+  for (const void* w : {r->w_out, r->gate, r->w_next})
+    if (w && !aligned_to(w, r->branch_type)) return MOK_ERR_INVALID_ARG;
+  memset(p, 0, sizeof(*p));
+  p->T = r->T;
+  p->H = r->H;
+  p->G = r->gate_rows;
+  p->rows_per_gate = r->gate_rows ? std::max(1, r->T / r->gate_rows) : 1;
+  p->scale = r->scale;
+  p->eps = r->eps;
+  p->w_out = r->w_out;
+  p->gate = r->gate;
+  p->w_next = r->w_next;
+  return drop_params(r->drop, &p->drop);
+}
+
+}  // namespace
+
+mok_status mok_dropout(int64_t rows, int64_t cols, mok_dtype type, const void* x, int64_t ldx, const mok_drop* drop,
+                       void* out, int64_t ldo, void* stream) {
+  MOK_TRY(check_dtype(type));
+  if (!drop || rows < 0 || cols < 0) return MOK_ERR_INVALID_ARG;
+  if (rows && cols > (int64_t(1) << 60) / rows) return MOK_ERR_UNSUPPORTED;
+  DropParams d;
+  MOK_TRY(drop_params(*drop, &d));
+  if (rows == 0 || cols == 0) return MOK_OK;
+  MOK_TRY(check_matrix(x, ldx, cols, type));
+  MOK_TRY(check_matrix(out, ldo, cols, type));
+  if (!same_or_apart(rows_of(x, ldx, cols, type), rows_of(out, ldo, cols, type), rows)) return MOK_ERR_INVALID_ARG;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  Phase ph(MOK_PHASE_DROPOUT, st, 1);
+  return launch_dropout(type, rows, cols, x, ldx, d, out, ldo, st) == cudaSuccess ? MOK_OK : MOK_ERR_CUDA;
+}
+
+size_t mok_residual_workspace_size(int32_t T, int32_t H) {
+  if (T < 0 || T > (1 << 30) || H < 1 || H > MOK_RESIDUAL_MAX_HIDDEN) return 0;
+  return align256(residual_part_floats(T, H) * 4);
+}
+
+mok_status mok_residual_forward(const mok_residual* r, const void* x, int64_t ldx, const void* y, int64_t ldy, void* xo,
+                                int64_t ldxo, void* n, int64_t ldn, void* stream) {
+  ResidualParams p;
+  MOK_TRY(residual_params(r, &p));
+  const mok_dtype S = r->stream_type, B = r->branch_type;
+  if ((n != nullptr) != (r->w_next != nullptr) && r->T > 0) return MOK_ERR_INVALID_ARG;
+  if (!y && r->T > 0 && (xo || r->w_out || r->gate || p.drop.below || !n)) return MOK_ERR_INVALID_ARG;
+  if (r->T == 0) return MOK_OK;
+  MOK_TRY(check_matrix(x, ldx, r->H, S));
+  if (y) {
+    MOK_TRY(check_matrix(y, ldy, r->H, B));
+    MOK_TRY(check_matrix(xo, ldxo, r->H, S));
+  }
+  if (n) MOK_TRY(check_matrix(n, ldn, r->H, B));
+  const Rows rx = rows_of(x, ldx, r->H, S), ry = rows_of(y, ldy, r->H, B), ro = rows_of(xo, ldxo, r->H, S),
+             rn = rows_of(n, ldn, r->H, B);
+  if (!same_or_apart(rx, ro, r->T) || !apart(ry, ro, r->T) || !same_or_apart(ry, rn, r->T) || !apart(ro, rn, r->T) ||
+      !(y ? apart(rx, rn, r->T) : same_or_apart(rx, rn, r->T)))
+    return MOK_ERR_INVALID_ARG;
+  p.x = x;
+  p.ldx = ldx;
+  p.y = y;
+  p.ldy = ldy;
+  p.xo = xo;
+  p.ldxo = ldxo;
+  p.n = n;
+  p.ldn = ldn;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  Phase ph(MOK_PHASE_RESIDUAL_FWD, st, 0);
+  int launches = 0;
+  const cudaError_t e = launch_residual_forward(S, B, p, &launches, st);
+  g_launches += launches;
+  return e == cudaSuccess ? MOK_OK : MOK_ERR_CUDA;
+}
+
+mok_status mok_residual_backward(const mok_residual* r, const void* x, int64_t ldx, const void* y, int64_t ldy,
+                                 const void* dxo, int64_t lddxo, const void* dn, int64_t lddn, void* dx, int64_t lddx,
+                                 void* dy, int64_t lddy, float* dw_out, void* dgate, float* dw_next, void* ws,
+                                 size_t ws_bytes, void* stream) {
+  ResidualParams p;
+  MOK_TRY(residual_params(r, &p));
+  const mok_dtype S = r->stream_type, B = r->branch_type;
+  const int32_t T = r->T, H = r->H;
+  // which of them belong together
+  if ((dw_next != nullptr) && !r->w_next) return MOK_ERR_INVALID_ARG;
+  if (T > 0 && (dn != nullptr) != (dw_next != nullptr)) return MOK_ERR_INVALID_ARG;
+  if ((dw_out != nullptr) != (dy != nullptr && r->w_out) || (dgate != nullptr) != (dy != nullptr && r->gate)) {
+    if (T > 0 || (dw_out && !r->w_out) || (dgate && !r->gate)) return MOK_ERR_INVALID_ARG;
+  }
+  if (T > 0) {
+    if (!dx && !dy) return MOK_ERR_INVALID_ARG;
+    if (!dxo && !dn) return MOK_ERR_INVALID_ARG;
+    if (dn) {
+      MOK_TRY(check_matrix(dn, lddn, H, B));
+      MOK_TRY(check_matrix(x, ldx, H, S));
+    }
+    if (dxo) MOK_TRY(check_matrix(dxo, lddxo, H, S));
+    if (dx) MOK_TRY(check_matrix(dx, lddx, H, S));
+    if (dy) {
+      MOK_TRY(check_matrix(dy, lddy, H, B));
+      if (r->w_out || r->gate) MOK_TRY(check_matrix(y, ldy, H, B));
+    }
+  }
+  for (const float* w : {static_cast<const float*>(dw_out), static_cast<const float*>(dw_next)})
+    if (w && !aligned_to(w, MOK_TYPE_F32)) return MOK_ERR_INVALID_ARG;
+  if (dgate && !aligned_to(dgate, B)) return MOK_ERR_INVALID_ARG;
+  const bool uses_y = dy && (r->w_out || r->gate);
+  const Rows rx = rows_of(dn ? x : nullptr, ldx, H, S), ry = rows_of(uses_y ? y : nullptr, ldy, H, B),
+             rg = rows_of(dxo, lddxo, H, S), rn = rows_of(dn, lddn, H, B), ox = rows_of(dx, lddx, H, S),
+             oy = rows_of(dy, lddy, H, B);
+  if (!same_or_apart(rg, ox, T) || !apart(rx, ox, T) || !apart(ry, ox, T) || !apart(rn, ox, T) || !apart(ox, oy, T) ||
+      !same_or_apart(rn, oy, T) || !same_or_apart(ry, oy, T) || !apart(rx, oy, T) || !apart(rg, oy, T))
+    return MOK_ERR_INVALID_ARG;
+  if (dw_next || dw_out || dgate) {
+    if (!ws || !aligned16(ws)) return MOK_ERR_INVALID_ARG;
+    if (ws_bytes < mok_residual_workspace_size(T, H)) return MOK_ERR_WORKSPACE_TOO_SMALL;
+  } else if (T == 0) {
+    return MOK_OK;
+  }
+  p.x = x;
+  p.ldx = ldx;
+  p.y = uses_y ? y : nullptr;
+  p.ldy = ldy;
+  p.dxo = dxo;
+  p.lddxo = lddxo;
+  p.dn = dn;
+  p.lddn = lddn;
+  p.dx = dx;
+  p.lddx = lddx;
+  p.dy = dy;
+  p.lddy = lddy;
+  p.dw_out = dw_out;
+  p.dgate = dgate;
+  p.dw_next = dw_next;
+  p.part = static_cast<float*>(ws);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  Phase ph(MOK_PHASE_RESIDUAL_BWD, st, 0);
+  int launches = 0;
+  const cudaError_t e = launch_residual_backward(S, B, p, &launches, st);
   g_launches += launches;
   return e == cudaSuccess ? MOK_OK : MOK_ERR_CUDA;
 }

@@ -1,0 +1,56 @@
+// Dropout's random bits, shared by the kernels that drop (dropout.cu,
+// residual.cu): Philox-4x32 with ten rounds, the counter-based generator of
+// Salmon, Moraes, Dror and Shaw, "Parallel random numbers: as easy as 1, 2,
+// 3" (SC 2011).  A block of eight consecutive elements takes one 128-bit
+// output, 16 bits an element, so nothing is stored between a forward pass and
+// its backward pass: both make the same bits from the element's index.
+//
+// 16 bits and not 32: ten rounds are 20 wide multiplications, which run at
+// half rate.  At one output per four elements they alone would take longer
+// than moving bf16 elements at the HBM's rate; at one per eight they take a
+// third of it.  The price is that p is a multiple of 2^-16.
+#pragma once
+
+#include "mok_internal.cuh"
+
+namespace mok {
+
+struct DropParams {
+  uint32_t key0, key1;       // the seed
+  uint64_t call;             // number of the call ...
+  const int64_t* call_dev;   // ... plus this device word, where it is given
+  uint32_t below;            // p * 65536: elements whose bits are below are dropped; 0: none (dropout off)
+  float scale;               // 1 / (1 - p); 0 where all are dropped
+};
+
+// The counter's upper half, read once per thread.
+__device__ __forceinline__ uint64_t drop_call(const DropParams& d) {
+  return d.call_dev ? d.call + (uint64_t)*d.call_dev : d.call;
+}
+
+__device__ __forceinline__ uint4 philox(uint64_t block, uint64_t call, uint32_t key0, uint32_t key1) {
+  uint4 c = make_uint4((uint32_t)block, (uint32_t)(block >> 32), (uint32_t)call, (uint32_t)(call >> 32));
+#pragma unroll
+  for (int r = 0; r < 10; ++r) {
+    const uint64_t a = (uint64_t)c.x * 0xD2511F53u, b = (uint64_t)c.z * 0xCD9E8D57u;
+    c = make_uint4((uint32_t)(b >> 32) ^ c.y ^ key0, (uint32_t)b, (uint32_t)(a >> 32) ^ c.w ^ key1, (uint32_t)a);
+    key0 += 0x9E3779B9u;
+    key1 += 0xBB67AE85u;
+  }
+  return c;
+}
+
+// Which of the eight elements of a block are kept, element j in bit j.
+__device__ __forceinline__ uint32_t drop_keep8(const DropParams& d, uint64_t block, uint64_t call) {
+  const uint4 r = philox(block, call, d.key0, d.key1);
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+  uint32_t keep = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    keep |= (uint32_t)((w[i] & 0xffffu) >= d.below) << (2 * i);
+    keep |= (uint32_t)((w[i] >> 16) >= d.below) << (2 * i + 1);
+  }
+  return keep;
+}
+
+}  // namespace mok
