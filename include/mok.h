@@ -766,6 +766,45 @@ mok_status mok_residual_backward(const mok_residual* r, const void* x, int64_t l
                                  void* dy, int64_t lddy, float* dw_out, void* dgate, float* dw_next, void* ws,
                                  size_t ws_bytes, void* stream);
 
+/*
+ * The dense gated feed-forward block (a shared expert beside the routed ones,
+ * or a block without routing) and its gradients, in BF16:
+ *
+ *   h = x W1,  u = x W3,  a = silu(h) * u,  out = a W2
+ *
+ *   x, out, dout, dX  (device) bf16 [T, H]
+ *   W1, W3, dW1, dW3  (device) bf16 [H, I];  W2, dW2 (device) bf16 [I, H]
+ *   ctx               (device) mok_ffn_ctx_size() bytes: h, u and a, which the
+ *                     forward keeps for the backward
+ *
+ *   mok_ffn_infer     out alone.  Up to MOK_FEW_MAX_TOKENS tokens with H and I
+ *                     multiples of 128 (and at most MOK_FEW_MAX_HIDDEN) run as mok_few_forward
+ *                     does, at the rate of the weights' read; else as mok_ffn_forward
+ *   mok_ffn_forward   out and ctx
+ *   mok_ffn_backward  all four gradients, of the same x and weights
+ * Sums are f32.  a comes from the f32 h and u and is rounded to bf16 for the
+ * second product (few tokens: to two bf16); h, u, dh and du are rounded to bf16 where
+ * the backward reads them.  H and I are multiples of 8, at most
+ * MOK_FFN_MAX_SIZE; T <= 2^22; T = 0 gives zero gradients of the weights.
+ * Tensors start at 16-byte boundaries; outputs share no byte with inputs
+ * or each other.  Results do not depend on timing: the same call gives the
+ * same bits.
+ * ws: mok_ffn_workspace_size bytes for at least this T (training 0: for
+ * mok_ffn_infer alone), zeroed once by the caller before its first use and
+ * again after MOK_ERR_TIMEOUT; its first word holds errors until mok_check.
+ * Calls that share a workspace must not overlap.
+ */
+#define MOK_FFN_MAX_SIZE 131072
+size_t mok_ffn_workspace_size(int32_t T, int32_t H, int32_t I, int32_t training);
+size_t mok_ffn_ctx_size(int32_t T, int32_t I);
+mok_status mok_ffn_infer(int32_t T, int32_t H, int32_t I, void* ws, size_t ws_bytes, const void* x, const void* W1,
+                         const void* W3, const void* W2, void* out, void* stream);
+mok_status mok_ffn_forward(int32_t T, int32_t H, int32_t I, void* ws, size_t ws_bytes, const void* x, const void* W1,
+                           const void* W3, const void* W2, void* out, void* ctx, void* stream);
+mok_status mok_ffn_backward(int32_t T, int32_t H, int32_t I, void* ws, size_t ws_bytes, const void* ctx, const void* x,
+                            const void* W1, const void* W3, const void* W2, const void* dout, void* dX, void* dW1,
+                            void* dW3, void* dW2, void* stream);
+
 /* Synchronise `stream`, then return (and clear) the status recorded in the
  * workspace's error word; MOK_OK if none. */
 mok_status mok_check(void* ws, void* stream);

@@ -42,7 +42,8 @@ EXPORTS = ["mok_workspace_size", "mok_ctx_size", "mok_workspace_layout", "mok_bu
            "mok_few_workspace_size", "mok_few_forward", "mok_few_layer", "mok_distill_workspace_size",
            "mok_distill_forward", "mok_distill_backward", "mok_distill_step", "mok_embed_workspace_size",
            "mok_embed_forward", "mok_embed_backward", "mok_dropout", "mok_residual_workspace_size",
-           "mok_residual_forward", "mok_residual_backward"]
+           "mok_residual_forward", "mok_residual_backward", "mok_ffn_workspace_size", "mok_ffn_ctx_size",
+           "mok_ffn_infer", "mok_ffn_forward", "mok_ffn_backward"]
 
 PHASES = ["schedule", "fwd_gemm", "fwd_combine", "bwd_da", "bwd_ds", "bwd_dx", "bwd_dx_combine", "bwd_wg13",
           "bwd_wg2", "quant", "bwd_sort", "router_fwd", "router_bwd", "bwd_replay", "fwd_fused", "fwd_sort",
@@ -148,6 +149,11 @@ def _load():
         "mok_residual_forward": (i32, [ctypes.POINTER(MokResidual), P, i64, P, i64, P, i64, P, i64, P]),
         "mok_residual_backward": (i32, [ctypes.POINTER(MokResidual), P, i64, P, i64, P, i64, P, i64, P, i64, P, i64, P,
                                         P, P, P, sz, P]),
+        "mok_ffn_workspace_size": (sz, [i32, i32, i32, i32]),
+        "mok_ffn_ctx_size": (sz, [i32, i32]),
+        "mok_ffn_infer": (i32, [i32, i32, i32, P, sz, P, P, P, P, P, P]),
+        "mok_ffn_forward": (i32, [i32, i32, i32, P, sz, P, P, P, P, P, P, P]),
+        "mok_ffn_backward": (i32, [i32, i32, i32, P, sz, P, P, P, P, P, P, P, P, P, P, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -489,3 +495,34 @@ def mok_residual_backward(r, x, y, dxo, dn, dx, dy, dw_out, dgate, dw_next, ws, 
     _ok(LIB.mok_residual_backward(r, *_rows(x), *_rows(y), *_rows(dxo), *_rows(dn), *_rows(dx), *_rows(dy),
                                   _ptr(dw_out), _ptr(dgate), _ptr(dw_next), ws.data_ptr(), ws.nbytes, _stream(stream)),
         "mok_residual_backward")
+
+
+# ---------------------------------------------------------------- dense feed-forward block
+MOK_FFN_MAX_SIZE = 131072
+
+
+def mok_ffn_workspace_size(T, H, I, training):
+    return LIB.mok_ffn_workspace_size(T, H, I, int(training))
+
+
+def mok_ffn_ctx_size(T, I):
+    return LIB.mok_ffn_ctx_size(T, I)
+
+
+def mok_ffn_infer(ws, x, W1, W3, W2, out, stream=None):
+    (T, H), I = x.shape, W2.shape[0]
+    _ok(LIB.mok_ffn_infer(T, H, I, ws.data_ptr(), ws.nbytes, _ptr(x), _ptr(W1), _ptr(W3), _ptr(W2), _ptr(out),
+                          _stream(stream)), "mok_ffn_infer")
+
+
+def mok_ffn_forward(ws, x, W1, W3, W2, out, ctx, stream=None):
+    (T, H), I = x.shape, W2.shape[0]
+    _ok(LIB.mok_ffn_forward(T, H, I, ws.data_ptr(), ws.nbytes, _ptr(x), _ptr(W1), _ptr(W3), _ptr(W2), _ptr(out),
+                            _ptr(ctx), _stream(stream)), "mok_ffn_forward")
+
+
+def mok_ffn_backward(ws, ctx, x, W1, W3, W2, dout, dX, dW1, dW3, dW2, stream=None):
+    (T, H), I = x.shape, W2.shape[0]
+    _ok(LIB.mok_ffn_backward(T, H, I, ws.data_ptr(), ws.nbytes, _ptr(ctx), _ptr(x), _ptr(W1), _ptr(W3), _ptr(W2),
+                             _ptr(dout), _ptr(dX), _ptr(dW1), _ptr(dW3), _ptr(dW2), _stream(stream)),
+        "mok_ffn_backward")

@@ -15,6 +15,7 @@
 #include "distill.cuh"
 #include "embed.cuh"
 #include "few.cuh"
+#include "ffn.cuh"
 #include "gemm.cuh"
 #include "residual.cuh"
 
@@ -2009,6 +2010,168 @@ mok_status mok_residual_backward(const mok_residual* r, const void* x, int64_t l
   const cudaError_t e = launch_residual_backward(S, B, p, &launches, st);
   g_launches += launches;
   return e == cudaSuccess ? MOK_OK : MOK_ERR_CUDA;
+}
+
+// ---------------------------------------------------------------- dense feed-forward block
+namespace {
+
+mok_status check_ffn(int32_t T, int32_t H, int32_t I) {
+  if (T < 0 || H < 1 || I < 1) return MOK_ERR_INVALID_ARG;
+  return H % 8 || I % 8 || H > MOK_FFN_MAX_SIZE || I > MOK_FFN_MAX_SIZE || T > (1 << 22) ? MOK_ERR_UNSUPPORTED : MOK_OK;
+}
+
+// Whether the few-token kernel takes such weights, as one expert's.
+bool ffn_few_sizes(int32_t H, int32_t I) {
+  return H % 128 == 0 && I % 128 == 0 && H <= MOK_FEW_MAX_HIDDEN && I <= MOK_FEW_MAX_HIDDEN;
+}
+
+// The few-token call's share of the workspace comes first: its counters, zero between calls, are at the same
+// place for every T.  Then a (infer) or dh and du (backward).
+struct FfnLayout {
+  size_t a, dh, du, total;
+};
+FfnLayout ffn_layout(int32_t T, int32_t H, int32_t I, bool training) {
+  FfnLayout L;
+  size_t off = kHeaderWords * 4;
+  if (ffn_few_sizes(H, I)) {
+    const mok_shape s = {std::min(std::max(T, 1), (int32_t)MOK_FEW_MAX_TOKENS), H, I, 1, 1};
+    off = few_layout(s, MOK_BF16).total;
+  }
+  const size_t n = align256((size_t)T * I * 2);
+  L.a = L.dh = off;
+  L.du = off + n;
+  L.total = off + (training ? 2 : 1) * n;
+  return L;
+}
+
+FfnParams ffn_params(void* ws, int M, int N, int K) {
+  FfnParams p;
+  memset(&p, 0, sizeof(p));
+  p.M = M;
+  p.N = N;
+  p.K = K;
+  p.hdr = static_cast<int32_t*>(ws);
+  return p;
+}
+
+// What a call's matrices are checked for: inputs and outputs whose bytes may not meet.
+struct Span {
+  const void* p;
+  size_t bytes;
+  bool written;
+};
+mok_status check_spans(std::initializer_list<Span> spans) {
+  for (const Span& s : spans)
+    if (!s.p || !aligned16(s.p)) return MOK_ERR_INVALID_ARG;
+  for (const Span& a : spans)
+    for (const Span& b : spans) {
+      if (&a == &b || !a.written) continue;
+      const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+      if (x < y + b.bytes && y < x + a.bytes) return MOK_ERR_INVALID_ARG;
+    }
+  return MOK_OK;
+}
+
+mok_status ffn_forward(int32_t T, int32_t H, int32_t I, void* ws, const void* x, const void* W1, const void* W3,
+                       const void* W2, void* out, __nv_bfloat16* a, __nv_bfloat16* h, __nv_bfloat16* u, void* stream) {
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  Phase ph(MOK_PHASE_FFN_FWD, st, 2);
+  FfnParams p = ffn_params(ws, T, I, H);
+  p.out[0] = a;
+  p.out[1] = h;
+  p.out[2] = u;
+  MOK_CUDA(launch_ffn(FFN_GATE, {{x, T, H}, {}}, {{W1, H, I}, {W3, H, I}}, p, st));
+  p = ffn_params(ws, T, H, I);
+  p.out[0] = static_cast<__nv_bfloat16*>(out);
+  MOK_CUDA(launch_ffn(FFN_OUT, {{a, T, I}, {}}, {{W2, I, H}, {}}, p, st));
+  return MOK_OK;
+}
+
+}  // namespace
+
+size_t mok_ffn_workspace_size(int32_t T, int32_t H, int32_t I, int32_t training) {
+  return check_ffn(T, H, I) == MOK_OK ? ffn_layout(T, H, I, training != 0).total : 0;
+}
+
+size_t mok_ffn_ctx_size(int32_t T, int32_t I) {
+  return check_ffn(T, 8, I) == MOK_OK ? std::max<size_t>(256, 3 * align256((size_t)T * I * 2)) : 0;
+}
+
+mok_status mok_ffn_infer(int32_t T, int32_t H, int32_t I, void* ws, size_t ws_bytes, const void* x, const void* W1,
+                         const void* W3, const void* W2, void* out, void* stream) {
+  MOK_TRY(check_ffn(T, H, I));
+  if (T == 0) return MOK_OK;
+  const FfnLayout L = ffn_layout(T, H, I, false);
+  const size_t rows = (size_t)T * H * 2, w = (size_t)H * I * 2;
+  MOK_TRY(check_spans({{x, rows}, {W1, w}, {W3, w}, {W2, w}, {out, rows, true}, {ws, L.total, true}}));
+  if (ws_bytes < L.total) return MOK_ERR_WORKSPACE_TOO_SMALL;
+  if (T <= MOK_FEW_MAX_TOKENS && ffn_few_sizes(H, I)) {
+    const mok_shape s = {T, H, I, 1, 1};
+    FewParams p;
+    MOK_TRY(few_params(s, MOK_BF16, ws, ws_bytes, x, W1, W3, W2, out, &p));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    Phase ph(MOK_PHASE_FFN_FWD, st, 0);
+    int launches = 0;
+    const cudaError_t e = launch_few(p, false, &launches, st);
+    g_launches += launches;
+    return e == cudaSuccess ? MOK_OK : MOK_ERR_CUDA;
+  }
+  return ffn_forward(T, H, I, ws, x, W1, W3, W2, out, reinterpret_cast<__nv_bfloat16*>(static_cast<uint8_t*>(ws) + L.a),
+                     nullptr, nullptr, stream);
+}
+
+mok_status mok_ffn_forward(int32_t T, int32_t H, int32_t I, void* ws, size_t ws_bytes, const void* x, const void* W1,
+                           const void* W3, const void* W2, void* out, void* ctx, void* stream) {
+  MOK_TRY(check_ffn(T, H, I));
+  if (T == 0) return MOK_OK;
+  const FfnLayout L = ffn_layout(T, H, I, true);
+  const size_t rows = (size_t)T * H * 2, w = (size_t)H * I * 2;
+  MOK_TRY(check_spans({{x, rows}, {W1, w}, {W3, w}, {W2, w}, {out, rows, true}, {ctx, mok_ffn_ctx_size(T, I), true},
+                       {ws, L.total, true}}));
+  if (ws_bytes < L.total) return MOK_ERR_WORKSPACE_TOO_SMALL;
+  const size_t n = align256((size_t)T * I * 2);
+  uint8_t* c = static_cast<uint8_t*>(ctx);
+  return ffn_forward(T, H, I, ws, x, W1, W3, W2, out, reinterpret_cast<__nv_bfloat16*>(c + 2 * n),
+                     reinterpret_cast<__nv_bfloat16*>(c), reinterpret_cast<__nv_bfloat16*>(c + n), stream);
+}
+
+mok_status mok_ffn_backward(int32_t T, int32_t H, int32_t I, void* ws, size_t ws_bytes, const void* ctx, const void* x,
+                            const void* W1, const void* W3, const void* W2, const void* dout, void* dX, void* dW1,
+                            void* dW3, void* dW2, void* stream) {
+  MOK_TRY(check_ffn(T, H, I));
+  const FfnLayout L = ffn_layout(T, H, I, true);
+  const size_t rows = (size_t)T * H * 2, w = (size_t)H * I * 2;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (T == 0) {
+    MOK_TRY(check_spans({{dW1, w, true}, {dW3, w, true}, {dW2, w, true}}));
+    for (void* d : {dW1, dW3, dW2}) MOK_CUDA(cudaMemsetAsync(d, 0, w, st));
+    return MOK_OK;
+  }
+  MOK_TRY(check_spans({{ctx, mok_ffn_ctx_size(T, I)}, {x, rows}, {W1, w}, {W3, w}, {W2, w}, {dout, rows}, {dX, rows, true},
+                       {dW1, w, true}, {dW3, w, true}, {dW2, w, true}, {ws, L.total, true}}));
+  if (ws_bytes < L.total) return MOK_ERR_WORKSPACE_TOO_SMALL;
+  const size_t n = align256((size_t)T * I * 2);
+  const uint8_t* c = static_cast<const uint8_t*>(ctx);
+  uint8_t* s = static_cast<uint8_t*>(ws);
+  const void* a = c + 2 * n;
+  Phase ph(MOK_PHASE_FFN_BWD, st, 4);
+  FfnParams p = ffn_params(ws, T, I, H);
+  p.h = reinterpret_cast<const __nv_bfloat16*>(c);
+  p.u = reinterpret_cast<const __nv_bfloat16*>(c + n);
+  p.out[0] = reinterpret_cast<__nv_bfloat16*>(s + L.dh);
+  p.out[1] = reinterpret_cast<__nv_bfloat16*>(s + L.du);
+  MOK_CUDA(launch_ffn(FFN_DA, {{dout, T, H}, {}}, {{W2, I, H}, {}}, p, st));
+  p = ffn_params(ws, I, H, T);
+  p.out[0] = static_cast<__nv_bfloat16*>(dW2);
+  MOK_CUDA(launch_ffn(FFN_DW2, {{a, T, I}, {}}, {{dout, T, H}, {}}, p, st));
+  p = ffn_params(ws, T, H, I);
+  p.out[0] = static_cast<__nv_bfloat16*>(dX);
+  MOK_CUDA(launch_ffn(FFN_DX, {{s + L.dh, T, I}, {s + L.du, T, I}}, {{W1, H, I}, {W3, H, I}}, p, st));
+  p = ffn_params(ws, H, I, T);
+  p.out[0] = static_cast<__nv_bfloat16*>(dW1);
+  p.out[1] = static_cast<__nv_bfloat16*>(dW3);
+  MOK_CUDA(launch_ffn(FFN_DW13, {{x, T, H}, {}}, {{s + L.dh, T, I}, {s + L.du, T, I}}, p, st));
+  return MOK_OK;
 }
 
 mok_status mok_check(void* ws, void* stream) {

@@ -1,0 +1,462 @@
+// The matrix products of the dense gated feed-forward block,
+//
+//   h = x W1,  u = x W3,  a = silu(h) * u,  out = a W2
+//
+// and of its gradients,
+//
+//   da = dout W2^T,  dh = da u sig(h) (1 + h (1 - sig(h))),  du = da silu(h)
+//   dx = dh W1^T + du W3^T,  dW1 = x^T dh,  dW3 = x^T du,  dW2 = a^T dout
+//
+// one persistent kernel for all of them, bound by the tensor cores: a cluster
+// of two CTAs shares a 256 x 256 tile of the result through one
+// tcgen05.mma.cta_group::2 (each CTA brings its 128 rows of A and half of B:
+// 32 KB a step of 64 along K, six steps in flight), FP32 sums in TMEM, two
+// accumulators so that the epilogue of a tile runs beside the next one's
+// products.  Operands are read as they lie in memory, either way round, by
+// TMA, which also fills in zeros past their ends: no size has to be a multiple
+// of a tile, only rows of whole 16 bytes are asked for.  Tiles are handed out
+// by their number, and every sum runs along K in one order: results do not
+// depend on timing.
+//
+//   warp 0      TMA (both CTAs)
+//   warp 1      TMEM allocation; the leader's issues the MMAs
+//   warps 2-9   epilogue: two warps for each quarter of the accumulator's rows,
+//               half of the columns each
+#include <string.h>
+
+#include <algorithm>
+#include <atomic>
+
+#include "ffn.cuh"
+#include "tc.cuh"
+
+namespace mok {
+
+namespace {
+
+constexpr int kFfnStages = 6;
+constexpr int kFfnOperandBytes = 128 * 128;               // A's or B's share of a CTA and stage
+constexpr int kFfnStageBytes = 2 * kFfnOperandBytes;
+constexpr int kFfnEpilogueWarps = 8;
+constexpr int kFfnThreads = 64 + 32 * kFfnEpilogueWarps;
+constexpr int kFfnOutStage = 32 * 64 * 2;                 // an epilogue warp's 32 x 64 bf16 on their way out
+// M tiles (of 256 rows) taken together: their A and the B of the tiles beside them stay in L2
+constexpr int kFfnGroup = 8;
+constexpr uint64_t kFfnDrainNs = 20000000ull;             // 20 ms
+
+struct FfnMaps {
+  CUtensorMap a[2], b[2];
+};
+
+struct FfnCtl {
+  uint64_t full[kFfnStages];
+  uint64_t empty[kFfnStages];
+  uint64_t tfull[2];
+  uint64_t tempty[2];
+  uint32_t tmem_base;
+  int abort;
+};
+
+constexpr size_t kFfnSmem =
+    1024 + kFfnStages * kFfnStageBytes + kFfnEpilogueWarps * kFfnOutStage + (sizeof(FfnCtl) + 127) / 128 * 128;
+static_assert(kFfnSmem <= 227 * 1024, "shared memory of an SM");
+
+// Whether an operand's rows run along M or N (and not along K).
+__host__ __device__ constexpr bool ffn_a_mn(int mode) { return mode == FFN_DW13 || mode == FFN_DW2; }
+__host__ __device__ constexpr bool ffn_b_mn(int mode) { return mode != FFN_DA && mode != FFN_DX; }
+
+// Columns of the result that a tile covers (FFN_GATE: 128 of h and the same of u).
+__host__ __device__ constexpr int ffn_tile_n(int mode) { return mode == FFN_GATE ? 128 : 256; }
+
+__host__ __device__ inline int ceil_div(int a, int b) { return (a + b - 1) / b; }
+
+template <int MODE>
+__device__ __forceinline__ int n_tiles(const FfnParams& p) {
+  const int n = ceil_div(p.N, ffn_tile_n(MODE));
+  return MODE == FFN_DW13 ? 2 * n : n;
+}
+
+struct FfnTile {
+  int m, n;    // tile's place: rows m * 256.., columns n * tile_n..
+  int which;   // FFN_DW13: 0 dW1, 1 dW3
+};
+
+// Tiles in groups of kFfnGroup along M, along M first within a group.
+template <int MODE>
+__device__ __forceinline__ FfnTile tile_of(const FfnParams& p, int item) {
+  const int mt = ceil_div(p.M, 256), nt = n_tiles<MODE>(p);
+  const int group = item / (kFfnGroup * nt), rest = item - group * kFfnGroup * nt;
+  const int rows = min(kFfnGroup, mt - group * kFfnGroup);
+  FfnTile t;
+  t.m = group * kFfnGroup + rest % rows;
+  t.n = rest / rows;
+  t.which = 0;
+  if (MODE == FFN_DW13) {
+    const int half = nt / 2;
+    t.which = t.n >= half;
+    t.n -= t.which * half;
+  }
+  return t;
+}
+
+// This CTA's operands of one step along K.
+template <int MODE>
+__device__ __forceinline__ void ffn_loads(const FfnMaps& mp, const FfnTile& t, int kk, int k_half, int rank, uint8_t* a,
+                                          uint8_t* b, uint32_t bar) {
+  const int row = t.m * 256 + rank * 128;
+  const int second = MODE == FFN_DX && kk >= k_half ? 1 : 0;
+  const int k = (kk - second * k_half) * 64;
+  if constexpr (ffn_a_mn(MODE)) {
+    for (int c = 0; c < 2; ++c) tma_load_2d_pair(a + c * 8192, &mp.a[0], bar, row + c * 64, k);
+  } else {
+    tma_load_2d_pair(a, &mp.a[second], bar, k, row);
+  }
+  if constexpr (MODE == FFN_GATE) {
+    // the leader's half of B are columns of W1, the other's the same columns of W3
+    for (int c = 0; c < 2; ++c) tma_load_2d_pair(b + c * 8192, &mp.b[rank], bar, t.n * 128 + c * 64, k);
+  } else {
+    const int col = t.n * 256 + rank * 128;
+    const CUtensorMap* m = &mp.b[MODE == FFN_DW13 ? t.which : second];
+    if constexpr (ffn_b_mn(MODE)) {
+      for (int c = 0; c < 2; ++c) tma_load_2d_pair(b + c * 8192, m, bar, col + c * 64, k);
+    } else {
+      tma_load_2d_pair(b, m, bar, k, col);
+    }
+  }
+}
+
+// ------------------------------------------------------------------ epilogue
+__device__ __forceinline__ float ffn_sigmoid(float h) { return 1.0f / (1.0f + __expf(-h)); }
+
+// 32 rows x 64 columns of bf16, a row of it a lane's 32 words, to row0.. and col0.. of
+// dst [rows, ld], whole 128-byte segments at a time through the warp's staging buffer
+// (16-byte pieces swizzled by row).  ld is a multiple of eight: a piece lies inside or outside.
+__device__ __forceinline__ void store_block(uint8_t* stage, int lane, const uint32_t (&w)[32], __nv_bfloat16* dst,
+                                            int row0, int rows, int col0, int ld) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    *reinterpret_cast<uint4*>(stage + lane * 128 + ((i ^ (lane & 7)) << 4)) =
+        make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+  __syncwarp();
+  const int ch = lane & 7, col = col0 + ch * 8;
+#pragma unroll
+  for (int s = 0; s < 8; ++s) {
+    const int r = 4 * s + (lane >> 3);
+    const uint4 v = *reinterpret_cast<const uint4*>(stage + r * 128 + ((ch ^ (r & 7)) << 4));
+    if (row0 + r < rows && col < ld) *reinterpret_cast<uint4*>(dst + (long)(row0 + r) * ld + col) = v;
+  }
+  __syncwarp();
+}
+
+// The reverse, in two halves: the loads (zeros outside), and the words of the lane's row.
+__device__ __forceinline__ void load_block(uint4 (&v)[8], int lane, const __nv_bfloat16* src, int row0, int rows, int col0,
+                                           int ld) {
+  const int ch = lane & 7, col = col0 + ch * 8;
+#pragma unroll
+  for (int s = 0; s < 8; ++s) {
+    const int r = 4 * s + (lane >> 3);
+    v[s] = row0 + r < rows && col < ld ? *reinterpret_cast<const uint4*>(src + (long)(row0 + r) * ld + col)
+                                       : make_uint4(0, 0, 0, 0);
+  }
+}
+__device__ __forceinline__ void turn_block(uint8_t* stage, int lane, const uint4 (&v)[8], uint32_t (&w)[32]) {
+  const int ch = lane & 7;
+#pragma unroll
+  for (int s = 0; s < 8; ++s) {
+    const int r = 4 * s + (lane >> 3);
+    *reinterpret_cast<uint4*>(stage + r * 128 + ((ch ^ (r & 7)) << 4)) = v[s];
+  }
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint4 t = *reinterpret_cast<const uint4*>(stage + lane * 128 + ((i ^ (lane & 7)) << 4));
+    w[4 * i] = t.x, w[4 * i + 1] = t.y, w[4 * i + 2] = t.z, w[4 * i + 3] = t.w;
+  }
+  __syncwarp();
+}
+
+__device__ __forceinline__ float lo_f32(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi_f32(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+// The 32 rows from row0 and this warp's half of a tile's columns.  `acc`: the accumulator's
+// address for these rows; `ready` waits for it.
+template <int MODE, typename Ready>
+__device__ __forceinline__ bool ffn_epilogue(const FfnParams& p, const FfnTile& t, uint32_t acc, int row0, int half,
+                                             int lane, uint8_t* stage, Ready&& ready) {
+  if constexpr (MODE == FFN_GATE) {
+    if (!ready()) return false;
+    const int col = t.n * 128 + half * 64;
+    uint32_t aw[32], hw[32], uw[32];
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      uint32_t h[32], u[32];
+      tmem_ld32_issue(acc + half * 64 + c * 32, h);
+      tmem_ld32_issue(acc + 128 + half * 64 + c * 32, u);
+      tmem_wait_ld();
+      tmem_regs_ready(h);
+      tmem_regs_ready(u);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float h0 = __uint_as_float(h[2 * i]), h1 = __uint_as_float(h[2 * i + 1]);
+        const float u0 = __uint_as_float(u[2 * i]), u1 = __uint_as_float(u[2 * i + 1]);
+        aw[16 * c + i] = pack_bf16x2(h0 * ffn_sigmoid(h0) * u0, h1 * ffn_sigmoid(h1) * u1);
+        hw[16 * c + i] = pack_bf16x2(h0, h1);
+        uw[16 * c + i] = pack_bf16x2(u0, u1);
+      }
+    }
+    store_block(stage, lane, aw, p.out[0], row0, p.M, col, p.N);
+    if (p.out[1]) {
+      store_block(stage, lane, hw, p.out[1], row0, p.M, col, p.N);
+      store_block(stage, lane, uw, p.out[2], row0, p.M, col, p.N);
+    }
+  } else {
+    uint4 hv[8], uv[8];
+    if constexpr (MODE == FFN_DA) {
+      // (on their way while the products still run)
+      load_block(hv, lane, p.h, row0, p.M, t.n * 256 + half * 128, p.N);
+      load_block(uv, lane, p.u, row0, p.M, t.n * 256 + half * 128, p.N);
+    }
+    if (!ready()) return false;
+#pragma unroll 1
+    for (int g = 0; g < 2; ++g) {
+      const int col = t.n * 256 + half * 128 + g * 64;
+      uint32_t ra[32], rb[32], w[32];
+      tmem_ld32_issue(acc + half * 128 + g * 64, ra);
+      tmem_ld32_issue(acc + half * 128 + g * 64 + 32, rb);
+      if constexpr (MODE == FFN_DA) {
+        uint32_t h[32], u[32];
+        turn_block(stage, lane, hv, h);
+        turn_block(stage, lane, uv, u);
+        if (g == 0) {
+          load_block(hv, lane, p.h, row0, p.M, col + 64, p.N);
+          load_block(uv, lane, p.u, row0, p.M, col + 64, p.N);
+        }
+        tmem_wait_ld();
+        tmem_regs_ready(ra);
+        tmem_regs_ready(rb);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          float dh[2], du[2];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const float da = __uint_as_float(i < 16 ? ra[2 * i + j] : rb[2 * (i - 16) + j]);
+            const float hh = j ? hi_f32(h[i]) : lo_f32(h[i]), uu = j ? hi_f32(u[i]) : lo_f32(u[i]);
+            const float sg = ffn_sigmoid(hh);
+            dh[j] = da * uu * sg * (1.0f + hh * (1.0f - sg));
+            du[j] = da * (hh * sg);
+          }
+          w[i] = pack_bf16x2(dh[0], dh[1]);
+          u[i] = pack_bf16x2(du[0], du[1]);
+        }
+        store_block(stage, lane, w, p.out[0], row0, p.M, col, p.N);
+        store_block(stage, lane, u, p.out[1], row0, p.M, col, p.N);
+      } else {
+        tmem_wait_ld();
+        tmem_regs_ready(ra);
+        tmem_regs_ready(rb);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          w[i] = pack_bf16x2(__uint_as_float(ra[2 * i]), __uint_as_float(ra[2 * i + 1]));
+          w[16 + i] = pack_bf16x2(__uint_as_float(rb[2 * i]), __uint_as_float(rb[2 * i + 1]));
+        }
+        store_block(stage, lane, w, MODE == FFN_DW13 && t.which ? p.out[1] : p.out[0], row0, p.M, col, p.N);
+      }
+    }
+  }
+  return true;
+}
+
+// ------------------------------------------------------------------ kernel
+template <int MODE>
+__global__ void __launch_bounds__(kFfnThreads, 1) ffn_kernel(const __grid_constant__ FfnMaps maps, const FfnParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sA = base;
+  uint8_t* sB = sA + kFfnStages * kFfnOperandBytes;
+  uint8_t* sOut = sB + kFfnStages * kFfnOperandBytes;
+  FfnCtl* ctl = reinterpret_cast<FfnCtl*>(sOut + kFfnEpilogueWarps * kFfnOutStage);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const WaitCtx wc{&ctl->abort, &p.hdr[kHdrAbort], &p.hdr[kHdrError]};
+  const int rank = (int)cluster_ctarank();
+  const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
+  const int items = ceil_div(p.M, 256) * n_tiles<MODE>(p);
+  const int k_half = ceil_div(p.K, 64), k_iters = MODE == FFN_DX ? 2 * k_half : k_half;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kFfnStages; ++i) {
+      mbar_init(&ctl->full[i], 1);
+      mbar_init(&ctl->empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&ctl->tfull[i], 1);
+      mbar_init(&ctl->tempty[i], 2 * kFfnEpilogueWarps);
+    }
+    ctl->abort = 0;
+    ctl->tmem_base = 0;
+    fence_mbar_init();
+    // a call that timed out left the abort word set: this one's results cannot be trusted either
+    if (blockIdx.x == 0 && *reinterpret_cast<volatile int*>(&p.hdr[kHdrAbort])) atomicOr(&p.hdr[kHdrError], MOK_ERRBIT_TIMEOUT);
+  }
+  if (warp == 0 && lane < 2) {
+    tma_prefetch_desc(&maps.a[lane]);
+    tma_prefetch_desc(&maps.b[lane]);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(&ctl->tmem_base, 512);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // both CTAs' barriers stand before either signals the other's
+  tc_fence_after();
+  const uint32_t tmem = ctl->tmem_base;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      uint32_t stage = 0, phase = 0;
+      bool ok = true;
+      for (int item = first; ok && item < items; item += step) {
+        const FfnTile t = tile_of<MODE>(p, item);
+        for (int kk = 0; kk < k_iters; ++kk) {
+          if (!mbar_wait(&ctl->empty[stage], phase ^ 1, wc)) { ok = false; break; }
+          // (the leader's barrier counts both CTAs' bytes)
+          if (rank == 0) mbar_arrive_expect_tx(&ctl->full[stage], 2 * kFfnStageBytes);
+          ffn_loads<MODE>(maps, t, kk, k_half, rank, sA + stage * kFfnOperandBytes, sB + stage * kFfnOperandBytes,
+                          mapa_shared(&ctl->full[stage], 0));
+          if (++stage == kFfnStages) { stage = 0; phase ^= 1; }
+        }
+      }
+      // no copy may be in flight, nor an MMA read these stages, when the CTA leaves: each stage's last
+      // fill is released by the MMAs that read it (after a timeout for a limited time)
+      const uint64_t t0 = globaltimer();
+      for (int j = 0; j < kFfnStages; ++j) {
+        const uint64_t spent = globaltimer() - t0;
+        if (spent < kFfnDrainNs) mbar_drain(&ctl->empty[stage], phase ^ 1, kFfnDrainNs - spent);
+        if (++stage == kFfnStages) { stage = 0; phase ^= 1; }
+      }
+    }
+  } else if (warp == 1) {
+    uint32_t stage = 0, phase = 0, tcount = 0;
+    constexpr uint32_t idesc = idesc_bf16(256, 256, ffn_a_mn(MODE) ? 1 : 0, ffn_b_mn(MODE) ? 1 : 0);
+    bool ok = rank == 0;
+    for (int item = first; ok && item < items; item += step, ++tcount) {
+      const uint32_t buf = tcount & 1, tph = (tcount >> 1) & 1;
+      if (!mbar_wait_cluster(&ctl->tempty[buf], tph ^ 1, wc)) break;
+      tc_fence_after();
+      const uint32_t d = tmem + buf * 256;
+      for (int kk = 0; kk < k_iters; ++kk) {
+        if (!mbar_wait(&ctl->full[stage], phase, wc)) { ok = false; break; }
+        tc_fence_after();
+        if (lane == 0) {
+          const uint32_t a0 = smem_u32(sA + stage * kFfnOperandBytes), b0 = smem_u32(sB + stage * kFfnOperandBytes);
+#pragma unroll
+          for (int k16 = 0; k16 < 4; ++k16) {
+            const uint64_t ad = ffn_a_mn(MODE) ? sdesc_sw128(a0 + k16 * 2048, 8192, 1024) : sdesc_sw128(a0 + k16 * 32, 16, 1024);
+            const uint64_t bd = ffn_b_mn(MODE) ? sdesc_sw128(b0 + k16 * 2048, 8192, 1024) : sdesc_sw128(b0 + k16 * 32, 16, 1024);
+            mma_bf16_pair(d, ad, bd, idesc, (kk | k16) != 0 ? 1u : 0u);
+          }
+          mma_commit_pair(&ctl->empty[stage]);
+        }
+        __syncwarp();
+        if (++stage == kFfnStages) { stage = 0; phase ^= 1; }
+      }
+      if (!ok) break;
+      if (lane == 0) mma_commit_pair(&ctl->tfull[buf]);
+      __syncwarp();
+    }
+  } else {
+    const int q = warp & 3, half = (warp - 2) >> 2;  // TMEM lanes that this warp may read; columns it takes
+    uint8_t* stage_out = sOut + (warp - 2) * kFfnOutStage;
+    uint32_t tcount = 0;
+    for (int item = first; item < items; item += step, ++tcount) {
+      const FfnTile t = tile_of<MODE>(p, item);
+      const uint32_t buf = tcount & 1, tph = (tcount >> 1) & 1;
+      auto ready = [&]() {
+        if (!mbar_wait(&ctl->tfull[buf], tph, wc)) return false;
+        tc_fence_after();
+        return true;
+      };
+      if (!ffn_epilogue<MODE>(p, t, tmem + ((uint32_t)(q * 32) << 16) + buf * 256, t.m * 256 + rank * 128 + q * 32, half,
+                              lane, stage_out, ready))
+        break;
+      tc_fence_before();
+      __syncwarp();
+      // (the leader's MMA warp waits for both CTAs' epilogues)
+      if (lane == 0) mbar_arrive_cluster(mapa_shared(&ctl->tempty[buf], 0));
+    }
+  }
+
+  tc_fence_before();
+  // (the non-aligned barrier form, defined for warps that arrive diverged)
+  asm volatile("barrier.sync 0;" ::: "memory");
+  // neither CTA leaves (nor frees TMEM) while the other may still signal its barriers or run MMAs on its memory
+  cluster_sync();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc_pair(tmem, 512);
+}
+
+// ------------------------------------------------------------------ launches
+// Rows along K: boxes of 128 rows x 64 of K; along M or N: 64 of K x 64.
+bool operand_map(CUtensorMap* m, const FfnOperand& o, bool mn) {
+  const uint64_t dims[2] = {(uint64_t)o.cols, (uint64_t)o.rows};
+  const uint64_t str[1] = {(uint64_t)o.cols * 2};
+  const uint32_t box[2] = {64, mn ? 64u : 128u};
+  return make_tmap(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, o.p, dims, str, box, true);
+}
+
+template <int MODE>
+cudaError_t launch_mode(const FfnMaps& maps, const FfnParams& p, cudaStream_t st) {
+  static std::atomic<uint64_t> allowed{0};
+  cudaError_t e = allow_smem((const void*)ffn_kernel<MODE>, kFfnSmem, allowed);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.gridDim = dim3((unsigned)device_sm_count() & ~1u);
+  cfg.blockDim = dim3(kFfnThreads);
+  cfg.dynamicSmemBytes = kFfnSmem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  // clusters that the device holds at once, asked for once per device
+  static std::atomic<int> held[64];
+  int dev = 0;
+  e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  int clusters = dev < 64 ? held[dev].load(std::memory_order_relaxed) : 0;
+  if (clusters == 0) {
+    e = cudaOccupancyMaxActiveClusters(&clusters, ffn_kernel<MODE>, &cfg);
+    if (e != cudaSuccess) return e;
+    if (clusters < 1) return cudaErrorNotSupported;
+    if (dev < 64) held[dev].store(clusters, std::memory_order_relaxed);
+  }
+  const int n = ceil_div(p.N, ffn_tile_n(MODE)) * (MODE == FFN_DW13 ? 2 : 1);
+  cfg.gridDim = dim3(2u * (unsigned)std::min<long>((long)ceil_div(p.M, 256) * n, clusters));
+  return cudaLaunchKernelEx(&cfg, ffn_kernel<MODE>, maps, p);
+}
+
+}  // namespace
+
+cudaError_t launch_ffn(FfnMode mode, const FfnOperand (&a)[2], const FfnOperand (&b)[2], const FfnParams& p,
+                       cudaStream_t st) {
+  FfnMaps maps;
+  memset(&maps, 0, sizeof(maps));
+  for (int i = 0; i < 2; ++i) {
+    if (!operand_map(&maps.a[i], a[i].p ? a[i] : a[0], ffn_a_mn(mode))) return cudaErrorInvalidValue;
+    if (!operand_map(&maps.b[i], b[i].p ? b[i] : b[0], ffn_b_mn(mode))) return cudaErrorInvalidValue;
+  }
+  switch (mode) {
+    case FFN_GATE: return launch_mode<FFN_GATE>(maps, p, st);
+    case FFN_OUT: return launch_mode<FFN_OUT>(maps, p, st);
+    case FFN_DA: return launch_mode<FFN_DA>(maps, p, st);
+    case FFN_DX: return launch_mode<FFN_DX>(maps, p, st);
+    case FFN_DW13: return launch_mode<FFN_DW13>(maps, p, st);
+    case FFN_DW2: return launch_mode<FFN_DW2>(maps, p, st);
+  }
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace mok

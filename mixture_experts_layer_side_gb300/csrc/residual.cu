@@ -33,8 +33,6 @@ __device__ __forceinline__ int column(int g, int e, int t, int nt) {
   return VEC ? (g * nt + t) * 8 + e : (g * 8 + e) * nt + t;
 }
 
-__device__ __forceinline__ float to_f32(float v) { return v; }
-__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
 template <typename E>
 __device__ __forceinline__ E from_f32(float v);
 template <>
@@ -60,7 +58,7 @@ __device__ __forceinline__ void load8(const __nv_bfloat16* row, int g, int t, in
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const int c = column<false>(g, e, t, nt);
-      v[e] = c < H ? to_f32(row[c]) : 0.0f;
+      v[e] = c < H ? __bfloat162float(row[c]) : 0.0f;
     }
   }
 }
