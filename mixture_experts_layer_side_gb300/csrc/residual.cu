@@ -18,91 +18,175 @@
 #include <algorithm>
 
 #include "residual.cuh"
+#include "rows.cuh"
 
 namespace mok {
 
 namespace {
 
-// ------------------------------------------------------------------ rows in registers
-// A row belongs to a team of NT threads (a warp, or a whole CTA), 8 NG
-// elements each.  VEC: thread t holds the eight elements from (g NT + t) 8,
-// loaded as vectors; otherwise the elements (8 g + e) NT + t, one by one, so
-// that neighbouring threads read neighbouring elements at any alignment.
-template <bool VEC>
-__device__ __forceinline__ int column(int g, int e, int t, int nt) {
-  return VEC ? (g * nt + t) * 8 + e : (g * 8 + e) * nt + t;
+// ------------------------------------------------------------------ pairs
+// Two f32 in a register pair: one instruction multiplies or adds both.  What
+// bounds these kernels beside HBM is the number of instructions an element,
+// and half of an unpacked one's are such.
+typedef unsigned long long f2;
+
+__device__ __forceinline__ f2 pair(float a, float b) {
+  f2 v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b));
+  return v;
 }
+__device__ __forceinline__ f2 both(float a) { return pair(a, a); }
+__device__ __forceinline__ void split(f2 v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ float lo(f2 v) {
+  float a, b;
+  split(v, a, b);
+  return a;
+}
+__device__ __forceinline__ float hi(f2 v) {
+  float a, b;
+  split(v, a, b);
+  return b;
+}
+__device__ __forceinline__ float sum(f2 v) { return lo(v) + hi(v); }
+__device__ __forceinline__ f2 mul(f2 a, f2 b) {
+  f2 v;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
+  return v;
+}
+__device__ __forceinline__ f2 fma(f2 a, f2 b, f2 c) {
+  f2 v;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(v) : "l"(a), "l"(b), "l"(c));
+  return v;
+}
+
+// ------------------------------------------------------------------ rows
+// A row belongs to a team of NT threads (a warp, or a whole CTA), 8 NG
+// elements each: thread t holds the eight from (g NT + t) 8 on.  ALIGNED: every row of
+// every tensor is made of whole 16-byte vectors.
+//
+// In the last group a thread may have fewer elements, or none: then it works
+// on the row's first ones beside their owner, and leaves them out of sums and
+// stores, so that no branch stands around a group.
+struct Place {
+  int t, nt;
+  int last;  // the first column of the thread's last group
+  int n;     // how many of its elements there are (0: none), and of the next lane's (0 past the warp)
+  int next;
+  int held;  // how many it works on
+};
+template <int NG>
+__device__ __forceinline__ Place place(int t, int nt, int H) {
+  const int c = ((NG - 1) * nt + t) * 8;
+  const int n = min(8, max(0, H - c)), next = (t & 31) < 31 ? min(8, max(0, H - c - 8)) : 0;
+  return Place{t, nt, n > 0 ? c : 0, n, next, n > 0 ? n : min(8, H)};
+}
+template <int NG>
+__device__ __forceinline__ int first_column(const Place& a, int g) {
+  return g == NG - 1 ? a.last : (g * a.nt + a.t) * 8;
+}
+template <int NG>
+__device__ __forceinline__ bool counts(const Place& a, int g) { return g < NG - 1 || a.n > 0; }
+
+__device__ __forceinline__ float to_f32(float v) { return v; }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <typename E>
+__device__ __forceinline__ E from_f32(float v) {
+  if constexpr (sizeof(E) == 4) return v;
+  else return __float2bfloat16_rn(v);
+}
+
+// Eight elements as four pairs.
+struct Eight {
+  f2 v[4];
+};
+__device__ __forceinline__ float squares(const Eight& a) {
+  f2 s = mul(a.v[0], a.v[0]);
+#pragma unroll
+  for (int i = 1; i < 4; ++i) s = fma(a.v[i], a.v[i], s);
+  return sum(s);
+}
+__device__ __forceinline__ Eight zeros() { return Eight{{0, 0, 0, 0}}; }
+__device__ __forceinline__ Eight ones() { return Eight{{both(1.0f), both(1.0f), both(1.0f), both(1.0f)}}; }
 
 template <typename E>
-__device__ __forceinline__ E from_f32(float v);
-template <>
-__device__ __forceinline__ float from_f32<float>(float v) { return v; }
-template <>
-__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
-
-__device__ __forceinline__ void unpack8(const uint4& w, float (&v)[8]) {
-  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+__device__ __forceinline__ Eight unpack(const uint32_t (&w)[words8<E>()]) {
+  Eight r;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(u[i] << 16);
-    v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+    if constexpr (sizeof(E) == 2) r.v[i] = pair(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+    else r.v[i] = pair(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
   }
+  return r;
 }
 
-template <bool VEC>
-__device__ __forceinline__ void load8(const __nv_bfloat16* row, int g, int t, int nt, int H, float (&v)[8]) {
-  if constexpr (VEC) {
-    const int c = column<true>(g, 0, t, nt);
-    unpack8(c < H ? *reinterpret_cast<const uint4*>(row + c) : make_uint4(0, 0, 0, 0), v);
-  } else {
+// A tensor of rows and where it ends (its ends matter where rows are not aligned).
+template <typename E>
+struct Rows {
+  E* p;
+  long ld;
+  Span8 span;
+  __device__ __forceinline__ E* operator[](long row) const { return p + row * ld; }
+};
+template <typename E>
+__device__ __forceinline__ Rows<const E> rows_in(const void* p, long ld, long rows, int H) {
+  const E* q = static_cast<const E*>(p);
+  return {q, ld, span_of(q, rows, ld, H)};
+}
+template <typename E>
+__device__ __forceinline__ Rows<E> rows_out(void* p, long ld) {
+  return {static_cast<E*>(p), ld, {0, 0}};
+}
+
+template <bool ALIGNED, int NG, typename E>
+__device__ __forceinline__ Eight load8(const E* row, const Span8& span, int g, const Place& a) {
+  uint32_t w[words8<E>()];
+  load_words<E, ALIGNED>(row + first_column<NG>(a, g), g < NG - 1 ? 8 : a.held, span, w);
+  return unpack<E>(w);
+}
+template <bool ALIGNED, int NG, typename E>
+__device__ __forceinline__ Eight load8(const Rows<const E>& r, long row, int g, const Place& a) {
+  return load8<ALIGNED, NG>(r[row], r.span, g, a);
+}
+template <bool ALIGNED, int NG, typename E>
+__device__ __forceinline__ void store8(E* row, int g, const Place& a, const Eight& v) {
+  float f[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int c = column<false>(g, e, t, nt);
-      v[e] = c < H ? __bfloat162float(row[c]) : 0.0f;
-    }
-  }
-}
-
-template <bool VEC>
-__device__ __forceinline__ void load8(const float* row, int g, int t, int nt, int H, float (&v)[8]) {
-  if constexpr (VEC) {
-    const int c = column<true>(g, 0, t, nt);
-    float4 a = make_float4(0, 0, 0, 0), b = a;
-    if (c < H) a = reinterpret_cast<const float4*>(row + c)[0], b = reinterpret_cast<const float4*>(row + c)[1];
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-  } else {
+  for (int i = 0; i < 4; ++i) split(v.v[i], f[2 * i], f[2 * i + 1]);
+  uint32_t w[words8<E>()];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int c = column<false>(g, e, t, nt);
-      v[e] = c < H ? row[c] : 0.0f;
-    }
-  }
-}
-
-template <bool VEC, typename E>
-__device__ __forceinline__ void store8(E* row, int g, int t, int nt, int H, const float (&v)[8]) {
-  if constexpr (VEC) {
-    const int c = column<true>(g, 0, t, nt);
-    if (c >= H) return;
+  for (int i = 0; i < words8<E>(); ++i) {
     if constexpr (sizeof(E) == 2) {
-      uint32_t u[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-        u[i] = *reinterpret_cast<const uint32_t*>(&b);
-      }
-      *reinterpret_cast<uint4*>(row + c) = make_uint4(u[0], u[1], u[2], u[3]);
+      const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&b);
     } else {
-      reinterpret_cast<float4*>(row + c)[0] = make_float4(v[0], v[1], v[2], v[3]);
-      reinterpret_cast<float4*>(row + c)[1] = make_float4(v[4], v[5], v[6], v[7]);
-    }
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int c = column<false>(g, e, t, nt);
-      if (c < H) row[c] = from_f32<E>(v[e]);
+      w[i] = __float_as_uint(f[i]);
     }
   }
+  E* at = row + first_column<NG>(a, g);
+  if constexpr (ALIGNED) {
+    if (counts<NG>(a, g)) store_words<E, true>(at, 8, 8, 0, w);
+  } else {
+    const int lane = a.t & 31;
+    store_words<E, false>(at, g < NG - 1 ? 8 : a.n, g < NG - 1 ? (lane < 31 ? 8 : 0) : a.next, lane, w);
+  }
+}
+
+// A row of f32 in shared memory, on a vector boundary and as long as whole vectors.
+template <int NG>
+__device__ __forceinline__ Eight shared8(const float* row, int g, const Place& a) {
+  const float* at = row + first_column<NG>(a, g);
+  const int n = g < NG - 1 ? 8 : a.held;
+  float f[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) f[e] = e < n ? at[e] : 0.0f;
+  return Eight{{pair(f[0], f[1]), pair(f[2], f[3]), pair(f[4], f[5]), pair(f[6], f[7])}};
+}
+
+__device__ __forceinline__ float product(const Eight& a, const Eight& b) {
+  f2 s = mul(a.v[0], b.v[0]);
+#pragma unroll
+  for (int i = 1; i < 4; ++i) s = fma(a.v[i], b.v[i], s);
+  return sum(s);
 }
 
 // ------------------------------------------------------------------ teams
@@ -112,33 +196,70 @@ __device__ __forceinline__ void team_sync(int nt) {
   else __syncwarp();
 }
 
+// Eight sums over a warp in nine exchanges: lanes 4 i .. 4 i + 3 have the i-th.
+__device__ __forceinline__ float warp_sum8(const float (&v)[8], int lane) {
+  float a[4], b[2];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const bool up = lane & 16;
+    a[i] = up ? v[4 + i] : v[i];
+    a[i] += __shfl_xor_sync(0xffffffffu, up ? v[i] : v[4 + i], 16);
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const bool up = lane & 8;
+    b[i] = up ? a[2 + i] : a[i];
+    b[i] += __shfl_xor_sync(0xffffffffu, up ? a[i] : a[2 + i], 8);
+  }
+  const bool up = lane & 4;
+  float s = up ? b[1] : b[0];
+  s += __shfl_xor_sync(0xffffffffu, up ? b[0] : b[1], 4);
+  s += __shfl_xor_sync(0xffffffffu, s, 2);
+  return s + __shfl_xor_sync(0xffffffffu, s, 1);
+}
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
 
-// N sums over the team, in a fixed order; `slots` holds N * 32 floats of shared memory
-// that no one else writes between two of the team's barriers.
-template <int N>
-__device__ __forceinline__ void team_sum(float (&v)[N], int t, int nt, float* slots) {
-#pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = warp_sum(v[i]);
-  if (nt == 32) return;
-  __syncthreads();  // (the slots' last readers are done)
-  if ((t & 31) == 0) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) slots[i * 32 + (t >> 5)] = v[i];
+// Sums over the team, in a fixed order.  Two areas of shared memory in turn
+// (`which`), so that one barrier a sum is enough: an area is written again
+// only after the barrier of the sum between.
+struct Slots {
+  float4 eight[2][32][2];
+};
+__device__ __forceinline__ void team_sum8(float (&v)[8], int t, int nt, Slots& slots, int& which) {
+  const int lane = t & 31;
+  float s = warp_sum8(v, lane);
+  if (nt > 32) {
+    float4(*area)[2] = slots.eight[which];
+    which ^= 1;
+    if ((lane & 3) == 0) reinterpret_cast<float*>(area[t >> 5])[lane >> 2] = s;
+    __syncthreads();
+    const float4 none = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    const float4 x = lane < (nt >> 5) ? area[lane][0] : none, y = lane < (nt >> 5) ? area[lane][1] : none;
+    const float u[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+    s = warp_sum8(u, lane);
   }
-  __syncthreads();
 #pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = warp_sum((t & 31) < (nt >> 5) ? slots[i * 32 + (t & 31)] : 0.0f);
+  for (int i = 0; i < 8; ++i) v[i] = __shfl_sync(0xffffffffu, s, 4 * i);
+}
+__device__ __forceinline__ float team_sum(float v, int t, int nt, Slots& slots, int& which) {
+  v = warp_sum(v);
+  if (nt == 32) return v;
+  float* area = reinterpret_cast<float*>(slots.eight[which]);
+  which ^= 1;
+  if ((t & 31) == 0) area[t >> 5] = v;
+  __syncthreads();
+  return warp_sum((t & 31) < (nt >> 5) ? area[t & 31] : 0.0f);
 }
 
-// Eight elements' keep bits.  VEC: the row's elements from a multiple of eight
-// are one of the generator's blocks.  Otherwise a block may straddle rows and
-// threads: the team makes the row's blocks together, a byte each, in `bytes`
-// (shared, (H + 14) / 8 + 1 of them), and every thread picks its bits.
+// ------------------------------------------------------------------ dropout
+// Eight elements' keep bits.  ALIGNED: the row's elements from a multiple of
+// eight are one of the generator's blocks.  Otherwise they lie in two, and the
+// team makes the row's blocks together, a byte each, in `bytes` (shared, (H +
+// 14) / 8 + 1 of them), of which every thread picks its bits.
 __device__ __forceinline__ void keep_bytes(const DropParams& d, uint64_t call, uint64_t first, int H, int t, int nt,
                                            uint8_t* bytes) {
   const uint64_t b0 = first >> 3;
@@ -147,299 +268,451 @@ __device__ __forceinline__ void keep_bytes(const DropParams& d, uint64_t call, u
   for (int i = t; i < n; i += nt) bytes[i] = (uint8_t)drop_keep8(d, b0 + i, call);
   team_sync(nt);
 }
-
-template <bool VEC>
-__device__ __forceinline__ uint32_t keep8(const DropParams& d, uint64_t call, uint64_t first, int g, int t, int nt, int H,
+template <bool ALIGNED, int NG>
+__device__ __forceinline__ uint32_t keep8(const DropParams& d, uint64_t call, uint64_t first, int g, const Place& a,
                                           const uint8_t* bytes) {
-  if constexpr (VEC) return drop_keep8(d, (first + column<true>(g, 0, t, nt)) >> 3, call);
-  uint32_t keep = 0;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const int c = column<false>(g, e, t, nt);
-    const uint32_t at = (uint32_t)(first & 7) + c;
-    if (c < H) keep |= ((bytes[at >> 3] >> (at & 7)) & 1u) << e;
-  }
-  return keep;
+  const int c = first_column<NG>(a, g);
+  if constexpr (ALIGNED) return drop_keep8(d, (first + c) >> 3, call);
+  const uint32_t at = (uint32_t)(first & 7) + c;
+  uint32_t keep = bytes[at >> 3] >> (at & 7);
+  // (the byte after is there if one of its elements is the row's)
+  if ((at & 7) + (g < NG - 1 ? 8 : a.held) > 8) keep |= (uint32_t)bytes[(at >> 3) + 1] << (8 - (at & 7));
+  return keep & 0xffu;
 }
-
 // (a dropped element is 0 whatever it was)
-__device__ __forceinline__ void drop8(float (&v)[8], uint32_t keep, float scale) {
+__device__ __forceinline__ void drop8(Eight& v, uint32_t keep) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) v[e] = (keep >> e) & 1u ? v[e] * scale : 0.0f;
+  for (int i = 0; i < 4; ++i) {
+    float a, b;
+    split(v.v[i], a, b);
+    v.v[i] = pair((keep >> (2 * i)) & 1u ? a : 0.0f, (keep >> (2 * i + 1)) & 1u ? b : 0.0f);
+  }
 }
 
-template <bool VEC, typename E>
-__device__ __forceinline__ void weights8(const void* w, int g, int t, int nt, int H, float (&v)[8]) {
-  load8<VEC>(static_cast<const E*>(w), g, t, nt, H, v);
+// ------------------------------------------------------------------ rows ahead
+// A thread's elements of the rows to come lie in shared memory, brought there
+// by its own 16-byte asynchronous copies, so that no register and no barrier
+// stands between HBM and the rows at work: a plane of 16 bytes a thread per
+// stage, tensor, group and vector that its eight elements touch.
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Waits until at most n (uniform, 0 to 3) of the thread's last groups are on their way.
+__device__ __forceinline__ void copies_wait(int n) {
+  if (n == 0) asm volatile("cp.async.wait_group 0;" ::: "memory");
+  else if (n == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
+  else if (n == 2) asm volatile("cp.async.wait_group 2;" ::: "memory");
+  else asm volatile("cp.async.wait_group 3;" ::: "memory");
+}
+
+// `at`: the tensor's first plane of the stage, this thread's 16 bytes.
+template <bool ALIGNED, int NG, typename E>
+__device__ __forceinline__ void row_ahead(uint4* at, const Rows<const E>& r, long row, const Place& a) {
+  const E* from = r[row];
+#pragma unroll
+  for (int g = 0; g < NG; ++g)
+    copy_words<E, ALIGNED>(at + g * vectors8<E, ALIGNED>() * a.nt, a.nt, from + first_column<NG>(a, g),
+                           g < NG - 1 ? 8 : a.held, r.span);
+}
+// Group g of a row that was brought ahead.
+template <bool ALIGNED, int NG, typename E>
+__device__ __forceinline__ Eight held8(const uint4* at, const Rows<const E>& r, long row, int g, const Place& a) {
+  uint32_t w[words8<E>()];
+  copied_words<E, ALIGNED>(at + g * vectors8<E, ALIGNED>() * a.nt, a.nt, r[row] + first_column<NG>(a, g),
+                           g < NG - 1 ? 8 : a.held, w);
+  return unpack<E>(w);
 }
 
 // ------------------------------------------------------------------ forward
 constexpr int kTeamRows = 8;  // rows, a warp each, in a CTA where a warp holds a row
 
-template <typename S, typename B, bool VEC, int NG>
-__global__ void __launch_bounds__(1024) residual_forward_kernel(const ResidualParams p) {
-  extern __shared__ uint8_t mask[];
-  __shared__ float slots[32];
+// AHEAD: the rows come through shared memory, `stages` rows ahead; otherwise
+// straight from global memory.
+template <typename S, typename B, bool ALIGNED, int NG, bool AHEAD>
+__global__ void __launch_bounds__(512, NG <= 2 ? 2 : 1) residual_forward_kernel(const ResidualParams p, int stages) {
+  extern __shared__ uint4 shared[];
+  __shared__ Slots slots;
   const int t = threadIdx.x, nt = blockDim.x, H = p.H;
-  const int row = blockIdx.x * blockDim.y + threadIdx.y;
-  if (row >= p.T) return;  // (a whole team: a warp of its own, or the whole CTA)
+  const int team = blockIdx.x * blockDim.y + threadIdx.y, teams = gridDim.x * blockDim.y;
+  if (team >= p.T) return;  // (a whole team: a warp of its own, or the whole CTA)
+  const Place a = place<NG>(t, nt, H);
   const float rH = 1.0f / (float)H;
-  float x[NG][8];
-  const S* xr = static_cast<const S*>(p.x) + row * p.ldx;
-#pragma unroll
-  for (int g = 0; g < NG; ++g) load8<VEC>(xr, g, t, nt, H, x[g]);
-  if (p.y) {
-    float z[NG][8];
-    const B* yr = static_cast<const B*>(p.y) + row * p.ldy;
-#pragma unroll
-    for (int g = 0; g < NG; ++g) load8<VEC>(yr, g, t, nt, H, z[g]);
-    float ry = 1.0f;
-    if (p.w_out) {
-      float s[1] = {0.0f};
-#pragma unroll
-      for (int g = 0; g < NG; ++g)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) s[0] = fmaf(z[g][e], z[g][e], s[0]);
-      team_sum(s, t, nt, slots);
-      ry = 1.0f / sqrtf(fmaf(s[0], rH, p.eps));
+  constexpr int kS = NG * vectors8<S, ALIGNED>(), kB = NG * vectors8<B, ALIGNED>(), kStage = kS + kB;  // planes
+  uint4* mine = shared + threadIdx.y * (AHEAD ? stages * kStage * nt : 0) + t;
+  uint8_t* bytes = reinterpret_cast<uint8_t*>(shared + blockDim.y * (AHEAD ? stages * kStage * nt : 0)) +
+                   threadIdx.y * ((H + 14) / 8 + 1);
+  const auto xs = rows_in<S>(p.x, p.ldx, p.T, H);
+  const auto ys = rows_in<B>(p.y, p.ldy, p.T, H), gates = rows_in<B>(p.gate, H, p.G, H);
+  const auto w_out = rows_in<B>(p.w_out, H, 1, H), w_next = rows_in<B>(p.w_next, H, 1, H);
+  const auto xo = rows_out<S>(p.xo, p.ldxo);
+  const auto n = rows_out<B>(p.n, p.ldn);
+  auto ahead = [&](long row, int stage) {
+    if (row < p.T) {
+      row_ahead<ALIGNED, NG>(mine + stage * kStage * nt, xs, row, a);
+      if (p.y) row_ahead<ALIGNED, NG>(mine + (stage * kStage + kS) * nt, ys, row, a);
     }
-    const uint64_t first = (uint64_t)row * (uint64_t)H;
-    uint8_t* bytes = mask + threadIdx.y * ((H + 14) / 8 + 1);
-    uint64_t call = 0;
-    if (p.drop.below) {
-      call = drop_call(p.drop);
-      if (!VEC) keep_bytes(p.drop, call, first, H, t, nt, bytes);
+    copies_commit();
+  };
+  if constexpr (AHEAD)
+    for (int i = 0; i < stages; ++i) ahead(team + (long)i * teams, i);
+  const uint64_t call = p.drop.below ? drop_call(p.drop) : 0;
+  const float scale = p.drop.below ? p.scale * p.drop.scale : p.scale;
+  int stage = 0, which = 0;
+  for (long row = team; row < p.T; row += teams) {
+    Eight x[NG];
+    auto get_x = [&](int g) {
+      if constexpr (AHEAD) return held8<ALIGNED, NG>(mine + stage * kStage * nt, xs, row, g, a);
+      else return load8<ALIGNED, NG>(xs, row, g, a);
+    };
+    if constexpr (AHEAD) copies_wait(stages - 1);
+    if (p.y) {
+      Eight z[NG];
+      if constexpr (!AHEAD) {
+        // (all of a row's loads together)
+#pragma unroll
+        for (int g = 0; g < NG; ++g) x[g] = get_x(g);
+      }
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        if constexpr (AHEAD) z[g] = held8<ALIGNED, NG>(mine + (stage * kStage + kS) * nt, ys, row, g, a);
+        else z[g] = load8<ALIGNED, NG>(ys, row, g, a);
+      }
+      float factor = scale;
+      if (p.w_out) {
+        float s = 0.0f;
+#pragma unroll
+        for (int g = 0; g < NG; ++g) s += counts<NG>(a, g) ? squares(z[g]) : 0.0f;
+        factor *= rsqrtf(fmaf(team_sum(s, t, nt, slots, which), rH, p.eps));
+      }
+      const uint64_t first = (uint64_t)row * (uint64_t)H;
+      if (!ALIGNED && p.drop.below) keep_bytes(p.drop, call, first, H, t, nt, bytes);
+      const uint32_t group = p.G ? (uint32_t)row / (uint32_t)p.rows_per_gate : 0;
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        if constexpr (AHEAD) x[g] = get_x(g);
+        if (p.drop.below) drop8(z[g], keep8<ALIGNED, NG>(p.drop, call, first, g, a, bytes));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) z[g].v[i] = mul(z[g].v[i], both(factor));
+        if (p.w_out) {
+          const Eight w = load8<ALIGNED, NG>(w_out, 0, g, a);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) z[g].v[i] = mul(z[g].v[i], w.v[i]);
+        }
+        const Eight f = p.G ? load8<ALIGNED, NG>(gates, group, g, a) : ones();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[g].v[i] = fma(z[g].v[i], f.v[i], x[g].v[i]);
+        store8<ALIGNED, NG>(xo[row], g, a, x[g]);
+      }
+    } else {
+#pragma unroll
+      for (int g = 0; g < NG; ++g) x[g] = get_x(g);
     }
-    const B* gr = p.G ? static_cast<const B*>(p.gate) + (long)(row / p.rows_per_gate) * H : nullptr;
+    if constexpr (AHEAD) {
+      // (the thread's values of this stage are in its registers)
+      ahead(row + (long)stages * teams, stage);
+      if (++stage == stages) stage = 0;
+    }
+    if (!p.n) continue;
+    float s = 0.0f;
+#pragma unroll
+    for (int g = 0; g < NG; ++g) s += counts<NG>(a, g) ? squares(x[g]) : 0.0f;
+    const float r = rsqrtf(fmaf(team_sum(s, t, nt, slots, which), rH, p.eps));
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
-      float w[8];
-      if (p.w_out) {
-        weights8<VEC, B>(p.w_out, g, t, nt, H, w);
+      const Eight w = load8<ALIGNED, NG>(w_next, 0, g, a);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) z[g][e] *= ry * w[e];
-      }
-      if (p.drop.below) drop8(z[g], keep8<VEC>(p.drop, call, first, g, t, nt, H, bytes), p.drop.scale);
-      if (gr) {
-        load8<VEC>(gr, g, t, nt, H, w);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[g][e] = fmaf(p.scale * w[e], z[g][e], x[g][e]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[g][e] = fmaf(p.scale, z[g][e], x[g][e]);
-      }
+      for (int i = 0; i < 4; ++i) x[g].v[i] = mul(mul(x[g].v[i], both(r)), w.v[i]);
+      store8<ALIGNED, NG>(n[row], g, a, x[g]);
     }
-    S* xo = static_cast<S*>(p.xo) + row * p.ldxo;
-#pragma unroll
-    for (int g = 0; g < NG; ++g) store8<VEC>(xo, g, t, nt, H, x[g]);
-  }
-  if (!p.n) return;
-  float s[1] = {0.0f};
-#pragma unroll
-  for (int g = 0; g < NG; ++g)
-#pragma unroll
-    for (int e = 0; e < 8; ++e) s[0] = fmaf(x[g][e], x[g][e], s[0]);
-  team_sum(s, t, nt, slots);
-  const float r = 1.0f / sqrtf(fmaf(s[0], rH, p.eps));
-  B* n = static_cast<B*>(p.n) + row * p.ldn;
-#pragma unroll
-  for (int g = 0; g < NG; ++g) {
-    float w[8];
-    weights8<VEC, B>(p.w_next, g, t, nt, H, w);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) w[e] *= x[g][e] * r;
-    store8<VEC>(n, g, t, nt, H, w);
   }
 }
 
 // ------------------------------------------------------------------ backward
 // The rows are cut into units, no unit across two gate rows' rows: G * split
 // of them, or as many as workers where there is no gate.  A worker (a team)
-// takes whole units and sums the columns of dw_next and dw_out over all of its
-// rows, of dgate over a unit; the sums of workers and units are then joined in
-// a fixed order by a second kernel.
+// takes whole units.  It sums two things over its rows, by column:
+//
+//   sum_next = sum dn xh,   sum_y = sum dropout(dx) yh  over a unit
+//
+// Within a unit the gate is one row, so both other gradients follow from
+// sum_y: dw_out = sum over units of scale gate sum_y, dgate = scale w_out
+// sum_y.  (Without w_out, yh stands for y.)  A second kernel joins the
+// workers' and units' sums in a fixed order.  With more gate rows than workers
+// (`own`) a unit is a gate row's rows: its worker writes that row of dgate
+// itself and keeps its share of dw_out in shared memory.
 struct BackwardPlan {
   int workers;   // teams
   int groups;    // rows of the gate, 1 without
   int split;     // units per group
+  int own;       // split is 1 and there are several gate rows
 };
 
-template <typename S, typename B, bool VEC, int NG>
-__global__ void __launch_bounds__(1024) residual_backward_kernel(const ResidualParams p, const BackwardPlan plan) {
-  extern __shared__ uint8_t mask[];
-  __shared__ float slots[3 * 32];
+// A worker's rows, one after the other.
+struct Walk {
+  int unit, group;
+  long row, end;  // the row at hand and the end of its unit
+};
+__device__ __forceinline__ void walk_unit(Walk& w, const ResidualParams& p, const BackwardPlan& plan) {
+  const long per = p.T / plan.groups;
+  w.group = w.unit / plan.split;
+  const int part = w.unit - w.group * plan.split;
+  w.row = w.group * per + per * part / plan.split;
+  w.end = w.group * per + per * (part + 1) / plan.split;
+}
+__device__ __forceinline__ bool walk_on(Walk& w, const ResidualParams& p, const BackwardPlan& plan) {
+  if (++w.row < w.end) return true;
+  w.unit += plan.workers;
+  if (w.unit >= plan.groups * plan.split) return false;
+  walk_unit(w, p, plan);
+  return true;
+}
+
+// Shared memory of a team beside its stages: its share of dw_out, and the keep bytes.
+__host__ __device__ __forceinline__ size_t backward_beside(int H, bool bytes, bool own) {
+  const size_t share = own ? (size_t)(H + 3) / 4 * 16 : 0;
+  return share + (bytes ? ((H + 14) / 8 + 16) / 16 * 16 : 0);
+}
+
+template <typename S, typename B, bool ALIGNED, int NG, bool AHEAD>
+__global__ void __launch_bounds__(NG == 1 ? 256 : 512, NG == 1 ? 3 : 1)
+    residual_backward_kernel(const ResidualParams p, const BackwardPlan plan, int stages) {
+  extern __shared__ uint4 shared[];
+  __shared__ Slots slots;
   const int t = threadIdx.x, nt = blockDim.x, H = p.H;
   const int worker = blockIdx.x * blockDim.y + threadIdx.y;
   if (worker >= plan.workers) return;  // (whole teams)
+  const Place a = place<NG>(t, nt, H);
   const float rH = 1.0f / (float)H;
-  const bool has_y = p.y != nullptr && (p.w_out || p.G);  // y's values matter
-  uint8_t* bytes = mask + threadIdx.y * ((H + 14) / 8 + 1);
+  const auto dxos = rows_in<S>(p.dxo, p.lddxo, p.T, H), xs = rows_in<S>(p.x, p.ldx, p.T, H);
+  const auto dns = rows_in<B>(p.dn, p.lddn, p.T, H), ys = rows_in<B>(p.y, p.ldy, p.T, H);
+  const auto gates = rows_in<B>(p.gate, H, p.G, H), w_out = rows_in<B>(p.w_out, H, 1, H),
+             w_next = rows_in<B>(p.w_next, H, 1, H);
+  const auto dx = rows_out<S>(p.dx, p.lddx);
+  const auto dy = rows_out<B>(p.dy, p.lddy);
   const uint64_t call = p.drop.below ? drop_call(p.drop) : 0;
-  const long rows_per_group = p.T / plan.groups;
-  float sum_next[NG][8], sum_out[NG][8], sum_gate[NG][8];
+  // a stage's planes: dxo, x, dn, y
+  constexpr int kS = NG * vectors8<S, ALIGNED>(), kB = NG * vectors8<B, ALIGNED>(), kStage = 2 * (kS + kB);
+  const int team_planes = AHEAD ? stages * kStage * nt : 0;
+  uint4* mine = shared + threadIdx.y * team_planes + t;
+  uint8_t* beside = reinterpret_cast<uint8_t*>(shared + blockDim.y * team_planes) +
+                    threadIdx.y * backward_beside(H, !ALIGNED && p.drop.below, plan.own);
+  float* share = reinterpret_cast<float*>(beside);  // whole vectors of its own: a thread's eight are its alone
+  uint8_t* bytes = beside + (plan.own ? (H + 3) / 4 * 16 : 0);
+  Eight sum_next[NG], sum_y[NG];
 #pragma unroll
-  for (int g = 0; g < NG; ++g)
-#pragma unroll
-    for (int e = 0; e < 8; ++e) sum_next[g][e] = sum_out[g][e] = 0.0f;
+  for (int g = 0; g < NG; ++g) {
+    sum_next[g] = sum_y[g] = zeros();
+    if (plan.own) store8<ALIGNED, NG>(share, g, a, zeros());
+  }
 
-  for (int unit = worker; unit < plan.groups * plan.split; unit += plan.workers) {
-    const int group = unit / plan.split, part = unit % plan.split;
-    const long row0 = group * rows_per_group + rows_per_group * part / plan.split;
-    const long row1 = group * rows_per_group + rows_per_group * (part + 1) / plan.split;
+  // (a worker without a unit, or the only one's rows with T = 0: no rows, sums of zero)
+  Walk at = {worker, 0, 0, 0};
+  if (worker < plan.groups * plan.split) walk_unit(at, p, plan);
+  bool more = at.row < at.end;
+  Walk next = at;
+  bool more_next = more;
+  auto ahead = [&](int stage) {
+    if (more_next) {
+      uint4* m = mine + stage * kStage * nt;
+      if (p.dxo) row_ahead<ALIGNED, NG>(m, dxos, next.row, a);
+      if (p.dn) {
+        row_ahead<ALIGNED, NG>(m + kS * nt, xs, next.row, a);
+        row_ahead<ALIGNED, NG>(m + 2 * kS * nt, dns, next.row, a);
+      }
+      if (p.y) row_ahead<ALIGNED, NG>(m + (2 * kS + kB) * nt, ys, next.row, a);
+      more_next = walk_on(next, p, plan);
+    }
+    copies_commit();
+  };
+  if constexpr (AHEAD)
+    for (int i = 0; i < stages; ++i) ahead(i);
+  int stage = 0, which = 0;
+  while (more) {
+    // A row's values are read again where they are used again (from shared memory, or the second time from L1):
+    // what stays in registers over the barrier is the columns' sums.
+    const long row = at.row;
+    const uint4* m = mine + stage * kStage * nt;
+    auto get_dxo = [&](int g) {
+      if constexpr (AHEAD) return held8<ALIGNED, NG>(m, dxos, row, g, a);
+      else return load8<ALIGNED, NG>(dxos, row, g, a);
+    };
+    auto get_x = [&](int g) {
+      if constexpr (AHEAD) return held8<ALIGNED, NG>(m + kS * nt, xs, row, g, a);
+      else return load8<ALIGNED, NG>(xs, row, g, a);
+    };
+    auto get_dn = [&](int g) {
+      if constexpr (AHEAD) return held8<ALIGNED, NG>(m + 2 * kS * nt, dns, row, g, a);
+      else return load8<ALIGNED, NG>(dns, row, g, a);
+    };
+    auto get_y = [&](int g) {
+      if constexpr (AHEAD) return held8<ALIGNED, NG>(m + (2 * kS + kB) * nt, ys, row, g, a);
+      else return load8<ALIGNED, NG>(ys, row, g, a);
+    };
+    const uint64_t first = (uint64_t)row * (uint64_t)H;
+    // what stands between dx and t': the gate, w_out and dropout (its factor and `scale` come in at the end)
+    auto between = [&](int g) {
+      Eight f = p.G ? load8<ALIGNED, NG>(gates, at.group, g, a) : ones();
+      if (p.w_out) {
+        const Eight w = load8<ALIGNED, NG>(w_out, 0, g, a);
 #pragma unroll
-    for (int g = 0; g < NG; ++g)
+        for (int i = 0; i < 4; ++i) f.v[i] = mul(f.v[i], w.v[i]);
+      }
+      return f;
+    };
+    if constexpr (AHEAD) copies_wait(stages - 1);
+    if (!ALIGNED && p.drop.below && p.dy) keep_bytes(p.drop, call, first, H, t, nt, bytes);
+    uint32_t keep[NG];
+    // Sums of y^2, x'^2, t x' and, with f as above and y, of dx' f y, t f y, x' f y: as dx is linear in the first
+    // norm's two factors, sum t' y follows from those three, and all of a row's sums are made at once.
+    float s[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-      for (int e = 0; e < 8; ++e) sum_gate[g][e] = 0.0f;
-    const B* gr = p.G ? static_cast<const B*>(p.gate) + (long)group * H : nullptr;
-    for (long row = row0; row < row1; ++row) {
-      const uint64_t first = (uint64_t)row * (uint64_t)H;
-      // dx in d, y in y
-      float d[NG][8], y[NG][8];
-      float s[3] = {0.0f, 0.0f, 0.0f};  // of y^2, x'^2, t x'
+    for (int g = 0; g < NG; ++g) {
+      float u[6] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+      Eight fy = zeros();
+      keep[g] = 0xffu;
+      if (p.drop.below && p.dy) keep[g] = keep8<ALIGNED, NG>(p.drop, call, first, g, a, bytes);
+      if (p.w_out && p.y) {
+        const Eight y = get_y(g);
+        fy = between(g);
+        u[0] = squares(y);
 #pragma unroll
-      for (int g = 0; g < NG; ++g) {
-        if (p.dxo) {
-          load8<VEC>(static_cast<const S*>(p.dxo) + row * p.lddxo, g, t, nt, H, d[g]);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) d[g][e] = 0.0f;
-        }
-        if (has_y) {
-          load8<VEC>(static_cast<const B*>(p.y) + row * p.ldy, g, t, nt, H, y[g]);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) s[0] = fmaf(y[g][e], y[g][e], s[0]);
-        }
+        for (int i = 0; i < 4; ++i) fy.v[i] = mul(fy.v[i], y.v[i]);
+        if (p.drop.below) drop8(fy, keep[g]);
+      }
+      if (p.dxo && p.w_out && p.y) {
+        Eight d = get_dxo(g);
+        if (p.drop.below) drop8(d, keep[g]);  // (a dropped gradient may be anything too)
+        u[3] = product(d, fy);
       }
       if (p.dn) {
-        float x[NG][8], dn[NG][8];
+        const Eight x = get_x(g), w = load8<ALIGNED, NG>(w_next, 0, g, a);
+        Eight v = get_dn(g);
 #pragma unroll
-        for (int g = 0; g < NG; ++g) {
-          float w[8];
-          load8<VEC>(static_cast<const S*>(p.x) + row * p.ldx, g, t, nt, H, x[g]);
-          load8<VEC>(static_cast<const B*>(p.dn) + row * p.lddn, g, t, nt, H, dn[g]);
-          weights8<VEC, B>(p.w_next, g, t, nt, H, w);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            s[1] = fmaf(x[g][e], x[g][e], s[1]);
-            s[2] = fmaf(dn[g][e] * w[e], x[g][e], s[2]);
-          }
-        }
-        team_sum(s, t, nt, slots);
-        const float r = 1.0f / sqrtf(fmaf(s[1], rH, p.eps));
-        const float m = s[2] * rH * r * r;  // mean(t xh) r / r
-#pragma unroll
-        for (int g = 0; g < NG; ++g) {
-          float w[8];
-          weights8<VEC, B>(p.w_next, g, t, nt, H, w);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            sum_next[g][e] = fmaf(dn[g][e], x[g][e] * r, sum_next[g][e]);
-            d[g][e] = fmaf(r, fmaf(dn[g][e], w[e], -m * x[g][e]), d[g][e]);
-          }
-        }
-      } else if (p.w_out) {
-        team_sum(s, t, nt, slots);
-      }
-      if (p.dx) {
-#pragma unroll
-        for (int g = 0; g < NG; ++g) store8<VEC>(static_cast<S*>(p.dx) + row * p.lddx, g, t, nt, H, d[g]);
-      }
-      if (!p.dy) continue;
-      // the branch: d becomes dz
-      const float ry = p.w_out ? 1.0f / sqrtf(fmaf(s[0], rH, p.eps)) : 1.0f;
-      if (!VEC && p.drop.below) keep_bytes(p.drop, call, first, H, t, nt, bytes);
-      float q[1] = {0.0f};  // of t' y
-#pragma unroll
-      for (int g = 0; g < NG; ++g) {
-        float w[8], v[8];
-        if (p.w_out) weights8<VEC, B>(p.w_out, g, t, nt, H, w);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) d[g][e] *= p.scale;
-        uint32_t keep = 0xffu;
-        if (p.drop.below) {
-          keep = keep8<VEC>(p.drop, call, first, g, t, nt, H, bytes);
-          drop8(d[g], keep, p.drop.scale);
-        }
-        if (gr) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            // (a dropped y may be anything, an infinity too)
-            const float z = !((keep >> e) & 1u) ? 0.0f : p.w_out ? y[g][e] * (ry * w[e]) : y[g][e];
-            sum_gate[g][e] = fmaf(d[g][e], z, sum_gate[g][e]);
-          }
-          load8<VEC>(gr, g, t, nt, H, v);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) d[g][e] *= v[e];
-        }
-        if (p.w_out) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            sum_out[g][e] = fmaf(d[g][e], y[g][e] * ry, sum_out[g][e]);
-            d[g][e] *= w[e];
-            q[0] = fmaf(d[g][e], y[g][e], q[0]);
-          }
-        }
-      }
-      if (p.w_out) {
-        team_sum(q, t, nt, slots);
-        const float m = q[0] * rH * ry * ry;
-#pragma unroll
-        for (int g = 0; g < NG; ++g)
-#pragma unroll
-          for (int e = 0; e < 8; ++e) d[g][e] = ry * fmaf(-m, y[g][e], d[g][e]);
+        for (int i = 0; i < 4; ++i) v.v[i] = mul(v.v[i], w.v[i]);
+        u[1] = squares(x);
+        u[2] = product(v, x);
+        u[4] = product(v, fy);
+        u[5] = product(x, fy);
       }
 #pragma unroll
-      for (int g = 0; g < NG; ++g) store8<VEC>(static_cast<B*>(p.dy) + row * p.lddy, g, t, nt, H, d[g]);
+      for (int i = 0; i < 6; ++i) s[i] += counts<NG>(a, g) ? u[i] : 0.0f;
     }
-    if (p.G) {
+    if (p.dn || p.w_out) team_sum8(s, t, nt, slots, which);
+    const float ry = p.w_out ? rsqrtf(fmaf(s[0], rH, p.eps)) : 1.0f, r = rsqrtf(fmaf(s[1], rH, p.eps));
+    const float mean = s[2] * rH * r * r;  // mean(t xh) r / r
+    const float mean_y = (s[3] + r * (s[4] - mean * s[5])) * rH * ry * ry;  // mean(t' yh) ry / ry
+    const float factor = (p.drop.below ? p.scale * p.drop.scale : p.scale) * ry;
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      Eight d = p.dxo ? get_dxo(g) : zeros();
+      if (p.dn) {
+        const Eight x = get_x(g), w = load8<ALIGNED, NG>(w_next, 0, g, a), v = get_dn(g);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          sum_next[g].v[i] = fma(v.v[i], mul(x.v[i], both(r)), sum_next[g].v[i]);
+          d.v[i] = fma(both(r), fma(both(-mean), x.v[i], mul(v.v[i], w.v[i])), d.v[i]);
+        }
+      }
+      Eight y = zeros();
+      if (p.y) y = get_y(g);
+      const Eight f = p.dy ? between(g) : zeros();
+      if (p.dx) store8<ALIGNED, NG>(dx[row], g, a, d);
+      if (!p.dy) continue;
+      // the branch
+      if (p.drop.below) drop8(d, keep[g]);
+      if (p.y) {
+        Eight u = y;
+        if (p.drop.below) drop8(u, keep[g]);  // (a dropped y may be anything, an infinity too)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sum_y[g].v[i] = fma(d.v[i], mul(u.v[i], both(ry)), sum_y[g].v[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        d.v[i] = mul(d.v[i], f.v[i]);
+        if (p.w_out) d.v[i] = fma(both(-mean_y), y.v[i], d.v[i]);
+        d.v[i] = mul(d.v[i], both(factor));
+      }
+      store8<ALIGNED, NG>(dy[row], g, a, d);
+    }
+    if constexpr (AHEAD) {
+      ahead(stage);
+      if (++stage == stages) stage = 0;
+    }
+    const int unit = at.unit, group = at.group;
+    more = walk_on(at, p, plan);
+    if ((!more || at.unit != unit) && plan.own) {
+      // the unit ends: its row of dgate, its share of dw_out
+      const float scale = p.drop.below ? p.scale * p.drop.scale : p.scale;
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
-        if (plan.split == 1)
-          store8<VEC>(static_cast<B*>(p.dgate) + (long)group * H, g, t, nt, H, sum_gate[g]);
-        else
+        Eight v = sum_y[g];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int c = column<VEC>(g, e, t, nt);
-            if (c < H) p.part[(2l * plan.workers + unit) * H + c] = sum_gate[g][e];
+        for (int i = 0; i < 4; ++i) v.v[i] = mul(v.v[i], both(scale));
+        if (p.dw_out) {
+          const Eight f = load8<ALIGNED, NG>(gates, group, g, a);
+          Eight sh = shared8<NG>(share, g, a);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sh.v[i] = fma(v.v[i], f.v[i], sh.v[i]);
+          store8<ALIGNED, NG>(share, g, a, sh);
+        }
+        if (p.dgate) {
+          if (p.w_out) {
+            const Eight w = load8<ALIGNED, NG>(w_out, 0, g, a);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v.v[i] = mul(v.v[i], w.v[i]);
           }
+          store8<ALIGNED, NG>(static_cast<B*>(p.dgate) + (long)group * H, g, a, v);
+        }
+        sum_y[g] = zeros();
       }
     }
   }
+  // (a worker has one unit at most unless it wrote them itself)
 #pragma unroll
-  for (int g = 0; g < NG; ++g)
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int c = column<VEC>(g, e, t, nt);
-      if (c < H) {
-        if (p.dw_next) p.part[(long)worker * H + c] = sum_next[g][e];
-        if (p.dw_out) p.part[((long)plan.workers + worker) * H + c] = sum_out[g][e];
-      }
-    }
+  for (int g = 0; g < NG; ++g) {
+    if (p.dw_next) store8<ALIGNED, NG>(p.part + (long)worker * H, g, a, sum_next[g]);
+    if (p.dw_out || p.dgate)
+      store8<ALIGNED, NG>(p.part + ((long)plan.workers + worker) * H, g, a, plan.own ? shared8<NG>(share, g, a) : sum_y[g]);
+  }
 }
 
 // Joins the column sums: 32 columns a CTA, 16 threads a column, each over
-// every 16th part and then in order.
+// every 16th part and then in order.  Row 0 of the grid is dw_next, row 1
+// dw_out (the units' sums by their gates), then the rows of dgate.
 constexpr int kJoinRows = 16;
 template <typename B>
 __global__ void __launch_bounds__(32 * kJoinRows) residual_join_kernel(const ResidualParams p, const BackwardPlan plan) {
   __shared__ float sums[kJoinRows][33];
-  const int c = blockIdx.x * 32 + threadIdx.x, what = blockIdx.y;  // 0 dw_next, 1 dw_out, 2 + g dgate
+  const int c = blockIdx.x * 32 + threadIdx.x, what = blockIdx.y;
   if ((what == 0 && !p.dw_next) || (what == 1 && !p.dw_out)) return;
+  const bool gated = what == 1 && p.G && !plan.own;
   const int n = what < 2 ? plan.workers : plan.split;
-  const float* part = p.part + (what < 2 ? (long)what * plan.workers : 2l * plan.workers + (long)(what - 2) * plan.split) * p.H;
+  const long part0 = what == 0 ? 0 : what == 1 ? plan.workers : plan.workers + (long)(what - 2) * plan.split;
+  const float* part = p.part + part0 * p.H;
+  const int units = plan.groups * plan.split;
   float s = 0.0f;
   if (c < p.H) {
-#pragma unroll 8
-    for (int i = threadIdx.y; i < n; i += kJoinRows) s += part[(long)i * p.H + c];
+#pragma unroll 4
+    for (int i = threadIdx.y; i < n; i += kJoinRows) {
+      const float v = part[(long)i * p.H + c];
+      // (a worker without a unit has sums of zero)
+      const int group = i < units ? i / plan.split : 0;
+      s = gated ? fmaf(v, to_f32(static_cast<const B*>(p.gate)[(long)group * p.H + c]), s) : s + v;
+    }
   }
   sums[threadIdx.y][threadIdx.x] = s;
   __syncthreads();
   if (threadIdx.y != 0 || c >= p.H) return;
 #pragma unroll
   for (int i = 1; i < kJoinRows; ++i) s += sums[i][threadIdx.x];
-  if (what == 0) p.dw_next[c] = s;
-  else if (what == 1) p.dw_out[c] = s;
-  else static_cast<B*>(p.dgate)[(long)(what - 2) * p.H + c] = from_f32<B>(s);
+  const float scale = p.drop.below ? p.scale * p.drop.scale : p.scale;
+  if (what == 0) {
+    p.dw_next[c] = s;
+  } else if (what == 1) {
+    p.dw_out[c] = plan.own ? s : s * scale;
+  } else {
+    s *= scale;
+    if (p.w_out) s *= to_f32(static_cast<const B*>(p.w_out)[c]);
+    static_cast<B*>(p.dgate)[(long)(what - 2) * p.H + c] = from_f32<B>(s);
+  }
 }
 
 // ------------------------------------------------------------------ launches
@@ -457,62 +730,119 @@ bool all_vectors(const ResidualParams& p) {
          vectors<B>(p.dy, p.lddy) && vectors<B>(p.dgate, 0);
 }
 
-int groups_per_thread(int H) { return H <= 8192 ? 1 : 2; }
-int team_threads(int H) {
-  const int per = 8 * groups_per_thread(H);
-  return ((H + per - 1) / per + 31) / 32 * 32;
+// Shared memory of the rows ahead, over all of an SM's CTAs: enough for what HBM has on its way, and the rest left to
+// L1 for the weights.
+constexpr size_t kAheadBytes = 176 * 1024;
+constexpr int kMaxStages = 4;
+
+int team_threads(int H, int ng) { return ((H + 8 * ng - 1) / (8 * ng) + 31) / 32 * 32; }
+int groups_forward(int H) { return H <= 4096 ? 1 : H <= 8192 ? 2 : 4; }
+int groups_backward(int H) { return H <= 2048 ? 1 : H <= 8192 ? 2 : 4; }
+// CTAs that an SM holds (registers).
+int ctas_forward(int threads, int ng) { return std::max(1, (ng <= 2 ? 1024 : 512) / threads); }
+int ctas_backward(int threads, int ng) { return std::max(1, (ng == 1 ? 768 : 512) / threads); }
+
+// How many rows ahead, with as many CTAs an SM as have room for two at least (0: none).
+int stages_ahead(int* ctas, size_t stage, size_t beside) {
+  for (int c = *ctas; c > 0; --c) {
+    const size_t room = kAheadBytes / c;
+    const int stages = room > beside ? std::min<int>(kMaxStages, (int)((room - beside) / stage)) : 0;
+    if (stages >= 2) {
+      *ctas = c;
+      return stages;
+    }
+  }
+  return 0;
 }
 
-BackwardPlan backward_plan(int T, int H, int G, int sms) {
+// All the teams that the SMs hold, and four rows at least for one of them, so that the parts stay few beside the rows.
+BackwardPlan backward_plan(int T, int G, int teams) {
   BackwardPlan b;
-  const int nt = team_threads(H);
-  // at most 2,048 threads an SM, and four rows at least for a worker, so that the
-  // parts stay few beside the rows
-  const int most = nt == 32 ? sms * 32 : sms * std::max(1, 1024 / nt);
-  b.workers = std::max(1, std::min(most, (T + 3) / 4));
+  b.workers = std::max(1, std::min(teams, (T + 3) / 4));
   b.groups = std::max(1, G);
   b.split = std::max(1, std::min(b.workers / b.groups, T / b.groups));
+  b.own = b.split == 1 && b.groups > 1;
   return b;
 }
 
-template <typename S, typename B>
-cudaError_t forward(const ResidualParams& p, cudaStream_t st) {
-  const int nt = team_threads(p.H), rows = nt == 32 ? kTeamRows : 1;
-  const dim3 grid((p.T + rows - 1) / rows), block(nt, rows);
-  const bool vec = all_vectors<S, B>(p);
-  const size_t smem = !vec && p.drop.below ? (size_t)rows * ((p.H + 14) / 8 + 1) : 0;
-  const bool one = groups_per_thread(p.H) == 1;
-  auto k = vec ? (one ? residual_forward_kernel<S, B, true, 1> : residual_forward_kernel<S, B, true, 2>)
-               : (one ? residual_forward_kernel<S, B, false, 1> : residual_forward_kernel<S, B, false, 2>);
-  k<<<grid, block, smem, st>>>(p);
+template <typename K, typename... A>
+cudaError_t start(K kernel, dim3 grid, dim3 block, size_t smem, cudaStream_t st, A... args) {
+  if (smem > 40 * 1024) {  // (what every kernel has, less what is there beside it)
+    const cudaError_t e = cudaFuncSetAttribute((const void*)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
+  kernel<<<grid, block, smem, st>>>(args...);
   return cudaGetLastError();
 }
 
-template <typename S, typename B>
+template <typename S, typename B, bool ALIGNED, int NG>
+cudaError_t forward(const ResidualParams& p, cudaStream_t st) {
+  const int nt = team_threads(p.H, NG), rows = nt == 32 ? kTeamRows : 1, sms = device_sm_count();
+  const dim3 block(nt, rows);
+  const size_t beside = !ALIGNED && p.drop.below ? (size_t)rows * ((p.H + 14) / 8 + 1) : 0;
+  const size_t stage = (size_t)rows * nt * NG * (vectors8<S, ALIGNED>() + vectors8<B, ALIGNED>()) * 16;
+  int ctas = ctas_forward(nt * rows, NG);
+  const int stages = stages_ahead(&ctas, stage, beside), grid = (p.T + rows - 1) / rows;
+  // (a team's only row needs no stage)
+  if (stages == 0 || grid <= ctas * sms)
+    return start(residual_forward_kernel<S, B, ALIGNED, NG, false>, dim3(grid), block, beside, st, p, 0);
+  return start(residual_forward_kernel<S, B, ALIGNED, NG, true>, dim3(ctas * sms), block, stages * stage + beside, st, p,
+               stages);
+}
+
+template <typename S, typename B, bool ALIGNED, int NG>
 cudaError_t backward(const ResidualParams& p, int* launches, cudaStream_t st) {
-  const BackwardPlan plan = backward_plan(p.T, p.H, p.G, device_sm_count());
-  const int nt = team_threads(p.H), rows = nt == 32 ? kTeamRows : 1;
+  const int nt = team_threads(p.H, NG), rows = nt == 32 ? kTeamRows : 1;
+  const size_t stage = (size_t)rows * nt * NG * 2 * (vectors8<S, ALIGNED>() + vectors8<B, ALIGNED>()) * 16;
+  const bool bytes = !ALIGNED && p.drop.below;
+  int ctas = ctas_backward(nt * rows, NG);
+  const int stages = stages_ahead(&ctas, stage, rows * backward_beside(p.H, bytes, p.G > 1));
+  const BackwardPlan plan = backward_plan(p.T, p.G, device_sm_count() * ctas * rows);
+  const size_t beside = rows * backward_beside(p.H, bytes, plan.own);
   const dim3 grid((plan.workers + rows - 1) / rows), block(nt, rows);
-  const bool vec = all_vectors<S, B>(p);
-  const size_t smem = !vec && p.drop.below ? (size_t)rows * ((p.H + 14) / 8 + 1) : 0;
-  const bool one = groups_per_thread(p.H) == 1;
-  auto k = vec ? (one ? residual_backward_kernel<S, B, true, 1> : residual_backward_kernel<S, B, true, 2>)
-               : (one ? residual_backward_kernel<S, B, false, 1> : residual_backward_kernel<S, B, false, 2>);
-  k<<<grid, block, smem, st>>>(p, plan);
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e;
+  if (stages == 0) e = start(residual_backward_kernel<S, B, ALIGNED, NG, false>, grid, block, beside, st, p, plan, 0);
+  else e = start(residual_backward_kernel<S, B, ALIGNED, NG, true>, grid, block, stages * stage + beside, st, p, plan, stages);
   *launches = 1;
-  const int joins = p.G && plan.split > 1 ? 2 + plan.groups : 2;
-  if (e != cudaSuccess || (joins == 2 && !p.dw_next && !p.dw_out)) return e;
-  residual_join_kernel<B><<<dim3((p.H + 31) / 32, joins), dim3(32, kJoinRows), 0, st>>>(p, plan);
+  const bool dgate = p.dgate && !plan.own;
+  if (e != cudaSuccess || (!p.dw_next && !p.dw_out && !dgate)) return e;
+  residual_join_kernel<B><<<dim3((p.H + 31) / 32, dgate ? 2 + plan.groups : 2), dim3(32, kJoinRows), 0, st>>>(p, plan);
   ++*launches;
   return cudaGetLastError();
+}
+
+template <typename S, typename B, bool ALIGNED>
+cudaError_t forward(const ResidualParams& p, cudaStream_t st) {
+  switch (groups_forward(p.H)) {
+    case 1: return forward<S, B, ALIGNED, 1>(p, st);
+    case 2: return forward<S, B, ALIGNED, 2>(p, st);
+    default: return forward<S, B, ALIGNED, 4>(p, st);
+  }
+}
+template <typename S, typename B>
+cudaError_t forward(const ResidualParams& p, cudaStream_t st) {
+  return all_vectors<S, B>(p) ? forward<S, B, true>(p, st) : forward<S, B, false>(p, st);
+}
+
+template <typename S, typename B, bool ALIGNED>
+cudaError_t backward(const ResidualParams& p, int* launches, cudaStream_t st) {
+  switch (groups_backward(p.H)) {
+    case 1: return backward<S, B, ALIGNED, 1>(p, launches, st);
+    case 2: return backward<S, B, ALIGNED, 2>(p, launches, st);
+    default: return backward<S, B, ALIGNED, 4>(p, launches, st);
+  }
+}
+template <typename S, typename B>
+cudaError_t backward(const ResidualParams& p, int* launches, cudaStream_t st) {
+  return all_vectors<S, B>(p) ? backward<S, B, true>(p, launches, st) : backward<S, B, false>(p, launches, st);
 }
 
 }  // namespace
 
 size_t residual_part_floats(int T, int H) {
-  // (any gate: units are no more than workers where their sums are parts)
-  return 3 * (size_t)backward_plan(T, H, 0, device_sm_count()).workers * H;
+  // (units are no more than workers where their sums are parts)
+  const int ng = groups_backward(H), nt = team_threads(H, ng), rows = nt == 32 ? kTeamRows : 1;
+  return 2 * (size_t)backward_plan(T, 0, device_sm_count() * ctas_backward(nt * rows, ng) * rows).workers * H;
 }
 
 cudaError_t launch_residual_forward(mok_dtype stream, mok_dtype branch, const ResidualParams& p, int* launches,
