@@ -1,0 +1,7 @@
+#include "residual_kernels.cuh"
+
+namespace mok {
+namespace residual {
+template cudaError_t forward_rows<__nv_bfloat16, __nv_bfloat16, true>(const ResidualParams&, cudaStream_t);
+}  // namespace residual
+}  // namespace mok

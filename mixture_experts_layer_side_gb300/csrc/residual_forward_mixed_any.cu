@@ -1,0 +1,7 @@
+#include "residual_kernels.cuh"
+
+namespace mok {
+namespace residual {
+template cudaError_t forward_rows<float, __nv_bfloat16, false>(const ResidualParams&, cudaStream_t);
+}  // namespace residual
+}  // namespace mok
