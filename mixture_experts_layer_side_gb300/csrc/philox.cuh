@@ -19,7 +19,7 @@ struct DropParams {
   uint32_t key0, key1;       // the seed
   uint64_t call;             // number of the call ...
   const int64_t* call_dev;   // ... plus this device word, where it is given
-  uint32_t below;            // p * 65536: elements whose bits are below are dropped; 0: none (dropout off)
+  uint32_t below;            // p * 65536: elements whose bits are below are dropped; 0: dropout is off
   float scale;               // 1 / (1 - p); 0 where all are dropped
 };
 
@@ -40,15 +40,18 @@ __device__ __forceinline__ uint4 philox(uint64_t block, uint64_t call, uint32_t 
   return c;
 }
 
-// Which of the eight elements of a block are kept, element j in bit j.
+// Which of the eight elements of a block are kept, element j in bit j.  Both halves of a word are compared at its
+// upper end, where the bits below them change nothing: 16 bits are not below p * 65536 if what they begin is more than
+// p * 2^32 - 1.
 __device__ __forceinline__ uint32_t drop_keep8(const DropParams& d, uint64_t block, uint64_t call) {
   const uint4 r = philox(block, call, d.key0, d.key1);
   const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+  const uint32_t most = (d.below << 16) - 1u;
   uint32_t keep = 0;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    keep |= (uint32_t)((w[i] & 0xffffu) >= d.below) << (2 * i);
-    keep |= (uint32_t)((w[i] >> 16) >= d.below) << (2 * i + 1);
+    keep |= (w[i] << 16) > most ? 1u << (2 * i) : 0u;
+    keep |= w[i] > most ? 2u << (2 * i) : 0u;
   }
   return keep;
 }

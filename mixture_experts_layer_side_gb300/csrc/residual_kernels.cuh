@@ -811,10 +811,11 @@ inline int stages_ahead(int* ctas, size_t stage, size_t beside) {
   return 0;
 }
 
-// All the teams that the SMs hold, and four rows at least for one of them, so that the parts stay few beside the rows.
+// All the teams that the SMs hold; where there are few rows, four of them at least for a team, so that the parts stay few
+// beside the rows, but teams for four on every SM (64 rows of 7,168 bf16: 16.4 us with four rows each, 9.1 with one).
 inline BackwardPlan backward_plan(int T, int G, int teams, int rows) {
   BackwardPlan b;
-  b.workers = std::max(1, std::min(teams, (T + 3) / 4));
+  b.workers = std::max(1, std::min(teams, std::max((T + 3) / 4, std::min(T, 4 * device_sm_count()))));
   b.groups = std::max(1, G);
   b.split = std::max(1, std::min(b.workers / b.groups, T / b.groups));
   b.own = b.split == 1 && b.groups > 1;
