@@ -2044,9 +2044,10 @@ FfnLayout ffn_layout(int32_t T, int32_t H, int32_t I, bool training) {
   return L;
 }
 
-FfnParams ffn_params(void* ws, int M, int N, int K) {
+FfnParams ffn_params(void* ws, FfnAfter after, int M, int N, int K) {
   FfnParams p;
   memset(&p, 0, sizeof(p));
+  p.after = after;
   p.M = M;
   p.N = N;
   p.K = K;
@@ -2076,12 +2077,12 @@ mok_status ffn_forward(int32_t T, int32_t H, int32_t I, void* ws, const void* x,
                        const void* W2, void* out, __nv_bfloat16* a, __nv_bfloat16* h, __nv_bfloat16* u, void* stream) {
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   Phase ph(MOK_PHASE_FFN_FWD, st, 2);
-  FfnParams p = ffn_params(ws, T, I, H);
+  FfnParams p = ffn_params(ws, FFN_AFTER_ALL, T, I, H);
   p.out[0] = a;
   p.out[1] = h;
   p.out[2] = u;
   MOK_CUDA(launch_ffn(FFN_GATE, {{x, T, H}, {}}, {{W1, H, I}, {W3, H, I}}, p, st));
-  p = ffn_params(ws, T, H, I);
+  p = ffn_params(ws, FFN_READS_IT, T, H, I);
   p.out[0] = static_cast<__nv_bfloat16*>(out);
   MOK_CUDA(launch_ffn(FFN_OUT, {{a, T, I}, {}}, {{W2, I, H}, {}}, p, st));
   return MOK_OK;
@@ -2155,19 +2156,20 @@ mok_status mok_ffn_backward(int32_t T, int32_t H, int32_t I, void* ws, size_t ws
   uint8_t* s = static_cast<uint8_t*>(ws);
   const void* a = c + 2 * n;
   Phase ph(MOK_PHASE_FFN_BWD, st, 4);
-  FfnParams p = ffn_params(ws, T, I, H);
+  // dW2 runs beside da, and dW1 and dW3 beside dx
+  FfnParams p = ffn_params(ws, FFN_AFTER_ALL, T, I, H);
   p.h = reinterpret_cast<const __nv_bfloat16*>(c);
   p.u = reinterpret_cast<const __nv_bfloat16*>(c + n);
   p.out[0] = reinterpret_cast<__nv_bfloat16*>(s + L.dh);
   p.out[1] = reinterpret_cast<__nv_bfloat16*>(s + L.du);
   MOK_CUDA(launch_ffn(FFN_DA, {{dout, T, H}, {}}, {{W2, I, H}, {}}, p, st));
-  p = ffn_params(ws, I, H, T);
+  p = ffn_params(ws, FFN_BESIDE_IT, I, H, T);
   p.out[0] = static_cast<__nv_bfloat16*>(dW2);
   MOK_CUDA(launch_ffn(FFN_DW2, {{a, T, I}, {}}, {{dout, T, H}, {}}, p, st));
-  p = ffn_params(ws, T, H, I);
+  p = ffn_params(ws, FFN_READS_IT, T, H, I);
   p.out[0] = static_cast<__nv_bfloat16*>(dX);
   MOK_CUDA(launch_ffn(FFN_DX, {{s + L.dh, T, I}, {s + L.du, T, I}}, {{W1, H, I}, {W3, H, I}}, p, st));
-  p = ffn_params(ws, H, I, T);
+  p = ffn_params(ws, FFN_BESIDE_IT, H, I, T);
   p.out[0] = static_cast<__nv_bfloat16*>(dW1);
   p.out[1] = static_cast<__nv_bfloat16*>(dW3);
   MOK_CUDA(launch_ffn(FFN_DW13, {{x, T, H}, {}}, {{s + L.dh, T, I}, {s + L.du, T, I}}, p, st));

@@ -16,7 +16,15 @@
 // TMA, which also fills in zeros past their ends: no size has to be a multiple
 // of a tile, only rows of whole 16 bytes are asked for.  Tiles are handed out
 // by their number, and every sum runs along K in one order: results do not
-// depend on timing.
+// depend on timing.  Launches of a pass overlap (programmatic dependent
+// launch): one that reads what the one before it writes has its barriers and
+// TMEM ready when that ends, and one that does not runs beside it.
+//
+// A product of few tiles leaves most SMs idle, and a tile alone takes in no
+// more than six steps of 32 KB a round trip to memory.  Such products run in a
+// second form: a cluster of 4, 8 or 16 CTAs has one tile, each pair a part of
+// K, and the parts' sums are exchanged through the cluster's shared memory, so
+// that every CTA adds and stores a slice of the columns.
 //
 //   warp 0      TMA (both CTAs)
 //   warp 1      TMEM allocation; the leader's issues the MMAs
@@ -99,14 +107,16 @@ __device__ __forceinline__ FfnTile tile_of(const FfnParams& p, int item) {
   return t;
 }
 
-// This CTA's operands of one step along K.
+// This CTA's operands of one step along K.  (A CTA whose rows of the result lie past the last needs no A: whatever its
+// rows of the product are, they are not stored.)
 template <int MODE>
-__device__ __forceinline__ void ffn_loads(const FfnMaps& mp, const FfnTile& t, int kk, int k_half, int rank, uint8_t* a,
-                                          uint8_t* b, uint32_t bar) {
+__device__ __forceinline__ void ffn_loads(const FfnMaps& mp, const FfnTile& t, int kk, int k_half, int rank, bool with_a,
+                                          uint8_t* a, uint8_t* b, uint32_t bar) {
   const int row = t.m * 256 + rank * 128;
   const int second = MODE == FFN_DX && kk >= k_half ? 1 : 0;
   const int k = (kk - second * k_half) * 64;
-  if constexpr (ffn_a_mn(MODE)) {
+  if (!with_a) {
+  } else if constexpr (ffn_a_mn(MODE)) {
     for (int c = 0; c < 2; ++c) tma_load_2d_pair(a + c * 8192, &mp.a[0], bar, row + c * 64, k);
   } else {
     tma_load_2d_pair(a, &mp.a[second], bar, k, row);
@@ -266,6 +276,18 @@ __device__ __forceinline__ bool ffn_epilogue(const FfnParams& p, const FfnTile& 
   return true;
 }
 
+// A launch's place in the stream (all threads), and from here on the next one may start where there is room: what that may
+// read without waiting stands.
+__device__ __forceinline__ void launch_in_turn(const FfnParams& p) {
+  if (p.after == FFN_READS_IT) griddep_wait();
+  griddep_launch_dependents();
+}
+
+// Bytes of a step that both CTAs of a pair bring: their halves of B, and A where they have rows of the result.
+__device__ __forceinline__ uint32_t step_bytes(const FfnParams& p, const FfnTile& t) {
+  return kFfnOperandBytes * (t.m * 256 + 128 < p.M ? 4u : 3u);
+}
+
 // ------------------------------------------------------------------ kernel
 template <int MODE>
 __global__ void __launch_bounds__(kFfnThreads, 1) ffn_kernel(const __grid_constant__ FfnMaps maps, const FfnParams p) {
@@ -310,6 +332,7 @@ __global__ void __launch_bounds__(kFfnThreads, 1) ffn_kernel(const __grid_consta
   cluster_sync();  // both CTAs' barriers stand before either signals the other's
   tc_fence_after();
   const uint32_t tmem = ctl->tmem_base;
+  launch_in_turn(p);
 
   if (warp == 0) {
     if (lane == 0) {
@@ -317,11 +340,12 @@ __global__ void __launch_bounds__(kFfnThreads, 1) ffn_kernel(const __grid_consta
       bool ok = true;
       for (int item = first; ok && item < items; item += step) {
         const FfnTile t = tile_of<MODE>(p, item);
+        const bool with_a = t.m * 256 + rank * 128 < p.M;
         for (int kk = 0; kk < k_iters; ++kk) {
           if (!mbar_wait(&ctl->empty[stage], phase ^ 1, wc)) { ok = false; break; }
           // (the leader's barrier counts both CTAs' bytes)
-          if (rank == 0) mbar_arrive_expect_tx(&ctl->full[stage], 2 * kFfnStageBytes);
-          ffn_loads<MODE>(maps, t, kk, k_half, rank, sA + stage * kFfnOperandBytes, sB + stage * kFfnOperandBytes,
+          if (rank == 0) mbar_arrive_expect_tx(&ctl->full[stage], step_bytes(p, t));
+          ffn_loads<MODE>(maps, t, kk, k_half, rank, with_a, sA + stage * kFfnOperandBytes, sB + stage * kFfnOperandBytes,
                           mapa_shared(&ctl->full[stage], 0));
           if (++stage == kFfnStages) { stage = 0; phase ^= 1; }
         }
@@ -393,9 +417,211 @@ __global__ void __launch_bounds__(kFfnThreads, 1) ffn_kernel(const __grid_consta
   cluster_sync();
   tc_fence_after();
   if (warp == 1) tmem_dealloc_pair(tmem, 512);
+  // (what comes after this launch comes after the one before it too)
+  if (p.after == FFN_BESIDE_IT) griddep_wait();
+}
+
+// ------------------------------------------------------------------ kernel, few tiles
+// S pairs of CTAs share a tile: pair i sums the i-th part of K.  Nothing in it loops over tiles, and every thread comes
+// to every cluster barrier, whether a wait gave up or not.
+//
+// After the sums: each warp of the epilogue sends its 32 rows x 128 columns to the CTAs of its rank that add them, as
+// fours of columns by rows, [part][column / 4 of the slice][row]; these then add the parts in the order of K.  FFN_GATE:
+// a slice is as many columns of h and the same of u.
+struct FfnFewCtl {
+  uint64_t full[kFfnStages];
+  uint64_t empty[kFfnStages];
+  uint64_t done;
+  uint32_t tmem_base;
+  int abort;
+};
+static_assert(sizeof(FfnFewCtl) <= sizeof(FfnCtl), "the control block's place");
+
+template <int MODE>
+__device__ __forceinline__ void few_store4(const FfnParams& p, const FfnTile& t, int row, int col, const float4& v, const float4& w) {
+  // col: within the tile's columns; (rows and sizes are in whole fours)
+  const float x[4] = {v.x, v.y, v.z, v.w}, y[4] = {w.x, w.y, w.z, w.w};
+  const int c = t.n * ffn_tile_n(MODE) + col;
+  if (c >= p.N) return;
+  const long at = (long)row * p.N + c;
+  auto put = [&](__nv_bfloat16* dst, const float (&f)[4]) {
+    *reinterpret_cast<uint2*>(dst + at) = make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]));
+  };
+  if constexpr (MODE == FFN_GATE) {
+    float a[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) a[i] = x[i] * ffn_sigmoid(x[i]) * y[i];
+    put(p.out[0], a);
+    if (p.out[1]) {
+      put(p.out[1], x);
+      put(p.out[2], y);
+    }
+  } else if constexpr (MODE == FFN_DA) {
+    const uint2 hw = *reinterpret_cast<const uint2*>(p.h + at), uw = *reinterpret_cast<const uint2*>(p.u + at);
+    const float h[4] = {lo_f32(hw.x), hi_f32(hw.x), lo_f32(hw.y), hi_f32(hw.y)};
+    const float u[4] = {lo_f32(uw.x), hi_f32(uw.x), lo_f32(uw.y), hi_f32(uw.y)};
+    float dh[4], du[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float sg = ffn_sigmoid(h[i]);
+      dh[i] = x[i] * u[i] * sg * (1.0f + h[i] * (1.0f - sg));
+      du[i] = x[i] * (h[i] * sg);
+    }
+    put(p.out[0], dh);
+    put(p.out[1], du);
+  } else {
+    put(MODE == FFN_DW13 && t.which ? p.out[1] : p.out[0], x);
+  }
+}
+
+template <int MODE, int S>
+__global__ void __launch_bounds__(kFfnThreads, 1) ffn_few_kernel(const __grid_constant__ FfnMaps maps, const FfnParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sA = base;
+  uint8_t* sB = sA + kFfnStages * kFfnOperandBytes;
+  FfnFewCtl* ctl = reinterpret_cast<FfnFewCtl*>(sB + kFfnStages * kFfnOperandBytes + kFfnEpilogueWarps * kFfnOutStage);
+  // where the parts of this CTA's slice arrive: the stages' place, once their last MMAs are done
+  float4* sums = reinterpret_cast<float4*>(base);
+  constexpr int kSlice4 = 64 / S;  // fours of columns in a slice, of 64 of the tile
+  static_assert(S * kSlice4 * 128 * 16 <= kFfnStages * kFfnStageBytes, "a slice's parts where the stages were");
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const WaitCtx wc{&ctl->abort, &p.hdr[kHdrAbort], &p.hdr[kHdrError]};
+  const int cta = (int)cluster_ctarank(), rank = cta & 1, part = cta >> 1;
+  const FfnTile t = tile_of<MODE>(p, blockIdx.x / (2 * S));
+  const int k_half = ceil_div(p.K, 64), k_iters = MODE == FFN_DX ? 2 * k_half : k_half;
+  const int k0 = k_iters * part / S, steps = k_iters * (part + 1) / S - k0;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kFfnStages; ++i) {
+      mbar_init(&ctl->full[i], 1);
+      mbar_init(&ctl->empty[i], 1);
+    }
+    mbar_init(&ctl->done, 1);
+    ctl->abort = 0;
+    ctl->tmem_base = 0;
+    fence_mbar_init();
+    if (blockIdx.x == 0 && *reinterpret_cast<volatile int*>(&p.hdr[kHdrAbort])) atomicOr(&p.hdr[kHdrError], MOK_ERRBIT_TIMEOUT);
+  }
+  if (warp == 0 && lane < 2) {
+    tma_prefetch_desc(&maps.a[lane]);
+    tma_prefetch_desc(&maps.b[lane]);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(&ctl->tmem_base, 256);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // all barriers stand before any CTA signals another's
+  tc_fence_after();
+  const uint32_t tmem = ctl->tmem_base;
+  launch_in_turn(p);
+
+  bool ok = true;
+  if (warp == 0) {
+    if (lane == 0) {
+      const bool with_a = t.m * 256 + rank * 128 < p.M;
+      for (int i = 0; i < steps; ++i) {
+        const int stage = i % kFfnStages;
+        if (i >= kFfnStages && !mbar_wait(&ctl->empty[stage], (uint32_t)(i / kFfnStages - 1) & 1, wc)) { ok = false; break; }
+        if (rank == 0) mbar_arrive_expect_tx(&ctl->full[stage], step_bytes(p, t));
+        ffn_loads<MODE>(maps, t, k0 + i, k_half, rank, with_a, sA + stage * kFfnOperandBytes, sB + stage * kFfnOperandBytes,
+                        mapa_shared(&ctl->full[stage], (uint32_t)(cta & ~1)));
+      }
+      // (after a timeout: copies in flight land before the shared memory serves again)
+      if (!ok) {
+        const uint64_t t0 = globaltimer();
+        for (int j = 0; j < kFfnStages; ++j) {
+          const uint64_t spent = globaltimer() - t0;
+          if (spent < kFfnDrainNs) mbar_drain(&ctl->full[j], 0, kFfnDrainNs - spent);
+        }
+      }
+    }
+  } else if (warp == 1 && rank == 0) {
+    constexpr uint32_t idesc = idesc_bf16(256, 256, ffn_a_mn(MODE) ? 1 : 0, ffn_b_mn(MODE) ? 1 : 0);
+    for (int i = 0; i < steps; ++i) {
+      const int stage = i % kFfnStages;
+      if (!mbar_wait(&ctl->full[stage], (uint32_t)(i / kFfnStages) & 1, wc)) { ok = false; break; }
+      tc_fence_after();
+      if (lane == 0) {
+        const uint32_t a0 = smem_u32(sA + stage * kFfnOperandBytes), b0 = smem_u32(sB + stage * kFfnOperandBytes);
+#pragma unroll
+        for (int k16 = 0; k16 < 4; ++k16) {
+          const uint64_t ad = ffn_a_mn(MODE) ? sdesc_sw128(a0 + k16 * 2048, 8192, 1024) : sdesc_sw128(a0 + k16 * 32, 16, 1024);
+          const uint64_t bd = ffn_b_mn(MODE) ? sdesc_sw128(b0 + k16 * 2048, 8192, 1024) : sdesc_sw128(b0 + k16 * 32, 16, 1024);
+          mma_bf16_pair(tmem, ad, bd, idesc, (i | k16) != 0 ? 1u : 0u);
+        }
+        mma_commit_pair(&ctl->empty[stage], 3u << (cta & ~1));
+      }
+      __syncwarp();
+    }
+    if (lane == 0) mma_commit_pair(&ctl->done, 3u << (cta & ~1));
+    __syncwarp();
+  }
+  // every MMA of the pair is done: the sums stand, the stages are free
+  const int q = warp & 3, half = (warp - 2) >> 2;  // epilogue warps: TMEM lanes that this warp may read; columns it takes
+  const bool summed = mbar_wait(&ctl->done, 0, wc);
+  tc_fence_after();
+  cluster_sync();
+  const int row0 = t.m * 256 + rank * 128;
+  if (warp >= 2 && summed && row0 + q * 32 < p.M) {
+    const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16);
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i) {
+      // 32 columns, in the tile's order of fours: 0 to 63 (FFN_GATE: h and then u)
+      const int col = half * 128 + i * 32;
+      float v[32];
+      tmem_ld32(acc + col, v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int c4 = col / 4 + j;
+        // whose slice: FFN_GATE has half of a slice of h and half of u
+        int owner, in_slice;
+        if (MODE == FFN_GATE) {
+          owner = (c4 & 31) / (kSlice4 / 2);
+          in_slice = (c4 >> 5) * (kSlice4 / 2) + (c4 & 31) % (kSlice4 / 2);
+        } else {
+          owner = c4 / kSlice4;
+          in_slice = c4 % kSlice4;
+        }
+        const uint32_t to = mapa_shared(sums + (part * kSlice4 + in_slice) * 128 + q * 32 + lane, (uint32_t)(2 * owner + rank));
+        asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(to), "f"(v[4 * j]), "f"(v[4 * j + 1]),
+                     "f"(v[4 * j + 2]), "f"(v[4 * j + 3])
+                     : "memory");
+      }
+    }
+  }
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc_pair(tmem, 256);
+  if (warp >= 2 && summed) {
+    constexpr int kPer = MODE == FFN_GATE ? kSlice4 / 2 : kSlice4;  // fours of results in a slice
+    const int rows = min(128, p.M - row0);
+    for (int i = threadIdx.x - 64; i < 128 * kPer; i += 32 * kFfnEpilogueWarps) {
+      const int row = i & 127, c = i >> 7;
+      if (row >= rows) continue;
+      auto add = [&](int at) {
+        float4 s = sums[at * 128 + row];
+#pragma unroll
+        for (int j = 1; j < S; ++j) {
+          const float4 w = sums[(j * kSlice4 + at) * 128 + row];
+          s.x += w.x, s.y += w.y, s.z += w.z, s.w += w.w;
+        }
+        return s;
+      };
+      const float4 v = add(c), w = MODE == FFN_GATE ? add(kPer + c) : v;
+      few_store4<MODE>(p, t, row0 + row, (part * kPer + c) * 4, v, w);
+    }
+  }
+  if (p.after == FFN_BESIDE_IT) griddep_wait();
 }
 
 // ------------------------------------------------------------------ launches
+// Steps along K that a pair's part has at least.
+constexpr int kFfnPartSteps = 2;
+
 // Rows along K: boxes of 128 rows x 64 of K; along M or N: 64 of K x 64.
 bool operand_map(CUtensorMap* m, const FfnOperand& o, bool mn) {
   const uint64_t dims[2] = {(uint64_t)o.cols, (uint64_t)o.rows};
@@ -404,38 +630,77 @@ bool operand_map(CUtensorMap* m, const FfnOperand& o, bool mn) {
   return make_tmap(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, o.p, dims, str, box, true);
 }
 
+// What the device holds of a kernel's clusters at once, asked for once per device (`held`: a number per device, the
+// kernel's own), and its shared memory allowed.
+cudaError_t clusters_held(const void* kernel, const cudaLaunchConfig_t& cfg, std::atomic<int>* held, int* clusters) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  *clusters = dev < 64 ? held[dev].load(std::memory_order_relaxed) : 0;
+  if (*clusters) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kFfnSmem);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(clusters, kernel, &cfg);
+  if (e != cudaSuccess) return e;
+  if (*clusters < 1) *clusters = -1;  // (none: known from here on)
+  if (dev < 64) held[dev].store(*clusters, std::memory_order_relaxed);
+  return cudaSuccess;
+}
+
+struct FfnLaunch {
+  cudaLaunchConfig_t cfg;
+  cudaLaunchAttribute attr[2];
+};
+void prepare(FfnLaunch* l, const FfnParams& p, int cluster, unsigned grid, cudaStream_t st) {
+  l->cfg = {};
+  l->attr[0].id = cudaLaunchAttributeClusterDimension;
+  l->attr[0].val.clusterDim.x = (unsigned)cluster;
+  l->attr[0].val.clusterDim.y = 1;
+  l->attr[0].val.clusterDim.z = 1;
+  l->attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  l->attr[1].val.programmaticStreamSerializationAllowed = 1;
+  l->cfg.gridDim = dim3(grid);
+  l->cfg.blockDim = dim3(kFfnThreads);
+  l->cfg.dynamicSmemBytes = kFfnSmem;
+  l->cfg.stream = st;
+  l->cfg.attrs = l->attr;
+  l->cfg.numAttrs = p.after == FFN_AFTER_ALL ? 1 : 2;
+}
+
+// The tile of a cluster of 2 S CTAs, if the device holds as many as there are tiles (*done: whether it was launched).
+template <int MODE, int S>
+cudaError_t launch_few_tiles(const FfnMaps& maps, const FfnParams& p, int tiles, int k_iters, bool* done, cudaStream_t st) {
+  *done = false;
+  if (tiles * 2 * S > device_sm_count() || k_iters < S * kFfnPartSteps) return cudaSuccess;
+  static std::atomic<int> held[64];
+  FfnLaunch l;
+  prepare(&l, p, 2 * S, 2u * S * (unsigned)tiles, st);
+  int clusters = 0;
+  const cudaError_t e = clusters_held((const void*)ffn_few_kernel<MODE, S>, l.cfg, held, &clusters);
+  if (e != cudaSuccess) return e;
+  if (clusters < tiles) return cudaSuccess;
+  *done = true;
+  return cudaLaunchKernelEx(&l.cfg, ffn_few_kernel<MODE, S>, maps, p);
+}
+
 template <int MODE>
 cudaError_t launch_mode(const FfnMaps& maps, const FfnParams& p, cudaStream_t st) {
-  static std::atomic<uint64_t> allowed{0};
-  cudaError_t e = allow_smem((const void*)ffn_kernel<MODE>, kFfnSmem, allowed);
-  if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.gridDim = dim3((unsigned)device_sm_count() & ~1u);
-  cfg.blockDim = dim3(kFfnThreads);
-  cfg.dynamicSmemBytes = kFfnSmem;
-  cfg.stream = st;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  // clusters that the device holds at once, asked for once per device
+  const int tiles = ceil_div(p.M, 256) * ceil_div(p.N, ffn_tile_n(MODE)) * (MODE == FFN_DW13 ? 2 : 1);
+  const int k_iters = ceil_div(p.K, 64) * (MODE == FFN_DX ? 2 : 1);
+  bool done;
+  cudaError_t e = launch_few_tiles<MODE, 8>(maps, p, tiles, k_iters, &done, st);
+  if (e == cudaSuccess && !done) e = launch_few_tiles<MODE, 4>(maps, p, tiles, k_iters, &done, st);
+  if (e == cudaSuccess && !done) e = launch_few_tiles<MODE, 2>(maps, p, tiles, k_iters, &done, st);
+  if (e != cudaSuccess || done) return e;
   static std::atomic<int> held[64];
-  int dev = 0;
-  e = cudaGetDevice(&dev);
+  FfnLaunch l;
+  prepare(&l, p, 2, (unsigned)device_sm_count() & ~1u, st);
+  int clusters = 0;
+  e = clusters_held((const void*)ffn_kernel<MODE>, l.cfg, held, &clusters);
   if (e != cudaSuccess) return e;
-  int clusters = dev < 64 ? held[dev].load(std::memory_order_relaxed) : 0;
-  if (clusters == 0) {
-    e = cudaOccupancyMaxActiveClusters(&clusters, ffn_kernel<MODE>, &cfg);
-    if (e != cudaSuccess) return e;
-    if (clusters < 1) return cudaErrorNotSupported;
-    if (dev < 64) held[dev].store(clusters, std::memory_order_relaxed);
-  }
-  const int n = ceil_div(p.N, ffn_tile_n(MODE)) * (MODE == FFN_DW13 ? 2 : 1);
-  cfg.gridDim = dim3(2u * (unsigned)std::min<long>((long)ceil_div(p.M, 256) * n, clusters));
-  return cudaLaunchKernelEx(&cfg, ffn_kernel<MODE>, maps, p);
+  if (clusters < 1) return cudaErrorNotSupported;
+  l.cfg.gridDim = dim3(2u * (unsigned)std::min(tiles, clusters));
+  return cudaLaunchKernelEx(&l.cfg, ffn_kernel<MODE>, maps, p);
 }
 
 }  // namespace
@@ -445,8 +710,10 @@ cudaError_t launch_ffn(FfnMode mode, const FfnOperand (&a)[2], const FfnOperand 
   FfnMaps maps;
   memset(&maps, 0, sizeof(maps));
   for (int i = 0; i < 2; ++i) {
-    if (!operand_map(&maps.a[i], a[i].p ? a[i] : a[0], ffn_a_mn(mode))) return cudaErrorInvalidValue;
-    if (!operand_map(&maps.b[i], b[i].p ? b[i] : b[0], ffn_b_mn(mode))) return cudaErrorInvalidValue;
+    if (!a[i].p) maps.a[i] = maps.a[0];
+    else if (!operand_map(&maps.a[i], a[i], ffn_a_mn(mode))) return cudaErrorInvalidValue;
+    if (!b[i].p) maps.b[i] = maps.b[0];
+    else if (!operand_map(&maps.b[i], b[i], ffn_b_mn(mode))) return cudaErrorInvalidValue;
   }
   switch (mode) {
     case FFN_GATE: return launch_mode<FFN_GATE>(maps, p, st);

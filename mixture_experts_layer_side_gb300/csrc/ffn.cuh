@@ -21,6 +21,14 @@ struct FfnParams {
   int32_t* hdr;    // workspace header: error and abort words
   __nv_bfloat16* out[3];        // FFN_GATE: a, h, u (h, u may be null); FFN_DA: dh, du; FFN_DW13: dW1, dW3; else [0]
   const __nv_bfloat16 *h, *u;   // FFN_DA
+  int after;       // FfnAfter
+};
+
+// How a launch stands to the one before it in the stream.
+enum FfnAfter : int {
+  FFN_AFTER_ALL = 0,   // an ordinary launch
+  FFN_READS_IT = 1,    // starts beside it, waits for its end before it reads anything
+  FFN_BESIDE_IT = 2,   // reads nothing that it writes: waits for its end at its own end
 };
 
 struct FfnOperand {

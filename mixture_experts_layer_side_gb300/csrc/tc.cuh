@@ -376,11 +376,12 @@ __device__ __forceinline__ void mma_bf16_pair(uint32_t d_tmem, uint64_t a_desc, 
 
 // Arrive on the mbarrier at this smem offset in both CTAs of the pair once
 // the leader's MMAs issued so far have completed.
-__device__ __forceinline__ void mma_commit_pair(uint64_t* bar) {
+// (`ctas`: the pair's ranks in its cluster, a bit each)
+__device__ __forceinline__ void mma_commit_pair(uint64_t* bar, uint32_t ctas = 3) {
   asm volatile(
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
           smem_u32(bar)),
-      "h"((uint16_t)3)
+      "h"((uint16_t)ctas)
       : "memory");
 }
 
