@@ -777,14 +777,13 @@ mok_status mok_residual_backward(const mok_residual* r, const void* x, int64_t l
  *   ctx               (device) mok_ffn_ctx_size() bytes: h, u and a, which the
  *                     forward keeps for the backward
  *
- *   mok_ffn_infer     out alone.  Up to MOK_FEW_MAX_TOKENS tokens with H and I
- *                     multiples of 128 (and at most MOK_FEW_MAX_HIDDEN) run as mok_few_forward
- *                     does, at the rate of the weights' read; else as mok_ffn_forward
+ *   mok_ffn_infer     out alone.  A few tokens (T <= 4) stream the weights
+ *                     through every SM at once; more run as mok_ffn_forward
  *   mok_ffn_forward   out and ctx
  *   mok_ffn_backward  all four gradients, of the same x and weights
  * Sums are f32.  a comes from the f32 h and u and is rounded to bf16 for the
- * second product (few tokens: to two bf16); h, u, dh and du are rounded to bf16 where
- * the backward reads them.  H and I are multiples of 8, at most
+ * second product (a few tokens': not at all); h, u, dh and du are rounded to
+ * bf16 where the backward reads them.  H and I are multiples of 8, at most
  * MOK_FFN_MAX_SIZE; T <= 2^22; T = 0 gives zero gradients of the weights.
  * Tensors start at 16-byte boundaries; outputs share no byte with inputs
  * or each other.  Results do not depend on timing: the same call gives the

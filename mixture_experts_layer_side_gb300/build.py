@@ -18,7 +18,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(HERE, "libmok.so")
 SOURCES = ["api.cu", "schedule.cu", "elementwise.cu", "gemm.cu", "mxfp8.cu", "router.cu", "ep.cu", "few.cu", "distill.cu",
-           "embed.cu", "residual.cu", "dropout.cu", "ffn.cu"]
+           "embed.cu", "residual.cu", "dropout.cu", "ffn.cu", "ffn_rows.cu"]
 SOURCES += [f"residual_{way}_{types}_{rows}.cu" for way in ("forward", "backward") for types in ("bf16", "mixed", "f32")
             for rows in ("aligned", "any")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

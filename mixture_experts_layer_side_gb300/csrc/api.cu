@@ -2020,27 +2020,17 @@ mok_status check_ffn(int32_t T, int32_t H, int32_t I) {
   return H % 8 || I % 8 || H > MOK_FFN_MAX_SIZE || I > MOK_FFN_MAX_SIZE || T > (1 << 22) ? MOK_ERR_UNSUPPORTED : MOK_OK;
 }
 
-// Whether the few-token kernel takes such weights, as one expert's.
-bool ffn_few_sizes(int32_t H, int32_t I) {
-  return H % 128 == 0 && I % 128 == 0 && H <= MOK_FEW_MAX_HIDDEN && I <= MOK_FEW_MAX_HIDDEN;
-}
-
-// The few-token call's share of the workspace comes first: its counters, zero between calls, are at the same
-// place for every T.  Then a (infer) or dh and du (backward).
+// The header, then a (infer) or dh and du (backward).
 struct FfnLayout {
   size_t a, dh, du, total;
 };
 FfnLayout ffn_layout(int32_t T, int32_t H, int32_t I, bool training) {
   FfnLayout L;
-  size_t off = kHeaderWords * 4;
-  if (ffn_few_sizes(H, I)) {
-    const mok_shape s = {std::min(std::max(T, 1), (int32_t)MOK_FEW_MAX_TOKENS), H, I, 1, 1};
-    off = few_layout(s, MOK_BF16).total;
-  }
-  const size_t n = align256((size_t)T * I * 2);
-  L.a = L.dh = off;
-  L.du = off + n;
-  L.total = off + (training ? 2 : 1) * n;
+  // (a of a few tokens is f32)
+  const size_t n = align256((size_t)std::max(T, 2 * std::min(T, (int32_t)kFfnRows)) * I * 2);
+  L.a = L.dh = kHeaderWords * 4;
+  L.du = L.dh + n;
+  L.total = L.dh + (training ? 2 : 1) * n;
   return L;
 }
 
@@ -2106,16 +2096,13 @@ mok_status mok_ffn_infer(int32_t T, int32_t H, int32_t I, void* ws, size_t ws_by
   const size_t rows = (size_t)T * H * 2, w = (size_t)H * I * 2;
   MOK_TRY(check_spans({{x, rows}, {W1, w}, {W3, w}, {W2, w}, {out, rows, true}, {ws, L.total, true}}));
   if (ws_bytes < L.total) return MOK_ERR_WORKSPACE_TOO_SMALL;
-  if (T <= MOK_FEW_MAX_TOKENS && ffn_few_sizes(H, I)) {
-    const mok_shape s = {T, H, I, 1, 1};
-    FewParams p;
-    MOK_TRY(few_params(s, MOK_BF16, ws, ws_bytes, x, W1, W3, W2, out, &p));
+  if (ffn_rows_take(T, H, I)) {
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    Phase ph(MOK_PHASE_FFN_FWD, st, 0);
-    int launches = 0;
-    const cudaError_t e = launch_few(p, false, &launches, st);
-    g_launches += launches;
-    return e == cudaSuccess ? MOK_OK : MOK_ERR_CUDA;
+    Phase ph(MOK_PHASE_FFN_FWD, st, 2);
+    return launch_ffn_rows(T, H, I, x, W1, W3, W2, reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + L.a), out, st) ==
+                   cudaSuccess
+               ? MOK_OK
+               : MOK_ERR_CUDA;
   }
   return ffn_forward(T, H, I, ws, x, W1, W3, W2, out, reinterpret_cast<__nv_bfloat16*>(static_cast<uint8_t*>(ws) + L.a),
                      nullptr, nullptr, stream);

@@ -485,7 +485,7 @@ __device__ void build_units(const FewParams& p, const Schedule& s, uint8_t* scra
   for (int f0 = threadIdx.x; f0 < R; f0 += 4 * nthreads) {
     int e[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) e[i] = p.idx && f0 + i * nthreads < R ? __ldcg(p.idx + f0 + i * nthreads) : 0;
+    for (int i = 0; i < 4; ++i) e[i] = f0 + i * nthreads < R ? __ldcg(p.idx + f0 + i * nthreads) : 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int f = f0 + i * nthreads;
@@ -765,7 +765,7 @@ __device__ __forceinline__ void combine(const FewParams& p, const Schedule& s, c
 #pragma unroll
       for (int m = 0; m < EACH; ++m) {
         const float4 none = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        w[m] = more[m] < 0 ? 0.0f : p.scores ? p.scores[t * p.k + j0 + sub + m] : 1.0f;
+        w[m] = more[m] >= 0 ? p.scores[t * p.k + j0 + sub + m] : 0.0f;
         y[m] = more[m] >= 0 ? __ldcg(from[m]) : none;
         z[m] = more[m] > 0 ? __ldcg(next[m]) : none;
       }
@@ -833,14 +833,14 @@ __global__ void __launch_bounds__(MX ? 448 : 384, 1) few_kernel(const __grid_con
   WaitCtx wc{&ctl->abort, p.hdr + kHdrAbort, p.hdr + kHdrError};
 
   // what the routing and the first tiles need soon, on its way from memory meanwhile
-  const int early_id = !p.Wr && warp == 0 && lane < R ? (p.idx ? __ldg(p.idx + lane) : 0) : -1;
+  const int early_id = !p.Wr && warp == 0 && lane < R ? __ldg(p.idx + lane) : -1;
   // a call that timed out left the abort word set: this one's results cannot be trusted either
   const int stale = c == 0 && threadIdx.x == 0 ? __ldcg(p.hdr + kHdrAbort) : 0;
   {
     const char* a = reinterpret_cast<const char*>(p.x);
     const long bytes = (long)p.T * p.H * 2, at = ((long)blockIdx.x * kThreads + threadIdx.x) * 128;
     if (at < bytes) asm volatile("prefetch.global.L2 [%0];" ::"l"(a + at));
-    if (!p.Wr && p.idx && R > 32 && threadIdx.x * 32 < R) asm volatile("prefetch.global.L2 [%0];" ::"l"(p.idx + threadIdx.x * 32));
+    if (!p.Wr && R > 32 && threadIdx.x * 32 < R) asm volatile("prefetch.global.L2 [%0];" ::"l"(p.idx + threadIdx.x * 32));
     if (blockIdx.x == 0 && p.bias && threadIdx.x * 32 < p.E)
       asm volatile("prefetch.global.L2 [%0];" ::"l"(p.bias + threadIdx.x * 32));
   }

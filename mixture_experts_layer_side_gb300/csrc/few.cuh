@@ -42,8 +42,8 @@ struct FewParams {
   int32_t* tile_count;  // [units, I/128]
   int max_units;        // capacity of the unit table
   const __nv_bfloat16* x;
-  const int32_t* idx;   // null without a router: one expert, every token its own
-  const float* scores;  // null: 1
+  const int32_t* idx;
+  const float* scores;
   // weights: bf16, or E4M3 codes with E8M0 scales sf*
   const void *W1, *W3, *W2;
   const uint8_t *sf1, *sf3, *sf2;

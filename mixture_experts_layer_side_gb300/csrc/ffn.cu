@@ -66,7 +66,7 @@ struct FfnCtl {
 };
 
 constexpr size_t kFfnSmem =
-    1024 + kFfnStages * kFfnStageBytes + kFfnEpilogueWarps * kFfnOutStage + (sizeof(FfnCtl) + 127) / 128 * 128;
+    1024 + kFfnStages * kFfnStageBytes + kFfnEpilogueWarps * kFfnOutStage + 256;
 static_assert(kFfnSmem <= 227 * 1024, "shared memory of an SM");
 
 // Whether an operand's rows run along M or N (and not along K).
@@ -284,8 +284,8 @@ __device__ __forceinline__ void launch_in_turn(const FfnParams& p) {
 }
 
 // Bytes of a step that both CTAs of a pair bring: their halves of B, and A where they have rows of the result.
-__device__ __forceinline__ uint32_t step_bytes(const FfnParams& p, const FfnTile& t) {
-  return kFfnOperandBytes * (t.m * 256 + 128 < p.M ? 4u : 3u);
+__device__ __forceinline__ uint32_t step_bytes(const FfnParams& p, const FfnTile& t, uint32_t a_bytes = kFfnOperandBytes) {
+  return 2 * kFfnOperandBytes + a_bytes * (t.m * 256 + 128 < p.M ? 2u : 1u);
 }
 
 // ------------------------------------------------------------------ kernel
@@ -344,7 +344,7 @@ __global__ void __launch_bounds__(kFfnThreads, 1) ffn_kernel(const __grid_consta
         for (int kk = 0; kk < k_iters; ++kk) {
           if (!mbar_wait(&ctl->empty[stage], phase ^ 1, wc)) { ok = false; break; }
           // (the leader's barrier counts both CTAs' bytes)
-          if (rank == 0) mbar_arrive_expect_tx(&ctl->full[stage], step_bytes(p, t));
+          if (rank == 0) mbar_arrive_expect_tx(&ctl->full[stage], step_bytes(p, t, p.a_rows * 128));
           ffn_loads<MODE>(maps, t, kk, k_half, rank, with_a, sA + stage * kFfnOperandBytes, sB + stage * kFfnOperandBytes,
                           mapa_shared(&ctl->full[stage], 0));
           if (++stage == kFfnStages) { stage = 0; phase ^= 1; }
@@ -428,14 +428,18 @@ __global__ void __launch_bounds__(kFfnThreads, 1) ffn_kernel(const __grid_consta
 // After the sums: each warp of the epilogue sends its 32 rows x 128 columns to the CTAs of its rank that add them, as
 // fours of columns by rows, [part][column / 4 of the slice][row]; these then add the parts in the order of K.  FFN_GATE:
 // a slice is as many columns of h and the same of u.
+//
+// A product with no more than 128 rows brings as much of A as it has: its stages are shorter, and more of them are on
+// their way (1 token, H 7168, I 2048: ten of 18 KB in place of six of 32).
+constexpr int kFfnMostStages = 10;
 struct FfnFewCtl {
-  uint64_t full[kFfnStages];
-  uint64_t empty[kFfnStages];
+  uint64_t full[kFfnMostStages];
+  uint64_t empty[kFfnMostStages];
   uint64_t done;
   uint32_t tmem_base;
   int abort;
 };
-static_assert(sizeof(FfnFewCtl) <= sizeof(FfnCtl), "the control block's place");
+static_assert(sizeof(FfnFewCtl) <= 256 && sizeof(FfnCtl) <= 256, "the control block's place");
 
 template <int MODE>
 __device__ __forceinline__ void few_store4(const FfnParams& p, const FfnTile& t, int row, int col, const float4& v, const float4& w) {
@@ -478,9 +482,12 @@ template <int MODE, int S>
 __global__ void __launch_bounds__(kFfnThreads, 1) ffn_few_kernel(const __grid_constant__ FfnMaps maps, const FfnParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* sA = base;
-  uint8_t* sB = sA + kFfnStages * kFfnOperandBytes;
-  FfnFewCtl* ctl = reinterpret_cast<FfnFewCtl*>(sB + kFfnStages * kFfnOperandBytes + kFfnEpilogueWarps * kFfnOutStage);
+  const uint32_t a_slot = p.a_rows * 128, slot = a_slot + kFfnOperandBytes;
+  const int stages = min(kFfnMostStages, (int)(kFfnStages * kFfnStageBytes / slot));
+  // (B first: an MMA reads 128 rows of A, past what is there, rows whose sums no one wants)
+  uint8_t* sB = base;
+  uint8_t* sA = sB + stages * kFfnOperandBytes;
+  FfnFewCtl* ctl = reinterpret_cast<FfnFewCtl*>(base + kFfnStages * kFfnStageBytes + kFfnEpilogueWarps * kFfnOutStage);
   // where the parts of this CTA's slice arrive: the stages' place, once their last MMAs are done
   float4* sums = reinterpret_cast<float4*>(base);
   constexpr int kSlice4 = 64 / S;  // fours of columns in a slice, of 64 of the tile
@@ -493,7 +500,7 @@ __global__ void __launch_bounds__(kFfnThreads, 1) ffn_few_kernel(const __grid_co
   const int k0 = k_iters * part / S, steps = k_iters * (part + 1) / S - k0;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kFfnStages; ++i) {
+    for (int i = 0; i < stages; ++i) {
       mbar_init(&ctl->full[i], 1);
       mbar_init(&ctl->empty[i], 1);
     }
@@ -522,17 +529,18 @@ __global__ void __launch_bounds__(kFfnThreads, 1) ffn_few_kernel(const __grid_co
   if (warp == 0) {
     if (lane == 0) {
       const bool with_a = t.m * 256 + rank * 128 < p.M;
+      uint32_t stage = 0, phase = 0;
       for (int i = 0; i < steps; ++i) {
-        const int stage = i % kFfnStages;
-        if (i >= kFfnStages && !mbar_wait(&ctl->empty[stage], (uint32_t)(i / kFfnStages - 1) & 1, wc)) { ok = false; break; }
-        if (rank == 0) mbar_arrive_expect_tx(&ctl->full[stage], step_bytes(p, t));
-        ffn_loads<MODE>(maps, t, k0 + i, k_half, rank, with_a, sA + stage * kFfnOperandBytes, sB + stage * kFfnOperandBytes,
+        if (!mbar_wait(&ctl->empty[stage], phase ^ 1, wc)) { ok = false; break; }
+        if (rank == 0) mbar_arrive_expect_tx(&ctl->full[stage], step_bytes(p, t, a_slot));
+        ffn_loads<MODE>(maps, t, k0 + i, k_half, rank, with_a, sA + stage * a_slot, sB + stage * kFfnOperandBytes,
                         mapa_shared(&ctl->full[stage], (uint32_t)(cta & ~1)));
+        if ((int)++stage == stages) { stage = 0; phase ^= 1; }
       }
       // (after a timeout: copies in flight land before the shared memory serves again)
       if (!ok) {
         const uint64_t t0 = globaltimer();
-        for (int j = 0; j < kFfnStages; ++j) {
+        for (int j = 0; j < stages; ++j) {
           const uint64_t spent = globaltimer() - t0;
           if (spent < kFfnDrainNs) mbar_drain(&ctl->full[j], 0, kFfnDrainNs - spent);
         }
@@ -540,12 +548,12 @@ __global__ void __launch_bounds__(kFfnThreads, 1) ffn_few_kernel(const __grid_co
     }
   } else if (warp == 1 && rank == 0) {
     constexpr uint32_t idesc = idesc_bf16(256, 256, ffn_a_mn(MODE) ? 1 : 0, ffn_b_mn(MODE) ? 1 : 0);
+    uint32_t stage = 0, phase = 0;
     for (int i = 0; i < steps; ++i) {
-      const int stage = i % kFfnStages;
-      if (!mbar_wait(&ctl->full[stage], (uint32_t)(i / kFfnStages) & 1, wc)) { ok = false; break; }
+      if (!mbar_wait(&ctl->full[stage], phase, wc)) { ok = false; break; }
       tc_fence_after();
       if (lane == 0) {
-        const uint32_t a0 = smem_u32(sA + stage * kFfnOperandBytes), b0 = smem_u32(sB + stage * kFfnOperandBytes);
+        const uint32_t a0 = smem_u32(sA + stage * a_slot), b0 = smem_u32(sB + stage * kFfnOperandBytes);
 #pragma unroll
         for (int k16 = 0; k16 < 4; ++k16) {
           const uint64_t ad = ffn_a_mn(MODE) ? sdesc_sw128(a0 + k16 * 2048, 8192, 1024) : sdesc_sw128(a0 + k16 * 32, 16, 1024);
@@ -554,6 +562,7 @@ __global__ void __launch_bounds__(kFfnThreads, 1) ffn_few_kernel(const __grid_co
         }
         mma_commit_pair(&ctl->empty[stage], 3u << (cta & ~1));
       }
+      if ((int)++stage == stages) { stage = 0; phase ^= 1; }
       __syncwarp();
     }
     if (lane == 0) mma_commit_pair(&ctl->done, 3u << (cta & ~1));
@@ -599,9 +608,11 @@ __global__ void __launch_bounds__(kFfnThreads, 1) ffn_few_kernel(const __grid_co
   if (warp >= 2 && summed) {
     constexpr int kPer = MODE == FFN_GATE ? kSlice4 / 2 : kSlice4;  // fours of results in a slice
     const int rows = min(128, p.M - row0);
-    for (int i = threadIdx.x - 64; i < 128 * kPer; i += 32 * kFfnEpilogueWarps) {
-      const int row = i & 127, c = i >> 7;
-      if (row >= rows) continue;
+    // (eight rows x four fours a warp: whole sectors out, no two lanes on a bank)
+    const int blocks = (rows + 7) / 8 * ((kPer + 3) / 4);
+    for (int i = warp - 2; i < blocks; i += kFfnEpilogueWarps) {
+      const int across = (kPer + 3) / 4, row = i / across * 8 + (lane & 7), c = i % across * 4 + (lane >> 3);
+      if (row >= rows || c >= kPer) continue;
       auto add = [&](int at) {
         float4 s = sums[at * 128 + row];
 #pragma unroll
@@ -623,10 +634,10 @@ __global__ void __launch_bounds__(kFfnThreads, 1) ffn_few_kernel(const __grid_co
 constexpr int kFfnPartSteps = 2;
 
 // Rows along K: boxes of 128 rows x 64 of K; along M or N: 64 of K x 64.
-bool operand_map(CUtensorMap* m, const FfnOperand& o, bool mn) {
+bool operand_map(CUtensorMap* m, const FfnOperand& o, bool mn, int rows = 128) {
   const uint64_t dims[2] = {(uint64_t)o.cols, (uint64_t)o.rows};
   const uint64_t str[1] = {(uint64_t)o.cols * 2};
-  const uint32_t box[2] = {64, mn ? 64u : 128u};
+  const uint32_t box[2] = {64, mn ? 64u : (uint32_t)rows};
   return make_tmap(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, o.p, dims, str, box, true);
 }
 
@@ -705,13 +716,15 @@ cudaError_t launch_mode(const FfnMaps& maps, const FfnParams& p, cudaStream_t st
 
 }  // namespace
 
-cudaError_t launch_ffn(FfnMode mode, const FfnOperand (&a)[2], const FfnOperand (&b)[2], const FfnParams& p,
+cudaError_t launch_ffn(FfnMode mode, const FfnOperand (&a)[2], const FfnOperand (&b)[2], FfnParams p,
                        cudaStream_t st) {
   FfnMaps maps;
   memset(&maps, 0, sizeof(maps));
+  // A's rows of a CTA: all of the result's where they are few (in whole eights, as the operand is laid out by)
+  p.a_rows = ffn_a_mn(mode) ? 128 : std::min(128, ceil_div(p.M, 8) * 8);
   for (int i = 0; i < 2; ++i) {
     if (!a[i].p) maps.a[i] = maps.a[0];
-    else if (!operand_map(&maps.a[i], a[i], ffn_a_mn(mode))) return cudaErrorInvalidValue;
+    else if (!operand_map(&maps.a[i], a[i], ffn_a_mn(mode), p.a_rows)) return cudaErrorInvalidValue;
     if (!b[i].p) maps.b[i] = maps.b[0];
     else if (!operand_map(&maps.b[i], b[i], ffn_b_mn(mode))) return cudaErrorInvalidValue;
   }

@@ -22,6 +22,7 @@ struct FfnParams {
   __nv_bfloat16* out[3];        // FFN_GATE: a, h, u (h, u may be null); FFN_DA: dh, du; FFN_DW13: dW1, dW3; else [0]
   const __nv_bfloat16 *h, *u;   // FFN_DA
   int after;       // FfnAfter
+  int a_rows;      // rows of A that a CTA brings (set by the launch)
 };
 
 // How a launch stands to the one before it in the stream.
@@ -37,7 +38,22 @@ struct FfnOperand {
 };
 
 // a[1], b[1]: the second operands of FFN_GATE (b: W3), FFN_DX (both) and FFN_DW13 (b)
-cudaError_t launch_ffn(FfnMode mode, const FfnOperand (&a)[2], const FfnOperand (&b)[2], const FfnParams& p,
+cudaError_t launch_ffn(FfnMode mode, const FfnOperand (&a)[2], const FfnOperand (&b)[2], FfnParams p,
                        cudaStream_t st);
+
+// The forward pass of a token or a few (ffn_rows.cu): two launches.
+// At most four tokens: eight are no faster so (H 2048, I 768: 1 token 7.9 us, 4 11.7, 8 15.7, on tensor cores 13.6; H
+// 7168, I 2048: 21.9, 30.5, 36.5, and 32.4).
+constexpr int kFfnRows = 4;
+constexpr size_t kFfnRowsSmem = 110 * 1024;  // two CTAs an SM
+struct FfnRowsParams {
+  int T, K, N;
+  int most_rows;       // of K in a CTA
+  const void *in, *W, *W3;
+  void* out;
+};
+bool ffn_rows_take(int T, int H, int I);
+cudaError_t launch_ffn_rows(int T, int H, int I, const void* x, const void* W1, const void* W3, const void* W2, float* a,
+                            void* out, cudaStream_t st);
 
 }  // namespace mok

@@ -18,8 +18,8 @@ class MoKFeedForward:
 
     Owns the workspace and, with ``training``, the context that ``forward`` keeps for
     ``backward`` (of the same x and weights, before the next forward).
-    ``infer`` keeps nothing; up to 128 tokens with sizes that are multiples of
-    128 it runs at the rate at which the weights are read.  Calls on one object must not overlap.
+    ``infer`` keeps nothing, and streams the weights through every SM for up to
+    four tokens.  Calls on one object must not overlap.
     After a timeout the results of all calls since the last ``check`` are void;
     ``check`` raises it and makes the workspace ready again."""
 
@@ -90,7 +90,8 @@ class MoKFeedForward:
             require(isinstance(grads, dict) and {"dX", "dW1", "dW3", "dW2"} <= set(grads),
                     "grads: a dict of dX, dW1, dW3 and dW2 is wanted")
             for name, shape in (("dX", rows), ("dW1", self._w13), ("dW3", self._w13), ("dW2", self._w2)):
-                tensor(grads[name], name, shape, (BF16,), self.device)
+                if not fits(grads[name], shape, BF16, self.device):
+                    tensor(grads[name], name, shape, (BF16,), self.device)
         _lib.mok_ffn_backward(self.ws, self.ctx, x, W1, W3, W2, dout, grads["dX"], grads["dW1"], grads["dW3"],
                               grads["dW2"], stream)
         return grads
@@ -101,7 +102,7 @@ class MoKFeedForward:
             return run_on(self, stream, self.check)
         st = _lib.mok_check(self.ws, stream)
         if st == _lib.MOK_ERR_TIMEOUT:
-            # a call that gave up leaves the abort word and counts of arrivals behind
+            # a call that gave up leaves the abort word behind
             self.ws.zero_()
             if self.device.type == "cuda":
                 torch.cuda.current_stream(self.device).synchronize()
