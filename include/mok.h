@@ -774,16 +774,16 @@ mok_status mok_residual_backward(const mok_residual* r, const void* x, int64_t l
  *
  *   x, out, dout, dX  (device) bf16 [T, H]
  *   W1, W3, dW1, dW3  (device) bf16 [H, I];  W2, dW2 (device) bf16 [I, H]
- *   ctx               (device) mok_ffn_ctx_size() bytes: h, u and a, which the
- *                     forward keeps for the backward
+ *   ctx               (device) mok_ffn_ctx_size() bytes: h and u in f32 and a in
+ *                     bf16, which the forward keeps for the backward
  *
  *   mok_ffn_infer     out alone.  A few tokens (T <= 4) stream the weights
  *                     through every SM at once; more run as mok_ffn_forward
  *   mok_ffn_forward   out and ctx
  *   mok_ffn_backward  all four gradients, of the same x and weights
  * Sums are f32.  a comes from the f32 h and u and is rounded to bf16 for the
- * second product (a few tokens': not at all); h, u, dh and du are rounded to
- * bf16 where the backward reads them.  H and I are multiples of 8, at most
+ * second product (a few tokens': not at all), dh and du where they are
+ * multiplied.  H and I are multiples of 8, at most
  * MOK_FFN_MAX_SIZE; T <= 2^22; T = 0 gives zero gradients of the weights.
  * Tensors start at 16-byte boundaries; outputs share no byte with inputs
  * or each other.  Results do not depend on timing: the same call gives the

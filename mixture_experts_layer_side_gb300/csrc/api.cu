@@ -2034,6 +2034,18 @@ FfnLayout ffn_layout(int32_t T, int32_t H, int32_t I, bool training) {
   return L;
 }
 
+// The context: h and u in f32, a in bf16.
+struct FfnCtxLayout {
+  size_t u, a, total;
+};
+FfnCtxLayout ffn_ctx_layout(int32_t T, int32_t I) {
+  FfnCtxLayout L;
+  L.u = align256(ffn_kept_floats(T, I) * 4);
+  L.a = 2 * L.u;
+  L.total = std::max<size_t>(256, L.a + align256((size_t)T * I * 2));
+  return L;
+}
+
 FfnParams ffn_params(void* ws, FfnAfter after, int M, int N, int K) {
   FfnParams p;
   memset(&p, 0, sizeof(p));
@@ -2064,13 +2076,13 @@ mok_status check_spans(std::initializer_list<Span> spans) {
 }
 
 mok_status ffn_forward(int32_t T, int32_t H, int32_t I, void* ws, const void* x, const void* W1, const void* W3,
-                       const void* W2, void* out, __nv_bfloat16* a, __nv_bfloat16* h, __nv_bfloat16* u, void* stream) {
+                       const void* W2, void* out, __nv_bfloat16* a, float* h, float* u, void* stream) {
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   Phase ph(MOK_PHASE_FFN_FWD, st, 2);
   FfnParams p = ffn_params(ws, FFN_AFTER_ALL, T, I, H);
   p.out[0] = a;
-  p.out[1] = h;
-  p.out[2] = u;
+  p.h = h;
+  p.u = u;
   MOK_CUDA(launch_ffn(FFN_GATE, {{x, T, H}, {}}, {{W1, H, I}, {W3, H, I}}, p, st));
   p = ffn_params(ws, FFN_READS_IT, T, H, I);
   p.out[0] = static_cast<__nv_bfloat16*>(out);
@@ -2085,7 +2097,7 @@ size_t mok_ffn_workspace_size(int32_t T, int32_t H, int32_t I, int32_t training)
 }
 
 size_t mok_ffn_ctx_size(int32_t T, int32_t I) {
-  return check_ffn(T, 8, I) == MOK_OK ? std::max<size_t>(256, 3 * align256((size_t)T * I * 2)) : 0;
+  return check_ffn(T, 8, I) == MOK_OK ? ffn_ctx_layout(T, I).total : 0;
 }
 
 mok_status mok_ffn_infer(int32_t T, int32_t H, int32_t I, void* ws, size_t ws_bytes, const void* x, const void* W1,
@@ -2117,10 +2129,10 @@ mok_status mok_ffn_forward(int32_t T, int32_t H, int32_t I, void* ws, size_t ws_
   MOK_TRY(check_spans({{x, rows}, {W1, w}, {W3, w}, {W2, w}, {out, rows, true}, {ctx, mok_ffn_ctx_size(T, I), true},
                        {ws, L.total, true}}));
   if (ws_bytes < L.total) return MOK_ERR_WORKSPACE_TOO_SMALL;
-  const size_t n = align256((size_t)T * I * 2);
+  const FfnCtxLayout C = ffn_ctx_layout(T, I);
   uint8_t* c = static_cast<uint8_t*>(ctx);
-  return ffn_forward(T, H, I, ws, x, W1, W3, W2, out, reinterpret_cast<__nv_bfloat16*>(c + 2 * n),
-                     reinterpret_cast<__nv_bfloat16*>(c), reinterpret_cast<__nv_bfloat16*>(c + n), stream);
+  return ffn_forward(T, H, I, ws, x, W1, W3, W2, out, reinterpret_cast<__nv_bfloat16*>(c + C.a),
+                     reinterpret_cast<float*>(c), reinterpret_cast<float*>(c + C.u), stream);
 }
 
 mok_status mok_ffn_backward(int32_t T, int32_t H, int32_t I, void* ws, size_t ws_bytes, const void* ctx, const void* x,
@@ -2138,15 +2150,15 @@ mok_status mok_ffn_backward(int32_t T, int32_t H, int32_t I, void* ws, size_t ws
   MOK_TRY(check_spans({{ctx, mok_ffn_ctx_size(T, I)}, {x, rows}, {W1, w}, {W3, w}, {W2, w}, {dout, rows}, {dX, rows, true},
                        {dW1, w, true}, {dW3, w, true}, {dW2, w, true}, {ws, L.total, true}}));
   if (ws_bytes < L.total) return MOK_ERR_WORKSPACE_TOO_SMALL;
-  const size_t n = align256((size_t)T * I * 2);
-  const uint8_t* c = static_cast<const uint8_t*>(ctx);
+  const FfnCtxLayout C = ffn_ctx_layout(T, I);
+  uint8_t* c = static_cast<uint8_t*>(const_cast<void*>(ctx));  // (read alone)
   uint8_t* s = static_cast<uint8_t*>(ws);
-  const void* a = c + 2 * n;
+  const void* a = c + C.a;
   Phase ph(MOK_PHASE_FFN_BWD, st, 4);
   // dW2 runs beside da, and dW1 and dW3 beside dx
   FfnParams p = ffn_params(ws, FFN_AFTER_ALL, T, I, H);
-  p.h = reinterpret_cast<const __nv_bfloat16*>(c);
-  p.u = reinterpret_cast<const __nv_bfloat16*>(c + n);
+  p.h = reinterpret_cast<float*>(c);
+  p.u = reinterpret_cast<float*>(c + C.u);
   p.out[0] = reinterpret_cast<__nv_bfloat16*>(s + L.dh);
   p.out[1] = reinterpret_cast<__nv_bfloat16*>(s + L.du);
   MOK_CUDA(launch_ffn(FFN_DA, {{dout, T, H}, {}}, {{W2, I, H}, {}}, p, st));

@@ -137,56 +137,46 @@ __device__ __forceinline__ void ffn_loads(const FfnMaps& mp, const FfnTile& t, i
 
 // ------------------------------------------------------------------ epilogue
 __device__ __forceinline__ float ffn_sigmoid(float h) { return 1.0f / (1.0f + __expf(-h)); }
+__device__ __forceinline__ void ffn_gate_gradient(float da, float h, float u, float& dh, float& du) {
+  const float s = ffn_sigmoid(h);
+  dh = da * u * s * (1.0f + h * (1.0f - s));
+  du = da * (h * s);
+}
 
-// 32 rows x 64 columns of bf16, a row of it a lane's 32 words, to row0.. and col0.. of
-// dst [rows, ld], whole 128-byte segments at a time through the warp's staging buffer
-// (16-byte pieces swizzled by row).  ld is a multiple of eight: a piece lies inside or outside.
-__device__ __forceinline__ void store_block(uint8_t* stage, int lane, const uint32_t (&w)[32], __nv_bfloat16* dst,
-                                            int row0, int rows, int col0, int ld) {
+// 32 rows of 128 bytes, a row a lane's 32 words, to memory in whole segments through the warp's staging buffer (16-byte
+// pieces swizzled by row): put(row, piece of eight) for each.
+template <typename Put>
+__device__ __forceinline__ void store_rows(uint8_t* stage, int lane, const uint32_t (&w)[32], Put&& put) {
 #pragma unroll
   for (int i = 0; i < 8; ++i)
     *reinterpret_cast<uint4*>(stage + lane * 128 + ((i ^ (lane & 7)) << 4)) =
         make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
   __syncwarp();
-  const int ch = lane & 7, col = col0 + ch * 8;
-#pragma unroll
-  for (int s = 0; s < 8; ++s) {
-    const int r = 4 * s + (lane >> 3);
-    const uint4 v = *reinterpret_cast<const uint4*>(stage + r * 128 + ((ch ^ (r & 7)) << 4));
-    if (row0 + r < rows && col < ld) *reinterpret_cast<uint4*>(dst + (long)(row0 + r) * ld + col) = v;
-  }
-  __syncwarp();
-}
-
-// The reverse, in two halves: the loads (zeros outside), and the words of the lane's row.
-__device__ __forceinline__ void load_block(uint4 (&v)[8], int lane, const __nv_bfloat16* src, int row0, int rows, int col0,
-                                           int ld) {
-  const int ch = lane & 7, col = col0 + ch * 8;
-#pragma unroll
-  for (int s = 0; s < 8; ++s) {
-    const int r = 4 * s + (lane >> 3);
-    v[s] = row0 + r < rows && col < ld ? *reinterpret_cast<const uint4*>(src + (long)(row0 + r) * ld + col)
-                                       : make_uint4(0, 0, 0, 0);
-  }
-}
-__device__ __forceinline__ void turn_block(uint8_t* stage, int lane, const uint4 (&v)[8], uint32_t (&w)[32]) {
   const int ch = lane & 7;
 #pragma unroll
   for (int s = 0; s < 8; ++s) {
     const int r = 4 * s + (lane >> 3);
-    *reinterpret_cast<uint4*>(stage + r * 128 + ((ch ^ (r & 7)) << 4)) = v[s];
-  }
-  __syncwarp();
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint4 t = *reinterpret_cast<const uint4*>(stage + lane * 128 + ((i ^ (lane & 7)) << 4));
-    w[4 * i] = t.x, w[4 * i + 1] = t.y, w[4 * i + 2] = t.z, w[4 * i + 3] = t.w;
+    put(r, *reinterpret_cast<const uint4*>(stage + r * 128 + ((ch ^ (r & 7)) << 4)));
   }
   __syncwarp();
 }
+// 64 columns of bf16 from row0, col0 on of dst [rows, ld].  ld is a multiple of eight: a piece lies inside or outside.
+__device__ __forceinline__ void store_block(uint8_t* stage, int lane, const uint32_t (&w)[32], __nv_bfloat16* dst,
+                                            int row0, int rows, int col0, int ld) {
+  const int col = col0 + (lane & 7) * 8;
+  store_rows(stage, lane, w, [&](int r, const uint4& v) {
+    if (row0 + r < rows && col < ld) *reinterpret_cast<uint4*>(dst + (long)(row0 + r) * ld + col) = v;
+  });
+}
 
-__device__ __forceinline__ float lo_f32(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float hi_f32(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+// h and u as they are kept for the backward pass: f32, as an epilogue's lanes have them, [row / 32][column / 4][row % 32]
+// fours of columns, so that a warp's 32 rows are 512 bytes in one piece both when they are written and when they are
+// read, and nothing has to be turned.  (In bf16 they were two roundings more in every gradient: relative errors of dx,
+// dW1 and dW3 of 3.0e-3 where 2.4e-3 come from dh, du and the result themselves.)
+__device__ __forceinline__ long kept_at(int row, int col, int N) {
+  return ((long)(row >> 5) * (N >> 2) + (col >> 2)) * 32 + (row & 31);
+}
+__device__ __forceinline__ float4 zero4() { return make_float4(0.0f, 0.0f, 0.0f, 0.0f); }
 
 // The 32 rows from row0 and this warp's half of a tile's columns.  `acc`: the accumulator's
 // address for these rows; `ready` waits for it.
@@ -196,7 +186,8 @@ __device__ __forceinline__ bool ffn_epilogue(const FfnParams& p, const FfnTile& 
   if constexpr (MODE == FFN_GATE) {
     if (!ready()) return false;
     const int col = t.n * 128 + half * 64;
-    uint32_t aw[32], hw[32], uw[32];
+    const bool keeps = p.h && row0 + lane < p.M;
+    uint32_t aw[32];
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
       uint32_t h[32], u[32];
@@ -210,22 +201,59 @@ __device__ __forceinline__ bool ffn_epilogue(const FfnParams& p, const FfnTile& 
         const float h0 = __uint_as_float(h[2 * i]), h1 = __uint_as_float(h[2 * i + 1]);
         const float u0 = __uint_as_float(u[2 * i]), u1 = __uint_as_float(u[2 * i + 1]);
         aw[16 * c + i] = pack_bf16x2(h0 * ffn_sigmoid(h0) * u0, h1 * ffn_sigmoid(h1) * u1);
-        hw[16 * c + i] = pack_bf16x2(h0, h1);
-        uw[16 * c + i] = pack_bf16x2(u0, u1);
+      }
+      if (keeps) {
+        uint4* hk = reinterpret_cast<uint4*>(p.h) + kept_at(row0 + lane, col + c * 32, p.N);
+        uint4* uk = reinterpret_cast<uint4*>(p.u) + kept_at(row0 + lane, col + c * 32, p.N);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (col + c * 32 + i * 4 >= p.N) break;
+          __stcs(hk + i * 32, make_uint4(h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3]));
+          __stcs(uk + i * 32, make_uint4(u[4 * i], u[4 * i + 1], u[4 * i + 2], u[4 * i + 3]));
+        }
       }
     }
     store_block(stage, lane, aw, p.out[0], row0, p.M, col, p.N);
-    if (p.out[1]) {
-      store_block(stage, lane, hw, p.out[1], row0, p.M, col, p.N);
-      store_block(stage, lane, uw, p.out[2], row0, p.M, col, p.N);
+  } else if constexpr (MODE == FFN_DA) {
+    // 32 columns of h and u are on their way while the products still run or the 32 before are worked on
+    const int col0 = t.n * 256 + half * 128;
+    const bool there = row0 + lane < p.M;
+    const float4* hk = reinterpret_cast<const float4*>(p.h) + kept_at(row0 + lane, col0, p.N);
+    const float4* uk = reinterpret_cast<const float4*>(p.u) + kept_at(row0 + lane, col0, p.N);
+    float4 hv[8], uv[8];
+    auto fetch = [&](int i, int c4) {  // the c4-th four from col0
+      const bool in = there && col0 + c4 * 4 < p.N;
+      hv[i] = in ? __ldcs(hk + c4 * 32) : zero4();
+      uv[i] = in ? __ldcs(uk + c4 * 32) : zero4();
+    };
+#pragma unroll
+    for (int i = 0; i < 8; ++i) fetch(i, i);
+    if (!ready()) return false;
+#pragma unroll 1
+    for (int c = 0; c < 4; ++c) {
+      float da[32];
+      uint32_t w[32];  // dh, then du
+      tmem_ld32(acc + half * 128 + c * 32, da);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float h[4] = {hv[i].x, hv[i].y, hv[i].z, hv[i].w}, u[4] = {uv[i].x, uv[i].y, uv[i].z, uv[i].w};
+        if (c < 3) fetch(i, c * 8 + 8 + i);
+        float dh[4], du[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) ffn_gate_gradient(da[4 * i + k], h[k], u[k], dh[k], du[k]);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          w[2 * i + k] = pack_bf16x2(dh[2 * k], dh[2 * k + 1]);
+          w[16 + 2 * i + k] = pack_bf16x2(du[2 * k], du[2 * k + 1]);
+        }
+      }
+      const int col = col0 + c * 32 + (lane & 3) * 8;
+      __nv_bfloat16* dst = p.out[(lane & 7) >> 2];
+      store_rows(stage, lane, w, [&](int r, const uint4& v) {
+        if (row0 + r < p.M && col < p.N) *reinterpret_cast<uint4*>(dst + (long)(row0 + r) * p.N + col) = v;
+      });
     }
   } else {
-    uint4 hv[8], uv[8];
-    if constexpr (MODE == FFN_DA) {
-      // (on their way while the products still run)
-      load_block(hv, lane, p.h, row0, p.M, t.n * 256 + half * 128, p.N);
-      load_block(uv, lane, p.u, row0, p.M, t.n * 256 + half * 128, p.N);
-    }
     if (!ready()) return false;
 #pragma unroll 1
     for (int g = 0; g < 2; ++g) {
@@ -233,44 +261,15 @@ __device__ __forceinline__ bool ffn_epilogue(const FfnParams& p, const FfnTile& 
       uint32_t ra[32], rb[32], w[32];
       tmem_ld32_issue(acc + half * 128 + g * 64, ra);
       tmem_ld32_issue(acc + half * 128 + g * 64 + 32, rb);
-      if constexpr (MODE == FFN_DA) {
-        uint32_t h[32], u[32];
-        turn_block(stage, lane, hv, h);
-        turn_block(stage, lane, uv, u);
-        if (g == 0) {
-          load_block(hv, lane, p.h, row0, p.M, col + 64, p.N);
-          load_block(uv, lane, p.u, row0, p.M, col + 64, p.N);
-        }
-        tmem_wait_ld();
-        tmem_regs_ready(ra);
-        tmem_regs_ready(rb);
+      tmem_wait_ld();
+      tmem_regs_ready(ra);
+      tmem_regs_ready(rb);
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          float dh[2], du[2];
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const float da = __uint_as_float(i < 16 ? ra[2 * i + j] : rb[2 * (i - 16) + j]);
-            const float hh = j ? hi_f32(h[i]) : lo_f32(h[i]), uu = j ? hi_f32(u[i]) : lo_f32(u[i]);
-            const float sg = ffn_sigmoid(hh);
-            dh[j] = da * uu * sg * (1.0f + hh * (1.0f - sg));
-            du[j] = da * (hh * sg);
-          }
-          w[i] = pack_bf16x2(dh[0], dh[1]);
-          u[i] = pack_bf16x2(du[0], du[1]);
-        }
-        store_block(stage, lane, w, p.out[0], row0, p.M, col, p.N);
-        store_block(stage, lane, u, p.out[1], row0, p.M, col, p.N);
-      } else {
-        tmem_wait_ld();
-        tmem_regs_ready(ra);
-        tmem_regs_ready(rb);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          w[i] = pack_bf16x2(__uint_as_float(ra[2 * i]), __uint_as_float(ra[2 * i + 1]));
-          w[16 + i] = pack_bf16x2(__uint_as_float(rb[2 * i]), __uint_as_float(rb[2 * i + 1]));
-        }
-        store_block(stage, lane, w, MODE == FFN_DW13 && t.which ? p.out[1] : p.out[0], row0, p.M, col, p.N);
+      for (int i = 0; i < 16; ++i) {
+        w[i] = pack_bf16x2(__uint_as_float(ra[2 * i]), __uint_as_float(ra[2 * i + 1]));
+        w[16 + i] = pack_bf16x2(__uint_as_float(rb[2 * i]), __uint_as_float(rb[2 * i + 1]));
       }
+      store_block(stage, lane, w, MODE == FFN_DW13 && t.which ? p.out[1] : p.out[0], row0, p.M, col, p.N);
     }
   }
   return true;
@@ -456,21 +455,17 @@ __device__ __forceinline__ void few_store4(const FfnParams& p, const FfnTile& t,
 #pragma unroll
     for (int i = 0; i < 4; ++i) a[i] = x[i] * ffn_sigmoid(x[i]) * y[i];
     put(p.out[0], a);
-    if (p.out[1]) {
-      put(p.out[1], x);
-      put(p.out[2], y);
+    if (p.h) {
+      __stcs(reinterpret_cast<float4*>(p.h) + kept_at(row, c, p.N), v);
+      __stcs(reinterpret_cast<float4*>(p.u) + kept_at(row, c, p.N), w);
     }
   } else if constexpr (MODE == FFN_DA) {
-    const uint2 hw = *reinterpret_cast<const uint2*>(p.h + at), uw = *reinterpret_cast<const uint2*>(p.u + at);
-    const float h[4] = {lo_f32(hw.x), hi_f32(hw.x), lo_f32(hw.y), hi_f32(hw.y)};
-    const float u[4] = {lo_f32(uw.x), hi_f32(uw.x), lo_f32(uw.y), hi_f32(uw.y)};
+    const float4 hv = reinterpret_cast<const float4*>(p.h)[kept_at(row, c, p.N)];
+    const float4 uv = reinterpret_cast<const float4*>(p.u)[kept_at(row, c, p.N)];
+    const float h[4] = {hv.x, hv.y, hv.z, hv.w}, u[4] = {uv.x, uv.y, uv.z, uv.w};
     float dh[4], du[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float sg = ffn_sigmoid(h[i]);
-      dh[i] = x[i] * u[i] * sg * (1.0f + h[i] * (1.0f - sg));
-      du[i] = x[i] * (h[i] * sg);
-    }
+    for (int i = 0; i < 4; ++i) ffn_gate_gradient(x[i], h[i], u[i], dh[i], du[i]);
     put(p.out[0], dh);
     put(p.out[1], du);
   } else {

@@ -19,8 +19,8 @@ struct FfnParams {
   int M, N;        // rows and columns of the result (FFN_GATE: N = I; FFN_DW13: N = I, twice)
   int K;           // length of the sums (FFN_DX: of each of the two)
   int32_t* hdr;    // workspace header: error and abort words
-  __nv_bfloat16* out[3];        // FFN_GATE: a, h, u (h, u may be null); FFN_DA: dh, du; FFN_DW13: dW1, dW3; else [0]
-  const __nv_bfloat16 *h, *u;   // FFN_DA
+  __nv_bfloat16* out[2];  // FFN_DA: dh, du; FFN_DW13: dW1, dW3; else [0]
+  float *h, *u;           // FFN_GATE: kept there (or null); FFN_DA: read (laid out by ffn_kept_floats)
   int after;       // FfnAfter
   int a_rows;      // rows of A that a CTA brings (set by the launch)
 };
@@ -31,6 +31,9 @@ enum FfnAfter : int {
   FFN_READS_IT = 1,    // starts beside it, waits for its end before it reads anything
   FFN_BESIDE_IT = 2,   // reads nothing that it writes: waits for its end at its own end
 };
+
+// Floats that h or u of T rows takes where it is kept: rows in whole 32s.
+inline size_t ffn_kept_floats(int T, int I) { return ((size_t)T + 31) / 32 * 32 * (size_t)I; }
 
 struct FfnOperand {
   const void* p;
