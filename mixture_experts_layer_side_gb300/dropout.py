@@ -7,7 +7,7 @@ import numbers
 import torch
 
 from . import _lib
-from ._check import away, on, require, rows_fit, run_on, tensor
+from ._check import MokArgError, away, on, require, rows_fit, run_on, tensor
 
 _TYPES = (torch.bfloat16, torch.float32)
 
@@ -35,7 +35,8 @@ class MoKDropout:
             require(call.numel() == 1, "call: a tensor of one element is wanted")
             tensor(call, "call", call.shape, (torch.int64,), self.device)
             return _lib.mok_drop(self.p, self.seed, 0, call)
-        require(isinstance(call, numbers.Integral) and 0 <= call < 2**63, f"call: {call}, wanted a whole number")
+        if not ((type(call) is int or isinstance(call, numbers.Integral)) and 0 <= call < 2**63):
+            raise MokArgError(f"call: {call}, wanted a whole number")
         return _lib.mok_drop(self.p, self.seed, int(call))
 
     def forward(self, x, call=0, out=None, stream=None):
@@ -44,13 +45,18 @@ class MoKDropout:
             return run_on(self, stream, self.forward, x, call, out)
         d = self.device
         require(isinstance(x, torch.Tensor), "x: a tensor is wanted")
-        tensor(x, "x", x.shape, _TYPES, d, rows_apart=x.dim() == 2)
+        matrix = x.dim() == 2
+        if not (matrix and x.dtype in _TYPES and rows_fit(x, x.shape, x.dtype, d)):
+            tensor(x, "x", x.shape, _TYPES, d, rows_apart=matrix)
         if out is None:
             out = torch.empty(x.shape, dtype=x.dtype, device=d)
-        elif not (x.dim() == 2 and rows_fit(out, x.shape, x.dtype, d)):
-            tensor(out, "out", x.shape, (x.dtype,), d, rows_apart=x.dim() == 2)
-        rows = x if x.dim() == 2 else x.reshape(1, -1)
-        _lib.mok_dropout(rows, self.drop(call), out if x.dim() == 2 else out.view(1, -1), stream)
+        elif not (matrix and rows_fit(out, x.shape, x.dtype, d)):
+            tensor(out, "out", x.shape, (x.dtype,), d, rows_apart=matrix)
+        drop = self.drop(call)
+        if matrix:
+            _lib.mok_dropout(x, drop, out, stream)
+        else:
+            _lib.mok_dropout(x.view(1, -1), drop, out.view(1, -1), stream)
         return out
 
     def backward(self, dout, call=0, out=None, stream=None):

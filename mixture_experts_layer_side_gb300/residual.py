@@ -7,7 +7,7 @@ import math
 import torch
 
 from . import _lib
-from ._check import away, fits, on, require, rows_fit, run_on, tensor, workspace
+from ._check import MokArgError, away, fits, on, require, rows_fit, run_on, tensor, workspace
 from .dropout import MoKDropout
 
 _TYPES = (torch.bfloat16, torch.float32)
@@ -39,14 +39,15 @@ class MoKResidual:
 
     def _begin(self, x, w_out, gate, w_next, scale, dropout, call, branch):
         """(T, branch type, mok_residual) of a call whose stream is like ``x``."""
+        # (what is wrong is put into words only where something is)
         d = self.device
-        require(isinstance(x, torch.Tensor) and x.dim() == 2 and x.shape[0] <= self.rows,
-                f"a matrix of at most {self.rows} rows of {self.hidden} is wanted")
+        if not (isinstance(x, torch.Tensor) and x.dim() == 2 and x.shape[0] <= self.rows):
+            raise MokArgError(f"a matrix of at most {self.rows} rows of {self.hidden} is wanted")
         T, S = x.shape[0], x.dtype
         self._matrix(x, "x", T, _TYPES)
         B = branch
-        require(B == torch.bfloat16 or S == B == torch.float32,
-                f"a branch of {B} beside a stream of {S}: wanted bf16, or both f32")
+        if not (B is torch.bfloat16 or S is B is torch.float32):
+            raise MokArgError(f"a branch of {B} beside a stream of {S}: wanted bf16, or both f32")
         for w, name in ((w_out, "w_out"), (w_next, "w_next")):
             if w is not None and not fits(w, (self.hidden,), B, d):
                 tensor(w, name, (self.hidden,), (B,), d)
@@ -54,13 +55,18 @@ class MoKResidual:
         if gate is not None:
             require(isinstance(gate, torch.Tensor) and gate.dim() in (1, 2), "gate: one or two dimensions are wanted")
             G = 1 if gate.dim() == 1 else gate.shape[0]
-            require(1 <= G <= max(T, 1) and T % G == 0, f"gate: {G} rows for {T} rows")
-            tensor(gate, "gate", (self.hidden,) if gate.dim() == 1 else (G, self.hidden), (B,), d)
+            if not (1 <= G <= max(T, 1) and T % G == 0):
+                raise MokArgError(f"gate: {G} rows for {T} rows")
+            shape = (self.hidden,) if gate.dim() == 1 else (G, self.hidden)
+            if not fits(gate, shape, B, d):
+                tensor(gate, "gate", shape, (B,), d)
         scale = float(scale)
-        require(math.isfinite(scale), f"scale: {scale}, wanted a finite number")
+        if not math.isfinite(scale):
+            raise MokArgError(f"scale: {scale}, wanted a finite number")
         drop = None
         if dropout is not None:
-            require(isinstance(dropout, MoKDropout) and dropout.device == d, f"dropout: a MoKDropout on {d} is wanted")
+            if not (isinstance(dropout, MoKDropout) and dropout.device == d):
+                raise MokArgError(f"dropout: a MoKDropout on {d} is wanted")
             drop = dropout.drop(call)
         return T, _lib.mok_residual(T, self.hidden, _lib.dtype_of(x), _lib._DTYPES[B], self.eps, scale, w_out, gate, G,
                                     w_next, drop)
