@@ -40,19 +40,23 @@ __device__ __forceinline__ uint4 philox(uint64_t block, uint64_t call, uint32_t 
   return c;
 }
 
-// Which of the eight elements of a block are kept, element j in bit j.  Both halves of a word are compared at its
-// upper end, where the bits below them change nothing: 16 bits are not below p * 65536 if what they begin is more than
-// p * 2^32 - 1.
+// Both halves of a word are compared at its upper end, where the bits below them change nothing: 16 bits are not below
+// p * 65536 if what they begin is more than p * 2^32 - 1.  (Nothing may be asked where p is 0.)
+__device__ __forceinline__ uint32_t drop_most(const DropParams& d) { return (d.below << 16) - 1u; }
+// Whether element j of a block is kept.
+__device__ __forceinline__ bool drop_kept(const uint4& r, int j, uint32_t most) {
+  const uint32_t w = j < 2 ? r.x : j < 4 ? r.y : j < 6 ? r.z : r.w;
+  return (j & 1 ? w : w << 16) > most;
+}
+__device__ __forceinline__ uint4 drop_block(const DropParams& d, uint64_t block, uint64_t call) {
+  return philox(block, call, d.key0, d.key1);
+}
+// Which of the eight elements of a block are kept, element j in bit j.
 __device__ __forceinline__ uint32_t drop_keep8(const DropParams& d, uint64_t block, uint64_t call) {
-  const uint4 r = philox(block, call, d.key0, d.key1);
-  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-  const uint32_t most = (d.below << 16) - 1u;
+  const uint4 r = drop_block(d, block, call);
   uint32_t keep = 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    keep |= (w[i] << 16) > most ? 1u << (2 * i) : 0u;
-    keep |= w[i] > most ? 2u << (2 * i) : 0u;
-  }
+  for (int j = 0; j < 8; ++j) keep |= drop_kept(r, j, drop_most(d)) ? 1u << j : 0u;
   return keep;
 }
 

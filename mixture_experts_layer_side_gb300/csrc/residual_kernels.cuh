@@ -787,8 +787,8 @@ __global__ void __launch_bounds__(32 * kJoinRows) residual_join_kernel(const Res
 
 // ------------------------------------------------------------------ launches
 // Shared memory of the rows ahead, over all of an SM's CTAs: enough for what HBM has on its way, and the rest left to
-// L1 for the weights.
-constexpr size_t kAheadBytes = 176 * 1024;
+// L1 for the weights (which the backward pass has in registers).
+constexpr size_t kAheadBytes = 176 * 1024, kAheadBytesBackward = 200 * 1024;
 constexpr int kMaxStages = 4;
 
 inline int team_threads(int H, int ng) { return ((H + 8 * ng - 1) / (8 * ng) + 31) / 32 * 32; }
@@ -798,17 +798,10 @@ inline int groups_backward(int H) { return H <= 256 ? 1 : H <= 8192 ? 2 : 4; }
 inline int ctas_forward(int threads, int ng) { return std::max(1, (ng <= 2 ? 1024 : 512) / threads); }
 inline int ctas_backward(int threads, int ng) { return std::max(1, (ng == 1 ? 768 : 512) / threads); }
 
-// How many rows ahead, with as many CTAs an SM as have room for two at least (0: none).
-inline int stages_ahead(int* ctas, size_t stage, size_t beside) {
-  for (int c = *ctas; c > 0; --c) {
-    const size_t room = kAheadBytes / c;
-    const int stages = room > beside ? std::min<int>(kMaxStages, (int)((room - beside) / stage)) : 0;
-    if (stages >= 2) {
-      *ctas = c;
-      return stages;
-    }
-  }
-  return 0;
+// How many rows ahead a CTA's share of the memory holds (0: not two at least).
+inline int stages_ahead(size_t room, size_t stage, size_t beside) {
+  const int stages = room > beside ? std::min<int>(kMaxStages, (int)((room - beside) / stage)) : 0;
+  return stages >= 2 ? stages : 0;
 }
 
 // All the teams that the SMs hold; where there are few rows, four of them at least for a team, so that the parts stay few
@@ -839,13 +832,13 @@ cudaError_t forward(const ResidualParams& p, cudaStream_t st) {
   const dim3 block(nt, rows);
   const size_t beside = !ALIGNED && p.drop.below ? (size_t)rows * ((p.H + 14) / 8 + 1) : 0;
   const size_t stage = (size_t)rows * nt * NG * (vectors8<S, ALIGNED>() + vectors8<B, ALIGNED>()) * 16;
-  int ctas = ctas_forward(nt * rows, NG);
-  const int most = ctas, stages = stages_ahead(&ctas, stage, beside), grid = (p.T + rows - 1) / rows;
+  const int ctas = ctas_forward(nt * rows, NG), grid = (p.T + rows - 1) / rows;
+  // (a team's only row needs no stage; rows so long that fewer CTAs would hold two are better off with all of them:
+  // 8,192 rows of 7,168 f32 of both kinds, 161 us, ahead on half the CTAs 272)
+  const int stages = grid > ctas * sms ? stages_ahead(kAheadBytes / ctas, stage, beside) : 0;
   auto run = [&](auto parts) {
     constexpr int kParts = decltype(parts)::value;
-    // (a team's only row needs no stage; rows so long that fewer CTAs would hold two are better off with all of them:
-    // 8,192 rows of 7,168 f32 of both kinds, 161 us, ahead on half the CTAs 272)
-    if (stages == 0 || ctas < most || grid <= ctas * sms)
+    if (stages == 0)
       return start(residual_forward_kernel<S, B, ALIGNED, NG, false, kParts>, dim3(grid), block, beside, st, p, 0);
     return start(residual_forward_kernel<S, B, ALIGNED, NG, true, kParts>, dim3(ctas * sms), block, stages * stage + beside,
                  st, p, stages);
@@ -869,15 +862,18 @@ cudaError_t forward(const ResidualParams& p, cudaStream_t st) {
 template <typename S, typename B, bool ALIGNED, int NG>
 cudaError_t backward(const ResidualParams& p, int* launches, cudaStream_t st) {
   const int nt = team_threads(p.H, NG), rows = nt == 32 ? kTeamRows : 1;
-  const size_t vector = (size_t)rows * nt * NG * 16;
   const bool bytes = !ALIGNED && p.drop.below;
-  int ctas = ctas_backward(nt * rows, NG);
-  const int stages = stages_ahead(
-      &ctas, vector * (2 * vectors8<S, ALIGNED>() + (p.G > 1 ? 3 : 2) * vectors8<B, ALIGNED>()),
-      rows * backward_beside(p.H, bytes, p.G > 1, rows > 1));
-  const BackwardPlan plan = backward_plan(p.T, p.G, device_sm_count() * ctas * rows, rows);
-  const size_t beside = rows * backward_beside(p.H, bytes, plan.own, rows > 1);
-  const size_t stage = vector * (2 * vectors8<S, ALIGNED>() + (plan.own ? 3 : 2) * vectors8<B, ALIGNED>());
+  const int most = ctas_backward(nt * rows, NG);
+  // as many CTAs an SM as have room for two rows ahead at least, or all of them with none
+  BackwardPlan plan;
+  size_t beside = 0, stage = 0;
+  int stages = 0;
+  for (int ctas = most; ctas >= 0 && !stages; --ctas) {
+    plan = backward_plan(p.T, p.G, device_sm_count() * (ctas ? ctas : most) * rows, rows);
+    beside = rows * backward_beside(p.H, bytes, plan.own, rows > 1);
+    stage = (size_t)rows * nt * NG * 16 * (2 * vectors8<S, ALIGNED>() + (plan.own ? 3 : 2) * vectors8<B, ALIGNED>());
+    if (ctas) stages = stages_ahead(kAheadBytesBackward / ctas, stage, beside);
+  }
   const dim3 grid(plan.ctas), block(nt, rows);
   auto run = [&](auto parts) {
     constexpr int kParts = decltype(parts)::value;
