@@ -271,24 +271,43 @@ __device__ __forceinline__ void keep_bytes(const DropParams& d, uint64_t call, u
   for (int i = t; i < n; i += nt) bytes[i] = (uint8_t)drop_keep8(d, b0 + i, call);
   team_sync(nt);
 }
+struct KeepBits {
+  uint32_t bits;
+  __device__ __forceinline__ bool operator()(int j) const { return (bits >> j) & 1u; }
+};
+struct KeepBlock {
+  uint4 r;
+  uint32_t most;
+  __device__ __forceinline__ bool operator()(int j) const { return drop_kept(r, j, most); }
+};
+// (Words need no bits made of them first, but registers, of which threads with four groups have none to spare: 8,192 rows
+// of 7,168 bf16, two groups, backward with dropout: bits 212 us, words 188; 4,096 of 12,288, four, without: 271 and 363.)
 template <bool ALIGNED, int NG>
-__device__ __forceinline__ uint32_t keep8(const DropParams& d, uint64_t call, uint64_t first, int g, const Place& a,
-                                          const uint8_t* bytes) {
+using Keep = std::conditional_t<ALIGNED && NG <= 2, KeepBlock, KeepBits>;
+template <bool ALIGNED, int NG>
+__device__ __forceinline__ Keep<ALIGNED, NG> keep8(const DropParams& d, uint64_t call, uint64_t first, int g, const Place& a,
+                                                   const uint8_t* bytes) {
   const int c = first_column<NG>(a, g);
-  if constexpr (ALIGNED) return drop_keep8(d, (first + c) >> 3, call);
-  const uint32_t at = (uint32_t)(first & 7) + c;
-  uint32_t keep = bytes[at >> 3] >> (at & 7);
-  // (the byte after is there if one of its elements is the row's)
-  if ((at & 7) + (g < NG - 1 ? 8 : a.held) > 8) keep |= (uint32_t)bytes[(at >> 3) + 1] << (8 - (at & 7));
-  return keep & 0xffu;
+  if constexpr (ALIGNED && NG <= 2) {
+    return {drop_block(d, (first + c) >> 3, call), drop_most(d)};
+  } else if constexpr (ALIGNED) {
+    return {drop_keep8(d, (first + c) >> 3, call)};
+  } else {
+    const uint32_t at = (uint32_t)(first & 7) + c;
+    uint32_t keep = bytes[at >> 3] >> (at & 7);
+    // (the byte after is there if one of its elements is the row's)
+    if ((at & 7) + (g < NG - 1 ? 8 : a.held) > 8) keep |= (uint32_t)bytes[(at >> 3) + 1] << (8 - (at & 7));
+    return {keep};
+  }
 }
 // (a dropped element is 0 whatever it was)
-__device__ __forceinline__ void drop8(Eight& v, uint32_t keep) {
+template <typename K>
+__device__ __forceinline__ void drop8(Eight& v, const K& keep) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     float a, b;
     split(v.v[i], a, b);
-    v.v[i] = pair((keep >> (2 * i)) & 1u ? a : 0.0f, (keep >> (2 * i + 1)) & 1u ? b : 0.0f);
+    v.v[i] = pair(keep(2 * i) ? a : 0.0f, keep(2 * i + 1) ? b : 0.0f);
   }
 }
 
@@ -596,7 +615,7 @@ __global__ void __launch_bounds__(NG == 1 ? 256 : 512, NG == 1 ? 3 : 1)
       if (plan.own && fresh) unit_weights(at.group, m + 2 * (kS + kB) * nt);
     }
     if (!ALIGNED && drops && to_y) keep_bytes(p.drop, call, first, H, t, nt, bytes);
-    uint32_t keep[NG];
+    Keep<ALIGNED, NG> keep[NG];
     // Sums of y^2, x'^2, t x' and, with f as above and y, of dx' f y, t f y, x' f y: as dx is linear in the first
     // norm's two factors, sum t' y follows from those three, and all of a row's sums are made at once.
     float s[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
@@ -604,7 +623,6 @@ __global__ void __launch_bounds__(NG == 1 ? 256 : 512, NG == 1 ? 3 : 1)
     for (int g = 0; g < NG; ++g) {
       float u[6] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
       Eight fy = zeros();
-      keep[g] = 0xffu;
       if (drops && to_y) keep[g] = keep8<ALIGNED, NG>(p.drop, call, first, g, a, bytes);
       if (has_out && has_y) {
         const Eight y = get_y(g);
