@@ -2156,19 +2156,26 @@ mok_status mok_ffn_backward(int32_t T, int32_t H, int32_t I, void* ws, size_t ws
   const void* a = c + C.a;
   Phase ph(MOK_PHASE_FFN_BWD, st, 4);
   // dW2 runs beside da, and dW1 and dW3 beside dx
+  int sms[2];
+  ffn_share_sms({{FFN_DA, T, I, H}, {FFN_DW2, I, H, T}}, sms);
   FfnParams p = ffn_params(ws, FFN_AFTER_ALL, T, I, H);
+  p.sms = sms[0];
   p.h = reinterpret_cast<float*>(c);
   p.u = reinterpret_cast<float*>(c + C.u);
   p.out[0] = reinterpret_cast<__nv_bfloat16*>(s + L.dh);
   p.out[1] = reinterpret_cast<__nv_bfloat16*>(s + L.du);
   MOK_CUDA(launch_ffn(FFN_DA, {{dout, T, H}, {}}, {{W2, I, H}, {}}, p, st));
   p = ffn_params(ws, FFN_BESIDE_IT, I, H, T);
+  p.sms = sms[1];
   p.out[0] = static_cast<__nv_bfloat16*>(dW2);
   MOK_CUDA(launch_ffn(FFN_DW2, {{a, T, I}, {}}, {{dout, T, H}, {}}, p, st));
+  ffn_share_sms({{FFN_DX, T, H, I}, {FFN_DW13, H, I, T}}, sms);
   p = ffn_params(ws, FFN_READS_IT, T, H, I);
+  p.sms = sms[0];
   p.out[0] = static_cast<__nv_bfloat16*>(dX);
   MOK_CUDA(launch_ffn(FFN_DX, {{s + L.dh, T, I}, {s + L.du, T, I}}, {{W1, H, I}, {W3, H, I}}, p, st));
   p = ffn_params(ws, FFN_BESIDE_IT, H, I, T);
+  p.sms = sms[1];
   p.out[0] = static_cast<__nv_bfloat16*>(dW1);
   p.out[1] = static_cast<__nv_bfloat16*>(dW3);
   MOK_CUDA(launch_ffn(FFN_DW13, {{x, T, H}, {}}, {{s + L.dh, T, I}, {s + L.du, T, I}}, p, st));

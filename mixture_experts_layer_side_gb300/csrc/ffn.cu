@@ -441,11 +441,11 @@ struct FfnFewCtl {
 static_assert(sizeof(FfnFewCtl) <= 256 && sizeof(FfnCtl) <= 256, "the control block's place");
 
 template <int MODE>
-__device__ __forceinline__ void few_store4(const FfnParams& p, const FfnTile& t, int row, int col, const float4& v, const float4& w) {
-  // col: within the tile's columns; (rows and sizes are in whole fours)
+__device__ __forceinline__ void few_store4(const FfnParams& p, const FfnTile& t, int row, int col, const float4& v,
+                                           const float4& w, const float4& hv, const float4& uv) {
+  // col: within the tile's columns; (rows and sizes are in whole fours)  FFN_GATE: v, w are h and u; FFN_DA: hv, uv
   const float x[4] = {v.x, v.y, v.z, v.w}, y[4] = {w.x, w.y, w.z, w.w};
   const int c = t.n * ffn_tile_n(MODE) + col;
-  if (c >= p.N) return;
   const long at = (long)row * p.N + c;
   auto put = [&](__nv_bfloat16* dst, const float (&f)[4]) {
     *reinterpret_cast<uint2*>(dst + at) = make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]));
@@ -460,8 +460,6 @@ __device__ __forceinline__ void few_store4(const FfnParams& p, const FfnTile& t,
       __stcs(reinterpret_cast<float4*>(p.u) + kept_at(row, c, p.N), w);
     }
   } else if constexpr (MODE == FFN_DA) {
-    const float4 hv = reinterpret_cast<const float4*>(p.h)[kept_at(row, c, p.N)];
-    const float4 uv = reinterpret_cast<const float4*>(p.u)[kept_at(row, c, p.N)];
     const float h[4] = {hv.x, hv.y, hv.z, hv.w}, u[4] = {uv.x, uv.y, uv.z, uv.w};
     float dh[4], du[4];
 #pragma unroll
@@ -569,6 +567,31 @@ __global__ void __launch_bounds__(kFfnThreads, 1) ffn_few_kernel(const __grid_co
   tc_fence_after();
   cluster_sync();
   const int row0 = t.m * 256 + rank * 128;
+  // what this thread adds and stores at last: eight rows x four fours a warp at a time (whole sectors out, no two lanes on
+  // a bank), kAtOnce of them together.  FFN_DA: the first ones' h and u are on their way from here on
+  constexpr int kPer = MODE == FFN_GATE ? kSlice4 / 2 : kSlice4, kAcross = (kPer + 3) / 4;  // fours of results in a slice
+  constexpr int kAtOnce = 4;
+  const int rows = min(128, p.M - row0), blocks = (rows + 7) / 8 * kAcross;
+  auto place = [&](int i, int& row, int& c) {
+    row = i / kAcross * 8 + (lane & 7);
+    c = i % kAcross * 4 + (lane >> 3);
+    return i < blocks && row < rows && c < kPer && t.n * ffn_tile_n(MODE) + (part * kPer + c) * 4 < p.N;
+  };
+  float4 hv[kAtOnce], uv[kAtOnce];
+  auto fetch = [&](int i0) {
+#pragma unroll
+    for (int j = 0; j < kAtOnce; ++j) {
+      hv[j] = uv[j] = zero4();
+      if constexpr (MODE == FFN_DA) {
+        int row, c;
+        if (!place(i0 + j * kFfnEpilogueWarps, row, c)) continue;
+        const long at = kept_at(row0 + row, t.n * 256 + (part * kPer + c) * 4, p.N);
+        hv[j] = __ldcs(reinterpret_cast<const float4*>(p.h) + at);
+        uv[j] = __ldcs(reinterpret_cast<const float4*>(p.u) + at);
+      }
+    }
+  };
+  if (warp >= 2) fetch(warp - 2);
   if (warp >= 2 && summed && row0 + q * 32 < p.M) {
     const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16);
 #pragma unroll 1
@@ -601,24 +624,25 @@ __global__ void __launch_bounds__(kFfnThreads, 1) ffn_few_kernel(const __grid_co
   tc_fence_after();
   if (warp == 1) tmem_dealloc_pair(tmem, 256);
   if (warp >= 2 && summed) {
-    constexpr int kPer = MODE == FFN_GATE ? kSlice4 / 2 : kSlice4;  // fours of results in a slice
-    const int rows = min(128, p.M - row0);
-    // (eight rows x four fours a warp: whole sectors out, no two lanes on a bank)
-    const int blocks = (rows + 7) / 8 * ((kPer + 3) / 4);
-    for (int i = warp - 2; i < blocks; i += kFfnEpilogueWarps) {
-      const int across = (kPer + 3) / 4, row = i / across * 8 + (lane & 7), c = i % across * 4 + (lane >> 3);
-      if (row >= rows || c >= kPer) continue;
-      auto add = [&](int at) {
-        float4 s = sums[at * 128 + row];
+    auto add = [&](int at, int row) {
+      float4 s = sums[at * 128 + row];
 #pragma unroll
-        for (int j = 1; j < S; ++j) {
-          const float4 w = sums[(j * kSlice4 + at) * 128 + row];
-          s.x += w.x, s.y += w.y, s.z += w.z, s.w += w.w;
-        }
-        return s;
-      };
-      const float4 v = add(c), w = MODE == FFN_GATE ? add(kPer + c) : v;
-      few_store4<MODE>(p, t, row0 + row, (part * kPer + c) * 4, v, w);
+      for (int j = 1; j < S; ++j) {
+        const float4 w = sums[(j * kSlice4 + at) * 128 + row];
+        s.x += w.x, s.y += w.y, s.z += w.z, s.w += w.w;
+      }
+      return s;
+    };
+#pragma unroll 1
+    for (int i = warp - 2; i < blocks; i += kAtOnce * kFfnEpilogueWarps) {
+      if (i >= kAtOnce * kFfnEpilogueWarps) fetch(i);
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j) {
+        int row, c;
+        if (!place(i + j * kFfnEpilogueWarps, row, c)) continue;
+        const float4 v = add(c, row), w = MODE == FFN_GATE ? add(kPer + c, row) : v;
+        few_store4<MODE>(p, t, row0 + row, (part * kPer + c) * 4, v, w, hv[j], uv[j]);
+      }
     }
   }
   if (p.after == FFN_BESIDE_IT) griddep_wait();
@@ -677,7 +701,7 @@ void prepare(FfnLaunch* l, const FfnParams& p, int cluster, unsigned grid, cudaS
 template <int MODE, int S>
 cudaError_t launch_few_tiles(const FfnMaps& maps, const FfnParams& p, int tiles, int k_iters, bool* done, cudaStream_t st) {
   *done = false;
-  if (tiles * 2 * S > device_sm_count() || k_iters < S * kFfnPartSteps) return cudaSuccess;
+  if (tiles * 2 * S > p.sms || k_iters < S * kFfnPartSteps) return cudaSuccess;
   static std::atomic<int> held[64];
   FfnLaunch l;
   prepare(&l, p, 2 * S, 2u * S * (unsigned)tiles, st);
@@ -689,10 +713,12 @@ cudaError_t launch_few_tiles(const FfnMaps& maps, const FfnParams& p, int tiles,
   return cudaLaunchKernelEx(&l.cfg, ffn_few_kernel<MODE, S>, maps, p);
 }
 
+int tiles_of(int mode, int M, int N) { return ceil_div(M, 256) * ceil_div(N, ffn_tile_n(mode)) * (mode == FFN_DW13 ? 2 : 1); }
+int steps_of(int mode, int K) { return ceil_div(K, 64) * (mode == FFN_DX ? 2 : 1); }
+
 template <int MODE>
 cudaError_t launch_mode(const FfnMaps& maps, const FfnParams& p, cudaStream_t st) {
-  const int tiles = ceil_div(p.M, 256) * ceil_div(p.N, ffn_tile_n(MODE)) * (MODE == FFN_DW13 ? 2 : 1);
-  const int k_iters = ceil_div(p.K, 64) * (MODE == FFN_DX ? 2 : 1);
+  const int tiles = tiles_of(MODE, p.M, p.N), k_iters = steps_of(MODE, p.K);
   bool done;
   cudaError_t e = launch_few_tiles<MODE, 8>(maps, p, tiles, k_iters, &done, st);
   if (e == cudaSuccess && !done) e = launch_few_tiles<MODE, 4>(maps, p, tiles, k_iters, &done, st);
@@ -711,11 +737,33 @@ cudaError_t launch_mode(const FfnMaps& maps, const FfnParams& p, cudaStream_t st
 
 }  // namespace
 
+void ffn_share_sms(const FfnSize (&two)[2], int (&sms)[2]) {
+  const int all = device_sm_count();
+  int tiles[2], steps[2], S[2] = {1, 1};
+  for (int i = 0; i < 2; ++i) {
+    tiles[i] = tiles_of(two[i].mode, two[i].M, two[i].N);
+    steps[i] = steps_of(two[i].mode, two[i].K);
+    sms[i] = all;
+  }
+  if ((long)tiles[0] + tiles[1] > all / 2) return;
+  // the longer parts are halved as long as there is room
+  bool open[2] = {true, true};
+  while (open[0] || open[1]) {
+    const int i = open[0] && (!open[1] || steps[0] / S[0] >= steps[1] / S[1]) ? 0 : 1;
+    if (S[i] < 8 && steps[i] >= 2 * S[i] * kFfnPartSteps && 2 * (tiles[0] * S[0] + tiles[1] * S[1] + tiles[i] * S[i]) <= all)
+      S[i] *= 2;
+    else
+      open[i] = false;
+  }
+  for (int i = 0; i < 2; ++i) sms[i] = 2 * S[i] * tiles[i];
+}
+
 cudaError_t launch_ffn(FfnMode mode, const FfnOperand (&a)[2], const FfnOperand (&b)[2], FfnParams p,
                        cudaStream_t st) {
   FfnMaps maps;
   memset(&maps, 0, sizeof(maps));
   // A's rows of a CTA: all of the result's where they are few (in whole eights, as the operand is laid out by)
+  if (p.sms == 0) p.sms = device_sm_count();
   p.a_rows = ffn_a_mn(mode) ? 128 : std::min(128, ceil_div(p.M, 8) * 8);
   for (int i = 0; i < 2; ++i) {
     if (!a[i].p) maps.a[i] = maps.a[0];

@@ -23,6 +23,7 @@ struct FfnParams {
   float *h, *u;           // FFN_GATE: kept there (or null); FFN_DA: read (laid out by ffn_kept_floats)
   int after;       // FfnAfter
   int a_rows;      // rows of A that a CTA brings (set by the launch)
+  int sms;         // SMs that its tiles may be spread over (0: all)
 };
 
 // How a launch stands to the one before it in the stream.
@@ -39,6 +40,15 @@ struct FfnOperand {
   const void* p;
   int rows, cols;  // as it lies in memory, dense
 };
+
+// Two launches of which the second runs beside the first: how many SMs each may spread its tiles over, so that both are
+// there at once where they are few (all where they are not).  (1,000 tokens, H 1144, I 680, backward: each by itself on all
+// SMs 45 us, shared SHARED.)
+struct FfnSize {
+  FfnMode mode;
+  int M, N, K;  // as in FfnParams
+};
+void ffn_share_sms(const FfnSize (&two)[2], int (&sms)[2]);
 
 // a[1], b[1]: the second operands of FFN_GATE (b: W3), FFN_DX (both) and FFN_DW13 (b)
 cudaError_t launch_ffn(FfnMode mode, const FfnOperand (&a)[2], const FfnOperand (&b)[2], FfnParams p,
