@@ -75,7 +75,7 @@ __global__ void __launch_bounds__(256, 5) dropout_kernel(int64_t rows, int64_t c
 // Rows of any alignment.  A piece is 32 blocks of the generator, from the one on that the row begins in: a lane makes a
 // block's bits and takes every 32nd element, whose bits it asks of the lane that has them, so that a warp's accesses are
 // of single elements side by side, which no alignment hinders.  (Vectors that are shifted into place take 204 us for
-// 16,384 rows of 7,168 bf16, 7,171 apart; these ANY_D.)
+// 16,384 rows of 7,168 bf16, 7,171 apart; these 185; of 4,099 f32 165, these 105.)
 template <typename E>
 __global__ void __launch_bounds__(256) dropout_any_kernel(int64_t rows, int64_t cols, int64_t row_pieces, const E* x,
                                                           int64_t ldx, const DropParams d, E* out, int64_t ldo) {

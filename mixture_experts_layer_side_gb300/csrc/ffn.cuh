@@ -43,7 +43,7 @@ struct FfnOperand {
 
 // Two launches of which the second runs beside the first: how many SMs each may spread its tiles over, so that both are
 // there at once where they are few (all where they are not).  (1,000 tokens, H 1144, I 680, backward: each by itself on all
-// SMs 45 us, shared SHARED.)
+// SMs 45 us, shared 32.)
 struct FfnSize {
   FfnMode mode;
   int M, N, K;  // as in FfnParams

@@ -31,22 +31,24 @@ __device__ __forceinline__ Span8 span_of(const E* p, long rows, long ld, long co
 
 __device__ __forceinline__ uint32_t misalign(const void* p) { return (uint32_t)reinterpret_cast<uintptr_t>(p) & 15u; }
 
-// Words from byte `m` (0 to 15, a multiple of the element) of c on.
+// Words from byte `m` (0 to 15, a multiple of the element) of c on.  m is the same for a whole row, so each of its four
+// distances in words has a branch of its own, and rows that lie on a vector's start go past all of it (8,192 rows of 4,099
+// bf16, forward: words moved step by step 128 us, so 115).
+template <typename E, int FIRST>
+__device__ __forceinline__ void shift_from(const uint32_t (&c)[words8<E>() + 4], uint32_t m, uint32_t (&w)[words8<E>()]) {
+#pragma unroll
+  for (int i = 0; i < words8<E>(); ++i) {
+    if constexpr (sizeof(E) == 2) w[i] = __funnelshift_r(c[i + FIRST], c[i + FIRST + 1], (m & 2) * 8);
+    else w[i] = c[i + FIRST];
+  }
+}
 template <typename E>
-__device__ __forceinline__ void shift8(uint32_t (&c)[words8<E>() + 4], uint32_t m, uint32_t (&w)[words8<E>()]) {
-  constexpr int W = words8<E>();
-  if (m & 8) {
-#pragma unroll
-    for (int i = 0; i < W + 2; ++i) c[i] = c[i + 2];
-  }
-  if (m & 4) {
-#pragma unroll
-    for (int i = 0; i < W + 1; ++i) c[i] = c[i + 1];
-  }
-#pragma unroll
-  for (int i = 0; i < W; ++i) {
-    if constexpr (sizeof(E) == 2) w[i] = __funnelshift_r(c[i], c[i + 1], (m & 2) * 8);
-    else w[i] = c[i];
+__device__ __forceinline__ void shift8(const uint32_t (&c)[words8<E>() + 4], uint32_t m, uint32_t (&w)[words8<E>()]) {
+  switch (m >> 2) {
+    case 0: shift_from<E, 0>(c, m, w); break;
+    case 1: shift_from<E, 1>(c, m, w); break;
+    case 2: shift_from<E, 2>(c, m, w); break;
+    default: shift_from<E, 3>(c, m, w); break;
   }
 }
 
@@ -79,7 +81,9 @@ __device__ __forceinline__ void load_words(const E* p, int n, const Span8& span,
     }
   } else {
     const uint32_t m = misalign(p);
-    if (whole_vectors(p, m, span)) {
+    if (m == 0 && n == 8) {
+      load_words<E, true>(p, 8, span, w);
+    } else if (whole_vectors(p, m, span)) {
       const uint4* at = reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(p) - m);
       uint32_t c[W + 4];
 #pragma unroll
@@ -142,13 +146,17 @@ __device__ __forceinline__ void copied_words(const uint4* src, int apart, const 
     }
   } else {
     const uint32_t m = misalign(p);
-    uint32_t c[W + 4];
+    if (m == 0) {
+      copied_words<E, true>(src, apart, p, n, w);
+    } else {
+      uint32_t c[W + 4];
 #pragma unroll
-    for (int i = 0; i <= W / 4; ++i) {
-      const uint4 v = i < W / 4 || m ? src[i * apart] : make_uint4(0, 0, 0, 0);
-      c[4 * i] = v.x, c[4 * i + 1] = v.y, c[4 * i + 2] = v.z, c[4 * i + 3] = v.w;
+      for (int i = 0; i <= W / 4; ++i) {
+        const uint4 v = src[i * apart];
+        c[4 * i] = v.x, c[4 * i + 1] = v.y, c[4 * i + 2] = v.z, c[4 * i + 3] = v.w;
+      }
+      shift8<E>(c, m, w);
     }
-    shift8<E>(c, m, w);
     if (n < 8) keep_first<E>(w, n);
   }
 }
