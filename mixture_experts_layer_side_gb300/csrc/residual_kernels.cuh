@@ -19,10 +19,12 @@
 #pragma once
 
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 
 #include "residual.cuh"
 #include "rows.cuh"
+#include "tc.cuh"
 
 namespace mok {
 namespace residual {
@@ -738,6 +740,9 @@ __global__ void __launch_bounds__(NG == 1 ? 256 : 512, NG == 1 ? 3 : 1)
     }
   }
 
+  // (the kernel that joins the sums may start, and waits for this one's end; started with the first rows it cost the
+  // others' time: 8,192 rows of 7,168, 129 -> 134 us)
+  griddep_launch_dependents();
   // What is left (a worker has one unit at most unless it wrote them itself): its sums into the parts, those of a CTA's
   // teams as one where they are of the same columns' whole.
   const long cta = blockIdx.x;
@@ -792,6 +797,7 @@ template <typename B>
 __global__ void __launch_bounds__(32 * kJoinRows) residual_join_kernel(const ResidualParams p, const BackwardPlan plan) {
   __shared__ float sums[kJoinRows][33];
   const int c = blockIdx.x * 32 + threadIdx.x, what = blockIdx.y;
+  griddep_wait();
   if ((what == 0 && !p.dw_next) || (what == 1 && !p.dw_out)) return;
   const int n = what < 2 || plan.groups == 1 ? plan.ctas : plan.split;
   const float* part = p.part + ((what < 2 ? (long)what : 2l) * plan.ctas + (what < 2 ? 0l : (long)(what - 2) * n)) * p.H;
@@ -848,12 +854,13 @@ inline BackwardPlan backward_plan(int T, int G, int teams, int rows) {
   return b;
 }
 
-template <typename K, typename... A>
-cudaError_t start(K kernel, dim3 grid, dim3 block, size_t smem, cudaStream_t st, A... args) {
-  if (smem > 40 * 1024) {  // (what every kernel has, less what is there beside it)
-    const cudaError_t e = cudaFuncSetAttribute((const void*)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-  }
+// (more than the rows ahead and what is beside them, or beside the longest rows, come to)
+constexpr size_t kMostSmem = 208 * 1024;
+template <auto kernel, typename... A>
+cudaError_t start(dim3 grid, dim3 block, size_t smem, cudaStream_t st, A... args) {
+  static std::atomic<uint64_t> allowed{0};
+  const cudaError_t e = allow_smem((const void*)kernel, kMostSmem, allowed);
+  if (e != cudaSuccess) return e;
   kernel<<<grid, block, smem, st>>>(args...);
   return cudaGetLastError();
 }
@@ -871,8 +878,8 @@ cudaError_t forward(const ResidualParams& p, cudaStream_t st) {
   auto run = [&](auto parts) {
     constexpr int kParts = decltype(parts)::value;
     if (stages == 0)
-      return start(residual_forward_kernel<S, B, ALIGNED, NG, false, kParts>, dim3(grid), block, beside, st, p, 0);
-    return start(residual_forward_kernel<S, B, ALIGNED, NG, true, kParts>, dim3(ctas * sms), block, stages * stage + beside,
+      return start<residual_forward_kernel<S, B, ALIGNED, NG, false, kParts>>(dim3(grid), block, beside, st, p, 0);
+    return start<residual_forward_kernel<S, B, ALIGNED, NG, true, kParts>>(dim3(ctas * sms), block, stages * stage + beside,
                  st, p, stages);
   };
   if constexpr (NG <= 2) {
@@ -909,7 +916,7 @@ cudaError_t backward(const ResidualParams& p, int* launches, cudaStream_t st) {
   const dim3 grid(plan.ctas), block(nt, rows);
   auto run = [&](auto parts) {
     constexpr int kParts = decltype(parts)::value;
-    return start(residual_backward_kernel<S, B, ALIGNED, NG, true, kParts>, grid, block, stages * stage + beside, st, p, plan,
+    return start<residual_backward_kernel<S, B, ALIGNED, NG, true, kParts>>(grid, block, stages * stage + beside, st, p, plan,
                  stages);
   };
   cudaError_t e = cudaErrorInvalidValue;
@@ -929,14 +936,22 @@ cudaError_t backward(const ResidualParams& p, int* launches, cudaStream_t st) {
   }
   if (NG > 2 || parts <= 0 || parts == kDrop) {
     e = stages ? run(std::integral_constant<int, kAnything>())
-               : start(residual_backward_kernel<S, B, ALIGNED, NG, false, kAnything>, grid, block, beside, st, p, plan, 0);
+               : start<residual_backward_kernel<S, B, ALIGNED, NG, false, kAnything>>(grid, block, beside, st, p, plan, 0);
   }
   *launches = 1;
   const bool dgate = p.dgate && !plan.own;
   if (e != cudaSuccess || (!p.dw_next && !p.dw_out && !dgate)) return e;
-  residual_join_kernel<B><<<dim3((p.H + 31) / 32, dgate ? 2 + plan.groups : 2), dim3(32, kJoinRows), 0, st>>>(p, plan);
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3((p.H + 31) / 32, dgate ? 2 + plan.groups : 2);
+  cfg.blockDim = dim3(32, kJoinRows);
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
   ++*launches;
-  return cudaGetLastError();
+  return cudaLaunchKernelEx(&cfg, residual_join_kernel<B>, p, plan);
 }
 
 // The instances, each in a file of its own.
