@@ -481,20 +481,27 @@ def mok_residual_workspace_size(T, H):
     return LIB.mok_residual_workspace_size(T, H)
 
 
-def _rows(t):
-    """Pointer and distance of the rows of a matrix, or of none."""
-    return (None, 0) if t is None else (t.data_ptr(), _rows_apart(t))
+def _rows(one, *matrices):
+    """Pointers and distances of the rows of the matrices (None: none), in turn.  ``one``: the distance to state where
+    there is one row, whose stride says nothing, and 0 where there are more."""
+    out = []
+    for t in matrices:
+        if t is None:
+            out += (None, 0)
+        else:
+            out += (t.data_ptr(), one or t.stride(0))
+    return out
 
 
 def mok_residual_forward(r, x, y, xo, n, stream=None):
-    _ok(LIB.mok_residual_forward(r, *_rows(x), *_rows(y), *_rows(xo), *_rows(n), _stream(stream)),
-        "mok_residual_forward")
+    one = r.H if r.T <= 1 else 0
+    _ok(LIB.mok_residual_forward(r, *_rows(one, x, y, xo, n), _stream(stream)), "mok_residual_forward")
 
 
 def mok_residual_backward(r, x, y, dxo, dn, dx, dy, dw_out, dgate, dw_next, ws, stream=None):
-    _ok(LIB.mok_residual_backward(r, *_rows(x), *_rows(y), *_rows(dxo), *_rows(dn), *_rows(dx), *_rows(dy),
-                                  _ptr(dw_out), _ptr(dgate), _ptr(dw_next), ws.data_ptr(), ws.nbytes, _stream(stream)),
-        "mok_residual_backward")
+    one = r.H if r.T <= 1 else 0
+    _ok(LIB.mok_residual_backward(r, *_rows(one, x, y, dxo, dn, dx, dy), _ptr(dw_out), _ptr(dgate), _ptr(dw_next),
+                                  ws.data_ptr(), ws.nbytes, _stream(stream)), "mok_residual_backward")
 
 
 # ---------------------------------------------------------------- dense feed-forward block
