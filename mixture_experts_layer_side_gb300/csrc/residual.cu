@@ -46,9 +46,13 @@ cudaError_t any_backward(const ResidualParams& p, int* launches, cudaStream_t st
 size_t residual_part_floats(int T, int H) {
   using namespace residual;
   // (units are no more than workers where their sums are parts)
-  const int ng = groups_backward(H), nt = team_threads(H, ng), rows = nt == 32 ? kTeamRows : 1;
-  const BackwardPlan b = backward_plan(T, 0, device_sm_count() * ctas_backward(nt * rows, ng) * rows, rows);
-  return (2 * (size_t)b.ctas + b.workers) * H;
+  size_t most = 0;
+  for (const bool aligned : {false, true}) {
+    const int ng = groups_backward(H, aligned), nt = team_threads(H, ng), rows = nt == 32 ? kTeamRows : 1;
+    const BackwardPlan b = backward_plan(T, 0, device_sm_count() * ctas_backward(nt * rows, ng) * rows, rows);
+    most = std::max(most, (2 * (size_t)b.ctas + b.workers) * H);
+  }
+  return most;
 }
 
 cudaError_t launch_residual_forward(mok_dtype stream, mok_dtype branch, const ResidualParams& p, int* launches,

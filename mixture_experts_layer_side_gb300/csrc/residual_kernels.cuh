@@ -831,7 +831,12 @@ constexpr int kMaxStages = 4;
 
 inline int team_threads(int H, int ng) { return ((H + 8 * ng - 1) / (8 * ng) + 31) / 32 * 32; }
 inline int groups_forward(int H) { return H <= 4096 ? 1 : H <= 8192 ? 2 : 4; }
-inline int groups_backward(int H) { return H <= 256 ? 1 : H <= 8192 ? 2 : 4; }
+// A warp holds rows of up to 512 columns, which need no barrier. Of longer ones at any alignment the shifts, not the
+// registers, are what counts, and more threads hide them (8,192 rows of 515 bf16, dropout: two groups 81 us, one 56; of
+// 1,003 84 and 69; of 2,043 without dropout 108 and 118; aligned, 4,096 of 2,048: 29 and 35).
+inline int groups_backward(int H, bool aligned) {
+  return H <= 256 || (!aligned && H > 512 && H <= 1536) ? 1 : H <= 8192 ? 2 : 4;
+}
 // CTAs that an SM holds (registers).
 inline int ctas_forward(int threads, int ng) { return std::max(1, (ng <= 2 ? 1024 : 512) / threads); }
 inline int ctas_backward(int threads, int ng) { return std::max(1, (ng == 1 ? 768 : 512) / threads); }
@@ -965,7 +970,7 @@ cudaError_t forward_rows(const ResidualParams& p, cudaStream_t st) {
 }
 template <typename S, typename B, bool ALIGNED>
 cudaError_t backward_rows(const ResidualParams& p, int* launches, cudaStream_t st) {
-  switch (groups_backward(p.H)) {
+  switch (groups_backward(p.H, ALIGNED)) {
     case 1: return backward<S, B, ALIGNED, 1>(p, launches, st);
     case 2: return backward<S, B, ALIGNED, 2>(p, launches, st);
     default: return backward<S, B, ALIGNED, 4>(p, launches, st);
