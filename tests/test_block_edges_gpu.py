@@ -4,6 +4,10 @@ between and beside rows, outputs among other data, very many rows, offsets past
 32 bits, the longest rows, calls between a forward pass and its backward pass.
 Bounds are those of the formulas' tests."""
 
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -267,3 +271,44 @@ def test_two_graphs_with_objects_of_their_own():
     torch.cuda.synchronize()
     for a, b in zip(want, held):
         assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+FIRST_CALLS = """
+import torch
+from mixture_experts_layer_side_gb300.dropout import MoKDropout
+from mixture_experts_layer_side_gb300.feedforward import MoKFeedForward
+from mixture_experts_layer_side_gb300.residual import MoKResidual
+bf16, cuda = torch.bfloat16, "cuda"
+for T, H, I in ((2, 256, 128), (70, 520, 264), (3000, 1024, 1024)):
+    g = torch.Generator(device=cuda).manual_seed(T)
+    x, dout = ((torch.randn((T, H), generator=g, device=cuda)).to(bf16) for _ in range(2))
+    W1, W3, W2 = ((0.05 * torch.randn(s, generator=g, device=cuda)).to(bf16) for s in ((H, I), (H, I), (I, H)))
+    w = torch.ones(H, dtype=bf16, device=cuda)
+    ffn, res, drop = MoKFeedForward(H, I, T), MoKResidual(H, T), MoKDropout(0.25)
+
+    def step():
+        y = ffn.forward(x, W1, W3, W2)
+        x2, n = res.forward(x, y, w_out=w, w_next=w, dropout=drop)
+        b = res.backward(dout, n, x2, y, w_out=w, w_next=w, dropout=drop)
+        d = ffn.backward(x, W1, W3, W2, b["dy"])
+        return [y, x2, n, b["dx"], b["dw_out"], *d.values(), ffn.infer(n, W1, W3, W2), drop.forward(y)]
+
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = step()
+    graph.replay()
+    torch.cuda.synchronize()
+    got = [t.clone() for t in held]
+    assert all(torch.equal(a, b) for a, b in zip(got, step())), (T, H, I)
+    ffn.check()
+print("captured")
+"""
+
+
+def test_first_calls_of_a_process_are_captured():
+    """Nothing of a kernel's first launch (its shared memory, how many clusters fit) hinders a capture."""
+    require_gpu()
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    done = subprocess.run([sys.executable, "-c", FIRST_CALLS], cwd=root, capture_output=True, text=True, timeout=300)
+    assert done.returncode == 0 and "captured" in done.stdout, done.stderr[-3000:]
