@@ -827,6 +827,7 @@ __global__ void __launch_bounds__(32 * kJoinRows) residual_join_kernel(const Res
 // Shared memory of the rows ahead, over all of an SM's CTAs: enough for what HBM has on its way, and the rest left to
 // L1 for the weights (which the backward pass has in registers).
 constexpr size_t kAheadBytes = 176 * 1024, kAheadBytesBackward = 200 * 1024;
+constexpr size_t kMostSmem = 227 * 1024 - sizeof(Slots);
 constexpr int kMaxStages = 4;
 
 inline int team_threads(int H, int ng) { return ((H + 8 * ng - 1) / (8 * ng) + 31) / 32 * 32; }
@@ -859,8 +860,6 @@ inline BackwardPlan backward_plan(int T, int G, int teams, int rows) {
   return b;
 }
 
-// (more than the rows ahead and what is beside them, or beside the longest rows, come to)
-constexpr size_t kMostSmem = 208 * 1024;
 template <auto kernel, typename... A>
 cudaError_t start(dim3 grid, dim3 block, size_t smem, cudaStream_t st, A... args) {
   static std::atomic<uint64_t> allowed{0};
@@ -917,6 +916,9 @@ cudaError_t backward(const ResidualParams& p, int* launches, cudaStream_t st) {
     beside = rows * backward_beside(p.H, bytes, plan.own, rows > 1);
     stage = (size_t)rows * nt * NG * 16 * (2 * vectors8<S, ALIGNED>() + (plan.own ? 3 : 2) * vectors8<B, ALIGNED>());
     if (ctas) stages = stages_ahead(kAheadBytesBackward / ctas, stage, beside);
+    // (two rows that need all of it: 8,192 of 4,099 f32 of both kinds 426 us, with none ahead 517; where three fit, a fourth
+    // for which L1 is given up costs: 8,192 of 7,168 bf16, dropout, 186 and 210)
+    if (ctas == 1 && !stages) stages = stages_ahead(kMostSmem, stage, beside);
   }
   const dim3 grid(plan.ctas), block(nt, rows);
   auto run = [&](auto parts) {
