@@ -359,18 +359,19 @@ __global__ void __launch_bounds__(kFfnThreads, 1) ffn_kernel(const __grid_consta
       }
     }
   } else if (warp == 1) {
-    uint32_t stage = 0, phase = 0, tcount = 0;
-    constexpr uint32_t idesc = idesc_bf16(256, 256, ffn_a_mn(MODE) ? 1 : 0, ffn_b_mn(MODE) ? 1 : 0);
-    bool ok = rank == 0;
-    for (int item = first; ok && item < items; item += step, ++tcount) {
-      const uint32_t buf = tcount & 1, tph = (tcount >> 1) & 1;
-      if (!mbar_wait_cluster(&ctl->tempty[buf], tph ^ 1, wc)) break;
-      tc_fence_after();
-      const uint32_t d = tmem + buf * 256;
-      for (int kk = 0; kk < k_iters; ++kk) {
-        if (!mbar_wait(&ctl->full[stage], phase, wc)) { ok = false; break; }
+    // (one thread alone waits and issues: lanes that each waited could find a wait given up at different times, and part)
+    if (lane == 0) {
+      uint32_t stage = 0, phase = 0, tcount = 0;
+      constexpr uint32_t idesc = idesc_bf16(256, 256, ffn_a_mn(MODE) ? 1 : 0, ffn_b_mn(MODE) ? 1 : 0);
+      bool ok = rank == 0;
+      for (int item = first; ok && item < items; item += step, ++tcount) {
+        const uint32_t buf = tcount & 1, tph = (tcount >> 1) & 1;
+        if (!mbar_wait_cluster(&ctl->tempty[buf], tph ^ 1, wc)) break;
         tc_fence_after();
-        if (lane == 0) {
+        const uint32_t d = tmem + buf * 256;
+        for (int kk = 0; kk < k_iters; ++kk) {
+          if (!mbar_wait(&ctl->full[stage], phase, wc)) { ok = false; break; }
+          tc_fence_after();
           const uint32_t a0 = smem_u32(sA + stage * kFfnOperandBytes), b0 = smem_u32(sB + stage * kFfnOperandBytes);
 #pragma unroll
           for (int k16 = 0; k16 < 4; ++k16) {
@@ -379,13 +380,10 @@ __global__ void __launch_bounds__(kFfnThreads, 1) ffn_kernel(const __grid_consta
             mma_bf16_pair(d, ad, bd, idesc, (kk | k16) != 0 ? 1u : 0u);
           }
           mma_commit_pair(&ctl->empty[stage]);
+          if (++stage == kFfnStages) { stage = 0; phase ^= 1; }
         }
-        __syncwarp();
-        if (++stage == kFfnStages) { stage = 0; phase ^= 1; }
+        if (ok) mma_commit_pair(&ctl->tfull[buf]);
       }
-      if (!ok) break;
-      if (lane == 0) mma_commit_pair(&ctl->tfull[buf]);
-      __syncwarp();
     }
   } else {
     const int q = warp & 3, half = (warp - 2) >> 2;  // TMEM lanes that this warp may read; columns it takes
@@ -395,7 +393,8 @@ __global__ void __launch_bounds__(kFfnThreads, 1) ffn_kernel(const __grid_consta
       const FfnTile t = tile_of<MODE>(p, item);
       const uint32_t buf = tcount & 1, tph = (tcount >> 1) & 1;
       auto ready = [&]() {
-        if (!mbar_wait(&ctl->tfull[buf], tph, wc)) return false;
+        // (what the warp loads from TMEM it loads together: it goes on together or not at all)
+        if (!__all_sync(0xffffffffu, mbar_wait(&ctl->tfull[buf], tph, wc))) return false;
         tc_fence_after();
         return true;
       };
@@ -412,6 +411,7 @@ __global__ void __launch_bounds__(kFfnThreads, 1) ffn_kernel(const __grid_consta
   tc_fence_before();
   // (the non-aligned barrier form, defined for warps that arrive diverged)
   asm volatile("barrier.sync 0;" ::: "memory");
+  __syncwarp();  // (the cluster's barrier is of the aligned form)
   // neither CTA leaves (nor frees TMEM) while the other may still signal its barriers or run MMAs on its memory
   cluster_sync();
   tc_fence_after();
@@ -540,12 +540,12 @@ __global__ void __launch_bounds__(kFfnThreads, 1) ffn_few_kernel(const __grid_co
       }
     }
   } else if (warp == 1 && rank == 0) {
-    constexpr uint32_t idesc = idesc_bf16(256, 256, ffn_a_mn(MODE) ? 1 : 0, ffn_b_mn(MODE) ? 1 : 0);
-    uint32_t stage = 0, phase = 0;
-    for (int i = 0; i < steps; ++i) {
-      if (!mbar_wait(&ctl->full[stage], phase, wc)) { ok = false; break; }
-      tc_fence_after();
-      if (lane == 0) {
+    if (lane == 0) {
+      constexpr uint32_t idesc = idesc_bf16(256, 256, ffn_a_mn(MODE) ? 1 : 0, ffn_b_mn(MODE) ? 1 : 0);
+      uint32_t stage = 0, phase = 0;
+      for (int i = 0; i < steps; ++i) {
+        if (!mbar_wait(&ctl->full[stage], phase, wc)) { ok = false; break; }
+        tc_fence_after();
         const uint32_t a0 = smem_u32(sA + stage * a_slot), b0 = smem_u32(sB + stage * kFfnOperandBytes);
 #pragma unroll
         for (int k16 = 0; k16 < 4; ++k16) {
@@ -554,16 +554,16 @@ __global__ void __launch_bounds__(kFfnThreads, 1) ffn_few_kernel(const __grid_co
           mma_bf16_pair(tmem, ad, bd, idesc, (i | k16) != 0 ? 1u : 0u);
         }
         mma_commit_pair(&ctl->empty[stage], 3u << (cta & ~1));
+        if ((int)++stage == stages) { stage = 0; phase ^= 1; }
       }
-      if ((int)++stage == stages) { stage = 0; phase ^= 1; }
-      __syncwarp();
+      mma_commit_pair(&ctl->done, 3u << (cta & ~1));
     }
-    if (lane == 0) mma_commit_pair(&ctl->done, 3u << (cta & ~1));
-    __syncwarp();
   }
+  __syncwarp();
   // every MMA of the pair is done: the sums stand, the stages are free
   const int q = warp & 3, half = (warp - 2) >> 2;  // epilogue warps: TMEM lanes that this warp may read; columns it takes
-  const bool summed = mbar_wait(&ctl->done, 0, wc);
+  // (a warp comes to the cluster's barrier, and to its loads from TMEM, in one piece and of one mind)
+  const bool summed = __all_sync(0xffffffffu, mbar_wait(&ctl->done, 0, wc));
   tc_fence_after();
   cluster_sync();
   const int row0 = t.m * 256 + rank * 128;
@@ -620,6 +620,7 @@ __global__ void __launch_bounds__(kFfnThreads, 1) ffn_few_kernel(const __grid_co
     }
   }
   tc_fence_before();
+  __syncwarp();
   cluster_sync();
   tc_fence_after();
   if (warp == 1) tmem_dealloc_pair(tmem, 256);

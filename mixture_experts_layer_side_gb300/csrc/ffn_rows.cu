@@ -122,6 +122,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) ffn_rows_kernel(const FfnRowsP
     for (int k = 1; k < kWorkers; ++k) v += sums[k * TM * kCols + i];
     sums[i] = v;
   }
+  __syncwarp();  // (the cluster's barrier is of the aligned form)
   cluster_sync();
   // each CTA finishes every ctas-th result
   constexpr int kResults = GATE ? kCols / 2 : kCols;
@@ -137,6 +138,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) ffn_rows_kernel(const FfnRowsP
     if (GATE) static_cast<float*>(p.out)[(long)m * p.N + n] = h / (1.0f + __expf(-h)) * u;
     else static_cast<__nv_bfloat16*>(p.out)[(long)m * p.N + n] = __float2bfloat16_rn(h);
   }
+  __syncwarp();
   cluster_sync();  // (no CTA leaves while another reads its sums)
 }
 
