@@ -36,6 +36,7 @@
 #include <atomic>
 
 #include "ffn.cuh"
+#include "ring.cuh"
 #include "tc.cuh"
 
 namespace mok {
@@ -523,20 +524,26 @@ __global__ void __launch_bounds__(kFfnThreads, 1) ffn_few_kernel(const __grid_co
     if (lane == 0) {
       const bool with_a = t.m * 256 + rank * 128 < p.M;
       uint32_t stage = 0, phase = 0;
-      for (int i = 0; i < steps; ++i) {
+      int i = 0;
+      for (; i < steps; ++i) {
         if (!mbar_wait(&ctl->empty[stage], phase ^ 1, wc)) { ok = false; break; }
         if (rank == 0) mbar_arrive_expect_tx(&ctl->full[stage], step_bytes(p, t, a_slot));
         ffn_loads<MODE>(maps, t, k0 + i, k_half, rank, with_a, sA + stage * a_slot, sB + stage * kFfnOperandBytes,
                         mapa_shared(&ctl->full[stage], (uint32_t)(cta & ~1)));
         if ((int)++stage == stages) { stage = 0; phase ^= 1; }
       }
-      // (after a timeout: copies in flight land before the shared memory serves again)
-      if (!ok) {
+      // Whoever gives up, no copy is in flight when the stages serve for the sums, nor when the CTA leaves: the leader,
+      // whose barriers count both CTAs' bytes, waits for each stage's last fill (the MMAs did for those before, and wait for
+      // these meanwhile).  Where the two CTAs gave up at different steps, not all that was asked for is counted: a fill that
+      // is short of the other's bytes, or the other's fills that were never armed here.  Those land within the limit.
+      if (rank == 0) {
         const uint64_t t0 = globaltimer();
-        for (int j = 0; j < stages; ++j) {
+        for (int f = last_fills_from(i, stages); f < i; ++f) {
+          if (mbar_try_wait(&ctl->full[f % stages], fill_parity(f, stages))) continue;
           const uint64_t spent = globaltimer() - t0;
-          if (spent < kFfnDrainNs) mbar_drain(&ctl->full[j], 0, kFfnDrainNs - spent);
+          if (spent < kFfnDrainNs) mbar_drain(&ctl->full[f % stages], fill_parity(f, stages), kFfnDrainNs - spent);
         }
+        while (!ok && globaltimer() - t0 < kFfnDrainNs) __nanosleep(10000);
       }
     }
   } else if (warp == 1 && rank == 0) {
@@ -564,6 +571,11 @@ __global__ void __launch_bounds__(kFfnThreads, 1) ffn_few_kernel(const __grid_co
   const int q = warp & 3, half = (warp - 2) >> 2;  // epilogue warps: TMEM lanes that this warp may read; columns it takes
   // (a warp comes to the cluster's barrier, and to its loads from TMEM, in one piece and of one mind)
   const bool summed = __all_sync(0xffffffffu, mbar_wait(&ctl->done, 0, wc));
+  if (!summed) {
+    // the leader commits `done` whether its own waits gave up or not: no MMA is under way past here either
+    mbar_drain(&ctl->done, 0, kWaitLimitNs);
+    __syncwarp();
+  }
   tc_fence_after();
   cluster_sync();
   const int row0 = t.m * 256 + rank * 128;
