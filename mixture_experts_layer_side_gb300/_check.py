@@ -106,6 +106,6 @@ def run_on(owner, stream, call, *args):
     with torch.cuda.stream(stream):
         got = call(*args)
     for t in got if isinstance(got, tuple) else got.values() if isinstance(got, dict) else (got,):
-        if t is not None:
+        if isinstance(t, torch.Tensor):  # (a dict is the caller's, who may keep other things in it)
             t.record_stream(caller)
     return got
