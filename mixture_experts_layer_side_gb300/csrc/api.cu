@@ -1985,7 +1985,13 @@ mok_status mok_residual_backward(const mok_residual* r, const void* x, int64_t l
   if (dw_next || dw_out || dgate) {
     if (!ws || !aligned16(ws)) return MOK_ERR_INVALID_ARG;
     if (ws_bytes < mok_residual_workspace_size(T, H)) return MOK_ERR_WORKSPACE_TOO_SMALL;
-  } else if (T == 0) {
+  }
+  if (T == 0) {
+    // sums of nothing, which no weight is multiplied with (it may be infinite)
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (dw_out) MOK_CUDA(cudaMemsetAsync(dw_out, 0, (size_t)H * 4, st));
+    if (dw_next) MOK_CUDA(cudaMemsetAsync(dw_next, 0, (size_t)H * 4, st));
+    if (dgate) MOK_CUDA(cudaMemsetAsync(dgate, 0, (size_t)r->gate_rows * H * (B == MOK_TYPE_BF16 ? 2 : 4), st));
     return MOK_OK;
   }
   p.x = x;

@@ -582,7 +582,7 @@ __global__ void __launch_bounds__(NG == 1 ? 256 : 512, NG == 1 ? 3 : 1)
     if (plan.own) store8<ALIGNED, NG>(share, g, a, zeros());
   }
 
-  // (a worker without a unit, or the only one's rows with T = 0: no rows, sums of zero)
+  // (a worker without a unit: no rows, sums of zero)
   Walk at = {worker, 0, 0, 0};
   if (worker < plan.workers && worker < plan.groups * plan.split) walk_unit(at, p, plan);
   bool more = at.row < at.end;
