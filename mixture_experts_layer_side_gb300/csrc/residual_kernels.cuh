@@ -441,7 +441,8 @@ __global__ void __launch_bounds__(512, NG <= 2 ? 2 : 1) residual_forward_kernel(
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
         if constexpr (AHEAD) x[g] = get_x(g);
-        if (drops) drop8(z[g], keep8<ALIGNED, NG>(p.drop, call, first, g, a, bytes));
+        Keep<ALIGNED, NG> keep = {};
+        if (drops) keep = keep8<ALIGNED, NG>(p.drop, call, first, g, a, bytes);
 #pragma unroll
         for (int i = 0; i < 4; ++i) z[g].v[i] = mul(z[g].v[i], both(factor));
         if (has_out) {
@@ -449,6 +450,8 @@ __global__ void __launch_bounds__(512, NG <= 2 ? 2 : 1) residual_forward_kernel(
 #pragma unroll
           for (int i = 0; i < 4; ++i) z[g].v[i] = mul(z[g].v[i], w.v[i]);
         }
+        // (of z as it is: a norm or a weight that is not finite reaches no dropped element)
+        if (drops) drop8(z[g], keep);
         const Eight f = p.G ? load8<ALIGNED, NG>(gates, group, g, a) : ones();
 #pragma unroll
         for (int i = 0; i < 4; ++i) x[g].v[i] = fma(z[g].v[i], f.v[i], x[g].v[i]);
