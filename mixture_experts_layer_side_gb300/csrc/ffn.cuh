@@ -26,11 +26,14 @@ struct FfnParams {
   int sms;         // SMs that its tiles may be spread over (0: all)
 };
 
-// How a launch stands to the one before it in the stream.
+// How a launch stands to the one before it in the stream.  Each lets the next one start when its own start is done, which
+// for FFN_READS_IT is after its wait: what may still run beside an FFN_BESIDE_IT are the launches back to the last of
+// another kind, that one among them, and what stands before those is over.  So dW1 and dW3, beside dx, may read dh and du,
+// as dx waits for dW2, which ends after da; right after dW2 they might not.
 enum FfnAfter : int {
   FFN_AFTER_ALL = 0,   // an ordinary launch
-  FFN_READS_IT = 1,    // starts beside it, waits for its end before it reads anything
-  FFN_BESIDE_IT = 2,   // reads nothing that it writes: waits for its end at its own end
+  FFN_READS_IT = 1,    // starts beside it, waits for its end (and so for all before it) before it reads anything
+  FFN_BESIDE_IT = 2,   // reads nothing that those beside it write, writes nothing that they touch: waits at its own end
 };
 
 // Floats that h or u of T rows takes where it is kept: rows in whole 32s.
