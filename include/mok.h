@@ -745,7 +745,9 @@ mok_status mok_dropout(int64_t rows, int64_t cols, mok_dtype type, const void* x
  * type and stride); otherwise outputs share no byte with inputs or each other
  * (MOK_ERR_INVALID_ARG, for the matrices).  1 <= H <= MOK_RESIDUAL_MAX_HIDDEN,
  * T <= 2^30; T = 0 gives zero gradients of the weights.  Sums in a fixed order:
- * the same call gives the same bits.
+ * the same call gives the same bits.  Backward, dropout keeps y and the
+ * gradients out where they are dropped, but not a gate or a norm that is not
+ * finite: those make dy, dgate and dw_out NaN there too.
  * ws: mok_residual_workspace_size bytes for at least this T, for the backward
  * pass alone; calls that share it must not overlap.
  */

@@ -5,10 +5,11 @@
 // output, 16 bits an element, so nothing is stored between a forward pass and
 // its backward pass: both make the same bits from the element's index.
 //
-// 16 bits and not 32: ten rounds are 20 wide multiplications, which run at
-// half rate.  At one output per four elements they alone would take longer
-// than moving bf16 elements at the HBM's rate; at one per eight they take a
-// third of it.  The price is that p is a multiple of 2^-16.
+// 16 bits and not 32: an output is ten dependent rounds of two wide
+// multiplications, and one per four elements, which 32 bits would take, bounds
+// bf16 (dropout of 16,384 rows of 7,168: one output a block of eight 84 us, two
+// 121; f32, with twice the bytes an element, is as fast with two).  The price is
+// that p is a multiple of 2^-16.
 #pragma once
 
 #include "mok_internal.cuh"

@@ -283,7 +283,8 @@ struct KeepBlock {
   __device__ __forceinline__ bool operator()(int j) const { return drop_kept(r, j, most); }
 };
 // (Words need no bits made of them first, but registers, of which threads with four groups have none to spare: 8,192 rows
-// of 7,168 bf16, two groups, backward with dropout: bits 212 us, words 188; 4,096 of 12,288, four, without: 271 and 363.)
+// of 7,168 bf16, two groups, backward with dropout: bits 212 us, words 188; 4,096 of 12,288, four: 293 and 401, and
+// 265 and 366 where the same kernel is called without dropout.)
 template <bool ALIGNED, int NG>
 using Keep = std::conditional_t<ALIGNED && NG <= 2, KeepBlock, KeepBits>;
 template <bool ALIGNED, int NG>
